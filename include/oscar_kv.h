@@ -305,6 +305,90 @@ int attn_decode_static(const oscar_kv_config* cfg, const void* cache, int32_t la
                        void* stream);
 
 /*
+ * kv_read — positions [start_pos[b], start_pos[b] + n) of every sequence read
+ * back into the basis they were appended in: k = k' R_K^T, v = v' R_V^T with
+ * k', v' the rotated rows as attn_decode sees them at length seq_lens[b]
+ * (BF16 rows of the windows, zero + scale * level of an INT2 row).  The
+ * counterpart of kv_append (no read-back is described on the pages): for
+ * handing a cached prompt to code that wants plain K and V, and for checks.
+ *   start_pos, seq_lens  device int32 [B].
+ *   k_out, v_out  device [B][n][Hkv][D] bf16 (float32 with OSCAR_FLAG_OUT_FP32),
+ *              16-byte aligned; one of them may be NULL (that role is not read).
+ *              Positions outside [0, seq_lens[b]) leave their rows as they were.
+ *              With OSCAR_FLAG_ABSORB_V v_out receives the rotated rows v'.
+ * A seq_len above capacity is clamped to it and sets OSCAR_DEV_OVER_CAPACITY.
+ */
+int kv_read(const oscar_kv_config* cfg, const void* cache, int32_t layer, const int32_t* start_pos,
+            const int32_t* seq_lens, int32_t n, const float* R_K, const float* R_V, void* k_out, void* v_out,
+            int32_t* dev_status, void* stream);
+
+/*
+ * attn_extend — attention of several new tokens per sequence over the cache:
+ * a chunk of a prompt, or drafted tokens to be verified.  Append their K and V
+ * first (kv_append); the q_lens[b] query tokens are the last ones of the
+ * sequence: token t sits at position p = seq_lens[b] - q_lens[b] + t and
+ * attends to every position <= p, each as attn_decode sees it at length
+ * seq_lens[b] (the windows are those of the sequence, not of the token).
+ *   q          device [B][n_new][Hq][D] bf16 (float32 with OSCAR_FLAG_IN_FP32), not rotated.
+ *   q_lens     device int32 [B] or NULL (= n_new for all): query tokens of each
+ *              sequence, at most n_new (more is treated as n_new); tokens
+ *              t >= q_lens[b] are not read and their rows of out and lse are
+ *              left as they were.
+ *   seq_lens   device int32 [B]; a token whose position is negative attends to
+ *              nothing: zero output, lse = -inf, OSCAR_DEV_EMPTY.  A length
+ *              above capacity is clamped to it and sets OSCAR_DEV_OVER_CAPACITY.
+ *   seq_len_hint host upper bound on seq_lens (0 = capacity), for the split count.
+ *   num_splits 0 = automatic; else every sequence's positions are cut into that
+ *              many shares (at most OSCAR_KV_MAX_SPLITS), merged afterwards.
+ *   out        device [B][n_new][Hq][D] bf16 (float32 with OSCAR_FLAG_OUT_FP32);
+ *              rotated basis with OSCAR_FLAG_ABSORB_V.  Repeated calls on the
+ *              same inputs give the same bits.
+ *   lse        device float32 [B][n_new][Hq] or NULL: natural log-sum-exp.
+ *   workspace  device, 256-byte aligned.  With n splits and rows =
+ *              B * n_new * Hq it holds align256(rows*D*4) +
+ *              align256(rows*n*D*4) + align256(rows*n*8) bytes;
+ *              attn_extend_workspace_query gives what the automatic split count
+ *              takes at most.  With less, the automatic count is reduced to
+ *              what fits (OSCAR_ERR_WORKSPACE if one split does not, or an
+ *              explicit count).  Concurrent calls must not share a workspace.
+ * Scores, probabilities and sums are float32.
+ * n_new = 0 does nothing; n_new > capacity is OSCAR_ERR_CAPACITY.
+ */
+int attn_extend_workspace_query(const oscar_kv_config* cfg, int32_t n_new, uint64_t* bytes);
+int attn_extend(const oscar_kv_config* cfg, const void* cache, int32_t layer, const void* q, int32_t n_new,
+                const int32_t* q_lens, const int32_t* seq_lens, int32_t seq_len_hint, const float* R_K,
+                const float* R_V, float sm_scale, int32_t num_splits, void* out, float* lse, void* workspace,
+                uint64_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * attn_decode_prefix — attn_decode for a batch whose sequences share a prefix:
+ * query b attends to the prefix_len[0] positions of the one sequence in
+ * `prefix_cache` and then to the seq_lens[b] positions of its own in `cache`.
+ * The prefix is kept and read once for the whole batch instead of once per
+ * sequence: its rows meet the B * G query rows of their KV head together.
+ * Fill the prefix cache as any cache of batch 1 (kv_append, attn_extend).  The
+ * windows of the two caches are their own.
+ *   prefix_cfg the prefix cache's configuration: batch 1, the heads, head_dim
+ *              and flags of cfg (else OSCAR_ERR_INVALID); its windows,
+ *              capacity and clips may differ.
+ *   prefix_len device int32 [1]; 0 is allowed, above capacity is clamped and
+ *              sets OSCAR_DEV_OVER_CAPACITY.  prefix_len_hint: host upper
+ *              bound (0 = the prefix cache's capacity).
+ *   seq_lens   device int32 [B]; 0 is allowed (only the prefix).  A sequence
+ *              with neither sets OSCAR_DEV_EMPTY (zero output, lse = -inf).
+ *   num_splits shares of the prefix; 0 = automatic.
+ *   workspace  device, 256-byte aligned, attn_decode_prefix_workspace_query
+ *              bytes; with less, the automatic counts are reduced to what fits.
+ * Other arguments, rounding and errors as attn_decode and attn_extend.
+ */
+int attn_decode_prefix_workspace_query(const oscar_kv_config* cfg, const oscar_kv_config* prefix_cfg, uint64_t* bytes);
+int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const oscar_kv_config* prefix_cfg,
+                       const void* prefix_cache, int32_t layer, const void* q, const int32_t* seq_lens,
+                       int32_t seq_len_hint, const int32_t* prefix_len, int32_t prefix_len_hint, const float* R_K,
+                       const float* R_V, float sm_scale, int32_t num_splits, void* out, float* lse, void* workspace,
+                       uint64_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
  * oscar_kv_set_profile_events — measurement hook (no counterpart on the pages).
  * While both events are non-NULL (cudaEvent_t passed as void*), every
  * attn_decode call made from the calling host thread records `split_start` on

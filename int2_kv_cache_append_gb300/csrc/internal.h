@@ -91,4 +91,72 @@ uint64_t calibrate_rv_workspace_bytes(int D, int64_t n_kv);
 int launch_calibrate_rv(const float* q, int64_t nq, const float* k, const float* v, int64_t nkv, int D, float* R,
                         void* ws, int32_t* status, cudaStream_t stream);
 
+// Positions [start_pos[b], start_pos[b] + n) read back into the model's basis
+// (kv_rows.cu).
+struct ReadArgs {
+  Geom g;
+  const uint8_t* layer_base;
+  const int32_t* start_pos;
+  const int32_t* seq_lens;
+  const float* R_K;
+  const float* R_V;
+  void* k_out;  // [B][n][Hkv][D], NULL = role not read
+  void* v_out;
+  int32_t* status;
+  int n;
+  int out_fp32, absorb_v, hadamard;
+};
+int launch_read(const ReadArgs& a, cudaStream_t stream);
+
+// Attention of blocks of query rows over one cache: unit (b, h) has n * G rows
+// r = t * G + e, row r being query head h * G + e of token t of sequence b.
+struct RowsArgs {
+  Geom g;                   // of the cache that is read
+  const uint8_t* layer_base;
+  const int32_t* seq_lens;  // [B]
+  const int32_t* q_lens;    // [B] or NULL (= n)
+  const float* qrot;        // [B][n][Hq][D] rotated queries in log2 units
+  float* acc;               // [B * n * Hq][ns][D] sums of 2^(score - m) v'
+  float* ml;                // [B * n * Hq][ns][2] (m, l)
+  int32_t* status;
+  int n, ns;
+  int causal;               // token t sees positions <= seq_len - q_len + t; else every position
+};
+int launch_attn_rows(const RowsArgs& a, cudaStream_t stream);
+// Splits of every (row tile, unit) for `rows` query rows per unit: enough
+// shares to fill the GPU, none shorter than the context gives.
+int rows_splits(const Geom& g, int64_t rows, int seq_len_hint);
+
+// q' = q R_K in log2 units, before the row attention (kv_rows.cu).
+struct QrotRowsArgs {
+  const void* q;       // [rows][D]
+  float* qrot;
+  const float* R_K;
+  int32_t* status;
+  int32_t* zero_word;  // set to 0 (a status word of the workspace), or NULL
+  const int32_t* q_lens;  // [B] or NULL: tokens t >= q_lens[b] are not read
+  int64_t rows;        // B * n * Hq
+  int n, Hq, D, in_fp32, hadamard;
+  float qscale;
+};
+int launch_qrot_rows(const QrotRowsArgs& a, cudaStream_t stream);
+
+// Merge of the splits' partial results, V un-rotation and store (kv_rows.cu).
+struct FinishArgs {
+  const float* acc;         // as in RowsArgs
+  const float* ml;
+  const float* own_o;       // [rows][D] and [rows]: one more, normalised partial result, or NULL
+  const float* own_lse;
+  const int32_t* own_status;
+  const int32_t* q_lens;    // [B] or NULL (= n): tokens t >= q_lens[b] are left as they were
+  const float* R_V;
+  void* out;
+  float* lse;
+  int32_t* status;
+  int64_t rows;             // B * n * Hq
+  int n, Hq, D, ns;
+  int out_fp32, absorb_v, hadamard;
+};
+int launch_finish_rows(const FinishArgs& a, cudaStream_t stream);
+
 }  // namespace oscar

@@ -1,0 +1,279 @@
+// Row products with a layer's rotation: kv_read (cached rows back into the
+// model's basis), the query rotation and the merge + un-rotation of the row
+// attention.  All three are X [rows x D] times R or R^T with a different way of
+// producing X and storing the result.
+//
+// A CTA holds 32 rows of X in shared memory (float32) and computes 128 output
+// columns in 32-deep chunks of the matrix, 4 x 4 outputs per thread, float32
+// FMA throughout.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "rows.cuh"
+
+namespace oscar {
+namespace {
+
+constexpr int kRows = 32;     // rows of X per CTA
+constexpr int kCols = 128;    // output columns per CTA
+constexpr int kDeep = 32;     // matrix rows staged at a time
+constexpr int kThreads = 256;
+constexpr int kPitch = kCols + 4;
+
+// y[4][4] = X[4 rws + i][:] . M[:][c0 + 4 lane + j] with M = R (trans = false) or R^T.
+__device__ __forceinline__ void rows_product(const float* X, int xpitch, const float* __restrict__ R, int D, int c0,
+                                             bool trans, bool hadamard, float* Ms, float (&y)[4][4]) {
+  const int lane = threadIdx.x & 31, rw = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[i][j] = 0.f;
+  for (int k0 = 0; k0 < D; k0 += kDeep) {
+    __syncthreads();  // the previous chunk (or X) is complete
+    for (int i = threadIdx.x; i < kDeep * kCols; i += kThreads) {
+      const int k = trans ? i % kDeep : i / kCols, c = trans ? i / kDeep : i % kCols;
+      float v;
+      if (hadamard) v = hadamard_at(k0 + k, c0 + c);
+      else v = trans ? __ldg(R + int64_t(c0 + c) * D + k0 + k) : __ldg(R + int64_t(k0 + k) * D + c0 + c);
+      Ms[k * kPitch + c] = v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kDeep; k += 4) {
+      float x[4][4], m[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        *reinterpret_cast<float4*>(x[i]) = *reinterpret_cast<const float4*>(X + (4 * rw + i) * xpitch + k0 + k);
+        *reinterpret_cast<float4*>(m[i]) = *reinterpret_cast<const float4*>(Ms + (k + i) * kPitch + 4 * lane);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[i][j] = fmaf(x[i][e], m[e][j], y[i][j]);
+    }
+  }
+}
+
+__device__ __forceinline__ void store4(void* out, int64_t at, int fp32, const float (&v)[4]) {
+  if (fp32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
+        make_uint2(pack_bf162(__float2bfloat16_rn(v[0]), __float2bfloat16_rn(v[1])),
+                   pack_bf162(__float2bfloat16_rn(v[2]), __float2bfloat16_rn(v[3])));
+  }
+}
+
+// Row (b n + t) Hq + head of a query block is one of the sequence's tokens.
+__device__ __forceinline__ bool row_live(int64_t row, int64_t rows, const int32_t* q_lens, int n, int Hq) {
+  if (row >= rows) return false;
+  if (!q_lens) return true;
+  const int64_t bt = row / Hq;
+  return int(bt % n) < q_lens[bt / n];
+}
+
+// ------------------------------------------------------------------- kv_read
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadArgs a) {
+  extern __shared__ float sm[];
+  const Geom& g = a.g;
+  const int D = g.D, role = blockIdx.z, xp = D + 4;
+  float* X = sm;
+  float* Ms = sm + kRows * xp;
+  void* out = role ? a.v_out : a.k_out;
+  if (!out) return;
+  const int64_t rows = int64_t(g.B) * a.n * g.Hkv, row0 = int64_t(blockIdx.x) * kRows;
+  for (int i = threadIdx.x; i < kRows * (D / 16); i += kThreads) {
+    const int r = i / (D / 16), w = i % (D / 16);
+    const int64_t row = row0 + r;
+    bool ok = row < rows;
+    if (ok) {
+      const int h = int(row % g.Hkv);
+      const int64_t bt = row / g.Hkv;
+      const int b = int(bt / a.n), t = int(bt % a.n);
+      int T = a.seq_lens[b];
+      if (T > g.cap) {
+        status_or(a.status, OSCAR_DEV_OVER_CAPACITY);
+        T = g.cap;
+      }
+      const int64_t p = int64_t(a.start_pos[b]) + t;
+      ok = p >= 0 && p < T;
+      if (ok) row_load16(g, row_ref(g, a.layer_base, role, int64_t(b) * g.Hkv + h, T, int(p)), role, w, X + r * xp);
+    }
+    if (!ok)
+      for (int e = 0; e < 16; ++e) X[r * xp + 16 * w + e] = 0.f;
+  }
+  const int c0 = blockIdx.y * kCols, lane = threadIdx.x & 31, rw = threadIdx.x >> 5;
+  float y[4][4];
+  if (role && a.absorb_v) {
+    __syncthreads();
+    for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < 4; ++j) y[i][j] = X[(4 * rw + i) * xp + c0 + 4 * lane + j];
+  } else {
+    rows_product(X, xp, role ? a.R_V : a.R_K, D, c0, true, a.hadamard != 0, Ms, y);
+  }
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = row0 + 4 * rw + i;
+    if (row >= rows) break;
+    const int64_t bt = row / g.Hkv;
+    const int b = int(bt / a.n);
+    const int64_t p = int64_t(a.start_pos[b]) + bt % a.n;
+    if (p < 0 || p >= min(a.seq_lens[b], g.cap)) continue;  // left as it was
+    store4(out, row * D + c0 + 4 * lane, a.out_fp32, y[i]);
+  }
+}
+
+// ------------------------------------------------------------ query rotation
+__global__ void __launch_bounds__(kThreads) qrot_rows_kernel(const QrotRowsArgs a) {
+  extern __shared__ float sm[];
+  const int D = a.D, xp = D + 4;
+  float* X = sm;
+  float* Ms = sm + kRows * xp;
+  const int64_t row0 = int64_t(blockIdx.x) * kRows;
+  if (a.zero_word && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.zero_word = 0;
+  bool finite = true;
+  for (int i = threadIdx.x; i < kRows * D; i += kThreads) {
+    const int r = i / D, c = i % D;
+    float v = 0.f;
+    if (row_live(row0 + r, a.rows, a.q_lens, a.n, a.Hq)) {
+      const int64_t at = (row0 + r) * D + c;
+      v = a.in_fp32 ? static_cast<const float*>(a.q)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at]);
+      finite &= isfinite(v) != 0;
+    }
+    X[r * xp + c] = v;
+  }
+  if (!finite) status_or(a.status, OSCAR_DEV_NONFINITE);
+  const int c0 = blockIdx.y * kCols, lane = threadIdx.x & 31, rw = threadIdx.x >> 5;
+  float y[4][4];
+  rows_product(X, xp, a.R_K, D, c0, false, a.hadamard != 0, Ms, y);
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = row0 + 4 * rw + i;
+    if (row >= a.rows) break;
+    for (int j = 0; j < 4; ++j) y[i][j] *= a.qscale;
+    store4(a.qrot, row * D + c0 + 4 * lane, 1, y[i]);
+  }
+}
+
+// --------------------------------------------------- merge, un-rotation, store
+__global__ void __launch_bounds__(kThreads) finish_rows_kernel(const FinishArgs a) {
+  extern __shared__ float sm[];
+  __shared__ float wgt[kRows][OSCAR_KV_MAX_SPLITS + 1];  // weight of each partial result over the sum
+  __shared__ int live[kRows];
+  const int D = a.D, xp = D + 4;
+  float* X = sm;
+  float* Ms = sm + kRows * xp;
+  const int64_t row0 = int64_t(blockIdx.x) * kRows;
+  if (a.own_status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    // an empty cache of its own is not an error when the prefix has positions
+    const int32_t st = *a.own_status & ~OSCAR_DEV_EMPTY;
+    if (st) status_or(a.status, st);
+  }
+  for (int r = threadIdx.x; r < kRows; r += kThreads) {
+    const int64_t row = row0 + r;
+    const bool ok = row_live(row, a.rows, a.q_lens, a.n, a.Hq);
+    live[r] = ok;
+    if (!ok) continue;
+    float m = -INFINITY;
+    for (int s = 0; s < a.ns; ++s)
+      if (a.ml[(row * a.ns + s) * 2 + 1] != 0.f) m = fmax_nan(m, a.ml[(row * a.ns + s) * 2]);
+    float ol = -INFINITY;
+    if (a.own_lse) {
+      ol = a.own_lse[row] * 1.4426950408889634f;
+      m = fmax_nan(m, ol);
+    }
+    float sum = 0.f;
+    for (int s = 0; s < a.ns; ++s) {
+      const float l = a.ml[(row * a.ns + s) * 2 + 1];
+      const float w = l != 0.f ? exp2f(a.ml[(row * a.ns + s) * 2] - m) : 0.f;
+      wgt[r][s] = w;
+      sum += w * l;
+    }
+    const float wo = ol != -INFINITY ? exp2f(ol - m) : 0.f;
+    sum += wo;
+    const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+    // a partial result without weight is not read, also where another one made the sum NaN
+    for (int s = 0; s < a.ns; ++s) wgt[r][s] = wgt[r][s] != 0.f ? wgt[r][s] * inv : 0.f;
+    wgt[r][a.ns] = wo != 0.f ? wo * inv : 0.f;
+    if (blockIdx.y == 0) {
+      if (sum == 0.f) status_or(a.status, OSCAR_DEV_EMPTY);
+      if (a.lse) a.lse[row] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live[r]) {
+      const int64_t row = row0 + r;
+      for (int s = 0; s <= a.ns; ++s) {
+        const float w = wgt[r][s];
+        if (w == 0.f) continue;
+        const float4 x = *reinterpret_cast<const float4*>(s < a.ns ? a.acc + (row * a.ns + s) * D + c : a.own_o + row * D + c);
+        v.x = fmaf(w, x.x, v.x);
+        v.y = fmaf(w, x.y, v.y);
+        v.z = fmaf(w, x.z, v.z);
+        v.w = fmaf(w, x.w, v.w);
+      }
+    }
+    *reinterpret_cast<float4*>(X + r * xp + c) = v;
+  }
+  const int c0 = blockIdx.y * kCols, lane = threadIdx.x & 31, rw = threadIdx.x >> 5;
+  float y[4][4];
+  if (a.absorb_v) {
+    __syncthreads();
+    for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < 4; ++j) y[i][j] = X[(4 * rw + i) * xp + c0 + 4 * lane + j];
+  } else {
+    rows_product(X, xp, a.R_V, D, c0, true, a.hadamard != 0, Ms, y);
+  }
+  for (int i = 0; i < 4; ++i)
+    if (live[4 * rw + i]) store4(a.out, (row0 + 4 * rw + i) * D + c0 + 4 * lane, a.out_fp32, y[i]);
+}
+
+size_t smem_of(int D) { return size_t(kRows * (D + 4) + kDeep * kPitch) * 4; }
+
+// Raises the dynamic shared memory limit of the three kernels, once per device.
+bool ready() {
+  static bool done[64] = {false};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
+  if (done[dev]) return true;
+  const int most = int(smem_of(512));
+  if (cudaFuncSetAttribute(kv_read_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+      cudaFuncSetAttribute(qrot_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+      cudaFuncSetAttribute(finish_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+    return false;
+  done[dev] = true;
+  return true;
+}
+
+int launched() { return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH; }
+
+}  // namespace
+
+int launch_read(const ReadArgs& a, cudaStream_t stream) {
+  const int64_t tiles = (int64_t(a.g.B) * a.n * a.g.Hkv + kRows - 1) / kRows;
+  if (tiles == 0) return OSCAR_OK;
+  if (tiles >= (int64_t(1) << 31)) return OSCAR_ERR_UNSUPPORTED;
+  if (!ready()) return OSCAR_ERR_LAUNCH;
+  kv_read_kernel<<<dim3(unsigned(tiles), a.g.Dg, 2), kThreads, smem_of(a.g.D), stream>>>(a);
+  return launched();
+}
+
+int launch_qrot_rows(const QrotRowsArgs& a, cudaStream_t stream) {
+  if (!ready()) return OSCAR_ERR_LAUNCH;
+  qrot_rows_kernel<<<dim3(unsigned((a.rows + kRows - 1) / kRows), a.D / kCols), kThreads, smem_of(a.D), stream>>>(a);
+  return launched();
+}
+
+int launch_finish_rows(const FinishArgs& a, cudaStream_t stream) {
+  if (!ready()) return OSCAR_ERR_LAUNCH;
+  finish_rows_kernel<<<dim3(unsigned((a.rows + kRows - 1) / kRows), a.D / kCols), kThreads, smem_of(a.D), stream>>>(a);
+  return launched();
+}
+
+}  // namespace oscar

@@ -170,6 +170,107 @@ int prep_decode(const oscar_kv_config* cfg, const void* cache, int32_t layer, co
   return OSCAR_OK;
 }
 
+// Workspace of the row attention: rotated queries and ns partial results per query row.
+uint64_t rows_workspace(const Geom& g, int64_t rows, int ns) {
+  return oscar::align256(uint64_t(rows) * g.D * 4) + oscar::align256(uint64_t(rows) * ns * g.D * 4) +
+         oscar::align256(uint64_t(rows) * ns * 8);
+}
+
+// Takes `bytes` from the workspace at *ws.
+template <typename T>
+T* take(uint8_t** ws, uint64_t bytes) {
+  T* p = reinterpret_cast<T*>(*ws);
+  *ws += oscar::align256(bytes);
+  return p;
+}
+
+float log2_scale(const Geom& g, float sm_scale) {
+  return (sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt(float(g.D))) * 1.4426950408889634f;
+}
+
+// attn_extend's and attn_decode_prefix's common part: query rotation, row
+// attention and the merge, laid out in the workspace at *ws.
+struct RowsPlan {
+  oscar::QrotRowsArgs q;
+  oscar::RowsArgs at;
+  oscar::FinishArgs fin;
+};
+void plan_rows(const oscar_kv_config* cfg, const Geom& g, const void* cache, int32_t layer, const void* q, int n,
+               const int32_t* seq_lens, const int32_t* q_lens, const float* R_K, const float* R_V, float sm_scale, int ns,
+               void* out, float* lse, int32_t* dev_status, uint8_t** ws, RowsPlan* p) {
+  std::memset(p, 0, sizeof(*p));
+  const int64_t rows = int64_t(g.B) * n * g.Hq;
+  const int hadamard = (cfg->flags & OSCAR_FLAG_HADAMARD) ? 1 : 0;
+  p->q.q = q;
+  p->q.qrot = take<float>(ws, uint64_t(rows) * g.D * 4);
+  p->q.R_K = R_K;
+  p->q.status = dev_status;
+  p->q.q_lens = q_lens;
+  p->q.rows = rows;
+  p->q.n = n;
+  p->q.Hq = g.Hq;
+  p->q.D = g.D;
+  p->q.in_fp32 = (cfg->flags & OSCAR_FLAG_IN_FP32) ? 1 : 0;
+  p->q.hadamard = hadamard;
+  p->q.qscale = log2_scale(g, sm_scale);
+  p->at.g = g;
+  p->at.layer_base = static_cast<const uint8_t*>(cache) + uint64_t(layer) * g.layer_bytes;
+  p->at.seq_lens = seq_lens;
+  p->at.q_lens = q_lens;
+  p->at.qrot = p->q.qrot;
+  p->at.acc = take<float>(ws, uint64_t(rows) * ns * g.D * 4);
+  p->at.ml = take<float>(ws, uint64_t(rows) * ns * 8);
+  p->at.status = dev_status;
+  p->at.n = n;
+  p->at.ns = ns;
+  p->fin.acc = p->at.acc;
+  p->fin.ml = p->at.ml;
+  p->fin.q_lens = q_lens;
+  p->fin.R_V = R_V;
+  p->fin.out = out;
+  p->fin.lse = lse;
+  p->fin.status = dev_status;
+  p->fin.rows = rows;
+  p->fin.n = n;
+  p->fin.Hq = g.Hq;
+  p->fin.D = g.D;
+  p->fin.ns = ns;
+  p->fin.out_fp32 = (cfg->flags & OSCAR_FLAG_OUT_FP32) ? 1 : 0;
+  p->fin.absorb_v = (cfg->flags & OSCAR_FLAG_ABSORB_V) ? 1 : 0;
+  p->fin.hadamard = hadamard;
+}
+
+// The row kernels count rows and workspace slots in ranges of these limits.
+bool rows_supported(const Geom& g, int64_t n) { return n * g.G < (int64_t(1) << 30) && g.B * n * g.Hq < (int64_t(1) << 31); }
+
+// The largest split count up to `want` whose workspace fits, 0 if none does;
+// an explicit count has to fit in full.
+int fit_splits(const Geom& g, int64_t rows, int want, bool explicit_count, uint64_t bytes) {
+  int ns = want;
+  if (!explicit_count)
+    while (ns > 1 && rows_workspace(g, rows, ns) > bytes) --ns;
+  return rows_workspace(g, rows, ns) > bytes ? 0 : ns;
+}
+
+// The prefix cache has the shape of the sequences' own, with one sequence.
+int validate_prefix(const oscar_kv_config* cfg, const oscar_kv_config* pcfg) {
+  int v = validate(cfg);
+  if (v != OSCAR_OK) return v;
+  v = validate(pcfg);
+  if (v != OSCAR_OK) return v;
+  if (pcfg->batch != 1 || pcfg->num_q_heads != cfg->num_q_heads || pcfg->num_kv_heads != cfg->num_kv_heads ||
+      pcfg->head_dim != cfg->head_dim || pcfg->flags != cfg->flags)
+    return OSCAR_ERR_INVALID;
+  return rows_supported(make_geom(pcfg), cfg->batch) ? OSCAR_OK : OSCAR_ERR_UNSUPPORTED;
+}
+
+// Workspace of attn_decode_prefix apart from the row attention's: the own
+// caches' outputs, lse and status word.
+uint64_t own_workspace(const Geom& g) {
+  const uint64_t bq = uint64_t(g.B) * g.Hq;
+  return oscar::align256(bq * g.D * 4) + oscar::align256(bq * 4) + 256;
+}
+
 }  // namespace
 
 extern "C" {
@@ -235,6 +336,140 @@ int decode_step(const oscar_kv_config* cfg, void* cache, int32_t layer, const vo
   v = oscar::launch_append(aa, st);
   if (v != OSCAR_OK) return v;
   return oscar::launch_decode(ad, st);
+}
+
+int kv_read(const oscar_kv_config* cfg, const void* cache, int32_t layer, const int32_t* start_pos,
+            const int32_t* seq_lens, int32_t n, const float* R_K, const float* R_V, void* k_out, void* v_out,
+            int32_t* dev_status, void* stream) {
+  const int v = validate(cfg);
+  if (v != OSCAR_OK) return v;
+  const bool had = (cfg->flags & OSCAR_FLAG_HADAMARD) != 0;
+  if (had) R_K = R_V = nullptr;
+  if (!cache || !start_pos || !seq_lens || (!had && (!R_K || !R_V)) || (!k_out && !v_out)) return OSCAR_ERR_INVALID;
+  if (layer < 0 || layer >= cfg->num_layers || n < 0) return OSCAR_ERR_INVALID;
+  if (!aligned(cache, 256) || !aligned(R_K, 16) || !aligned(R_V, 16) || !aligned(k_out, 16) || !aligned(v_out, 16))
+    return OSCAR_ERR_INVALID;
+  oscar::ReadArgs a;
+  a.g = make_geom(cfg);
+  a.layer_base = static_cast<const uint8_t*>(cache) + uint64_t(layer) * a.g.layer_bytes;
+  a.start_pos = start_pos;
+  a.seq_lens = seq_lens;
+  a.R_K = R_K;
+  a.R_V = R_V;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.status = dev_status;
+  a.n = n;
+  a.out_fp32 = (cfg->flags & OSCAR_FLAG_OUT_FP32) ? 1 : 0;
+  a.absorb_v = (cfg->flags & OSCAR_FLAG_ABSORB_V) ? 1 : 0;
+  a.hadamard = had ? 1 : 0;
+  return oscar::launch_read(a, static_cast<cudaStream_t>(stream));
+}
+
+int attn_extend_workspace_query(const oscar_kv_config* cfg, int32_t n_new, uint64_t* bytes) {
+  const int v = validate(cfg);
+  if (v != OSCAR_OK) return v;
+  if (!bytes || n_new < 0) return OSCAR_ERR_INVALID;
+  if (n_new > cfg->capacity) return OSCAR_ERR_CAPACITY;
+  const Geom g = make_geom(cfg);
+  if (!rows_supported(g, n_new)) return OSCAR_ERR_UNSUPPORTED;
+  *bytes = n_new == 0 ? 0 : rows_workspace(g, int64_t(g.B) * n_new * g.Hq, oscar::rows_splits(g, int64_t(n_new) * g.G, g.cap));
+  return OSCAR_OK;
+}
+
+int attn_extend(const oscar_kv_config* cfg, const void* cache, int32_t layer, const void* q, int32_t n_new,
+                const int32_t* q_lens, const int32_t* seq_lens, int32_t seq_len_hint, const float* R_K,
+                const float* R_V, float sm_scale, int32_t num_splits, void* out, float* lse, void* workspace,
+                uint64_t workspace_bytes, int32_t* dev_status, void* stream) {
+  const int v = validate(cfg);
+  if (v != OSCAR_OK) return v;
+  const bool had = (cfg->flags & OSCAR_FLAG_HADAMARD) != 0;
+  if (had) R_K = R_V = nullptr;
+  if (!cache || !q || !seq_lens || (!had && (!R_K || !R_V)) || !out || !workspace) return OSCAR_ERR_INVALID;
+  if (layer < 0 || layer >= cfg->num_layers || n_new < 0 || num_splits < 0 || num_splits > OSCAR_KV_MAX_SPLITS ||
+      seq_len_hint < 0)
+    return OSCAR_ERR_INVALID;
+  if (!aligned(cache, 256) || !aligned(workspace, 256) || !aligned(R_K, 16) || !aligned(R_V, 16) ||
+      !aligned(q, 16) || !aligned(out, 16))
+    return OSCAR_ERR_INVALID;
+  if (n_new > cfg->capacity || seq_len_hint > cfg->capacity) return OSCAR_ERR_CAPACITY;
+  const Geom g = make_geom(cfg);
+  if (!rows_supported(g, n_new)) return OSCAR_ERR_UNSUPPORTED;
+  if (n_new == 0) return OSCAR_OK;
+  const int hint = seq_len_hint > 0 ? seq_len_hint : cfg->capacity;
+  const int want = num_splits > 0 ? num_splits : oscar::rows_splits(g, int64_t(n_new) * g.G, hint);
+  const int ns = fit_splits(g, int64_t(g.B) * n_new * g.Hq, want, num_splits > 0, workspace_bytes);
+  if (ns == 0) return OSCAR_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  RowsPlan p;
+  plan_rows(cfg, g, cache, layer, q, n_new, seq_lens, q_lens, R_K, R_V, sm_scale, ns, out, lse, dev_status, &ws, &p);
+  p.at.causal = 1;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int rc = oscar::launch_qrot_rows(p.q, st);
+  if (rc == OSCAR_OK) rc = oscar::launch_attn_rows(p.at, st);
+  if (rc == OSCAR_OK) rc = oscar::launch_finish_rows(p.fin, st);
+  return rc;
+}
+
+int attn_decode_prefix_workspace_query(const oscar_kv_config* cfg, const oscar_kv_config* prefix_cfg,
+                                       uint64_t* bytes) {
+  const int v = validate_prefix(cfg, prefix_cfg);
+  if (v != OSCAR_OK) return v;
+  if (!bytes) return OSCAR_ERR_INVALID;
+  const Geom g = make_geom(cfg), pg = make_geom(prefix_cfg);
+  *bytes = rows_workspace(pg, int64_t(g.B) * g.Hq, oscar::rows_splits(pg, int64_t(g.B) * g.G, pg.cap)) +
+           own_workspace(g) + oscar::decode_workspace_bytes(g, OSCAR_KV_MAX_SPLITS);
+  return OSCAR_OK;
+}
+
+int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const oscar_kv_config* prefix_cfg,
+                       const void* prefix_cache, int32_t layer, const void* q, const int32_t* seq_lens,
+                       int32_t seq_len_hint, const int32_t* prefix_len, int32_t prefix_len_hint, const float* R_K,
+                       const float* R_V, float sm_scale, int32_t num_splits, void* out, float* lse, void* workspace,
+                       uint64_t workspace_bytes, int32_t* dev_status, void* stream) {
+  int v = validate_prefix(cfg, prefix_cfg);
+  if (v != OSCAR_OK) return v;
+  if (cfg->flags & OSCAR_FLAG_HADAMARD) R_K = R_V = nullptr;
+  if (!prefix_cache || !prefix_len || !workspace || !out) return OSCAR_ERR_INVALID;
+  if (layer < 0 || layer >= prefix_cfg->num_layers || num_splits < 0 || num_splits > OSCAR_KV_MAX_SPLITS ||
+      prefix_len_hint < 0)
+    return OSCAR_ERR_INVALID;
+  if (!aligned(prefix_cache, 256) || !aligned(workspace, 256) || !aligned(out, 16)) return OSCAR_ERR_INVALID;
+  if (prefix_len_hint > prefix_cfg->capacity) return OSCAR_ERR_CAPACITY;
+  const Geom g = make_geom(cfg), pg = make_geom(prefix_cfg);
+  const int64_t rows = int64_t(g.B) * g.Hq;
+  const int hint = prefix_len_hint > 0 ? prefix_len_hint : prefix_cfg->capacity;
+  const int want = num_splits > 0 ? num_splits : oscar::rows_splits(pg, int64_t(g.B) * g.G, hint);
+  // the own caches' part has to fit with one split at least; what is left goes to the prefix
+  const uint64_t own = own_workspace(g) + oscar::decode_workspace_bytes(g, 1);
+  const int ns =
+      workspace_bytes < own ? 0 : fit_splits(pg, rows, want, num_splits > 0, workspace_bytes - own);
+  if (ns == 0) return OSCAR_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  RowsPlan p;
+  // one query token per sequence: the batch is the block of query rows of the one prefix
+  plan_rows(cfg, pg, prefix_cache, layer, q, g.B, prefix_len, nullptr, R_K, R_V, sm_scale, ns, out, lse, dev_status, &ws,
+            &p);
+  float* own_o = take<float>(&ws, uint64_t(rows) * g.D * 4);
+  float* own_lse = take<float>(&ws, uint64_t(rows) * 4);
+  int32_t* own_status = take<int32_t>(&ws, 256);
+  p.q.zero_word = own_status;
+  p.fin.own_o = own_o;
+  p.fin.own_lse = own_lse;
+  p.fin.own_status = own_status;
+  // the own caches through attn_decode's kernels, in the rotated basis and float32
+  oscar_kv_config dcfg = *cfg;
+  dcfg.flags |= OSCAR_FLAG_ABSORB_V | OSCAR_FLAG_OUT_FP32;
+  oscar::DecodeArgs d;
+  v = prep_decode(&dcfg, cache, layer, q, seq_lens, seq_len_hint, R_K, R_V, sm_scale, 0, own_o, own_lse, ws,
+                  workspace_bytes - uint64_t(ws - static_cast<uint8_t*>(workspace)), own_status, &d);
+  if (v != OSCAR_OK) return v;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int rc = oscar::launch_qrot_rows(p.q, st);
+  if (rc == OSCAR_OK) rc = oscar::launch_attn_rows(p.at, st);
+  if (rc == OSCAR_OK) rc = oscar::launch_decode(d, st);
+  if (rc == OSCAR_OK) rc = oscar::launch_finish_rows(p.fin, st);
+  return rc;
 }
 
 int oscar_kv_set_profile_events(void* split_start, void* split_stop) {

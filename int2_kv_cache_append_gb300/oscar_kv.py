@@ -31,7 +31,8 @@ DEV_EMPTY = 16
 STATUS_NAMES = {0: "OK", -1: "INVALID", -2: "CAPACITY", -3: "WORKSPACE", -4: "LAUNCH", -5: "UNSUPPORTED"}
 
 # every symbol include/oscar_kv.h declares
-EXPORTS = ("kv_layout_query", "kv_append", "attn_decode", "decode_step", "attn_decode_static",
+EXPORTS = ("kv_layout_query", "kv_append", "attn_decode", "decode_step", "attn_decode_static", "kv_read",
+           "attn_extend_workspace_query", "attn_extend", "attn_decode_prefix_workspace_query", "attn_decode_prefix",
            "oscar_kv_set_profile_events", "oscar_kv_set_wait_test", "oscar_kv_decode_kernels",
            "oscar_calibrate_workspace_query",
            "oscar_calibrate_rk",
@@ -105,6 +106,21 @@ def lib():
         L.decode_step.argtypes = [ctypes.POINTER(_Config), P, ctypes.c_int32, P, P, P, ctypes.c_int32, P, P,
                                   ctypes.c_int32, P, P, ctypes.c_float, ctypes.c_int32, P, P, P, ctypes.c_uint64, P, P]
         L.decode_step.restype = ctypes.c_int
+        L.kv_read.argtypes = [ctypes.POINTER(_Config), P, ctypes.c_int32, P, P, ctypes.c_int32, P, P, P, P, P, P]
+        L.kv_read.restype = ctypes.c_int
+        L.attn_extend_workspace_query.argtypes = [ctypes.POINTER(_Config), ctypes.c_int32,
+                                                  ctypes.POINTER(ctypes.c_uint64)]
+        L.attn_extend_workspace_query.restype = ctypes.c_int
+        L.attn_extend.argtypes = [ctypes.POINTER(_Config), P, ctypes.c_int32, P, ctypes.c_int32, P, P, ctypes.c_int32,
+                                  P, P, ctypes.c_float, ctypes.c_int32, P, P, P, ctypes.c_uint64, P, P]
+        L.attn_extend.restype = ctypes.c_int
+        L.attn_decode_prefix_workspace_query.argtypes = [ctypes.POINTER(_Config), ctypes.POINTER(_Config),
+                                                         ctypes.POINTER(ctypes.c_uint64)]
+        L.attn_decode_prefix_workspace_query.restype = ctypes.c_int
+        L.attn_decode_prefix.argtypes = [ctypes.POINTER(_Config), P, ctypes.POINTER(_Config), P, ctypes.c_int32, P, P,
+                                         ctypes.c_int32, P, ctypes.c_int32, P, P, ctypes.c_float, ctypes.c_int32, P, P,
+                                         P, ctypes.c_uint64, P, P]
+        L.attn_decode_prefix.restype = ctypes.c_int
         L.oscar_kv_set_profile_events.argtypes = [P, P]
         L.oscar_kv_set_profile_events.restype = ctypes.c_int
         L.oscar_kv_set_wait_test.argtypes = [ctypes.c_uint64, ctypes.c_int32]
@@ -268,6 +284,110 @@ def attn_decode_static(cfg: KVConfig, cache, layer: int, q, seq_lens, R_K, R_V, 
                                   _ptr(out), _ptr(lse), _ptr(status), _stream(stream))
     if check and rc != 0:
         raise OscarError("attn_decode_static", rc)
+    return rc
+
+
+def _same_device(*tensors) -> None:
+    """The library launches on the current device: refuse tensors that live on another one."""
+    torch = _dt()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"oscar_kv: tensor on {t.device}, current device is cuda:{torch.cuda.current_device()}")
+
+
+def kv_read(cfg: KVConfig, cache, layer: int, start_pos, seq_lens, R_K, R_V, k_out=None, v_out=None, status=None,
+            stream=None, check: bool = True) -> int:
+    """Positions [start_pos[b], start_pos[b] + n) of every sequence back into k_out / v_out ([B][n][Hkv][D]; either
+    may be None), in the basis the rows were appended in.  Positions outside [0, seq_lens[b]) are left as they were."""
+    torch = _dt()
+    B, H, D = cfg.batch, cfg.num_kv_heads, cfg.head_dim
+    first = k_out if k_out is not None else v_out
+    if first is None or first.dim() != 4:
+        raise ValueError("oscar_kv: k_out or v_out must be [batch][n][num_kv_heads][head_dim]")
+    n = int(first.shape[1])
+    kind = (torch.float32,) if cfg.flags & FLAG_OUT_FP32 else (torch.bfloat16,)
+    _check(k_out, "k_out", kind, shape=(B, n, H, D), optional=True)
+    _check(v_out, "v_out", kind, shape=(B, n, H, D), optional=True)
+    _check(start_pos, "start_pos", (torch.int32,), shape=(B,))
+    _check(seq_lens, "seq_lens", (torch.int32,), shape=(B,))
+    _check(status, "status", (torch.int32,), min_bytes=4, optional=True)
+    _check_cache(cfg, cache)
+    _check_rot(cfg, R_K, "R_K")
+    _check_rot(cfg, R_V, "R_V")
+    _same_device(cache, start_pos, seq_lens, R_K, R_V, k_out, v_out, status)
+    rc = lib().kv_read(ctypes.byref(cfg.c()), _ptr(cache), layer, _ptr(start_pos), _ptr(seq_lens), n, _ptr(R_K),
+                       _ptr(R_V), _ptr(k_out), _ptr(v_out), _ptr(status), _stream(stream))
+    if check and rc != 0:
+        raise OscarError("kv_read", rc)
+    return rc
+
+
+def attn_extend_workspace_bytes(cfg: KVConfig, n_new: int) -> int:
+    n = ctypes.c_uint64(0)
+    rc = lib().attn_extend_workspace_query(ctypes.byref(cfg.c()), int(n_new), ctypes.byref(n))
+    if rc != 0:
+        raise OscarError("attn_extend_workspace_query", rc)
+    return int(n.value)
+
+
+def attn_extend(cfg: KVConfig, cache, layer: int, q, seq_lens, R_K, R_V, out, workspace, q_lens=None, lse=None,
+                seq_len_hint: int = 0, sm_scale: float = 0.0, num_splits: int = 0, status=None, stream=None,
+                check: bool = True) -> int:
+    """Causal attention of the last q_lens[b] (None: n) tokens of every sequence, q [B][n][Hq][D], over its cache
+    (append their K and V first).  Rows t >= q_lens[b] of out and lse ([B][n][Hq]) are left as they were."""
+    torch = _dt()
+    B, Hq, D = cfg.batch, cfg.num_q_heads, cfg.head_dim
+    if q is None or q.dim() != 4:
+        raise ValueError("oscar_kv: q must be [batch][n_new][num_q_heads][head_dim]")
+    n = int(q.shape[1])
+    _check(q, "q", _in_dtypes(cfg), shape=(B, n, Hq, D))
+    _check(out, "out", (torch.float32,) if cfg.flags & FLAG_OUT_FP32 else (torch.bfloat16,), shape=(B, n, Hq, D))
+    _check(lse, "lse", (torch.float32,), shape=(B, n, Hq), optional=True)
+    _check(seq_lens, "seq_lens", (torch.int32,), shape=(B,))
+    _check(q_lens, "q_lens", (torch.int32,), shape=(B,), optional=True)
+    _check(status, "status", (torch.int32,), min_bytes=4, optional=True)
+    _check(workspace, "workspace", (torch.uint8,))
+    _check_cache(cfg, cache)
+    _check_rot(cfg, R_K, "R_K")
+    _check_rot(cfg, R_V, "R_V")
+    _same_device(cache, q, seq_lens, q_lens, R_K, R_V, out, lse, workspace, status)
+    rc = lib().attn_extend(ctypes.byref(cfg.c()), _ptr(cache), layer, _ptr(q), n, _ptr(q_lens), _ptr(seq_lens),
+                           int(seq_len_hint), _ptr(R_K), _ptr(R_V), float(sm_scale), int(num_splits), _ptr(out),
+                           _ptr(lse), _ptr(workspace), int(workspace.numel()), _ptr(status), _stream(stream))
+    if check and rc != 0:
+        raise OscarError("attn_extend", rc)
+    return rc
+
+
+def attn_decode_prefix_workspace_bytes(cfg: KVConfig, prefix_cfg: KVConfig) -> int:
+    n = ctypes.c_uint64(0)
+    rc = lib().attn_decode_prefix_workspace_query(ctypes.byref(cfg.c()), ctypes.byref(prefix_cfg.c()), ctypes.byref(n))
+    if rc != 0:
+        raise OscarError("attn_decode_prefix_workspace_query", rc)
+    return int(n.value)
+
+
+def attn_decode_prefix(cfg: KVConfig, cache, prefix_cfg: KVConfig, prefix_cache, layer: int, q, seq_lens, prefix_len,
+                       R_K, R_V, out, workspace, lse=None, seq_len_hint: int = 0, prefix_len_hint: int = 0,
+                       sm_scale: float = 0.0, num_splits: int = 0, status=None, stream=None, check: bool = True) -> int:
+    """attn_decode over a prefix that the whole batch shares (prefix_cache, one sequence of prefix_len[0] positions)
+    followed by every sequence's own cache (seq_lens[b] positions, 0 allowed)."""
+    torch = _dt()
+    _check_decode_io(cfg, q, seq_lens, out, lse, status)
+    _check(prefix_len, "prefix_len", (torch.int32,), shape=(1,))
+    _check_cache(cfg, cache)
+    _check(prefix_cache, "prefix_cache", (torch.uint8,), min_bytes=layout_query(prefix_cfg)["total_bytes"])
+    _check_rot(cfg, R_K, "R_K")
+    _check_rot(cfg, R_V, "R_V")
+    _check(workspace, "workspace", (torch.uint8,))
+    _same_device(cache, prefix_cache, q, seq_lens, prefix_len, R_K, R_V, out, lse, workspace, status)
+    rc = lib().attn_decode_prefix(ctypes.byref(cfg.c()), _ptr(cache), ctypes.byref(prefix_cfg.c()), _ptr(prefix_cache),
+                                  layer, _ptr(q), _ptr(seq_lens), int(seq_len_hint), _ptr(prefix_len),
+                                  int(prefix_len_hint), _ptr(R_K), _ptr(R_V), float(sm_scale), int(num_splits),
+                                  _ptr(out), _ptr(lse), _ptr(workspace), int(workspace.numel()), _ptr(status),
+                                  _stream(stream))
+    if check and rc != 0:
+        raise OscarError("attn_decode_prefix", rc)
     return rc
 
 
