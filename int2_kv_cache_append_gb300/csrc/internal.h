@@ -123,9 +123,11 @@ struct RowsArgs {
   int causal;               // token t sees positions <= seq_len - q_len + t; else every position
 };
 int launch_attn_rows(const RowsArgs& a, cudaStream_t stream);
+int launch_attn_rows_tc(const RowsArgs& a, cudaStream_t stream);  // fp16 products (attn_rows_tc.cu)
 // Splits of every (row tile, unit) for `rows` query rows per unit: enough
 // shares to fill the GPU, none shorter than the context gives.
 int rows_splits(const Geom& g, int64_t rows, int seq_len_hint);
+int rows_splits_tc(const Geom& g, int64_t rows, int seq_len_hint);
 
 // q' = q R_K in log2 units, before the row attention (kv_rows.cu).
 struct QrotRowsArgs {

@@ -240,6 +240,14 @@ void plan_rows(const oscar_kv_config* cfg, const Geom& g, const void* cache, int
   p->fin.hadamard = hadamard;
 }
 
+// The row attention in float32 when the output is float32, else on the tensor cores.
+int splits_of(const oscar_kv_config* cfg, const Geom& g, int64_t rows, int hint) {
+  return (cfg->flags & OSCAR_FLAG_OUT_FP32) ? oscar::rows_splits(g, rows, hint) : oscar::rows_splits_tc(g, rows, hint);
+}
+int launch_rows(const oscar_kv_config* cfg, const oscar::RowsArgs& a, cudaStream_t st) {
+  return (cfg->flags & OSCAR_FLAG_OUT_FP32) ? oscar::launch_attn_rows(a, st) : oscar::launch_attn_rows_tc(a, st);
+}
+
 // The row kernels count rows and workspace slots in ranges of these limits.
 bool rows_supported(const Geom& g, int64_t n) { return n * g.G < (int64_t(1) << 30) && g.B * n * g.Hq < (int64_t(1) << 31); }
 
@@ -373,7 +381,7 @@ int attn_extend_workspace_query(const oscar_kv_config* cfg, int32_t n_new, uint6
   if (n_new > cfg->capacity) return OSCAR_ERR_CAPACITY;
   const Geom g = make_geom(cfg);
   if (!rows_supported(g, n_new)) return OSCAR_ERR_UNSUPPORTED;
-  *bytes = n_new == 0 ? 0 : rows_workspace(g, int64_t(g.B) * n_new * g.Hq, oscar::rows_splits(g, int64_t(n_new) * g.G, g.cap));
+  *bytes = n_new == 0 ? 0 : rows_workspace(g, int64_t(g.B) * n_new * g.Hq, splits_of(cfg, g, int64_t(n_new) * g.G, g.cap));
   return OSCAR_OK;
 }
 
@@ -397,7 +405,7 @@ int attn_extend(const oscar_kv_config* cfg, const void* cache, int32_t layer, co
   if (!rows_supported(g, n_new)) return OSCAR_ERR_UNSUPPORTED;
   if (n_new == 0) return OSCAR_OK;
   const int hint = seq_len_hint > 0 ? seq_len_hint : cfg->capacity;
-  const int want = num_splits > 0 ? num_splits : oscar::rows_splits(g, int64_t(n_new) * g.G, hint);
+  const int want = num_splits > 0 ? num_splits : splits_of(cfg, g, int64_t(n_new) * g.G, hint);
   const int ns = fit_splits(g, int64_t(g.B) * n_new * g.Hq, want, num_splits > 0, workspace_bytes);
   if (ns == 0) return OSCAR_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -406,7 +414,7 @@ int attn_extend(const oscar_kv_config* cfg, const void* cache, int32_t layer, co
   p.at.causal = 1;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int rc = oscar::launch_qrot_rows(p.q, st);
-  if (rc == OSCAR_OK) rc = oscar::launch_attn_rows(p.at, st);
+  if (rc == OSCAR_OK) rc = launch_rows(cfg, p.at, st);
   if (rc == OSCAR_OK) rc = oscar::launch_finish_rows(p.fin, st);
   return rc;
 }
@@ -417,7 +425,7 @@ int attn_decode_prefix_workspace_query(const oscar_kv_config* cfg, const oscar_k
   if (v != OSCAR_OK) return v;
   if (!bytes) return OSCAR_ERR_INVALID;
   const Geom g = make_geom(cfg), pg = make_geom(prefix_cfg);
-  *bytes = rows_workspace(pg, int64_t(g.B) * g.Hq, oscar::rows_splits(pg, int64_t(g.B) * g.G, pg.cap)) +
+  *bytes = rows_workspace(pg, int64_t(g.B) * g.Hq, splits_of(cfg, pg, int64_t(g.B) * g.G, pg.cap)) +
            own_workspace(g) + oscar::decode_workspace_bytes(g, OSCAR_KV_MAX_SPLITS);
   return OSCAR_OK;
 }
@@ -439,7 +447,7 @@ int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const osca
   const Geom g = make_geom(cfg), pg = make_geom(prefix_cfg);
   const int64_t rows = int64_t(g.B) * g.Hq;
   const int hint = prefix_len_hint > 0 ? prefix_len_hint : prefix_cfg->capacity;
-  const int want = num_splits > 0 ? num_splits : oscar::rows_splits(pg, int64_t(g.B) * g.G, hint);
+  const int want = num_splits > 0 ? num_splits : splits_of(cfg, pg, int64_t(g.B) * g.G, hint);
   // the own caches' part has to fit with one split at least; what is left goes to the prefix
   const uint64_t own = own_workspace(g) + oscar::decode_workspace_bytes(g, 1);
   const int ns =
@@ -466,7 +474,7 @@ int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const osca
   if (v != OSCAR_OK) return v;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int rc = oscar::launch_qrot_rows(p.q, st);
-  if (rc == OSCAR_OK) rc = oscar::launch_attn_rows(p.at, st);
+  if (rc == OSCAR_OK) rc = launch_rows(cfg, p.at, st);
   if (rc == OSCAR_OK) rc = oscar::launch_decode(d, st);
   if (rc == OSCAR_OK) rc = oscar::launch_finish_rows(p.fin, st);
   return rc;
