@@ -1,0 +1,409 @@
+// Attention of blocks of query rows over one cache on the 5th-generation tensor
+// cores, head_dim 128, query rows in the TMEM lanes: the kernel behind
+// attn_extend and attn_decode_prefix for a bf16 output and more than 64 query
+// rows per (sequence, KV head).
+//
+// A CTA holds 128 rotated query rows and walks its share of the positions 128 at
+// a time:
+//
+//   S [128 rows x 128 tokens] = Q K^T,   O [128 rows x 128 channels] += P V
+//
+// The arithmetic is that of the token-lane kernel (attn_rows_tc.cu): INT2 keys
+// as exact fp16 values with the row's scale and zero applied to the sum, queries
+// as two fp16 values, value rows with an exponent of their own that joins the
+// score.  A row is one thread's, so its maximum and sum need no exchange; its
+// reference M follows the maximum only when that has grown by 2^12 (P is fp16),
+// and then the warp rescales its rows of O.
+//
+// Two softmax groups of four warps take turns: group w has the tiles i = w mod 2
+// with scores S_w, sums O_w and (M, l) of its own, so nothing passes between
+// them until the end, where the two are merged.  P overwrites S in TMEM and is
+// the A operand from there: in shared memory it would take 64 KB of traffic per
+// tile from a budget (128 bytes per clock) that the products already use up.
+#include <algorithm>
+
+#include "rows_tc.cuh"
+
+namespace oscar {
+namespace {
+
+constexpr int N = 128;                  // query rows per CTA
+constexpr int D = 128;
+constexpr int kSoftWarps = 8;
+constexpr int kThreads = (kSoftWarps + 4 + 4 + 1) * 32;
+constexpr float kNone = -1e30f;         // M before the first visible position
+constexpr float kGrow = 12.f;           // log2 of the largest P
+constexpr int KU = 4, VU = 3, CB = 4, kStages = 3;
+constexpr int kQ = N * 256;             // one of Q's two parts
+constexpr int oQ = 0;
+constexpr int oK = 2 * kQ;
+constexpr int oV = oK + KU * kUnit;
+constexpr int oRawK = oV + VU * kUnit;
+constexpr int oRawV = oRawK + kStages * kRawStage;
+constexpr int oConst = oRawV + kStages * kRawStage;
+constexpr int oRow = oConst + CB * TokenConsts<1>::kBytes;  // row index, sum of q; (M, l) of both groups
+constexpr int oBar = oRow + N * 8 + 2 * N * 8;
+constexpr int kBars = 2 * KU + 2 * VU + 2 * CB + 3 * 2 + 2 + 1;
+constexpr int kBytes = oBar + kBars * 8 + 32 + 1024;        // + alignment slack
+static_assert(oBar % 8 == 0 && kBytes <= 232448, "shared memory");
+constexpr uint32_t cS = 0, cO = 256;    // TMEM columns: two score tiles, two output tiles
+
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
+      "[%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a));
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const RowsArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (base - raw);
+  const Geom& g = a.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // item: split s of row tile rt (last tiles first: with a causal mask they are the longest) of unit u
+  const int units = g.B * g.Hkv, rows = a.n * g.G, tiles = (rows + N - 1) / N;
+  const int s = int(blockIdx.x % unsigned(a.ns));
+  const int it = int(blockIdx.x / unsigned(a.ns));
+  const int u = it % units, rt = tiles - 1 - it / units;
+  const int b = u / g.Hkv, h = u % g.Hkv;
+  const int T = row_seq_len(a, b, threadIdx.x == 0 && rt == 0);
+  const int ql = row_q_len(a, b);
+  const int t_first = rt * N / g.G;
+  if (t_first >= ql) return;  // only padding
+  const int t_last = min((rt * N + N - 1) / g.G, ql - 1);
+  const int vis = max(0, a.causal ? min(T, T - ql + t_last + 1) : T);
+  const int see_all = a.causal ? T - ql + t_first : T - 1;  // every row sees the positions up to this one
+  const int blocks = (vis + kTok - 1) / kTok;
+  const int p0 = int(int64_t(blocks) * s / a.ns) * kTok;
+  const int p1 = min(vis, int(int64_t(blocks) * (s + 1) / a.ns) * kTok);
+  const int nt = (p1 - p0 + kTok - 1) / kTok;
+
+  int* outr = reinterpret_cast<int*>(sm + oRow);            // a row's index among all query rows, -1 = none
+  float* qsum = reinterpret_cast<float*>(outr + N);
+  float2* both = reinterpret_cast<float2*>(qsum + N);       // [2][N] (M, l)
+  const uint32_t bar = base + oBar;
+  const uint32_t k_full = bar, k_empty = k_full + 8 * KU, v_full = k_empty + 8 * KU, v_empty = v_full + 8 * VU,
+                 c_full = v_empty + 8 * VU, c_empty = c_full + 8 * CB, s_full = c_empty + 8 * CB, p_full = s_full + 16,
+                 p_done = p_full + 16, q_full = p_done + 16, f_full = q_full + 8, drained = f_full + 8;
+  uint32_t* words = reinterpret_cast<uint32_t*>(sm + oBar + kBars * 8);
+  uint32_t* tmem_slot = words;
+  volatile uint32_t* abort_flag = words + 1;
+  uint32_t* qmax = words + 2;
+  float* scale_f = reinterpret_cast<float*>(words + 3);
+
+  for (int c = threadIdx.x; c < N; c += kThreads) {
+    const int row = rt * N + c, t = row / g.G;
+    const bool live = row < rows && t < ql;
+    outr[c] = live ? (b * a.n + t) * g.Hq + h * g.G + row % g.G : -1;
+    if (nt <= 0 && live) *reinterpret_cast<float2*>(a.ml + (int64_t(outr[c]) * a.ns + s) * 2) = make_float2(kNone, 0.f);
+  }
+  if (nt <= 0) return;  // nothing visible in this share
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < KU; ++i) mbar_init(k_full + 8 * i, 4), mbar_init(k_empty + 8 * i, 1);
+    for (int i = 0; i < VU; ++i) mbar_init(v_full + 8 * i, 4), mbar_init(v_empty + 8 * i, 1);
+    for (int i = 0; i < CB; ++i) mbar_init(c_full + 8 * i, 8), mbar_init(c_empty + 8 * i, 4);
+    for (int i = 0; i < 2; ++i) mbar_init(s_full + 8 * i, 1), mbar_init(p_full + 8 * i, 4), mbar_init(p_done + 8 * i, 1);
+    mbar_init(q_full, kSoftWarps);
+    mbar_init(f_full, kSoftWarps);
+    mbar_init(drained, 1);
+    mbar_fence_init();
+    words[1] = 0;
+    words[2] = 0;
+  }
+  if (warp == kSoftWarps + 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto fail = [&]() {
+    *abort_flag = 1;
+    status_or(a.status, OSCAR_DEV_TIMEOUT);
+  };
+  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity, lane, abort_flag); };
+
+  if (warp < kSoftWarps) {
+    // ------------------------------- softmax ---------------------------------
+    const int grp = warp >> 2, row = threadIdx.x & 127;      // the thread's group and row (TMEM lane)
+    const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;  // the warp's TMEM lanes
+    load_queries<1, N, kSoftWarps>(a, sm + oQ, kQ, outr, qsum, qmax, scale_f, f_full, warp, lane);
+    if (lane == 0) mbar_arrive(q_full);
+
+    const int t_row = (rt * N + row) / g.G;
+    const int lim = outr[row] < 0 ? -1 : a.causal ? T - ql + t_row : T - 1;  // last position that the row sees
+    const uint64_t q2 = splat_x2(qsum[row]);
+    const uint32_t S = tmem + lanes + cS + grp * 128, O = tmem + lanes + cO + grp * 128;
+    float M = kNone;
+    uint64_t l2 = 0;
+    bool ok = true;
+    for (int i = grp; i < nt; i += 2) {
+      const int cb = i % CB, base_pos = p0 + i * kTok;
+      ok = ok && wait(c_full + 8 * cb, (i / CB) & 1);
+      ok = ok && wait(s_full + 8 * grp, (i >> 1) & 1);
+      if (!ok) break;
+      fence_after();
+      const TokenConsts<1> tc(sm + oConst, cb);
+      const bool masked = base_pos + kTok - 1 > see_all;  // some row does not see some position of the tile
+      const bool plain = !masked && *tc.uneven() == 0;
+      const int see = lim - base_pos;                      // columns j <= see are visible
+      const float* ks = tc.ks(0);
+      const float* kz = tc.kz(0);
+      const float* ev = tc.e();
+      const float* rv = tc.rv();
+      // u + n of 32 columns from c on (n = 0 or -M), in pairs
+      auto scores = [&](int c, const uint32_t (&r)[32], uint64_t n2, uint64_t (&x)[16]) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(kz + c + 2 * j);
+          const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(ks + c + 2 * j);
+          x[j] = fma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), k.x, fma2(q2, z.x, n2));
+          x[j + 1] = fma2(pack2(__uint_as_float(r[2 * j + 2]), __uint_as_float(r[2 * j + 3])), k.y, fma2(q2, z.y, n2));
+        }
+        if (!plain) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(ev + c + 2 * j);
+            x[j] = add2(x[j], e.x);
+            x[j + 1] = add2(x[j + 1], e.y);
+          }
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float p, q;
+              unpack2(x[j], p, q);
+              x[j] = pack2(c + 2 * j <= see ? p : -INFINITY, c + 2 * j + 1 <= see ? q : -INFINITY);
+            }
+          }
+        }
+      };
+      // the row's maximum over the tile
+      float top = -INFINITY;
+      {
+        uint32_t r[32];
+        tmem_ld32(S, r);
+#pragma unroll 1
+        for (int c = 0; c < kTok; c += 32) {
+          uint64_t x[16];
+          tmem_wait32(r);
+          scores(c, r, 0, x);
+          if (c + 32 < kTok) tmem_ld32(S + c + 32, r);
+          float top1 = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            float p, q;
+            unpack2(x[j], p, q);
+            top = max3(top, p, q);
+            unpack2(x[j + 1], p, q);
+            top1 = max3(top1, p, q);
+          }
+          top = fmaxf(top, top1);
+        }
+      }
+      const bool grow = top > M + kGrow;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float f = grow ? exp2f(M - top) : 1.f;
+        if (grow) M = top;
+        const uint64_t f2 = splat_x2(f);
+        l2 = mul2(l2, f2);
+        if (i >= 2) {  // S is full again only after the group's previous product is complete
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(O + c, r);
+            tmem_wait32(r);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
+            tmem_st32(O + c, r);
+          }
+        }
+      }
+      // P, over S's columns that have been read
+      const uint64_t n2 = splat_x2(-M);
+      {
+        uint32_t r[32];
+        tmem_ld32(S, r);
+#pragma unroll 1
+        for (int c = 0; c < kTok; c += 32) {
+          uint64_t x[16];
+          uint32_t p[16];
+          tmem_wait32(r);
+          scores(c, r, n2, x);
+          if (c + 32 < kTok) tmem_ld32(S + c + 32, r);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float v, w;
+            unpack2(x[j], v, w);
+            v = ex2(v);
+            w = ex2(w);
+            p[j] = half2_of(v, w);
+            x[j] = pack2(v, w);
+          }
+          if (plain) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) l2 = add2(l2, x[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(rv + c + 2 * j);
+              l2 = fma2(x[j], v.x, l2);
+              l2 = fma2(x[j + 1], v.y, l2);
+            }
+          }
+          tmem_st16(S + c / 2, p);
+        }
+      }
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(p_full + 8 * grp);
+        mbar_arrive(c_empty + 8 * cb);
+      }
+    }
+    // the two groups' results become one
+    if (ok && grp < nt) {
+      const int last = nt - 1 - ((nt - 1 - grp) & 1);
+      ok = wait(p_done + 8 * grp, (last >> 1) & 1);
+    }
+    float l, l1;
+    unpack2(l2, l, l1);
+    l += l1;
+    both[grp * N + row] = make_float2(M, l);
+    if (!ok && lane == 0) fail();
+    asm volatile("bar.sync 3, 256;" ::: "memory");
+    if (__all_sync(0xffffffffu, *abort_flag == 0)) {
+      fence_after();
+      const float2 x = both[row], y = both[N + row];
+      const float top = fmaxf(x.x, y.x), f = exp2f(x.x - top), f1 = exp2f(y.x - top);
+      const int r = outr[row];
+      if (r >= 0 && grp == 0)
+        *reinterpret_cast<float2*>(a.ml + (int64_t(r) * a.ns + s) * 2) = make_float2(top, x.y * f + y.y * f1);
+#pragma unroll 1
+      for (int c = 64 * grp; c < 64 * grp + 64; c += 16) {
+        uint32_t v[16], w[16];
+        tmem_ld16(tmem + lanes + cO + c, v);
+        if (nt > 1) tmem_ld16(tmem + lanes + cO + 128 + c, w);  // with one tile the second group has nothing
+        tmem_wait16(v);
+        if (nt > 1) tmem_wait16(w);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float o = __uint_as_float(v[j]) * f;
+          if (nt > 1) o = fmaf(__uint_as_float(w[j]), f1, o);
+          v[j] = __float_as_uint(o);
+        }
+        if (r >= 0) {
+          uint4* dst = reinterpret_cast<uint4*>(a.acc + (int64_t(r) * a.ns + s) * D + c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dst[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+      }
+    }
+  } else if (warp < kSoftWarps + 8) {
+    Share x{&a, u, T, p0, p1, nt, sm, base, abort_flag, scale_f, f_full, k_full, k_empty, v_full, v_empty, c_full, c_empty,
+            oK, oV, oRawK, oRawV, oConst};
+    const bool ok = warp < kSoftWarps + 4 ? expand_k<1, KU, CB, kStages>(x, threadIdx.x - kSoftWarps * 32, lane)
+                                          : expand_v<1, VU, CB, kStages>(x, warp & 3, lane);
+    if (!ok && lane == 0) fail();
+  } else if (lane == 0) {
+    // ------------------------------ MMA issuer --------------------------------
+    constexpr uint32_t id_qk = idesc_of(kTok, false, false), id_pv = idesc_of(D, false, true);
+    const uint32_t sQ = base + oQ, sK = base + oK, sV = base + oV;
+    auto wait1 = [&](uint32_t br, uint32_t parity) { return *abort_flag == 0 && mbar_wait(br, parity); };
+    auto product_qk = [&](int i) {
+      const uint32_t d = tmem + cS + (i & 1) * 128;
+#pragma unroll 1
+      for (int kb = 0; kb < 2; ++kb) {
+        const int n = 2 * i + kb, st = n % KU;
+        if (!wait1(k_full + 8 * st, (n / KU) & 1)) return false;
+        fence_after();
+        const uint64_t q = desc_of(sQ + kb * (N * 128), 16), k = desc_of(sK + st * kUnit, 16);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)  // Q's high, then its low part; descriptors count 16 bytes
+          mma_f16_ss(d, q + (j >> 2) * (kQ >> 4) + 2 * (j & 3), k + 2 * (j & 3), id_qk, kb | j);
+        mma_commit(k_empty + 8 * st);
+      }
+      mma_commit(s_full + 8 * (i & 1));
+      return true;
+    };
+    auto product_pv = [&](int i) {
+      if (!wait1(p_full + 8 * (i & 1), (i >> 1) & 1)) return false;
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        const int n = 2 * i + k, st = n % VU;
+        if (!wait1(v_full + 8 * st, (n / VU) & 1)) return false;
+        fence_after();
+        const uint64_t v = desc_of(sV + st * kUnit, kUnit / 2);
+        const uint32_t p = tmem + cS + (i & 1) * 128 + 32 * k;  // 64 tokens of P in 32 columns
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mma_f16_ts(tmem + cO + (i & 1) * 128, p + 8 * j, v + 128 * j, id_pv, (i >> 1) | k | j);
+        mma_commit(v_empty + 8 * st);
+      }
+      mma_commit(p_done + 8 * (i & 1));
+      return true;
+    };
+    bool ok = wait1(q_full, 0);
+    if (ok) {
+      fence_after();
+      ok = product_qk(0);
+    }
+    if (ok && nt > 1) ok = product_qk(1);
+#pragma unroll 1
+    for (int i = 0; ok && i < nt; ++i) {
+      ok = product_pv(i);
+      if (ok && i + 2 < nt) {
+        // the scores of tile i + 2 overwrite P
+        ok = wait1(p_done + 8 * (i & 1), (i >> 1) & 1);
+        if (ok) fence_after(), ok = product_qk(i + 2);
+      }
+    }
+    if (!ok) fail();
+    mma_commit(drained);  // every product issued is complete before TMEM is freed
+    mbar_wait(drained, 0);
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == kSoftWarps + 8) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+}  // namespace
+
+int launch_attn_rows_lanes(const RowsArgs& a, cudaStream_t stream) {
+  static bool done[64] = {false};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return OSCAR_ERR_LAUNCH;
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(attn_rows_lanes_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
+      return OSCAR_ERR_LAUNCH;
+    done[dev] = true;
+  }
+  const int64_t tiles = (int64_t(a.n) * a.g.G + N - 1) / N;
+  const int64_t items = tiles * a.g.B * a.g.Hkv * a.ns;
+  if (items >= (int64_t(1) << 31)) return OSCAR_ERR_UNSUPPORTED;
+  attn_rows_lanes_kernel<<<unsigned(items), kThreads, kBytes, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
+}
+
+}  // namespace oscar

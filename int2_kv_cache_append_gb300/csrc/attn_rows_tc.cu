@@ -39,197 +39,49 @@
 //
 // Every wait is bounded; on a timeout the kernel flags OSCAR_DEV_TIMEOUT, waits
 // (bounded) for its own MMAs and frees TMEM.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <algorithm>
 
-#include "internal.h"
-#include "rows.cuh"
+#include "rows_tc.cuh"
 
 namespace oscar {
 namespace {
 
-constexpr int kTok = 128;              // positions per tile
-constexpr int kUnit = 16384;           // bytes of a K or V unit
 constexpr int kSoftWarps = 8;
 constexpr int kThreads = (kSoftWarps + 4 + 4 + 1) * 32;
 constexpr float kNone = -1e30f;        // M before the first tile
 constexpr float kTop = 15.f;           // largest t = u - M that P holds
 constexpr float kRoom = 6.f;           // a new M lies this far below the maximum
-constexpr int kConsts = 3;             // tiles whose token constants are kept
 
 // Shared memory and TMEM of one instantiation.
 template <int DG, int N>
 struct Plan {
   static constexpr bool kBig = DG == 4 && N == 64;
-  static constexpr int KU = kBig ? 2 : 4;                    // K units
-  static constexpr int VU = kBig ? 2 : 3;                    // V units
+  static constexpr bool kFull = DG * N >= 128;               // Q leaves room for fewer buffers
+  static constexpr int KU = kBig ? 2 : kFull ? 3 : 4;        // K units
+  static constexpr int VU = kBig ? 1 : 3;                    // V units
   static constexpr int SB = kBig ? 1 : 2;                    // score buffers
-  static constexpr int PB = (kBig || N == 128) ? 1 : 2;      // P buffers
+  static constexpr int PB = kFull ? 1 : 2;                   // P buffers
+  static constexpr int CB = kBig ? 2 : 3;                    // tiles whose token constants are kept
+  static constexpr int kStages = kBig ? 2 : 3;               // (tile, group) steps whose codes are staged, plus one
   static constexpr int kQ = N * 256 * DG;                    // one of Q's two parts
   static constexpr int kP = (N > 64 ? 2 : 1) * kTok * 128;   // one P buffer
   static constexpr int oQ = 0;
   static constexpr int oP = oQ + 2 * kQ;
   static constexpr int oK = oP + PB * kP;
   static constexpr int oV = oK + KU * kUnit;
-  static constexpr int oConst = oV + VU * kUnit;             // kConsts x (DG x 128 float2, 128 float)
-  static constexpr int kConst = DG * kTok * 8 + kTok * 4;
-  static constexpr int oRow = oConst + kConsts * kConst;     // per column: -M, limit, output row, factor, DG sums; scratch
+  static constexpr int oRawK = oV + VU * kUnit;
+  static constexpr int oRawV = oRawK + kStages * kRawStage;
+  static constexpr int oConst = oRawV + kStages * kRawStage;
+  static constexpr int oRow = oConst + CB * TokenConsts<DG>::kBytes;  // per column: -M, limit, output row, factor, DG sums; scratch
   static constexpr int kRow = N * 4 * (4 + DG) + 8 * N / 2 * 4;
   static constexpr int oBar = oRow + kRow;
-  static constexpr int kBars = 2 * KU + 2 * VU + 2 * SB + 2 * PB + 2 * kConsts + 2;
+  static constexpr int kBars = 2 * KU + 2 * VU + 2 * SB + 2 * PB + 2 * CB + 3;
   static constexpr int kBytes = oBar + kBars * 8 + 32 + 1024;  // + alignment slack
   static constexpr int cS = 0;                                // TMEM columns of the scores
   static constexpr int cO = SB * DG * N;                      // and of O^T
   static_assert(cO + DG * N <= 512, "TMEM");
   static_assert(kBytes <= 232448, "shared memory");
 };
-
-// Shared-memory descriptors, 128-byte swizzle.  K-major: 8-row groups 1024 bytes
-// apart.  MN-major: 64-element blocks `lead` bytes apart, groups of eight k
-// 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_of(uint32_t saddr, uint32_t lead) {
-  return uint64_t((saddr >> 4) & 0x3FFF) | (uint64_t(lead >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
-         (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
-// kind::f16, fp16 operands, float32 accumulator, M = 128; bits 15 / 16: A / B MN-major.
-template <int N>
-__device__ __forceinline__ constexpr uint32_t idesc_of(bool mn_major) {
-  return (1u << 4) | (mn_major ? 3u << 15 : 0u) | (uint32_t(N >> 3) << 17) | (uint32_t(128 >> 4) << 24);
-}
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// 16 consecutive columns of the thread's TMEM lane, and their store.
-__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(a));
-}
-__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
-      : "memory");
-}
-
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-  return d;
-}
-__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-// true in every thread of the named barrier's 128 if it is in one of them
-__device__ __forceinline__ bool any128(int id, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(id), "r"(uint32_t(p))
-      : "memory");
-  return r != 0;
-}
-// Bounded wait of a whole warp, given up at once when the CTA is aborting.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int lane, const volatile uint32_t* abort_flag) {
-  int ok = 1;
-  if (lane == 0) ok = *abort_flag == 0 && mbar_wait(bar, parity);
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
-// v[j] of lane l, summed over the lanes, for column j = l (n = 32) or l % 16 (n = 16).
-template <int n>
-__device__ __forceinline__ float sum_columns(float (&v)[n], int lane) {
-#pragma unroll
-  for (int m = n / 2; m; m >>= 1)
-#pragma unroll
-    for (int j = 0; j < m; ++j) {
-      const bool up = (lane & m) != 0;
-      const float give = up ? v[j] : v[j + m];
-      v[j] = (up ? v[j + m] : v[j]) + __shfl_xor_sync(0xffffffffu, give, m);
-    }
-  if (n == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
-  return v[0];
-}
-__device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t x) {
-  // bf16 pairs: magnitudes compare as integers (a NaN is above infinity)
-  return __vmaxu2(m, x & 0x7FFF7FFFu);
-}
-// 2^e as a float, -126 <= e <= 127
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }
-// smallest e in [-60, 126] with x < 2^e (x >= 0 finite; 126 is not enough for x >= 2^126, whose 2^-126 x < 4 still
-// fits; below 2^-60 a row keeps an absolute precision of 2^-85)
-__device__ __forceinline__ int exponent_above(float x) {
-  return min(126, max(-60, (int(__float_as_uint(x)) >> 23) - 126));
-}
-// the two codes of a word at bits 2 p and 16 + 2 p, moved to bits 8 and 24
-__device__ __forceinline__ uint32_t codes_at8(uint32_t w, int p) {
-  const int sh = 8 - 2 * p;
-  return (sh >= 0 ? w << sh : w >> -sh) & 0x03000300u;
-}
-// Lloyd-Max: 150 times the level's distance from the middle (rho + 1/2 levels),
-// for codes at bits 8 and 24: with x = 2 c - 3, 150 (level - middle) = x (74 + x^2)
-// (75 = 1 * 75, 249 = 3 * 83), every step exact in fp16.
-__device__ __forceinline__ uint32_t lm_value(uint32_t c8) {
-  const uint32_t x = hfma2(c8 | 0x3C003C00u, 0x48004800u /* 8 */, 0xC980C980u /* -11 */);
-  return hmul2(x, hfma2(x, x, 0x54A054A0u /* 74 */));
-}
-constexpr float kLmMiddle = kLmRho + 0.5f;
-// a bf16 pair times `scale`, as fp16
-__device__ __forceinline__ uint32_t scaled_half2(uint32_t x, float scale) {
-  return half2_of(__uint_as_float(x << 16) * scale, __uint_as_float(x & 0xFFFF0000u) * scale);
-}
 
 template <int DG, int N>
 __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArgs a) {
@@ -260,8 +112,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
   const int p1 = min(vis, int(int64_t(blocks) * (s + 1) / a.ns) * kTok);
   const int nt = (p1 - p0 + kTok - 1) / kTok;
 
-  auto kconst = [&](int cb) { return reinterpret_cast<float2*>(sm + L::oConst + cb * L::kConst); };  // (ks, kz)
-  auto econst = [&](int cb) { return reinterpret_cast<float*>(sm + L::oConst + cb * L::kConst + DG * kTok * 8); };
   float* negM = reinterpret_cast<float*>(sm + L::oRow);
   int* limit = reinterpret_cast<int*>(negM + N);   // last position that the row sees
   int* outr = limit + N;                            // its index among all query rows, -1 = none
@@ -280,12 +130,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
   auto p_empty = [&](int i) { return bar + 8u * (b1 + 2 * L::SB + L::PB + i); };
   constexpr int b2 = b1 + 2 * L::SB + 2 * L::PB;
   auto c_full = [&](int i) { return bar + 8u * (b2 + i); };
-  auto c_empty = [&](int i) { return bar + 8u * (b2 + kConsts + i); };
-  const uint32_t q_full = bar + 8u * (b2 + 2 * kConsts), drained = q_full + 8;
+  auto c_empty = [&](int i) { return bar + 8u * (b2 + L::CB + i); };
+  const uint32_t q_full = bar + 8u * (b2 + 2 * L::CB), f_full = q_full + 8, drained = f_full + 8;
   uint32_t* words = reinterpret_cast<uint32_t*>(sm + L::oBar + L::kBars * 8);
   uint32_t* tmem_slot = words;
   volatile uint32_t* abort_flag = words + 1;
   uint32_t* qmax = words + 2;
+  float* scale_f = reinterpret_cast<float*>(words + 3);
 
   for (int c = threadIdx.x; c < N; c += kThreads) {
     const int row = rt * N + c, t = row / g.G;
@@ -301,8 +152,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     for (int i = 0; i < L::VU; ++i) mbar_init(v_full(i), 4), mbar_init(v_empty(i), 1);
     for (int i = 0; i < L::SB; ++i) mbar_init(s_full(i), 1), mbar_init(s_empty(i), kSoftWarps);
     for (int i = 0; i < L::PB; ++i) mbar_init(p_full(i), kSoftWarps), mbar_init(p_empty(i), 1);
-    for (int i = 0; i < kConsts; ++i) mbar_init(c_full(i), 8), mbar_init(c_empty(i), kSoftWarps);
+    for (int i = 0; i < L::CB; ++i) mbar_init(c_full(i), 8), mbar_init(c_empty(i), kSoftWarps);
     mbar_init(q_full, kSoftWarps);
+    mbar_init(f_full, kSoftWarps);
     mbar_init(drained, 1);
     mbar_fence_init();
     words[1] = 0;
@@ -328,52 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     const int tok = threadIdx.x & 127;                      // and this thread's token (TMEM lane)
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16; // the warp's TMEM lanes
     const int id = 1 + grp;                                 // named barrier of the group
-    // Q: scaled by a power of two so that the largest component of the CTA's rows is just below 2^14, split into two
-    // fp16 values (22 bits below that), written K-major; a warp takes one (row, group) at a time.
-    {
-      uint32_t mx = 0;
-      for (int i = warp; i < N * DG; i += kSoftWarps) {
-        const int r = outr[i / DG];
-        if (r < 0) continue;
-        const float4 v = *reinterpret_cast<const float4*>(a.qrot + int64_t(r) * D + (i % DG) * 128 + 4 * lane);
-        const float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (isfinite(f[e])) mx = max(mx, __float_as_uint(fabsf(f[e])));
-      }
-      mx = __reduce_max_sync(0xffffffffu, mx);
-      if (lane == 0) atomicMax(qmax, mx);
-    }
-    asm volatile("bar.sync 3, 256;" ::: "memory");
-    const int fe = max(-100, min(100, (int(*qmax) >> 23) - 126 - 14));  // q = 2^fe q^
-    const float F = pow2i(fe), invF = pow2i(-fe);
-    for (int i = warp; i < N * DG; i += kSoftWarps) {
-      const int c = i / DG, gr = i % DG, r = outr[c];
-      float f[4] = {0.f, 0.f, 0.f, 0.f};
-      if (r >= 0) {
-        const float4 v = *reinterpret_cast<const float4*>(a.qrot + int64_t(r) * D + gr * 128 + 4 * lane);
-        f[0] = v.x * invF, f[1] = v.y * invF, f[2] = v.z * invF, f[3] = v.w * invF;
-      }
-      uint32_t hi[2], lo[2];
-      float sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        hi[e] = half2_of(f[2 * e], f[2 * e + 1]);
-        const float2 x = __half22float2(*reinterpret_cast<__half2*>(&hi[e]));
-        lo[e] = half2_of(f[2 * e] - x.x, f[2 * e + 1] - x.y);
-        const float2 y = __half22float2(*reinterpret_cast<__half2*>(&lo[e]));
-        sum += (x.x + y.x) + (x.y + y.y);
-      }
-#pragma unroll
-      for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-      // channels 4 lane .. 4 lane + 3: block lane / 16, 16-byte chunk (lane / 2) % 8, half lane % 2
-      const int off = (2 * gr + (lane >> 4)) * (N * 128) + c * 128 + ((((lane >> 1) & 7) ^ (c & 7)) << 4) + ((lane & 1) << 3);
-      *reinterpret_cast<uint2*>(sm + L::oQ + off) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(sm + L::oQ + L::kQ + off) = make_uint2(lo[0], lo[1]);
-      if (lane == 0) qsum[gr * N + c] = sum;
-    }
-    fence_async();
-    asm volatile("bar.sync 3, 256;" ::: "memory");
+    load_queries<DG, N, kSoftWarps>(a, sm + L::oQ, L::kQ, outr, qsum, qmax, scale_f, f_full, warp, lane);
     if (lane == 0) mbar_arrive(q_full);
 
     uint64_t l2[C / 2];  // this token's part of l, two columns at a time
@@ -381,21 +188,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     for (int i = 0; i < C / 2; ++i) l2[i] = 0;
     bool ok = true;
     for (int i = 0; i < nt; ++i) {
-      const int sb = i % L::SB, pb = i % L::PB, cb = i % kConsts;
+      const int sb = i % L::SB, pb = i % L::PB, cb = i % L::CB;
       const int pos = p0 + i * kTok + tok;
-      ok = ok && wait(c_full(cb), (i / kConsts) & 1);
+      ok = ok && wait(c_full(cb), (i / L::CB) & 1);
       ok = ok && wait(s_full(sb), (i / L::SB) & 1);
       if (i >= L::PB) ok = ok && wait(p_empty(pb), ((i / L::PB) & 1) ^ 1);
       fence_after();
+      const TokenConsts<DG> tc(sm + L::oConst, cb);
       uint64_t ks[DG], kz[DG];
 #pragma unroll
       for (int gr = 0; gr < DG; ++gr) {
-        const float2 k = kconst(cb)[gr * kTok + tok];
-        ks[gr] = splat_x2(k.x * F);
-        kz[gr] = splat_x2(k.y * F);
+        ks[gr] = splat_x2(tc.ks(gr)[tok]);
+        kz[gr] = splat_x2(tc.kz(gr)[tok]);
       }
-      const float e = econst(cb)[tok];
-      const uint64_t e2 = splat_x2(e), rv2 = splat_x2(isfinite(e) ? pow2i(-int(e)) : 1.f);
+      const uint64_t e2 = splat_x2(tc.e()[tok]), rv2 = splat_x2(tc.rv()[tok]);
       const bool masked = p0 + i * kTok + kTok - 1 > see_all;  // some row does not see some position of the tile
       uint8_t* P = sm + L::oP + pb * L::kP + tok * 128;
       const uint32_t S = tmem + lanes + L::cS + sb * DG * N;
@@ -594,212 +400,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     } else if (lane == 0) {
       fail();
     }
-  } else if (warp < kSoftWarps + 4) {
-    // ------------------------- K: codes to operands ---------------------------
-    const int tok = threadIdx.x - kSoftWarps * 32;
-    struct Raw {
-      RowRef ref;
-      uint4 c0, c1;
-      __half2 sz;
-    };
-    auto load = [&](int k, Raw& x) {  // (tile k / DG, group k % DG)
-      const int pos = p0 + k / DG * kTok + tok;
-      x.ref = RowRef{nullptr, nullptr, nullptr};
-      if (k >= nt * DG || pos >= p1) return;
-      x.ref = row_ref(g, a.layer_base, 0, u, T, pos);
-      if (x.ref.codes) {
-        const uint4* c = reinterpret_cast<const uint4*>(x.ref.codes + 8 * (k % DG));
-        x.c0 = __ldg(c);
-        x.c1 = __ldg(c + 1);
-        x.sz = __ldg(x.ref.sz + k % DG);
-      }
-    };
-    auto emit = [&](int k, const Raw& x) {
-      const int i = k / DG, gr = k % DG, cb = i % kConsts;
-      if (gr == 0 && i >= kConsts && !wait(c_empty(cb), ((i / kConsts) & 1) ^ 1)) return false;
-      float scale = 0.f;
-      float2 kk = make_float2(0.f, 0.f);
-      if (x.ref.wide) {
-        uint32_t m = 0;
-        const uint4* src = reinterpret_cast<const uint4*>(x.ref.wide + gr * 128);
-#pragma unroll 4
-        for (int j = 0; j < 16; ++j) {
-          const uint4 v = src[j];
-          m = absmax2(absmax2(absmax2(absmax2(m, v.x), v.y), v.z), v.w);
-        }
-        m = max(m & 0xFFFFu, m >> 16);
-        const int e = max(-104, int(m >> 7) - 126) - 15;  // 2^-e times the row's largest value is just below 2^15
-        scale = pow2i(-e);
-        kk.x = pow2i(e);
-      } else if (x.ref.codes) {
-        const float2 sz = __half22float2(x.sz);
-        if (g.lm) kk = make_float2(sz.x * (1.0f / 150.0f), fmaf(sz.x, kLmMiddle, sz.y));
-        else kk = make_float2(4.0f * sz.x, fmaf(-4.0f, sz.x, sz.y));
-      }
-      kconst(cb)[gr * kTok + tok] = kk;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int n = 2 * k + half, st = n % L::KU;
-        if (n >= L::KU && !wait(k_empty(st), ((n / L::KU) & 1) ^ 1)) return false;
-        uint8_t* row = sm + L::oK + st * kUnit + tok * 128;
-        if (x.ref.codes) {
-          // word 2 c + half: pair c of every 16-byte chunk
-          const uint32_t w[4] = {half ? x.c0.y : x.c0.x, half ? x.c0.w : x.c0.z, half ? x.c1.y : x.c1.x, half ? x.c1.w : x.c1.z};
-          if (g.lm) {
-#pragma unroll
-            for (int p = 0; p < 8; ++p)
-              *reinterpret_cast<uint4*>(row + ((p ^ (tok & 7)) << 4)) =
-                  make_uint4(lm_value(codes_at8(w[0], p)), lm_value(codes_at8(w[1], p)), lm_value(codes_at8(w[2], p)),
-                             lm_value(codes_at8(w[3], p)));
-          } else {
-#pragma unroll
-            for (int p = 0; p < 8; ++p)
-              *reinterpret_cast<uint4*>(row + ((p ^ (tok & 7)) << 4)) =
-                  make_uint4(codes_at8(w[0], p) | 0x3C003C00u, codes_at8(w[1], p) | 0x3C003C00u,
-                             codes_at8(w[2], p) | 0x3C003C00u, codes_at8(w[3], p) | 0x3C003C00u);
-          }
-        } else {
-#pragma unroll 2
-          for (int p = 0; p < 8; ++p) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (x.ref.wide) v = reinterpret_cast<const uint4*>(x.ref.wide + gr * 128 + half * 64)[p];
-            *reinterpret_cast<uint4*>(row + ((p ^ (tok & 7)) << 4)) =
-                make_uint4(scaled_half2(v.x, scale), scaled_half2(v.y, scale), scaled_half2(v.z, scale), scaled_half2(v.w, scale));
-          }
-        }
-        fence_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(k_full(st));
-      }
-      if (gr == DG - 1) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(c_full(cb));
-      }
-      return true;
-    };
-    Raw x, y;
-    load(0, x);
-    load(1, y);
-    bool ok = true;
-    for (int k = 0; ok && k < nt * DG; k += 2) {
-      ok = emit(k, x);
-      load(k + 2, x);
-      if (ok && k + 1 < nt * DG) ok = emit(k + 1, y);
-      load(k + 3, y);
-    }
-    if (!ok && lane == 0) fail();
   } else if (warp < kSoftWarps + 8) {
-    // ------------------------- V: codes to operands ---------------------------
-    const int tid = threadIdx.x - (kSoftWarps + 4) * 32;
-    const int cb = lane >> 4;                                // 64-channel block
-    const int sub = 16 * (warp & 3) + (lane & 15);           // token within a unit
-    struct Raw {
-      RowRef ref;
-      uint4 c0, c1;
-      __half2 sz;
-    };
-    auto load = [&](int k, Raw& x) {  // unit k: tile k / (2 DG), group (k / 2) % DG, token half k % 2
-      const int pos = p0 + k / (2 * DG) * kTok + 64 * (k & 1) + sub, gr = (k >> 1) % DG;
-      x.ref = RowRef{nullptr, nullptr, nullptr};
-      if (k >= 2 * nt * DG || pos >= p1) return;
-      x.ref = row_ref(g, a.layer_base, 1, u, T, pos);
-      if (x.ref.codes) {
-        const uint4* c = reinterpret_cast<const uint4*>(x.ref.codes + 8 * gr);
-        x.c0 = __ldg(c);
-        x.c1 = __ldg(c + 1);
-        x.sz = __ldg(x.ref.sz + gr);
-      }
-    };
-    bool ok = true;  // a warp that gave up still comes to the group's next barrier
-    // the exponents of a tile's 128 tokens, one per thread
-    auto exponents = [&](int i) {
-      const int buf = i % kConsts, pos = p0 + i * kTok + tid;
-      if (i >= kConsts) ok = ok && wait(c_empty(buf), ((i / kConsts) & 1) ^ 1);
-      float e = -INFINITY;
-      if (pos < p1) {
-        const RowRef r = row_ref(g, a.layer_base, 1, u, T, pos);
-        float m = 0.f;
-        if (r.codes) {
-          for (int gr = 0; gr < DG; ++gr) {
-            const float2 sz = __half22float2(__ldg(r.sz + gr));
-            m = fmax_nan(m, fmax_nan(fabsf(sz.y), fabsf(fmaf(sz.x, g.lm ? kLmSpan : 3.0f, sz.y))));
-          }
-        } else {
-          uint32_t w = 0;
-          const uint4* src = reinterpret_cast<const uint4*>(r.wide);
-#pragma unroll 4
-          for (int j = 0; j < D / 8; ++j) {
-            const uint4 v = src[j];
-            w = absmax2(absmax2(absmax2(absmax2(w, v.x), v.y), v.z), v.w);
-          }
-          m = __uint_as_float(max(w & 0xFFFFu, w >> 16) << 16);
-        }
-        e = isfinite(m) ? float(exponent_above(m)) : NAN;
-      }
-      econst(buf)[tid] = e;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(c_full(buf));
-      return !any128(4, !ok);  // the group's exponents are written
-    };
-    auto emit = [&](int k, const Raw& x) {
-      if (k % (2 * DG) == 0 && !exponents(k / (2 * DG))) return false;
-      const int st = k % L::VU, gr = (k >> 1) % DG;
-      const float e = econst(k / (2 * DG) % kConsts)[64 * (k & 1) + sub];
-      if (k >= L::VU) ok = ok && wait(v_empty(st), ((k / L::VU) & 1) ^ 1);
-      if (!ok) return true;
-      uint8_t* row = sm + L::oV + st * kUnit + cb * (kUnit / 2) + sub * 128;
-      const float scale = isfinite(e) ? pow2i(-int(e)) : 0.f;
-      if (x.ref.codes && isfinite(e)) {
-        const uint32_t sel = cb ? 0x7632u : 0x5410u;
-        const uint32_t w[4] = {prmt(x.c0.x, x.c0.y, sel), prmt(x.c0.z, x.c0.w, sel), prmt(x.c1.x, x.c1.y, sel),
-                               prmt(x.c1.z, x.c1.w, sel)};
-        const float2 sz = __half22float2(x.sz);
-        if (g.lm) {
-          const uint32_t s2 = half2_of(sz.x * scale * (1.0f / 150.0f), sz.x * scale * (1.0f / 150.0f));
-          const float mid = fmaf(sz.x, kLmMiddle, sz.y) * scale;
-          const uint32_t z2 = half2_of(mid, mid);
-#pragma unroll
-          for (int p = 0; p < 8; ++p)
-            *reinterpret_cast<uint4*>(row + ((p ^ (sub & 7)) << 4)) =
-                make_uint4(hfma2(lm_value(codes_at8(w[0], p)), s2, z2), hfma2(lm_value(codes_at8(w[1], p)), s2, z2),
-                           hfma2(lm_value(codes_at8(w[2], p)), s2, z2), hfma2(lm_value(codes_at8(w[3], p)), s2, z2));
-        } else {
-          // a code at bits 8 and 9 of a half is 2^-16 times the code (a subnormal, multiplied exactly)
-          const uint32_t s2 = half2_of(sz.x * scale * 65536.0f, sz.x * scale * 65536.0f);
-          const uint32_t z2 = half2_of(sz.y * scale, sz.y * scale);
-#pragma unroll
-          for (int p = 0; p < 8; ++p)
-            *reinterpret_cast<uint4*>(row + ((p ^ (sub & 7)) << 4)) =
-                make_uint4(hfma2(codes_at8(w[0], p), s2, z2), hfma2(codes_at8(w[1], p), s2, z2),
-                           hfma2(codes_at8(w[2], p), s2, z2), hfma2(codes_at8(w[3], p), s2, z2));
-        }
-      } else {
-        const uint4* src = x.ref.wide && isfinite(e) ? reinterpret_cast<const uint4*>(x.ref.wide + gr * 128 + cb * 64) : nullptr;
-#pragma unroll 2
-        for (int p = 0; p < 8; ++p) {
-          const uint4 v = src ? src[p] : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(row + ((p ^ (sub & 7)) << 4)) =
-              make_uint4(scaled_half2(v.x, scale), scaled_half2(v.y, scale), scaled_half2(v.z, scale), scaled_half2(v.w, scale));
-        }
-      }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(v_full(st));
-      return true;
-    };
-    Raw x, y;
-    load(0, x);
-    load(1, y);
-    for (int k = 0; k < 2 * nt * DG; k += 2) {
-      if (!emit(k, x)) break;  // the whole group leaves
-      load(k + 2, x);
-      emit(k + 1, y);  // an odd unit starts no tile
-      load(k + 3, y);
-    }
+    Share x{&a, u, T, p0, p1, nt, sm, base, abort_flag, scale_f, f_full, k_full(0), k_empty(0), v_full(0), v_empty(0),
+            c_full(0), c_empty(0), L::oK, L::oV, L::oRawK, L::oRawV, L::oConst};
+    const bool ok = warp < kSoftWarps + 4 ? expand_k<DG, L::KU, L::CB, L::kStages>(x, threadIdx.x - kSoftWarps * 32, lane)
+                                          : expand_v<DG, L::VU, L::CB, L::kStages>(x, warp & 3, lane);
     if (!ok && lane == 0) fail();
   } else if (lane == 0) {
     // ------------------------------ MMA issuer --------------------------------
-    constexpr uint32_t id_qk = idesc_of<N>(false), id_pv = idesc_of<N>(true);
+    constexpr uint32_t id_qk = idesc_of(N, false, false), id_pv = idesc_of(N, true, true);
     const uint32_t sQ = base + L::oQ, sK = base + L::oK, sV = base + L::oV, sP = base + L::oP;
     auto wait1 = [&](uint32_t br, uint32_t parity) { return *abort_flag == 0 && mbar_wait(br, parity); };
     auto product_qk = [&](int i) {
@@ -876,7 +485,7 @@ int launch(const RowsArgs& a, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
 }
 
-// Query rows per CTA: the smallest tile that holds a unit's rows, at most what TMEM and shared memory hold.
+// Query rows per CTA.  More than 64 rows go to the row-lane kernel where its accumulators fit TMEM.
 int tile_rows(int D, int64_t rows) {
   if (rows <= 32) return 32;
   return rows <= 64 || D > 128 ? 64 : 128;
@@ -902,7 +511,8 @@ int rows_splits_tc(const Geom& g, int64_t rows, int seq_len_hint) {
 
 int launch_attn_rows_tc(const RowsArgs& a, cudaStream_t stream) {
   const int N = tile_rows(a.g.D, int64_t(a.n) * a.g.G);
-  if (a.g.D == 128) return N == 32 ? launch<1, 32>(a, stream) : N == 64 ? launch<1, 64>(a, stream) : launch<1, 128>(a, stream);
+  if (N == 128) return launch_attn_rows_lanes(a, stream);
+  if (a.g.D == 128) return N == 32 ? launch<1, 32>(a, stream) : launch<1, 64>(a, stream);
   if (a.g.D == 256) return N == 32 ? launch<2, 32>(a, stream) : launch<2, 64>(a, stream);
   return N == 32 ? launch<4, 32>(a, stream) : launch<4, 64>(a, stream);
 }

@@ -124,6 +124,7 @@ struct RowsArgs {
 };
 int launch_attn_rows(const RowsArgs& a, cudaStream_t stream);
 int launch_attn_rows_tc(const RowsArgs& a, cudaStream_t stream);  // fp16 products (attn_rows_tc.cu)
+int launch_attn_rows_lanes(const RowsArgs& a, cudaStream_t stream);  // its form for many rows (attn_rows_lanes.cu)
 // Splits of every (row tile, unit) for `rows` query rows per unit: enough
 // shares to fill the GPU, none shorter than the context gives.
 int rows_splits(const Geom& g, int64_t rows, int seq_len_hint);

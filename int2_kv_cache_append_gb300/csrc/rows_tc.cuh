@@ -1,0 +1,522 @@
+// Device code shared by the tensor-core row attention kernels: tcgen05 and
+// packed-arithmetic wrappers, and the warps that expand cached K and V rows into
+// fp16 operands.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "rows.cuh"
+
+namespace oscar {
+
+constexpr int kTok = 128;    // positions per tile
+constexpr int kUnit = 16384; // bytes of a K unit (64 channels of 128 tokens) or V unit (64 tokens of 128 channels)
+
+// Shared-memory descriptors, 128-byte swizzle.  K-major: 8-row groups 1024 bytes
+// apart.  MN-major: 64-element blocks `lead` bytes apart, groups of eight k
+// 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_of(uint32_t saddr, uint32_t lead) {
+  return uint64_t((saddr >> 4) & 0x3FFF) | (uint64_t(lead >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// kind::f16, fp16 operands, float32 accumulator, M = 128.
+__device__ __forceinline__ constexpr uint32_t idesc_of(int n, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | (a_mn_major ? 1u << 15 : 0u) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) |
+         (uint32_t(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// A from TMEM (fp16 pairs along k in a lane's columns)
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 16 consecutive columns of the thread's TMEM lane, and their store.
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a));
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(a)
+      : "memory");
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// true in every thread of the named barrier's 128 if it is in one of them
+__device__ __forceinline__ bool any128(int id, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(uint32_t(p))
+      : "memory");
+  return r != 0;
+}
+// Bounded wait of a whole warp, given up at once when the CTA is aborting.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int lane, const volatile uint32_t* abort_flag) {
+  int ok = 1;
+  if (lane == 0) ok = *abort_flag == 0 && mbar_wait(bar, parity);
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+// v[j] of lane l, summed over the lanes, for column j = l (n = 32) or l % 16 (n = 16).
+template <int n>
+__device__ __forceinline__ float sum_columns(float (&v)[n], int lane) {
+#pragma unroll
+  for (int m = n / 2; m; m >>= 1)
+#pragma unroll
+    for (int j = 0; j < m; ++j) {
+      const bool up = (lane & m) != 0;
+      const float give = up ? v[j] : v[j + m];
+      v[j] = (up ? v[j + m] : v[j]) + __shfl_xor_sync(0xffffffffu, give, m);
+    }
+  if (n == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+  return v[0];
+}
+__device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t x) {
+  // bf16 pairs: magnitudes compare as integers (a NaN is above infinity)
+  return __vmaxu2(m, x & 0x7FFF7FFFu);
+}
+// 2^e as a float, -126 <= e <= 127
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }
+// smallest e in [-60, 126] with x < 2^e (x >= 0 finite; 126 is not enough for x >= 2^126, whose 2^-126 x < 4 still
+// fits; below 2^-60 a row keeps an absolute precision of 2^-85)
+__device__ __forceinline__ int exponent_above(float x) {
+  return min(126, max(-60, (int(__float_as_uint(x)) >> 23) - 126));
+}
+// the two codes of a word at bits 2 p and 16 + 2 p, moved to bits 8 and 24
+__device__ __forceinline__ uint32_t codes_at8(uint32_t w, int p) {
+  const int sh = 8 - 2 * p;
+  return (sh >= 0 ? w << sh : w >> -sh) & 0x03000300u;
+}
+// Lloyd-Max: 150 times the level's distance from the middle (rho + 1/2 levels),
+// for codes at bits 8 and 24: with x = 2 c - 3, 150 (level - middle) = x (74 + x^2)
+// (75 = 1 * 75, 249 = 3 * 83), every step exact in fp16.
+__device__ __forceinline__ uint32_t lm_value(uint32_t c8) {
+  const uint32_t x = hfma2(c8 | 0x3C003C00u, 0x48004800u /* 8 */, 0xC980C980u /* -11 */);
+  return hmul2(x, hfma2(x, x, 0x54A054A0u /* 74 */));
+}
+constexpr float kLmMiddle = kLmRho + 0.5f;
+// a bf16 pair times `scale`, as fp16
+__device__ __forceinline__ uint32_t scaled_half2(uint32_t x, float scale) {
+  return half2_of(__uint_as_float(x << 16) * scale, __uint_as_float(x & 0xFFFF0000u) * scale);
+}
+
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The CTA's query rows as fp16 operands, by `warps` warps (named barrier 3):
+// scaled by a power of two so that the largest finite component is just below
+// 2^14, split into two fp16 values (22 bits below that), written K-major in
+// blocks of 64 channels; a warp takes one (row, group) at a time.  *scale and
+// f_full: the power of two that undoes the scaling; qsum[DG][N]: sums of the
+// operands' channels.
+template <int DG, int N, int warps>
+__device__ __forceinline__ void load_queries(const RowsArgs& a, uint8_t* sq, int part, const int* outr, float* qsum,
+                                             uint32_t* qmax, float* scale, uint32_t f_full, int warp, int lane) {
+  constexpr int D = DG * 128;
+  uint32_t mx = 0;
+#pragma unroll 4
+  for (int i = warp; i < N * DG; i += warps) {
+    const int r = outr[i / DG];
+    if (r < 0) continue;
+    const float4 v = *reinterpret_cast<const float4*>(a.qrot + int64_t(r) * D + (i % DG) * 128 + 4 * lane);
+    const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (isfinite(f[e])) mx = max(mx, __float_as_uint(fabsf(f[e])));
+  }
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  if (lane == 0) atomicMax(qmax, mx);
+  asm volatile("bar.sync 3, %0;" ::"n"(warps * 32) : "memory");
+  const int fe = max(-100, min(100, (int(*qmax) >> 23) - 126 - 14));  // q = 2^fe q^
+  const float inv = pow2i(-fe);
+  if (warp == 0 && lane == 0) *scale = pow2i(fe);
+#pragma unroll 2
+  for (int i = warp; i < N * DG; i += warps) {
+    const int c = i / DG, gr = i % DG, r = outr[c];
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+    if (r >= 0) {
+      const float4 v = *reinterpret_cast<const float4*>(a.qrot + int64_t(r) * D + gr * 128 + 4 * lane);
+      f[0] = v.x * inv, f[1] = v.y * inv, f[2] = v.z * inv, f[3] = v.w * inv;
+    }
+    uint32_t hi[2], lo[2];
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      hi[e] = half2_of(f[2 * e], f[2 * e + 1]);
+      const float2 x = __half22float2(*reinterpret_cast<__half2*>(&hi[e]));
+      lo[e] = half2_of(f[2 * e] - x.x, f[2 * e + 1] - x.y);
+      const float2 y = __half22float2(*reinterpret_cast<__half2*>(&lo[e]));
+      sum += (x.x + y.x) + (x.y + y.y);
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    // channels 4 lane .. 4 lane + 3: block lane / 16, 16-byte chunk (lane / 2) % 8, half lane % 2
+    const int off = (2 * gr + (lane >> 4)) * (N * 128) + c * 128 + ((((lane >> 1) & 7) ^ (c & 7)) << 4) + ((lane & 1) << 3);
+    *reinterpret_cast<uint2*>(sq + off) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2*>(sq + part + off) = make_uint2(lo[0], lo[1]);
+    if (lane == 0) qsum[gr * N + c] = sum;
+  }
+  fence_async();
+  asm volatile("bar.sync 3, %0;" ::"n"(warps * 32) : "memory");
+  if (lane == 0) mbar_arrive(f_full);
+}
+
+// Constants of a tile's tokens, one slot of the ring: float ks[DG][128],
+// kz[DG][128] (score = ks * acc + kz * sum q), e[128] (the value row's
+// exponent), rv[128] (2^-e), and a word that is set when some e is not 0.
+template <int DG>
+struct TokenConsts {
+  static constexpr int kBytes = (2 * DG + 2) * kTok * 4 + 16;
+  float* p;
+  __device__ __forceinline__ TokenConsts(uint8_t* ring, int slot) : p(reinterpret_cast<float*>(ring + slot * kBytes)) {}
+  __device__ __forceinline__ float* ks(int g) const { return p + g * kTok; }
+  __device__ __forceinline__ float* kz(int g) const { return p + (DG + g) * kTok; }
+  __device__ __forceinline__ float* e() const { return p + 2 * DG * kTok; }
+  __device__ __forceinline__ float* rv() const { return p + (2 * DG + 1) * kTok; }
+  __device__ __forceinline__ uint32_t* uneven() const { return reinterpret_cast<uint32_t*>(p + (2 * DG + 2) * kTok); }
+};
+
+// What the expanding warps work on: positions [p0, p1) of unit u.
+struct Share {
+  const RowsArgs* a;
+  int u, T, p0, p1, nt;
+  uint8_t* sm;                    // shared memory and its address
+  uint32_t base;
+  volatile uint32_t* abort_flag;
+  const float* F;                 // scale of the queries, valid after f_full
+  uint32_t f_full;
+  uint32_t k_full, k_empty, v_full, v_empty, c_full, c_empty;  // first barrier of each kind
+  int oK, oV, oRawK, oRawV, oConst;
+};
+constexpr int kRawStage = kTok * 36;  // staged codes (32 bytes) and scale / zero pairs of one (tile, group) and role
+
+// K, four warps, a thread per token.  Steps k = (tile, group); codes are staged
+// kStages - 1 steps ahead by cp.async, each thread its own row.
+template <int DG, int KU, int CB, int kStages>
+__device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
+  const Geom& g = x.a->g;
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity, lane, x.abort_flag); };
+  const int steps = x.nt * DG;
+  const uint8_t* role = x.a->layer_base + g.sink_bytes + g.ring_bytes;
+  const int64_t row0 = int64_t(x.u) * g.ncap + (x.p0 + tok - g.S);  // INT2 row of the first tile's token
+  const uint8_t* codes = role + row0 * (32 * DG);
+  const uint8_t* szs = role + g.codes_bytes + row0 * (4 * DG);
+  const int ring0 = max(g.S, x.T - g.W);  // INT2: S <= position < ring0
+  const uint32_t raw = x.base + x.oRawK + tok * 32, rsz = x.base + x.oRawK + kTok * 32 + tok * 4;
+  auto stage = [&](int k) {
+    const int i = k / DG, gr = k % DG, pos = x.p0 + i * kTok + tok, st = (k % kStages) * kRawStage;
+    if (k < steps && pos >= g.S && pos < ring0 && pos < x.p1) {
+      const uint8_t* c = codes + int64_t(i) * (kTok * 32 * DG) + gr * 32;
+      cp_async16(raw + st, c);
+      cp_async16(raw + st + 16, c + 16);
+      cp_async4(rsz + st, szs + int64_t(i) * (kTok * 4 * DG) + gr * 4);
+    }
+    cp_async_commit();
+  };
+#pragma unroll 1
+  for (int k = 0; k < kStages - 1; ++k) stage(k);
+  if (!wait(x.f_full, 0)) return false;
+  const float F = *x.F;
+#pragma unroll 1
+  for (int k = 0; k < steps; ++k) {
+    stage(k + kStages - 1);
+    cp_async_wait<kStages - 1>();
+    const int i = k / DG, gr = k % DG, cb = i % CB, pos = x.p0 + i * kTok + tok;
+    if (gr == 0 && i >= CB && !wait(x.c_empty + 8 * cb, ((i / CB) & 1) ^ 1)) return false;
+    const bool valid = pos < x.p1, packed = valid && pos >= g.S && pos < ring0;
+    const uint8_t* st = x.sm + x.oRawK + (k % kStages) * kRawStage;
+    const uint4 c0 = *reinterpret_cast<const uint4*>(st + tok * 32), c1 = *reinterpret_cast<const uint4*>(st + tok * 32 + 16);
+    float ks = 0.f, kz = 0.f, scale = 0.f;
+    const __nv_bfloat16* wide = nullptr;
+    if (packed) {
+      const float2 sz = __half22float2(*reinterpret_cast<const __half2*>(st + kTok * 32 + tok * 4));
+      if (g.lm) ks = sz.x * (1.0f / 150.0f), kz = fmaf(sz.x, kLmMiddle, sz.y);
+      else ks = 4.0f * sz.x, kz = fmaf(-4.0f, sz.x, sz.y);
+    } else if (valid) {
+      wide = row_ref(g, x.a->layer_base, 0, x.u, x.T, pos).wide + gr * 128;
+      uint32_t m = 0;
+      const uint4* src = reinterpret_cast<const uint4*>(wide);
+#pragma unroll 8
+      for (int j = 0; j < 16; ++j) {
+        const uint4 v = src[j];
+        m = absmax2(absmax2(absmax2(absmax2(m, v.x), v.y), v.z), v.w);
+      }
+      m = max(m & 0xFFFFu, m >> 16);
+      const int e = max(-104, int(m >> 7) - 126) - 15;  // 2^-e times the row's largest value is just below 2^15
+      scale = pow2i(-e);
+      ks = pow2i(e);
+    }
+    const TokenConsts<DG> tc(x.sm + x.oConst, cb);
+    tc.ks(gr)[tok] = ks * F;
+    tc.kz(gr)[tok] = kz * F;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      const int n = 2 * k + half, u = n % KU;
+      if (n >= KU && !wait(x.k_empty + 8 * u, ((n / KU) & 1) ^ 1)) return false;
+      uint8_t* row = x.sm + x.oK + u * kUnit + tok * 128;
+      if (packed) {
+        // word 2 c + half: pair c of every 16-byte chunk
+        const uint32_t w[4] = {half ? c0.y : c0.x, half ? c0.w : c0.z, half ? c1.y : c1.x, half ? c1.w : c1.z};
+        if (g.lm) {
+#pragma unroll
+          for (int p = 0; p < 8; ++p)
+            *reinterpret_cast<uint4*>(row + ((p ^ (tok & 7)) << 4)) =
+                make_uint4(lm_value(codes_at8(w[0], p)), lm_value(codes_at8(w[1], p)), lm_value(codes_at8(w[2], p)),
+                           lm_value(codes_at8(w[3], p)));
+        } else {
+#pragma unroll
+          for (int p = 0; p < 8; ++p)
+            *reinterpret_cast<uint4*>(row + ((p ^ (tok & 7)) << 4)) =
+                make_uint4(codes_at8(w[0], p) | 0x3C003C00u, codes_at8(w[1], p) | 0x3C003C00u,
+                           codes_at8(w[2], p) | 0x3C003C00u, codes_at8(w[3], p) | 0x3C003C00u);
+        }
+      } else {
+#pragma unroll 4
+        for (int p = 0; p < 8; ++p) {
+          const uint4 v = wide ? reinterpret_cast<const uint4*>(wide + half * 64)[p] : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(row + ((p ^ (tok & 7)) << 4)) =
+              make_uint4(scaled_half2(v.x, scale), scaled_half2(v.y, scale), scaled_half2(v.z, scale), scaled_half2(v.w, scale));
+        }
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x.k_full + 8 * u);
+    }
+    if (gr == DG - 1 && lane == 0) mbar_arrive(x.c_full + 8 * cb);
+  }
+  return true;
+}
+
+// V, four warps.  Warp w holds tokens 64 h + 16 w .. + 15 of both unit halves h;
+// lanes 16 c + j write the 64-channel block c of token 16 w + j.  For the
+// exponents and the scale / zero pairs, fetched a tile ahead, lane 16 h + j
+// stands for the token of half h.
+template <int DG, int VU, int CB, int kStages>
+__device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
+  const Geom& g = x.a->g;
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity, lane, x.abort_flag); };
+  const int steps = x.nt * DG, cb = lane >> 4, sub = 16 * warp4 + (lane & 15);
+  const uint8_t* role = x.a->layer_base + g.role_bytes + g.sink_bytes + g.ring_bytes;
+  const int64_t row0 = int64_t(x.u) * g.ncap + (x.p0 + sub - g.S);
+  const uint8_t* codes = role + row0 * (32 * DG) + 16 * cb;
+  const __half2* szs = reinterpret_cast<const __half2*>(role + g.codes_bytes) + (row0 + 64 * cb) * DG;
+  const int pk0 = g.vb ? 0x7fffffff : g.S, pk1 = min(x.p1, max(g.S, x.T - g.W));  // INT2: pk0 <= position < pk1
+  const uint32_t raw = x.base + x.oRawV + sub * 32 + 16 * cb;
+  auto stage = [&](int k) {
+    const int i = k / DG, pos = x.p0 + i * kTok + sub, st = (k % kStages) * kRawStage;
+    const uint8_t* c = codes + int64_t(i) * (kTok * 32 * DG) + (k % DG) * 32;
+    if (k < steps && pos >= pk0 && pos < pk1) cp_async16(raw + st, c);
+    if (k < steps && pos + 64 >= pk0 && pos + 64 < pk1) cp_async16(raw + st + 64 * 32, c + 64 * 32 * DG);
+    cp_async_commit();
+  };
+  const int mine = 64 * cb + sub;  // the lane's token for exponents
+  __half2 sz[DG], nsz[DG];
+  auto pairs = [&](int i, __half2 (&d)[DG]) {
+    const int pos = x.p0 + i * kTok + mine;
+    const bool packed = pos >= pk0 && pos < pk1;
+#pragma unroll
+    for (int gr = 0; gr < DG; ++gr) d[gr] = packed ? __ldg(szs + int64_t(i) * (kTok * DG) + gr) : __half2half2(__half(0.f));
+  };
+  pairs(0, nsz);
+#pragma unroll 1
+  for (int k = 0; k < kStages - 1; ++k) stage(k);
+  float e = 0.f;
+#pragma unroll 1
+  for (int k = 0; k < steps; ++k) {
+    stage(k + kStages - 1);
+    const int i = k / DG, gr = k % DG, slot = i % CB;
+    if (gr == 0) {
+#pragma unroll
+      for (int j = 0; j < DG; ++j) sz[j] = nsz[j];
+      pairs(i + 1, nsz);
+      const int pos = x.p0 + i * kTok + mine;
+      float m = 0.f;
+      if (pos >= pk0 && pos < pk1) {
+#pragma unroll
+        for (int j = 0; j < DG; ++j) {
+          const float2 v = __half22float2(sz[j]);
+          m = fmax_nan(m, fmax_nan(fabsf(v.y), fabsf(fmaf(v.x, g.lm ? kLmSpan : 3.0f, v.y))));
+        }
+      } else if (pos < x.p1) {
+        uint32_t w = 0;
+        const uint4* src = reinterpret_cast<const uint4*>(row_ref(g, x.a->layer_base, 1, x.u, x.T, pos).wide);
+#pragma unroll 8
+        for (int j = 0; j < DG * 16; ++j) {
+          const uint4 v = src[j];
+          w = absmax2(absmax2(absmax2(absmax2(w, v.x), v.y), v.z), v.w);
+        }
+        m = __uint_as_float(max(w & 0xFFFFu, w >> 16) << 16);
+      }
+      // rows of ordinary size keep exponent 0
+      e = pos >= x.p1 ? -INFINITY
+          : !isfinite(m) ? NAN
+          : m >= 0x1p-8f && m < 0x1p14f ? 0.f : float(exponent_above(m));
+      if (i >= CB && !wait(x.c_empty + 8 * slot, ((i / CB) & 1) ^ 1)) return false;
+      const TokenConsts<DG> tc(x.sm + x.oConst, slot);
+      tc.e()[mine] = e;
+      tc.rv()[mine] = isfinite(e) ? pow2i(-int(e)) : 1.f;
+      const bool uneven = __any_sync(0xffffffffu, e != 0.f);
+      if (lane == 0) {
+        // one byte per warp
+        reinterpret_cast<volatile uint8_t*>(tc.uneven())[warp4] = uneven;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x.c_full + 8 * slot);
+    }
+    cp_async_wait<kStages - 1>();
+    __syncwarp();  // the other lane's half of the row has landed, too
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      const int n = 2 * k + half, u = n % VU;
+      const int pos = x.p0 + i * kTok + 64 * half + sub, from = 16 * half + (lane & 15);
+      const float eh = __shfl_sync(0xffffffffu, e, from);
+      uint32_t pair = 0;
+#pragma unroll
+      for (int j = 0; j < DG; ++j)
+        if (j == gr) pair = __shfl_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&sz[j]), from);
+      const uint8_t* st = x.sm + x.oRawV + (k % kStages) * kRawStage + (64 * half + sub) * 32;
+      const uint4 c0 = *reinterpret_cast<const uint4*>(st), c1 = *reinterpret_cast<const uint4*>(st + 16);
+      if (n >= VU && !wait(x.v_empty + 8 * u, ((n / VU) & 1) ^ 1)) return false;
+      uint8_t* row = x.sm + x.oV + u * kUnit + cb * (kUnit / 2) + sub * 128;
+      const bool fine = isfinite(eh);
+      const float scale = fine ? pow2i(-int(eh)) : 0.f;
+      if (fine && pos >= pk0 && pos < pk1) {
+        const uint32_t sel = cb ? 0x7632u : 0x5410u;
+        const uint32_t w[4] = {prmt(c0.x, c0.y, sel), prmt(c0.z, c0.w, sel), prmt(c1.x, c1.y, sel), prmt(c1.z, c1.w, sel)};
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&pair));
+        if (g.lm) {
+          const uint32_t s2 = half2_of(v.x * scale * (1.0f / 150.0f), v.x * scale * (1.0f / 150.0f));
+          const float mid = fmaf(v.x, kLmMiddle, v.y) * scale;
+          const uint32_t z2 = half2_of(mid, mid);
+#pragma unroll
+          for (int p = 0; p < 8; ++p)
+            *reinterpret_cast<uint4*>(row + ((p ^ (sub & 7)) << 4)) =
+                make_uint4(hfma2(lm_value(codes_at8(w[0], p)), s2, z2), hfma2(lm_value(codes_at8(w[1], p)), s2, z2),
+                           hfma2(lm_value(codes_at8(w[2], p)), s2, z2), hfma2(lm_value(codes_at8(w[3], p)), s2, z2));
+        } else {
+          // c / 4 from 1 + c / 4, exactly; then one rounding
+          const uint32_t s2 = half2_of(v.x * scale * 4.0f, v.x * scale * 4.0f), z2 = half2_of(v.y * scale, v.y * scale);
+          auto value = [&](uint32_t word, int p) {
+            return hfma2(hadd2(codes_at8(word, p) | 0x3C003C00u, 0xBC00BC00u), s2, z2);
+          };
+#pragma unroll
+          for (int p = 0; p < 8; ++p)
+            *reinterpret_cast<uint4*>(row + ((p ^ (sub & 7)) << 4)) =
+                make_uint4(value(w[0], p), value(w[1], p), value(w[2], p), value(w[3], p));
+        }
+      } else {
+        const uint4* src = fine && pos < x.p1
+                               ? reinterpret_cast<const uint4*>(row_ref(g, x.a->layer_base, 1, x.u, x.T, pos).wide + gr * 128 + cb * 64)
+                               : nullptr;
+#pragma unroll 4
+        for (int p = 0; p < 8; ++p) {
+          const uint4 v = src ? src[p] : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(row + ((p ^ (sub & 7)) << 4)) =
+              make_uint4(scaled_half2(v.x, scale), scaled_half2(v.y, scale), scaled_half2(v.z, scale), scaled_half2(v.w, scale));
+        }
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x.v_full + 8 * u);
+    }
+    __syncwarp();  // the stage has been read by both lanes before it is written again
+  }
+  return true;
+}
+
+}  // namespace oscar

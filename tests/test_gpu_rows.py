@@ -203,10 +203,12 @@ def test_extend_values_beyond_fp16():
             K.attn_extend(kcfg(c), torch.from_numpy(x).cuda(), 0, q, dev_i32([50]), eye, eye, out, ws)
             torch.cuda.synchronize()
             res.append(out.double().cpu() * 2.0 ** -p)
-        # The rows' power of two joins the scores' exponents before they are rounded to float32: |score + power| < 2^7
-        # rounds by at most 2^-18 (2^-17 for two), which moves a probability by 2^-17 ln 2 of itself and an output by
-        # less than 2^-17 of the largest value; the bf16 results then differ by that and one rounding each (2^-8).
-        lim = 2 * 2.0 ** -8 * res[0].abs() + 2.0 ** -17 * 8 * res[0].abs().max()
+        # The rows' power of two joins the scores' exponents before they are rounded to float32 (|score + power| < 2^7:
+        # off by 2^-18, which moves a probability by less than 2^-17 of itself) and moves the reference of the
+        # probabilities, so either result has fp16 roundings of its own: 2^-12 of each probability, 2 * 2^-12 of the
+        # largest value between the two.  Then one bf16 rounding each (2^-8).
+        vmax = float(np.abs(np.concatenate([O.dequant_history(c, cache, 0, 1, 0, h, 50) for h in range(2)])).max())
+        lim = 2 * 2.0 ** -8 * res[0].abs() + (2.0 ** -11 + 2 * 2.0 ** -17) * vmax
         assert ((res[0] - res[1]).abs() <= lim).all(), power
 
 
