@@ -9,17 +9,17 @@
 //   S [128 rows x 128 tokens] = Q K^T,   O [128 rows x 128 channels] += P V
 //
 // The arithmetic is that of the token-lane kernel (attn_rows_tc.cu): INT2 keys
-// as exact fp16 values with the row's scale and zero applied to the sum, queries
-// as two fp16 values, value rows with an exponent of their own that joins the
-// score.  A row is one thread's, so its maximum and sum need no exchange; its
-// reference M follows the maximum only when that has grown by 2^12 (P is fp16),
-// and then the warp rescales its rows of O.
+// as exact fp16 values and a rank-one term, queries as two fp16 values, value rows with an exponent of their own that joins the
+// score.  A row's reference M follows its maximum only when that has grown by
+// 2^12 (P is fp16), and then its warps rescale their rows of O.
 //
-// Two softmax groups of four warps take turns: group w has the tiles i = w mod 2
-// with scores S_w, sums O_w and (M, l) of its own, so nothing passes between
-// them until the end, where the two are merged.  P overwrites S in TMEM and is
-// the A operand from there: in shared memory it would take 64 KB of traffic per
-// tile from a budget (128 bytes per clock) that the products already use up.
+// Eight softmax warps: warp w has rows 32 (w mod 4) .. + 31 and the tokens of
+// half w / 4; the two threads of a row exchange their maxima once per tile.  Two
+// score tiles alternate, so the products of one run under the softmax of the
+// other.  Both left operands come from TMEM: Q's two parts stay there, and P
+// overwrites the scores that it was made from.  In shared memory they would
+// take 96 KB of reads per tile from a budget (128 bytes per clock) that K, V
+// and their expansion already use.
 #include <algorithm>
 
 #include "rows_tc.cuh"
@@ -33,20 +33,20 @@ constexpr int kSoftWarps = 8;
 constexpr int kThreads = (kSoftWarps + 4 + 4 + 1) * 32;
 constexpr float kNone = -1e30f;         // M before the first visible position
 constexpr float kGrow = 12.f;           // log2 of the largest P
-constexpr int KU = 4, VU = 3, CB = 4, kStages = 3;
-constexpr int kQ = N * 256;             // one of Q's two parts
-constexpr int oQ = 0;
-constexpr int oK = 2 * kQ;
+constexpr int KU = 4, VU = 4, CB = 4, kStages = 4;
+constexpr int oK = 0;
 constexpr int oV = oK + KU * kUnit;
 constexpr int oRawK = oV + VU * kUnit;
 constexpr int oRawV = oRawK + kStages * kRawStage;
-constexpr int oConst = oRawV + kStages * kRawStage;
-constexpr int oRow = oConst + CB * TokenConsts<1>::kBytes;  // row index, sum of q; (M, l) of both groups
-constexpr int oBar = oRow + N * 8 + 2 * N * 8;
-constexpr int kBars = 2 * KU + 2 * VU + 2 * CB + 3 * 2 + 2 + 1;
-constexpr int kBytes = oBar + kBars * 8 + 32 + 1024;        // + alignment slack
+constexpr int oRank = oRawV + kStages * kRawStage;  // the keys' two and the queries' rank-one operands
+constexpr int oConst = oRank + 3 * kRank;
+constexpr int oRow = oConst + CB * TileConsts::kBytes;
+constexpr int kRow = N * 4 + 4 * N * 4 + 64;        // row index; exchange [2][2][N]; the K warps' scratch
+constexpr int oBar = oRow + kRow;
+constexpr int kBars = 2 * KU + 2 * VU + 2 * CB + 2 + 1 + 1 + 3;
+constexpr int kBytes = oBar + kBars * 8 + 32 + 1024;  // + alignment slack
 static_assert(oBar % 8 == 0 && kBytes <= 232448, "shared memory");
-constexpr uint32_t cS = 0, cO = 256;    // TMEM columns: two score tiles, two output tiles
+constexpr uint32_t cS = 0, cO = 256, cQ = 384;        // TMEM columns: two score tiles, O, Q's two parts
 
 __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32]) {
   asm volatile(
@@ -96,12 +96,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
   const int nt = (p1 - p0 + kTok - 1) / kTok;
 
   int* outr = reinterpret_cast<int*>(sm + oRow);            // a row's index among all query rows, -1 = none
-  float* qsum = reinterpret_cast<float*>(outr + N);
-  float2* both = reinterpret_cast<float2*>(qsum + N);       // [2][N] (M, l)
+  float* swap = reinterpret_cast<float*>(outr + N);         // [2][2][N]
   const uint32_t bar = base + oBar;
   const uint32_t k_full = bar, k_empty = k_full + 8 * KU, v_full = k_empty + 8 * KU, v_empty = v_full + 8 * VU,
                  c_full = v_empty + 8 * VU, c_empty = c_full + 8 * CB, s_full = c_empty + 8 * CB, p_full = s_full + 16,
-                 p_done = p_full + 16, q_full = p_done + 16, f_full = q_full + 8, drained = f_full + 8;
+                 p_done = p_full + 8, q_full = p_done + 8, f_full = q_full + 8, drained = f_full + 8;
   uint32_t* words = reinterpret_cast<uint32_t*>(sm + oBar + kBars * 8);
   uint32_t* tmem_slot = words;
   volatile uint32_t* abort_flag = words + 1;
@@ -118,8 +117,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
   if (threadIdx.x == 0) {
     for (int i = 0; i < KU; ++i) mbar_init(k_full + 8 * i, 4), mbar_init(k_empty + 8 * i, 1);
     for (int i = 0; i < VU; ++i) mbar_init(v_full + 8 * i, 4), mbar_init(v_empty + 8 * i, 1);
-    for (int i = 0; i < CB; ++i) mbar_init(c_full + 8 * i, 8), mbar_init(c_empty + 8 * i, 4);
-    for (int i = 0; i < 2; ++i) mbar_init(s_full + 8 * i, 1), mbar_init(p_full + 8 * i, 4), mbar_init(p_done + 8 * i, 1);
+    for (int i = 0; i < CB; ++i) mbar_init(c_full + 8 * i, 8), mbar_init(c_empty + 8 * i, kSoftWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(s_full + 8 * i, 1);
+    mbar_init(p_full, kSoftWarps);
+    mbar_init(p_done, 1);
     mbar_init(q_full, kSoftWarps);
     mbar_init(f_full, kSoftWarps);
     mbar_init(drained, 1);
@@ -143,111 +144,184 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
 
   if (warp < kSoftWarps) {
     // ------------------------------- softmax ---------------------------------
-    const int grp = warp >> 2, row = threadIdx.x & 127;      // the thread's group and row (TMEM lane)
+    const int half = warp >> 2, row = threadIdx.x & 127;     // the thread's tokens of a tile and row (TMEM lane)
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;  // the warp's TMEM lanes
-    load_queries<1, N, kSoftWarps>(a, sm + oQ, kQ, outr, qsum, qmax, scale_f, f_full, warp, lane);
-    if (lane == 0) mbar_arrive(q_full);
-
+    // Q: this thread's 64 channels of its row, scaled (query_exponent) and split into two fp16 parts
+    {
+      const int r = outr[row];
+      const float4* src = reinterpret_cast<const float4*>(a.qrot + int64_t(max(r, 0)) * D + 64 * half);
+      uint32_t mx = 0;
+      if (r >= 0) {
+#pragma unroll 8
+        for (int j = 0; j < 16; ++j) {
+          const float4 v = __ldg(src + j);
+          const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (isfinite(f[e])) mx = max(mx, __float_as_uint(fabsf(f[e])));
+        }
+      }
+      mx = __reduce_max_sync(0xffffffffu, mx);
+      if (lane == 0) atomicMax(qmax, mx);
+      asm volatile("bar.sync 3, 256;" ::: "memory");
+      const int fe = query_exponent(*qmax);
+      const float inv = pow2i(-fe);
+      if (threadIdx.x == 0) *scale_f = pow2i(fe);
+      float sum = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r >= 0) v = __ldg(src + 8 * c + j);
+          sum += split_pair(v.x * inv, v.y * inv, hi[2 * j], lo[2 * j]);
+          sum += split_pair(v.z * inv, v.w * inv, hi[2 * j + 1], lo[2 * j + 1]);
+        }
+        tmem_st16(tmem + lanes + cQ + 32 * half + 16 * c, hi);
+        tmem_st16(tmem + lanes + cQ + 64 + 32 * half + 16 * c, lo);
+      }
+      swap[half * N + row] = sum;
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      asm volatile("bar.sync 3, 256;" ::: "memory");
+      if (half == 0) {
+        const uint2 q = rank_query(swap[row] + swap[N + row]);
+        uint8_t* rank = sm + oRank + 2 * kRank;
+        *reinterpret_cast<uint4*>(rank + rank_offset(row, 0)) = make_uint4(q.x, q.y, 0, 0);
+        *reinterpret_cast<uint4*>(rank + rank_offset(row, 8)) = make_uint4(0, 0, 0, 0);
+      }
+      fence_async();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(f_full);
+        mbar_arrive(q_full);
+      }
+      asm volatile("bar.sync 3, 256;" ::: "memory");  // the sums have been read
+    }
     const int t_row = (rt * N + row) / g.G;
     const int lim = outr[row] < 0 ? -1 : a.causal ? T - ql + t_row : T - 1;  // last position that the row sees
-    const uint64_t q2 = splat_x2(qsum[row]);
-    const uint32_t S = tmem + lanes + cS + grp * 128, O = tmem + lanes + cO + grp * 128;
+    const uint32_t O = tmem + lanes + cO + 64 * half;
     float M = kNone;
     uint64_t l2 = 0;
     bool ok = true;
-    for (int i = grp; i < nt; i += 2) {
+#pragma unroll 1
+    for (int i = 0; i < nt; ++i) {
       const int cb = i % CB, base_pos = p0 + i * kTok;
       ok = ok && wait(c_full + 8 * cb, (i / CB) & 1);
-      ok = ok && wait(s_full + 8 * grp, (i >> 1) & 1);
-      if (!ok) break;
+      ok = ok && wait(s_full + 8 * (i & 1), (i >> 1) & 1);
       fence_after();
-      const TokenConsts<1> tc(sm + oConst, cb);
+      const uint32_t S = tmem + lanes + cS + (i & 1) * 128 + 64 * half;
+      const TileConsts tc(sm + oConst, cb);
+      const float phi = *tc.phi();
+      const uint64_t phi2 = splat_x2(phi);
       const bool masked = base_pos + kTok - 1 > see_all;  // some row does not see some position of the tile
       const bool plain = !masked && *tc.uneven() == 0;
-      const int see = lim - base_pos;                      // columns j <= see are visible
-      const float* ks = tc.ks(0);
-      const float* kz = tc.kz(0);
-      const float* ev = tc.e();
-      const float* rv = tc.rv();
-      // u + n of 32 columns from c on (n = 0 or -M), in pairs
+      const int see = lim - base_pos - 64 * half;          // the thread's columns j <= see are visible
+      const float* ev = tc.e() + 64 * half;
+      const float* rv = tc.rv() + 64 * half;
+      // u + n of columns c .. c + 31 (n = 0 or -M) in a tile with exponents or hidden positions
       auto scores = [&](int c, const uint32_t (&r)[32], uint64_t n2, uint64_t (&x)[16]) {
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
-          const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(kz + c + 2 * j);
-          const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(ks + c + 2 * j);
-          x[j] = fma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), k.x, fma2(q2, z.x, n2));
-          x[j + 1] = fma2(pack2(__uint_as_float(r[2 * j + 2]), __uint_as_float(r[2 * j + 3])), k.y, fma2(q2, z.y, n2));
+          const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(ev + c + 2 * j);
+          x[j] = fma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), phi2, add2(e.x, n2));
+          x[j + 1] = fma2(pack2(__uint_as_float(r[2 * j + 2]), __uint_as_float(r[2 * j + 3])), phi2, add2(e.y, n2));
         }
-        if (!plain) {
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(ev + c + 2 * j);
-            x[j] = add2(x[j], e.x);
-            x[j + 1] = add2(x[j + 1], e.y);
-          }
-          if (masked) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              float p, q;
-              unpack2(x[j], p, q);
-              x[j] = pack2(c + 2 * j <= see ? p : -INFINITY, c + 2 * j + 1 <= see ? q : -INFINITY);
-            }
-          }
+        for (int j = 0; j < 16; ++j) {
+          float p, q;
+          unpack2(x[j], p, q);
+          x[j] = pack2(c + 2 * j <= see ? p : -INFINITY, c + 2 * j + 1 <= see ? q : -INFINITY);
         }
       };
       // the row's maximum over the tile
-      float top = -INFINITY;
-      {
-        uint32_t r[32];
-        tmem_ld32(S, r);
+      uint32_t r[32];
+      float top = -INFINITY, top1 = -INFINITY;
+      tmem_ld32(S, r);
+      if (plain) {
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          tmem_wait32(r);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            top = max3(top, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+            top1 = max3(top1, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+          }
+          if (c == 0) tmem_ld32(S + 32, r);
+        }
+        top = fmaxf(top, top1) * phi;
+      } else {
 #pragma unroll 1
-        for (int c = 0; c < kTok; c += 32) {
+        for (int c = 0; c < 64; c += 32) {
           uint64_t x[16];
           tmem_wait32(r);
           scores(c, r, 0, x);
-          if (c + 32 < kTok) tmem_ld32(S + c + 32, r);
-          float top1 = -INFINITY;
+          if (c == 0) tmem_ld32(S + 32, r);
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
+          for (int j = 0; j < 16; ++j) {
             float p, q;
             unpack2(x[j], p, q);
             top = max3(top, p, q);
-            unpack2(x[j + 1], p, q);
-            top1 = max3(top1, p, q);
           }
-          top = fmaxf(top, top1);
         }
       }
+      swap[(i & 1) * 2 * N + half * N + row] = top;
+      if (any256(3, !ok)) {
+        ok = false;
+        break;
+      }
+      top = fmaxf(top, swap[(i & 1) * 2 * N + (half ^ 1) * N + row]);
+      tmem_ld32(S, r);
       const bool grow = top > M + kGrow;
       if (__any_sync(0xffffffffu, grow)) {
         const float f = grow ? exp2f(M - top) : 1.f;
         if (grow) M = top;
-        const uint64_t f2 = splat_x2(f);
-        l2 = mul2(l2, f2);
-        if (i >= 2) {  // S is full again only after the group's previous product is complete
+        l2 = mul2(l2, splat_x2(f));
+        if (i > 0) {
+          ok = wait(p_done, (i - 1) & 1);  // O is not in use
+          fence_after();
+          tmem_wait32(r);
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t r[32];
+          for (int c = 0; c < 64; c += 32) {
             tmem_ld32(O + c, r);
             tmem_wait32(r);
 #pragma unroll
             for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
             tmem_st32(O + c, r);
           }
+          tmem_ld32(S, r);
         }
       }
-      // P, over S's columns that have been read
+      // P, over scores of this thread's that have been read
       const uint64_t n2 = splat_x2(-M);
-      {
-        uint32_t r[32];
-        tmem_ld32(S, r);
+      if (plain) {
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t p[16];
+          tmem_wait32(r);
+          uint64_t sum[2] = {0, 0};
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float v, w;
+            unpack2(fma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), phi2, n2), v, w);
+            v = ex2(v);
+            w = ex2(w);
+            p[j] = half2_of(v, w);
+            sum[j & 1] = add2(sum[j & 1], pack2(v, w));
+          }
+          if (c == 0) tmem_ld32(S + 32, r);
+          l2 = add2(l2, add2(sum[0], sum[1]));
+          tmem_st16(S + c / 2, p);
+        }
+      } else {
 #pragma unroll 1
-        for (int c = 0; c < kTok; c += 32) {
+        for (int c = 0; c < 64; c += 32) {
           uint64_t x[16];
           uint32_t p[16];
           tmem_wait32(r);
           scores(c, r, n2, x);
-          if (c + 32 < kTok) tmem_ld32(S + c + 32, r);
+          if (c == 0) tmem_ld32(S + 32, r);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             float v, w;
@@ -257,16 +331,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
             p[j] = half2_of(v, w);
             x[j] = pack2(v, w);
           }
-          if (plain) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) l2 = add2(l2, x[j]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(rv + c + 2 * j);
-              l2 = fma2(x[j], v.x, l2);
-              l2 = fma2(x[j + 1], v.y, l2);
-            }
+          for (int j = 0; j < 16; j += 2) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(rv + c + 2 * j);
+            l2 = fma2(x[j], v.x, l2);
+            l2 = fma2(x[j + 1], v.y, l2);
           }
           tmem_st16(S + c / 2, p);
         }
@@ -275,90 +344,90 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(p_full + 8 * grp);
+        mbar_arrive(p_full);
         mbar_arrive(c_empty + 8 * cb);
       }
     }
-    // the two groups' results become one
-    if (ok && grp < nt) {
-      const int last = nt - 1 - ((nt - 1 - grp) & 1);
-      ok = wait(p_done + 8 * grp, (last >> 1) & 1);
-    }
+    // the sums of a row's two threads, then O
+    // (one phase after the other: the last tile's scores only tell that the product before the last two is complete)
+    if (nt > 1) ok = ok && wait(p_done, (nt - 2) & 1);
+    ok = ok && wait(p_done, (nt - 1) & 1);
     float l, l1;
     unpack2(l2, l, l1);
     l += l1;
-    both[grp * N + row] = make_float2(M, l);
-    if (!ok && lane == 0) fail();
-    asm volatile("bar.sync 3, 256;" ::: "memory");
-    if (__all_sync(0xffffffffu, *abort_flag == 0)) {
+    float* sums = swap + (nt & 1) * 2 * N;  // not the last tile's maxima, which may still be read
+    sums[half * N + row] = l;
+    if (!any256(3, !ok)) {
       fence_after();
-      const float2 x = both[row], y = both[N + row];
-      const float top = fmaxf(x.x, y.x), f = exp2f(x.x - top), f1 = exp2f(y.x - top);
       const int r = outr[row];
-      if (r >= 0 && grp == 0)
-        *reinterpret_cast<float2*>(a.ml + (int64_t(r) * a.ns + s) * 2) = make_float2(top, x.y * f + y.y * f1);
+      if (r >= 0 && half == 0)
+        *reinterpret_cast<float2*>(a.ml + (int64_t(r) * a.ns + s) * 2) = make_float2(M, l + sums[N + row]);
 #pragma unroll 1
-      for (int c = 64 * grp; c < 64 * grp + 64; c += 16) {
-        uint32_t v[16], w[16];
-        tmem_ld16(tmem + lanes + cO + c, v);
-        if (nt > 1) tmem_ld16(tmem + lanes + cO + 128 + c, w);  // with one tile the second group has nothing
+      for (int c = 0; c < 64; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(O + c, v);
         tmem_wait16(v);
-        if (nt > 1) tmem_wait16(w);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float o = __uint_as_float(v[j]) * f;
-          if (nt > 1) o = fmaf(__uint_as_float(w[j]), f1, o);
-          v[j] = __float_as_uint(o);
-        }
         if (r >= 0) {
-          uint4* dst = reinterpret_cast<uint4*>(a.acc + (int64_t(r) * a.ns + s) * D + c);
+          uint4* dst = reinterpret_cast<uint4*>(a.acc + (int64_t(r) * a.ns + s) * D + 64 * half + c);
 #pragma unroll
           for (int j = 0; j < 4; ++j) dst[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         }
       }
+    } else if (lane == 0) {
+      fail();
     }
   } else if (warp < kSoftWarps + 8) {
     Share x{&a, u, T, p0, p1, nt, sm, base, abort_flag, scale_f, f_full, k_full, k_empty, v_full, v_empty, c_full, c_empty,
-            oK, oV, oRawK, oRawV, oConst};
+            oK, oV, oRawK, oRawV, oConst, oRank, oRow + 5 * N * 4};
     const bool ok = warp < kSoftWarps + 4 ? expand_k<1, KU, CB, kStages>(x, threadIdx.x - kSoftWarps * 32, lane)
                                           : expand_v<1, VU, CB, kStages>(x, warp & 3, lane);
     if (!ok && lane == 0) fail();
   } else if (lane == 0) {
     // ------------------------------ MMA issuer --------------------------------
     constexpr uint32_t id_qk = idesc_of(kTok, false, false), id_pv = idesc_of(D, false, true);
-    const uint32_t sQ = base + oQ, sK = base + oK, sV = base + oV;
+    const uint32_t sK = base + oK, sV = base + oV, sRank = base + oRank;
     auto wait1 = [&](uint32_t br, uint32_t parity) { return *abort_flag == 0 && mbar_wait(br, parity); };
+    int n = 0;  // K units used
     auto product_qk = [&](int i) {
-      const uint32_t d = tmem + cS + (i & 1) * 128;
+      const uint32_t d = tmem + cS + (i & 1) * 128, q = tmem + cQ;
 #pragma unroll 1
       for (int kb = 0; kb < 2; ++kb) {
-        const int n = 2 * i + kb, st = n % KU;
-        if (!wait1(k_full + 8 * st, (n / KU) & 1)) return false;
+        if (!wait1(k_full + 8 * (n % KU), (n / KU) & 1)) return false;
         fence_after();
-        const uint64_t q = desc_of(sQ + kb * (N * 128), 16), k = desc_of(sK + st * kUnit, 16);
+        const uint64_t k = desc_of(sK + n % KU * kUnit, 16);
 #pragma unroll
         for (int j = 0; j < 8; ++j)  // Q's high, then its low part; descriptors count 16 bytes
-          mma_f16_ss(d, q + (j >> 2) * (kQ >> 4) + 2 * (j & 3), k + 2 * (j & 3), id_qk, kb | j);
-        mma_commit(k_empty + 8 * st);
+          mma_f16_ts(d, q + 64 * (j >> 2) + 32 * kb + 8 * (j & 3), k + 2 * (j & 3), id_qk, kb | j);
+        if (kb == 0) mma_f16_ss(d, rank_desc(sRank + 2 * kRank), rank_desc(sRank + (i & 1) * kRank), id_qk, 1);
+        mma_commit(k_empty + 8 * (n % KU));
+        ++n;
+        if (g.lm) {
+          if (!wait1(k_full + 8 * (n % KU), (n / KU) & 1)) return false;
+          fence_after();
+          const uint64_t x = desc_of(sK + n % KU * kUnit, 16);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma_f16_ts(d, q + 32 * kb + 8 * j, x + 2 * j, id_qk, 1);
+          mma_commit(k_empty + 8 * (n % KU));
+          ++n;
+        }
       }
       mma_commit(s_full + 8 * (i & 1));
       return true;
     };
     auto product_pv = [&](int i) {
-      if (!wait1(p_full + 8 * (i & 1), (i >> 1) & 1)) return false;
+      if (!wait1(p_full, i & 1)) return false;
 #pragma unroll 1
       for (int k = 0; k < 2; ++k) {
         const int n = 2 * i + k, st = n % VU;
         if (!wait1(v_full + 8 * st, (n / VU) & 1)) return false;
         fence_after();
         const uint64_t v = desc_of(sV + st * kUnit, kUnit / 2);
-        const uint32_t p = tmem + cS + (i & 1) * 128 + 32 * k;  // 64 tokens of P in 32 columns
+        const uint32_t p = tmem + cS + (i & 1) * 128 + 64 * k;  // 64 tokens of P in 32 columns
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mma_f16_ts(tmem + cO + (i & 1) * 128, p + 8 * j, v + 128 * j, id_pv, (i >> 1) | k | j);
+        for (int j = 0; j < 4; ++j) mma_f16_ts(tmem + cO, p + 8 * j, v + 128 * j, id_pv, i | k | j);
         mma_commit(v_empty + 8 * st);
       }
-      mma_commit(p_done + 8 * (i & 1));
+      mma_commit(p_done);
       return true;
     };
     bool ok = wait1(q_full, 0);
@@ -372,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       ok = product_pv(i);
       if (ok && i + 2 < nt) {
         // the scores of tile i + 2 overwrite P
-        ok = wait1(p_done + 8 * (i & 1), (i >> 1) & 1);
+        ok = wait1(p_done, i & 1);
         if (ok) fence_after(), ok = product_qk(i + 2);
       }
     }

@@ -12,13 +12,10 @@
 //
 // and a token's scale, zero and exponents are one thread's scalars.
 //
-//   * Scores.  INT2 keys enter as the fp16 values y = 1 + code / 4 (Lloyd-Max:
-//     150 times the level's distance from the middle, +-75 or +-249), which are
-//     exact; the row's scale and zero are applied to the sum:
-//       score = ks * sum_d q_d y_d + kz * sum_d q_d,
-//     ks = 4 s, kz = z - 4 s.  BF16 keys are scaled by a power of two per row
-//     and group (ks = 2^e, kz = 0), exact as well.  q, scaled by a power of two per CTA, is
-//     the sum of two fp16 values, so scores have float32 accuracy.
+//   * Scores.  INT2 keys enter the product exactly, as s (c - 1) with the middles
+//     z + s as a rank-one term, BF16 keys exactly (expand_k in rows_tc.cuh); q,
+//     scaled by a power of two per CTA, is the sum of two fp16 values.  So the
+//     products' sums are scores of float32 accuracy.
 //   * Probabilities carry the value row's exponent: with v_t = 2^(e_t) w_t, |w| < 1,
 //     u = score + e_t, P = 2^(u - M) in fp16 and l += 2^(-e_t) 2^(u - M) in float32.
 //     Value rows w in fp16 and P round with 2^-12 each, far below the bf16
@@ -50,7 +47,7 @@ constexpr int kSoftWarps = 8;
 constexpr int kThreads = (kSoftWarps + 4 + 4 + 1) * 32;
 constexpr float kNone = -1e30f;        // M before the first tile
 constexpr float kTop = 15.f;           // largest t = u - M that P holds
-constexpr float kRoom = 6.f;           // a new M lies this far below the maximum
+constexpr float kRoom = 0.f;           // a new M lies this far below the maximum
 
 // Shared memory and TMEM of one instantiation.
 template <int DG, int N>
@@ -59,26 +56,27 @@ struct Plan {
   static constexpr bool kFull = DG * N >= 128;               // Q leaves room for fewer buffers
   static constexpr int KU = kBig ? 2 : kFull ? 3 : 4;        // K units
   static constexpr int VU = kBig ? 1 : 3;                    // V units
-  static constexpr int SB = kBig ? 1 : 2;                    // score buffers
+  static constexpr int SB = 2;                               // score buffers
   static constexpr int PB = kFull ? 1 : 2;                   // P buffers
-  static constexpr int CB = kBig ? 2 : 3;                    // tiles whose token constants are kept
-  static constexpr int kStages = kBig ? 2 : 3;               // (tile, group) steps whose codes are staged, plus one
+  static constexpr int CB = 3;                               // tiles whose constants are kept
+  static constexpr int kStages = kBig ? 2 : DG * N == 32 ? 5 : 3;  // (tile, group) steps whose codes are staged, plus one
   static constexpr int kQ = N * 256 * DG;                    // one of Q's two parts
-  static constexpr int kP = (N > 64 ? 2 : 1) * kTok * 128;   // one P buffer
+  static constexpr int kP = kTok * 128;                      // one P buffer
   static constexpr int oQ = 0;
   static constexpr int oP = oQ + 2 * kQ;
   static constexpr int oK = oP + PB * kP;
   static constexpr int oV = oK + KU * kUnit;
   static constexpr int oRawK = oV + VU * kUnit;
   static constexpr int oRawV = oRawK + kStages * kRawStage;
-  static constexpr int oConst = oRawV + kStages * kRawStage;
-  static constexpr int oRow = oConst + CB * TokenConsts<DG>::kBytes;  // per column: -M, limit, output row, factor, DG sums; scratch
-  static constexpr int kRow = N * 4 * (4 + DG) + 8 * N / 2 * 4;
+  static constexpr int oRank = oRawV + kStages * kRawStage;  // the keys' two and the queries' rank-one operands
+  static constexpr int oConst = oRank + 2 * kRank + N * 32;
+  static constexpr int oRow = oConst + CB * TileConsts::kBytes;  // per column: -M, limit, output row, factor; scratch
+  static constexpr int kRow = N * 4 * 4 + 8 * N / 2 * 4 + 64;
   static constexpr int oBar = oRow + kRow;
   static constexpr int kBars = 2 * KU + 2 * VU + 2 * SB + 2 * PB + 2 * CB + 3;
   static constexpr int kBytes = oBar + kBars * 8 + 32 + 1024;  // + alignment slack
   static constexpr int cS = 0;                                // TMEM columns of the scores
-  static constexpr int cO = SB * DG * N;                      // and of O^T
+  static constexpr int cO = SB * N;                           // and of O^T
   static_assert(cO + DG * N <= 512, "TMEM");
   static_assert(kBytes <= 232448, "shared memory");
 };
@@ -116,8 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
   int* limit = reinterpret_cast<int*>(negM + N);   // last position that the row sees
   int* outr = limit + N;                            // its index among all query rows, -1 = none
   float* factor = reinterpret_cast<float*>(outr + N);
-  float* qsum = factor + N;                         // [DG][N]
-  float* part = qsum + DG * N;                      // [8 warps][C]
+  float* part = factor + N;                         // [8 warps][C]
   const uint32_t bar = base + L::oBar;
   auto k_full = [&](int i) { return bar + 8u * i; };
   auto k_empty = [&](int i) { return bar + 8u * (L::KU + i); };
@@ -180,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     const int tok = threadIdx.x & 127;                      // and this thread's token (TMEM lane)
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16; // the warp's TMEM lanes
     const int id = 1 + grp;                                 // named barrier of the group
-    load_queries<DG, N, kSoftWarps>(a, sm + L::oQ, L::kQ, outr, qsum, qmax, scale_f, f_full, warp, lane);
+    load_queries<DG, N, kSoftWarps>(a, sm + L::oQ, L::kQ, outr, sm + L::oRank + 2 * kRank, qmax, scale_f, f_full, warp, lane);
     if (lane == 0) mbar_arrive(q_full);
 
     uint64_t l2[C / 2];  // this token's part of l, two columns at a time
@@ -194,17 +191,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
       ok = ok && wait(s_full(sb), (i / L::SB) & 1);
       if (i >= L::PB) ok = ok && wait(p_empty(pb), ((i / L::PB) & 1) ^ 1);
       fence_after();
-      const TokenConsts<DG> tc(sm + L::oConst, cb);
-      uint64_t ks[DG], kz[DG];
-#pragma unroll
-      for (int gr = 0; gr < DG; ++gr) {
-        ks[gr] = splat_x2(tc.ks(gr)[tok]);
-        kz[gr] = splat_x2(tc.kz(gr)[tok]);
-      }
+      const TileConsts tc(sm + L::oConst, cb);
+      const uint64_t phi2 = splat_x2(*tc.phi());
       const uint64_t e2 = splat_x2(tc.e()[tok]), rv2 = splat_x2(tc.rv()[tok]);
       const bool masked = p0 + i * kTok + kTok - 1 > see_all;  // some row does not see some position of the tile
       uint8_t* P = sm + L::oP + pb * L::kP + tok * 128;
-      const uint32_t S = tmem + lanes + L::cS + sb * DG * N;
+      const uint32_t S = tmem + lanes + L::cS + sb * N;
       // t = u - M (or u) of columns c .. c + 15
       auto scores = [&](int c, float (&t)[16], bool less_m) {
         uint64_t x[8];
@@ -218,28 +210,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
             x[j] = x[j + 1] = e2;
           }
         }
-        constexpr int GS = DG > 1 ? 2 : 1;  // groups in flight
+        uint32_t r[16];
+        tmem_ld16(S + c, r);
+        tmem_wait16(r);
 #pragma unroll
-        for (int g0 = 0; g0 < DG; g0 += GS) {
-          uint32_t r[GS][16];
-#pragma unroll
-          for (int gr = 0; gr < GS; ++gr) tmem_ld16(S + (g0 + gr) * N + c, r[gr]);
-#pragma unroll
-          for (int gr = 0; gr < GS; ++gr)
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(qsum + (g0 + gr) * N + c + 2 * j);
-              x[j] = fma2(q.x, kz[g0 + gr], x[j]);
-              x[j + 1] = fma2(q.y, kz[g0 + gr], x[j + 1]);
-            }
-#pragma unroll
-          for (int gr = 0; gr < GS; ++gr) tmem_wait16(r[gr]);
-#pragma unroll
-          for (int gr = 0; gr < GS; ++gr)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              x[j] = fma2(pack2(__uint_as_float(r[gr][2 * j]), __uint_as_float(r[gr][2 * j + 1])), ks[g0 + gr], x[j]);
-        }
+        for (int j = 0; j < 8; ++j)
+          x[j] = fma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), phi2, x[j]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) unpack2(x[j], t[2 * j], t[2 * j + 1]);
         if (masked) {
@@ -402,7 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     }
   } else if (warp < kSoftWarps + 8) {
     Share x{&a, u, T, p0, p1, nt, sm, base, abort_flag, scale_f, f_full, k_full(0), k_empty(0), v_full(0), v_empty(0),
-            c_full(0), c_empty(0), L::oK, L::oV, L::oRawK, L::oRawV, L::oConst};
+            c_full(0), c_empty(0), L::oK, L::oV, L::oRawK, L::oRawV, L::oConst, L::oRank,
+            L::oRow + L::kRow - 64};
     const bool ok = warp < kSoftWarps + 4 ? expand_k<DG, L::KU, L::CB, L::kStages>(x, threadIdx.x - kSoftWarps * 32, lane)
                                           : expand_v<DG, L::VU, L::CB, L::kStages>(x, warp & 3, lane);
     if (!ok && lane == 0) fail();
@@ -411,21 +388,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     constexpr uint32_t id_qk = idesc_of(N, false, false), id_pv = idesc_of(N, true, true);
     const uint32_t sQ = base + L::oQ, sK = base + L::oK, sV = base + L::oV, sP = base + L::oP;
     auto wait1 = [&](uint32_t br, uint32_t parity) { return *abort_flag == 0 && mbar_wait(br, parity); };
+    const uint32_t sRank = base + L::oRank;
+    int n = 0;  // K units used
     auto product_qk = [&](int i) {
       const int sb = i % L::SB;
       if (i >= L::SB && !wait1(s_empty(sb), ((i / L::SB) & 1) ^ 1)) return false;
+      const uint32_t d = tmem + L::cS + sb * N;
+#pragma unroll 1
       for (int kb = 0; kb < 2 * DG; ++kb) {
-        const int n = i * 2 * DG + kb, st = n % L::KU;
-        if (!wait1(k_full(st), (n / L::KU) & 1)) return false;
+        if (!wait1(k_full(n % L::KU), (n / L::KU) & 1)) return false;
         fence_after();
-        const uint32_t d = tmem + L::cS + (sb * DG + (kb >> 1)) * N;
+        const uint64_t k = desc_of(sK + n % L::KU * kUnit, 16), q = desc_of(sQ + kb * (N * 128), 16);
 #pragma unroll
-        for (int part = 0; part < 2; ++part)  // Q's high, then its low part
+        for (int j = 0; j < 8; ++j)  // Q's high, then its low part; descriptors count 16 bytes
+          mma_f16_ss(d, k + 2 * (j & 3), q + (j >> 2) * (L::kQ >> 4) + 2 * (j & 3), id_qk, kb | j);
+        if (kb == 2 * DG - 2)  // the middles of all groups are there
+          mma_f16_ss(d, rank_desc(sRank + (i & 1) * kRank), rank_desc(sRank + 2 * kRank), id_qk, 1);
+        mma_commit(k_empty(n % L::KU));
+        ++n;
+        if (g.lm) {
+          if (!wait1(k_full(n % L::KU), (n / L::KU) & 1)) return false;
+          fence_after();
+          const uint64_t x = desc_of(sK + n % L::KU * kUnit, 16);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_ss(d, desc_of(sK + st * kUnit + 32 * k, 16), desc_of(sQ + part * L::kQ + kb * (N * 128) + 32 * k, 16),
-                       id_qk, (kb & 1) | part | k);
-        mma_commit(k_empty(st));
+          for (int j = 0; j < 4; ++j) mma_f16_ss(d, x + 2 * j, q + 2 * j, id_qk, 1);
+          mma_commit(k_empty(n % L::KU));
+          ++n;
+        }
       }
       mma_commit(s_full(sb));
       return true;

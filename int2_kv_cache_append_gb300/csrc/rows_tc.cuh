@@ -126,7 +126,16 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// true in every thread of the named barrier's 128 if it is in one of them
+// true in every thread of the named barrier's 256 (128) if it is in one of them
+__device__ __forceinline__ bool any256(int id, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(uint32_t(p))
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ bool any128(int id, bool p) {
   uint32_t r;
   asm volatile(
@@ -172,7 +181,7 @@ __device__ __forceinline__ uint32_t codes_at8(uint32_t w, int p) {
   const int sh = 8 - 2 * p;
   return (sh >= 0 ? w << sh : w >> -sh) & 0x03000300u;
 }
-// Lloyd-Max: 150 times the level's distance from the middle (rho + 1/2 levels),
+// Lloyd-Max values: 150 times the level's distance from the middle (rho + 1/2 levels),
 // for codes at bits 8 and 24: with x = 2 c - 3, 150 (level - middle) = x (74 + x^2)
 // (75 = 1 * 75, 249 = 3 * 83), every step exact in fp16.
 __device__ __forceinline__ uint32_t lm_value(uint32_t c8) {
@@ -180,6 +189,11 @@ __device__ __forceinline__ uint32_t lm_value(uint32_t c8) {
   return hmul2(x, hfma2(x, x, 0x54A054A0u /* 74 */));
 }
 constexpr float kLmMiddle = kLmRho + 0.5f;
+// (c - [c > 1] - 1) / 4 = -1/4, 0, 0, 1/4 for codes at bits 8 and 24: the sum of a code's two bits, less one.
+__device__ __forceinline__ uint32_t lm_extra(uint32_t c8) {
+  const uint32_t sum = (c8 & 0x01000100u) + ((c8 >> 1) & 0x01000100u);
+  return hadd2(sum | 0x3C003C00u, 0xBD00BD00u);
+}
 // a bf16 pair times `scale`, as fp16
 __device__ __forceinline__ uint32_t scaled_half2(uint32_t x, float scale) {
   return half2_of(__uint_as_float(x << 16) * scale, __uint_as_float(x & 0xFFFF0000u) * scale);
@@ -198,14 +212,46 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The CTA's query rows as fp16 operands, by `warps` warps (named barrier 3):
-// scaled by a power of two so that the largest finite component is just below
-// 2^14, split into two fp16 values (22 bits below that), written K-major in
-// blocks of 64 channels; a warp takes one (row, group) at a time.  *scale and
-// f_full: the power of two that undoes the scaling; qsum[DG][N]: sums of the
-// operands' channels.
+// (x, y) as the sum of two fp16 pairs; returns the sum of what they stand for
+__device__ __forceinline__ float split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = half2_of(x, y);
+  const float2 a = __half22float2(*reinterpret_cast<__half2*>(&hi));
+  lo = half2_of(x - a.x, y - a.y);
+  const float2 b = __half22float2(*reinterpret_cast<__half2*>(&lo));
+  return (a.x + b.x) + (a.y + b.y);
+}
+
+// Scale of the CTA's query rows: a power of two that brings the largest finite
+// component just below 2^7 (sums of 128 of them stay in fp16).
+__device__ __forceinline__ int query_exponent(uint32_t max_bits) { return max(-100, min(100, (int(max_bits) >> 23) - 126 - 7)); }
+
+// Byte offset of element (row, k) of an operand of 16 k without swizzle: core
+// matrices of 8 rows x 16 bytes, the two of a row group 128 bytes apart.
+__device__ __forceinline__ uint32_t rank_offset(int row, int k) {
+  return uint32_t(row >> 3) * 256 + uint32_t(k >> 3) * 128 + uint32_t(row & 7) * 16 + uint32_t(k & 7) * 2;
+}
+__device__ __forceinline__ uint64_t rank_desc(uint32_t saddr) {
+  return uint64_t((saddr >> 4) & 0x3FFF) | (uint64_t(128 >> 4) << 16) | (uint64_t(256 >> 4) << 32) | (uint64_t(1) << 46);
+}
+// (hi, hi, lo, lo) of a row's sum and (hi, lo, hi, lo) of a key row's middle: their products' sum is sum * middle
+__device__ __forceinline__ uint2 rank_query(float x) {
+  const uint32_t h = half2_of(x, x);
+  const float r = x - __half2float(__ushort_as_half(uint16_t(h & 0xFFFF)));
+  return make_uint2(h, half2_of(r, r));
+}
+__device__ __forceinline__ uint2 rank_key(float x) {
+  const float h = __half2float(__float2half_rn(x));
+  const uint32_t hl = half2_of(h, x - h);
+  return make_uint2(hl, hl);
+}
+
+// The CTA's query rows as fp16 operands in shared memory, by `warps` warps
+// (named barrier 3): scaled (query_exponent), split into two fp16 values whose
+// sum has 22 bits, written K-major in blocks of 64 channels; a warp takes one
+// (row, group) at a time.  rank: the rows' sums per group for the rank-one term.
+// *scale and f_full: the power of two that undoes the scaling.
 template <int DG, int N, int warps>
-__device__ __forceinline__ void load_queries(const RowsArgs& a, uint8_t* sq, int part, const int* outr, float* qsum,
+__device__ __forceinline__ void load_queries(const RowsArgs& a, uint8_t* sq, int part, const int* outr, uint8_t* rank,
                                              uint32_t* qmax, float* scale, uint32_t f_full, int warp, int lane) {
   constexpr int D = DG * 128;
   uint32_t mx = 0;
@@ -221,8 +267,9 @@ __device__ __forceinline__ void load_queries(const RowsArgs& a, uint8_t* sq, int
   }
   mx = __reduce_max_sync(0xffffffffu, mx);
   if (lane == 0) atomicMax(qmax, mx);
+  for (int i = warp * 32 + lane; i < N * 2; i += warps * 32) *reinterpret_cast<uint4*>(rank + i * 16) = make_uint4(0, 0, 0, 0);
   asm volatile("bar.sync 3, %0;" ::"n"(warps * 32) : "memory");
-  const int fe = max(-100, min(100, (int(*qmax) >> 23) - 126 - 14));  // q = 2^fe q^
+  const int fe = query_exponent(*qmax);
   const float inv = pow2i(-fe);
   if (warp == 0 && lane == 0) *scale = pow2i(fe);
 #pragma unroll 2
@@ -236,39 +283,31 @@ __device__ __forceinline__ void load_queries(const RowsArgs& a, uint8_t* sq, int
     uint32_t hi[2], lo[2];
     float sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      hi[e] = half2_of(f[2 * e], f[2 * e + 1]);
-      const float2 x = __half22float2(*reinterpret_cast<__half2*>(&hi[e]));
-      lo[e] = half2_of(f[2 * e] - x.x, f[2 * e + 1] - x.y);
-      const float2 y = __half22float2(*reinterpret_cast<__half2*>(&lo[e]));
-      sum += (x.x + y.x) + (x.y + y.y);
-    }
+    for (int e = 0; e < 2; ++e) sum += split_pair(f[2 * e], f[2 * e + 1], hi[e], lo[e]);
 #pragma unroll
     for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
     // channels 4 lane .. 4 lane + 3: block lane / 16, 16-byte chunk (lane / 2) % 8, half lane % 2
     const int off = (2 * gr + (lane >> 4)) * (N * 128) + c * 128 + ((((lane >> 1) & 7) ^ (c & 7)) << 4) + ((lane & 1) << 3);
     *reinterpret_cast<uint2*>(sq + off) = make_uint2(hi[0], hi[1]);
     *reinterpret_cast<uint2*>(sq + part + off) = make_uint2(lo[0], lo[1]);
-    if (lane == 0) qsum[gr * N + c] = sum;
+    if (lane == 0) *reinterpret_cast<uint2*>(rank + rank_offset(c, 4 * gr)) = rank_query(sum);
   }
   fence_async();
   asm volatile("bar.sync 3, %0;" ::"n"(warps * 32) : "memory");
   if (lane == 0) mbar_arrive(f_full);
 }
 
-// Constants of a tile's tokens, one slot of the ring: float ks[DG][128],
-// kz[DG][128] (score = ks * acc + kz * sum q), e[128] (the value row's
-// exponent), rv[128] (2^-e), and a word that is set when some e is not 0.
-template <int DG>
-struct TokenConsts {
-  static constexpr int kBytes = (2 * DG + 2) * kTok * 4 + 16;
+// Constants of a tile, one slot of the ring: e[128] (the value rows'
+// exponents), rv[128] (2^-e), a word that is set when some e is not 0, and the
+// factor from the products' sums to scores in log2 units.
+struct TileConsts {
+  static constexpr int kBytes = 2 * kTok * 4 + 16;
   float* p;
-  __device__ __forceinline__ TokenConsts(uint8_t* ring, int slot) : p(reinterpret_cast<float*>(ring + slot * kBytes)) {}
-  __device__ __forceinline__ float* ks(int g) const { return p + g * kTok; }
-  __device__ __forceinline__ float* kz(int g) const { return p + (DG + g) * kTok; }
-  __device__ __forceinline__ float* e() const { return p + 2 * DG * kTok; }
-  __device__ __forceinline__ float* rv() const { return p + (2 * DG + 1) * kTok; }
-  __device__ __forceinline__ uint32_t* uneven() const { return reinterpret_cast<uint32_t*>(p + (2 * DG + 2) * kTok); }
+  __device__ __forceinline__ TileConsts(uint8_t* ring, int slot) : p(reinterpret_cast<float*>(ring + slot * kBytes)) {}
+  __device__ __forceinline__ float* e() const { return p; }
+  __device__ __forceinline__ float* rv() const { return p + kTok; }
+  __device__ __forceinline__ uint32_t* uneven() const { return reinterpret_cast<uint32_t*>(p + 2 * kTok); }
+  __device__ __forceinline__ float* phi() const { return p + 2 * kTok + 1; }
 };
 
 // What the expanding warps work on: positions [p0, p1) of unit u.
@@ -281,17 +320,30 @@ struct Share {
   const float* F;                 // scale of the queries, valid after f_full
   uint32_t f_full;
   uint32_t k_full, k_empty, v_full, v_empty, c_full, c_empty;  // first barrier of each kind
-  int oK, oV, oRawK, oRawV, oConst;
+  int oK, oV, oRawK, oRawV, oConst, oRank, oScratch;
 };
 constexpr int kRawStage = kTok * 36;  // staged codes (32 bytes) and scale / zero pairs of one (tile, group) and role
+constexpr int kRank = kTok * 32;      // one tile's rank-one operand
 
-// K, four warps, a thread per token.  Steps k = (tile, group); codes are staged
-// kStages - 1 steps ahead by cp.async, each thread its own row.
+// K, four warps, a thread per token.  An INT2 key is z + s c = (z + s) + s (c - 1),
+// and s (c - 1) is -s, 0, s or 2 s: exact in fp16.  The middles z + s enter as a
+// rank-one term of 16 more k (rank_key), so the products' sums are the scores.
+// Lloyd-Max levels are the uniform ones plus 0.16 (0, 1, 1, 2): z + rho s is the
+// middle and 0.16 s (-1, 0, 0, 1) goes to a second set of units that only Q's
+// high part meets (it is a twelfth of the first; its fp16 rounding and Q's low
+// part with it are below 2^-14 of a product).  BF16 keys are exact in fp16 once the tile's largest value is below 2^15; where it is not, or
+// far below 1, the whole tile is scaled by a power of two.
+//
+// Steps k = (tile, group); codes are staged kStages - 1 steps ahead by cp.async,
+// each thread its own row.  Returns false after a timeout.
 template <int DG, int KU, int CB, int kStages>
 __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
+  // the rank-one operand of tile i + 2 is written after unit 0 of that tile has found the unit KU before it empty, and
+  // tile i's is used with the first unit of its last group
+  static_assert(2 * (DG + 1) >= KU, "two rank-one operands");
   const Geom& g = x.a->g;
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity, lane, x.abort_flag); };
-  const int steps = x.nt * DG;
+  const int steps = x.nt * DG, per = g.lm ? 4 : 2;  // units of a step
   const uint8_t* role = x.a->layer_base + g.sink_bytes + g.ring_bytes;
   const int64_t row0 = int64_t(x.u) * g.ncap + (x.p0 + tok - g.S);  // INT2 row of the first tile's token
   const uint8_t* codes = role + row0 * (32 * DG);
@@ -310,82 +362,114 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
   };
 #pragma unroll 1
   for (int k = 0; k < kStages - 1; ++k) stage(k);
-  if (!wait(x.f_full, 0)) return false;
+  for (int j = 0; j < 4; ++j)  // columns beyond 4 DG stay zero
+    *reinterpret_cast<uint4*>(x.sm + x.oRank + (j >> 1) * kRank + rank_offset(tok, 8 * (j & 1))) = make_uint4(0, 0, 0, 0);
+  bool ok = wait(x.f_full, 0);  // a warp that gave up still comes to the group's barriers
   const float F = *x.F;
+  float down = 0.5f;            // the tile's power of two; one half keeps 2 s and z + s within fp16
+  int n = 0;                    // units written
 #pragma unroll 1
   for (int k = 0; k < steps; ++k) {
     stage(k + kStages - 1);
     cp_async_wait<kStages - 1>();
-    const int i = k / DG, gr = k % DG, cb = i % CB, pos = x.p0 + i * kTok + tok;
-    if (gr == 0 && i >= CB && !wait(x.c_empty + 8 * cb, ((i / CB) & 1) ^ 1)) return false;
+    const int i = k / DG, gr = k % DG, slot = i % CB, pos = x.p0 + i * kTok + tok;
     const bool valid = pos < x.p1, packed = valid && pos >= g.S && pos < ring0;
+    const __nv_bfloat16* wide = valid && !packed ? row_ref(g, x.a->layer_base, 0, x.u, x.T, pos).wide : nullptr;
+    if (gr == 0) {
+      float phi = 2.0f * F;
+      down = 0.5f;
+      const int first = x.p0 + i * kTok, last = min(x.p1, first + kTok) - 1;
+      if (first < g.S || last >= ring0) {  // the tile has BF16 rows
+        float m = 0.f;
+        if (packed) {
+#pragma unroll
+          for (int j = 0; j < DG; ++j) {
+            const float2 sz = __half22float2(reinterpret_cast<const __half2*>(szs + int64_t(i) * (kTok * 4 * DG))[j]);
+            m = fmaxf(m, fmaxf(fabsf(sz.y), fabsf(fmaf(sz.x, g.lm ? kLmSpan : 3.0f, sz.y))));
+          }
+        } else if (wide) {
+          uint32_t w = 0;
+          const uint4* src = reinterpret_cast<const uint4*>(wide);
+#pragma unroll 8
+          for (int j = 0; j < DG * 16; ++j) {
+            const uint4 v = src[j];
+            w = absmax2(absmax2(absmax2(absmax2(w, v.x), v.y), v.z), v.w);
+          }
+          m = __uint_as_float(max(w & 0xFFFFu, w >> 16) << 16);
+        }
+        const uint32_t wm = __reduce_max_sync(0xffffffffu, isfinite(m) ? __float_as_uint(m) : 0u);
+        uint32_t* most = reinterpret_cast<uint32_t*>(x.sm + x.oScratch) + 4 * (i & 3);
+        if (lane == 0) most[tok >> 5] = wm;
+        if (any128(5, !ok)) return false;
+        m = __uint_as_float(max(max(most[0], most[1]), max(most[2], most[3])));
+        if (m > 0.f && !(m >= 0x1p-4f && m < 0x1p14f)) {
+          const int e = max(-104, min(127, (int(__float_as_uint(m)) >> 23) - 126)) - 13;  // 2^-e m is just below 2^13
+          down = pow2i(-e);
+          phi = F * pow2i(e);
+        }
+      }
+      if (i >= CB) ok = ok && wait(x.c_empty + 8 * slot, ((i / CB) & 1) ^ 1);
+      if (tok == 0) *TileConsts(x.sm + x.oConst, slot).phi() = phi;
+      if (lane == 0) mbar_arrive(x.c_full + 8 * slot);
+    }
     const uint8_t* st = x.sm + x.oRawK + (k % kStages) * kRawStage;
     const uint4 c0 = *reinterpret_cast<const uint4*>(st + tok * 32), c1 = *reinterpret_cast<const uint4*>(st + tok * 32 + 16);
-    float ks = 0.f, kz = 0.f, scale = 0.f;
-    const __nv_bfloat16* wide = nullptr;
-    if (packed) {
-      const float2 sz = __half22float2(*reinterpret_cast<const __half2*>(st + kTok * 32 + tok * 4));
-      if (g.lm) ks = sz.x * (1.0f / 150.0f), kz = fmaf(sz.x, kLmMiddle, sz.y);
-      else ks = 4.0f * sz.x, kz = fmaf(-4.0f, sz.x, sz.y);
-    } else if (valid) {
-      wide = row_ref(g, x.a->layer_base, 0, x.u, x.T, pos).wide + gr * 128;
-      uint32_t m = 0;
-      const uint4* src = reinterpret_cast<const uint4*>(wide);
-#pragma unroll 8
-      for (int j = 0; j < 16; ++j) {
-        const uint4 v = src[j];
-        m = absmax2(absmax2(absmax2(absmax2(m, v.x), v.y), v.z), v.w);
-      }
-      m = max(m & 0xFFFFu, m >> 16);
-      const int e = max(-104, int(m >> 7) - 126) - 15;  // 2^-e times the row's largest value is just below 2^15
-      scale = pow2i(-e);
-      ks = pow2i(e);
-    }
-    const TokenConsts<DG> tc(x.sm + x.oConst, cb);
-    tc.ks(gr)[tok] = ks * F;
-    tc.kz(gr)[tok] = kz * F;
+    float2 sz = make_float2(0.f, 0.f);
+    if (packed) sz = __half22float2(*reinterpret_cast<const __half2*>(st + kTok * 32 + tok * 4));
+    const uint32_t s1 = half2_of(sz.x * down, sz.x * down);
+    const uint32_t d4 = half2_of(4.0f * (kLmRho - 1.0f) * sz.x * down, 4.0f * (kLmRho - 1.0f) * sz.x * down);
+    const float middle = fmaf(g.lm ? kLmRho : 1.0f, sz.x, sz.y) * down;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
-      const int n = 2 * k + half, u = n % KU;
-      if (n >= KU && !wait(x.k_empty + 8 * u, ((n / KU) & 1) ^ 1)) return false;
-      uint8_t* row = x.sm + x.oK + u * kUnit + tok * 128;
-      if (packed) {
-        // word 2 c + half: pair c of every 16-byte chunk
-        const uint32_t w[4] = {half ? c0.y : c0.x, half ? c0.w : c0.z, half ? c1.y : c1.x, half ? c1.w : c1.z};
-        if (g.lm) {
+      // word 2 c + half: pair c of every 16-byte chunk
+      const uint32_t w[4] = {half ? c0.y : c0.x, half ? c0.w : c0.z, half ? c1.y : c1.x, half ? c1.w : c1.z};
+#pragma unroll 1
+      for (int set = 0; set < per; set += 2, ++n) {
+        const int u = n % KU;
+        if (n >= KU) ok = ok && wait(x.k_empty + 8 * u, ((n / KU) & 1) ^ 1);
+        if (!ok) continue;
+        if (half == 0 && set == 0)
+          *reinterpret_cast<uint2*>(x.sm + x.oRank + (i & 1) * kRank + rank_offset(tok, 4 * gr)) = rank_key(middle);
+        uint8_t* row = x.sm + x.oK + u * kUnit + tok * 128;
+        if (packed && set == 0) {
 #pragma unroll
-          for (int p = 0; p < 8; ++p)
-            *reinterpret_cast<uint4*>(row + ((p ^ (tok & 7)) << 4)) =
-                make_uint4(lm_value(codes_at8(w[0], p)), lm_value(codes_at8(w[1], p)), lm_value(codes_at8(w[2], p)),
-                           lm_value(codes_at8(w[3], p)));
+          for (int p = 0; p < 8; ++p) {
+            uint32_t v[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)  // (4 (1 + c / 4) - 5) s
+              v[c] = hmul2(hfma2(codes_at8(w[c], p) | 0x3C003C00u, 0x44004400u, 0xC500C500u), s1);
+            *reinterpret_cast<uint4*>(row + ((p ^ (tok & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        } else if (packed) {
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            uint32_t v[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = hmul2(lm_extra(codes_at8(w[c], p)), d4);
+            *reinterpret_cast<uint4*>(row + ((p ^ (tok & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
         } else {
-#pragma unroll
-          for (int p = 0; p < 8; ++p)
-            *reinterpret_cast<uint4*>(row + ((p ^ (tok & 7)) << 4)) =
-                make_uint4(codes_at8(w[0], p) | 0x3C003C00u, codes_at8(w[1], p) | 0x3C003C00u,
-                           codes_at8(w[2], p) | 0x3C003C00u, codes_at8(w[3], p) | 0x3C003C00u);
-        }
-      } else {
 #pragma unroll 4
-        for (int p = 0; p < 8; ++p) {
-          const uint4 v = wide ? reinterpret_cast<const uint4*>(wide + half * 64)[p] : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(row + ((p ^ (tok & 7)) << 4)) =
-              make_uint4(scaled_half2(v.x, scale), scaled_half2(v.y, scale), scaled_half2(v.z, scale), scaled_half2(v.w, scale));
+          for (int p = 0; p < 8; ++p) {
+            const uint4 v = wide && set == 0 ? reinterpret_cast<const uint4*>(wide + gr * 128 + half * 64)[p] : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(row + ((p ^ (tok & 7)) << 4)) =
+                make_uint4(scaled_half2(v.x, down), scaled_half2(v.y, down), scaled_half2(v.z, down), scaled_half2(v.w, down));
+          }
         }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x.k_full + 8 * u);
       }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(x.k_full + 8 * u);
     }
-    if (gr == DG - 1 && lane == 0) mbar_arrive(x.c_full + 8 * cb);
   }
-  return true;
+  return ok;
 }
 
 // V, four warps.  Warp w holds tokens 64 h + 16 w .. + 15 of both unit halves h;
 // lanes 16 c + j write the 64-channel block c of token 16 w + j.  For the
-// exponents and the scale / zero pairs, fetched a tile ahead, lane 16 h + j
-// stands for the token of half h.
+// exponents and the scale / zero pairs, fetched two tiles ahead, lane 16 h + j
+// stands for the token of half h.  The exponents of a tile are published before
+// the previous tile's units, which wait for products, are written.
 template <int DG, int VU, int CB, int kStages>
 __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
   const Geom& g = x.a->g;
@@ -405,58 +489,63 @@ __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
     cp_async_commit();
   };
   const int mine = 64 * cb + sub;  // the lane's token for exponents
-  __half2 sz[DG], nsz[DG];
-  auto pairs = [&](int i, __half2 (&d)[DG]) {
+  uint32_t sz[DG], nsz[DG], fsz[DG];  // this tile's pairs, the next one's and those on their way
+  auto pairs = [&](int i, uint32_t (&d)[DG]) {
     const int pos = x.p0 + i * kTok + mine;
     const bool packed = pos >= pk0 && pos < pk1;
 #pragma unroll
-    for (int gr = 0; gr < DG; ++gr) d[gr] = packed ? __ldg(szs + int64_t(i) * (kTok * DG) + gr) : __half2half2(__half(0.f));
+    for (int gr = 0; gr < DG; ++gr)
+      d[gr] = packed ? __ldg(reinterpret_cast<const uint32_t*>(szs + int64_t(i) * (kTok * DG) + gr)) : 0u;
+  };
+  float e = 0.f, ne = 0.f;
+  auto publish = [&](int i, const uint32_t (&pr)[DG]) {  // tile i's exponents
+    const int pos = x.p0 + i * kTok + mine, slot = i % CB;
+    float m = 0.f;
+    if (pos >= pk0 && pos < pk1) {
+#pragma unroll
+      for (int j = 0; j < DG; ++j) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&pr[j]));
+        m = fmax_nan(m, fmax_nan(fabsf(v.y), fabsf(fmaf(v.x, g.lm ? kLmSpan : 3.0f, v.y))));
+      }
+    } else if (pos < x.p1) {
+      uint32_t w = 0;
+      const uint4* src = reinterpret_cast<const uint4*>(row_ref(g, x.a->layer_base, 1, x.u, x.T, pos).wide);
+#pragma unroll 8
+      for (int j = 0; j < DG * 16; ++j) {
+        const uint4 v = src[j];
+        w = absmax2(absmax2(absmax2(absmax2(w, v.x), v.y), v.z), v.w);
+      }
+      m = __uint_as_float(max(w & 0xFFFFu, w >> 16) << 16);
+    }
+    // rows of ordinary size keep exponent 0
+    ne = pos >= x.p1 ? -INFINITY
+         : !isfinite(m) ? NAN
+         : m >= 0x1p-8f && m < 0x1p14f ? 0.f : float(exponent_above(m));
+    if (i >= CB && !wait(x.c_empty + 8 * slot, ((i / CB) & 1) ^ 1)) return false;
+    const TileConsts tc(x.sm + x.oConst, slot);
+    tc.e()[mine] = ne;
+    tc.rv()[mine] = isfinite(ne) ? pow2i(-int(ne)) : 1.f;
+    const bool uneven = __any_sync(0xffffffffu, ne != 0.f);
+    if (lane == 0) reinterpret_cast<volatile uint8_t*>(tc.uneven())[warp4] = uneven;  // one byte per warp
+    __syncwarp();
+    if (lane == 0) mbar_arrive(x.c_full + 8 * slot);
+    return true;
   };
   pairs(0, nsz);
+  pairs(1, fsz);
 #pragma unroll 1
   for (int k = 0; k < kStages - 1; ++k) stage(k);
-  float e = 0.f;
+  if (!publish(0, nsz)) return false;
 #pragma unroll 1
   for (int k = 0; k < steps; ++k) {
     stage(k + kStages - 1);
-    const int i = k / DG, gr = k % DG, slot = i % CB;
+    const int i = k / DG, gr = k % DG;
     if (gr == 0) {
+      e = ne;
 #pragma unroll
-      for (int j = 0; j < DG; ++j) sz[j] = nsz[j];
-      pairs(i + 1, nsz);
-      const int pos = x.p0 + i * kTok + mine;
-      float m = 0.f;
-      if (pos >= pk0 && pos < pk1) {
-#pragma unroll
-        for (int j = 0; j < DG; ++j) {
-          const float2 v = __half22float2(sz[j]);
-          m = fmax_nan(m, fmax_nan(fabsf(v.y), fabsf(fmaf(v.x, g.lm ? kLmSpan : 3.0f, v.y))));
-        }
-      } else if (pos < x.p1) {
-        uint32_t w = 0;
-        const uint4* src = reinterpret_cast<const uint4*>(row_ref(g, x.a->layer_base, 1, x.u, x.T, pos).wide);
-#pragma unroll 8
-        for (int j = 0; j < DG * 16; ++j) {
-          const uint4 v = src[j];
-          w = absmax2(absmax2(absmax2(absmax2(w, v.x), v.y), v.z), v.w);
-        }
-        m = __uint_as_float(max(w & 0xFFFFu, w >> 16) << 16);
-      }
-      // rows of ordinary size keep exponent 0
-      e = pos >= x.p1 ? -INFINITY
-          : !isfinite(m) ? NAN
-          : m >= 0x1p-8f && m < 0x1p14f ? 0.f : float(exponent_above(m));
-      if (i >= CB && !wait(x.c_empty + 8 * slot, ((i / CB) & 1) ^ 1)) return false;
-      const TokenConsts<DG> tc(x.sm + x.oConst, slot);
-      tc.e()[mine] = e;
-      tc.rv()[mine] = isfinite(e) ? pow2i(-int(e)) : 1.f;
-      const bool uneven = __any_sync(0xffffffffu, e != 0.f);
-      if (lane == 0) {
-        // one byte per warp
-        reinterpret_cast<volatile uint8_t*>(tc.uneven())[warp4] = uneven;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(x.c_full + 8 * slot);
+      for (int j = 0; j < DG; ++j) sz[j] = nsz[j], nsz[j] = fsz[j];
+      pairs(i + 2, fsz);
+      if (i + 1 < x.nt && !publish(i + 1, nsz)) return false;
     }
     cp_async_wait<kStages - 1>();
     __syncwarp();  // the other lane's half of the row has landed, too
@@ -468,7 +557,7 @@ __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
       uint32_t pair = 0;
 #pragma unroll
       for (int j = 0; j < DG; ++j)
-        if (j == gr) pair = __shfl_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&sz[j]), from);
+        if (j == gr) pair = __shfl_sync(0xffffffffu, sz[j], from);
       const uint8_t* st = x.sm + x.oRawV + (k % kStages) * kRawStage + (64 * half + sub) * 32;
       const uint4 c0 = *reinterpret_cast<const uint4*>(st), c1 = *reinterpret_cast<const uint4*>(st + 16);
       if (n >= VU && !wait(x.v_empty + 8 * u, ((n / VU) & 1) ^ 1)) return false;
