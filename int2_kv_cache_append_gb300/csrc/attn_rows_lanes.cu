@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     *abort_flag = 1;
     status_or(a.status, OSCAR_DEV_TIMEOUT);
   };
-  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity, lane, abort_flag); };
+  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity, abort_flag); };
 
   if (warp < kSoftWarps) {
     // ------------------------------- softmax ---------------------------------
@@ -193,10 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       fence_async();
       fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(f_full);
-        mbar_arrive(q_full);
-      }
+            mbar_arrive_if(f_full, lane == 0);
+      mbar_arrive_if(q_full, lane == 0);
       asm volatile("bar.sync 3, 256;" ::: "memory");  // the sums have been read
     }
     const int t_row = (rt * N + row) / g.G;
@@ -305,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
           for (int j = 0; j < 16; ++j) {
             float v, w;
             unpack2(fma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), phi2, n2), v, w);
-            v = ex2(v);
-            w = ex2(w);
+            v = ex2z(v);
+            w = ex2z(w);
             p[j] = half2_of(v, w);
             sum[j & 1] = add2(sum[j & 1], pack2(v, w));
           }
@@ -326,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
           for (int j = 0; j < 16; ++j) {
             float v, w;
             unpack2(x[j], v, w);
-            v = ex2(v);
-            w = ex2(w);
+            v = ex2z(v);
+            w = ex2z(w);
             p[j] = half2_of(v, w);
             x[j] = pack2(v, w);
           }
@@ -343,10 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(p_full);
-        mbar_arrive(c_empty + 8 * cb);
-      }
+            mbar_arrive_if(p_full, lane == 0);
+      mbar_arrive_if(c_empty + 8 * cb, lane == 0);
     }
     // the sums of a row's two threads, then O
     // (one phase after the other: the last tile's scores only tell that the product before the last two is complete)

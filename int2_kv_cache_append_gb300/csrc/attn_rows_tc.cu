@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     *abort_flag = 1;
     status_or(a.status, OSCAR_DEV_TIMEOUT);
   };
-  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity, lane, abort_flag); };
+  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity, abort_flag); };
 
   if (warp < kSoftWarps) {
     // ------------------------------- softmax ---------------------------------
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16; // the warp's TMEM lanes
     const int id = 1 + grp;                                 // named barrier of the group
     load_queries<DG, N, kSoftWarps>(a, sm + L::oQ, L::kQ, outr, sm + L::oRank + 2 * kRank, qmax, scale_f, f_full, warp, lane);
-    if (lane == 0) mbar_arrive(q_full);
+    mbar_arrive_if(q_full, lane == 0);
 
     uint64_t l2[C / 2];  // this token's part of l, two columns at a time
 #pragma unroll
@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
             top = max3(top, t[j], t[j + 1]);
-            t[j] = ex2(t[j]);
-            t[j + 1] = ex2(t[j + 1]);
+            t[j] = ex2z(t[j]);
+            t[j + 1] = ex2z(t[j + 1]);
             l2[(c + j) / 2] = fma2(pack2(t[j], t[j + 1]), rv2, l2[(c + j) / 2]);
           }
           store(c0 + c, t);
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
           float t[16];
           scores(c0 + c, t, true);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) t[j] = ex2(t[j]);
+          for (int j = 0; j < 16; ++j) t[j] = ex2z(t[j]);
           float rv, unused;
           unpack2(rv2, rv, unused);
 #pragma unroll
@@ -330,11 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
       fence_async();
       fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(s_empty(sb));
-        mbar_arrive(p_full(pb));
-        mbar_arrive(c_empty(cb));
-      }
+            mbar_arrive_if(s_empty(sb), lane == 0);
+      mbar_arrive_if(p_full(pb), lane == 0);
+      mbar_arrive_if(c_empty(cb), lane == 0);
     }
     // sums over the tokens, then O^T
     if (ok) ok = wait(p_empty((nt - 1) % L::PB), ((nt - 1) / L::PB) & 1);

@@ -145,11 +145,24 @@ __device__ __forceinline__ bool any128(int id, bool p) {
       : "memory");
   return r != 0;
 }
-// Bounded wait of a whole warp, given up at once when the CTA is aborting.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int lane, const volatile uint32_t* abort_flag) {
-  int ok = 1;
-  if (lane == 0) ok = *abort_flag == 0 && mbar_wait(bar, parity);
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+// Bounded wait of a whole warp, given up at once when the CTA is aborting.  All
+// lanes poll (one instruction); the way out of the fast path is warp-uniform.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const volatile uint32_t* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const bool ok = *abort_flag == 0 && mbar_wait(bar, parity);
+  return __all_sync(0xffffffffu, ok);
+}
+// Arrival of the threads with `p`, without a branch.
+__device__ __forceinline__ void mbar_arrive_if(uint32_t bar, bool p) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar),
+               "r"(uint32_t(p))
+               : "memory");
+}
+// 2^x, results below the normal range are 0
+__device__ __forceinline__ float ex2z(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 // v[j] of lane l, summed over the lanes, for column j = l (n = 32) or l % 16 (n = 16).
 template <int n>
@@ -176,23 +189,37 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) 
 __device__ __forceinline__ int exponent_above(float x) {
   return min(126, max(-60, (int(__float_as_uint(x)) >> 23) - 126));
 }
-// the two codes of a word at bits 2 p and 16 + 2 p, moved to bits 8 and 24
-__device__ __forceinline__ uint32_t codes_at8(uint32_t w, int p) {
-  const int sh = 8 - 2 * p;
-  return (sh >= 0 ? w << sh : w >> -sh) & 0x03000300u;
+// Codes of a word at bits 2 p and 16 + 2 p as fp16 pairs, two p per shift: for
+// w = code_shift(word, q), p = 2 q + 1 lies at bits 8 and 24 (1 + c / 4) and
+// p = 2 q at bits 6 and 22 (1 + c / 16).
+__device__ __forceinline__ uint32_t code_shift(uint32_t word, int q) {
+  const int sh = 6 - 4 * q;
+  return sh >= 0 ? word << sh : word >> -sh;
 }
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t code_odd(uint32_t w) { return and_or(w, 0x03000300u, 0x3C003C00u); }
+__device__ __forceinline__ uint32_t code_even(uint32_t w) { return and_or(w, 0x00C000C0u, 0x3C003C00u); }
+// c - 1 of a code
+__device__ __forceinline__ uint32_t less_one_odd(uint32_t w) { return hfma2(code_odd(w), 0x44004400u /* 4 */, 0xC500C500u /* -5 */); }
+__device__ __forceinline__ uint32_t less_one_even(uint32_t w) { return hfma2(code_even(w), 0x4C004C00u /* 16 */, 0xCC40CC40u /* -17 */); }
 // Lloyd-Max values: 150 times the level's distance from the middle (rho + 1/2 levels),
-// for codes at bits 8 and 24: with x = 2 c - 3, 150 (level - middle) = x (74 + x^2)
+// from c - 1: with x = 2 c - 3 = 2 (c - 1) - 1, 150 (level - middle) = x (74 + x^2)
 // (75 = 1 * 75, 249 = 3 * 83), every step exact in fp16.
-__device__ __forceinline__ uint32_t lm_value(uint32_t c8) {
-  const uint32_t x = hfma2(c8 | 0x3C003C00u, 0x48004800u /* 8 */, 0xC980C980u /* -11 */);
+__device__ __forceinline__ uint32_t lm_value(uint32_t c1) {
+  const uint32_t x = hfma2(c1, 0x40004000u /* 2 */, 0xBC00BC00u /* -1 */);
   return hmul2(x, hfma2(x, x, 0x54A054A0u /* 74 */));
 }
 constexpr float kLmMiddle = kLmRho + 0.5f;
-// (c - [c > 1] - 1) / 4 = -1/4, 0, 0, 1/4 for codes at bits 8 and 24: the sum of a code's two bits, less one.
-__device__ __forceinline__ uint32_t lm_extra(uint32_t c8) {
-  const uint32_t sum = (c8 & 0x01000100u) + ((c8 >> 1) & 0x01000100u);
-  return hadd2(sum | 0x3C003C00u, 0xBD00BD00u);
+// c - [c > 1] - 1 = -1, 0, 0, 1 from c - 1 = -1, 0, 1, 2 = k: k - (k > 0), the step taken from k by clamping to [0, 1].
+__device__ __forceinline__ uint32_t lm_extra(uint32_t c1) {
+  uint32_t step;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(step) : "r"(c1), "r"(0u));
+  asm("min.f16x2 %0, %0, %1;" : "+r"(step) : "r"(0x3C003C00u));
+  return hfma2(step, 0xBC00BC00u, c1);
 }
 // a bf16 pair times `scale`, as fp16
 __device__ __forceinline__ uint32_t scaled_half2(uint32_t x, float scale) {
@@ -294,7 +321,7 @@ __device__ __forceinline__ void load_queries(const RowsArgs& a, uint8_t* sq, int
   }
   fence_async();
   asm volatile("bar.sync 3, %0;" ::"n"(warps * 32) : "memory");
-  if (lane == 0) mbar_arrive(f_full);
+  mbar_arrive_if(f_full, lane == 0);
 }
 
 // Constants of a tile, one slot of the ring: e[128] (the value rows'
@@ -308,6 +335,11 @@ struct TileConsts {
   __device__ __forceinline__ float* rv() const { return p + kTok; }
   __device__ __forceinline__ uint32_t* uneven() const { return reinterpret_cast<uint32_t*>(p + 2 * kTok); }
   __device__ __forceinline__ float* phi() const { return p + 2 * kTok + 1; }
+};
+
+template <bool b>
+struct Flag {
+  static constexpr bool value = b;
 };
 
 // What the expanding warps work on: positions [p0, p1) of unit u.
@@ -342,7 +374,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
   // tile i's is used with the first unit of its last group
   static_assert(2 * (DG + 1) >= KU, "two rank-one operands");
   const Geom& g = x.a->g;
-  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity, lane, x.abort_flag); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity, x.abort_flag); };
   const int steps = x.nt * DG, per = g.lm ? 4 : 2;  // units of a step
   const uint8_t* role = x.a->layer_base + g.sink_bytes + g.ring_bytes;
   const int64_t row0 = int64_t(x.u) * g.ncap + (x.p0 + tok - g.S);  // INT2 row of the first tile's token
@@ -410,14 +442,14 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
       }
       if (i >= CB) ok = ok && wait(x.c_empty + 8 * slot, ((i / CB) & 1) ^ 1);
       if (tok == 0) *TileConsts(x.sm + x.oConst, slot).phi() = phi;
-      if (lane == 0) mbar_arrive(x.c_full + 8 * slot);
+      mbar_arrive_if(x.c_full + 8 * slot, lane == 0);
     }
     const uint8_t* st = x.sm + x.oRawK + (k % kStages) * kRawStage;
     const uint4 c0 = *reinterpret_cast<const uint4*>(st + tok * 32), c1 = *reinterpret_cast<const uint4*>(st + tok * 32 + 16);
     float2 sz = make_float2(0.f, 0.f);
     if (packed) sz = __half22float2(*reinterpret_cast<const __half2*>(st + kTok * 32 + tok * 4));
     const uint32_t s1 = half2_of(sz.x * down, sz.x * down);
-    const uint32_t d4 = half2_of(4.0f * (kLmRho - 1.0f) * sz.x * down, 4.0f * (kLmRho - 1.0f) * sz.x * down);
+    const uint32_t d1 = half2_of((kLmRho - 1.0f) * sz.x * down, (kLmRho - 1.0f) * sz.x * down);
     const float middle = fmaf(g.lm ? kLmRho : 1.0f, sz.x, sz.y) * down;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
@@ -433,20 +465,29 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
         uint8_t* row = x.sm + x.oK + u * kUnit + tok * 128;
         if (packed && set == 0) {
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            uint32_t v[4];
+          for (int q = 0; q < 4; ++q) {
+            uint32_t v[4], o[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)  // (4 (1 + c / 4) - 5) s
-              v[c] = hmul2(hfma2(codes_at8(w[c], p) | 0x3C003C00u, 0x44004400u, 0xC500C500u), s1);
-            *reinterpret_cast<uint4*>(row + ((p ^ (tok & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t y = code_shift(w[c], q);
+              v[c] = hmul2(less_one_even(y), s1);
+              o[c] = hmul2(less_one_odd(y), s1);
+            }
+            *reinterpret_cast<uint4*>(row + (((2 * q) ^ (tok & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(row + (((2 * q + 1) ^ (tok & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         } else if (packed) {
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            uint32_t v[4];
+          for (int q = 0; q < 4; ++q) {
+            uint32_t v[4], o[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] = hmul2(lm_extra(codes_at8(w[c], p)), d4);
-            *reinterpret_cast<uint4*>(row + ((p ^ (tok & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t y = code_shift(w[c], q);
+              v[c] = hmul2(lm_extra(less_one_even(y)), d1);
+              o[c] = hmul2(lm_extra(less_one_odd(y)), d1);
+            }
+            *reinterpret_cast<uint4*>(row + (((2 * q) ^ (tok & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(row + (((2 * q + 1) ^ (tok & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         } else {
 #pragma unroll 4
@@ -458,7 +499,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(x.k_full + 8 * u);
+        mbar_arrive_if(x.k_full + 8 * u, lane == 0);
       }
     }
   }
@@ -473,7 +514,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
 template <int DG, int VU, int CB, int kStages>
 __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
   const Geom& g = x.a->g;
-  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity, lane, x.abort_flag); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity, x.abort_flag); };
   const int steps = x.nt * DG, cb = lane >> 4, sub = 16 * warp4 + (lane & 15);
   const uint8_t* role = x.a->layer_base + g.role_bytes + g.sink_bytes + g.ring_bytes;
   const int64_t row0 = int64_t(x.u) * g.ncap + (x.p0 + sub - g.S);
@@ -520,7 +561,7 @@ __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
     // rows of ordinary size keep exponent 0
     ne = pos >= x.p1 ? -INFINITY
          : !isfinite(m) ? NAN
-         : m >= 0x1p-8f && m < 0x1p14f ? 0.f : float(exponent_above(m));
+         : m >= 0x1p-8f && m < 0x1p12f ? 0.f : float(exponent_above(m));
     if (i >= CB && !wait(x.c_empty + 8 * slot, ((i / CB) & 1) ^ 1)) return false;
     const TileConsts tc(x.sm + x.oConst, slot);
     tc.e()[mine] = ne;
@@ -528,7 +569,7 @@ __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
     const bool uneven = __any_sync(0xffffffffu, ne != 0.f);
     if (lane == 0) reinterpret_cast<volatile uint8_t*>(tc.uneven())[warp4] = uneven;  // one byte per warp
     __syncwarp();
-    if (lane == 0) mbar_arrive(x.c_full + 8 * slot);
+    mbar_arrive_if(x.c_full + 8 * slot, lane == 0);
     return true;
   };
   pairs(0, nsz);
@@ -568,26 +609,39 @@ __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
         const uint32_t sel = cb ? 0x7632u : 0x5410u;
         const uint32_t w[4] = {prmt(c0.x, c0.y, sel), prmt(c0.z, c0.w, sel), prmt(c1.x, c1.y, sel), prmt(c1.z, c1.w, sel)};
         const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&pair));
+        // Uniform: c / 4 or c / 16 from 1 + that, exactly; then one rounding of s c + z.  Lloyd-Max: one of the unit, one
+        // of the middle and one of the sum.
+        uint32_t s_odd, s_even, z2;
         if (g.lm) {
-          const uint32_t s2 = half2_of(v.x * scale * (1.0f / 150.0f), v.x * scale * (1.0f / 150.0f));
+          s_odd = s_even = half2_of(v.x * scale * (1.0f / 150.0f), v.x * scale * (1.0f / 150.0f));
           const float mid = fmaf(v.x, kLmMiddle, v.y) * scale;
-          const uint32_t z2 = half2_of(mid, mid);
-#pragma unroll
-          for (int p = 0; p < 8; ++p)
-            *reinterpret_cast<uint4*>(row + ((p ^ (sub & 7)) << 4)) =
-                make_uint4(hfma2(lm_value(codes_at8(w[0], p)), s2, z2), hfma2(lm_value(codes_at8(w[1], p)), s2, z2),
-                           hfma2(lm_value(codes_at8(w[2], p)), s2, z2), hfma2(lm_value(codes_at8(w[3], p)), s2, z2));
+          z2 = half2_of(mid, mid);
         } else {
-          // c / 4 from 1 + c / 4, exactly; then one rounding
-          const uint32_t s2 = half2_of(v.x * scale * 4.0f, v.x * scale * 4.0f), z2 = half2_of(v.y * scale, v.y * scale);
-          auto value = [&](uint32_t word, int p) {
-            return hfma2(hadd2(codes_at8(word, p) | 0x3C003C00u, 0xBC00BC00u), s2, z2);
-          };
-#pragma unroll
-          for (int p = 0; p < 8; ++p)
-            *reinterpret_cast<uint4*>(row + ((p ^ (sub & 7)) << 4)) =
-                make_uint4(value(w[0], p), value(w[1], p), value(w[2], p), value(w[3], p));
+          s_odd = half2_of(v.x * scale * 4.0f, v.x * scale * 4.0f);
+          s_even = half2_of(v.x * scale * 16.0f, v.x * scale * 16.0f);
+          z2 = half2_of(v.y * scale, v.y * scale);
         }
+        auto write = [&](auto lm) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t a[4], o[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t y = code_shift(w[c], q);
+              if constexpr (decltype(lm)::value) {
+                a[c] = hfma2(lm_value(less_one_even(y)), s_even, z2);
+                o[c] = hfma2(lm_value(less_one_odd(y)), s_odd, z2);
+              } else {
+                a[c] = hfma2(hadd2(code_even(y), 0xBC00BC00u), s_even, z2);
+                o[c] = hfma2(hadd2(code_odd(y), 0xBC00BC00u), s_odd, z2);
+              }
+            }
+            *reinterpret_cast<uint4*>(row + (((2 * q) ^ (sub & 7)) << 4)) = make_uint4(a[0], a[1], a[2], a[3]);
+            *reinterpret_cast<uint4*>(row + (((2 * q + 1) ^ (sub & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        };
+        if (g.lm) write(Flag<true>());
+        else write(Flag<false>());
       } else {
         const uint4* src = fine && pos < x.p1
                                ? reinterpret_cast<const uint4*>(row_ref(g, x.a->layer_base, 1, x.u, x.T, pos).wide + gr * 128 + cb * 64)
@@ -601,7 +655,7 @@ __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
       }
       fence_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(x.v_full + 8 * u);
+      mbar_arrive_if(x.v_full + 8 * u, lane == 0);
     }
     __syncwarp();  // the stage has been read by both lanes before it is written again
   }
