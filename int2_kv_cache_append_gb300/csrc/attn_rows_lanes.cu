@@ -48,23 +48,28 @@ constexpr int kBytes = oBar + kBars * 8 + 32 + 1024;  // + alignment slack
 static_assert(oBar % 8 == 0 && kBytes <= 232448, "shared memory");
 constexpr uint32_t cS = 0, cO = 256, cQ = 384;        // TMEM columns: two score tiles, O, Q's two parts
 
-__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32]) {
+// 64 consecutive columns of the thread's TMEM lane
+__device__ __forceinline__ void tmem_ld64(uint32_t a, uint32_t (&r)[64]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
-      "[%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(a));
-}
-__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                  "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
                  "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]),
+                 "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]),
+                 "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]),
+                 "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
+                 "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
                :
                : "memory");
 }
@@ -193,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       fence_async();
       fence_before();
       __syncwarp();
-            mbar_arrive_if(f_full, lane == 0);
+      mbar_arrive_if(f_full, lane == 0);
       mbar_arrive_if(q_full, lane == 0);
       asm volatile("bar.sync 3, 256;" ::: "memory");  // the sums have been read
     }
@@ -212,57 +217,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       const uint32_t S = tmem + lanes + cS + (i & 1) * 128 + 64 * half;
       const TileConsts tc(sm + oConst, cb);
       const float phi = *tc.phi();
-      const uint64_t phi2 = splat_x2(phi);
       const bool masked = base_pos + kTok - 1 > see_all;  // some row does not see some position of the tile
       const bool plain = !masked && *tc.uneven() == 0;
       const int see = lim - base_pos - 64 * half;          // the thread's columns j <= see are visible
       const float* ev = tc.e() + 64 * half;
       const float* rv = tc.rv() + 64 * half;
-      // u + n of columns c .. c + 31 (n = 0 or -M) in a tile with exponents or hidden positions
-      auto scores = [&](int c, const uint32_t (&r)[32], uint64_t n2, uint64_t (&x)[16]) {
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(ev + c + 2 * j);
-          x[j] = fma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), phi2, add2(e.x, n2));
-          x[j + 1] = fma2(pack2(__uint_as_float(r[2 * j + 2]), __uint_as_float(r[2 * j + 3])), phi2, add2(e.y, n2));
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float p, q;
-          unpack2(x[j], p, q);
-          x[j] = pack2(c + 2 * j <= see ? p : -INFINITY, c + 2 * j + 1 <= see ? q : -INFINITY);
-        }
-      };
-      // the row's maximum over the tile
-      uint32_t r[32];
+      // the scores of this thread's 64 tokens; with exponents or hidden positions, u = phi S + e or -inf instead
+      uint32_t r[64];
+      tmem_ld64(S, r);
       float top = -INFINITY, top1 = -INFINITY;
-      tmem_ld32(S, r);
       if (plain) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          tmem_wait32(r);
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            top = max3(top, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
-            top1 = max3(top1, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
-          }
-          if (c == 0) tmem_ld32(S + 32, r);
+        for (int j = 0; j < 64; j += 4) {
+          top = max3(top, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+          top1 = max3(top1, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
         }
         top = fmaxf(top, top1) * phi;
       } else {
-#pragma unroll 1
-        for (int c = 0; c < 64; c += 32) {
-          uint64_t x[16];
-          tmem_wait32(r);
-          scores(c, r, 0, x);
-          if (c == 0) tmem_ld32(S + 32, r);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float p, q;
-            unpack2(x[j], p, q);
-            top = max3(top, p, q);
-          }
+        for (int j = 0; j < 64; j += 4) {
+          const float4 e = *reinterpret_cast<const float4*>(ev + j);
+          const float x[4] = {fmaf(__uint_as_float(r[j]), phi, e.x), fmaf(__uint_as_float(r[j + 1]), phi, e.y),
+                              fmaf(__uint_as_float(r[j + 2]), phi, e.z), fmaf(__uint_as_float(r[j + 3]), phi, e.w)};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) r[j + q] = __float_as_uint(j + q <= see ? x[q] : -INFINITY);
+          top = max3(top, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+          top1 = max3(top1, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
         }
+        top = fmaxf(top, top1);
       }
       swap[(i & 1) * 2 * N + half * N + row] = top;
       if (any256(3, !ok)) {
@@ -270,7 +252,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
         break;
       }
       top = fmaxf(top, swap[(i & 1) * 2 * N + (half ^ 1) * N + row]);
-      tmem_ld32(S, r);
       const bool grow = top > M + kGrow;
       if (__any_sync(0xffffffffu, grow)) {
         const float f = grow ? exp2f(M - top) : 1.f;
@@ -279,74 +260,67 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
         if (i > 0) {
           ok = wait(p_done, (i - 1) & 1);  // O is not in use
           fence_after();
-          tmem_wait32(r);
 #pragma unroll 1
-          for (int c = 0; c < 64; c += 32) {
-            tmem_ld32(O + c, r);
-            tmem_wait32(r);
+          for (int c = 0; c < 64; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(O + c, o);
+            tmem_wait16(o);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
-            tmem_st32(O + c, r);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st16(O + c, o);
           }
-          tmem_ld32(S, r);
         }
       }
-      // P, over scores of this thread's that have been read
+      // P, over the scores
       const uint64_t n2 = splat_x2(-M);
+      uint64_t sum = 0;
       if (plain) {
+        const uint64_t phi2 = splat_x2(phi);
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
           uint32_t p[16];
-          tmem_wait32(r);
-          uint64_t sum[2] = {0, 0};
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             float v, w;
-            unpack2(fma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), phi2, n2), v, w);
+            unpack2(fma2(pack2(__uint_as_float(r[c + 2 * j]), __uint_as_float(r[c + 2 * j + 1])), phi2, n2), v, w);
             v = ex2z(v);
             w = ex2z(w);
             p[j] = half2_of(v, w);
-            sum[j & 1] = add2(sum[j & 1], pack2(v, w));
+            if (j & 1) sum = add2(sum, pack2(v, w));
+            else l2 = add2(l2, pack2(v, w));
           }
-          if (c == 0) tmem_ld32(S + 32, r);
-          l2 = add2(l2, add2(sum[0], sum[1]));
           tmem_st16(S + c / 2, p);
         }
       } else {
-#pragma unroll 1
-        for (int c = 0; c < 64; c += 32) {
-          uint64_t x[16];
-          uint32_t p[16];
-          tmem_wait32(r);
-          scores(c, r, n2, x);
-          if (c == 0) tmem_ld32(S + 32, r);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float v, w;
-            unpack2(x[j], v, w);
-            v = ex2z(v);
-            w = ex2z(w);
-            p[j] = half2_of(v, w);
-            x[j] = pack2(v, w);
-          }
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t p[16];
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
-            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(rv + c + 2 * j);
-            l2 = fma2(x[j], v.x, l2);
-            l2 = fma2(x[j + 1], v.y, l2);
+            const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(rv + c + 2 * j);
+            float v[4];
+            unpack2(add2(pack2(__uint_as_float(r[c + 2 * j]), __uint_as_float(r[c + 2 * j + 1])), n2), v[0], v[1]);
+            unpack2(add2(pack2(__uint_as_float(r[c + 2 * j + 2]), __uint_as_float(r[c + 2 * j + 3])), n2), v[2], v[3]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = ex2z(v[q]);
+            p[j] = half2_of(v[0], v[1]);
+            p[j + 1] = half2_of(v[2], v[3]);
+            l2 = fma2(pack2(v[0], v[1]), y.x, l2);
+            sum = fma2(pack2(v[2], v[3]), y.y, sum);
           }
           tmem_st16(S + c / 2, p);
         }
       }
+      l2 = add2(l2, sum);
+      // every warp sees every phase of p_done: the next one cannot complete before this warp's arrival below
+      if (i > 0) ok = ok && wait(p_done, (i - 1) & 1);
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       fence_before();
       __syncwarp();
-            mbar_arrive_if(p_full, lane == 0);
+      mbar_arrive_if(p_full, lane == 0);
       mbar_arrive_if(c_empty + 8 * cb, lane == 0);
     }
     // the sums of a row's two threads, then O
-    // (one phase after the other: the last tile's scores only tell that the product before the last two is complete)
-    if (nt > 1) ok = ok && wait(p_done, (nt - 2) & 1);
     ok = ok && wait(p_done, (nt - 1) & 1);
     float l, l1;
     unpack2(l2, l, l1);
@@ -378,55 +352,55 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     const bool ok = warp < kSoftWarps + 4 ? expand_k<1, KU, CB, kStages>(x, threadIdx.x - kSoftWarps * 32, lane)
                                           : expand_v<1, VU, CB, kStages>(x, warp & 3, lane);
     if (!ok && lane == 0) fail();
-  } else if (lane == 0) {
+  } else {
     // ------------------------------ MMA issuer --------------------------------
+    const uint32_t leader = elect_one();
     constexpr uint32_t id_qk = idesc_of(kTok, false, false), id_pv = idesc_of(D, false, true);
     const uint32_t sK = base + oK, sV = base + oV, sRank = base + oRank;
-    auto wait1 = [&](uint32_t br, uint32_t parity) { return *abort_flag == 0 && mbar_wait(br, parity); };
     int n = 0;  // K units used
     auto product_qk = [&](int i) {
       const uint32_t d = tmem + cS + (i & 1) * 128, q = tmem + cQ;
 #pragma unroll 1
       for (int kb = 0; kb < 2; ++kb) {
-        if (!wait1(k_full + 8 * (n % KU), (n / KU) & 1)) return false;
+        if (!wait(k_full + 8 * (n % KU), (n / KU) & 1)) return false;
         fence_after();
         const uint64_t k = desc_of(sK + n % KU * kUnit, 16);
 #pragma unroll
         for (int j = 0; j < 8; ++j)  // Q's high, then its low part; descriptors count 16 bytes
-          mma_f16_ts(d, q + 64 * (j >> 2) + 32 * kb + 8 * (j & 3), k + 2 * (j & 3), id_qk, kb | j);
-        if (kb == 0) mma_f16_ss(d, rank_desc(sRank + 2 * kRank), rank_desc(sRank + (i & 1) * kRank), id_qk, 1);
-        mma_commit(k_empty + 8 * (n % KU));
+          mma_f16_ts(d, q + 64 * (j >> 2) + 32 * kb + 8 * (j & 3), k + 2 * (j & 3), id_qk, kb | j, leader);
+        if (kb == 0) mma_f16_ss(d, rank_desc(sRank + 2 * kRank), rank_desc(sRank + (i & 1) * kRank), id_qk, 1, leader);
+        mma_commit(k_empty + 8 * (n % KU), leader);
         ++n;
         if (g.lm) {
-          if (!wait1(k_full + 8 * (n % KU), (n / KU) & 1)) return false;
+          if (!wait(k_full + 8 * (n % KU), (n / KU) & 1)) return false;
           fence_after();
           const uint64_t x = desc_of(sK + n % KU * kUnit, 16);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma_f16_ts(d, q + 32 * kb + 8 * j, x + 2 * j, id_qk, 1);
-          mma_commit(k_empty + 8 * (n % KU));
+          for (int j = 0; j < 4; ++j) mma_f16_ts(d, q + 32 * kb + 8 * j, x + 2 * j, id_qk, 1, leader);
+          mma_commit(k_empty + 8 * (n % KU), leader);
           ++n;
         }
       }
-      mma_commit(s_full + 8 * (i & 1));
+      mma_commit(s_full + 8 * (i & 1), leader);
       return true;
     };
     auto product_pv = [&](int i) {
-      if (!wait1(p_full, i & 1)) return false;
+      if (!wait(p_full, i & 1)) return false;
 #pragma unroll 1
       for (int k = 0; k < 2; ++k) {
         const int n = 2 * i + k, st = n % VU;
-        if (!wait1(v_full + 8 * st, (n / VU) & 1)) return false;
+        if (!wait(v_full + 8 * st, (n / VU) & 1)) return false;
         fence_after();
         const uint64_t v = desc_of(sV + st * kUnit, kUnit / 2);
         const uint32_t p = tmem + cS + (i & 1) * 128 + 64 * k;  // 64 tokens of P in 32 columns
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_f16_ts(tmem + cO, p + 8 * j, v + 128 * j, id_pv, i | k | j);
-        mma_commit(v_empty + 8 * st);
+        for (int j = 0; j < 4; ++j) mma_f16_ts(tmem + cO, p + 8 * j, v + 128 * j, id_pv, i | k | j, leader);
+        mma_commit(v_empty + 8 * st, leader);
       }
-      mma_commit(p_done);
+      mma_commit(p_done, leader);
       return true;
     };
-    bool ok = wait1(q_full, 0);
+    bool ok = wait(q_full, 0);
     if (ok) {
       fence_after();
       ok = product_qk(0);
@@ -437,13 +411,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       ok = product_pv(i);
       if (ok && i + 2 < nt) {
         // the scores of tile i + 2 overwrite P
-        ok = wait1(p_done, i & 1);
+        ok = wait(p_done, i & 1);
         if (ok) fence_after(), ok = product_qk(i + 2);
       }
     }
-    if (!ok) fail();
-    mma_commit(drained);  // every product issued is complete before TMEM is freed
+    if (!ok && lane == 0) fail();
+    mma_commit(drained, leader);  // every product issued is complete before TMEM is freed
     mbar_wait(drained, 0);
+    __syncwarp();
   }
   fence_before();
   __syncthreads();

@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
       fence_async();
       fence_before();
       __syncwarp();
-            mbar_arrive_if(s_empty(sb), lane == 0);
+      mbar_arrive_if(s_empty(sb), lane == 0);
       mbar_arrive_if(p_full(pb), lane == 0);
       mbar_arrive_if(c_empty(cb), lane == 0);
     }
@@ -381,59 +381,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     const bool ok = warp < kSoftWarps + 4 ? expand_k<DG, L::KU, L::CB, L::kStages>(x, threadIdx.x - kSoftWarps * 32, lane)
                                           : expand_v<DG, L::VU, L::CB, L::kStages>(x, warp & 3, lane);
     if (!ok && lane == 0) fail();
-  } else if (lane == 0) {
+  } else {
     // ------------------------------ MMA issuer --------------------------------
+    const uint32_t leader = elect_one();
     constexpr uint32_t id_qk = idesc_of(N, false, false), id_pv = idesc_of(N, true, true);
     const uint32_t sQ = base + L::oQ, sK = base + L::oK, sV = base + L::oV, sP = base + L::oP;
-    auto wait1 = [&](uint32_t br, uint32_t parity) { return *abort_flag == 0 && mbar_wait(br, parity); };
     const uint32_t sRank = base + L::oRank;
     int n = 0;  // K units used
     auto product_qk = [&](int i) {
       const int sb = i % L::SB;
-      if (i >= L::SB && !wait1(s_empty(sb), ((i / L::SB) & 1) ^ 1)) return false;
+      if (i >= L::SB && !wait(s_empty(sb), ((i / L::SB) & 1) ^ 1)) return false;
       const uint32_t d = tmem + L::cS + sb * N;
 #pragma unroll 1
       for (int kb = 0; kb < 2 * DG; ++kb) {
-        if (!wait1(k_full(n % L::KU), (n / L::KU) & 1)) return false;
+        if (!wait(k_full(n % L::KU), (n / L::KU) & 1)) return false;
         fence_after();
         const uint64_t k = desc_of(sK + n % L::KU * kUnit, 16), q = desc_of(sQ + kb * (N * 128), 16);
 #pragma unroll
         for (int j = 0; j < 8; ++j)  // Q's high, then its low part; descriptors count 16 bytes
-          mma_f16_ss(d, k + 2 * (j & 3), q + (j >> 2) * (L::kQ >> 4) + 2 * (j & 3), id_qk, kb | j);
+          mma_f16_ss(d, k + 2 * (j & 3), q + (j >> 2) * (L::kQ >> 4) + 2 * (j & 3), id_qk, kb | j, leader);
         if (kb == 2 * DG - 2)  // the middles of all groups are there
-          mma_f16_ss(d, rank_desc(sRank + (i & 1) * kRank), rank_desc(sRank + 2 * kRank), id_qk, 1);
-        mma_commit(k_empty(n % L::KU));
+          mma_f16_ss(d, rank_desc(sRank + (i & 1) * kRank), rank_desc(sRank + 2 * kRank), id_qk, 1, leader);
+        mma_commit(k_empty(n % L::KU), leader);
         ++n;
         if (g.lm) {
-          if (!wait1(k_full(n % L::KU), (n / L::KU) & 1)) return false;
+          if (!wait(k_full(n % L::KU), (n / L::KU) & 1)) return false;
           fence_after();
           const uint64_t x = desc_of(sK + n % L::KU * kUnit, 16);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma_f16_ss(d, x + 2 * j, q + 2 * j, id_qk, 1);
-          mma_commit(k_empty(n % L::KU));
+          for (int j = 0; j < 4; ++j) mma_f16_ss(d, x + 2 * j, q + 2 * j, id_qk, 1, leader);
+          mma_commit(k_empty(n % L::KU), leader);
           ++n;
         }
       }
-      mma_commit(s_full(sb));
+      mma_commit(s_full(sb), leader);
       return true;
     };
     auto product_pv = [&](int i) {
       const int pb = i % L::PB;
-      if (!wait1(p_full(pb), (i / L::PB) & 1)) return false;
+      if (!wait(p_full(pb), (i / L::PB) & 1)) return false;
       for (int k = 0; k < 2 * DG; ++k) {  // group k / 2, token half k % 2
         const int n = i * 2 * DG + k, st = n % L::VU;
-        if (!wait1(v_full(st), (n / L::VU) & 1)) return false;
+        if (!wait(v_full(st), (n / L::VU) & 1)) return false;
         fence_after();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           mma_f16_ss(tmem + L::cO + (k >> 1) * N, desc_of(sV + st * kUnit + 2048 * j, kUnit / 2),
-                     desc_of(sP + pb * L::kP + (k & 1) * 8192 + 2048 * j, kTok * 128), id_pv, i | (k & 1) | j);
-        mma_commit(v_empty(st));
+                     desc_of(sP + pb * L::kP + (k & 1) * 8192 + 2048 * j, kTok * 128), id_pv, i | (k & 1) | j, leader);
+        mma_commit(v_empty(st), leader);
       }
-      mma_commit(p_empty(pb));
+      mma_commit(p_empty(pb), leader);
       return true;
     };
-    bool ok = wait1(q_full, 0);
+    bool ok = wait(q_full, 0);
     if (ok) {
       fence_after();
       ok = product_qk(0);
@@ -442,9 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
       if (i + 1 < nt) ok = product_qk(i + 1);
       if (ok) ok = product_pv(i);
     }
-    if (!ok) fail();
-    mma_commit(drained);  // every product issued is complete before TMEM is freed
+    if (!ok && lane == 0) fail();
+    mma_commit(drained, leader);  // every product issued is complete before TMEM is freed
     mbar_wait(drained, 0);
+    __syncwarp();
   }
   fence_before();
   __syncthreads();
