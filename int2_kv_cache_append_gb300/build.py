@@ -18,7 +18,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liboscar_kv.so")
 SOURCES = ["oscar_kv_api.cu", "kv_append.cu", "kv_append_tc.cu", "attn_decode.cu", "attn_decode_static.cu",
            "calibrate.cu", "kv_rows.cu", "attn_rows.cu", "attn_rows_tc.cu",
-           "attn_rows_lanes.cu"]
+           "attn_rows_lanes.cu", "kv_rows_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -107,6 +107,7 @@ struct ReadArgs {
   int out_fp32, absorb_v, hadamard;
 };
 int launch_read(const ReadArgs& a, cudaStream_t stream);
+int launch_read_tc(const ReadArgs& a, cudaStream_t stream);  // (kv_rows_tc.cu)
 
 // Attention of blocks of query rows over one cache: unit (b, h) has n * G rows
 // r = t * G + e, row r being query head h * G + e of token t of sequence b.
@@ -143,6 +144,7 @@ struct QrotRowsArgs {
   float qscale;
 };
 int launch_qrot_rows(const QrotRowsArgs& a, cudaStream_t stream);
+int launch_qrot_rows_tc(const QrotRowsArgs& a, cudaStream_t stream);
 
 // Merge of the splits' partial results, V un-rotation and store (kv_rows.cu).
 struct FinishArgs {
@@ -161,5 +163,6 @@ struct FinishArgs {
   int out_fp32, absorb_v, hadamard;
 };
 int launch_finish_rows(const FinishArgs& a, cudaStream_t stream);
+int launch_finish_rows_tc(const FinishArgs& a, cudaStream_t stream);
 
 }  // namespace oscar

@@ -69,14 +69,6 @@ __device__ __forceinline__ void store4(void* out, int64_t at, int fp32, const fl
   }
 }
 
-// Row (b n + t) Hq + head of a query block is one of the sequence's tokens.
-__device__ __forceinline__ bool row_live(int64_t row, int64_t rows, const int32_t* q_lens, int n, int Hq) {
-  if (row >= rows) return false;
-  if (!q_lens) return true;
-  const int64_t bt = row / Hq;
-  return int(bt % n) < q_lens[bt / n];
-}
-
 // ------------------------------------------------------------------- kv_read
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadArgs a) {
   extern __shared__ float sm[];
@@ -234,6 +226,9 @@ __global__ void __launch_bounds__(kThreads) finish_rows_kernel(const FinishArgs 
     if (live[4 * rw + i]) store4(a.out, (row0 + 4 * rw + i) * D + c0 + 4 * lane, a.out_fp32, y[i]);
 }
 
+// Rows from which the tensor-core kernels take over.
+constexpr int64_t kTensorRows = 1024;
+
 size_t smem_of(int D) { return size_t(kRows * (D + 4) + kDeep * kPitch) * 4; }
 
 // Raises the dynamic shared memory limit of the three kernels, once per device.
@@ -258,6 +253,8 @@ int launched() { return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR
 int launch_read(const ReadArgs& a, cudaStream_t stream) {
   const int64_t tiles = (int64_t(a.g.B) * a.n * a.g.Hkv + kRows - 1) / kRows;
   if (tiles == 0) return OSCAR_OK;
+  const int64_t rows = int64_t(a.g.B) * a.n * a.g.Hkv;
+  if (rows >= kTensorRows && rows < (int64_t(1) << 31)) return launch_read_tc(a, stream);
   if (tiles >= (int64_t(1) << 31)) return OSCAR_ERR_UNSUPPORTED;
   if (!ready()) return OSCAR_ERR_LAUNCH;
   kv_read_kernel<<<dim3(unsigned(tiles), a.g.Dg, 2), kThreads, smem_of(a.g.D), stream>>>(a);
@@ -265,12 +262,14 @@ int launch_read(const ReadArgs& a, cudaStream_t stream) {
 }
 
 int launch_qrot_rows(const QrotRowsArgs& a, cudaStream_t stream) {
+  if (a.rows >= kTensorRows && !a.zero_word) return launch_qrot_rows_tc(a, stream);
   if (!ready()) return OSCAR_ERR_LAUNCH;
   qrot_rows_kernel<<<dim3(unsigned((a.rows + kRows - 1) / kRows), a.D / kCols), kThreads, smem_of(a.D), stream>>>(a);
   return launched();
 }
 
 int launch_finish_rows(const FinishArgs& a, cudaStream_t stream) {
+  if (a.rows >= kTensorRows && a.ns <= 8 && !a.own_o) return launch_finish_rows_tc(a, stream);
   if (!ready()) return OSCAR_ERR_LAUNCH;
   finish_rows_kernel<<<dim3(unsigned((a.rows + kRows - 1) / kRows), a.D / kCols), kThreads, smem_of(a.D), stream>>>(a);
   return launched();

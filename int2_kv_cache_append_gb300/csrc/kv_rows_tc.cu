@@ -1,0 +1,530 @@
+// Products of many rows with a layer's rotation on the 5th-generation tensor
+// cores: kv_read, the query rotation and the merge + un-rotation of the row
+// attention for larger calls (kv_rows.cu has the float32 form).
+//
+//   out [128 rows x NC columns] = X [128 x D] B^T,  B [NC x D] = rows of R (or of R^T)
+//
+// A CTA keeps its NC columns of the matrix in shared memory as fp16 values,
+// split into two parts where the result is float32 or a query, and walks the
+// row tiles.  X is expanded to fp16 operands in units of 64 channels: cached
+// INT2 rows as s (c - 1) / 2 with the middles as a rank-one term (exact; see
+// expand_k), other rows scaled by a power of two per row, with a second set of
+// units for the rounding residues where the result is float32.  A bf16 result
+// takes one product, R and X rounded to fp16 (2^-12 each, against 2^-9 of the
+// output); a query from bf16 two; a float32 result two or three, 2^-22.
+//
+// Two groups of four warps expand alternate tiles, one warp issues the
+// products, four warps scale and store the result of the previous tile: per
+// tile, 512 (one product) to 1536 tensor cycles, the expansion and the stores
+// overlap.  Every wait is bounded, as in the attention kernels.
+#include <algorithm>
+
+#include "rows_tc.cuh"
+
+namespace oscar {
+namespace {
+
+enum { kQuery, kFinish, kRead };
+
+struct MmArgs {
+  QrotRowsArgs q;
+  FinishArgs f;
+  ReadArgs r;
+  int64_t tiles;
+  int rl, xl;   // the matrix's / the rows' low parts take part
+};
+
+constexpr int kExpandWarps = 8, kStoreWarps = 4;
+constexpr int kThreads = (kExpandWarps + kStoreWarps + 1) * 32;
+
+template <int DG>
+struct Plan {
+  static constexpr int D = 128 * DG;
+  static constexpr int NC = DG == 4 ? 64 : 128;             // columns of a CTA
+  static constexpr int PU = DG == 1 ? 3 : 2;                // units of an expanding group
+  static constexpr int kB = NC * D * 2;                     // one part of the matrix
+  static constexpr int oB = 0;
+  static constexpr int oX = 2 * kB;
+  static constexpr int oRank = oX + 2 * PU * kUnit;          // rows' (two), then the matrix's rank-one operand
+  static constexpr int oRow = oRank + 2 * kRank + NC * 32;   // factors of the rows [2][128]; sums of the matrix [NC][DG]
+  static constexpr int oBar = oRow + 2 * 128 * 4 + NC * DG * 4;
+  static constexpr int kBars = 4 * PU + 6 + 1;
+  static constexpr int kBytes = oBar + kBars * 8 + 16 + 1024;
+  static_assert(kBytes <= 232448, "shared memory");
+};
+
+// 32 bytes of a row, at once where the output is aligned to that
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8], bool aligned) {
+  if (!aligned) {
+    static_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    static_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    return;
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+template <int SRC, int DG>
+__global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_constant__ MmArgs a) {
+  using L = Plan<DG>;
+  constexpr int D = L::D, NC = L::NC, PU = L::PU;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c0 = blockIdx.y * NC, role = blockIdx.z;
+  const Geom& g = a.r.g;
+  const float* R = SRC == kQuery ? a.q.R_K : SRC == kFinish ? a.f.R_V : role ? a.r.R_V : a.r.R_K;
+  const bool hadamard = SRC == kQuery ? a.q.hadamard : SRC == kFinish ? a.f.hadamard : a.r.hadamard;
+  const bool plain = SRC == kFinish ? a.f.absorb_v : SRC == kRead ? role && a.r.absorb_v : false;  // no matrix
+  void* out = SRC == kQuery ? a.q.qrot : SRC == kFinish ? a.f.out : role ? a.r.v_out : a.r.k_out;
+  const bool out32 = SRC == kQuery || (SRC == kFinish ? a.f.out_fp32 : a.r.out_fp32);
+  int32_t* status = SRC == kQuery ? a.q.status : SRC == kFinish ? a.f.status : a.r.status;
+  const int64_t rows = SRC == kQuery ? a.q.rows : SRC == kFinish ? a.f.rows : int64_t(g.B) * a.r.n * g.Hkv;
+  if (!out) return;
+
+  float* factor = reinterpret_cast<float*>(sm + L::oRow);      // [2][128]
+  float* sums = factor + 256;                                  // [NC][DG]
+  const uint32_t bar = base + L::oBar;
+  auto x_full = [&](int p, int i) { return bar + 8u * (p * PU + i); };
+  auto x_empty = [&](int p, int i) { return bar + 8u * (2 * PU + p * PU + i); };
+  const uint32_t f_full = bar + 32u * PU, acc_full = f_full + 16, acc_empty = acc_full + 16, drained = acc_empty + 16;
+  uint32_t* words = reinterpret_cast<uint32_t*>(sm + L::oBar + L::kBars * 8);
+  uint32_t* tmem_slot = words;
+  volatile uint32_t* abort_flag = words + 1;
+
+  if (threadIdx.x == 0) {
+    for (int p = 0; p < 2; ++p) {
+      for (int i = 0; i < PU; ++i) mbar_init(x_full(p, i), 4), mbar_init(x_empty(p, i), 1);
+      mbar_init(f_full + 8 * p, 4);
+      mbar_init(acc_full + 8 * p, 1);
+      mbar_init(acc_empty + 8 * p, kStoreWarps);
+    }
+    mbar_init(drained, 1);
+    mbar_fence_init();
+    words[1] = 0;
+  }
+  if (warp == kExpandWarps + kStoreWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_u32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // B: a thread makes 16-byte chunks of 8 k of one column; sums of every column's groups for the rank-one term
+  for (int i = threadIdx.x; i < NC * DG; i += kThreads) sums[i] = 0.f;
+  __syncthreads();
+  for (int i = threadIdx.x; i < NC * (D / 8); i += kThreads) {
+    // consecutive threads: consecutive columns of R (query), or consecutive chunks of a row of R
+    const int n = SRC == kQuery ? i % NC : i / (D / 8), k0 = (SRC == kQuery ? i / NC : i % (D / 8)) * 8;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (plain) v[e] = c0 + n == k0 + e ? 1.f : 0.f;
+      else if (hadamard) v[e] = hadamard_at(c0 + n, k0 + e);
+      else v[e] = SRC == kQuery ? __ldg(R + int64_t(k0 + e) * D + c0 + n) : __ldg(R + int64_t(c0 + n) * D + k0 + e);
+    }
+    uint32_t hi[4], lo[4];
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float both = split_pair(v[2 * e], v[2 * e + 1], hi[e], lo[e]);
+      const float2 h = __half22float2(*reinterpret_cast<__half2*>(&hi[e]));
+      sum += a.rl ? both : h.x + h.y;
+    }
+    uint8_t* dst = sm + L::oB + (k0 >> 6) * (NC * 128) + n * 128 + ((((k0 >> 3) & 7) ^ (n & 7)) << 4);
+    *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if (a.rl) *reinterpret_cast<uint4*>(dst + L::kB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if (SRC == kRead) {
+      // the 16 chunks of a (column, group) lie in 16 neighbouring lanes: one fixed order of summation
+#pragma unroll
+      for (int x = 8; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      if ((lane & 15) == 0) sums[n * DG + (k0 >> 7)] = sum;
+    }
+  }
+  if (SRC == kRead) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < NC * 2; i += kThreads) {
+      uint2 q[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int gr = 2 * (i & 1) + e;
+        q[e] = gr < DG ? rank_query(sums[(i >> 1) * DG + gr]) : make_uint2(0, 0);
+      }
+      *reinterpret_cast<uint4*>(sm + L::oRank + 2 * kRank + rank_offset(i >> 1, 8 * (i & 1))) = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
+    }
+    for (int i = threadIdx.x; i < 2 * kRank / 16; i += kThreads)
+      *reinterpret_cast<uint4*>(sm + L::oRank + 16 * i) = make_uint4(0, 0, 0, 0);
+  }
+  fence_async();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto fail = [&]() {
+    *abort_flag = 1;
+    status_or(status, OSCAR_DEV_TIMEOUT);
+  };
+  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity, abort_flag); };
+  const int sets = a.xl ? 2 : 1;
+  const int mine = int((a.tiles - blockIdx.x + gridDim.x - 1) / gridDim.x);  // this CTA's tiles
+
+  if (warp < kExpandWarps) {
+    // ------------------------------ rows of X --------------------------------
+    const int p = warp >> 2, r = threadIdx.x & 127;
+    bool ok = true;
+    int n = 0;  // units written
+#pragma unroll 1
+    for (int j = p; ok && j < mine; j += 2) {
+      const int64_t row = (int64_t(blockIdx.x) + int64_t(j) * gridDim.x) * 128 + r;
+      // where the row comes from, and the factor that undoes its scaling
+      RowRef ref{nullptr, nullptr, nullptr};
+      const __nv_bfloat16* b16 = nullptr;
+      const float* f32 = nullptr;
+      float up = 0.f, down = 0.f, top = -INFINITY, inv = 0.f, own = 0.f;
+      if (SRC == kRead) {
+        if (row < rows) {
+          const uint32_t bt = uint32_t(row / g.Hkv);
+          const int h = int(row - int64_t(bt) * g.Hkv), b = int(bt / uint32_t(a.r.n));
+          int T = a.r.seq_lens[b];
+          if (T > g.cap) {
+            status_or(status, OSCAR_DEV_OVER_CAPACITY);
+            T = g.cap;
+          }
+          const int64_t pos = int64_t(a.r.start_pos[b]) + int(bt % uint32_t(a.r.n));
+          if (pos >= 0 && pos < T) ref = row_ref(g, a.r.layer_base, role, int64_t(b) * g.Hkv + h, T, int(pos));
+          b16 = ref.wide;
+        }
+      } else if (SRC == kQuery) {
+        if (row_live(row, rows, a.q.q_lens, a.q.n, a.q.Hq)) {
+          if (a.q.in_fp32) f32 = static_cast<const float*>(a.q.q) + row * D;
+          else b16 = static_cast<const __nv_bfloat16*>(a.q.q) + row * D;
+        }
+      } else if (row_live(row, rows, a.f.q_lens, a.f.n, a.f.Hq)) {
+        f32 = a.f.acc + row * a.f.ns * D;
+        const float2* ml = reinterpret_cast<const float2*>(a.f.ml) + row * a.f.ns;
+        float m = -INFINITY;
+        for (int s = 0; s < a.f.ns; ++s)
+          if (ml[s].y != 0.f) m = fmax_nan(m, ml[s].x);
+        float ol = -INFINITY;
+        if (a.f.own_lse) {
+          ol = a.f.own_lse[row] * 1.4426950408889634f;
+          m = fmax_nan(m, ol);
+        }
+        float sum = 0.f;
+        for (int s = 0; s < a.f.ns; ++s)
+          if (ml[s].y != 0.f) sum += exp2f(ml[s].x - m) * ml[s].y;
+        own = ol != -INFINITY ? exp2f(ol - m) : 0.f;
+        sum += own;
+        top = m;
+        inv = sum != 0.f ? 1.0f / sum : 0.f;
+        if (c0 == 0) {
+          if (sum == 0.f) status_or(status, OSCAR_DEV_EMPTY);
+          if (a.f.lse) a.f.lse[row] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+      // 16 channels from k on in float32 (query float32, merged partial results)
+      auto fetch = [&](int k, float (&x)[16]) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = 0.f;
+        if (SRC == kQuery) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(x + e) = __ldg(reinterpret_cast<const float4*>(f32 + k + e));
+        } else if (SRC == kFinish) {
+          const float2* ml = reinterpret_cast<const float2*>(a.f.ml) + row * a.f.ns;
+          for (int s = 0; s <= a.f.ns; ++s) {
+            float w;
+            const float* src;
+            if (s < a.f.ns) {
+              if (ml[s].y == 0.f) continue;  // nothing was written there
+              w = exp2f(ml[s].x - top) * inv;
+              src = f32 + int64_t(s) * D + k;
+            } else {
+              if (own == 0.f) break;
+              w = own * inv;
+              src = a.f.own_o + row * D + k;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 v = *reinterpret_cast<const float4*>(src + e);
+              x[e] = fmaf(w, v.x, x[e]);
+              x[e + 1] = fmaf(w, v.y, x[e + 1]);
+              x[e + 2] = fmaf(w, v.z, x[e + 2]);
+              x[e + 3] = fmaf(w, v.w, x[e + 3]);
+            }
+          }
+        }
+      };
+      bool finite = true;
+      if (b16 || f32) {
+        uint32_t m = 0;
+        if (b16) {
+          uint32_t w = 0;
+          const uint4* src = reinterpret_cast<const uint4*>(b16);
+#pragma unroll 8
+          for (int e = 0; e < D / 8; ++e) {
+            const uint4 v = __ldg(src + e);
+            w = absmax2(absmax2(absmax2(absmax2(w, v.x), v.y), v.z), v.w);
+          }
+          m = max(w & 0xFFFFu, w >> 16) << 16;
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < D; k += 16) {
+            float x[16];
+            fetch(k, x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(fabsf(x[e])));
+          }
+        }
+        finite = m < 0x7F800000u;
+        const int e = max(-104, min(127, int(m >> 23) - 126)) - 7;  // 2^-e times the row's largest value is just below 2^7
+        down = pow2i(-e);
+        up = pow2i(e);
+      }
+      if (SRC == kQuery) {
+        if (!finite) status_or(status, OSCAR_DEV_NONFINITE);
+        up *= a.q.qscale;
+      }
+      if (SRC == kRead && ref.codes) up = 2.0f, down = 0.5f;
+      const int use = j >> 1;  // the buffers' use by this group
+      if (use > 0) ok = ok && wait(acc_empty + 8 * p, (use & 1) ^ 1);
+      factor[p * 128 + r] = up;
+      __syncwarp();
+      mbar_arrive_if(f_full + 8 * p, lane == 0);
+#pragma unroll 1
+      for (int kb = 0; ok && kb < 2 * DG; ++kb) {
+        const int gr = kb >> 1, half = kb & 1;
+        uint32_t w[4];
+        float2 sz = make_float2(0.f, 0.f);
+        if (SRC == kRead && ref.codes) {
+          const uint4 q0 = __ldg(reinterpret_cast<const uint4*>(ref.codes) + 2 * gr), q1 = __ldg(reinterpret_cast<const uint4*>(ref.codes) + 2 * gr + 1);
+          sz = __half22float2(__ldg(ref.sz + gr));
+          if (role == 0) {  // word 2 c + half: pair c of every 16-byte chunk
+            w[0] = half ? q0.y : q0.x, w[1] = half ? q0.w : q0.z, w[2] = half ? q1.y : q1.x, w[3] = half ? q1.w : q1.z;
+          } else {          // words 2 m and 2 m + 1, codes 8 half ..: pair m
+            const uint32_t sel = half ? 0x7632u : 0x5410u;
+            w[0] = prmt(q0.x, q0.y, sel), w[1] = prmt(q0.z, q0.w, sel), w[2] = prmt(q1.x, q1.y, sel), w[3] = prmt(q1.z, q1.w, sel);
+          }
+        }
+#pragma unroll 1
+        for (int set = 0; set < sets; ++set, ++n) {
+          const int un = n % PU;
+          if (n >= PU) ok = ok && wait(x_empty(p, un), ((n / PU) & 1) ^ 1);
+          if (!ok) break;
+          uint8_t* dst = sm + L::oX + (p * PU + un) * kUnit + r * 128;
+          if (SRC == kRead && ref.codes) {
+            if (half == 0 && set == 0)
+              *reinterpret_cast<uint2*>(sm + L::oRank + p * kRank + rank_offset(r, 4 * gr)) =
+                  rank_key(fmaf(g.lm ? kLmMiddle : 1.0f, sz.x, sz.y) * 0.5f);
+            const uint32_t s1 = half2_of(sz.x * 0.5f, sz.x * 0.5f);
+            const float unit = sz.x * (0.5f / 150.0f);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t v[4], o[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t y = code_shift(w[c], q);
+                v[c] = less_one_even(y);
+                o[c] = less_one_odd(y);
+                if (!g.lm) {
+                  v[c] = hmul2(v[c], s1);
+                  o[c] = hmul2(o[c], s1);
+                } else {  // (level - middle) s / 2 in float32, split
+                  v[c] = lm_part(lm_value(v[c]), unit, set);
+                  o[c] = lm_part(lm_value(o[c]), unit, set);
+                }
+              }
+              if (set && !g.lm) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] = o[c] = 0u;
+              }
+              *reinterpret_cast<uint4*>(dst + (((2 * q) ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(dst + (((2 * q + 1) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          } else if (f32) {
+#pragma unroll 1
+            for (int q = 0; q < 8; q += 2) {
+              float x[16];
+              uint32_t hi[8], lo[8];
+              fetch(64 * kb + 8 * q, x);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) split_pair(x[2 * e] * down, x[2 * e + 1] * down, hi[e], lo[e]);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (set) hi[e] = lo[e];
+              *reinterpret_cast<uint4*>(dst + ((q ^ (r & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(dst + (((q + 1) ^ (r & 7)) << 4)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+            }
+          } else {
+            const uint4* src = b16 && !set ? reinterpret_cast<const uint4*>(b16 + 64 * kb) : nullptr;
+#pragma unroll 4
+            for (int q = 0; q < 8; ++q) {
+              const uint4 v = src ? __ldg(src + q) : make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(dst + ((q ^ (r & 7)) << 4)) =
+                  make_uint4(scaled_half2(v.x, down), scaled_half2(v.y, down), scaled_half2(v.z, down), scaled_half2(v.w, down));
+            }
+            if (SRC == kRead && half == 0 && set == 0)
+              *reinterpret_cast<uint2*>(sm + L::oRank + p * kRank + rank_offset(r, 4 * gr)) = make_uint2(0, 0);
+          }
+          fence_async();
+          __syncwarp();
+          mbar_arrive_if(x_full(p, un), lane == 0);
+        }
+      }
+    }
+    if (!ok && lane == 0) fail();
+  } else if (warp < kExpandWarps + kStoreWarps) {
+    // ----------------------------- scale and store ----------------------------
+    const int r = threadIdx.x & 127;
+    const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
+    const bool aligned = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int j = 0; ok && j < mine; ++j) {
+      const int p = j & 1;
+      const int64_t row = (int64_t(blockIdx.x) + int64_t(j) * gridDim.x) * 128 + r;
+      bool keep;  // the row is stored
+      if (SRC == kRead) {
+        keep = row < rows;
+        if (keep) {
+          const uint32_t bt = uint32_t(row / g.Hkv);
+          const int b = int(bt / uint32_t(a.r.n));
+          const int64_t pos = int64_t(a.r.start_pos[b]) + int(bt % uint32_t(a.r.n));
+          keep = pos >= 0 && pos < min(a.r.seq_lens[b], g.cap);
+        }
+      } else {
+        const int32_t* ql = SRC == kQuery ? a.q.q_lens : a.f.q_lens;
+        keep = row_live(row, rows, ql, SRC == kQuery ? a.q.n : a.f.n, SRC == kQuery ? a.q.Hq : a.f.Hq);
+      }
+      ok = wait(f_full + 8 * p, (j >> 1) & 1);
+      ok = ok && wait(acc_full + 8 * p, (j >> 1) & 1);
+      if (!ok) break;
+      fence_after();
+      const float up = factor[p * 128 + r];
+#pragma unroll 1
+      for (int c = 0; c < NC; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(tmem + lanes + p * 128 + c, v);
+        tmem_wait16(v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * up);
+        if (!keep) continue;
+        if (out32) {
+          float* dst = static_cast<float*>(out) + row * D + c0 + c;
+          const uint32_t lo[8] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+          const uint32_t hi[8] = {v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]};
+          store32(dst, lo, aligned);
+          store32(dst + 8, hi, aligned);
+        } else {
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            h[e] = pack_bf162(__float2bfloat16_rn(__uint_as_float(v[2 * e])), __float2bfloat16_rn(__uint_as_float(v[2 * e + 1])));
+          store32(static_cast<__nv_bfloat16*>(out) + row * D + c0 + c, h, aligned);
+        }
+      }
+      fence_before();
+      __syncwarp();
+      mbar_arrive_if(acc_empty + 8 * p, lane == 0);
+    }
+    if (!ok && lane == 0) fail();
+  } else {
+    // ------------------------------ MMA issuer --------------------------------
+    const uint32_t leader = elect_one();
+    constexpr uint32_t id = idesc_of(NC, false, false);
+    const uint32_t sX = base + L::oX, sB = base + L::oB, sRank = base + L::oRank;
+    int n[2] = {0, 0};
+    bool ok = true;
+#pragma unroll 1
+    for (int j = 0; ok && j < mine; ++j) {
+      const int p = j & 1;
+      if (j >= 2) ok = wait(acc_empty + 8 * p, ((j >> 1) & 1) ^ 1);
+      const uint32_t d = tmem + p * 128;
+      int used = p ? n[1] : n[0];
+#pragma unroll 1
+      for (int kb = 0; ok && kb < 2 * DG; ++kb) {
+        const uint64_t m = desc_of(sB + kb * (NC * 128), 16);
+#pragma unroll 1
+        for (int set = 0; ok && set < sets; ++set, ++used) {
+          const int un = used % PU;
+          ok = wait(x_full(p, un), (used / PU) & 1);
+          if (!ok) break;
+          fence_after();
+          const uint64_t x = desc_of(sX + (p * PU + un) * kUnit, 16);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_f16_ss(d, x + 2 * k, m + 2 * k, id, kb | set | k, leader);
+          if (a.rl && set == 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_f16_ss(d, x + 2 * k, m + (L::kB >> 4) + 2 * k, id, 1, leader);
+          }
+          if (SRC == kRead && kb == 2 * DG - 2 && set == 0)  // the middles of all groups are there
+            mma_f16_ss(d, rank_desc(sRank + p * kRank), rank_desc(sRank + 2 * kRank), id, 1, leader);
+          mma_commit(x_empty(p, un), leader);
+        }
+      }
+      if (ok) mma_commit(acc_full + 8 * p, leader);
+      if (p) n[1] = used;
+      else n[0] = used;
+    }
+    if (!ok && lane == 0) fail();
+    mma_commit(drained, leader);  // every product issued is complete before TMEM is freed
+    mbar_wait(drained, 0);
+    __syncwarp();
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == kExpandWarps + kStoreWarps) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem) : "memory");
+  }
+}
+
+template <int SRC, int DG>
+int launch(MmArgs& a, int64_t rows, int roles, cudaStream_t stream) {
+  static int sms[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return OSCAR_ERR_LAUNCH;
+  if (!sms[dev]) {
+    int n = 0;
+    if (cudaFuncSetAttribute(rows_mm_kernel<SRC, DG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<DG>::kBytes) !=
+            cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return OSCAR_ERR_LAUNCH;
+    sms[dev] = n;
+  }
+  a.tiles = (rows + 127) / 128;
+  const int chunks = DG * 128 / Plan<DG>::NC;
+  const int per = int(std::min<int64_t>(a.tiles, std::max(1, sms[dev] / (chunks * roles))));
+  rows_mm_kernel<SRC, DG><<<dim3(per, chunks, roles), kThreads, Plan<DG>::kBytes, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
+}
+
+template <int SRC>
+int launch_dim(MmArgs& a, int D, int64_t rows, int roles, cudaStream_t stream) {
+  return D == 128 ? launch<SRC, 1>(a, rows, roles, stream) : D == 256 ? launch<SRC, 2>(a, rows, roles, stream)
+                                                                      : launch<SRC, 4>(a, rows, roles, stream);
+}
+
+}  // namespace
+
+int launch_read_tc(const ReadArgs& r, cudaStream_t stream) {
+  MmArgs a{};
+  a.r = r;
+  a.rl = r.out_fp32;
+  a.xl = r.out_fp32 && r.g.lm;
+  return launch_dim<kRead>(a, r.g.D, int64_t(r.g.B) * r.n * r.g.Hkv, 2, stream);
+}
+int launch_qrot_rows_tc(const QrotRowsArgs& q, cudaStream_t stream) {
+  MmArgs a{};
+  a.q = q;
+  a.rl = 1;
+  a.xl = q.in_fp32;
+  return launch_dim<kQuery>(a, q.D, q.rows, 1, stream);
+}
+int launch_finish_rows_tc(const FinishArgs& f, cudaStream_t stream) {
+  MmArgs a{};
+  a.f = f;
+  a.rl = a.xl = f.out_fp32;
+  return launch_dim<kFinish>(a, f.D, f.rows, 1, stream);
+}
+
+}  // namespace oscar

@@ -23,6 +23,14 @@ __device__ __forceinline__ int row_q_len(const RowsArgs& a, int b) {
   return a.q_lens ? min(a.q_lens[b], a.n) : a.n;
 }
 
+// Row (b n + t) Hq + head of a query block is one of the sequence's tokens.
+__device__ __forceinline__ bool row_live(int64_t row, int64_t rows, const int32_t* q_lens, int n, int Hq) {
+  if (row >= rows) return false;
+  if (!q_lens) return true;
+  const int64_t bt = row / Hq;
+  return int(bt % n) < q_lens[bt / n];
+}
+
 // Where one cached row of a role lives: BF16 (a window, or K-only INT2's V
 // rows) or INT2 (codes and scale / zero pairs).
 struct RowRef {

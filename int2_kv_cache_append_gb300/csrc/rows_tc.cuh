@@ -235,6 +235,15 @@ __device__ __forceinline__ uint32_t lm_extra(uint32_t c1) {
   asm("min.f16x2 %0, %0, %1;" : "+r"(step) : "r"(0x3C003C00u));
   return hfma2(step, 0xBC00BC00u, c1);
 }
+// unit * value of an fp16 pair in float32: its fp16 rounding (part 0) or what that leaves (part 1)
+__device__ __forceinline__ uint32_t lm_part(uint32_t value, float unit, int part) {
+  const float2 x = __half22float2(*reinterpret_cast<__half2*>(&value));
+  const float a = x.x * unit, b = x.y * unit;
+  const uint32_t hi = half2_of(a, b);
+  if (!part) return hi;
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return half2_of(a - h.x, b - h.y);
+}
 // a bf16 pair times `scale`, as fp16
 __device__ __forceinline__ uint32_t scaled_half2(uint32_t x, float scale) {
   return half2_of(__uint_as_float(x << 16) * scale, __uint_as_float(x & 0xFFFF0000u) * scale);
