@@ -33,7 +33,7 @@ constexpr int kSoftWarps = 8;
 constexpr int kThreads = (kSoftWarps + 4 + 4 + 1) * 32;
 constexpr float kNone = -1e30f;         // M before the first visible position
 constexpr float kGrow = 12.f;           // log2 of the largest P
-constexpr int KU = 4, VU = 4, CB = 4, kStages = 4;
+constexpr int KU = 4, VU = 4, CB = 4, kStages = 4;  // two tiles of K and of V units
 constexpr int oK = 0;
 constexpr int oV = oK + KU * kUnit;
 constexpr int oRawK = oV + VU * kUnit;
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     *abort_flag = 1;
     status_or(a.status, OSCAR_DEV_TIMEOUT);
   };
-  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity, abort_flag); };
+  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity); };
 
   if (warp < kSoftWarps) {
     // ------------------------------- softmax ---------------------------------
@@ -354,67 +354,71 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     if (!ok && lane == 0) fail();
   } else {
     // ------------------------------ MMA issuer --------------------------------
+    // One warp issues every product; its instructions, not the tensor cores, would be the kernel's bound if it computed
+    // buffer indices and looked at the outcome of every wait.
     const uint32_t leader = elect_one();
     constexpr uint32_t id_qk = idesc_of(kTok, false, false), id_pv = idesc_of(D, false, true);
-    const uint32_t sK = base + oK, sV = base + oV, sRank = base + oRank;
-    int n = 0;  // K units used
-    auto product_qk = [&](int i) {
-      const uint32_t d = tmem + cS + (i & 1) * 128, q = tmem + cQ;
-#pragma unroll 1
-      for (int kb = 0; kb < 2; ++kb) {
-        if (!wait(k_full + 8 * (n % KU), (n / KU) & 1)) return false;
+    const uint32_t dK = desc_of(base + oK, 16), dV = desc_of(base + oV, kUnit / 2), dRank = rank_desc(base + oRank);
+    bool ok = true;
+    Ring<KU> kr;
+    Ring<VU> vr;
+    auto product_qk = [&](uint32_t odd) {
+      const uint32_t d = cS + odd * 128;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        ok = poll(k_full + 8 * kr.at, kr.phase) && ok;
         fence_after();
-        const uint64_t k = desc_of(sK + n % KU * kUnit, 16);
+        const uint32_t k = dK + kr.at * (kUnit >> 4);
 #pragma unroll
         for (int j = 0; j < 8; ++j)  // Q's high, then its low part; descriptors count 16 bytes
-          mma_f16_ts(d, q + 64 * (j >> 2) + 32 * kb + 8 * (j & 3), k + 2 * (j & 3), id_qk, kb | j, leader);
-        if (kb == 0) mma_f16_ss(d, rank_desc(sRank + 2 * kRank), rank_desc(sRank + (i & 1) * kRank), id_qk, 1, leader);
-        mma_commit(k_empty + 8 * (n % KU), leader);
-        ++n;
+          mma_f16_ts(d, cQ + 64 * (j >> 2) + 32 * half + 8 * (j & 3), k + 2 * (j & 3), id_qk, half | j, leader);
+        if (half == 0) mma_f16_ss<kDescRank>(d, dRank + (2 * kRank >> 4), dRank + odd * (kRank >> 4), id_qk, 1, leader);
+        mma_commit(k_empty + 8 * kr.at, leader);
+        kr.next();
         if (g.lm) {
-          if (!wait(k_full + 8 * (n % KU), (n / KU) & 1)) return false;
+          ok = poll(k_full + 8 * kr.at, kr.phase) && ok;
           fence_after();
-          const uint64_t x = desc_of(sK + n % KU * kUnit, 16);
+          const uint32_t x = dK + kr.at * (kUnit >> 4);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma_f16_ts(d, q + 32 * kb + 8 * j, x + 2 * j, id_qk, 1, leader);
-          mma_commit(k_empty + 8 * (n % KU), leader);
-          ++n;
+          for (int j = 0; j < 4; ++j) mma_f16_ts(d, cQ + 32 * half + 8 * j, x + 2 * j, id_qk, 1, leader);
+          mma_commit(k_empty + 8 * kr.at, leader);
+          kr.next();
         }
       }
-      mma_commit(s_full + 8 * (i & 1), leader);
-      return true;
+      mma_commit(s_full + 8 * odd, leader);
     };
-    auto product_pv = [&](int i) {
-      if (!wait(p_full, i & 1)) return false;
-#pragma unroll 1
-      for (int k = 0; k < 2; ++k) {
-        const int n = 2 * i + k, st = n % VU;
-        if (!wait(v_full + 8 * st, (n / VU) & 1)) return false;
-        fence_after();
-        const uint64_t v = desc_of(sV + st * kUnit, kUnit / 2);
-        const uint32_t p = tmem + cS + (i & 1) * 128 + 64 * k;  // 64 tokens of P in 32 columns
+    auto product_pv = [&](uint32_t odd, uint32_t acc) {
+      ok = poll(p_full, odd) && ok;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_f16_ts(tmem + cO, p + 8 * j, v + 128 * j, id_pv, i | k | j, leader);
-        mma_commit(v_empty + 8 * st, leader);
+      for (int k = 0; k < 2; ++k) {
+        ok = poll(v_full + 8 * vr.at, vr.phase) && ok;
+        fence_after();
+        const uint32_t v = dV + vr.at * (kUnit >> 4);
+        const uint32_t p = cS + odd * 128 + 64 * k;  // 64 tokens of P in 32 columns
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma_f16_ts(cO, p + 8 * j, v + 128 * j, id_pv, k | j ? 1 : acc, leader);
+        mma_commit(v_empty + 8 * vr.at, leader);
+        vr.next();
       }
       mma_commit(p_done, leader);
-      return true;
     };
-    bool ok = wait(q_full, 0);
-    if (ok) {
-      fence_after();
-      ok = product_qk(0);
+    ok = poll(q_full, 0) && tmem == 0;  // all of TMEM: column addresses are constants
+    fence_after();
+    if (__all_sync(0xffffffffu, ok)) {
+      product_qk(0);
+      if (nt > 1) product_qk(1);
     }
-    if (ok && nt > 1) ok = product_qk(1);
 #pragma unroll 1
-    for (int i = 0; ok && i < nt; ++i) {
-      ok = product_pv(i);
-      if (ok && i + 2 < nt) {
-        // the scores of tile i + 2 overwrite P
-        ok = wait(p_done, i & 1);
-        if (ok) fence_after(), ok = product_qk(i + 2);
+    for (int i = 0; i < nt; ++i) {
+      if (!__all_sync(0xffffffffu, ok)) break;
+      product_pv(i & 1, i > 0);
+      if (i + 2 < nt) {
+        ok = poll(p_done, i & 1) && ok;  // the scores of tile i + 2 overwrite P
+        fence_after();
+        product_qk(i & 1);
       }
     }
+    ok = __all_sync(0xffffffffu, ok);
     if (!ok && lane == 0) fail();
     mma_commit(drained, leader);  // every product issued is complete before TMEM is freed
     mbar_wait(drained, 0);

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     *abort_flag = 1;
     status_or(a.status, OSCAR_DEV_TIMEOUT);
   };
-  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity, abort_flag); };
+  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity); };
 
   if (warp < kSoftWarps) {
     // ------------------------------- softmax ---------------------------------
@@ -383,65 +383,74 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     if (!ok && lane == 0) fail();
   } else {
     // ------------------------------ MMA issuer --------------------------------
+    // One warp issues every product; its instructions, not the tensor cores, would be the kernel's bound if it computed
+    // buffer indices and looked at the outcome of every wait.
     const uint32_t leader = elect_one();
     constexpr uint32_t id_qk = idesc_of(N, false, false), id_pv = idesc_of(N, true, true);
-    const uint32_t sQ = base + L::oQ, sK = base + L::oK, sV = base + L::oV, sP = base + L::oP;
-    const uint32_t sRank = base + L::oRank;
-    int n = 0;  // K units used
-    auto product_qk = [&](int i) {
-      const int sb = i % L::SB;
-      if (i >= L::SB && !wait(s_empty(sb), ((i / L::SB) & 1) ^ 1)) return false;
-      const uint32_t d = tmem + L::cS + sb * N;
+    const uint32_t dQ = desc_of(base + L::oQ, 16), dK = desc_of(base + L::oK, 16), dV = desc_of(base + L::oV, kUnit / 2),
+                   dP = desc_of(base + L::oP, kTok * 128), dRank = rank_desc(base + L::oRank);
+    bool ok = true;
+    Ring<L::KU> kr;
+    Ring<L::VU> vr;
+    Ring<L::SB> sr;
+    Ring<L::PB> pr;
+    uint32_t odd = 0;  // the tile's rank-one operand
+    auto product_qk = [&](bool reuse) {
+      if (reuse) ok = poll(s_empty(sr.at), sr.phase ^ 1) && ok;
+      const uint32_t d = L::cS + sr.at * N;
 #pragma unroll 1
       for (int kb = 0; kb < 2 * DG; ++kb) {
-        if (!wait(k_full(n % L::KU), (n / L::KU) & 1)) return false;
+        ok = poll(k_full(kr.at), kr.phase) && ok;
         fence_after();
-        const uint64_t k = desc_of(sK + n % L::KU * kUnit, 16), q = desc_of(sQ + kb * (N * 128), 16);
+        const uint32_t k = dK + kr.at * (kUnit >> 4), q = dQ + kb * (N * 128 >> 4);
 #pragma unroll
         for (int j = 0; j < 8; ++j)  // Q's high, then its low part; descriptors count 16 bytes
-          mma_f16_ss(d, k + 2 * (j & 3), q + (j >> 2) * (L::kQ >> 4) + 2 * (j & 3), id_qk, kb | j, leader);
+          mma_f16_ss(d, k + 2 * (j & 3), q + (j >> 2) * (L::kQ >> 4) + 2 * (j & 3), id_qk, j ? 1 : kb, leader);
         if (kb == 2 * DG - 2)  // the middles of all groups are there
-          mma_f16_ss(d, rank_desc(sRank + (i & 1) * kRank), rank_desc(sRank + 2 * kRank), id_qk, 1, leader);
-        mma_commit(k_empty(n % L::KU), leader);
-        ++n;
+          mma_f16_ss<kDescRank>(d, dRank + odd * (kRank >> 4), dRank + (2 * kRank >> 4), id_qk, 1, leader);
+        mma_commit(k_empty(kr.at), leader);
+        kr.next();
         if (g.lm) {
-          if (!wait(k_full(n % L::KU), (n / L::KU) & 1)) return false;
+          ok = poll(k_full(kr.at), kr.phase) && ok;
           fence_after();
-          const uint64_t x = desc_of(sK + n % L::KU * kUnit, 16);
+          const uint32_t x = dK + kr.at * (kUnit >> 4);
 #pragma unroll
           for (int j = 0; j < 4; ++j) mma_f16_ss(d, x + 2 * j, q + 2 * j, id_qk, 1, leader);
-          mma_commit(k_empty(n % L::KU), leader);
-          ++n;
+          mma_commit(k_empty(kr.at), leader);
+          kr.next();
         }
       }
-      mma_commit(s_full(sb), leader);
-      return true;
+      mma_commit(s_full(sr.at), leader);
+      sr.next();
+      odd ^= 1;
     };
-    auto product_pv = [&](int i) {
-      const int pb = i % L::PB;
-      if (!wait(p_full(pb), (i / L::PB) & 1)) return false;
+    auto product_pv = [&](uint32_t acc) {
+      ok = poll(p_full(pr.at), pr.phase) && ok;
+      const uint32_t p = dP + pr.at * (L::kP >> 4);
+#pragma unroll 1
       for (int k = 0; k < 2 * DG; ++k) {  // group k / 2, token half k % 2
-        const int n = i * 2 * DG + k, st = n % L::VU;
-        if (!wait(v_full(st), (n / L::VU) & 1)) return false;
+        ok = poll(v_full(vr.at), vr.phase) && ok;
         fence_after();
+        const uint32_t v = dV + vr.at * (kUnit >> 4), half = k & 1;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          mma_f16_ss(tmem + L::cO + (k >> 1) * N, desc_of(sV + st * kUnit + 2048 * j, kUnit / 2),
-                     desc_of(sP + pb * L::kP + (k & 1) * 8192 + 2048 * j, kTok * 128), id_pv, i | (k & 1) | j, leader);
-        mma_commit(v_empty(st), leader);
+          mma_f16_ss(L::cO + (k >> 1) * N, v + 128 * j, p + half * 512 + 128 * j, id_pv, j ? 1 : acc | half, leader);
+        mma_commit(v_empty(vr.at), leader);
+        vr.next();
       }
-      mma_commit(p_empty(pb), leader);
-      return true;
+      mma_commit(p_empty(pr.at), leader);
+      pr.next();
     };
-    bool ok = wait(q_full, 0);
-    if (ok) {
-      fence_after();
-      ok = product_qk(0);
+    ok = poll(q_full, 0) && tmem == 0;  // all of TMEM: column addresses are constants
+    fence_after();
+    if (__all_sync(0xffffffffu, ok)) product_qk(false);
+#pragma unroll 1
+    for (int i = 0; i < nt; ++i) {
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (i + 1 < nt) product_qk(i + 1 >= L::SB);
+      product_pv(i > 0);
     }
-    for (int i = 0; ok && i < nt; ++i) {
-      if (i + 1 < nt) ok = product_qk(i + 1);
-      if (ok) ok = product_pv(i);
-    }
+    ok = __all_sync(0xffffffffu, ok);
     if (!ok && lane == 0) fail();
     mma_commit(drained, leader);  // every product issued is complete before TMEM is freed
     mbar_wait(drained, 0);

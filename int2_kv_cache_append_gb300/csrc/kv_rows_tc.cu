@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
     *abort_flag = 1;
     status_or(status, OSCAR_DEV_TIMEOUT);
   };
-  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity, abort_flag); };
+  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity); };
   const int sets = a.xl ? 2 : 1;
   const int mine = int((a.tiles - blockIdx.x + gridDim.x - 1) / gridDim.x);  // this CTA's tiles
 
@@ -442,14 +442,14 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
       int used = p ? n[1] : n[0];
 #pragma unroll 1
       for (int kb = 0; ok && kb < 2 * DG; ++kb) {
-        const uint64_t m = desc_of(sB + kb * (NC * 128), 16);
+        const uint32_t m = desc_of(sB + kb * (NC * 128), 16);
 #pragma unroll 1
         for (int set = 0; ok && set < sets; ++set, ++used) {
           const int un = used % PU;
           ok = wait(x_full(p, un), (used / PU) & 1);
           if (!ok) break;
           fence_after();
-          const uint64_t x = desc_of(sX + (p * PU + un) * kUnit, 16);
+          const uint32_t x = desc_of(sX + (p * PU + un) * kUnit, 16);
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma_f16_ss(d, x + 2 * k, m + 2 * k, id, kb | set | k, leader);
           if (a.rl && set == 0) {
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
             for (int k = 0; k < 4; ++k) mma_f16_ss(d, x + 2 * k, m + (L::kB >> 4) + 2 * k, id, 1, leader);
           }
           if (SRC == kRead && kb == 2 * DG - 2 && set == 0)  // the middles of all groups are there
-            mma_f16_ss(d, rank_desc(sRank + p * kRank), rank_desc(sRank + 2 * kRank), id, 1, leader);
+            mma_f16_ss<kDescRank>(d, rank_desc(sRank + p * kRank), rank_desc(sRank + 2 * kRank), id, 1, leader);
           mma_commit(x_empty(p, un), leader);
         }
       }

@@ -13,13 +13,12 @@ namespace oscar {
 constexpr int kTok = 128;    // positions per tile
 constexpr int kUnit = 16384; // bytes of a K unit (64 channels of 128 tokens) or V unit (64 tokens of 128 channels)
 
-// Shared-memory descriptors, 128-byte swizzle.  K-major: 8-row groups 1024 bytes
-// apart.  MN-major: 64-element blocks `lead` bytes apart, groups of eight k
-// 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_of(uint32_t saddr, uint32_t lead) {
-  return uint64_t((saddr >> 4) & 0x3FFF) | (uint64_t(lead >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
-         (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
+// Shared-memory descriptors: their low word is the address and the leading byte
+// offset, the high word constant.  128-byte swizzle: K-major, 8-row groups 1024
+// bytes apart (the leading offset is not used); MN-major: 64-element blocks
+// `lead` bytes apart, groups of eight k 1024 bytes apart.
+constexpr uint32_t kDescSwizzled = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_of(uint32_t saddr, uint32_t lead) { return ((saddr >> 4) & 0x3FFF) | ((lead >> 4) << 16); }
 // kind::f16, fp16 operands, float32 accumulator, M = 128.
 __device__ __forceinline__ constexpr uint32_t idesc_of(int n, bool a_mn_major, bool b_mn_major) {
   return (1u << 4) | (a_mn_major ? 1u << 15 : 0u) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) |
@@ -28,19 +27,21 @@ __device__ __forceinline__ constexpr uint32_t idesc_of(int n, bool a_mn_major, b
 // Issued by the lane with `leader` set; the whole warp comes along, so that
 // descriptors are computed in uniform registers (in one lane's branch every
 // product costs an extra eight instructions, more than its own 64 cycles).
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t leader) {
+template <uint32_t hi = kDescSwizzled>
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t leader) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
+      "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " mov.b64 x, {%1, %6};\n mov.b64 y, {%2, %6};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(leader), "n"(hi)
       : "memory");
 }
 // A from TMEM (fp16 pairs along k in a lane's columns)
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t leader) {
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t leader) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
+      "{\n .reg .pred p, q;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n mov.b64 y, {%2, %6};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(leader), "n"(kDescSwizzled)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t leader) {
@@ -159,13 +160,31 @@ __device__ __forceinline__ bool any128(int id, bool p) {
       : "memory");
   return r != 0;
 }
-// Bounded wait of a whole warp, given up at once when the CTA is aborting.  All
-// lanes poll (one instruction); the way out of the fast path is warp-uniform.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const volatile uint32_t* abort_flag) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  const bool ok = *abort_flag == 0 && mbar_wait(bar, parity);
-  return __all_sync(0xffffffffu, ok);
+// Bounded wait of a whole warp.  All lanes poll, four instructions a turn: the
+// waiting warps share the issue slots with the ones that work.  A turn takes 0.1
+// us or more, so the limit is of the order of a second.
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b32 n;\n mov.b32 n, 0;\n"
+      "again_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra done_%=;\n"
+      " add.u32 n, n, 1;\n setp.lt.u32 q, n, 10000000;\n @q bra again_%=;\n"
+      "done_%=:\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, poll(bar, parity)); }
+// Position in a ring of n buffers: index and phase, advanced without division.
+template <int n>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == n) at = 0, phase ^= 1;
+  }
+};
 // Arrival of the threads with `p`, without a branch.
 __device__ __forceinline__ void mbar_arrive_if(uint32_t bar, bool p) {
   asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar),
@@ -280,9 +299,8 @@ __device__ __forceinline__ int query_exponent(uint32_t max_bits) { return max(-1
 __device__ __forceinline__ uint32_t rank_offset(int row, int k) {
   return uint32_t(row >> 3) * 256 + uint32_t(k >> 3) * 128 + uint32_t(row & 7) * 16 + uint32_t(k & 7) * 2;
 }
-__device__ __forceinline__ uint64_t rank_desc(uint32_t saddr) {
-  return uint64_t((saddr >> 4) & 0x3FFF) | (uint64_t(128 >> 4) << 16) | (uint64_t(256 >> 4) << 32) | (uint64_t(1) << 46);
-}
+constexpr uint32_t kDescRank = (256 >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t rank_desc(uint32_t saddr) { return desc_of(saddr, 128); }
 // (hi, hi, lo, lo) of a row's sum and (hi, lo, hi, lo) of a key row's middle: their products' sum is sum * middle
 __device__ __forceinline__ uint2 rank_query(float x) {
   const uint32_t h = half2_of(x, x);
@@ -397,7 +415,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
   // tile i's is used with the first unit of its last group
   static_assert(2 * (DG + 1) >= KU, "two rank-one operands");
   const Geom& g = x.a->g;
-  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity, x.abort_flag); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity); };
   const int steps = x.nt * DG, per = g.lm ? 4 : 2;  // units of a step
   const uint8_t* role = x.a->layer_base + g.sink_bytes + g.ring_bytes;
   const int64_t row0 = int64_t(x.u) * g.ncap + (x.p0 + tok - g.S);  // INT2 row of the first tile's token
@@ -537,7 +555,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
 template <int DG, int VU, int CB, int kStages>
 __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
   const Geom& g = x.a->g;
-  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity, x.abort_flag); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity); };
   const int steps = x.nt * DG, cb = lane >> 4, sub = 16 * warp4 + (lane & 15);
   const uint8_t* role = x.a->layer_base + g.role_bytes + g.sink_bytes + g.ring_bytes;
   const int64_t row0 = int64_t(x.u) * g.ncap + (x.p0 + sub - g.S);
