@@ -378,7 +378,8 @@ int attn_extend(const oscar_kv_config* cfg, const void* cache, int32_t layer, co
  *              with neither sets OSCAR_DEV_EMPTY (zero output, lse = -inf).
  *   num_splits shares of the prefix; 0 = automatic.
  *   workspace  device, 256-byte aligned, attn_decode_prefix_workspace_query
- *              bytes; with less, the automatic counts are reduced to what fits.
+ *              bytes (enough for every num_splits); with less, the automatic
+ *              count is reduced to what fits.
  * Other arguments, rounding and errors as attn_decode and attn_extend.
  */
 int attn_decode_prefix_workspace_query(const oscar_kv_config* cfg, const oscar_kv_config* prefix_cfg, uint64_t* bytes);

@@ -150,6 +150,8 @@ int launch_qrot_rows_tc(const QrotRowsArgs& a, cudaStream_t stream);
 struct FinishArgs {
   const float* acc;         // as in RowsArgs
   const float* ml;
+  const float* acc2;        // partial results of another cache, ns2 a row, or NULL
+  const float* ml2;
   const float* own_o;       // [rows][D] and [rows]: one more, normalised partial result, or NULL
   const float* own_lse;
   const int32_t* own_status;
@@ -159,7 +161,7 @@ struct FinishArgs {
   float* lse;
   int32_t* status;
   int64_t rows;             // B * n * Hq
-  int n, Hq, D, ns;
+  int n, Hq, D, ns, ns2;
   int out_fp32, absorb_v, hadamard;
 };
 int launch_finish_rows(const FinishArgs& a, cudaStream_t stream);

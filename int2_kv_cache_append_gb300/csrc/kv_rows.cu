@@ -119,129 +119,199 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadArgs a) {
   }
 }
 
-// ------------------------------------------------------------ query rotation
-__global__ void __launch_bounds__(kThreads) qrot_rows_kernel(const QrotRowsArgs a) {
-  extern __shared__ float sm[];
-  const int D = a.D, xp = D + 4;
-  float* X = sm;
-  float* Ms = sm + kRows * xp;
-  const int64_t row0 = int64_t(blockIdx.x) * kRows;
-  if (a.zero_word && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.zero_word = 0;
-  bool finite = true;
-  for (int i = threadIdx.x; i < kRows * D; i += kThreads) {
-    const int r = i / D, c = i % D;
-    float v = 0.f;
-    if (row_live(row0 + r, a.rows, a.q_lens, a.n, a.Hq)) {
-      const int64_t at = (row0 + r) * D + c;
-      v = a.in_fp32 ? static_cast<const float*>(a.q)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at]);
-      finite &= isfinite(v) != 0;
+// ---------------------------------------------- query rotation and merge, few rows
+//
+// A CTA takes kFew rows and 128 output columns with four quarters of the sum
+// over the row's channels side by side: 512 threads, thread (column, quarter).
+// What counts at these sizes is the latency of reading the matrix, so every
+// thread has its D / 4 loads in flight at once and there are as many CTAs as
+// the rows give; the quarters meet in shared memory.
+constexpr int kFew = 8;
+constexpr int kFewThreads = 512;
+
+// y[r] of this thread's column c0 + (tid & 127) for rows 0 .. kFew - 1 of X, returned in the threads of quarter 0.
+template <int D, bool trans>
+__device__ __forceinline__ void few_product(const float (*X)[D], float* red, const float* __restrict__ R, int c0, bool hadamard,
+                                            float (&y)[kFew]) {
+  const int c = threadIdx.x & 127, kq = threadIdx.x >> 7;
+  constexpr int part = D / 4;
+#pragma unroll
+  for (int r = 0; r < kFew; ++r) y[r] = 0.f;
+#pragma unroll 1
+  for (int k0 = kq * part; k0 < (kq + 1) * part; k0 += 32) {
+    float m[32];
+    if (hadamard) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) m[k] = hadamard_at(k0 + k, c0 + c);
+    } else if (trans) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 4)
+        *reinterpret_cast<float4*>(m + k) = __ldg(reinterpret_cast<const float4*>(R + int64_t(c0 + c) * D + k0 + k));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) m[k] = __ldg(R + int64_t(k0 + k) * D + c0 + c);
     }
-    X[r * xp + c] = v;
+#pragma unroll
+    for (int r = 0; r < kFew; ++r)
+#pragma unroll
+      for (int k = 0; k < 32; k += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(&X[r][k0 + k]);
+        y[r] = fmaf(x.x, m[k], fmaf(x.y, m[k + 1], fmaf(x.z, m[k + 2], fmaf(x.w, m[k + 3], y[r]))));
+      }
   }
-  if (!finite) status_or(a.status, OSCAR_DEV_NONFINITE);
-  const int c0 = blockIdx.y * kCols, lane = threadIdx.x & 31, rw = threadIdx.x >> 5;
-  float y[4][4];
-  rows_product(X, xp, a.R_K, D, c0, false, a.hadamard != 0, Ms, y);
-  for (int i = 0; i < 4; ++i) {
-    const int64_t row = row0 + 4 * rw + i;
-    if (row >= a.rows) break;
-    for (int j = 0; j < 4; ++j) y[i][j] *= a.qscale;
-    store4(a.qrot, row * D + c0 + 4 * lane, 1, y[i]);
+#pragma unroll
+  for (int r = 0; r < kFew; ++r) red[(kq * kFew + r) * 128 + c] = y[r];
+  __syncthreads();
+  if (kq == 0) {
+#pragma unroll
+    for (int r = 0; r < kFew; ++r)
+      y[r] = (red[r * 128 + c] + red[(kFew + r) * 128 + c]) + (red[(2 * kFew + r) * 128 + c] + red[(3 * kFew + r) * 128 + c]);
   }
 }
 
-// --------------------------------------------------- merge, un-rotation, store
-__global__ void __launch_bounds__(kThreads) finish_rows_kernel(const FinishArgs a) {
-  extern __shared__ float sm[];
-  __shared__ float wgt[kRows][OSCAR_KV_MAX_SPLITS + 1];  // weight of each partial result over the sum
-  __shared__ int live[kRows];
-  const int D = a.D, xp = D + 4;
-  float* X = sm;
-  float* Ms = sm + kRows * xp;
-  const int64_t row0 = int64_t(blockIdx.x) * kRows;
+__device__ __forceinline__ void store1(void* out, int64_t at, int fp32, float v) {
+  if (fp32) static_cast<float*>(out)[at] = v;
+  else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFewThreads) qrot_few_kernel(const QrotRowsArgs a) {
+  __shared__ alignas(16) float X[kFew][D];
+  __shared__ float red[4 * kFew * 128];
+  const int64_t row0 = int64_t(blockIdx.x) * kFew;
+  if (a.zero_word && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.zero_word = 0;
+  bool finite = true;
+#pragma unroll
+  for (int i = 0; i < kFew * D / kFewThreads; ++i) {
+    const int at = threadIdx.x + i * kFewThreads, r = at / D, c = at % D;
+    float v = 0.f;
+    if (row_live(row0 + r, a.rows, a.q_lens, a.n, a.Hq)) {
+      const int64_t src = (row0 + r) * D + c;
+      v = a.in_fp32 ? static_cast<const float*>(a.q)[src] : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[src]);
+      finite &= isfinite(v) != 0;
+    }
+    X[r][c] = v;
+  }
+  if (!finite) status_or(a.status, OSCAR_DEV_NONFINITE);
+  __syncthreads();
+  float y[kFew];
+  few_product<D, false>(X, red, a.R_K, blockIdx.y * 128, a.hadamard != 0, y);
+  if (threadIdx.x < 128)
+#pragma unroll
+    for (int r = 0; r < kFew; ++r)
+      if (row0 + r < a.rows) a.qrot[(row0 + r) * D + blockIdx.y * 128 + threadIdx.x] = y[r] * a.qscale;
+}
+
+// Merge of the partial results, V un-rotation and store.
+template <int D>
+__global__ void __launch_bounds__(kFewThreads) finish_few_kernel(const FinishArgs a) {
+  __shared__ alignas(16) float X[kFew][D];
+  __shared__ float red[4 * kFew * 128];
+  __shared__ float wgt[kFew][2 * OSCAR_KV_MAX_SPLITS + 1];  // weight of each partial result over the sum
+  __shared__ int live[kFew];
+  const int64_t row0 = int64_t(blockIdx.x) * kFew;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, all = a.ns + a.ns2;
   if (a.own_status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
     // an empty cache of its own is not an error when the prefix has positions
     const int32_t st = *a.own_status & ~OSCAR_DEV_EMPTY;
     if (st) status_or(a.status, st);
   }
-  for (int r = threadIdx.x; r < kRows; r += kThreads) {
-    const int64_t row = row0 + r;
+  if (warp < kFew) {  // a warp per row, a lane per partial result
+    const int64_t row = row0 + warp;
     const bool ok = row_live(row, a.rows, a.q_lens, a.n, a.Hq);
-    live[r] = ok;
-    if (!ok) continue;
-    float m = -INFINITY;
-    for (int s = 0; s < a.ns; ++s)
-      if (a.ml[(row * a.ns + s) * 2 + 1] != 0.f) m = fmax_nan(m, a.ml[(row * a.ns + s) * 2]);
-    float ol = -INFINITY;
-    if (a.own_lse) {
-      ol = a.own_lse[row] * 1.4426950408889634f;
-      m = fmax_nan(m, ol);
-    }
-    float sum = 0.f;
-    for (int s = 0; s < a.ns; ++s) {
-      const float l = a.ml[(row * a.ns + s) * 2 + 1];
-      const float w = l != 0.f ? exp2f(a.ml[(row * a.ns + s) * 2] - m) : 0.f;
-      wgt[r][s] = w;
-      sum += w * l;
-    }
-    const float wo = ol != -INFINITY ? exp2f(ol - m) : 0.f;
-    sum += wo;
-    const float inv = sum != 0.f ? 1.0f / sum : 0.f;
-    // a partial result without weight is not read, also where another one made the sum NaN
-    for (int s = 0; s < a.ns; ++s) wgt[r][s] = wgt[r][s] != 0.f ? wgt[r][s] * inv : 0.f;
-    wgt[r][a.ns] = wo != 0.f ? wo * inv : 0.f;
-    if (blockIdx.y == 0) {
-      if (sum == 0.f) status_or(a.status, OSCAR_DEV_EMPTY);
-      if (a.lse) a.lse[row] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    if (lane == 0) live[warp] = ok;
+    if (ok) {
+      float m[4], l[4], top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int s = lane + 32 * j;
+        float2 p = make_float2(-INFINITY, 0.f);
+        if (s < a.ns) p = *reinterpret_cast<const float2*>(a.ml + (row * a.ns + s) * 2);
+        else if (s < all) p = *reinterpret_cast<const float2*>(a.ml2 + (row * a.ns2 + s - a.ns) * 2);
+        m[j] = p.x;
+        l[j] = p.y;
+        if (l[j] != 0.f) top = fmax_nan(top, m[j]);
+      }
+      const float ol = a.own_lse ? a.own_lse[row] * 1.4426950408889634f : -INFINITY;
+#pragma unroll
+      for (int x = 16; x; x >>= 1) top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, x));
+      top = fmax_nan(top, ol);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        m[j] = l[j] != 0.f ? exp2f(m[j] - top) : 0.f;
+        sum += m[j] * l[j];
+      }
+#pragma unroll
+      for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      const float wo = ol != -INFINITY ? exp2f(ol - top) : 0.f;
+      sum += wo;
+      const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+      // a partial result without weight is not read, also where another one made the sum NaN
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (lane + 32 * j < all) wgt[warp][lane + 32 * j] = m[j] != 0.f ? m[j] * inv : 0.f;
+      if (lane == 0) {
+        wgt[warp][all] = wo != 0.f ? wo * inv : 0.f;
+        if (blockIdx.y == 0) {
+          if (sum == 0.f) status_or(a.status, OSCAR_DEV_EMPTY);
+          if (a.lse) a.lse[row] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
+  for (int i = threadIdx.x; i < kFew * (D / 4); i += kFewThreads) {
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live[r]) {
       const int64_t row = row0 + r;
-      for (int s = 0; s <= a.ns; ++s) {
-        const float w = wgt[r][s];
-        if (w == 0.f) continue;
-        const float4 x = *reinterpret_cast<const float4*>(s < a.ns ? a.acc + (row * a.ns + s) * D + c : a.own_o + row * D + c);
+      auto add = [&](const float* src, float w) {
+        if (w == 0.f) return;
+        const float4 x = *reinterpret_cast<const float4*>(src + c);
         v.x = fmaf(w, x.x, v.x);
         v.y = fmaf(w, x.y, v.y);
         v.z = fmaf(w, x.z, v.z);
         v.w = fmaf(w, x.w, v.w);
-      }
+      };
+#pragma unroll 4
+      for (int s = 0; s < a.ns; ++s) add(a.acc + (row * a.ns + s) * D, wgt[r][s]);
+#pragma unroll 4
+      for (int s = 0; s < a.ns2; ++s) add(a.acc2 + (row * a.ns2 + s) * D, wgt[r][a.ns + s]);
+      if (a.own_o) add(a.own_o + row * D, wgt[r][all]);
     }
-    *reinterpret_cast<float4*>(X + r * xp + c) = v;
+    *reinterpret_cast<float4*>(&X[r][c]) = v;
   }
-  const int c0 = blockIdx.y * kCols, lane = threadIdx.x & 31, rw = threadIdx.x >> 5;
-  float y[4][4];
+  __syncthreads();
+  const int c0 = blockIdx.y * 128;
+  float y[kFew];
   if (a.absorb_v) {
-    __syncthreads();
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) y[i][j] = X[(4 * rw + i) * xp + c0 + 4 * lane + j];
+    if (threadIdx.x < 128)
+#pragma unroll
+      for (int r = 0; r < kFew; ++r) y[r] = X[r][c0 + threadIdx.x];
   } else {
-    rows_product(X, xp, a.R_V, D, c0, true, a.hadamard != 0, Ms, y);
+    few_product<D, true>(X, red, a.R_V, c0, a.hadamard != 0, y);
   }
-  for (int i = 0; i < 4; ++i)
-    if (live[4 * rw + i]) store4(a.out, (row0 + 4 * rw + i) * D + c0 + 4 * lane, a.out_fp32, y[i]);
+  if (threadIdx.x < 128)
+#pragma unroll
+    for (int r = 0; r < kFew; ++r)
+      if (live[r]) store1(a.out, (row0 + r) * D + c0 + threadIdx.x, a.out_fp32, y[r]);
 }
 
 // Rows from which the tensor-core kernels take over.
-constexpr int64_t kTensorRows = 1024;
+constexpr int64_t kTensorRows = 1024;       // kv_read
+constexpr int64_t kTensorRowsQuery = 4096;  // query rotation, merge
 
 size_t smem_of(int D) { return size_t(kRows * (D + 4) + kDeep * kPitch) * 4; }
 
-// Raises the dynamic shared memory limit of the three kernels, once per device.
+// Raises the dynamic shared memory limit of kv_read, once per device.
 bool ready() {
   static bool done[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
   if (done[dev]) return true;
   const int most = int(smem_of(512));
-  if (cudaFuncSetAttribute(kv_read_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-      cudaFuncSetAttribute(qrot_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-      cudaFuncSetAttribute(finish_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
-    return false;
+  if (cudaFuncSetAttribute(kv_read_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return false;
   done[dev] = true;
   return true;
 }
@@ -262,16 +332,20 @@ int launch_read(const ReadArgs& a, cudaStream_t stream) {
 }
 
 int launch_qrot_rows(const QrotRowsArgs& a, cudaStream_t stream) {
-  if (a.rows >= kTensorRows && !a.zero_word) return launch_qrot_rows_tc(a, stream);
-  if (!ready()) return OSCAR_ERR_LAUNCH;
-  qrot_rows_kernel<<<dim3(unsigned((a.rows + kRows - 1) / kRows), a.D / kCols), kThreads, smem_of(a.D), stream>>>(a);
+  if (a.rows >= kTensorRowsQuery) return launch_qrot_rows_tc(a, stream);
+  const dim3 grid(unsigned((a.rows + kFew - 1) / kFew), a.D / 128);
+  if (a.D == 128) qrot_few_kernel<128><<<grid, kFewThreads, 0, stream>>>(a);
+  else if (a.D == 256) qrot_few_kernel<256><<<grid, kFewThreads, 0, stream>>>(a);
+  else qrot_few_kernel<512><<<grid, kFewThreads, 0, stream>>>(a);
   return launched();
 }
 
 int launch_finish_rows(const FinishArgs& a, cudaStream_t stream) {
-  if (a.rows >= kTensorRows && a.ns <= 8 && !a.own_o) return launch_finish_rows_tc(a, stream);
-  if (!ready()) return OSCAR_ERR_LAUNCH;
-  finish_rows_kernel<<<dim3(unsigned((a.rows + kRows - 1) / kRows), a.D / kCols), kThreads, smem_of(a.D), stream>>>(a);
+  if (a.rows >= kTensorRowsQuery && a.ns <= 8 && a.ns2 <= 8) return launch_finish_rows_tc(a, stream);
+  const dim3 grid(unsigned((a.rows + kFew - 1) / kFew), a.D / 128);
+  if (a.D == 128) finish_few_kernel<128><<<grid, kFewThreads, 0, stream>>>(a);
+  else if (a.D == 256) finish_few_kernel<256><<<grid, kFewThreads, 0, stream>>>(a);
+  else finish_few_kernel<512><<<grid, kFewThreads, 0, stream>>>(a);
   return launched();
 }
 

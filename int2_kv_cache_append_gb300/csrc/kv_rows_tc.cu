@@ -95,6 +95,14 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
   uint32_t* tmem_slot = words;
   volatile uint32_t* abort_flag = words + 1;
 
+  if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) {
+    if (SRC == kQuery && a.q.zero_word) *a.q.zero_word = 0;
+    if (SRC == kFinish && a.f.own_status) {
+      // an empty cache of its own is not an error when the prefix has positions
+      const int32_t st = *a.f.own_status & ~OSCAR_DEV_EMPTY;
+      if (st) status_or(status, st);
+    }
+  }
   if (threadIdx.x == 0) {
     for (int p = 0; p < 2; ++p) {
       for (int i = 0; i < PU; ++i) mbar_init(x_full(p, i), 4), mbar_init(x_empty(p, i), 1);
@@ -202,9 +210,12 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
       } else if (row_live(row, rows, a.f.q_lens, a.f.n, a.f.Hq)) {
         f32 = a.f.acc + row * a.f.ns * D;
         const float2* ml = reinterpret_cast<const float2*>(a.f.ml) + row * a.f.ns;
+        const float2* ml2 = reinterpret_cast<const float2*>(a.f.ml2) + row * a.f.ns2;
         float m = -INFINITY;
         for (int s = 0; s < a.f.ns; ++s)
           if (ml[s].y != 0.f) m = fmax_nan(m, ml[s].x);
+        for (int s = 0; s < a.f.ns2; ++s)
+          if (ml2[s].y != 0.f) m = fmax_nan(m, ml2[s].x);
         float ol = -INFINITY;
         if (a.f.own_lse) {
           ol = a.f.own_lse[row] * 1.4426950408889634f;
@@ -213,6 +224,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
         float sum = 0.f;
         for (int s = 0; s < a.f.ns; ++s)
           if (ml[s].y != 0.f) sum += exp2f(ml[s].x - m) * ml[s].y;
+        for (int s = 0; s < a.f.ns2; ++s)
+          if (ml2[s].y != 0.f) sum += exp2f(ml2[s].x - m) * ml2[s].y;
         own = ol != -INFINITY ? exp2f(ol - m) : 0.f;
         sum += own;
         top = m;
@@ -231,13 +244,15 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
           for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(x + e) = __ldg(reinterpret_cast<const float4*>(f32 + k + e));
         } else if (SRC == kFinish) {
           const float2* ml = reinterpret_cast<const float2*>(a.f.ml) + row * a.f.ns;
-          for (int s = 0; s <= a.f.ns; ++s) {
+          const float2* ml2 = reinterpret_cast<const float2*>(a.f.ml2) + row * a.f.ns2;
+          for (int s = 0; s <= a.f.ns + a.f.ns2; ++s) {
             float w;
             const float* src;
-            if (s < a.f.ns) {
-              if (ml[s].y == 0.f) continue;  // nothing was written there
-              w = exp2f(ml[s].x - top) * inv;
-              src = f32 + int64_t(s) * D + k;
+            if (s < a.f.ns + a.f.ns2) {
+              const float2 p = s < a.f.ns ? ml[s] : ml2[s - a.f.ns];
+              if (p.y == 0.f) continue;  // nothing was written there
+              w = exp2f(p.x - top) * inv;
+              src = (s < a.f.ns ? f32 + int64_t(s) * D : a.f.acc2 + (row * a.f.ns2 + s - a.f.ns) * D) + k;
             } else {
               if (own == 0.f) break;
               w = own * inv;

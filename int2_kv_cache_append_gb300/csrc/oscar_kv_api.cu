@@ -1,4 +1,5 @@
 // C ABI: argument validation, cache layout arithmetic and kernel dispatch.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -272,8 +273,16 @@ int validate_prefix(const oscar_kv_config* cfg, const oscar_kv_config* pcfg) {
   return rows_supported(make_geom(pcfg), cfg->batch) ? OSCAR_OK : OSCAR_ERR_UNSUPPORTED;
 }
 
-// Workspace of attn_decode_prefix apart from the row attention's: the own
-// caches' outputs, lse and status word.
+// Longest own cache that attn_decode_prefix gives to the row attention; longer
+// ones go to attn_decode's kernels.
+constexpr int kOwnRows = 1024;
+
+// Workspace of attn_decode_prefix apart from the prefix's row attention: the own
+// caches' partial results, or attn_decode's outputs, lse and status word.
+uint64_t own_rows_workspace(const Geom& g, int ns) {
+  const uint64_t bq = uint64_t(g.B) * g.Hq;
+  return oscar::align256(bq * ns * g.D * 4) + oscar::align256(bq * ns * 8);
+}
 uint64_t own_workspace(const Geom& g) {
   const uint64_t bq = uint64_t(g.B) * g.Hq;
   return oscar::align256(bq * g.D * 4) + oscar::align256(bq * 4) + 256;
@@ -425,8 +434,9 @@ int attn_decode_prefix_workspace_query(const oscar_kv_config* cfg, const oscar_k
   if (v != OSCAR_OK) return v;
   if (!bytes) return OSCAR_ERR_INVALID;
   const Geom g = make_geom(cfg), pg = make_geom(prefix_cfg);
-  *bytes = rows_workspace(pg, int64_t(g.B) * g.Hq, splits_of(cfg, pg, int64_t(g.B) * g.G, pg.cap)) +
-           own_workspace(g) + oscar::decode_workspace_bytes(g, OSCAR_KV_MAX_SPLITS);
+  *bytes = rows_workspace(pg, int64_t(g.B) * g.Hq, OSCAR_KV_MAX_SPLITS) +
+           std::max(own_rows_workspace(g, splits_of(cfg, g, g.G, std::min(g.cap, kOwnRows))),
+                    g.cap > kOwnRows ? own_workspace(g) + oscar::decode_workspace_bytes(g, OSCAR_KV_MAX_SPLITS) : 0);
   return OSCAR_OK;
 }
 
@@ -437,19 +447,26 @@ int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const osca
                        uint64_t workspace_bytes, int32_t* dev_status, void* stream) {
   int v = validate_prefix(cfg, prefix_cfg);
   if (v != OSCAR_OK) return v;
-  if (cfg->flags & OSCAR_FLAG_HADAMARD) R_K = R_V = nullptr;
-  if (!prefix_cache || !prefix_len || !workspace || !out) return OSCAR_ERR_INVALID;
-  if (layer < 0 || layer >= prefix_cfg->num_layers || num_splits < 0 || num_splits > OSCAR_KV_MAX_SPLITS ||
-      prefix_len_hint < 0)
+  const bool had = (cfg->flags & OSCAR_FLAG_HADAMARD) != 0;
+  if (had) R_K = R_V = nullptr;
+  if (!cache || !q || !seq_lens || !prefix_cache || !prefix_len || (!had && (!R_K || !R_V)) || !workspace || !out)
     return OSCAR_ERR_INVALID;
-  if (!aligned(prefix_cache, 256) || !aligned(workspace, 256) || !aligned(out, 16)) return OSCAR_ERR_INVALID;
-  if (prefix_len_hint > prefix_cfg->capacity) return OSCAR_ERR_CAPACITY;
+  if (layer < 0 || layer >= cfg->num_layers || layer >= prefix_cfg->num_layers || num_splits < 0 ||
+      num_splits > OSCAR_KV_MAX_SPLITS || prefix_len_hint < 0 || seq_len_hint < 0)
+    return OSCAR_ERR_INVALID;
+  if (!aligned(cache, 256) || !aligned(prefix_cache, 256) || !aligned(workspace, 256) || !aligned(R_K, 16) ||
+      !aligned(R_V, 16) || !aligned(q, 16) || !aligned(out, 16))
+    return OSCAR_ERR_INVALID;
+  if (prefix_len_hint > prefix_cfg->capacity || seq_len_hint > cfg->capacity) return OSCAR_ERR_CAPACITY;
   const Geom g = make_geom(cfg), pg = make_geom(prefix_cfg);
   const int64_t rows = int64_t(g.B) * g.Hq;
   const int hint = prefix_len_hint > 0 ? prefix_len_hint : prefix_cfg->capacity;
+  const int own_hint = seq_len_hint > 0 ? seq_len_hint : cfg->capacity;
   const int want = num_splits > 0 ? num_splits : splits_of(cfg, pg, int64_t(g.B) * g.G, hint);
   // the own caches' part has to fit with one split at least; what is left goes to the prefix
-  const uint64_t own = own_workspace(g) + oscar::decode_workspace_bytes(g, 1);
+  const bool own_by_rows = own_hint <= kOwnRows;
+  const int want2 = own_by_rows ? splits_of(cfg, g, g.G, own_hint) : 0;
+  const uint64_t own = own_by_rows ? own_rows_workspace(g, want2) : own_workspace(g) + oscar::decode_workspace_bytes(g, 1);
   const int ns =
       workspace_bytes < own ? 0 : fit_splits(pg, rows, want, num_splits > 0, workspace_bytes - own);
   if (ns == 0) return OSCAR_ERR_WORKSPACE;
@@ -458,6 +475,25 @@ int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const osca
   // one query token per sequence: the batch is the block of query rows of the one prefix
   plan_rows(cfg, pg, prefix_cache, layer, q, g.B, prefix_len, nullptr, R_K, R_V, sm_scale, ns, out, lse, dev_status, &ws,
             &p);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (own_by_rows) {
+    oscar::RowsArgs own_at = p.at;
+    own_at.g = g;
+    own_at.layer_base = static_cast<const uint8_t*>(cache) + uint64_t(layer) * g.layer_bytes;
+    own_at.seq_lens = seq_lens;
+    own_at.n = 1;
+    own_at.ns = want2;
+    own_at.acc = take<float>(&ws, uint64_t(rows) * want2 * g.D * 4);
+    own_at.ml = take<float>(&ws, uint64_t(rows) * want2 * 8);
+    p.fin.acc2 = own_at.acc;
+    p.fin.ml2 = own_at.ml;
+    p.fin.ns2 = want2;
+    int rc = oscar::launch_qrot_rows(p.q, st);
+    if (rc == OSCAR_OK) rc = launch_rows(cfg, p.at, st);
+    if (rc == OSCAR_OK) rc = launch_rows(cfg, own_at, st);
+    if (rc == OSCAR_OK) rc = oscar::launch_finish_rows(p.fin, st);
+    return rc;
+  }
   float* own_o = take<float>(&ws, uint64_t(rows) * g.D * 4);
   float* own_lse = take<float>(&ws, uint64_t(rows) * 4);
   int32_t* own_status = take<int32_t>(&ws, 256);
@@ -465,14 +501,13 @@ int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const osca
   p.fin.own_o = own_o;
   p.fin.own_lse = own_lse;
   p.fin.own_status = own_status;
-  // the own caches through attn_decode's kernels, in the rotated basis and float32
+  // long own caches through attn_decode's kernels, in the rotated basis and float32
   oscar_kv_config dcfg = *cfg;
   dcfg.flags |= OSCAR_FLAG_ABSORB_V | OSCAR_FLAG_OUT_FP32;
   oscar::DecodeArgs d;
   v = prep_decode(&dcfg, cache, layer, q, seq_lens, seq_len_hint, R_K, R_V, sm_scale, 0, own_o, own_lse, ws,
                   workspace_bytes - uint64_t(ws - static_cast<uint8_t*>(workspace)), own_status, &d);
   if (v != OSCAR_OK) return v;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int rc = oscar::launch_qrot_rows(p.q, st);
   if (rc == OSCAR_OK) rc = launch_rows(cfg, p.at, st);
   if (rc == OSCAR_OK) rc = oscar::launch_decode(d, st);

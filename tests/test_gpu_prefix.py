@@ -49,6 +49,11 @@ def refill(c, lens, RK, RV, seed):
     (256, 3, 8, 4, (4, 8), (4, 40), [30, 11, 140], 260, K.FLAG_ABSORB_V, 0),
     (512, 2, 8, 2, (4, 8), (4, 8), [30, 21], 140, 0, 0),
     (512, 2, 8, 1, (4, 8), (4, 8), [30, 21], 200, K.FLAG_LLOYD_MAX, 4),
+    # own caches of more than 1024 positions go through attn_decode's kernels
+    (128, 3, 8, 2, (4, 64), (4, 8), [1500, 20, 0], 150, 0, 0),
+    (128, 2, 16, 2, (4, 64), (4, 8), [1100, 1030], 0, K.FLAG_HADAMARD | K.FLAG_V_BF16, 0),
+    (256, 2, 4, 2, (4, 64), (4, 8), [1100, 7], 90, K.FLAG_LLOYD_MAX, 0),
+    (128, 600, 16, 2, (0, 4), (4, 8), [2] * 600, 40, 0, 0),                # rows of query beyond 4096
 ], ids=lambda x: "-".join(map(str, x[:4])) + f"-{x[7]}-{x[8]}-{x[9]}")
 def test_prefix(case, fp32):
     D, B, Hq, Hkv, own, pre, lens, plen, flags, splits = case
