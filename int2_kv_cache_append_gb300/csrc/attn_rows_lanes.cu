@@ -96,8 +96,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
   const int vis = max(0, a.causal ? min(T, T - ql + t_last + 1) : T);
   const int see_all = a.causal ? T - ql + t_first : T - 1;  // every row sees the positions up to this one
   const int blocks = (vis + kTok - 1) / kTok;
-  const int p0 = int(int64_t(blocks) * s / a.ns) * kTok;
-  const int p1 = min(vis, int(int64_t(blocks) * (s + 1) / a.ns) * kTok);
+  const int p0 = share_start(g, T, blocks, s, a.ns) * kTok;
+  const int p1 = min(vis, share_start(g, T, blocks, s + 1, a.ns) * kTok);
   const int nt = (p1 - p0 + kTok - 1) / kTok;
 
   int* outr = reinterpret_cast<int*>(sm + oRow);            // a row's index among all query rows, -1 = none
@@ -349,8 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
   } else if (warp < kSoftWarps + 8) {
     Share x{&a, u, T, p0, p1, nt, sm, base, abort_flag, scale_f, f_full, k_full, k_empty, v_full, v_empty, c_full, c_empty,
             oK, oV, oRawK, oRawV, oConst, oRank, oRow + 5 * N * 4};
-    const bool ok = warp < kSoftWarps + 4 ? expand_k<1, KU, CB, kStages>(x, threadIdx.x - kSoftWarps * 32, lane)
-                                          : expand_v<1, VU, CB, kStages>(x, warp & 3, lane);
+    const bool ok = warp < kSoftWarps + 4 ? expand_k<1, KU, CB, kStages, 4>(x, threadIdx.x - kSoftWarps * 32, lane)
+                                          : expand_v<1, VU, CB, kStages, 4>(x, warp & 3, lane);
     if (!ok && lane == 0) fail();
   } else {
     // ------------------------------ MMA issuer --------------------------------

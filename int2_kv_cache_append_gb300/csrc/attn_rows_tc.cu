@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
   const int vis = max(0, a.causal ? min(T, T - ql + t_last + 1) : T);
   const int see_all = a.causal ? T - ql + t_first : T - 1;  // every row sees the positions up to this one
   const int blocks = (vis + kTok - 1) / kTok;
-  const int p0 = int(int64_t(blocks) * s / a.ns) * kTok;
-  const int p1 = min(vis, int(int64_t(blocks) * (s + 1) / a.ns) * kTok);
+  const int p0 = share_start(g, T, blocks, s, a.ns) * kTok;
+  const int p1 = min(vis, share_start(g, T, blocks, s + 1, a.ns) * kTok);
   const int nt = (p1 - p0 + kTok - 1) / kTok;
 
   float* negM = reinterpret_cast<float*>(sm + L::oRow);
@@ -378,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     Share x{&a, u, T, p0, p1, nt, sm, base, abort_flag, scale_f, f_full, k_full(0), k_empty(0), v_full(0), v_empty(0),
             c_full(0), c_empty(0), L::oK, L::oV, L::oRawK, L::oRawV, L::oConst, L::oRank,
             L::oRow + L::kRow - 64};
-    const bool ok = warp < kSoftWarps + 4 ? expand_k<DG, L::KU, L::CB, L::kStages>(x, threadIdx.x - kSoftWarps * 32, lane)
-                                          : expand_v<DG, L::VU, L::CB, L::kStages>(x, warp & 3, lane);
+    const bool ok = warp < kSoftWarps + 4 ? expand_k<DG, L::KU, L::CB, L::kStages, 8>(x, threadIdx.x - kSoftWarps * 32, lane)
+                                          : expand_v<DG, L::VU, L::CB, L::kStages, 8>(x, warp & 3, lane);
     if (!ok && lane == 0) fail();
   } else {
     // ------------------------------ MMA issuer --------------------------------

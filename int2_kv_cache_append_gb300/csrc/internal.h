@@ -148,8 +148,8 @@ int launch_qrot_rows_tc(const QrotRowsArgs& a, cudaStream_t stream);
 
 // Merge of the splits' partial results, V un-rotation and store (kv_rows.cu).
 struct FinishArgs {
-  const float* acc;         // as in RowsArgs
-  const float* ml;
+  float* acc;               // as in RowsArgs; a row's first partial result is scratch once it has been merged
+  float* ml;
   const float* acc2;        // partial results of another cache, ns2 a row, or NULL
   const float* ml2;
   const float* own_o;       // [rows][D] and [rows]: one more, normalised partial result, or NULL

@@ -31,24 +31,26 @@ struct MmArgs {
   FinishArgs f;
   ReadArgs r;
   int64_t tiles;
-  int rl, xl;   // the matrix's / the rows' low parts take part
+  int xl;  // the rows' low parts take part
+  FastDiv div_hkv, div_n;  // of kv_read
 };
 
 constexpr int kExpandWarps = 8, kStoreWarps = 4;
 constexpr int kThreads = (kExpandWarps + kStoreWarps + 1) * 32;
 
-template <int DG>
+template <int DG, bool RL>  // RL: the matrix's low part takes part
 struct Plan {
   static constexpr int D = 128 * DG;
-  static constexpr int NC = DG == 4 ? 64 : 128;             // columns of a CTA
+  static constexpr int NC = DG == 1 ? 128 : (RL ? 256 : 512) / DG;  // columns of a CTA
   static constexpr int PU = DG == 1 ? 3 : 2;                // units of an expanding group
+  static constexpr int kAcc = DG == 4 ? 4 : 2;               // accumulators
   static constexpr int kB = NC * D * 2;                     // one part of the matrix
   static constexpr int oB = 0;
-  static constexpr int oX = 2 * kB;
+  static constexpr int oX = (RL ? 2 : 1) * kB;
   static constexpr int oRank = oX + 2 * PU * kUnit;          // rows' (two), then the matrix's rank-one operand
-  static constexpr int oRow = oRank + 2 * kRank + NC * 32;   // factors of the rows [2][128]; sums of the matrix [NC][DG]
-  static constexpr int oBar = oRow + 2 * 128 * 4 + NC * DG * 4;
-  static constexpr int kBars = 4 * PU + 6 + 1;
+  static constexpr int oRow = oRank + 2 * kRank + NC * 32;   // factors of the rows [kAcc][128]; sums of the matrix [NC][DG]
+  static constexpr int oBar = oRow + kAcc * 128 * 4 + NC * DG * 4;
+  static constexpr int kBars = 4 * PU + 3 * kAcc + 1;
   static constexpr int kBytes = oBar + kBars * 8 + 16 + 1024;
   static_assert(kBytes <= 232448, "shared memory");
 };
@@ -65,10 +67,10 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8], bool 
                : "memory");
 }
 
-template <int SRC, int DG>
+template <int SRC, int DG, bool RL>
 __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_constant__ MmArgs a) {
-  using L = Plan<DG>;
-  constexpr int D = L::D, NC = L::NC, PU = L::PU;
+  using L = Plan<DG, RL>;
+  constexpr int D = L::D, NC = L::NC, PU = L::PU, kAcc = L::kAcc, kCols = kAcc * NC;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -85,27 +87,23 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
   const int64_t rows = SRC == kQuery ? a.q.rows : SRC == kFinish ? a.f.rows : int64_t(g.B) * a.r.n * g.Hkv;
   if (!out) return;
 
-  float* factor = reinterpret_cast<float*>(sm + L::oRow);      // [2][128]
-  float* sums = factor + 256;                                  // [NC][DG]
+  float* factor = reinterpret_cast<float*>(sm + L::oRow);      // [kAcc][128]
+  float* sums = factor + kAcc * 128;                                  // [NC][DG]
   const uint32_t bar = base + L::oBar;
   auto x_full = [&](int p, int i) { return bar + 8u * (p * PU + i); };
   auto x_empty = [&](int p, int i) { return bar + 8u * (2 * PU + p * PU + i); };
-  const uint32_t f_full = bar + 32u * PU, acc_full = f_full + 16, acc_empty = acc_full + 16, drained = acc_empty + 16;
+  const uint32_t f_full = bar + 32u * PU, acc_full = f_full + 8 * kAcc, acc_empty = acc_full + 8 * kAcc, drained = acc_empty + 8 * kAcc;
   uint32_t* words = reinterpret_cast<uint32_t*>(sm + L::oBar + L::kBars * 8);
   uint32_t* tmem_slot = words;
   volatile uint32_t* abort_flag = words + 1;
 
   if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) {
     if (SRC == kQuery && a.q.zero_word) *a.q.zero_word = 0;
-    if (SRC == kFinish && a.f.own_status) {
-      // an empty cache of its own is not an error when the prefix has positions
-      const int32_t st = *a.f.own_status & ~OSCAR_DEV_EMPTY;
-      if (st) status_or(status, st);
-    }
   }
   if (threadIdx.x == 0) {
-    for (int p = 0; p < 2; ++p) {
+    for (int p = 0; p < 2; ++p)
       for (int i = 0; i < PU; ++i) mbar_init(x_full(p, i), 4), mbar_init(x_empty(p, i), 1);
+    for (int p = 0; p < kAcc; ++p) {
       mbar_init(f_full + 8 * p, 4);
       mbar_init(acc_full + 8 * p, 1);
       mbar_init(acc_empty + 8 * p, kStoreWarps);
@@ -115,7 +113,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
     words[1] = 0;
   }
   if (warp == kExpandWarps + kStoreWarps) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_u32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "n"(kCols)
+                 : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   // B: a thread makes 16-byte chunks of 8 k of one column; sums of every column's groups for the rank-one term
@@ -137,11 +136,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
     for (int e = 0; e < 4; ++e) {
       const float both = split_pair(v[2 * e], v[2 * e + 1], hi[e], lo[e]);
       const float2 h = __half22float2(*reinterpret_cast<__half2*>(&hi[e]));
-      sum += a.rl ? both : h.x + h.y;
+      sum += RL ? both : h.x + h.y;
     }
     uint8_t* dst = sm + L::oB + (k0 >> 6) * (NC * 128) + n * 128 + ((((k0 >> 3) & 7) ^ (n & 7)) << 4);
     *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    if (a.rl) *reinterpret_cast<uint4*>(dst + L::kB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if (RL) *reinterpret_cast<uint4*>(dst + L::kB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     if (SRC == kRead) {
       // the 16 chunks of a (column, group) lie in 16 neighbouring lanes: one fixed order of summation
 #pragma unroll
@@ -181,93 +180,62 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
     const int p = warp >> 2, r = threadIdx.x & 127;
     bool ok = true;
     int n = 0;  // units written
+    auto cached = [&](int64_t row) {  // of kv_read
+      RowRef ref{nullptr, nullptr, nullptr};
+      if (row >= rows) return ref;
+      const uint32_t bt = fastdiv(uint32_t(row), a.div_hkv), b = fastdiv(bt, a.div_n);
+      const int h = int(uint32_t(row) - bt * uint32_t(g.Hkv));
+      int T = a.r.seq_lens[b];
+      if (T > g.cap) {
+        status_or(status, OSCAR_DEV_OVER_CAPACITY);
+        T = g.cap;
+      }
+      const int64_t pos = int64_t(a.r.start_pos[b]) + int(bt - b * uint32_t(a.r.n));
+      if (pos >= 0 && pos < T) ref = row_ref(g, a.r.layer_base, role, int64_t(b) * g.Hkv + h, T, int(pos));
+      return ref;
+    };
+    // INT2 codes and the scale / zero pair, a group ahead
+    RowRef ref{nullptr, nullptr, nullptr}, next{nullptr, nullptr, nullptr};
+    uint4 q0, q1, n0 = make_uint4(0, 0, 0, 0), n1 = n0;
+    __half2 pair = __half2(), npair = __half2();
+    auto fetch_codes = [&](const RowRef& from, int gr) {
+      if (!from.codes) return;
+      n0 = __ldg(reinterpret_cast<const uint4*>(from.codes) + 2 * gr);
+      n1 = __ldg(reinterpret_cast<const uint4*>(from.codes) + 2 * gr + 1);
+      npair = __ldg(from.sz + gr);
+    };
+    if (SRC == kRead && p < mine) {
+      next = cached((int64_t(blockIdx.x) + int64_t(p) * gridDim.x) * 128 + r);
+      fetch_codes(next, 0);
+    }
 #pragma unroll 1
     for (int j = p; ok && j < mine; j += 2) {
       const int64_t row = (int64_t(blockIdx.x) + int64_t(j) * gridDim.x) * 128 + r;
       // where the row comes from, and the factor that undoes its scaling
-      RowRef ref{nullptr, nullptr, nullptr};
       const __nv_bfloat16* b16 = nullptr;
       const float* f32 = nullptr;
-      float up = 0.f, down = 0.f, top = -INFINITY, inv = 0.f, own = 0.f;
+      const __half* merged = nullptr;  // scaled already; its residues D further on
+      float up = 0.f, down = 0.f;
       if (SRC == kRead) {
-        if (row < rows) {
-          const uint32_t bt = uint32_t(row / g.Hkv);
-          const int h = int(row - int64_t(bt) * g.Hkv), b = int(bt / uint32_t(a.r.n));
-          int T = a.r.seq_lens[b];
-          if (T > g.cap) {
-            status_or(status, OSCAR_DEV_OVER_CAPACITY);
-            T = g.cap;
-          }
-          const int64_t pos = int64_t(a.r.start_pos[b]) + int(bt % uint32_t(a.r.n));
-          if (pos >= 0 && pos < T) ref = row_ref(g, a.r.layer_base, role, int64_t(b) * g.Hkv + h, T, int(pos));
-          b16 = ref.wide;
-        }
+        ref = next;
+        b16 = ref.wide;
+        next = j + 2 < mine ? cached(row + 2 * int64_t(gridDim.x) * 128) : RowRef{nullptr, nullptr, nullptr};
+        if (next.wide) prefetch_row<DG>(next.wide);
       } else if (SRC == kQuery) {
         if (row_live(row, rows, a.q.q_lens, a.q.n, a.q.Hq)) {
           if (a.q.in_fp32) f32 = static_cast<const float*>(a.q.q) + row * D;
           else b16 = static_cast<const __nv_bfloat16*>(a.q.q) + row * D;
         }
       } else if (row_live(row, rows, a.f.q_lens, a.f.n, a.f.Hq)) {
-        f32 = a.f.acc + row * a.f.ns * D;
-        const float2* ml = reinterpret_cast<const float2*>(a.f.ml) + row * a.f.ns;
-        const float2* ml2 = reinterpret_cast<const float2*>(a.f.ml2) + row * a.f.ns2;
-        float m = -INFINITY;
-        for (int s = 0; s < a.f.ns; ++s)
-          if (ml[s].y != 0.f) m = fmax_nan(m, ml[s].x);
-        for (int s = 0; s < a.f.ns2; ++s)
-          if (ml2[s].y != 0.f) m = fmax_nan(m, ml2[s].x);
-        float ol = -INFINITY;
-        if (a.f.own_lse) {
-          ol = a.f.own_lse[row] * 1.4426950408889634f;
-          m = fmax_nan(m, ol);
-        }
-        float sum = 0.f;
-        for (int s = 0; s < a.f.ns; ++s)
-          if (ml[s].y != 0.f) sum += exp2f(ml[s].x - m) * ml[s].y;
-        for (int s = 0; s < a.f.ns2; ++s)
-          if (ml2[s].y != 0.f) sum += exp2f(ml2[s].x - m) * ml2[s].y;
-        own = ol != -INFINITY ? exp2f(ol - m) : 0.f;
-        sum += own;
-        top = m;
-        inv = sum != 0.f ? 1.0f / sum : 0.f;
-        if (c0 == 0) {
-          if (sum == 0.f) status_or(status, OSCAR_DEV_EMPTY);
-          if (a.f.lse) a.f.lse[row] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-        }
+        merged = reinterpret_cast<const __half*>(a.f.acc + row * a.f.ns * D);
+        up = a.f.ml[row * a.f.ns * 2];
+        if (j + 2 < mine && row + 2 * int64_t(gridDim.x) * 128 < rows)
+          prefetch_row<DG>(reinterpret_cast<const __nv_bfloat16*>(merged + 2 * int64_t(gridDim.x) * 128 * a.f.ns * (2 * D)));
       }
-      // 16 channels from k on in float32 (query float32, merged partial results)
+      // 16 channels from k on of a float32 query
       auto fetch = [&](int k, float (&x)[16]) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = 0.f;
-        if (SRC == kQuery) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(x + e) = __ldg(reinterpret_cast<const float4*>(f32 + k + e));
-        } else if (SRC == kFinish) {
-          const float2* ml = reinterpret_cast<const float2*>(a.f.ml) + row * a.f.ns;
-          const float2* ml2 = reinterpret_cast<const float2*>(a.f.ml2) + row * a.f.ns2;
-          for (int s = 0; s <= a.f.ns + a.f.ns2; ++s) {
-            float w;
-            const float* src;
-            if (s < a.f.ns + a.f.ns2) {
-              const float2 p = s < a.f.ns ? ml[s] : ml2[s - a.f.ns];
-              if (p.y == 0.f) continue;  // nothing was written there
-              w = exp2f(p.x - top) * inv;
-              src = (s < a.f.ns ? f32 + int64_t(s) * D : a.f.acc2 + (row * a.f.ns2 + s - a.f.ns) * D) + k;
-            } else {
-              if (own == 0.f) break;
-              w = own * inv;
-              src = a.f.own_o + row * D + k;
-            }
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 v = *reinterpret_cast<const float4*>(src + e);
-              x[e] = fmaf(w, v.x, x[e]);
-              x[e + 1] = fmaf(w, v.y, x[e + 1]);
-              x[e + 2] = fmaf(w, v.z, x[e + 2]);
-              x[e + 3] = fmaf(w, v.w, x[e + 3]);
-            }
-          }
-        }
+        for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(x + e) = __ldg(reinterpret_cast<const float4*>(f32 + k + e));
       };
       bool finite = true;
       if (b16 || f32) {
@@ -275,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
         if (b16) {
           uint32_t w = 0;
           const uint4* src = reinterpret_cast<const uint4*>(b16);
-#pragma unroll 8
+#pragma unroll 16
           for (int e = 0; e < D / 8; ++e) {
             const uint4 v = __ldg(src + e);
             w = absmax2(absmax2(absmax2(absmax2(w, v.x), v.y), v.z), v.w);
@@ -300,19 +268,22 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
         up *= a.q.qscale;
       }
       if (SRC == kRead && ref.codes) up = 2.0f, down = 0.5f;
-      const int use = j >> 1;  // the buffers' use by this group
-      if (use > 0) ok = ok && wait(acc_empty + 8 * p, (use & 1) ^ 1);
-      factor[p * 128 + r] = up;
+      const int acc = j % kAcc;
+      if (j >= kAcc) ok = ok && wait(acc_empty + 8 * acc, ((j / kAcc) & 1) ^ 1);
+      factor[acc * 128 + r] = up;
       __syncwarp();
-      mbar_arrive_if(f_full + 8 * p, lane == 0);
+      mbar_arrive_if(f_full + 8 * acc, lane == 0);
 #pragma unroll 1
       for (int kb = 0; ok && kb < 2 * DG; ++kb) {
         const int gr = kb >> 1, half = kb & 1;
         uint32_t w[4];
         float2 sz = make_float2(0.f, 0.f);
+        if (SRC == kRead && half == 0) {
+          q0 = n0, q1 = n1, pair = npair;
+          fetch_codes(gr + 1 < DG ? ref : next, gr + 1 < DG ? gr + 1 : 0);
+        }
         if (SRC == kRead && ref.codes) {
-          const uint4 q0 = __ldg(reinterpret_cast<const uint4*>(ref.codes) + 2 * gr), q1 = __ldg(reinterpret_cast<const uint4*>(ref.codes) + 2 * gr + 1);
-          sz = __half22float2(__ldg(ref.sz + gr));
+          sz = __half22float2(pair);
           if (role == 0) {  // word 2 c + half: pair c of every 16-byte chunk
             w[0] = half ? q0.y : q0.x, w[1] = half ? q0.w : q0.z, w[2] = half ? q1.y : q1.x, w[3] = half ? q1.w : q1.z;
           } else {          // words 2 m and 2 m + 1, codes 8 half ..: pair m
@@ -355,6 +326,13 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
               *reinterpret_cast<uint4*>(dst + (((2 * q) ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
               *reinterpret_cast<uint4*>(dst + (((2 * q + 1) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
             }
+          } else if (SRC == kFinish) {
+            uint4 v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              v[q] = merged ? reinterpret_cast<const uint4*>(merged + set * D + 64 * kb)[q] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(dst + ((q ^ (r & 7)) << 4)) = v[q];
           } else if (f32) {
 #pragma unroll 1
             for (int q = 0; q < 8; q += 2) {
@@ -371,12 +349,13 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
             }
           } else {
             const uint4* src = b16 && !set ? reinterpret_cast<const uint4*>(b16 + 64 * kb) : nullptr;
-#pragma unroll 4
-            for (int q = 0; q < 8; ++q) {
-              const uint4 v = src ? __ldg(src + q) : make_uint4(0, 0, 0, 0);
+            uint4 v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = src ? __ldg(src + q) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
               *reinterpret_cast<uint4*>(dst + ((q ^ (r & 7)) << 4)) =
-                  make_uint4(scaled_half2(v.x, down), scaled_half2(v.y, down), scaled_half2(v.z, down), scaled_half2(v.w, down));
-            }
+                  make_uint4(scaled_half2(v[q].x, down), scaled_half2(v[q].y, down), scaled_half2(v[q].z, down), scaled_half2(v[q].w, down));
             if (SRC == kRead && half == 0 && set == 0)
               *reinterpret_cast<uint2*>(sm + L::oRank + p * kRank + rank_offset(r, 4 * gr)) = make_uint2(0, 0);
           }
@@ -395,30 +374,29 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
     bool ok = true;
 #pragma unroll 1
     for (int j = 0; ok && j < mine; ++j) {
-      const int p = j & 1;
+      const int acc = j % kAcc;
       const int64_t row = (int64_t(blockIdx.x) + int64_t(j) * gridDim.x) * 128 + r;
       bool keep;  // the row is stored
       if (SRC == kRead) {
         keep = row < rows;
         if (keep) {
-          const uint32_t bt = uint32_t(row / g.Hkv);
-          const int b = int(bt / uint32_t(a.r.n));
-          const int64_t pos = int64_t(a.r.start_pos[b]) + int(bt % uint32_t(a.r.n));
+          const uint32_t bt = fastdiv(uint32_t(row), a.div_hkv), b = fastdiv(bt, a.div_n);
+          const int64_t pos = int64_t(a.r.start_pos[b]) + int(bt - b * uint32_t(a.r.n));
           keep = pos >= 0 && pos < min(a.r.seq_lens[b], g.cap);
         }
       } else {
         const int32_t* ql = SRC == kQuery ? a.q.q_lens : a.f.q_lens;
         keep = row_live(row, rows, ql, SRC == kQuery ? a.q.n : a.f.n, SRC == kQuery ? a.q.Hq : a.f.Hq);
       }
-      ok = wait(f_full + 8 * p, (j >> 1) & 1);
-      ok = ok && wait(acc_full + 8 * p, (j >> 1) & 1);
+      ok = wait(f_full + 8 * acc, (j / kAcc) & 1);
+      ok = ok && wait(acc_full + 8 * acc, (j / kAcc) & 1);
       if (!ok) break;
       fence_after();
-      const float up = factor[p * 128 + r];
+      const float up = factor[acc * 128 + r];
 #pragma unroll 1
       for (int c = 0; c < NC; c += 16) {
         uint32_t v[16];
-        tmem_ld16(tmem + lanes + p * 128 + c, v);
+        tmem_ld16(tmem + lanes + acc * NC + c, v);
         tmem_wait16(v);
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * up);
@@ -439,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
       }
       fence_before();
       __syncwarp();
-      mbar_arrive_if(acc_empty + 8 * p, lane == 0);
+      mbar_arrive_if(acc_empty + 8 * acc, lane == 0);
     }
     if (!ok && lane == 0) fail();
   } else {
@@ -447,38 +425,41 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
     const uint32_t leader = elect_one();
     constexpr uint32_t id = idesc_of(NC, false, false);
     const uint32_t sX = base + L::oX, sB = base + L::oB, sRank = base + L::oRank;
-    int n[2] = {0, 0};
+    // D = 512: a tile has more units than a group's buffers hold, so the groups' tiles take turns unit by unit
+    constexpr int kTogether = DG == 4 ? 2 : 1;
     bool ok = true;
 #pragma unroll 1
-    for (int j = 0; ok && j < mine; ++j) {
-      const int p = j & 1;
-      if (j >= 2) ok = wait(acc_empty + 8 * p, ((j >> 1) & 1) ^ 1);
-      const uint32_t d = tmem + p * 128;
-      int used = p ? n[1] : n[0];
+    for (int j = 0; ok && j < mine; j += kTogether) {
+      const int count = min(kTogether, mine - j);
+      if (j >= kAcc)
+        for (int q = 0; q < count; ++q) ok = ok && wait(acc_empty + 8 * ((j + q) % kAcc), ((j / kAcc) & 1) ^ 1);
+      int used = (j >> 1) * 2 * DG * sets;  // units of the group
 #pragma unroll 1
       for (int kb = 0; ok && kb < 2 * DG; ++kb) {
         const uint32_t m = desc_of(sB + kb * (NC * 128), 16);
 #pragma unroll 1
         for (int set = 0; ok && set < sets; ++set, ++used) {
           const int un = used % PU;
-          ok = wait(x_full(p, un), (used / PU) & 1);
-          if (!ok) break;
-          fence_after();
-          const uint32_t x = desc_of(sX + (p * PU + un) * kUnit, 16);
+#pragma unroll 1
+          for (int q = 0; q < count; ++q) {
+            const int p = (j + q) & 1;
+            ok = wait(x_full(p, un), (used / PU) & 1);
+            if (!ok) break;
+            fence_after();
+            const uint32_t d = tmem + (j + q) % kAcc * NC, x = desc_of(sX + (p * PU + un) * kUnit, 16);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_f16_ss(d, x + 2 * k, m + 2 * k, id, kb | set | k, leader);
-          if (a.rl && set == 0) {
+            for (int k = 0; k < 4; ++k) mma_f16_ss(d, x + 2 * k, m + 2 * k, id, kb | set | k, leader);
+            if (RL && set == 0) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16_ss(d, x + 2 * k, m + (L::kB >> 4) + 2 * k, id, 1, leader);
+              for (int k = 0; k < 4; ++k) mma_f16_ss(d, x + 2 * k, m + (L::kB >> 4) + 2 * k, id, 1, leader);
+            }
+            if (SRC == kRead && kb == 2 * DG - 2 && set == 0)  // the middles of all groups are there
+              mma_f16_ss<kDescRank>(d, rank_desc(sRank + p * kRank), rank_desc(sRank + 2 * kRank), id, 1, leader);
+            mma_commit(x_empty(p, un), leader);
           }
-          if (SRC == kRead && kb == 2 * DG - 2 && set == 0)  // the middles of all groups are there
-            mma_f16_ss<kDescRank>(d, rank_desc(sRank + p * kRank), rank_desc(sRank + 2 * kRank), id, 1, leader);
-          mma_commit(x_empty(p, un), leader);
         }
       }
-      if (ok) mma_commit(acc_full + 8 * p, leader);
-      if (p) n[1] = used;
-      else n[0] = used;
+      for (int q = 0; ok && q < count; ++q) mma_commit(acc_full + 8 * ((j + q) % kAcc), leader);
     }
     if (!ok && lane == 0) fail();
     mma_commit(drained, leader);  // every product issued is complete before TMEM is freed
@@ -489,34 +470,34 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
   __syncthreads();
   if (warp == kExpandWarps + kStoreWarps) {
     fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kCols) : "memory");
   }
 }
 
-template <int SRC, int DG>
+template <int SRC, int DG, bool RL>
 int launch(MmArgs& a, int64_t rows, int roles, cudaStream_t stream) {
   static int sms[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return OSCAR_ERR_LAUNCH;
   if (!sms[dev]) {
     int n = 0;
-    if (cudaFuncSetAttribute(rows_mm_kernel<SRC, DG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<DG>::kBytes) !=
+    if (cudaFuncSetAttribute(rows_mm_kernel<SRC, DG, RL>, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<DG, RL>::kBytes) !=
             cudaSuccess ||
         cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return OSCAR_ERR_LAUNCH;
     sms[dev] = n;
   }
   a.tiles = (rows + 127) / 128;
-  const int chunks = DG * 128 / Plan<DG>::NC;
+  const int chunks = DG * 128 / Plan<DG, RL>::NC;
   const int per = int(std::min<int64_t>(a.tiles, std::max(1, sms[dev] / (chunks * roles))));
-  rows_mm_kernel<SRC, DG><<<dim3(per, chunks, roles), kThreads, Plan<DG>::kBytes, stream>>>(a);
+  rows_mm_kernel<SRC, DG, RL><<<dim3(per, chunks, roles), kThreads, Plan<DG, RL>::kBytes, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
 }
 
-template <int SRC>
+template <int SRC, bool RL>
 int launch_dim(MmArgs& a, int D, int64_t rows, int roles, cudaStream_t stream) {
-  return D == 128 ? launch<SRC, 1>(a, rows, roles, stream) : D == 256 ? launch<SRC, 2>(a, rows, roles, stream)
-                                                                      : launch<SRC, 4>(a, rows, roles, stream);
+  return D == 128 ? launch<SRC, 1, RL>(a, rows, roles, stream) : D == 256 ? launch<SRC, 2, RL>(a, rows, roles, stream)
+                                                                          : launch<SRC, 4, RL>(a, rows, roles, stream);
 }
 
 }  // namespace
@@ -524,22 +505,23 @@ int launch_dim(MmArgs& a, int D, int64_t rows, int roles, cudaStream_t stream) {
 int launch_read_tc(const ReadArgs& r, cudaStream_t stream) {
   MmArgs a{};
   a.r = r;
-  a.rl = r.out_fp32;
   a.xl = r.out_fp32 && r.g.lm;
-  return launch_dim<kRead>(a, r.g.D, int64_t(r.g.B) * r.n * r.g.Hkv, 2, stream);
+  a.div_hkv = fastdiv_make(uint32_t(r.g.Hkv));
+  a.div_n = fastdiv_make(uint32_t(r.n));
+  const int64_t rows = int64_t(r.g.B) * r.n * r.g.Hkv;
+  return r.out_fp32 ? launch_dim<kRead, true>(a, r.g.D, rows, 2, stream) : launch_dim<kRead, false>(a, r.g.D, rows, 2, stream);
 }
 int launch_qrot_rows_tc(const QrotRowsArgs& q, cudaStream_t stream) {
   MmArgs a{};
   a.q = q;
-  a.rl = 1;
   a.xl = q.in_fp32;
-  return launch_dim<kQuery>(a, q.D, q.rows, 1, stream);
+  return launch_dim<kQuery, true>(a, q.D, q.rows, 1, stream);
 }
 int launch_finish_rows_tc(const FinishArgs& f, cudaStream_t stream) {
   MmArgs a{};
   a.f = f;
-  a.rl = a.xl = f.out_fp32;
-  return launch_dim<kFinish>(a, f.D, f.rows, 1, stream);
+  a.xl = f.out_fp32;
+  return f.out_fp32 ? launch_dim<kFinish, true>(a, f.D, f.rows, 1, stream) : launch_dim<kFinish, false>(a, f.D, f.rows, 1, stream);
 }
 
 }  // namespace oscar

@@ -27,8 +27,8 @@ __device__ __forceinline__ int row_q_len(const RowsArgs& a, int b) {
 __device__ __forceinline__ bool row_live(int64_t row, int64_t rows, const int32_t* q_lens, int n, int Hq) {
   if (row >= rows) return false;
   if (!q_lens) return true;
-  const int64_t bt = row / Hq;
-  return int(bt % n) < q_lens[bt / n];
+  const uint32_t bt = uint32_t(row) / uint32_t(Hq);  // rows < 2^31
+  return int(bt % uint32_t(n)) < q_lens[bt / uint32_t(n)];
 }
 
 // Where one cached row of a role lives: BF16 (a window, or K-only INT2's V
@@ -90,6 +90,9 @@ __device__ __forceinline__ void row_load16(const Geom& g, const RowRef& r, int r
     dst[128 * (w >> 3) + ch] = fmaf(sz.x, level, sz.y);
   }
 }
+
+// 2^e as a float, -126 <= e <= 127
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }
 
 // Element [i][k] of the in-quant Hadamard: block-diagonal, order 128.
 __device__ __forceinline__ float hadamard_at(int i, int k) {

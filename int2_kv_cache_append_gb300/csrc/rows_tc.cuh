@@ -215,8 +215,6 @@ __device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t x) {
   // bf16 pairs: magnitudes compare as integers (a NaN is above infinity)
   return __vmaxu2(m, x & 0x7FFF7FFFu);
 }
-// 2^e as a float, -126 <= e <= 127
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }
 // smallest e in [-60, 126] with x < 2^e (x >= 0 finite; 126 is not enough for x >= 2^126, whose 2^-126 x < 4 still
 // fits; below 2^-60 a row keeps an absolute precision of 2^-85)
 __device__ __forceinline__ int exponent_above(float x) {
@@ -365,6 +363,40 @@ __device__ __forceinline__ void load_queries(const RowsArgs& a, uint8_t* sq, int
   mbar_arrive_if(f_full, lane == 0);
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+template <int DG>
+__device__ __forceinline__ void prefetch_row(const __nv_bfloat16* row) {
+#pragma unroll
+  for (int e = 0; e < 128 * DG; e += 64) prefetch_l2(row + e);
+}
+// bits of a BF16 row's largest |value|, kU 16-byte loads on their way at once
+template <int DG, int kU>
+__device__ __forceinline__ uint32_t row_max(const __nv_bfloat16* row) {
+  uint32_t w = 0;
+  const uint4* src = reinterpret_cast<const uint4*>(row);
+#pragma unroll kU
+  for (int j = 0; j < DG * 16; ++j) {
+    const uint4 v = src[j];
+    w = absmax2(absmax2(absmax2(absmax2(w, v.x), v.y), v.z), v.w);
+  }
+  return max(w & 0xFFFFu, w >> 16) << 16;
+}
+// 64 BF16 channels (zeros where src is null), scaled, into row r of a unit
+template <int kU>
+__device__ __forceinline__ void write_wide(const __nv_bfloat16* src, uint8_t* dst, int r, float scale) {
+  static_assert(8 % kU == 0);
+#pragma unroll 1
+  for (int p0 = 0; p0 < 8; p0 += kU) {
+    uint4 v[kU];
+#pragma unroll
+    for (int p = 0; p < kU; ++p) v[p] = src ? reinterpret_cast<const uint4*>(src)[p0 + p] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int p = 0; p < kU; ++p)
+      *reinterpret_cast<uint4*>(dst + (((p0 + p) ^ (r & 7)) << 4)) =
+          make_uint4(scaled_half2(v[p].x, scale), scaled_half2(v[p].y, scale), scaled_half2(v[p].z, scale), scaled_half2(v[p].w, scale));
+  }
+}
+
 // Constants of a tile, one slot of the ring: e[128] (the value rows'
 // exponents), rv[128] (2^-e), a word that is set when some e is not 0, and the
 // factor from the products' sums to scores in log2 units.
@@ -398,6 +430,29 @@ struct Share {
 constexpr int kRawStage = kTok * 36;  // staged codes (32 bytes) and scale / zero pairs of one (tile, group) and role
 constexpr int kRank = kTok * 32;      // one tile's rank-one operand
 
+// First tile of share s of ns.  Tiles with BF16 rows take about kWideCost times an INT2 tile's time, and the shares are of
+// equal time.
+constexpr int kWideCost = 3;
+__device__ __forceinline__ int share_start(const Geom& g, int T, int blocks, int s, int ns) {
+  const int w = g.vb ? 1 : kWideCost;
+  const int lo = min(blocks, (g.S + kTok - 1) / kTok), hi = min(blocks, max(lo, (T - g.W) / kTok));  // INT2 tiles: lo .. hi - 1
+  int64_t x = (int64_t(lo + blocks - hi) * w + (hi - lo)) * s / ns;
+  if (x < int64_t(lo) * w) return int(x) / w;
+  x -= int64_t(lo) * w;
+  return x < hi - lo ? lo + int(x) : hi + int(x - (hi - lo)) / w;
+}
+
+// The tiles from position p0 on that lie within [from, to).
+struct Tiles {
+  int first;
+  uint32_t count;
+  __device__ Tiles(int p0, int from, int to) {
+    first = from > p0 ? (from - p0 - 1) / kTok + 1 : 0;
+    count = uint32_t(max(0, (to - p0) / kTok - first));
+  }
+  __device__ bool has(int i) const { return uint32_t(i - first) < count; }
+};
+
 // K, four warps, a thread per token.  An INT2 key is z + s c = (z + s) + s (c - 1),
 // and s (c - 1) is -s, 0, s or 2 s: exact in fp16.  The middles z + s enter as a
 // rank-one term of 16 more k (rank_key), so the products' sums are the scores.
@@ -409,7 +464,7 @@ constexpr int kRank = kTok * 32;      // one tile's rank-one operand
 //
 // Steps k = (tile, group); codes are staged kStages - 1 steps ahead by cp.async,
 // each thread its own row.  Returns false after a timeout.
-template <int DG, int KU, int CB, int kStages>
+template <int DG, int KU, int CB, int kStages, int kU>
 __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
   // the rank-one operand of tile i + 2 is written after unit 0 of that tile has found the unit KU before it empty, and
   // tile i's is used with the first unit of its last group
@@ -437,6 +492,12 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
   for (int k = 0; k < kStages - 1; ++k) stage(k);
   for (int j = 0; j < 4; ++j)  // columns beyond 4 DG stay zero
     *reinterpret_cast<uint4*>(x.sm + x.oRank + (j >> 1) * kRank + rank_offset(tok, 8 * (j & 1))) = make_uint4(0, 0, 0, 0);
+  auto ahead = [&](int i) {  // a BF16 row of tile i on its way to the L2 cache
+    const int pos = x.p0 + i * kTok + tok;
+    if (pos < x.p1 && (pos < g.S || pos >= ring0)) prefetch_row<DG>(row_ref(g, x.a->layer_base, 0, x.u, x.T, pos).wide);
+  };
+  ahead(0);
+  const Tiles packed_tiles(x.p0, g.S, ring0);
   bool ok = wait(x.f_full, 0);  // a warp that gave up still comes to the group's barriers
   const float F = *x.F;
   float down = 0.5f;            // the tile's power of two; one half keeps 2 s and z + s within fp16
@@ -449,6 +510,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
     const bool valid = pos < x.p1, packed = valid && pos >= g.S && pos < ring0;
     const __nv_bfloat16* wide = valid && !packed ? row_ref(g, x.a->layer_base, 0, x.u, x.T, pos).wide : nullptr;
     if (gr == 0) {
+      if (!packed_tiles.has(i + 1)) ahead(i + 1);
       float phi = 2.0f * F;
       down = 0.5f;
       const int first = x.p0 + i * kTok, last = min(x.p1, first + kTok) - 1;
@@ -461,14 +523,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
             m = fmaxf(m, fmaxf(fabsf(sz.y), fabsf(fmaf(sz.x, g.lm ? kLmSpan : 3.0f, sz.y))));
           }
         } else if (wide) {
-          uint32_t w = 0;
-          const uint4* src = reinterpret_cast<const uint4*>(wide);
-#pragma unroll 8
-          for (int j = 0; j < DG * 16; ++j) {
-            const uint4 v = src[j];
-            w = absmax2(absmax2(absmax2(absmax2(w, v.x), v.y), v.z), v.w);
-          }
-          m = __uint_as_float(max(w & 0xFFFFu, w >> 16) << 16);
+          m = __uint_as_float(row_max<DG, 2 * kU>(wide));
         }
         const uint32_t wm = __reduce_max_sync(0xffffffffu, isfinite(m) ? __float_as_uint(m) : 0u);
         uint32_t* most = reinterpret_cast<uint32_t*>(x.sm + x.oScratch) + 4 * (i & 3);
@@ -531,12 +586,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
             *reinterpret_cast<uint4*>(row + (((2 * q + 1) ^ (tok & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         } else {
-#pragma unroll 4
-          for (int p = 0; p < 8; ++p) {
-            const uint4 v = wide && set == 0 ? reinterpret_cast<const uint4*>(wide + gr * 128 + half * 64)[p] : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(row + ((p ^ (tok & 7)) << 4)) =
-                make_uint4(scaled_half2(v.x, down), scaled_half2(v.y, down), scaled_half2(v.z, down), scaled_half2(v.w, down));
-          }
+          write_wide<kU>(wide && set == 0 ? wide + gr * 128 + half * 64 : nullptr, row, tok, down);
         }
         fence_async();
         __syncwarp();
@@ -552,7 +602,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
 // exponents and the scale / zero pairs, fetched two tiles ahead, lane 16 h + j
 // stands for the token of half h.  The exponents of a tile are published before
 // the previous tile's units, which wait for products, are written.
-template <int DG, int VU, int CB, int kStages>
+template <int DG, int VU, int CB, int kStages, int kU>
 __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
   const Geom& g = x.a->g;
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity); };
@@ -571,6 +621,7 @@ __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
     cp_async_commit();
   };
   const int mine = 64 * cb + sub;  // the lane's token for exponents
+  const Tiles packed_tiles(x.p0, pk0, pk1);
   uint32_t sz[DG], nsz[DG], fsz[DG];  // this tile's pairs, the next one's and those on their way
   auto pairs = [&](int i, uint32_t (&d)[DG]) {
     const int pos = x.p0 + i * kTok + mine;
@@ -590,14 +641,7 @@ __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
         m = fmax_nan(m, fmax_nan(fabsf(v.y), fabsf(fmaf(v.x, g.lm ? kLmSpan : 3.0f, v.y))));
       }
     } else if (pos < x.p1) {
-      uint32_t w = 0;
-      const uint4* src = reinterpret_cast<const uint4*>(row_ref(g, x.a->layer_base, 1, x.u, x.T, pos).wide);
-#pragma unroll 8
-      for (int j = 0; j < DG * 16; ++j) {
-        const uint4 v = src[j];
-        w = absmax2(absmax2(absmax2(absmax2(w, v.x), v.y), v.z), v.w);
-      }
-      m = __uint_as_float(max(w & 0xFFFFu, w >> 16) << 16);
+      m = __uint_as_float(row_max<DG, 2 * kU>(row_ref(g, x.a->layer_base, 1, x.u, x.T, pos).wide));
     }
     // rows of ordinary size keep exponent 0
     ne = pos >= x.p1 ? -INFINITY
@@ -613,6 +657,12 @@ __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
     mbar_arrive_if(x.c_full + 8 * slot, lane == 0);
     return true;
   };
+  auto ahead = [&](int i) {  // a BF16 row of tile i on its way to the L2 cache
+    const int pos = x.p0 + i * kTok + mine;
+    if (pos < x.p1 && (pos < pk0 || pos >= pk1)) prefetch_row<DG>(row_ref(g, x.a->layer_base, 1, x.u, x.T, pos).wide);
+  };
+  ahead(0);
+  ahead(1);
   pairs(0, nsz);
   pairs(1, fsz);
 #pragma unroll 1
@@ -627,6 +677,7 @@ __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
 #pragma unroll
       for (int j = 0; j < DG; ++j) sz[j] = nsz[j], nsz[j] = fsz[j];
       pairs(i + 2, fsz);
+      if (!packed_tiles.has(i + 2)) ahead(i + 2);
       if (i + 1 < x.nt && !publish(i + 1, nsz)) return false;
     }
     cp_async_wait<kStages - 1>();
@@ -684,15 +735,8 @@ __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
         if (g.lm) write(Flag<true>());
         else write(Flag<false>());
       } else {
-        const uint4* src = fine && pos < x.p1
-                               ? reinterpret_cast<const uint4*>(row_ref(g, x.a->layer_base, 1, x.u, x.T, pos).wide + gr * 128 + cb * 64)
-                               : nullptr;
-#pragma unroll 4
-        for (int p = 0; p < 8; ++p) {
-          const uint4 v = src ? src[p] : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(row + ((p ^ (sub & 7)) << 4)) =
-              make_uint4(scaled_half2(v.x, scale), scaled_half2(v.y, scale), scaled_half2(v.z, scale), scaled_half2(v.w, scale));
-        }
+        write_wide<kU>(fine && pos < x.p1 ? row_ref(g, x.a->layer_base, 1, x.u, x.T, pos).wide + gr * 128 + cb * 64 : nullptr, row, sub,
+                       scale);
       }
       fence_async();
       __syncwarp();
