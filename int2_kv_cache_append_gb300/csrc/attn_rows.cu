@@ -35,6 +35,8 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const RowsArgs a) {
   float* Vs = Ks + kTokTile * xp;
   float* Ss = Vs + kTokTile * xp;
   // item: split s of row tile rt (last tiles first: with a causal mask they are the longest) of unit u
+  pdl_wait();
+  if (a.early) pdl_trigger();
   const int units = g.B * g.Hkv, rows = a.n * g.G, tiles = (rows + kRowTile - 1) / kRowTile;
   const int s = int(blockIdx.x % unsigned(a.ns));
   const int64_t it = blockIdx.x / unsigned(a.ns);
@@ -156,8 +158,7 @@ int launch(const RowsArgs& a, cudaStream_t stream) {
   const int64_t tiles = (int64_t(a.n) * a.g.G + kRowTile - 1) / kRowTile;
   const int64_t items = tiles * a.g.B * a.g.Hkv * a.ns;
   if (items >= (int64_t(1) << 31)) return OSCAR_ERR_UNSUPPORTED;
-  attn_rows_kernel<D><<<unsigned(items), kThreads, smem, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
+  return row_launch(true, attn_rows_kernel<D>, dim3(unsigned(items)), kThreads, smem, stream, a);
 }
 
 }  // namespace

@@ -91,7 +91,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
   const int T = row_seq_len(a, b, threadIdx.x == 0 && rt == 0);
   const int ql = row_q_len(a, b);
   const int t_first = rt * N / g.G;
-  if (t_first >= ql) return;  // only padding
+  if (t_first >= ql) {  // only padding
+    pdl_wait();
+    return;
+  }
   const int t_last = min((rt * N + N - 1) / g.G, ql - 1);
   const int vis = max(0, a.causal ? min(T, T - ql + t_last + 1) : T);
   const int see_all = a.causal ? T - ql + t_first : T - 1;  // every row sees the positions up to this one
@@ -118,7 +121,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     outr[c] = live ? (b * a.n + t) * g.Hq + h * g.G + row % g.G : -1;
     if (nt <= 0 && live) *reinterpret_cast<float2*>(a.ml + (int64_t(outr[c]) * a.ns + s) * 2) = make_float2(kNone, 0.f);
   }
-  if (nt <= 0) return;  // nothing visible in this share
+  if (nt <= 0) {  // nothing visible in this share
+    pdl_wait();
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < KU; ++i) mbar_init(k_full + 8 * i, 4), mbar_init(k_empty + 8 * i, 1);
     for (int i = 0; i < VU; ++i) mbar_init(v_full + 8 * i, 4), mbar_init(v_empty + 8 * i, 1);
@@ -141,6 +147,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (!a.beside) pdl_wait();  // the queries
+  if (a.early) pdl_trigger();
   auto fail = [&]() {
     *abort_flag = 1;
     status_or(a.status, OSCAR_DEV_TIMEOUT);
@@ -424,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     mbar_wait(drained, 0);
     __syncwarp();
   }
+  if (a.beside) pdl_wait();
   fence_before();
   __syncthreads();
   if (warp == kSoftWarps + 8) {
@@ -446,8 +455,7 @@ int launch_attn_rows_lanes(const RowsArgs& a, cudaStream_t stream) {
   const int64_t tiles = (int64_t(a.n) * a.g.G + N - 1) / N;
   const int64_t items = tiles * a.g.B * a.g.Hkv * a.ns;
   if (items >= (int64_t(1) << 31)) return OSCAR_ERR_UNSUPPORTED;
-  attn_rows_lanes_kernel<<<unsigned(items), kThreads, kBytes, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
+  return row_launch(true, attn_rows_lanes_kernel, dim3(unsigned(items)), kThreads, kBytes, stream, a);
 }
 
 }  // namespace oscar

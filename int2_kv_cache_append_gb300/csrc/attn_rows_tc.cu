@@ -101,7 +101,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
   const int T = row_seq_len(a, b, threadIdx.x == 0 && rt == 0);
   const int ql = row_q_len(a, b);
   const int t_first = rt * N / g.G;
-  if (t_first >= ql) return;  // only padding
+  if (t_first >= ql) {  // only padding
+    pdl_wait();
+    return;
+  }
   const int t_last = min((rt * N + N - 1) / g.G, ql - 1);
   const int vis = max(0, a.causal ? min(T, T - ql + t_last + 1) : T);
   const int see_all = a.causal ? T - ql + t_first : T - 1;  // every row sees the positions up to this one
@@ -143,7 +146,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     negM[c] = -kNone;
     if (nt <= 0 && live) *reinterpret_cast<float2*>(a.ml + (int64_t(outr[c]) * a.ns + s) * 2) = make_float2(kNone, 0.f);
   }
-  if (nt <= 0) return;  // nothing visible in this share
+  if (nt <= 0) {  // nothing visible in this share
+    pdl_wait();
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::KU; ++i) mbar_init(k_full(i), 4), mbar_init(k_empty(i), 1);
     for (int i = 0; i < L::VU; ++i) mbar_init(v_full(i), 4), mbar_init(v_empty(i), 1);
@@ -165,6 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (!a.beside) pdl_wait();  // the queries
+  if (a.early) pdl_trigger();
   auto fail = [&]() {
     *abort_flag = 1;
     status_or(a.status, OSCAR_DEV_TIMEOUT);
@@ -456,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     mbar_wait(drained, 0);
     __syncwarp();
   }
+  if (a.beside) pdl_wait();
   fence_before();
   __syncthreads();
   if (warp == kSoftWarps + 8) {
@@ -478,8 +487,7 @@ int launch(const RowsArgs& a, cudaStream_t stream) {
   const int64_t tiles = (int64_t(a.n) * a.g.G + N - 1) / N;
   const int64_t items = tiles * a.g.B * a.g.Hkv * a.ns;
   if (items >= (int64_t(1) << 31)) return OSCAR_ERR_UNSUPPORTED;
-  attn_rows_tc_kernel<DG, N><<<unsigned(items), kThreads, Plan<DG, N>::kBytes, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
+  return row_launch(true, attn_rows_tc_kernel<DG, N>, dim3(unsigned(items)), kThreads, Plan<DG, N>::kBytes, stream, a);
 }
 
 // Query rows per CTA.  More than 64 rows go to the row-lane kernel where its accumulators fit TMEM.

@@ -122,6 +122,10 @@ struct RowsArgs {
   int32_t* status;
   int n, ns;
   int causal;               // token t sees positions <= seq_len - q_len + t; else every position
+  // Within a call the kernels follow each other by programmatic dependent launch (row_launch).  early: the next kernel may
+  // start with this one's last blocks; beside: this kernel reads nothing of the one before it, which has itself waited for
+  // the queries, and waits for it only at its own end.
+  int early, beside;
 };
 int launch_attn_rows(const RowsArgs& a, cudaStream_t stream);
 int launch_attn_rows_tc(const RowsArgs& a, cudaStream_t stream);  // fp16 products (attn_rows_tc.cu)
@@ -163,6 +167,7 @@ struct FinishArgs {
   int64_t rows;             // B * n * Hq
   int n, Hq, D, ns, ns2;
   int out_fp32, absorb_v, hadamard;
+  int dependent;            // follows its predecessor by programmatic dependent launch
 };
 int launch_finish_rows(const FinishArgs& a, cudaStream_t stream);
 int launch_finish_rows_tc(const FinishArgs& a, cudaStream_t stream);

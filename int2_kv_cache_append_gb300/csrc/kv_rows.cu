@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kFewThreads) qrot_few_kernel(const QrotRowsArg
   __shared__ alignas(16) float X[kFew][D];
   __shared__ float red[4 * kFew * 128];
   const int64_t row0 = int64_t(blockIdx.x) * kFew;
+  pdl_trigger();
   if (a.zero_word && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.zero_word = 0;
   bool finite = true;
 #pragma unroll
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(kFewThreads) finish_few_kernel(const FinishArg
   __shared__ int live[kFew];
   const int64_t row0 = int64_t(blockIdx.x) * kFew;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, all = a.ns + a.ns2;
+  pdl_wait();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) own_status(a);
   if (warp < kFew) {  // a warp per row, a lane per partial result
     const int64_t row = row0 + warp;
@@ -253,6 +255,8 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_kernel(const FinishArgs
   __shared__ float weights[kMergeRows][2 * OSCAR_KV_MAX_SPLITS + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, all = a.ns + a.ns2;
   const int64_t row = int64_t(blockIdx.x) * kMergeRows + warp;
+  pdl_wait();
+  pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x == 0) own_status(a);
   if (!row_live(row, a.rows, a.q_lens, a.n, a.Hq)) return;
   float* wgt = weights[warp];
@@ -349,18 +353,14 @@ int launch_qrot_rows(const QrotRowsArgs& a, cudaStream_t stream) {
 
 int launch_finish_rows(const FinishArgs& a, cudaStream_t stream) {
   if (a.rows * a.D * a.D >= kTensorQuery) {
-    const unsigned blocks = unsigned((a.rows + kMergeRows - 1) / kMergeRows);
-    if (a.D == 128) merge_kernel<1><<<blocks, 32 * kMergeRows, 0, stream>>>(a);
-    else if (a.D == 256) merge_kernel<2><<<blocks, 32 * kMergeRows, 0, stream>>>(a);
-    else merge_kernel<4><<<blocks, 32 * kMergeRows, 0, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return OSCAR_ERR_LAUNCH;
-    return launch_finish_rows_tc(a, stream);
+    const dim3 blocks(unsigned((a.rows + kMergeRows - 1) / kMergeRows));
+    const auto kernel = a.D == 128 ? merge_kernel<1> : a.D == 256 ? merge_kernel<2> : merge_kernel<4>;
+    const int rc = row_launch(a.dependent, kernel, blocks, 32 * kMergeRows, 0, stream, a);
+    return rc == OSCAR_OK ? launch_finish_rows_tc(a, stream) : rc;
   }
   const dim3 grid(unsigned((a.rows + kFew - 1) / kFew), a.D / 128);
-  if (a.D == 128) finish_few_kernel<128><<<grid, kFewThreads, 0, stream>>>(a);
-  else if (a.D == 256) finish_few_kernel<256><<<grid, kFewThreads, 0, stream>>>(a);
-  else finish_few_kernel<512><<<grid, kFewThreads, 0, stream>>>(a);
-  return launched();
+  const auto kernel = a.D == 128 ? finish_few_kernel<128> : a.D == 256 ? finish_few_kernel<256> : finish_few_kernel<512>;
+  return row_launch(a.dependent, kernel, grid, kFewThreads, 0, stream, a);
 }
 
 }  // namespace oscar

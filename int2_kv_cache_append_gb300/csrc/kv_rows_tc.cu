@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
   int32_t* status = SRC == kQuery ? a.q.status : SRC == kFinish ? a.f.status : a.r.status;
   const int64_t rows = SRC == kQuery ? a.q.rows : SRC == kFinish ? a.f.rows : int64_t(g.B) * a.r.n * g.Hkv;
   if (!out) return;
+  if (SRC == kQuery) pdl_trigger();
 
   float* factor = reinterpret_cast<float*>(sm + L::oRow);      // [kAcc][128]
   float* sums = factor + kAcc * 128;                                  // [NC][DG]
@@ -167,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (SRC == kFinish) pdl_wait();  // the merged rows
   auto fail = [&]() {
     *abort_flag = 1;
     status_or(status, OSCAR_DEV_TIMEOUT);
@@ -490,8 +492,7 @@ int launch(MmArgs& a, int64_t rows, int roles, cudaStream_t stream) {
   a.tiles = (rows + 127) / 128;
   const int chunks = DG * 128 / Plan<DG, RL>::NC;
   const int per = int(std::min<int64_t>(a.tiles, std::max(1, sms[dev] / (chunks * roles))));
-  rows_mm_kernel<SRC, DG, RL><<<dim3(per, chunks, roles), kThreads, Plan<DG, RL>::kBytes, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
+  return row_launch(SRC == kFinish, rows_mm_kernel<SRC, DG, RL>, dim3(per, chunks, roles), kThreads, Plan<DG, RL>::kBytes, stream, a);
 }
 
 template <int SRC, bool RL>

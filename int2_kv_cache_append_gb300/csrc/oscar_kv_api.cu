@@ -418,9 +418,10 @@ int attn_extend(const oscar_kv_config* cfg, const void* cache, int32_t layer, co
   const int ns = fit_splits(g, int64_t(g.B) * n_new * g.Hq, want, num_splits > 0, workspace_bytes);
   if (ns == 0) return OSCAR_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  RowsPlan p;
+  RowsPlan p{};
   plan_rows(cfg, g, cache, layer, q, n_new, seq_lens, q_lens, R_K, R_V, sm_scale, ns, out, lse, dev_status, &ws, &p);
   p.at.causal = 1;
+  p.at.early = p.fin.dependent = 1;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int rc = oscar::launch_qrot_rows(p.q, st);
   if (rc == OSCAR_OK) rc = launch_rows(cfg, p.at, st);
@@ -471,7 +472,7 @@ int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const osca
       workspace_bytes < own ? 0 : fit_splits(pg, rows, want, num_splits > 0, workspace_bytes - own);
   if (ns == 0) return OSCAR_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  RowsPlan p;
+  RowsPlan p{};
   // one query token per sequence: the batch is the block of query rows of the one prefix
   plan_rows(cfg, pg, prefix_cache, layer, q, g.B, prefix_len, nullptr, R_K, R_V, sm_scale, ns, out, lse, dev_status, &ws,
             &p);
@@ -482,6 +483,7 @@ int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const osca
     own_at.layer_base = static_cast<const uint8_t*>(cache) + uint64_t(layer) * g.layer_bytes;
     own_at.seq_lens = seq_lens;
     own_at.n = 1;
+    p.at.early = own_at.early = own_at.beside = p.fin.dependent = 1;
     own_at.ns = want2;
     own_at.acc = take<float>(&ws, uint64_t(rows) * want2 * g.D * 4);
     own_at.ml = take<float>(&ws, uint64_t(rows) * want2 * 8);

@@ -2,11 +2,30 @@
 // positions or of query rows (kv_read, attn_extend, attn_decode_prefix).
 #pragma once
 
+#include "common.cuh"
 #include "internal.h"
 
 namespace oscar {
 
 constexpr int kSplitUnit = 128;  // positions: the shares of a split cache start at multiples of it
+
+// Launch after the kernel before it in the stream; dependent: it may start once every block of that one has called
+// pdl_trigger or ended, and waits (pdl_wait) before it reads what that one or an earlier one wrote.  Every block of a
+// kernel that is launched so waits before it ends, so that "complete" holds for everything before it, too.
+template <class... P>
+int row_launch(bool dependent, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, P... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
+}
 
 // Length of sequence b in the cache that is read, clamped to the capacity;
 // `report`: this thread flags a length above it.

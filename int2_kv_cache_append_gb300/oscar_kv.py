@@ -141,7 +141,7 @@ def _ptr(t):
         raise ValueError(f"oscar_kv: expected a CUDA tensor, got one on {t.device}")
     if not t.is_contiguous():
         raise ValueError("oscar_kv: expected a contiguous tensor")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _check(t, name: str, dtypes, shape=None, min_bytes=None, optional: bool = False):
@@ -153,10 +153,10 @@ def _check(t, name: str, dtypes, shape=None, min_bytes=None, optional: bool = Fa
         raise ValueError(f"oscar_kv: {name} is required")
     if t.dtype not in dtypes:
         raise ValueError(f"oscar_kv: {name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"oscar_kv: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if min_bytes is not None and t.numel() * t.element_size() < min_bytes:
-        raise ValueError(f"oscar_kv: {name} holds {t.numel() * t.element_size()} bytes, needs {min_bytes}")
+    if min_bytes is not None and t.nbytes < min_bytes:
+        raise ValueError(f"oscar_kv: {name} holds {t.nbytes} bytes, needs {min_bytes}")
 
 
 def _dt():
@@ -164,9 +164,26 @@ def _dt():
     return torch
 
 
-def _check_cache(cfg: "KVConfig", cache):
+_known = {}  # (C struct, cache bytes) of the configurations in use, by their values
+
+
+def _known_cfg(cfg: "KVConfig"):
+    key = (cfg.num_layers, cfg.batch, cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim, cfg.sink, cfg.recent,
+           cfg.capacity, cfg.k_clip, cfg.v_clip, cfg.flags, cfg.group_size)
+    hit = _known.get(key)
+    if hit is None:
+        if len(_known) >= 256:
+            _known.clear()
+        hit = _known[key] = (cfg.c(), layout_query(cfg)["total_bytes"])
+    return hit
+
+
+def _check_cache(cfg: "KVConfig", cache, name: str = "cache"):
+    """Returns the configuration for the library."""
     torch = _dt()
-    _check(cache, "cache", (torch.uint8,), min_bytes=layout_query(cfg)["total_bytes"])
+    c, total = _known_cfg(cfg)
+    _check(cache, name, (torch.uint8,), min_bytes=total)
+    return ctypes.byref(c)
 
 
 def _check_rot(cfg: "KVConfig", R, name: str):
@@ -289,10 +306,13 @@ def attn_decode_static(cfg: KVConfig, cache, layer: int, q, seq_lens, R_K, R_V, 
 
 def _same_device(*tensors) -> None:
     """The library launches on the current device: refuse tensors that live on another one."""
-    torch = _dt()
+    current = None
     for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"oscar_kv: tensor on {t.device}, current device is cuda:{torch.cuda.current_device()}")
+        if t is not None and t.is_cuda:
+            if current is None:
+                current = _dt().cuda.current_device()
+            if t.get_device() != current:
+                raise ValueError(f"oscar_kv: tensor on {t.device}, current device is cuda:{current}")
 
 
 def kv_read(cfg: KVConfig, cache, layer: int, start_pos, seq_lens, R_K, R_V, k_out=None, v_out=None, status=None,
@@ -311,11 +331,11 @@ def kv_read(cfg: KVConfig, cache, layer: int, start_pos, seq_lens, R_K, R_V, k_o
     _check(start_pos, "start_pos", (torch.int32,), shape=(B,))
     _check(seq_lens, "seq_lens", (torch.int32,), shape=(B,))
     _check(status, "status", (torch.int32,), min_bytes=4, optional=True)
-    _check_cache(cfg, cache)
+    c = _check_cache(cfg, cache)
     _check_rot(cfg, R_K, "R_K")
     _check_rot(cfg, R_V, "R_V")
     _same_device(cache, start_pos, seq_lens, R_K, R_V, k_out, v_out, status)
-    rc = lib().kv_read(ctypes.byref(cfg.c()), _ptr(cache), layer, _ptr(start_pos), _ptr(seq_lens), n, _ptr(R_K),
+    rc = lib().kv_read(c, _ptr(cache), layer, _ptr(start_pos), _ptr(seq_lens), n, _ptr(R_K),
                        _ptr(R_V), _ptr(k_out), _ptr(v_out), _ptr(status), _stream(stream))
     if check and rc != 0:
         raise OscarError("kv_read", rc)
@@ -347,11 +367,11 @@ def attn_extend(cfg: KVConfig, cache, layer: int, q, seq_lens, R_K, R_V, out, wo
     _check(q_lens, "q_lens", (torch.int32,), shape=(B,), optional=True)
     _check(status, "status", (torch.int32,), min_bytes=4, optional=True)
     _check(workspace, "workspace", (torch.uint8,))
-    _check_cache(cfg, cache)
+    c = _check_cache(cfg, cache)
     _check_rot(cfg, R_K, "R_K")
     _check_rot(cfg, R_V, "R_V")
     _same_device(cache, q, seq_lens, q_lens, R_K, R_V, out, lse, workspace, status)
-    rc = lib().attn_extend(ctypes.byref(cfg.c()), _ptr(cache), layer, _ptr(q), n, _ptr(q_lens), _ptr(seq_lens),
+    rc = lib().attn_extend(c, _ptr(cache), layer, _ptr(q), n, _ptr(q_lens), _ptr(seq_lens),
                            int(seq_len_hint), _ptr(R_K), _ptr(R_V), float(sm_scale), int(num_splits), _ptr(out),
                            _ptr(lse), _ptr(workspace), int(workspace.numel()), _ptr(status), _stream(stream))
     if check and rc != 0:
@@ -375,13 +395,13 @@ def attn_decode_prefix(cfg: KVConfig, cache, prefix_cfg: KVConfig, prefix_cache,
     torch = _dt()
     _check_decode_io(cfg, q, seq_lens, out, lse, status)
     _check(prefix_len, "prefix_len", (torch.int32,), shape=(1,))
-    _check_cache(cfg, cache)
-    _check(prefix_cache, "prefix_cache", (torch.uint8,), min_bytes=layout_query(prefix_cfg)["total_bytes"])
+    c = _check_cache(cfg, cache)
+    pc = _check_cache(prefix_cfg, prefix_cache, "prefix_cache")
     _check_rot(cfg, R_K, "R_K")
     _check_rot(cfg, R_V, "R_V")
     _check(workspace, "workspace", (torch.uint8,))
     _same_device(cache, prefix_cache, q, seq_lens, prefix_len, R_K, R_V, out, lse, workspace, status)
-    rc = lib().attn_decode_prefix(ctypes.byref(cfg.c()), _ptr(cache), ctypes.byref(prefix_cfg.c()), _ptr(prefix_cache),
+    rc = lib().attn_decode_prefix(c, _ptr(cache), pc, _ptr(prefix_cache),
                                   layer, _ptr(q), _ptr(seq_lens), int(seq_len_hint), _ptr(prefix_len),
                                   int(prefix_len_hint), _ptr(R_K), _ptr(R_V), float(sm_scale), int(num_splits),
                                   _ptr(out), _ptr(lse), _ptr(workspace), int(workspace.numel()), _ptr(status),
