@@ -357,8 +357,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
   } else if (warp < kSoftWarps + 8) {
     Share x{&a, u, T, p0, p1, nt, sm, base, abort_flag, scale_f, f_full, k_full, k_empty, v_full, v_empty, c_full, c_empty,
             oK, oV, oRawK, oRawV, oConst, oRank, oRow + 5 * N * 4};
-    const bool ok = warp < kSoftWarps + 4 ? expand_k<1, KU, CB, kStages, 4>(x, threadIdx.x - kSoftWarps * 32, lane)
-                                          : expand_v<1, VU, CB, kStages, 4>(x, warp & 3, lane);
+    const int tok = threadIdx.x - kSoftWarps * 32;
+    const bool ok = warp < kSoftWarps + 4 ? (g.lm ? expand_k<1, KU, CB, kStages, 4, true>(x, tok, lane) : expand_k<1, KU, CB, kStages, 4, false>(x, tok, lane))
+                                          : (g.lm ? expand_v<1, VU, CB, kStages, 4, true>(x, warp & 3, lane) : expand_v<1, VU, CB, kStages, 4, false>(x, warp & 3, lane));
     if (!ok && lane == 0) fail();
   } else {
     // ------------------------------ MMA issuer --------------------------------

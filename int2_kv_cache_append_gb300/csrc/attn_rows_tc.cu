@@ -75,8 +75,11 @@ struct Plan {
   static constexpr int oBar = oRow + kRow;
   static constexpr int kBars = 2 * KU + 2 * VU + 2 * SB + 2 * PB + 2 * CB + 3;
   static constexpr int kBytes = oBar + kBars * 8 + 32 + 1024;  // + alignment slack
+  // The tensor cores cut each of their sums' additions off (towards zero).  At D = 512 a score would be 65 additions and
+  // 1e-6 too small, so two accumulators share them.
+  static constexpr int kParts = DG == 4 ? 2 : 1;
   static constexpr int cS = 0;                                // TMEM columns of the scores
-  static constexpr int cO = SB * N;                           // and of O^T
+  static constexpr int cO = SB * kParts * N;                  // and of O^T
   static_assert(cO + DG * N <= 512, "TMEM");
   static_assert(kBytes <= 232448, "shared memory");
 };
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
       const uint64_t e2 = splat_x2(tc.e()[tok]), rv2 = splat_x2(tc.rv()[tok]);
       const bool masked = p0 + i * kTok + kTok - 1 > see_all;  // some row does not see some position of the tile
       uint8_t* P = sm + L::oP + pb * L::kP + tok * 128;
-      const uint32_t S = tmem + lanes + L::cS + sb * N;
+      const uint32_t S = tmem + lanes + L::cS + sb * (L::kParts * N);
       // t = u - M (or u) of columns c .. c + 15
       auto scores = [&](int c, float (&t)[16], bool less_m) {
         uint64_t x[8];
@@ -221,6 +224,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
         uint32_t r[16];
         tmem_ld16(S + c, r);
         tmem_wait16(r);
+        if (L::kParts == 2) {
+          uint32_t r2[16];
+          tmem_ld16(S + N + c, r2);
+          tmem_wait16(r2);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(r2[j]));
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           x[j] = fma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), phi2, x[j]);
@@ -386,8 +396,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     Share x{&a, u, T, p0, p1, nt, sm, base, abort_flag, scale_f, f_full, k_full(0), k_empty(0), v_full(0), v_empty(0),
             c_full(0), c_empty(0), L::oK, L::oV, L::oRawK, L::oRawV, L::oConst, L::oRank,
             L::oRow + L::kRow - 64};
-    const bool ok = warp < kSoftWarps + 4 ? expand_k<DG, L::KU, L::CB, L::kStages, 8>(x, threadIdx.x - kSoftWarps * 32, lane)
-                                          : expand_v<DG, L::VU, L::CB, L::kStages, 8>(x, warp & 3, lane);
+    const int tok = threadIdx.x - kSoftWarps * 32;
+    const bool ok = warp < kSoftWarps + 4 ? (g.lm ? expand_k<DG, L::KU, L::CB, L::kStages, 8, true>(x, tok, lane) : expand_k<DG, L::KU, L::CB, L::kStages, 8, false>(x, tok, lane))
+                                          : (g.lm ? expand_v<DG, L::VU, L::CB, L::kStages, 8, true>(x, warp & 3, lane) : expand_v<DG, L::VU, L::CB, L::kStages, 8, false>(x, warp & 3, lane));
     if (!ok && lane == 0) fail();
   } else {
     // ------------------------------ MMA issuer --------------------------------
@@ -405,15 +416,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     uint32_t odd = 0;  // the tile's rank-one operand
     auto product_qk = [&](bool reuse) {
       if (reuse) ok = poll(s_empty(sr.at), sr.phase ^ 1) && ok;
-      const uint32_t d = L::cS + sr.at * N;
+      const uint32_t d = L::cS + sr.at * (L::kParts * N);
 #pragma unroll 1
       for (int kb = 0; kb < 2 * DG; ++kb) {
         ok = poll(k_full(kr.at), kr.phase) && ok;
         fence_after();
         const uint32_t k = dK + kr.at * (kUnit >> 4), q = dQ + kb * (N * 128 >> 4);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)  // Q's high, then its low part; descriptors count 16 bytes
-          mma_f16_ss(d, k + 2 * (j & 3), q + (j >> 2) * (L::kQ >> 4) + 2 * (j & 3), id_qk, j ? 1 : kb, leader);
+        for (int j = 0; j < 8; ++j) {  // Q's high, then its low part; descriptors count 16 bytes
+          // two accumulators: the high parts of the first half of the channels in one, of the rest in the other
+          const uint32_t at = L::kParts == 2 && (j < 4) == (kb >= DG) ? d + N : d;
+          mma_f16_ss(at, k + 2 * (j & 3), q + (j >> 2) * (L::kQ >> 4) + 2 * (j & 3), id_qk,
+                     (L::kParts == 2 ? j & 3 : j) ? 1 : kb, leader);
+        }
         if (kb == 2 * DG - 2)  // the middles of all groups are there
           mma_f16_ss<kDescRank>(d, dRank + odd * (kRank >> 4), dRank + (2 * kRank >> 4), id_qk, 1, leader);
         mma_commit(k_empty(kr.at), leader);

@@ -35,6 +35,9 @@ struct MmArgs {
   FastDiv div_hkv, div_n;  // of kv_read
 };
 
+// The matrix enters times this: elements of a rotation are below 1, most far below, and the low part of a small one would
+// be a subnormal fp16 number with few bits (float32 results were off by 1.4e-6 of their norm without it).
+constexpr float kMatrixScale = 128.0f;
 constexpr int kExpandWarps = 8, kStoreWarps = 4;
 constexpr int kThreads = (kExpandWarps + kStoreWarps + 1) * 32;
 
@@ -43,7 +46,11 @@ struct Plan {
   static constexpr int D = 128 * DG;
   static constexpr int NC = DG == 1 ? 128 : (RL ? 256 : 512) / DG;  // columns of a CTA
   static constexpr int PU = DG == 1 ? 3 : 2;                // units of an expanding group
-  static constexpr int kAcc = DG == 4 ? 4 : 2;               // accumulators
+  // The tensor cores cut every addition off: the 64 of two products over D = 512 in one sum make it 1e-6 too small.  So the
+  // products with the low part have an accumulator of their own, and at D = 512 either half of the channels has one, too.
+  static constexpr int kParts = !RL ? 1 : DG == 4 ? 3 : 2;
+  static constexpr int kAcc = DG == 4 && !RL ? 4 : 2;        // tiles that have accumulators
+  static constexpr int kCols = kAcc * kParts * NC > 256 ? 512 : 256;  // of TMEM
   static constexpr int kB = NC * D * 2;                     // one part of the matrix
   static constexpr int oB = 0;
   static constexpr int oX = (RL ? 2 : 1) * kB;
@@ -70,7 +77,7 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8], bool 
 template <int SRC, int DG, bool RL>
 __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_constant__ MmArgs a) {
   using L = Plan<DG, RL>;
-  constexpr int D = L::D, NC = L::NC, PU = L::PU, kAcc = L::kAcc, kCols = kAcc * NC;
+  constexpr int D = L::D, NC = L::NC, PU = L::PU, kAcc = L::kAcc, kParts = L::kParts, kStep = kParts * NC, kCols = L::kCols;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -130,6 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
       if (plain) v[e] = c0 + n == k0 + e ? 1.f : 0.f;
       else if (hadamard) v[e] = hadamard_at(c0 + n, k0 + e);
       else v[e] = SRC == kQuery ? __ldg(R + int64_t(k0 + e) * D + c0 + n) : __ldg(R + int64_t(c0 + n) * D + k0 + e);
+      v[e] *= kMatrixScale;
     }
     uint32_t hi[4], lo[4];
     float sum = 0.f;
@@ -272,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
       if (SRC == kRead && ref.codes) up = 2.0f, down = 0.5f;
       const int acc = j % kAcc;
       if (j >= kAcc) ok = ok && wait(acc_empty + 8 * acc, ((j / kAcc) & 1) ^ 1);
-      factor[acc * 128 + r] = up;
+      factor[acc * 128 + r] = up * (1.0f / kMatrixScale);
       __syncwarp();
       mbar_arrive_if(f_full + 8 * acc, lane == 0);
 #pragma unroll 1
@@ -398,8 +406,16 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
 #pragma unroll 1
       for (int c = 0; c < NC; c += 16) {
         uint32_t v[16];
-        tmem_ld16(tmem + lanes + acc * NC + c, v);
+        tmem_ld16(tmem + lanes + acc * kStep + c, v);
         tmem_wait16(v);
+#pragma unroll
+        for (int part = 1; part < kParts; ++part) {
+          uint32_t w[16];
+          tmem_ld16(tmem + lanes + acc * kStep + part * NC + c, w);
+          tmem_wait16(w);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(w[e]));
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * up);
         if (!keep) continue;
@@ -448,12 +464,15 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
             ok = wait(x_full(p, un), (used / PU) & 1);
             if (!ok) break;
             fence_after();
-            const uint32_t d = tmem + (j + q) % kAcc * NC, x = desc_of(sX + (p * PU + un) * kUnit, 16);
+            const uint32_t d = tmem + (j + q) % kAcc * kStep, large = kParts == 3 && kb >= DG ? d + NC : d,
+                           small = d + (kParts - 1) * NC;
+            const int done = kParts == 3 ? kb % DG : kb;  // units that the large accumulator has
+            const uint32_t x = desc_of(sX + (p * PU + un) * kUnit, 16);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16_ss(d, x + 2 * k, m + 2 * k, id, kb | set | k, leader);
+            for (int k = 0; k < 4; ++k) mma_f16_ss(set ? small : large, x + 2 * k, m + 2 * k, id, done | set | k, leader);
             if (RL && set == 0) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) mma_f16_ss(d, x + 2 * k, m + (L::kB >> 4) + 2 * k, id, 1, leader);
+              for (int k = 0; k < 4; ++k) mma_f16_ss(small, x + 2 * k, m + (L::kB >> 4) + 2 * k, id, kb | k, leader);
             }
             if (SRC == kRead && kb == 2 * DG - 2 && set == 0)  // the middles of all groups are there
               mma_f16_ss<kDescRank>(d, rank_desc(sRank + p * kRank), rank_desc(sRank + 2 * kRank), id, 1, leader);

@@ -252,6 +252,13 @@ __device__ __forceinline__ uint32_t lm_extra(uint32_t c1) {
   asm("min.f16x2 %0, %0, %1;" : "+r"(step) : "r"(0x3C003C00u));
   return hfma2(step, 0xBC00BC00u, c1);
 }
+// t = -1, 0, 0, 1 times: a where t is -1, b where it is 1
+__device__ __forceinline__ uint32_t by_sign(uint32_t t, uint32_t minus_a, uint32_t b) {
+  uint32_t up, down;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(up) : "r"(t), "r"(0u));
+  asm("min.f16x2 %0, %1, %2;" : "=r"(down) : "r"(t), "r"(0u));
+  return hfma2(up, b, hmul2(down, minus_a));
+}
 // unit * value of an fp16 pair in float32: its fp16 rounding (part 0) or what that leaves (part 1)
 __device__ __forceinline__ uint32_t lm_part(uint32_t value, float unit, int part) {
   const float2 x = __half22float2(*reinterpret_cast<__half2*>(&value));
@@ -457,21 +464,21 @@ struct Tiles {
 // and s (c - 1) is -s, 0, s or 2 s: exact in fp16.  The middles z + s enter as a
 // rank-one term of 16 more k (rank_key), so the products' sums are the scores.
 // Lloyd-Max levels are the uniform ones plus 0.16 (0, 1, 1, 2): z + rho s is the
-// middle and 0.16 s (-1, 0, 0, 1) goes to a second set of units that only Q's
-// high part meets (it is a twelfth of the first; its fp16 rounding and Q's low
-// part with it are below 2^-14 of a product).  BF16 keys are exact in fp16 once the tile's largest value is below 2^15; where it is not, or
+// middle, and s (-rho, 0, 1, rho + 1) is rounded to fp16 with the residues in a
+// second set of units, which only Q's high part meets (2^-24 of a product is lost).
+// BF16 keys are exact in fp16 once the tile's largest value is below 2^15; where it is not, or
 // far below 1, the whole tile is scaled by a power of two.
 //
 // Steps k = (tile, group); codes are staged kStages - 1 steps ahead by cp.async,
 // each thread its own row.  Returns false after a timeout.
-template <int DG, int KU, int CB, int kStages, int kU>
+template <int DG, int KU, int CB, int kStages, int kU, bool LM>
 __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
   // the rank-one operand of tile i + 2 is written after unit 0 of that tile has found the unit KU before it empty, and
   // tile i's is used with the first unit of its last group
   static_assert(2 * (DG + 1) >= KU, "two rank-one operands");
   const Geom& g = x.a->g;
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity); };
-  const int steps = x.nt * DG, per = g.lm ? 4 : 2;  // units of a step
+  const int steps = x.nt * DG, per = LM ? 4 : 2;  // units of a step
   const uint8_t* role = x.a->layer_base + g.sink_bytes + g.ring_bytes;
   const int64_t row0 = int64_t(x.u) * g.ncap + (x.p0 + tok - g.S);  // INT2 row of the first tile's token
   const uint8_t* codes = role + row0 * (32 * DG);
@@ -520,7 +527,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
 #pragma unroll
           for (int j = 0; j < DG; ++j) {
             const float2 sz = __half22float2(reinterpret_cast<const __half2*>(szs + int64_t(i) * (kTok * 4 * DG))[j]);
-            m = fmaxf(m, fmaxf(fabsf(sz.y), fabsf(fmaf(sz.x, g.lm ? kLmSpan : 3.0f, sz.y))));
+            m = fmaxf(m, fmaxf(fabsf(sz.y), fabsf(fmaf(sz.x, LM ? kLmSpan : 3.0f, sz.y))));
           }
         } else if (wide) {
           m = __uint_as_float(row_max<DG, 2 * kU>(wide));
@@ -545,8 +552,18 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
     float2 sz = make_float2(0.f, 0.f);
     if (packed) sz = __half22float2(*reinterpret_cast<const __half2*>(st + kTok * 32 + tok * 4));
     const uint32_t s1 = half2_of(sz.x * down, sz.x * down);
-    const uint32_t d1 = half2_of((kLmRho - 1.0f) * sz.x * down, (kLmRho - 1.0f) * sz.x * down);
-    const float middle = fmaf(g.lm ? kLmRho : 1.0f, sz.x, sz.y) * down;
+    // Lloyd-Max: -rho s, 0, s, (1 + rho) s as the uniform part plus d1 (-1, 0, 0, 1), rounded, and what that leaves
+    uint32_t d1 = 0, left0 = 0, left3 = 0;
+    if (LM) {
+      const float x1 = sz.x * down;
+      const __half d = __float2half_rn((kLmRho - 1.0f) * x1), h = __float2half_rn(x1);
+      const float l0 = -kLmRho * x1 + __half2float(__hfma(d, __float2half_rn(1.0f), h));
+      const float l3 = (kLmRho + 1.0f) * x1 - __half2float(__hfma(h, __float2half_rn(2.0f), d));
+      d1 = half2_of(__half2float(d), __half2float(d));
+      left0 = half2_of(-l0, -l0);
+      left3 = half2_of(l3, l3);
+    }
+    const float middle = fmaf(LM ? kLmRho : 1.0f, sz.x, sz.y) * down;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
       // word 2 c + half: pair c of every 16-byte chunk
@@ -560,18 +577,28 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
           *reinterpret_cast<uint2*>(x.sm + x.oRank + (i & 1) * kRank + rank_offset(tok, 4 * gr)) = rank_key(middle);
         uint8_t* row = x.sm + x.oK + u * kUnit + tok * 128;
         if (packed && set == 0) {
+          auto write = [&](auto lm) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t v[4], o[4];
+            for (int q = 0; q < 4; ++q) {
+              uint32_t v[4], o[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t y = code_shift(w[c], q);
-              v[c] = hmul2(less_one_even(y), s1);
-              o[c] = hmul2(less_one_odd(y), s1);
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t y = code_shift(w[c], q);
+                if constexpr (decltype(lm)::value) {
+                  v[c] = less_one_even(y);
+                  o[c] = less_one_odd(y);
+                  v[c] = hfma2(lm_extra(v[c]), d1, hmul2(v[c], s1));
+                  o[c] = hfma2(lm_extra(o[c]), d1, hmul2(o[c], s1));
+                } else {
+                  v[c] = hmul2(less_one_even(y), s1);
+                  o[c] = hmul2(less_one_odd(y), s1);
+                }
+              }
+              *reinterpret_cast<uint4*>(row + (((2 * q) ^ (tok & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(row + (((2 * q + 1) ^ (tok & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            *reinterpret_cast<uint4*>(row + (((2 * q) ^ (tok & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<uint4*>(row + (((2 * q + 1) ^ (tok & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
+          };
+          write(Flag<LM>());
         } else if (packed) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -579,8 +606,8 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const uint32_t y = code_shift(w[c], q);
-              v[c] = hmul2(lm_extra(less_one_even(y)), d1);
-              o[c] = hmul2(lm_extra(less_one_odd(y)), d1);
+              v[c] = by_sign(lm_extra(less_one_even(y)), left0, left3);
+              o[c] = by_sign(lm_extra(less_one_odd(y)), left0, left3);
             }
             *reinterpret_cast<uint4*>(row + (((2 * q) ^ (tok & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
             *reinterpret_cast<uint4*>(row + (((2 * q + 1) ^ (tok & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -602,7 +629,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
 // exponents and the scale / zero pairs, fetched two tiles ahead, lane 16 h + j
 // stands for the token of half h.  The exponents of a tile are published before
 // the previous tile's units, which wait for products, are written.
-template <int DG, int VU, int CB, int kStages, int kU>
+template <int DG, int VU, int CB, int kStages, int kU, bool LM>
 __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
   const Geom& g = x.a->g;
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity); };
@@ -638,7 +665,7 @@ __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
 #pragma unroll
       for (int j = 0; j < DG; ++j) {
         const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&pr[j]));
-        m = fmax_nan(m, fmax_nan(fabsf(v.y), fabsf(fmaf(v.x, g.lm ? kLmSpan : 3.0f, v.y))));
+        m = fmax_nan(m, fmax_nan(fabsf(v.y), fabsf(fmaf(v.x, LM ? kLmSpan : 3.0f, v.y))));
       }
     } else if (pos < x.p1) {
       m = __uint_as_float(row_max<DG, 2 * kU>(row_ref(g, x.a->layer_base, 1, x.u, x.T, pos).wide));
@@ -704,7 +731,7 @@ __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
         // Uniform: c / 4 or c / 16 from 1 + that, exactly; then one rounding of s c + z.  Lloyd-Max: one of the unit, one
         // of the middle and one of the sum.
         uint32_t s_odd, s_even, z2;
-        if (g.lm) {
+        if (LM) {
           s_odd = s_even = half2_of(v.x * scale * (1.0f / 150.0f), v.x * scale * (1.0f / 150.0f));
           const float mid = fmaf(v.x, kLmMiddle, v.y) * scale;
           z2 = half2_of(mid, mid);
@@ -732,8 +759,7 @@ __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
             *reinterpret_cast<uint4*>(row + (((2 * q + 1) ^ (sub & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         };
-        if (g.lm) write(Flag<true>());
-        else write(Flag<false>());
+        write(Flag<LM>());
       } else {
         write_wide<kU>(fine && pos < x.p1 ? row_ref(g, x.a->layer_base, 1, x.u, x.T, pos).wide + gr * 128 + cb * 64 : nullptr, row, sub,
                        scale);
