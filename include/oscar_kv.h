@@ -351,7 +351,13 @@ int kv_read(const oscar_kv_config* cfg, const void* cache, int32_t layer, const 
  *              takes at most.  With less, the automatic count is reduced to
  *              what fits (OSCAR_ERR_WORKSPACE if one split does not, or an
  *              explicit count).  Concurrent calls must not share a workspace.
- * Scores, probabilities and sums are float32.
+ * With a float32 output everything is float32.  A bf16 output is computed on
+ * the tensor cores: cached keys enter the products exactly, rotated queries as
+ * a sum of two fp16 values (2^-22), so scores and lse have float32 accuracy
+ * (relative 1e-6, the tensor cores' sums being cut off rather than rounded);
+ * probabilities, value rows and, for many rows, the merged rows and R_V in the
+ * un-rotation are rounded to fp16 (relative 2^-12 each).  OSCAR_DEV_TIMEOUT in
+ * dev_status: a bounded wait inside a kernel ran out and out is not valid.
  * n_new = 0 does nothing; n_new > capacity is OSCAR_ERR_CAPACITY.
  */
 int attn_extend_workspace_query(const oscar_kv_config* cfg, int32_t n_new, uint64_t* bytes);

@@ -7,7 +7,8 @@
 // rows' maxima, sums and outputs in registers.  Eight threads share a row: each
 // takes every eighth position of the scores and D / 8 channels of the output.
 // What bounds it: shared-memory reads (one 16-byte read per four FMAs in
-// P V, five per sixteen in Q K^T).
+// P V, five per sixteen in Q K^T).  No size of it has been made fast: it is
+// there for its precision.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

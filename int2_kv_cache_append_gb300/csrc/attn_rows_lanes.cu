@@ -9,9 +9,10 @@
 //   S [128 rows x 128 tokens] = Q K^T,   O [128 rows x 128 channels] += P V
 //
 // The arithmetic is that of the token-lane kernel (attn_rows_tc.cu): INT2 keys
-// as exact fp16 values and a rank-one term, queries as two fp16 values, value rows with an exponent of their own that joins the
-// score.  A row's reference M follows its maximum only when that has grown by
-// 2^12 (P is fp16), and then its warps rescale their rows of O.
+// as exact fp16 values and a rank-one term, queries as two fp16 values, value
+// rows with an exponent of their own that joins the score.  A row's reference M
+// follows its maximum only when that has grown by 2^12 (P is fp16), and then its
+// warps rescale their rows of O.
 //
 // Eight softmax warps: warp w has rows 32 (w mod 4) .. + 31 and the tokens of
 // half w / 4; the two threads of a row exchange their maxima once per tile.  Two
@@ -20,6 +21,14 @@
 // overwrites the scores that it was made from.  In shared memory they would
 // take 96 KB of reads per tile from a budget (128 bytes per clock) that K, V
 // and their expansion already use.
+//
+// What bounds it: the hand-overs from the products to the softmax to the next
+// products, and beside them the V expanders, busy all the time.  A tile takes
+// about 2850 cycles, of which the tensor cores need 1600; without the expansion,
+// or without the softmax, it would still take three quarters of that.  A chunk of 2048 tokens x 32
+// heads over 16,384 positions (4 sequences, 8 KV heads): 1.28 ms, 0.8 PFLOP/s
+// of products that the operator needs (the low part of Q doubles those of the
+// scores).
 #include <algorithm>
 
 #include "rows_tc.cuh"

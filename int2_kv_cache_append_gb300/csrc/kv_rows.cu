@@ -2,7 +2,9 @@
 // into the model's basis), the query rotation and the merge + un-rotation of the
 // row attention, float32 throughout.  X [rows x D] times R or R^T with a
 // different way of producing X and storing the result; kv_rows_tc.cu has the
-// form for many rows.
+// form for many rows.  What bounds it: the latency of reading R (kv_read of one
+// position: 8 us from launch to launch), with more rows the reads of R from the
+// L2 cache by every CTA.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

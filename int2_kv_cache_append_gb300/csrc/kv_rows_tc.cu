@@ -1,6 +1,6 @@
 // Products of many rows with a layer's rotation on the 5th-generation tensor
-// cores: kv_read, the query rotation and the merge + un-rotation of the row
-// attention for larger calls (kv_rows.cu has the float32 form).
+// cores: kv_read, the query rotation and the un-rotation of the merged rows for
+// larger calls (kv_rows.cu has the float32 form and the merge).
 //
 //   out [128 rows x NC columns] = X [128 x D] B^T,  B [NC x D] = rows of R (or of R^T)
 //
@@ -9,14 +9,22 @@
 // row tiles.  X is expanded to fp16 operands in units of 64 channels: cached
 // INT2 rows as s (c - 1) / 2 with the middles as a rank-one term (exact; see
 // expand_k), other rows scaled by a power of two per row, with a second set of
-// units for the rounding residues where the result is float32.  A bf16 result
-// takes one product, R and X rounded to fp16 (2^-12 each, against 2^-9 of the
-// output); a query from bf16 two; a float32 result two or three, 2^-22.
+// units for the rounding residues where the result is float32; merged rows are
+// such operands already.  A bf16 result takes one product, R and X rounded to
+// fp16 (2^-12 each, against 2^-9 of the output); a query from bf16 two; a
+// float32 result two or three, 2^-22.
 //
 // Two groups of four warps expand alternate tiles, one warp issues the
-// products, four warps scale and store the result of the previous tile: per
-// tile, 512 (one product) to 1536 tensor cycles, the expansion and the stores
-// overlap.  Every wait is bounded, as in the attention kernels.
+// products, four warps scale and store the result of the previous tile.
+//
+// What bounds it: at D = 128 the expansion and the stores (kv_read of 4 x 8192
+// positions, 8 KV heads: 66 us, 2.4 TB/s, a third of the copy rate).  At larger
+// D a row is expanded again for every NC columns, up to 8 times at D = 512, and
+// the latency of BF16 rows counts, which are read once more for their largest
+// value: 4 x 4099 positions at D = 512 take 220 us as INT2 rows into bf16, 500
+// us into float32 and 1.04 ms with 2560 BF16 rows among them.  Reading those
+// rows by whole warps, line by line, was slower (1.33 ms).  Every wait is
+// bounded, as in the attention kernels.
 #include <algorithm>
 
 #include "rows_tc.cuh"

@@ -466,7 +466,8 @@ int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const osca
   const int want = num_splits > 0 ? num_splits : splits_of(cfg, pg, int64_t(g.B) * g.G, hint);
   // the own caches' part has to fit with one split at least; what is left goes to the prefix
   const bool own_by_rows = own_hint <= kOwnRows;
-  const int want2 = own_by_rows ? splits_of(cfg, g, g.G, own_hint) : 0;
+  // not more than the workspace query counts with, whatever the hint
+  const int want2 = own_by_rows ? std::min(splits_of(cfg, g, g.G, own_hint), splits_of(cfg, g, g.G, std::min(g.cap, kOwnRows))) : 0;
   const uint64_t own = own_by_rows ? own_rows_workspace(g, want2) : own_workspace(g) + oscar::decode_workspace_bytes(g, 1);
   const int ns =
       workspace_bytes < own ? 0 : fit_splits(pg, rows, want, num_splits > 0, workspace_bytes - own);
