@@ -1,6 +1,6 @@
 // Attention of blocks of query rows over one cache on the 5th-generation tensor
 // cores, head_dim 128, query rows in the TMEM lanes: the kernel behind
-// attn_extend and attn_decode_prefix for a bf16 output and more than 64 query
+// attn_extend and attn_decode_prefix for a bf16 output and more than 32 query
 // rows per (sequence, KV head).
 //
 // A CTA holds 128 rotated query rows and walks its share of the positions 128 at

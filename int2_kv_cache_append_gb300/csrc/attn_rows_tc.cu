@@ -513,12 +513,13 @@ int launch(const RowsArgs& a, cudaStream_t stream) {
   return row_launch(true, attn_rows_tc_kernel<DG, N>, dim3(unsigned(items)), kThreads, Plan<DG, N>::kBytes, stream, a);
 }
 
-// Query rows per CTA.  The columns of a tile cost little beside its expansion, so a CTA takes all rows of a unit up to 64.
-// More than 64 rows go to the row-lane kernel where its accumulators fit TMEM: 32 sequences x 8 heads a KV head on one
-// prefix of 65,536 positions took 522 us there and 785 us here, four CTAs expanding the same keys.
+// Query rows per CTA: the least of 32, 64 (D > 128) or 128 that holds a unit's rows, because a CTA with more columns costs
+// little more and the keys are expanded once.  D = 128 with more than 32 rows goes to the row-lane kernel; us a call here
+// with 64 rows a CTA and there: 8 sequences x 9 / 12 / 16 tokens x 4 heads a KV head (36 / 48 / 64 rows) over 4096 positions
+// 71 / 83 / 87 and 60 / 69 / 75, 512 rows on one prefix of 131,072 positions 808 and 450.  32 rows: 62 here, 69 with 64.
 int tile_rows(int D, int64_t rows) {
   if (rows <= 32) return 32;
-  return rows <= 64 || D > 128 ? 64 : 128;
+  return D > 128 ? 64 : 128;
 }
 
 }  // namespace
@@ -552,7 +553,7 @@ int rows_splits_tc(const Geom& g, int64_t rows, int seq_len_hint) {
 int launch_attn_rows_tc(const RowsArgs& a, cudaStream_t stream) {
   const int N = tile_rows(a.g.D, int64_t(a.n) * a.g.G);
   if (N == 128) return launch_attn_rows_lanes(a, stream);
-  if (a.g.D == 128) return N == 32 ? launch<1, 32>(a, stream) : launch<1, 64>(a, stream);
+  if (a.g.D == 128) return launch<1, 32>(a, stream);
   if (a.g.D == 256) return N == 32 ? launch<2, 32>(a, stream) : launch<2, 64>(a, stream);
   return N == 32 ? launch<4, 32>(a, stream) : launch<4, 64>(a, stream);
 }

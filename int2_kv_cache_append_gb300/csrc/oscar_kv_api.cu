@@ -273,9 +273,17 @@ int validate_prefix(const oscar_kv_config* cfg, const oscar_kv_config* pcfg) {
   return rows_supported(make_geom(pcfg), cfg->batch) ? OSCAR_OK : OSCAR_ERR_UNSUPPORTED;
 }
 
-// Longest own cache that attn_decode_prefix gives to the row attention; longer
-// ones go to attn_decode's kernels.
-constexpr int kOwnRows = 1024;
+// Longest own cache that attn_decode_prefix gives to the row attention, which
+// runs beside the prefix's; longer ones go to attn_decode's kernels, which take
+// about 20 us more to begin with and less per position.  Row attention against
+// those, us a call: 8 sequences x 8 KV heads with 64 / 512 positions 36 / 48
+// against 54 / 56, 32 x 8 with 64 / 256 / 512 / 1024 62 / 75 / 85 / 95 against
+// 65 / 71 / 73 / 77, at D = 512 with 64 / 256 / 512 153 / 222 / 257 against
+// 208 / 230 / 239.
+constexpr int kOwnRows = 1024, kOwnTiles = 512;  // positions; tiles of 128 in all
+int own_rows_limit(const Geom& g) {
+  return int(std::min<int64_t>(kOwnRows, kOwnTiles / (int64_t(g.B) * g.Hkv) * 128));
+}
 
 // Workspace of attn_decode_prefix apart from the prefix's row attention: the own
 // caches' partial results, or attn_decode's outputs, lse and status word.
@@ -437,7 +445,7 @@ int attn_decode_prefix_workspace_query(const oscar_kv_config* cfg, const oscar_k
   const Geom g = make_geom(cfg), pg = make_geom(prefix_cfg);
   *bytes = rows_workspace(pg, int64_t(g.B) * g.Hq, OSCAR_KV_MAX_SPLITS) +
            std::max(own_rows_workspace(g, splits_of(cfg, g, g.G, std::min(g.cap, kOwnRows))),
-                    g.cap > kOwnRows ? own_workspace(g) + oscar::decode_workspace_bytes(g, OSCAR_KV_MAX_SPLITS) : 0);
+                    g.cap > own_rows_limit(g) ? own_workspace(g) + oscar::decode_workspace_bytes(g, OSCAR_KV_MAX_SPLITS) : 0);
   return OSCAR_OK;
 }
 
@@ -465,7 +473,7 @@ int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const osca
   const int own_hint = seq_len_hint > 0 ? seq_len_hint : cfg->capacity;
   const int want = num_splits > 0 ? num_splits : splits_of(cfg, pg, int64_t(g.B) * g.G, hint);
   // the own caches' part has to fit with one split at least; what is left goes to the prefix
-  const bool own_by_rows = own_hint <= kOwnRows;
+  const bool own_by_rows = own_hint <= own_rows_limit(g);
   // not more than the workspace query counts with, whatever the hint
   const int want2 = own_by_rows ? std::min(splits_of(cfg, g, g.G, own_hint), splits_of(cfg, g, g.G, std::min(g.cap, kOwnRows))) : 0;
   const uint64_t own = own_by_rows ? own_rows_workspace(g, want2) : own_workspace(g) + oscar::decode_workspace_bytes(g, 1);
