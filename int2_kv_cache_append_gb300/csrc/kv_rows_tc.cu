@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c0 = blockIdx.y * NC, role = blockIdx.z;
+  const int c0 = blockIdx.y * NC;
+  const int role = SRC == kRead && !a.r.k_out ? 1 : blockIdx.z;  // of kv_read: K, V, or the one that is asked for
   const Geom& g = a.r.g;
   const float* R = SRC == kQuery ? a.q.R_K : SRC == kFinish ? a.f.R_V : role ? a.r.R_V : a.r.R_K;
   const bool hadamard = SRC == kQuery ? a.q.hadamard : SRC == kFinish ? a.f.hadamard : a.r.hadamard;
@@ -100,7 +101,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
   const bool out32 = SRC == kQuery || (SRC == kFinish ? a.f.out_fp32 : a.r.out_fp32);
   int32_t* status = SRC == kQuery ? a.q.status : SRC == kFinish ? a.f.status : a.r.status;
   const int64_t rows = SRC == kQuery ? a.q.rows : SRC == kFinish ? a.f.rows : int64_t(g.B) * a.r.n * g.Hkv;
-  if (!out) return;
   if (SRC == kQuery) pdl_trigger();
 
   float* factor = reinterpret_cast<float*>(sm + L::oRow);      // [kAcc][128]
@@ -537,7 +537,8 @@ int launch_read_tc(const ReadArgs& r, cudaStream_t stream) {
   a.div_hkv = fastdiv_make(uint32_t(r.g.Hkv));
   a.div_n = fastdiv_make(uint32_t(r.n));
   const int64_t rows = int64_t(r.g.B) * r.n * r.g.Hkv;
-  return r.out_fp32 ? launch_dim<kRead, true>(a, r.g.D, rows, 2, stream) : launch_dim<kRead, false>(a, r.g.D, rows, 2, stream);
+  const int roles = r.k_out && r.v_out ? 2 : 1;
+  return r.out_fp32 ? launch_dim<kRead, true>(a, r.g.D, rows, roles, stream) : launch_dim<kRead, false>(a, r.g.D, rows, roles, stream);
 }
 int launch_qrot_rows_tc(const QrotRowsArgs& q, cudaStream_t stream) {
   MmArgs a{};

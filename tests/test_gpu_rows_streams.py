@@ -172,3 +172,24 @@ def test_append_extend_read_on_a_side_stream(n):
         assert all(torch.equal(a, b) for a, b in zip(res[0], r))
     err = (res[0][1].float() - k.float()).norm() / k.float().norm()
     assert np.isfinite(float(err)) and float(err) < 0.8  # 2-bit rows and BF16 ones: it is these tokens that came back
+
+
+@pytest.mark.parametrize("n", [3, 1500])
+@pytest.mark.parametrize("fp32", [False, True], ids=["bf16", "fp32"])
+def test_read_of_one_role(n, fp32):
+    """Either role alone gives the bits that it has beside the other."""
+    c = cfg_of(128, 2, 8, 2, 4, 40, 1600, K.FLAG_OUT_FP32 if fp32 else 0)
+    cache, RK, RV, _, _ = filled(c, [1600, 1510], 11)
+    kc, R = kcfg(c), (dev_rot(RK), dev_rot(RV))
+    cache, pos, sl = torch.from_numpy(cache).cuda(), dev_i32([100, 10]), dev_i32([1600, 1510])
+
+    def empty():
+        return torch.zeros(2, n, 2, 128, dtype=torch.float32 if fp32 else torch.bfloat16, device="cuda")
+
+    k, v, k1, v1 = empty(), empty(), empty(), empty()
+    K.kv_read(kc, cache, 0, pos, sl, *R, k_out=k, v_out=v)
+    K.kv_read(kc, cache, 0, pos, sl, *R, k_out=k1)
+    K.kv_read(kc, cache, 0, pos, sl, *R, v_out=v1)
+    torch.cuda.synchronize()
+    assert torch.equal(k, k1) and torch.equal(v, v1)
+    assert not torch.equal(k, v) and float(k.abs().sum()) > 0
