@@ -120,9 +120,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
                  p_done = p_full + 8, q_full = p_done + 8, f_full = q_full + 8, drained = f_full + 8;
   uint32_t* words = reinterpret_cast<uint32_t*>(sm + oBar + kBars * 8);
   uint32_t* tmem_slot = words;
-  volatile uint32_t* abort_flag = words + 1;
-  uint32_t* qmax = words + 2;
-  float* scale_f = reinterpret_cast<float*>(words + 3);
+  uint32_t* qmax = words + 1;
+  float* scale_f = reinterpret_cast<float*>(words + 2);
 
   for (int c = threadIdx.x; c < N; c += kThreads) {
     const int row = rt * N + c, t = row / g.G;
@@ -145,8 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     mbar_init(f_full, kSoftWarps);
     mbar_init(drained, 1);
     mbar_fence_init();
-    words[1] = 0;
-    words[2] = 0;
+    *qmax = 0;
   }
   if (warp == kSoftWarps + 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
@@ -159,7 +157,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
   if (!a.beside) pdl_wait();  // the queries
   if (a.early) pdl_trigger();
   auto fail = [&]() {
-    *abort_flag = 1;
     status_or(a.status, OSCAR_DEV_TIMEOUT);
   };
   auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity); };
@@ -364,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       fail();
     }
   } else if (warp < kSoftWarps + 8) {
-    Share x{&a, u, T, p0, p1, nt, sm, base, abort_flag, scale_f, f_full, k_full, k_empty, v_full, v_empty, c_full, c_empty,
+    Share x{&a, u, T, p0, p1, nt, sm, base, scale_f, f_full, k_full, k_empty, v_full, v_empty, c_full, c_empty,
             oK, oV, oRawK, oRawV, oConst, oRank, oRow + 5 * N * 4};
     const int tok = threadIdx.x - kSoftWarps * 32;
     const bool ok = warp < kSoftWarps + 4 ? (g.lm ? expand_k<1, KU, CB, kStages, 4, true>(x, tok, lane) : expand_k<1, KU, CB, kStages, 4, false>(x, tok, lane))

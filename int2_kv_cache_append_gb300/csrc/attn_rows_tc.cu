@@ -55,7 +55,6 @@ constexpr int kSoftWarps = 8;
 constexpr int kThreads = (kSoftWarps + 4 + 4 + 1) * 32;
 constexpr float kNone = -1e30f;        // M before the first tile
 constexpr float kTop = 15.f;           // largest t = u - M that P holds (fp16 below 2^16)
-constexpr float kRoom = 0.f;           // a new M lies this far below the maximum
 
 // Shared memory and TMEM of one instantiation.
 template <int DG, int N>
@@ -145,9 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
   const uint32_t q_full = bar + 8u * (b2 + 2 * L::CB), f_full = q_full + 8, drained = f_full + 8;
   uint32_t* words = reinterpret_cast<uint32_t*>(sm + L::oBar + L::kBars * 8);
   uint32_t* tmem_slot = words;
-  volatile uint32_t* abort_flag = words + 1;
-  uint32_t* qmax = words + 2;
-  float* scale_f = reinterpret_cast<float*>(words + 3);
+  uint32_t* qmax = words + 1;
+  float* scale_f = reinterpret_cast<float*>(words + 2);
 
   for (int c = threadIdx.x; c < N; c += kThreads) {
     const int row = rt * N + c, t = row / g.G;
@@ -171,8 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     mbar_init(f_full, kSoftWarps);
     mbar_init(drained, 1);
     mbar_fence_init();
-    words[1] = 0;
-    words[2] = 0;
+    *qmax = 0;
   }
   if (warp == kSoftWarps + 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
@@ -185,7 +182,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
   if (!a.beside) pdl_wait();  // the queries
   if (a.early) pdl_trigger();
   auto fail = [&]() {
-    *abort_flag = 1;
     status_or(a.status, OSCAR_DEV_TIMEOUT);
   };
   auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity); };
@@ -302,8 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
           const float M = -negM[c0 + tok];
           float f = 1.f;
           if (mx - M > kTop) {
-            f = exp2f(M - (mx - kRoom));
-            negM[c0 + tok] = kRoom - mx;
+            f = exp2f(M - mx);
+            negM[c0 + tok] = -mx;
           }
           factor[c0 + tok] = f;
         }
@@ -401,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
       fail();
     }
   } else if (warp < kSoftWarps + 8) {
-    Share x{&a, u, T, p0, p1, nt, sm, base, abort_flag, scale_f, f_full, k_full(0), k_empty(0), v_full(0), v_empty(0),
+    Share x{&a, u, T, p0, p1, nt, sm, base, scale_f, f_full, k_full(0), k_empty(0), v_full(0), v_empty(0),
             c_full(0), c_empty(0), L::oK, L::oV, L::oRawK, L::oRawV, L::oConst, L::oRank,
             L::oRow + L::kRow - 64};
     const int tok = threadIdx.x - kSoftWarps * 32;

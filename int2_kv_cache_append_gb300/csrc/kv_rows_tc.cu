@@ -111,7 +111,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
   const uint32_t f_full = bar + 32u * PU, acc_full = f_full + 8 * kAcc, acc_empty = acc_full + 8 * kAcc, drained = acc_empty + 8 * kAcc;
   uint32_t* words = reinterpret_cast<uint32_t*>(sm + L::oBar + L::kBars * 8);
   uint32_t* tmem_slot = words;
-  volatile uint32_t* abort_flag = words + 1;
 
   if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) {
     if (SRC == kQuery && a.q.zero_word) *a.q.zero_word = 0;
@@ -126,7 +125,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
     }
     mbar_init(drained, 1);
     mbar_fence_init();
-    words[1] = 0;
   }
   if (warp == kExpandWarps + kStoreWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "n"(kCols)
@@ -186,7 +184,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
   const uint32_t tmem = *tmem_slot;
   if (SRC == kFinish) pdl_wait();  // the merged rows
   auto fail = [&]() {
-    *abort_flag = 1;
     status_or(status, OSCAR_DEV_TIMEOUT);
   };
   auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity); };
