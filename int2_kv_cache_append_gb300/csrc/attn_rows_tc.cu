@@ -83,8 +83,8 @@ struct Plan {
   static constexpr int kBars = 2 * KU + 2 * VU + 2 * SB + 2 * PB + 2 * CB + 3;
   static constexpr int kBytes = oBar + kBars * 8 + 32 + 1024;  // + alignment slack
   // The tensor cores cut each of their sums' additions off (towards zero).  At D = 512 a score would be 65 additions and
-  // 1e-6 too small, so two accumulators share them.
-  static constexpr int kParts = DG == 4 ? 2 : 1;
+  // 1e-6 too small, so at D = 256 and 512 two accumulators share them.
+  static constexpr int kParts = DG > 1 ? 2 : 1;
   static constexpr int cS = 0;                                // TMEM columns of the scores
   static constexpr int cO = SB * kParts * N;                  // and of O^T
   static_assert(cO + DG * N <= 512, "TMEM");
@@ -442,7 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
           fence_after();
           const uint32_t x = dK + kr.at * (kUnit >> 4);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma_f16_ss(d, x + 2 * j, q + 2 * j, id_qk, 1, leader);
+          for (int j = 0; j < 4; ++j)
+            mma_f16_ss(L::kParts == 2 && kb < DG ? d + N : d, x + 2 * j, q + 2 * j, id_qk, 1, leader);
           mma_commit(k_empty(kr.at), leader);
           kr.next();
         }
