@@ -165,7 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     // ------------------------------- softmax ---------------------------------
     const int half = warp >> 2, row = threadIdx.x & 127;     // the thread's tokens of a tile and row (TMEM lane)
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;  // the warp's TMEM lanes
-    // Q: this thread's 64 channels of its row, scaled (query_exponent) and split into two fp16 parts
+    // Q: this thread's 64 channels of its row, scaled (query_exponent) and split into two fp16 parts.  Plain loads: the
+    // rotation may still be writing when this kernel starts (row_launch).
     {
       const int r = outr[row];
       const float4* src = reinterpret_cast<const float4*>(a.qrot + int64_t(max(r, 0)) * D + 64 * half);
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       if (r >= 0) {
 #pragma unroll 8
         for (int j = 0; j < 16; ++j) {
-          const float4 v = __ldg(src + j);
+          const float4 v = src[j];
           const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (r >= 0) v = __ldg(src + 8 * c + j);
+          if (r >= 0) v = src[8 * c + j];
           sum += split_pair(v.x * inv, v.y * inv, hi[2 * j], lo[2 * j]);
           sum += split_pair(v.z * inv, v.w * inv, hi[2 * j + 1], lo[2 * j + 1]);
         }

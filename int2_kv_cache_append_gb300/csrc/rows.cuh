@@ -11,7 +11,9 @@ constexpr int kSplitUnit = 128;  // positions: the shares of a split cache start
 
 // Launch after the kernel before it in the stream; dependent: it may start once every block of that one has called
 // pdl_trigger or ended, and waits (pdl_wait) before it reads what that one or an earlier one wrote.  Every block of a
-// kernel that is launched so waits before it ends, so that "complete" holds for everything before it, too.
+// kernel that is launched so waits before it ends, so that "complete" holds for everything before it, too.  What an earlier
+// kernel of the same call writes (rotated queries, partial results, merged rows) is read by plain loads: __ldg promises
+// memory that nobody writes while the kernel runs, and its loads may be moved above pdl_wait.
 template <class... P>
 int row_launch(bool dependent, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, P... args) {
   cudaLaunchAttribute attr[1];
