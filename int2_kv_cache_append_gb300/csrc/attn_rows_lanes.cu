@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
   const int ql = row_q_len(a, b);
   const int t_first = rt * N / g.G;
   if (t_first >= ql) {  // only padding
-    pdl_wait();
+    rows_wait(a);
     return;
   }
   const int t_last = min((rt * N + N - 1) / g.G, ql - 1);
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     if (nt <= 0 && live) *reinterpret_cast<float2*>(a.ml + (int64_t(outr[c]) * a.ns + s) * 2) = make_float2(kNone, 0.f);
   }
   if (nt <= 0) {  // nothing visible in this share
-    pdl_wait();
+    rows_wait(a);
     return;
   }
   if (threadIdx.x == 0) {
@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     mbar_init(drained, 1);
     mbar_fence_init();
     *qmax = 0;
+    if (a.beside && !ready_wait(a.ready)) status_or(a.status, OSCAR_DEV_TIMEOUT);  // the queries
   }
   if (warp == kSoftWarps + 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (!a.beside) pdl_wait();  // the queries
+  if (!a.beside) rows_wait(a);  // the queries
   if (a.early) pdl_trigger();
   auto fail = [&]() {
     status_or(a.status, OSCAR_DEV_TIMEOUT);

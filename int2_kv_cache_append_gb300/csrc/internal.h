@@ -123,9 +123,12 @@ struct RowsArgs {
   int n, ns;
   int causal;               // token t sees positions <= seq_len - q_len + t; else every position
   // Within a call the kernels follow each other by programmatic dependent launch (row_launch).  early: the next kernel may
-  // start with this one's last blocks; beside: this kernel reads nothing of the one before it, which has itself waited for
-  // the queries, and waits for it only at its own end.
+  // start with this one's last blocks; beside: this kernel reads nothing of the one before it and waits for it only at its
+  // own end.  The queries come from the kernel before that one, and only a thread that has waited is promised to see them:
+  // so the one before, once it has waited, releases *ready (0 until then), and the beside one acquires it.  What was
+  // complete when the call's first kernel started (cache, lengths) is taken to be visible to all of them.
   int early, beside;
+  int32_t* ready;  // a word of the workspace, or NULL
 };
 int launch_attn_rows(const RowsArgs& a, cudaStream_t stream);
 int launch_attn_rows_tc(const RowsArgs& a, cudaStream_t stream);  // fp16 products (attn_rows_tc.cu)

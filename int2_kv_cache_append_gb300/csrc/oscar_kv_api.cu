@@ -286,10 +286,11 @@ int own_rows_limit(const Geom& g) {
 }
 
 // Workspace of attn_decode_prefix apart from the prefix's row attention: the own
-// caches' partial results, or attn_decode's outputs, lse and status word.
+// caches' partial results and a word that says that the queries are there, or
+// attn_decode's outputs, lse and status word.
 uint64_t own_rows_workspace(const Geom& g, int ns) {
   const uint64_t bq = uint64_t(g.B) * g.Hq;
-  return oscar::align256(bq * ns * g.D * 4) + oscar::align256(bq * ns * 8);
+  return oscar::align256(bq * ns * g.D * 4) + oscar::align256(bq * ns * 8) + 256;
 }
 uint64_t own_workspace(const Geom& g) {
   const uint64_t bq = uint64_t(g.B) * g.Hq;
@@ -487,6 +488,7 @@ int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const osca
             &p);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (own_by_rows) {
+    p.at.ready = p.q.zero_word = take<int32_t>(&ws, 256);
     oscar::RowsArgs own_at = p.at;
     own_at.g = g;
     own_at.layer_base = static_cast<const uint8_t*>(cache) + uint64_t(layer) * g.layer_bytes;

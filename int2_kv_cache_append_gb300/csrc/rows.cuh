@@ -29,6 +29,24 @@ int row_launch(bool dependent, void (*kernel)(P...), dim3 grid, int threads, siz
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
 }
 
+// A row attention's wait for the kernels before it (RowsArgs::ready).
+__device__ __forceinline__ void rows_wait(const RowsArgs& a) {
+  pdl_wait();
+  if (a.ready && !a.beside && blockIdx.x == 0 && threadIdx.x == 0)
+    asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(a.ready) : "memory");
+}
+// One thread's bounded wait for *ready, a barrier before the others read the queries: the store has been made, or will be by
+// a block that is running, when a kernel starts beside.
+__device__ __forceinline__ bool ready_wait(const int32_t* ready, uint64_t limit_ns = 2000000000ull) {
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    int32_t x;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(ready) : "memory");
+    if (x) return true;
+    if (global_timer_ns() - t0 > limit_ns) return false;
+  }
+}
+
 // Length of sequence b in the cache that is read, clamped to the capacity;
 // `report`: this thread flags a length above it.
 __device__ __forceinline__ int row_seq_len(const RowsArgs& a, int b, bool report) {

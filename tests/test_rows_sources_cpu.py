@@ -21,3 +21,12 @@ def test_attention_reads_the_calls_own_results_by_plain_loads(name):
     assert "qrot" in code or "load_queries" in code
     assert "__ldg" not in code
 
+
+
+@pytest.mark.parametrize("name,first_read", [("attn_rows_tc.cu", "load_queries<"), ("attn_rows_lanes.cu", "a.qrot")])
+def test_attention_beside_its_predecessor_acquires_the_queries(name, first_read):
+    """The kernel that does not wait for the one before it takes the queries
+    from that one's release, with a barrier behind it, before it reads them."""
+    code = _code(name)
+    acquire = code.index("a.beside && !ready_wait(a.ready)")
+    assert acquire < code.index("__syncthreads()") < code.index(first_read)
