@@ -430,7 +430,13 @@ int oscar_kv_decode_kernels(const oscar_kv_config* cfg);
  * makes the first copy issued by CTA 0 expect `extra_bytes` more than its copies
  * deliver, so that its barrier never completes and the bounded wait runs out;
  * every copy still completes.  (0, 0) restores normal operation.  A decode run
- * with extra_bytes > 0 leaves at least one output unit unwritten.  Returns
+ * with extra_bytes > 0 leaves at least one output unit unwritten.  The same
+ * goes for the tensor-core kernels of kv_read, attn_extend and
+ * attn_decode_prefix: with extra_bytes > 0 the first barrier behind the products
+ * (of CTA 0 in kv_read and the rotations, of every CTA in the attentions)
+ * expects an arrival that never comes, and the kernel waits (bounded) for the
+ * products and copies it issued and frees its tensor memory before it returns.
+ * Returns
  * OSCAR_ERR_INVALID for wait_ns > 10 s or extra_bytes outside [0, 2^20].
  */
 int oscar_kv_set_wait_test(uint64_t wait_ns, int32_t extra_bytes);

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     for (int i = 0; i < KU; ++i) mbar_init(k_full + 8 * i, 4), mbar_init(k_empty + 8 * i, 1);
     for (int i = 0; i < VU; ++i) mbar_init(v_full + 8 * i, 4), mbar_init(v_empty + 8 * i, 1);
     for (int i = 0; i < CB; ++i) mbar_init(c_full + 8 * i, 8), mbar_init(c_empty + 8 * i, kSoftWarps);
-    for (int i = 0; i < 2; ++i) mbar_init(s_full + 8 * i, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(s_full + 8 * i, 1 + (i == 0 && a.wait_poison > 0));
     mbar_init(p_full, kSoftWarps);
     mbar_init(p_done, 1);
     mbar_init(q_full, kSoftWarps);
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     mbar_init(drained, 1);
     mbar_fence_init();
     *qmax = 0;
-    if (a.beside && !ready_wait(a.ready)) status_or(a.status, OSCAR_DEV_TIMEOUT);  // the queries
+    if (a.beside && !ready_wait(a.ready, a.wait_turns * 1000ull)) status_or(a.status, OSCAR_DEV_TIMEOUT);  // the queries
   }
   if (warp == kSoftWarps + 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
   auto fail = [&]() {
     status_or(a.status, OSCAR_DEV_TIMEOUT);
   };
-  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity); };
+  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity, a.wait_turns); };
 
   if (warp < kSoftWarps) {
     // ------------------------------- softmax ---------------------------------
@@ -368,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     const int tok = threadIdx.x - kSoftWarps * 32;
     const bool ok = warp < kSoftWarps + 4 ? (g.lm ? expand_k<1, KU, CB, kStages, 4, true>(x, tok, lane) : expand_k<1, KU, CB, kStages, 4, false>(x, tok, lane))
                                           : (g.lm ? expand_v<1, VU, CB, kStages, 4, true>(x, warp & 3, lane) : expand_v<1, VU, CB, kStages, 4, false>(x, warp & 3, lane));
+    cp_async_wait<0>();  // also where a wait ran out
     if (!ok && lane == 0) fail();
   } else {
     // ------------------------------ MMA issuer --------------------------------
@@ -376,14 +377,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     const uint32_t leader = elect_one();
     constexpr uint32_t id_qk = idesc_of(kTok, false, false), id_pv = idesc_of(D, false, true);
     const uint32_t dK = desc_of(base + oK, 16), dV = desc_of(base + oV, kUnit / 2), dRank = rank_desc(base + oRank);
-    bool ok = true;
+    Waits waits{a.wait_turns};
     Ring<KU> kr;
     Ring<VU> vr;
     auto product_qk = [&](uint32_t odd) {
       const uint32_t d = cS + odd * 128;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        ok = poll(k_full + 8 * kr.at, kr.phase) && ok;
+        waits.on(k_full + 8 * kr.at, kr.phase);
         fence_after();
         const uint32_t k = dK + kr.at * (kUnit >> 4);
 #pragma unroll
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
         mma_commit(k_empty + 8 * kr.at, leader);
         kr.next();
         if (g.lm) {
-          ok = poll(k_full + 8 * kr.at, kr.phase) && ok;
+          waits.on(k_full + 8 * kr.at, kr.phase);
           fence_after();
           const uint32_t x = dK + kr.at * (kUnit >> 4);
 #pragma unroll
@@ -405,10 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       mma_commit(s_full + 8 * odd, leader);
     };
     auto product_pv = [&](uint32_t odd, uint32_t acc) {
-      ok = poll(p_full, odd) && ok;
+      waits.on(p_full, odd);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        ok = poll(v_full + 8 * vr.at, vr.phase) && ok;
+        waits.on(v_full + 8 * vr.at, vr.phase);
         fence_after();
         const uint32_t v = dV + vr.at * (kUnit >> 4);
         const uint32_t p = cS + odd * 128 + 64 * k;  // 64 tokens of P in 32 columns
@@ -419,23 +420,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       }
       mma_commit(p_done, leader);
     };
-    ok = poll(q_full, 0) && tmem == 0;  // all of TMEM: column addresses are constants
+    waits.on(q_full, 0);
+    waits.ok &= tmem == 0;  // all of TMEM: column addresses are constants
     fence_after();
-    if (__all_sync(0xffffffffu, ok)) {
+    if (__all_sync(0xffffffffu, waits.ok)) {
       product_qk(0);
       if (nt > 1) product_qk(1);
     }
 #pragma unroll 1
     for (int i = 0; i < nt; ++i) {
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!__all_sync(0xffffffffu, waits.ok)) break;
       product_pv(i & 1, i > 0);
       if (i + 2 < nt) {
-        ok = poll(p_done, i & 1) && ok;  // the scores of tile i + 2 overwrite P
+        waits.on(p_done, i & 1);  // the scores of tile i + 2 overwrite P
         fence_after();
         product_qk(i & 1);
       }
     }
-    ok = __all_sync(0xffffffffu, ok);
+    const bool ok = __all_sync(0xffffffffu, waits.ok);
     if (!ok && lane == 0) fail();
     mma_commit(drained, leader);  // every product issued is complete before TMEM is freed
     mbar_wait(drained, 0);

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::KU; ++i) mbar_init(k_full(i), 4), mbar_init(k_empty(i), 1);
     for (int i = 0; i < L::VU; ++i) mbar_init(v_full(i), 4), mbar_init(v_empty(i), 1);
-    for (int i = 0; i < L::SB; ++i) mbar_init(s_full(i), 1), mbar_init(s_empty(i), kSoftWarps);
+    for (int i = 0; i < L::SB; ++i) mbar_init(s_full(i), 1 + (i == 0 && a.wait_poison > 0)), mbar_init(s_empty(i), kSoftWarps);
     for (int i = 0; i < L::PB; ++i) mbar_init(p_full(i), kSoftWarps), mbar_init(p_empty(i), 1);
     for (int i = 0; i < L::CB; ++i) mbar_init(c_full(i), 8), mbar_init(c_empty(i), kSoftWarps);
     mbar_init(q_full, kSoftWarps);
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     mbar_init(drained, 1);
     mbar_fence_init();
     *qmax = 0;
-    if (a.beside && !ready_wait(a.ready)) status_or(a.status, OSCAR_DEV_TIMEOUT);  // the queries
+    if (a.beside && !ready_wait(a.ready, a.wait_turns * 1000ull)) status_or(a.status, OSCAR_DEV_TIMEOUT);  // the queries
   }
   if (warp == kSoftWarps + 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
   auto fail = [&]() {
     status_or(a.status, OSCAR_DEV_TIMEOUT);
   };
-  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity); };
+  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity, a.wait_turns); };
 
   if (warp < kSoftWarps) {
     // ------------------------------- softmax ---------------------------------
@@ -404,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     const int tok = threadIdx.x - kSoftWarps * 32;
     const bool ok = warp < kSoftWarps + 4 ? (g.lm ? expand_k<DG, L::KU, L::CB, L::kStages, 8, true>(x, tok, lane) : expand_k<DG, L::KU, L::CB, L::kStages, 8, false>(x, tok, lane))
                                           : (g.lm ? expand_v<DG, L::VU, L::CB, L::kStages, 8, true>(x, warp & 3, lane) : expand_v<DG, L::VU, L::CB, L::kStages, 8, false>(x, warp & 3, lane));
+    cp_async_wait<0>();  // also where a wait ran out
     if (!ok && lane == 0) fail();
   } else {
     // ------------------------------ MMA issuer --------------------------------
@@ -413,18 +414,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     constexpr uint32_t id_qk = idesc_of(N, false, false), id_pv = idesc_of(N, true, true);
     const uint32_t dQ = desc_of(base + L::oQ, 16), dK = desc_of(base + L::oK, 16), dV = desc_of(base + L::oV, kUnit / 2),
                    dP = desc_of(base + L::oP, kTok * 128), dRank = rank_desc(base + L::oRank);
-    bool ok = true;
+    Waits waits{a.wait_turns};
     Ring<L::KU> kr;
     Ring<L::VU> vr;
     Ring<L::SB> sr;
     Ring<L::PB> pr;
     uint32_t odd = 0;  // the tile's rank-one operand
     auto product_qk = [&](bool reuse) {
-      if (reuse) ok = poll(s_empty(sr.at), sr.phase ^ 1) && ok;
+      if (reuse) waits.on(s_empty(sr.at), sr.phase ^ 1);
       const uint32_t d = L::cS + sr.at * (L::kParts * N);
 #pragma unroll 1
       for (int kb = 0; kb < 2 * DG; ++kb) {
-        ok = poll(k_full(kr.at), kr.phase) && ok;
+        waits.on(k_full(kr.at), kr.phase);
         fence_after();
         const uint32_t k = dK + kr.at * (kUnit >> 4), q = dQ + kb * (N * 128 >> 4);
 #pragma unroll
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
         mma_commit(k_empty(kr.at), leader);
         kr.next();
         if (g.lm) {
-          ok = poll(k_full(kr.at), kr.phase) && ok;
+          waits.on(k_full(kr.at), kr.phase);
           fence_after();
           const uint32_t x = dK + kr.at * (kUnit >> 4);
 #pragma unroll
@@ -454,11 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
       odd ^= 1;
     };
     auto product_pv = [&](uint32_t acc) {
-      ok = poll(p_full(pr.at), pr.phase) && ok;
+      waits.on(p_full(pr.at), pr.phase);
       const uint32_t p = dP + pr.at * (L::kP >> 4);
 #pragma unroll 1
       for (int k = 0; k < 2 * DG; ++k) {  // group k / 2, token half k % 2
-        ok = poll(v_full(vr.at), vr.phase) && ok;
+        waits.on(v_full(vr.at), vr.phase);
         fence_after();
         const uint32_t v = dV + vr.at * (kUnit >> 4), half = k & 1;
 #pragma unroll
@@ -470,16 +471,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
       mma_commit(p_empty(pr.at), leader);
       pr.next();
     };
-    ok = poll(q_full, 0) && tmem == 0;  // all of TMEM: column addresses are constants
+    waits.on(q_full, 0);
+    waits.ok &= tmem == 0;  // all of TMEM: column addresses are constants
     fence_after();
-    if (__all_sync(0xffffffffu, ok)) product_qk(false);
+    if (__all_sync(0xffffffffu, waits.ok)) product_qk(false);
 #pragma unroll 1
     for (int i = 0; i < nt; ++i) {
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!__all_sync(0xffffffffu, waits.ok)) break;
       if (i + 1 < nt) product_qk(i + 1 >= L::SB);
       product_pv(i > 0);
     }
-    ok = __all_sync(0xffffffffu, ok);
+    const bool ok = __all_sync(0xffffffffu, waits.ok);
     if (!ok && lane == 0) fail();
     mma_commit(drained, leader);  // every product issued is complete before TMEM is freed
     mbar_wait(drained, 0);

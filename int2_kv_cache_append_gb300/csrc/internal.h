@@ -67,6 +67,8 @@ extern thread_local cudaEvent_t g_prof_start, g_prof_stop;
 // timeout-path test hook (per host thread): wait limit and extra expected bytes
 extern thread_local uint64_t g_test_wait_ns;
 extern thread_local int g_test_wait_poison;
+inline uint64_t wait_limit_ns() { return g_test_wait_ns > 0 ? g_test_wait_ns : 2000000000ull; }
+inline uint32_t wait_turns() { return uint32_t((wait_limit_ns() + 999) / 1000); }
 int launch_append(const AppendArgs& a, cudaStream_t stream);
 int launch_append_tc(const AppendArgs& a, cudaStream_t stream);  // D = 128, bf16 inputs
 // 2-D tiled TMA map of a row-major bf16 matrix [rows][cols], 128-byte swizzle
@@ -129,6 +131,8 @@ struct RowsArgs {
   // complete when the call's first kernel started (cache, lengths) is taken to be visible to all of them.
   int early, beside;
   int32_t* ready;  // a word of the workspace, or NULL
+  uint32_t wait_turns;  // limit of every barrier wait, a microsecond each at most
+  int wait_poison;   // test hook: above 0, the first score barrier expects an arrival that never comes
 };
 int launch_attn_rows(const RowsArgs& a, cudaStream_t stream);
 int launch_attn_rows_tc(const RowsArgs& a, cudaStream_t stream);  // fp16 products (attn_rows_tc.cu)

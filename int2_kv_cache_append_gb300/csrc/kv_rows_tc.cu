@@ -41,6 +41,8 @@ struct MmArgs {
   int64_t tiles;
   int xl;  // the rows' low parts take part
   FastDiv div_hkv, div_n;  // of kv_read
+  uint32_t wait_turns;     // limit of every barrier wait, a microsecond each at most
+  int wait_poison;         // test hook: above 0, CTA 0's first accumulator expects an arrival that never comes
 };
 
 // The matrix enters times this: elements of a rotation are below 1, most far below, and the low part of a small one would
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
       for (int i = 0; i < PU; ++i) mbar_init(x_full(p, i), 4), mbar_init(x_empty(p, i), 1);
     for (int p = 0; p < kAcc; ++p) {
       mbar_init(f_full + 8 * p, 4);
-      mbar_init(acc_full + 8 * p, 1);
+      mbar_init(acc_full + 8 * p, 1 + (p == 0 && blockIdx.x + blockIdx.y + blockIdx.z == 0 && a.wait_poison > 0));
       mbar_init(acc_empty + 8 * p, kStoreWarps);
     }
     mbar_init(drained, 1);
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
   auto fail = [&]() {
     status_or(status, OSCAR_DEV_TIMEOUT);
   };
-  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity); };
+  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity, a.wait_turns); };
   const int sets = a.xl ? 2 : 1;
   const int mine = int((a.tiles - blockIdx.x + gridDim.x - 1) / gridDim.x);  // this CTA's tiles
 
@@ -514,6 +516,8 @@ int launch(MmArgs& a, int64_t rows, int roles, cudaStream_t stream) {
     sms[dev] = n;
   }
   a.tiles = (rows + 127) / 128;
+  a.wait_turns = wait_turns();
+  a.wait_poison = g_test_wait_poison;
   const int chunks = DG * 128 / Plan<DG, RL>::NC;
   const int per = int(std::min<int64_t>(a.tiles, std::max(1, sms[dev] / (chunks * roles))));
   return row_launch(SRC == kFinish, rows_mm_kernel<SRC, DG, RL>, dim3(per, chunks, roles), kThreads, Plan<DG, RL>::kBytes, stream, a);

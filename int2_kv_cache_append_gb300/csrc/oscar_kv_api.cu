@@ -166,7 +166,7 @@ int prep_decode(const oscar_kv_config* cfg, const void* cache, int32_t layer, co
   a.new_pos = nullptr;
   a.new_n = 0;
   a.fused = 0;
-  a.wait_ns = oscar::g_test_wait_ns > 0 ? oscar::g_test_wait_ns : 2000000000ull;
+  a.wait_ns = oscar::wait_limit_ns();
   a.wait_poison = oscar::g_test_wait_poison;
   return OSCAR_OK;
 }
@@ -224,6 +224,8 @@ void plan_rows(const oscar_kv_config* cfg, const Geom& g, const void* cache, int
   p->at.status = dev_status;
   p->at.n = n;
   p->at.ns = ns;
+  p->at.wait_turns = oscar::wait_turns();
+  p->at.wait_poison = oscar::g_test_wait_poison;
   p->fin.acc = p->at.acc;
   p->fin.ml = p->at.ml;
   p->fin.q_lens = q_lens;

@@ -37,7 +37,7 @@ __device__ __forceinline__ void rows_wait(const RowsArgs& a) {
 }
 // One thread's bounded wait for *ready, a barrier before the others read the queries: the store has been made, or will be by
 // a block that is running, when a kernel starts beside.
-__device__ __forceinline__ bool ready_wait(const int32_t* ready, uint64_t limit_ns = 2000000000ull) {
+__device__ __forceinline__ bool ready_wait(const int32_t* ready, uint64_t limit_ns) {
   const uint64_t t0 = global_timer_ns();
   for (;;) {
     int32_t x;

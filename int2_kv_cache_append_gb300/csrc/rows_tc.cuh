@@ -151,21 +151,32 @@ __device__ __forceinline__ bool any128(int id, bool p) {
   return r != 0;
 }
 // Bounded wait of a whole warp.  All lanes poll, four instructions a turn: the
-// waiting warps share the issue slots with the ones that work.  A turn takes 0.1
-// us or more, so the limit is of the order of a second.
-__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+// waiting warps share the issue slots with the ones that work.  The hardware
+// suspends a turn for a microsecond at most, so `turns` of them take at most
+// about as many microseconds.  (Reading the clock in this loop instead made the attentions 3 to 8 % slower.)
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t turns) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p, q;\n .reg .b32 n;\n mov.b32 n, 0;\n"
-      "again_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra done_%=;\n"
-      " add.u32 n, n, 1;\n setp.lt.u32 q, n, 10000000;\n @q bra again_%=;\n"
+      "again_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n @p bra done_%=;\n"
+      " add.u32 n, n, 1;\n setp.lt.u32 q, n, %3;\n @q bra again_%=;\n"
       "done_%=:\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(turns)
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, poll(bar, parity)); }
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint32_t turns) {
+  return __all_sync(0xffffffffu, poll(bar, parity, turns));
+}
+// The waits of a warp that goes on after one that ran out: those behind it only look.
+struct Waits {
+  uint32_t turns;
+  bool ok = true;
+  __device__ __forceinline__ void on(uint32_t bar, uint32_t parity) {
+    if (!poll(bar, parity, turns)) ok = false, turns = 0;
+  }
+};
 // Position in a ring of n buffers: index and phase, advanced without division.
 template <int n>
 struct Ring {
@@ -467,7 +478,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
   // tile i's is used with the first unit of its last group
   static_assert(2 * (DG + 1) >= KU, "two rank-one operands");
   const Geom& g = x.a->g;
-  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity, x.a->wait_turns); };
   const int steps = x.nt * DG, per = LM ? 4 : 2;  // units of a step
   const uint8_t* role = x.a->layer_base + g.sink_bytes + g.ring_bytes;
   const int64_t row0 = int64_t(x.u) * g.ncap + (x.p0 + tok - g.S);  // INT2 row of the first tile's token
@@ -622,7 +633,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
 template <int DG, int VU, int CB, int kStages, int kU, bool LM>
 __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
   const Geom& g = x.a->g;
-  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity, x.a->wait_turns); };
   const int steps = x.nt * DG, cb = lane >> 4, sub = 16 * warp4 + (lane & 15);
   const uint8_t* role = x.a->layer_base + g.role_bytes + g.sink_bytes + g.ring_bytes;
   const int64_t row0 = int64_t(x.u) * g.ncap + (x.p0 + sub - g.S);

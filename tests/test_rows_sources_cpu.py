@@ -28,5 +28,5 @@ def test_attention_beside_its_predecessor_acquires_the_queries(name, first_read)
     """The kernel that does not wait for the one before it takes the queries
     from that one's release, with a barrier behind it, before it reads them."""
     code = _code(name)
-    acquire = code.index("a.beside && !ready_wait(a.ready)")
+    acquire = code.index("a.beside && !ready_wait(a.ready")
     assert acquire < code.index("__syncthreads()") < code.index(first_read)
