@@ -52,7 +52,7 @@ constexpr int oConst = oRank + 3 * kRank;
 constexpr int oRow = oConst + CB * TileConsts::kBytes;
 constexpr int kRow = N * 4 + 4 * N * 4 + 64;        // row index; exchange [2][2][N]; the K warps' scratch
 constexpr int oBar = oRow + kRow;
-constexpr int kBars = 2 * KU + 2 * VU + 2 * CB + 2 + 1 + 1 + 3;
+constexpr int kBars = 2 * KU + 2 * VU + 2 * CB + 2 + 1 + 1 + 2;
 constexpr int kBytes = oBar + kBars * 8 + 32 + 1024;  // + alignment slack
 static_assert(oBar % 8 == 0 && kBytes <= 232448, "shared memory");
 constexpr uint32_t cS = 0, cO = 256, cQ = 384;        // TMEM columns: two score tiles, O, Q's two parts
@@ -117,11 +117,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
   const uint32_t bar = base + oBar;
   const uint32_t k_full = bar, k_empty = k_full + 8 * KU, v_full = k_empty + 8 * KU, v_empty = v_full + 8 * VU,
                  c_full = v_empty + 8 * VU, c_empty = c_full + 8 * CB, s_full = c_empty + 8 * CB, p_full = s_full + 16,
-                 p_done = p_full + 8, q_full = p_done + 8, f_full = q_full + 8, drained = f_full + 8;
+                 p_done = p_full + 8, q_full = p_done + 8, drained = q_full + 8;
   uint32_t* words = reinterpret_cast<uint32_t*>(sm + oBar + kBars * 8);
   uint32_t* tmem_slot = words;
-  uint32_t* qmax = words + 1;
-  float* scale_f = reinterpret_cast<float*>(words + 2);
 
   for (int c = threadIdx.x; c < N; c += kThreads) {
     const int row = rt * N + c, t = row / g.G;
@@ -141,10 +139,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     mbar_init(p_full, kSoftWarps);
     mbar_init(p_done, 1);
     mbar_init(q_full, kSoftWarps);
-    mbar_init(f_full, kSoftWarps);
     mbar_init(drained, 1);
     mbar_fence_init();
-    *qmax = 0;
     if (a.beside && !ready_wait(a.ready, a.wait_turns * 1000ull)) status_or(a.status, OSCAR_DEV_TIMEOUT);  // the queries
   }
   if (warp == kSoftWarps + 8) {
@@ -166,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     // ------------------------------- softmax ---------------------------------
     const int half = warp >> 2, row = threadIdx.x & 127;     // the thread's tokens of a tile and row (TMEM lane)
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;  // the warp's TMEM lanes
+    float qscale;  // power of two that undoes the row's scaling
     // Q: this thread's 64 channels of its row, scaled (query_exponent) and split into two fp16 parts.  Plain loads: the
     // rotation may still be writing when this kernel starts (row_launch).
     {
@@ -182,12 +179,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
             if (isfinite(f[e])) mx = max(mx, __float_as_uint(fabsf(f[e])));
         }
       }
-      mx = __reduce_max_sync(0xffffffffu, mx);
-      if (lane == 0) atomicMax(qmax, mx);
+      uint32_t* both = reinterpret_cast<uint32_t*>(swap + 2 * N);  // the row's two threads
+      both[half * N + row] = mx;
       asm volatile("bar.sync 3, 256;" ::: "memory");
-      const int fe = query_exponent(*qmax);
+      const int fe = query_exponent(max(mx, both[(half ^ 1) * N + row]));
       const float inv = pow2i(-fe);
-      if (threadIdx.x == 0) *scale_f = pow2i(fe);
+      qscale = pow2i(fe);
       float sum = 0.f;
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
@@ -214,7 +211,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       fence_async();
       fence_before();
       __syncwarp();
-      mbar_arrive_if(f_full, lane == 0);
       mbar_arrive_if(q_full, lane == 0);
       asm volatile("bar.sync 3, 256;" ::: "memory");  // the sums have been read
     }
@@ -232,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       fence_after();
       const uint32_t S = tmem + lanes + cS + (i & 1) * 128 + 64 * half;
       const TileConsts tc(sm + oConst, cb);
-      const float phi = *tc.phi();
+      const float phi = *tc.phi() * qscale;
       const bool masked = base_pos + kTok - 1 > see_all;  // some row does not see some position of the tile
       const bool plain = !masked && *tc.uneven() == 0;
       const int see = lim - base_pos - 64 * half;          // the thread's columns j <= see are visible
@@ -363,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       fail();
     }
   } else if (warp < kSoftWarps + 8) {
-    Share x{&a, u, T, p0, p1, nt, sm, base, scale_f, f_full, k_full, k_empty, v_full, v_empty, c_full, c_empty,
+    Share x{&a, u, T, p0, p1, nt, sm, base, k_full, k_empty, v_full, v_empty, c_full, c_empty,
             oK, oV, oRawK, oRawV, oConst, oRank, oRow + 5 * N * 4};
     const int tok = threadIdx.x - kSoftWarps * 32;
     const bool ok = warp < kSoftWarps + 4 ? (g.lm ? expand_k<1, KU, CB, kStages, 4, true>(x, tok, lane) : expand_k<1, KU, CB, kStages, 4, false>(x, tok, lane))

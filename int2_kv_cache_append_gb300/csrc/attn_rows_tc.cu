@@ -14,7 +14,7 @@
 //
 //   * Scores.  INT2 keys enter the product exactly, as s (c - 1) with the middles
 //     z + s as a rank-one term, BF16 keys exactly (expand_k in rows_tc.cuh); q,
-//     scaled by a power of two per CTA, is the sum of two fp16 values.  So the
+//     scaled by a power of two per row, is the sum of two fp16 values.  So the
 //     products' sums are scores of float32 accuracy.
 //   * Probabilities carry the value row's exponent: with v_t = 2^(e_t) w_t, |w| < 1,
 //     u = score + e_t, P = 2^(u - M) in fp16 and l += 2^(-e_t) 2^(u - M) in float32.
@@ -77,10 +77,10 @@ struct Plan {
   static constexpr int oRawV = oRawK + kStages * kRawStage;
   static constexpr int oRank = oRawV + kStages * kRawStage;  // the keys' two and the queries' rank-one operands
   static constexpr int oConst = oRank + 2 * kRank + N * 32;
-  static constexpr int oRow = oConst + CB * TileConsts::kBytes;  // per column: -M, limit, output row, factor; scratch
-  static constexpr int kRow = N * 4 * 4 + 8 * N / 2 * 4 + 64;
+  static constexpr int oRow = oConst + CB * TileConsts::kBytes;  // per column: -M, limit, output row, factor, query scale; scratch
+  static constexpr int kRow = N * 5 * 4 + 8 * N / 2 * 4 + 64;
   static constexpr int oBar = oRow + kRow;
-  static constexpr int kBars = 2 * KU + 2 * VU + 2 * SB + 2 * PB + 2 * CB + 3;
+  static constexpr int kBars = 2 * KU + 2 * VU + 2 * SB + 2 * PB + 2 * CB + 2;
   static constexpr int kBytes = oBar + kBars * 8 + 32 + 1024;  // + alignment slack
   // The tensor cores cut each of their sums' additions off (towards zero).  At D = 512 a score would be 65 additions and
   // 1e-6 too small, so at D = 256 and 512 two accumulators share them.
@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
   int* limit = reinterpret_cast<int*>(negM + N);   // last position that the row sees
   int* outr = limit + N;                            // its index among all query rows, -1 = none
   float* factor = reinterpret_cast<float*>(outr + N);
-  float* part = factor + N;                         // [8 warps][C]
+  float* qscale = factor + N;                       // power of two that undoes the row's scaling
+  float* part = qscale + N;                         // [8 warps][C]
   const uint32_t bar = base + L::oBar;
   auto k_full = [&](int i) { return bar + 8u * i; };
   auto k_empty = [&](int i) { return bar + 8u * (L::KU + i); };
@@ -141,11 +142,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
   constexpr int b2 = b1 + 2 * L::SB + 2 * L::PB;
   auto c_full = [&](int i) { return bar + 8u * (b2 + i); };
   auto c_empty = [&](int i) { return bar + 8u * (b2 + L::CB + i); };
-  const uint32_t q_full = bar + 8u * (b2 + 2 * L::CB), f_full = q_full + 8, drained = f_full + 8;
+  const uint32_t q_full = bar + 8u * (b2 + 2 * L::CB), drained = q_full + 8;
   uint32_t* words = reinterpret_cast<uint32_t*>(sm + L::oBar + L::kBars * 8);
   uint32_t* tmem_slot = words;
-  uint32_t* qmax = words + 1;
-  float* scale_f = reinterpret_cast<float*>(words + 2);
 
   for (int c = threadIdx.x; c < N; c += kThreads) {
     const int row = rt * N + c, t = row / g.G;
@@ -166,10 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     for (int i = 0; i < L::PB; ++i) mbar_init(p_full(i), kSoftWarps), mbar_init(p_empty(i), 1);
     for (int i = 0; i < L::CB; ++i) mbar_init(c_full(i), 8), mbar_init(c_empty(i), kSoftWarps);
     mbar_init(q_full, kSoftWarps);
-    mbar_init(f_full, kSoftWarps);
     mbar_init(drained, 1);
     mbar_fence_init();
-    *qmax = 0;
     if (a.beside && !ready_wait(a.ready, a.wait_turns * 1000ull)) status_or(a.status, OSCAR_DEV_TIMEOUT);  // the queries
   }
   if (warp == kSoftWarps + 8) {
@@ -193,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     const int tok = threadIdx.x & 127;                      // and this thread's token (TMEM lane)
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16; // the warp's TMEM lanes
     const int id = 1 + grp;                                 // named barrier of the group
-    load_queries<DG, N, kSoftWarps>(a, sm + L::oQ, L::kQ, outr, sm + L::oRank + 2 * kRank, qmax, scale_f, f_full, warp, lane);
+    load_queries<DG, N, kSoftWarps>(a, sm + L::oQ, L::kQ, outr, sm + L::oRank + 2 * kRank, qscale, warp, lane);
     mbar_arrive_if(q_full, lane == 0);
 
     uint64_t l2[C / 2];  // this token's part of l, two columns at a time
@@ -237,8 +234,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
           for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(r2[j]));
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          x[j] = fma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), phi2, x[j]);
+        for (int j = 0; j < 8; j += 2) {
+          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(qscale + c + 2 * j);
+          x[j] = fma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), mul2(phi2, f.x), x[j]);
+          x[j + 1] = fma2(pack2(__uint_as_float(r[2 * j + 2]), __uint_as_float(r[2 * j + 3])), mul2(phi2, f.y), x[j + 1]);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) unpack2(x[j], t[2 * j], t[2 * j + 1]);
         if (masked) {
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
       fail();
     }
   } else if (warp < kSoftWarps + 8) {
-    Share x{&a, u, T, p0, p1, nt, sm, base, scale_f, f_full, k_full(0), k_empty(0), v_full(0), v_empty(0),
+    Share x{&a, u, T, p0, p1, nt, sm, base, k_full(0), k_empty(0), v_full(0), v_empty(0),
             c_full(0), c_empty(0), L::oK, L::oV, L::oRawK, L::oRawV, L::oConst, L::oRank,
             L::oRow + L::kRow - 64};
     const int tok = threadIdx.x - kSoftWarps * 32;

@@ -296,9 +296,10 @@ __device__ __forceinline__ float split_pair(float x, float y, uint32_t& hi, uint
   return (a.x + b.x) + (a.y + b.y);
 }
 
-// Scale of the CTA's query rows: a power of two that brings the largest finite
-// component just below 2^7 (sums of 128 of them stay in fp16).
-__device__ __forceinline__ int query_exponent(uint32_t max_bits) { return max(-100, min(100, (int(max_bits) >> 23) - 126 - 7)); }
+// Scale of a query row: a power of two that brings its largest finite component
+// just below 2^7 (sums of 128 of them stay in fp16).  Every row has its own, so
+// that no row's bits depend on the others of its CTA.
+__device__ __forceinline__ int query_exponent(uint32_t max_bits) { return max(-119, (int(max_bits) >> 23) - 126 - 7); }
 
 // Byte offset of element (row, k) of an operand of 16 k without swizzle: core
 // matrices of 8 rows x 16 bytes, the two of a row group 128 bytes apart.
@@ -320,55 +321,55 @@ __device__ __forceinline__ uint2 rank_key(float x) {
 }
 
 // The CTA's query rows as fp16 operands in shared memory, by `warps` warps
-// (named barrier 3): scaled (query_exponent), split into two fp16 values whose
-// sum has 22 bits, written K-major in blocks of 64 channels; a warp takes one
-// (row, group) at a time.  rank: the rows' sums per group for the rank-one term.
-// *scale and f_full: the power of two that undoes the scaling.
+// (named barrier 3), a row at a time each: scaled (query_exponent), split into two
+// fp16 values whose sum has 22 bits, written K-major in blocks of 64 channels.
+// rank: the rows' sums per group for the rank-one term.  factor: the powers of
+// two that undo the scaling.
 template <int DG, int N, int warps>
 __device__ __forceinline__ void load_queries(const RowsArgs& a, uint8_t* sq, int part, const int* outr, uint8_t* rank,
-                                             uint32_t* qmax, float* scale, uint32_t f_full, int warp, int lane) {
+                                             float* factor, int warp, int lane) {
   constexpr int D = DG * 128;
-  uint32_t mx = 0;
-#pragma unroll 4
-  for (int i = warp; i < N * DG; i += warps) {
-    const int r = outr[i / DG];
-    if (r < 0) continue;
-    const float4 v = *reinterpret_cast<const float4*>(a.qrot + int64_t(r) * D + (i % DG) * 128 + 4 * lane);
-    const float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (isfinite(f[e])) mx = max(mx, __float_as_uint(fabsf(f[e])));
-  }
-  mx = __reduce_max_sync(0xffffffffu, mx);
-  if (lane == 0) atomicMax(qmax, mx);
-  for (int i = warp * 32 + lane; i < N * 2; i += warps * 32) *reinterpret_cast<uint4*>(rank + i * 16) = make_uint4(0, 0, 0, 0);
-  asm volatile("bar.sync 3, %0;" ::"n"(warps * 32) : "memory");
-  const int fe = query_exponent(*qmax);
-  const float inv = pow2i(-fe);
-  if (warp == 0 && lane == 0) *scale = pow2i(fe);
 #pragma unroll 2
-  for (int i = warp; i < N * DG; i += warps) {
-    const int c = i / DG, gr = i % DG, r = outr[c];
-    float f[4] = {0.f, 0.f, 0.f, 0.f};
-    if (r >= 0) {
-      const float4 v = *reinterpret_cast<const float4*>(a.qrot + int64_t(r) * D + gr * 128 + 4 * lane);
-      f[0] = v.x * inv, f[1] = v.y * inv, f[2] = v.z * inv, f[3] = v.w * inv;
+  for (int c = warp; c < N; c += warps) {
+    const int r = outr[c];
+    float4 v[DG];
+    uint32_t mx = 0;
+#pragma unroll
+    for (int gr = 0; gr < DG; ++gr) {
+      v[gr] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r >= 0) v[gr] = *reinterpret_cast<const float4*>(a.qrot + int64_t(r) * D + gr * 128 + 4 * lane);
     }
-    uint32_t hi[2], lo[2];
-    float sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) sum += split_pair(f[2 * e], f[2 * e + 1], hi[e], lo[e]);
+    for (int gr = 0; gr < DG; ++gr) {
+      const float f[4] = {v[gr].x, v[gr].y, v[gr].z, v[gr].w};
 #pragma unroll
-    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    // channels 4 lane .. 4 lane + 3: block lane / 16, 16-byte chunk (lane / 2) % 8, half lane % 2
-    const int off = (2 * gr + (lane >> 4)) * (N * 128) + c * 128 + ((((lane >> 1) & 7) ^ (c & 7)) << 4) + ((lane & 1) << 3);
-    *reinterpret_cast<uint2*>(sq + off) = make_uint2(hi[0], hi[1]);
-    *reinterpret_cast<uint2*>(sq + part + off) = make_uint2(lo[0], lo[1]);
-    if (lane == 0) *reinterpret_cast<uint2*>(rank + rank_offset(c, 4 * gr)) = rank_query(sum);
+      for (int e = 0; e < 4; ++e)
+        if (isfinite(f[e])) mx = max(mx, __float_as_uint(fabsf(f[e])));
+    }
+    const int fe = query_exponent(__reduce_max_sync(0xffffffffu, mx));
+    const float inv = pow2i(-fe);
+    uint2 sums[4] = {make_uint2(0, 0), make_uint2(0, 0), make_uint2(0, 0), make_uint2(0, 0)};
+#pragma unroll
+    for (int gr = 0; gr < DG; ++gr) {
+      uint32_t hi[2], lo[2];
+      float sum = split_pair(v[gr].x * inv, v[gr].y * inv, hi[0], lo[0]);
+      sum += split_pair(v[gr].z * inv, v[gr].w * inv, hi[1], lo[1]);
+#pragma unroll
+      for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      sums[gr] = rank_query(sum);
+      // channels 4 lane .. 4 lane + 3: block lane / 16, 16-byte chunk (lane / 2) % 8, half lane % 2
+      const int off = (2 * gr + (lane >> 4)) * (N * 128) + c * 128 + ((((lane >> 1) & 7) ^ (c & 7)) << 4) + ((lane & 1) << 3);
+      *reinterpret_cast<uint2*>(sq + off) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(sq + part + off) = make_uint2(lo[0], lo[1]);
+    }
+    if (lane == 0) {
+      factor[c] = pow2i(fe);
+      *reinterpret_cast<uint4*>(rank + rank_offset(c, 0)) = make_uint4(sums[0].x, sums[0].y, sums[1].x, sums[1].y);
+      *reinterpret_cast<uint4*>(rank + rank_offset(c, 8)) = make_uint4(sums[2].x, sums[2].y, sums[3].x, sums[3].y);
+    }
   }
   fence_async();
   asm volatile("bar.sync 3, %0;" ::"n"(warps * 32) : "memory");
-  mbar_arrive_if(f_full, lane == 0);
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
@@ -407,7 +408,7 @@ __device__ __forceinline__ void write_wide(const __nv_bfloat16* src, uint8_t* ds
 
 // Constants of a tile, one slot of the ring: e[128] (the value rows'
 // exponents), rv[128] (2^-e), a word that is set when some e is not 0, and the
-// factor from the products' sums to scores in log2 units.
+// factor that undoes the keys' scaling.
 struct TileConsts {
   static constexpr int kBytes = 2 * kTok * 4 + 16;
   float* p;
@@ -429,8 +430,6 @@ struct Share {
   int u, T, p0, p1, nt;
   uint8_t* sm;                    // shared memory and its address
   uint32_t base;
-  const float* F;                 // scale of the queries, valid after f_full
-  uint32_t f_full;
   uint32_t k_full, k_empty, v_full, v_empty, c_full, c_empty;  // first barrier of each kind
   int oK, oV, oRawK, oRawV, oConst, oRank, oScratch;
 };
@@ -506,8 +505,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
   };
   ahead(0);
   const Tiles packed_tiles(x.p0, g.S, ring0);
-  bool ok = wait(x.f_full, 0);  // a warp that gave up still comes to the group's barriers
-  const float F = *x.F;
+  bool ok = true;               // a warp that gave up still comes to the group's barriers
   float down = 0.5f;            // the tile's power of two; one half keeps 2 s and z + s within fp16
   int n = 0;                    // units written
 #pragma unroll 1
@@ -519,7 +517,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
     const __nv_bfloat16* wide = valid && !packed ? row_ref(g, x.a->layer_base, 0, x.u, x.T, pos).wide : nullptr;
     if (gr == 0) {
       if (!packed_tiles.has(i + 1)) ahead(i + 1);
-      float phi = 2.0f * F;
+      float phi = 2.0f;
       down = 0.5f;
       const int first = x.p0 + i * kTok, last = min(x.p1, first + kTok) - 1;
       if (first < g.S || last >= ring0) {  // the tile has BF16 rows
@@ -541,7 +539,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
         if (m > 0.f && !(m >= 0x1p-4f && m < 0x1p14f)) {
           const int e = max(-104, min(127, (int(__float_as_uint(m)) >> 23) - 126)) - 13;  // 2^-e m is just below 2^13
           down = pow2i(-e);
-          phi = F * pow2i(e);
+          phi = pow2i(e);
         }
       }
       if (i >= CB) ok = ok && wait(x.c_empty + 8 * slot, ((i / CB) & 1) ^ 1);
