@@ -352,8 +352,10 @@ int kv_read(const oscar_kv_config* cfg, const void* cache, int32_t layer, const 
  *              what fits (OSCAR_ERR_WORKSPACE if one split does not, or an
  *              explicit count).  Concurrent calls must not share a workspace.
  * With a float32 output everything is float32.  A bf16 output is computed on
- * the tensor cores: cached keys enter the products exactly, rotated queries as
- * a sum of two fp16 values (2^-22), so scores and lse have float32 accuracy
+ * the tensor cores: cached keys enter the products exactly (to 2^-22 of a row's
+ * largest value where its values differ much in size), rotated queries as
+ * a sum of two fp16 values (2^-22), every row with a power of two of its own,
+ * so scores and lse have float32 accuracy
  * (relative 1e-6, the tensor cores' sums being cut off rather than rounded);
  * probabilities, value rows and, for many rows, the merged rows and R_V in the
  * un-rotation are rounded to fp16 (relative 2^-12 each).  OSCAR_DEV_TIMEOUT in

@@ -49,8 +49,8 @@ constexpr int oRawK = oV + VU * kUnit;
 constexpr int oRawV = oRawK + kStages * kRawStage;
 constexpr int oRank = oRawV + kStages * kRawStage;  // the keys' two and the queries' rank-one operands
 constexpr int oConst = oRank + 3 * kRank;
-constexpr int oRow = oConst + CB * TileConsts::kBytes;
-constexpr int kRow = N * 4 + 4 * N * 4 + 64;        // row index; exchange [2][2][N]; the K warps' scratch
+constexpr int oRow = oConst + CB * TileConsts<true>::kBytes;
+constexpr int kRow = N * 4 + 4 * N * 4;             // row index; exchange [2][2][N]
 constexpr int oBar = oRow + kRow;
 constexpr int kBars = 2 * KU + 2 * VU + 2 * CB + 2 + 1 + 1 + 2;
 constexpr int kBytes = oBar + kBars * 8 + 32 + 1024;  // + alignment slack
@@ -227,8 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       ok = ok && wait(s_full + 8 * (i & 1), (i >> 1) & 1);
       fence_after();
       const uint32_t S = tmem + lanes + cS + (i & 1) * 128 + 64 * half;
-      const TileConsts tc(sm + oConst, cb);
-      const float phi = *tc.phi() * qscale;
+      const TileConsts<true> tc(sm + oConst, cb);
+      float phi = kKeyEven * qscale;
       const bool masked = base_pos + kTok - 1 > see_all;  // some row does not see some position of the tile
       const bool plain = !masked && *tc.uneven() == 0;
       const int see = lim - base_pos - 64 * half;          // the thread's columns j <= see are visible
@@ -237,6 +237,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       // the scores of this thread's 64 tokens; with exponents or hidden positions, u = phi S + e or -inf instead
       uint32_t r[64];
       tmem_ld64(S, r);
+      if (*tc.k_uneven()) {  // some key row has a factor of its own
+        phi = 1.f;
+        const float* kf = tc.k() + 64 * half;
+#pragma unroll
+        for (int j = 0; j < 64; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(kf + j);
+          r[j] = __float_as_uint(__uint_as_float(r[j]) * (f.x * qscale));
+          r[j + 1] = __float_as_uint(__uint_as_float(r[j + 1]) * (f.y * qscale));
+          r[j + 2] = __float_as_uint(__uint_as_float(r[j + 2]) * (f.z * qscale));
+          r[j + 3] = __float_as_uint(__uint_as_float(r[j + 3]) * (f.w * qscale));
+        }
+      }
       float top = -INFINITY, top1 = -INFINITY;
       if (plain) {
 #pragma unroll
@@ -360,10 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
     }
   } else if (warp < kSoftWarps + 8) {
     Share x{&a, u, T, p0, p1, nt, sm, base, k_full, k_empty, v_full, v_empty, c_full, c_empty,
-            oK, oV, oRawK, oRawV, oConst, oRank, oRow + 5 * N * 4};
+            oK, oV, oRawK, oRawV, oConst, oRank};
     const int tok = threadIdx.x - kSoftWarps * 32;
-    const bool ok = warp < kSoftWarps + 4 ? (g.lm ? expand_k<1, KU, CB, kStages, 4, true>(x, tok, lane) : expand_k<1, KU, CB, kStages, 4, false>(x, tok, lane))
-                                          : (g.lm ? expand_v<1, VU, CB, kStages, 4, true>(x, warp & 3, lane) : expand_v<1, VU, CB, kStages, 4, false>(x, warp & 3, lane));
+    const bool ok = warp < kSoftWarps + 4 ? (g.lm ? expand_k<1, KU, CB, kStages, 4, true, true>(x, tok, lane) : expand_k<1, KU, CB, kStages, 4, false, true>(x, tok, lane))
+                                          : (g.lm ? expand_v<1, VU, CB, kStages, 4, true, true>(x, warp & 3, lane) : expand_v<1, VU, CB, kStages, 4, false, true>(x, warp & 3, lane));
     cp_async_wait<0>();  // also where a wait ran out
     if (!ok && lane == 0) fail();
   } else {

@@ -77,8 +77,8 @@ struct Plan {
   static constexpr int oRawV = oRawK + kStages * kRawStage;
   static constexpr int oRank = oRawV + kStages * kRawStage;  // the keys' two and the queries' rank-one operands
   static constexpr int oConst = oRank + 2 * kRank + N * 32;
-  static constexpr int oRow = oConst + CB * TileConsts::kBytes;  // per column: -M, limit, output row, factor, query scale; scratch
-  static constexpr int kRow = N * 5 * 4 + 8 * N / 2 * 4 + 64;
+  static constexpr int oRow = oConst + CB * TileConsts<false>::kBytes;  // per column: -M, limit, output row, factor, query scale; sums
+  static constexpr int kRow = N * 5 * 4 + 8 * N / 2 * 4;
   static constexpr int oBar = oRow + kRow;
   static constexpr int kBars = 2 * KU + 2 * VU + 2 * SB + 2 * PB + 2 * CB + 2;
   static constexpr int kBytes = oBar + kBars * 8 + 32 + 1024;  // + alignment slack
@@ -204,9 +204,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
       ok = ok && wait(s_full(sb), (i / L::SB) & 1);
       if (i >= L::PB) ok = ok && wait(p_empty(pb), ((i / L::PB) & 1) ^ 1);
       fence_after();
-      const TileConsts tc(sm + L::oConst, cb);
-      const uint64_t phi2 = splat_x2(*tc.phi());
-      const uint64_t e2 = splat_x2(tc.e()[tok]), rv2 = splat_x2(tc.rv()[tok]);
+      const TileConsts<false> tc(sm + L::oConst, cb);
+      const uint64_t phi2 = splat_x2(tc.k()[tok]);
+      const uint64_t e2 = splat_x2(tc.e()[tok]), rv2 = splat_x2(rv_of(tc.e()[tok]));
       const bool masked = p0 + i * kTok + kTok - 1 > see_all;  // some row does not see some position of the tile
       uint8_t* P = sm + L::oP + pb * L::kP + tok * 128;
       const uint32_t S = tmem + lanes + L::cS + sb * (L::kParts * N);
@@ -399,11 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
     }
   } else if (warp < kSoftWarps + 8) {
     Share x{&a, u, T, p0, p1, nt, sm, base, k_full(0), k_empty(0), v_full(0), v_empty(0),
-            c_full(0), c_empty(0), L::oK, L::oV, L::oRawK, L::oRawV, L::oConst, L::oRank,
-            L::oRow + L::kRow - 64};
+            c_full(0), c_empty(0), L::oK, L::oV, L::oRawK, L::oRawV, L::oConst, L::oRank};
     const int tok = threadIdx.x - kSoftWarps * 32;
-    const bool ok = warp < kSoftWarps + 4 ? (g.lm ? expand_k<DG, L::KU, L::CB, L::kStages, 8, true>(x, tok, lane) : expand_k<DG, L::KU, L::CB, L::kStages, 8, false>(x, tok, lane))
-                                          : (g.lm ? expand_v<DG, L::VU, L::CB, L::kStages, 8, true>(x, warp & 3, lane) : expand_v<DG, L::VU, L::CB, L::kStages, 8, false>(x, warp & 3, lane));
+    const bool ok = warp < kSoftWarps + 4 ? (g.lm ? expand_k<DG, L::KU, L::CB, L::kStages, 8, true, false>(x, tok, lane) : expand_k<DG, L::KU, L::CB, L::kStages, 8, false, false>(x, tok, lane))
+                                          : (g.lm ? expand_v<DG, L::VU, L::CB, L::kStages, 8, true, false>(x, warp & 3, lane) : expand_v<DG, L::VU, L::CB, L::kStages, 8, false, false>(x, warp & 3, lane));
     cp_async_wait<0>();  // also where a wait ran out
     if (!ok && lane == 0) fail();
   } else {

@@ -406,18 +406,24 @@ __device__ __forceinline__ void write_wide(const __nv_bfloat16* src, uint8_t* ds
   }
 }
 
-// Constants of a tile, one slot of the ring: e[128] (the value rows'
-// exponents), rv[128] (2^-e), a word that is set when some e is not 0, and the
-// factor that undoes the keys' scaling.
+// Constants of a tile, one slot of the ring: e[128] (the value rows' exponents),
+// k[128] (the factors that undo the keys' scaling), two words that are set when
+// some e is not 0 and when some k is not kKeyEven, and, for rows in the TMEM lanes
+// (RV), rv[128] (2^-e).
+constexpr float kKeyEven = 2.0f;
+template <bool RV>
 struct TileConsts {
-  static constexpr int kBytes = 2 * kTok * 4 + 16;
+  static constexpr int kBytes = (RV ? 3 : 2) * kTok * 4 + 16;
   float* p;
   __device__ __forceinline__ TileConsts(uint8_t* ring, int slot) : p(reinterpret_cast<float*>(ring + slot * kBytes)) {}
   __device__ __forceinline__ float* e() const { return p; }
-  __device__ __forceinline__ float* rv() const { return p + kTok; }
+  __device__ __forceinline__ float* k() const { return p + kTok; }
   __device__ __forceinline__ uint32_t* uneven() const { return reinterpret_cast<uint32_t*>(p + 2 * kTok); }
-  __device__ __forceinline__ float* phi() const { return p + 2 * kTok + 1; }
+  __device__ __forceinline__ uint32_t* k_uneven() const { return uneven() + 1; }
+  __device__ __forceinline__ float* rv() const { return p + 2 * kTok + 4; }
 };
+// 2^-e of a value row's exponent, 1 for the rows that have none
+__device__ __forceinline__ float rv_of(float e) { return isfinite(e) ? pow2i(-int(e)) : 1.f; }
 
 template <bool b>
 struct Flag {
@@ -431,7 +437,7 @@ struct Share {
   uint8_t* sm;                    // shared memory and its address
   uint32_t base;
   uint32_t k_full, k_empty, v_full, v_empty, c_full, c_empty;  // first barrier of each kind
-  int oK, oV, oRawK, oRawV, oConst, oRank, oScratch;
+  int oK, oV, oRawK, oRawV, oConst, oRank;
 };
 constexpr int kRawStage = kTok * 36;  // staged codes (32 bytes) and scale / zero pairs of one (tile, group) and role
 constexpr int kRank = kTok * 32;      // one tile's rank-one operand
@@ -466,12 +472,16 @@ struct Tiles {
 // Lloyd-Max levels are the uniform ones plus 0.16 (0, 1, 1, 2): z + rho s is the
 // middle, and s (-rho, 0, 1, rho + 1) is rounded to fp16 with the residues in a
 // second set of units, which only Q's high part meets (2^-24 of a product is lost).
-// BF16 keys are exact in fp16 once the tile's largest value is below 2^15; where it is not, or
-// far below 1, the whole tile is scaled by a power of two.
+// BF16 keys are exact in fp16 within its range.  Every key row is scaled by a
+// power of two of its own, one half (which keeps 2 s and z + s within fp16) where
+// its largest value lies between 2^-2 and 2^14, else what brings that just below
+// 2^13: what is cut off, 2^-25 of a scaled row, is then 2^-22 of the row's largest
+// value at most.  The factor that undoes it meets the row's scores; one factor
+// for a tile would let a key of a later position cost the earlier ones' bits.
 //
 // Steps k = (tile, group); codes are staged kStages - 1 steps ahead by cp.async,
 // each thread its own row.  Returns false after a timeout.
-template <int DG, int KU, int CB, int kStages, int kU, bool LM>
+template <int DG, int KU, int CB, int kStages, int kU, bool LM, bool RV>
 __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
   // the rank-one operand of tile i + 2 is written after unit 0 of that tile has found the unit KU before it empty, and
   // tile i's is used with the first unit of its last group
@@ -505,9 +515,17 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
   };
   ahead(0);
   const Tiles packed_tiles(x.p0, g.S, ring0);
-  bool ok = true;               // a warp that gave up still comes to the group's barriers
-  float down = 0.5f;            // the tile's power of two; one half keeps 2 s and z + s within fp16
-  int n = 0;                    // units written
+  uint32_t nsz[DG];  // the next tile's scale / zero pairs
+  auto pairs = [&](int i) {
+    const int pos = x.p0 + i * kTok + tok;
+    const bool packed = pos >= g.S && pos < ring0 && pos < x.p1;
+#pragma unroll
+    for (int gr = 0; gr < DG; ++gr)
+      nsz[gr] = packed ? __ldg(reinterpret_cast<const uint32_t*>(szs + int64_t(i) * (kTok * 4 * DG)) + gr) : 0u;
+  };
+  pairs(0);
+  float down = 0.5f;  // the row's power of two
+  int n = 0;          // units written
 #pragma unroll 1
   for (int k = 0; k < steps; ++k) {
     stage(k + kStages - 1);
@@ -517,33 +535,27 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
     const __nv_bfloat16* wide = valid && !packed ? row_ref(g, x.a->layer_base, 0, x.u, x.T, pos).wide : nullptr;
     if (gr == 0) {
       if (!packed_tiles.has(i + 1)) ahead(i + 1);
-      float phi = 2.0f;
-      down = 0.5f;
-      const int first = x.p0 + i * kTok, last = min(x.p1, first + kTok) - 1;
-      if (first < g.S || last >= ring0) {  // the tile has BF16 rows
-        float m = 0.f;
-        if (packed) {
+      float m = 0.f;
+      if (packed) {
 #pragma unroll
-          for (int j = 0; j < DG; ++j) {
-            const float2 sz = __half22float2(reinterpret_cast<const __half2*>(szs + int64_t(i) * (kTok * 4 * DG))[j]);
-            m = fmaxf(m, fmaxf(fabsf(sz.y), fabsf(fmaf(sz.x, LM ? kLmSpan : 3.0f, sz.y))));
-          }
-        } else if (wide) {
-          m = __uint_as_float(row_max<DG, 2 * kU>(wide));
+        for (int j = 0; j < DG; ++j) {
+          const float2 sz = __half22float2(*reinterpret_cast<const __half2*>(&nsz[j]));
+          m = fmaxf(m, fmaxf(fabsf(sz.y), fabsf(fmaf(sz.x, LM ? kLmSpan : 3.0f, sz.y))));
         }
-        const uint32_t wm = __reduce_max_sync(0xffffffffu, isfinite(m) ? __float_as_uint(m) : 0u);
-        uint32_t* most = reinterpret_cast<uint32_t*>(x.sm + x.oScratch) + 4 * (i & 3);
-        if (lane == 0) most[tok >> 5] = wm;
-        if (any128(5, !ok)) return false;
-        m = __uint_as_float(max(max(most[0], most[1]), max(most[2], most[3])));
-        if (m > 0.f && !(m >= 0x1p-4f && m < 0x1p14f)) {
-          const int e = max(-104, min(127, (int(__float_as_uint(m)) >> 23) - 126)) - 13;  // 2^-e m is just below 2^13
-          down = pow2i(-e);
-          phi = pow2i(e);
-        }
+      } else if (wide) {
+        m = __uint_as_float(row_max<DG, 2 * kU>(wide));
       }
-      if (i >= CB) ok = ok && wait(x.c_empty + 8 * slot, ((i / CB) & 1) ^ 1);
-      if (tok == 0) *TileConsts(x.sm + x.oConst, slot).phi() = phi;
+      pairs(i + 1);
+      int e = 1;
+      if (m > 0.f && !(m >= 0x1p-2f && m < 0x1p14f) && isfinite(m))
+        e = max(-104, min(127, (int(__float_as_uint(m)) >> 23) - 126)) - 13;  // 2^-e m is just below 2^13
+      down = pow2i(-e);
+      if (i >= CB && !wait(x.c_empty + 8 * slot, ((i / CB) & 1) ^ 1)) return false;
+      const TileConsts<RV> tc(x.sm + x.oConst, slot);
+      tc.k()[tok] = pow2i(e);
+      const bool uneven = __any_sync(0xffffffffu, e != 1);
+      if (lane == 0) reinterpret_cast<volatile uint8_t*>(tc.k_uneven())[tok >> 5] = uneven;  // one byte per warp
+      __syncwarp();
       mbar_arrive_if(x.c_full + 8 * slot, lane == 0);
     }
     const uint8_t* st = x.sm + x.oRawK + (k % kStages) * kRawStage;
@@ -570,8 +582,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
 #pragma unroll 1
       for (int set = 0; set < per; set += 2, ++n) {
         const int u = n % KU;
-        if (n >= KU) ok = ok && wait(x.k_empty + 8 * u, ((n / KU) & 1) ^ 1);
-        if (!ok) continue;
+        if (n >= KU && !wait(x.k_empty + 8 * u, ((n / KU) & 1) ^ 1)) return false;
         if (half == 0 && set == 0)
           *reinterpret_cast<uint2*>(x.sm + x.oRank + (i & 1) * kRank + rank_offset(tok, 4 * gr)) = rank_key(middle);
         uint8_t* row = x.sm + x.oK + u * kUnit + tok * 128;
@@ -620,7 +631,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
       }
     }
   }
-  return ok;
+  return true;
 }
 
 // V, four warps.  Warp w holds tokens 64 h + 16 w .. + 15 of both unit halves h;
@@ -628,7 +639,7 @@ __device__ __forceinline__ bool expand_k(const Share& x, int tok, int lane) {
 // exponents and the scale / zero pairs, fetched two tiles ahead, lane 16 h + j
 // stands for the token of half h.  The exponents of a tile are published before
 // the previous tile's units, which wait for products, are written.
-template <int DG, int VU, int CB, int kStages, int kU, bool LM>
+template <int DG, int VU, int CB, int kStages, int kU, bool LM, bool RV>
 __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
   const Geom& g = x.a->g;
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity, x.a->wait_turns); };
@@ -674,9 +685,9 @@ __device__ __forceinline__ bool expand_v(const Share& x, int warp4, int lane) {
          : !isfinite(m) ? NAN
          : m >= 0x1p-8f && m < 0x1p12f ? 0.f : float(exponent_above(m));
     if (i >= CB && !wait(x.c_empty + 8 * slot, ((i / CB) & 1) ^ 1)) return false;
-    const TileConsts tc(x.sm + x.oConst, slot);
+    const TileConsts<RV> tc(x.sm + x.oConst, slot);
     tc.e()[mine] = ne;
-    tc.rv()[mine] = isfinite(ne) ? pow2i(-int(ne)) : 1.f;
+    if (RV) tc.rv()[mine] = rv_of(ne);
     const bool uneven = __any_sync(0xffffffffu, ne != 0.f);
     if (lane == 0) reinterpret_cast<volatile uint8_t*>(tc.uneven())[warp4] = uneven;  // one byte per warp
     __syncwarp();

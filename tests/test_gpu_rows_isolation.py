@@ -1,11 +1,13 @@
 """No row of attn_extend and attn_decode_prefix depends on finite values that are
 none of its business, however large: on another row's query, or on a key that
 its mask hides.  All comparisons are of bits."""
+import numpy as np
 import pytest
 import torch
 
 from int2_kv_cache_append_gb300 import oscar_kv as K
 from int2_kv_cache_append_gb300 import synth as S
+from oracle import oscar_oracle as O
 from tests.gpu_helpers import dev, dev_i32, dev_rot, kcfg
 from tests.test_gpu_rows import cfg_of, filled
 from tests.test_gpu_rows_streams import Prefix
@@ -79,3 +81,60 @@ def test_results_scale_with_a_query(D, n):
         res.append((out, lse))
     for out, lse in res[1:]:
         assert torch.equal(out, res[0][0]) and torch.equal(lse, res[0][1])
+
+
+@pytest.mark.parametrize("size", [1e8, 1e12, 1e30])
+@pytest.mark.parametrize("D,n,W,flags", [(128, 3, 40, 0), (128, 80, 200, 0), (128, 80, 200, K.FLAG_LLOYD_MAX), (256, 40, 100, 0),
+                                         (512, 12, 40, 0), (512, 40, 100, K.FLAG_V_BF16)])
+def test_a_large_hidden_key_or_value_row_leaves_earlier_tokens_alone(D, n, W, flags, size):
+    """The last position's BF16 rows times 1e8 to 1e30: the tokens before it do not see them."""
+    T = 300
+    c = cfg_of(D, 1, 8, 2, 4, W, T, flags)
+    cache, RK, RV, ch, rng = filled(c, [T], D + n)
+    kc, R = kcfg(c), (dev_rot(RK), dev_rot(RV))
+    q = dev(S.activations(rng, (1, n, 8, D), ch, mag=3.0), torch.bfloat16)
+    ws = torch.empty(K.attn_extend_workspace_bytes(kc, n), dtype=torch.uint8, device="cuda")
+    large = cache.copy()
+    for role in (0, 1):
+        view = O.CacheView(c, large, 0, role)
+        row = view.full[0, :, T - 1] if role and flags & K.FLAG_V_BF16 else view.ring[0, :, (T - 1) % W]
+        row[...] = O.f32_to_bf16_bits(O.bf16_bits_to_f32(row) * np.float32(size))
+    res = []
+    for x in (cache, large):
+        out, lse = torch.empty(1, n, 8, D, dtype=torch.bfloat16, device="cuda"), torch.empty(1, n, 8, device="cuda")
+        K.attn_extend(kc, torch.from_numpy(x).cuda(), 0, q, dev_i32([T]), *R, out, ws, lse=lse)
+        torch.cuda.synchronize()
+        res.append((out[:, :-1], lse[:, :-1]))
+    assert torch.equal(bits(res[0][0]), bits(res[1][0])) and torch.equal(bits(res[0][1]), bits(res[1][1]))
+
+
+@pytest.mark.parametrize("D,n,flags", [(128, 3, 0), (128, 80, 0), (128, 80, K.FLAG_LLOYD_MAX), (256, 40, 0), (512, 3, K.FLAG_LLOYD_MAX),
+                                       (512, 40, 0)])
+@pytest.mark.parametrize("size", [1e-3, 1e-5])
+def test_small_keys_keep_their_bits(D, n, flags, size):
+    """Keys of 1e-3 and 1e-5 against queries that bring the scores to ordinary size.  Without rotations a score is off
+    by some 2^-18 of the sum of its products' magnitudes (two fp16 parts of the query, sums that are cut off); 2^-14 is
+    allowed.  A middle or step that has lost its bits to fp16's smallest number is off by 2^-10 and more."""
+    T = 300
+    c = cfg_of(D, 1, 8, 2, 4, 40, T, flags)
+    rng = np.random.default_rng(D)
+    k, v = (S.to_bf16_values(S.activations(rng, (1, T, 2, D), [3, 70], mag=3.0)) for _ in range(2))
+    k = S.to_bf16_values(k * np.float32(size))
+    eye = np.eye(D, dtype=np.float32)
+    cache = O.new_cache(c)
+    O.append(c, cache, 0, k, v, [0], eye, eye)
+    q = S.to_bf16_values(S.activations(rng, (1, n, 8, D), [3, 70], mag=3.0) / np.float32(size))
+    kc = kcfg(c)
+    ws = torch.empty(K.attn_extend_workspace_bytes(kc, n), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty(1, n, 8, D, dtype=torch.bfloat16, device="cuda"), torch.empty(1, n, 8, device="cuda")
+    K.attn_extend(kc, torch.from_numpy(cache).cuda(), 0, dev(q), dev_i32([T]), dev_rot(eye), dev_rot(eye), out, ws, lse=lse)
+    torch.cuda.synchronize()
+    got = lse.cpu().numpy().astype(np.float64)
+    for h in range(8):
+        x = O.dequant_history(c, cache, 0, 0, 0, h // 4, T).astype(np.float64)
+        s = q[0, :, h].astype(np.float64) @ x.T / D ** 0.5
+        s[np.arange(T)[None, :] > (T - n + np.arange(n))[:, None]] = -np.inf
+        top = s.max(1)
+        want = top + np.log(np.exp(s - top[:, None]).sum(1))
+        lim = 2.0 ** -14 * (np.abs(q[0, :, h]).astype(np.float64) @ np.abs(x).T).max(1) / D ** 0.5
+        assert (np.abs(got[0, :, h] - want) <= lim).all(), (h, np.abs(got[0, :, h] - want).max(), lim.min())
