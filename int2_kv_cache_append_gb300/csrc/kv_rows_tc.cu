@@ -7,8 +7,8 @@
 // A CTA keeps its NC columns of the matrix in shared memory as fp16 values,
 // split into two parts where the result is float32 or a query, and walks the
 // row tiles.  X is expanded to fp16 operands in units of 64 channels: cached
-// INT2 rows as s (c - 1) / 2 with the middles as a rank-one term (exact; see
-// expand_k), other rows scaled by a power of two per row, with a second set of
+// INT2 rows as s (c - 1) with the middles as a rank-one term (see expand_k), all
+// rows scaled by a power of two per row, the others with a second set of
 // units for the rounding residues where the result is float32; merged rows are
 // such operands already.  A bf16 result takes one product, R and X rounded to
 // fp16 (2^-12 each, against 2^-9 of the output); a query from bf16 two; a
@@ -211,19 +211,23 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
       if (pos >= 0 && pos < T) ref = row_ref(g, a.r.layer_base, role, int64_t(b) * g.Hkv + h, T, int(pos));
       return ref;
     };
-    // INT2 codes and the scale / zero pair, a group ahead
+    // INT2 codes a group ahead, scale / zero pairs a row ahead
     RowRef ref{nullptr, nullptr, nullptr}, next{nullptr, nullptr, nullptr};
     uint4 q0, q1, n0 = make_uint4(0, 0, 0, 0), n1 = n0;
-    __half2 pair = __half2(), npair = __half2();
+    __half2 pairs[DG], npairs[DG];
     auto fetch_codes = [&](const RowRef& from, int gr) {
       if (!from.codes) return;
       n0 = __ldg(reinterpret_cast<const uint4*>(from.codes) + 2 * gr);
       n1 = __ldg(reinterpret_cast<const uint4*>(from.codes) + 2 * gr + 1);
-      npair = __ldg(from.sz + gr);
+    };
+    auto fetch_pairs = [&](const RowRef& from) {
+#pragma unroll
+      for (int gr = 0; gr < DG; ++gr) npairs[gr] = from.codes ? __ldg(from.sz + gr) : __half2();
     };
     if (SRC == kRead && p < mine) {
       next = cached((int64_t(blockIdx.x) + int64_t(p) * gridDim.x) * 128 + r);
       fetch_codes(next, 0);
+      fetch_pairs(next);
     }
 #pragma unroll 1
     for (int j = p; ok && j < mine; j += 2) {
@@ -238,6 +242,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
         b16 = ref.wide;
         next = j + 2 < mine ? cached(row + 2 * int64_t(gridDim.x) * 128) : RowRef{nullptr, nullptr, nullptr};
         if (next.wide) prefetch_row<DG>(next.wide);
+#pragma unroll
+        for (int gr = 0; gr < DG; ++gr) pairs[gr] = npairs[gr];
+        fetch_pairs(next);
       } else if (SRC == kQuery) {
         if (row_live(row, rows, a.q.q_lens, a.q.n, a.q.Hq)) {
           if (a.q.in_fp32) f32 = static_cast<const float*>(a.q.q) + row * D;
@@ -284,7 +291,17 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
         if (!finite) status_or(status, OSCAR_DEV_NONFINITE);
         up *= a.q.qscale;
       }
-      if (SRC == kRead && ref.codes) up = 2.0f, down = 0.5f;
+      if (SRC == kRead && ref.codes) {  // as expand_k, always scaled: the largest value is just below 2^13
+        float m = 0.f;
+#pragma unroll
+        for (int gr = 0; gr < DG; ++gr) {
+          const float2 sz = __half22float2(pairs[gr]);
+          m = fmaxf(m, fmaxf(fabsf(sz.y), fabsf(fmaf(sz.x, g.lm ? kLmSpan : 3.0f, sz.y))));
+        }
+        const int e = isfinite(m) ? (int(__float_as_uint(m)) >> 23) - 126 - 13 : 1;  // -36 .. 6 for fp16 pairs
+        down = m > 0.f ? pow2i(-e) : 0.f;
+        up = m > 0.f ? pow2i(e) : 0.f;
+      }
       const int acc = j % kAcc;
       if (j >= kAcc) ok = ok && wait(acc_empty + 8 * acc, ((j / kAcc) & 1) ^ 1);
       factor[acc * 128 + r] = up * (1.0f / kMatrixScale);
@@ -296,11 +313,13 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
         uint32_t w[4];
         float2 sz = make_float2(0.f, 0.f);
         if (SRC == kRead && half == 0) {
-          q0 = n0, q1 = n1, pair = npair;
+          q0 = n0, q1 = n1;
           fetch_codes(gr + 1 < DG ? ref : next, gr + 1 < DG ? gr + 1 : 0);
         }
         if (SRC == kRead && ref.codes) {
-          sz = __half22float2(pair);
+#pragma unroll
+          for (int j = 0; j < DG; ++j)
+            if (j == gr) sz = __half22float2(pairs[j]);
           if (role == 0) {  // word 2 c + half: pair c of every 16-byte chunk
             w[0] = half ? q0.y : q0.x, w[1] = half ? q0.w : q0.z, w[2] = half ? q1.y : q1.x, w[3] = half ? q1.w : q1.z;
           } else {          // words 2 m and 2 m + 1, codes 8 half ..: pair m
@@ -317,9 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
           if (SRC == kRead && ref.codes) {
             if (half == 0 && set == 0)
               *reinterpret_cast<uint2*>(sm + L::oRank + p * kRank + rank_offset(r, 4 * gr)) =
-                  rank_key(fmaf(g.lm ? kLmMiddle : 1.0f, sz.x, sz.y) * 0.5f);
-            const uint32_t s1 = half2_of(sz.x * 0.5f, sz.x * 0.5f);
-            const float unit = sz.x * (0.5f / 150.0f);
+                  rank_key(fmaf(g.lm ? kLmMiddle : 1.0f, sz.x, sz.y) * down);
+            const uint32_t s1 = half2_of(sz.x * down, sz.x * down);
+            const float unit = sz.x * (down / 150.0f);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint32_t v[4], o[4];
@@ -331,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_mm_kernel(const __grid_const
                 if (!g.lm) {
                   v[c] = hmul2(v[c], s1);
                   o[c] = hmul2(o[c], s1);
-                } else {  // (level - middle) s / 2 in float32, split
+                } else {  // (level - middle) s in float32, split
                   v[c] = lm_part(lm_value(v[c]), unit, set);
                   o[c] = lm_part(lm_value(o[c]), unit, set);
                 }
