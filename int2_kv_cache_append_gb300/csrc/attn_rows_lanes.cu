@@ -11,8 +11,8 @@
 // The arithmetic is that of the token-lane kernel (attn_rows_tc.cu): INT2 keys
 // as exact fp16 values and a rank-one term, queries as two fp16 values, value
 // rows with an exponent of their own that joins the score.  A row's reference M
-// follows its maximum only when that has grown by 2^12 (P is fp16), and then its
-// warps rescale their rows of O.
+// lies 8 below its maximum when it is chosen and follows it only when that has
+// grown by 2^7 (P is fp16), and then its warps rescale their rows of O.
 //
 // Eight softmax warps: warp w has rows 32 (w mod 4) .. + 31 and the tokens of
 // half w / 4; the two threads of a row exchange their maxima once per tile.  Two
@@ -41,7 +41,8 @@ constexpr int D = 128;
 constexpr int kSoftWarps = 8;
 constexpr int kThreads = (kSoftWarps + 4 + 4 + 1) * 32;
 constexpr float kNone = -1e30f;         // M before the first visible position
-constexpr float kGrow = 12.f;           // log2 of the largest P
+constexpr float kTop = 15.f;            // log2 of the largest P (fp16 below 2^16)
+constexpr float kBelow = 8.f;           // a new M lies this far below its row's maximum
 constexpr int KU = 4, VU = 4, CB = 4, kStages = 4;  // two tiles of K and of V units
 constexpr int oK = 0;
 constexpr int oV = oK + KU * kUnit;
@@ -276,10 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
         break;
       }
       top = fmaxf(top, swap[(i & 1) * 2 * N + (half ^ 1) * N + row]);
-      const bool grow = top > M + kGrow;
+      const bool grow = top > M + kTop;
       if (__any_sync(0xffffffffu, grow)) {
-        const float f = grow ? exp2f(M - top) : 1.f;
-        if (grow) M = top;
+        const float f = grow ? exp2f(M - (top - kBelow)) : 1.f;
+        if (grow) M = top - kBelow;
         l2 = mul2(l2, splat_x2(f));
         if (i > 0) {
           ok = wait(p_done, (i - 1) & 1);  // O is not in use
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
       }
       // P, over the scores
       const uint64_t n2 = splat_x2(-M);
-      uint64_t sum = 0;
+      uint64_t sum = 0, sum1 = 0;  // of this tile, so that l takes one rounding a tile
       if (plain) {
         const uint64_t phi2 = splat_x2(phi);
 #pragma unroll
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
             w = ex2z(w);
             p[j] = half2_of(v, w);
             if (j & 1) sum = add2(sum, pack2(v, w));
-            else l2 = add2(l2, pack2(v, w));
+            else sum1 = add2(sum1, pack2(v, w));
           }
           tmem_st16(S + c / 2, p);
         }
@@ -329,13 +330,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_lanes_kernel(const Rows
             for (int q = 0; q < 4; ++q) v[q] = ex2z(v[q]);
             p[j] = half2_of(v[0], v[1]);
             p[j + 1] = half2_of(v[2], v[3]);
-            l2 = fma2(pack2(v[0], v[1]), y.x, l2);
+            sum1 = fma2(pack2(v[0], v[1]), y.x, sum1);
             sum = fma2(pack2(v[2], v[3]), y.y, sum);
           }
           tmem_st16(S + c / 2, p);
         }
       }
-      l2 = add2(l2, sum);
+      l2 = add2(l2, add2(sum, sum1));
       // every warp sees every phase of p_done: the next one cannot complete before this warp's arrival below
       if (i > 0) ok = ok && wait(p_done, (i - 1) & 1);
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");

@@ -18,12 +18,15 @@
 //     products' sums are scores of float32 accuracy.
 //   * Probabilities carry the value row's exponent: with v_t = 2^(e_t) w_t, |w| < 1,
 //     u = score + e_t, P = 2^(u - M) in fp16 and l += 2^(-e_t) 2^(u - M) in float32.
-//     Value rows w in fp16 and P round with 2^-12 each, far below the bf16
-//     output's 2^-9; without the exponent BF16 rows could leave fp16's range.
+//     Value rows w in fp16 and P round with 2^-11 each, far below the bf16
+//     output's 2^-8; without the exponent BF16 rows could leave fp16's range.
 //   * The running reference M of a row need not be its maximum: P may reach
 //     2^15.  A tile is computed with the M at hand; only when some t = u - M
 //     exceeds 15 (the first tile, and rarely later) its columns get the maximum
-//     as M, O^T and l are rescaled and P is computed again.  One barrier with an
+//     less 8 as M, O^T and l are rescaled and P is computed again.  Below 2^-14 P
+//     is off by up to 2^-25, so with the maximum at 2^8 or above a weight is off
+//     by 2^-33 of the largest; with M at the maximum every weight below 2^-25 of
+//     it would be lost, 2^-8 of the sum beside 131,072 of them.  One barrier with an
 //     OR per tile decides; no reduction over tokens is made otherwise.
 //   * A value row that is not finite enters as zero with exponent NaN: rows that
 //     see the token become NaN, rows that do not keep their values.
@@ -55,6 +58,7 @@ constexpr int kSoftWarps = 8;
 constexpr int kThreads = (kSoftWarps + 4 + 4 + 1) * 32;
 constexpr float kNone = -1e30f;        // M before the first tile
 constexpr float kTop = 15.f;           // largest t = u - M that P holds (fp16 below 2^16)
+constexpr float kBelow = 8.f;          // a new M lies this far below its tile's maximum
 
 // Shared memory and TMEM of one instantiation.
 template <int DG, int N>
@@ -299,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_tc_kernel(const RowsArg
           const float M = -negM[c0 + tok];
           float f = 1.f;
           if (mx - M > kTop) {
-            f = exp2f(M - mx);
-            negM[c0 + tok] = -mx;
+            f = exp2f(M - (mx - kBelow));
+            negM[c0 + tok] = kBelow - mx;
           }
           factor[c0 + tok] = f;
         }
