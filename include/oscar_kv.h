@@ -317,6 +317,7 @@ int attn_decode_static(const oscar_kv_config* cfg, const void* cache, int32_t la
  *              Positions outside [0, seq_lens[b]) leave their rows as they were.
  *              With OSCAR_FLAG_ABSORB_V v_out receives the rotated rows v'.
  * A seq_len above capacity is clamped to it and sets OSCAR_DEV_OVER_CAPACITY.
+ * n = 0 does nothing (k_out and v_out may then both be NULL).
  */
 int kv_read(const oscar_kv_config* cfg, const void* cache, int32_t layer, const int32_t* start_pos,
             const int32_t* seq_lens, int32_t n, const float* R_K, const float* R_V, void* k_out, void* v_out,
@@ -361,7 +362,8 @@ int kv_read(const oscar_kv_config* cfg, const void* cache, int32_t layer, const 
  * probability below 2^-22 of its row's largest to 2^-33 of that), for many rows
  * the merged rows and R_V in the un-rotation, too.  OSCAR_DEV_TIMEOUT in
  * dev_status: a bounded wait inside a kernel ran out and out is not valid.
- * n_new = 0 does nothing; n_new > capacity is OSCAR_ERR_CAPACITY.
+ * n_new = 0 does nothing (q, out, lse and workspace may then be NULL); n_new >
+ * capacity is OSCAR_ERR_CAPACITY.
  */
 int attn_extend_workspace_query(const oscar_kv_config* cfg, int32_t n_new, uint64_t* bytes);
 int attn_extend(const oscar_kv_config* cfg, const void* cache, int32_t layer, const void* q, int32_t n_new,

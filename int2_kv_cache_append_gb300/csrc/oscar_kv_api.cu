@@ -373,7 +373,8 @@ int kv_read(const oscar_kv_config* cfg, const void* cache, int32_t layer, const 
   if (v != OSCAR_OK) return v;
   const bool had = (cfg->flags & OSCAR_FLAG_HADAMARD) != 0;
   if (had) R_K = R_V = nullptr;
-  if (!cache || !start_pos || !seq_lens || (!had && (!R_K || !R_V)) || (!k_out && !v_out)) return OSCAR_ERR_INVALID;
+  // no positions: the output of an empty tensor may be NULL
+  if (!cache || !start_pos || !seq_lens || (!had && (!R_K || !R_V)) || (!k_out && !v_out && n != 0)) return OSCAR_ERR_INVALID;
   if (layer < 0 || layer >= cfg->num_layers || n < 0) return OSCAR_ERR_INVALID;
   if (!aligned(cache, 256) || !aligned(R_K, 16) || !aligned(R_V, 16) || !aligned(k_out, 16) || !aligned(v_out, 16))
     return OSCAR_ERR_INVALID;
@@ -413,7 +414,8 @@ int attn_extend(const oscar_kv_config* cfg, const void* cache, int32_t layer, co
   if (v != OSCAR_OK) return v;
   const bool had = (cfg->flags & OSCAR_FLAG_HADAMARD) != 0;
   if (had) R_K = R_V = nullptr;
-  if (!cache || !q || !seq_lens || (!had && (!R_K || !R_V)) || !out || !workspace) return OSCAR_ERR_INVALID;
+  // no tokens: their empty tensors may be NULL, as may the workspace, whose size is then 0
+  if (!cache || !seq_lens || (!had && (!R_K || !R_V)) || (n_new != 0 && (!q || !out || !workspace))) return OSCAR_ERR_INVALID;
   if (layer < 0 || layer >= cfg->num_layers || n_new < 0 || num_splits < 0 || num_splits > OSCAR_KV_MAX_SPLITS ||
       seq_len_hint < 0)
     return OSCAR_ERR_INVALID;
