@@ -325,7 +325,8 @@ int kv_read(const oscar_kv_config* cfg, const void* cache, int32_t layer, const 
 
 /*
  * attn_extend — attention of several new tokens per sequence over the cache:
- * a chunk of a prompt, or drafted tokens to be verified.  Append their K and V
+ * a chunk of a prompt, or drafted tokens to be verified (see below for the
+ * drafts that are refused).  Append their K and V
  * first (kv_append); the q_lens[b] query tokens are the last ones of the
  * sequence: token t sits at position p = seq_lens[b] - q_lens[b] + t and
  * attends to every position <= p, each as attn_decode sees it at length
@@ -370,6 +371,21 @@ int attn_extend(const oscar_kv_config* cfg, const void* cache, int32_t layer, co
                 const int32_t* q_lens, const int32_t* seq_lens, int32_t seq_len_hint, const float* R_K,
                 const float* R_V, float sm_scale, int32_t num_splits, void* out, float* lse, void* workspace,
                 uint64_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * Sequences that become shorter: attn_extend over drafted tokens of which the
+ * last r are refused, the sequence going on at a length T' that is r less.
+ * kv_append of the n drafts (n <= recent; with more of them, accepted rows are
+ * missing from the ring as well) has overwritten ring slots that held the
+ * oldest rows of the window, and at length T' the positions T' - recent ..
+ * T' - recent + r - 1 that are >= sink are read from those slots again: they
+ * would give the refused rows, in every read until the ring has turned past
+ * them.  Copy the slots p mod recent of the drafts' positions p, of every layer
+ * and of both roles (K alone with OSCAR_FLAG_V_BF16), before the append and put
+ * back those of the refused positions p >= T' (oscar_kv.ring_rows gives the
+ * rings as tensors).  Nothing else is to be undone: sink and INT2 rows at or
+ * beyond the length are not read, and with recent = 0 there is no ring.
+ */
 
 /*
  * attn_decode_prefix — attn_decode for a batch whose sequences share a prefix:

@@ -7,6 +7,7 @@ has not been built: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass, field
 
@@ -236,6 +237,29 @@ def layout_query(cfg: KVConfig) -> dict:
     if rc != 0:
         raise OscarError("kv_layout_query", rc)
     return {name: getattr(out, name) for name, _ in _Layout._fields_}
+
+
+def ring_rows(cfg: KVConfig, cache, layer: int):
+    """The rings of a layer as views of the cache: (K, V), each [batch][num_kv_heads][recent][head_dim] bf16, position p
+    in slot p % recent; V is None with FLAG_V_BF16, whose V role keeps every position.
+
+    For a sequence that gets shorter, as by refused drafts: an append overwrites the oldest rows of the window, which the
+    shorter sequence reads again.  Keep ``ring[b, :, slots]`` of the drafts' positions before the append and put back the
+    refused ones' (at most ``recent`` drafts; include/oscar_kv.h, attn_extend)."""
+    torch = _dt()
+    _check_cache(cfg, cache)
+    if not cache.is_contiguous():
+        raise ValueError("oscar_kv: expected a contiguous tensor")
+    if not 0 <= layer < cfg.num_layers:
+        raise ValueError(f"oscar_kv: layer {layer} of {cfg.num_layers}")
+    lay = layout_query(cfg)
+    shape = (cfg.batch, cfg.num_kv_heads, cfg.recent, cfg.head_dim)
+
+    def view(role):
+        at = layer * lay["layer_bytes"] + role * lay["role_bytes"] + lay["sink_bytes"]
+        return cache.view(-1)[at:at + 2 * math.prod(shape)].view(torch.bfloat16).view(shape)
+
+    return view(0), None if cfg.flags & FLAG_V_BF16 else view(1)
 
 
 def kv_append(cfg: KVConfig, cache, layer: int, k_new, v_new, start_pos, R_K, R_V, debug_rot=None,
