@@ -8,7 +8,10 @@
 // takes every eighth position of the scores and D / 8 channels of the output.
 // What bounds it: shared-memory reads (one 16-byte read per four FMAs in
 // P V, five per sixteen in Q K^T).  No size of it has been made fast: it is
-// there for its precision.
+// there for its precision.  A chunk of 2048 tokens x 64 heads over 16,384
+// positions takes 62 ms, 64 sequences x 64 heads on a prefix of 131,072 40 ms:
+// both longer than the formula in elementary float32 tensor operations (40 and
+// 23 ms) and 45 to 90 times the bf16 output's kernels.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -165,6 +168,7 @@ int launch(const RowsArgs& a, cudaStream_t stream) {
 }  // namespace
 
 int rows_splits(const Geom& g, int64_t rows, int seq_len_hint) {
+  // two CTAs on each of 152 SMs, whichever device there is (as rows_splits_tc)
   const int64_t items = (rows + kRowTile - 1) / kRowTile * g.B * g.Hkv;
   const int64_t blocks = (int64_t(seq_len_hint) + kSplitUnit - 1) / kSplitUnit;
   return int(std::max<int64_t>(1, std::min<int64_t>({OSCAR_KV_MAX_SPLITS, 304 / items, blocks})));

@@ -25,8 +25,8 @@
 // What bounds it: the hand-overs from the products to the softmax to the next
 // products, and beside them the V expanders, busy all the time.  A tile takes
 // about 2850 cycles, of which the tensor cores need 1600; without the expansion,
-// or without the softmax, it would still take three quarters of that.  A chunk of 2048 tokens x 32
-// heads over 16,384 positions (4 sequences, 8 KV heads): 1.28 ms, 0.8 PFLOP/s
+// or without the softmax, it would still take three quarters of that.  A chunk of 2048 tokens x 64
+// heads over 16,384 positions (one sequence, 8 KV heads): 1.28 ms, 0.8 PFLOP/s
 // of products that the operator needs (the low part of Q doubles those of the
 // scores).
 #include <algorithm>

@@ -39,9 +39,10 @@
 //
 // What bounds it: the expansion, 16-bit arithmetic on every code and its stores
 // to shared memory, by the eight expanding warps; per tile of 128 positions and
-// group about 4200 cycles with INT2 rows and 10,000 where the rows are BF16
-// (their loads' latency).  16,384 positions with INT2 rows only, 8 KV heads: 106
-// us for 8 sequences x 5 tokens at D = 128, 271 us for 4 x 32 tokens at D = 512.
+// group about 4200 cycles with INT2 rows and three times that where the rows are
+// BF16 (their loads' latency).  16,384 positions, 8 KV heads, 8 sequences x 5
+// tokens at D = 128: 106 us with INT2 rows only, 346 us with BF16 rows only; 4 x
+// 32 tokens at D = 512, INT2 rows only: 284 us.
 // Twice the expanding warps (which halves the registers) were slower, as were
 // rolled loops and reading BF16 rows by whole warps, line by line.
 //
@@ -519,7 +520,7 @@ int launch(const RowsArgs& a, cudaStream_t stream) {
 // Query rows per CTA: the least of 32, 64 (D > 128) or 128 that holds a unit's rows, because a CTA with more columns costs
 // little more and the keys are expanded once.  D = 128 with more than 32 rows goes to the row-lane kernel; us a call here
 // with 64 rows a CTA and there: 8 sequences x 9 / 12 / 16 tokens x 4 heads a KV head (36 / 48 / 64 rows) over 4096 positions
-// 71 / 83 / 87 and 60 / 69 / 75, 512 rows on one prefix of 131,072 positions 808 and 450.  32 rows: 62 here, 69 with 64.
+// 71 / 83 / 87 and 61 / 69 / 75, 512 rows on one prefix of 131,072 positions 808 and 450.  32 rows: 62 here, 69 with 64.
 int tile_rows(int D, int64_t rows) {
   if (rows <= 32) return 32;
   return D > 128 ? 64 : 128;
@@ -531,7 +532,8 @@ int rows_splits_tc(const Geom& g, int64_t rows, int seq_len_hint) {
   const int N = tile_rows(g.D, rows);
   const int64_t items = (rows + N - 1) / N * g.B * g.Hkv;
   const int64_t blocks = (int64_t(seq_len_hint) + kTok - 1) / kTok;
-  // Time of ns splits: waves of CTAs on 152 SMs, each its tiles and a fixed part worth `fixed` tiles (queries, set-up, the
+  // Time of ns splits: waves of CTAs on 152 SMs (written in, because the workspace query gives the same answer without a
+  // device and results do not depend on the one that runs them), each its tiles and a fixed part worth `fixed` tiles (queries, set-up, the
   // first tile's latency, the merge).  With 3 in place of 6, 64 sequences on one prefix took 512 us, with 6 or 10 490 us;
   // the other sizes measured did not change.
   const double fixed = 6.0;
@@ -543,8 +545,8 @@ int rows_splits_tc(const Geom& g, int64_t rows, int seq_len_hint) {
   for (int ns = 2; ns <= most; ++ns)
     if (time(ns) < time(best) * 0.98) best = ns;
   // Sequences of a batch differ in length, and shorter shares even that out: the most of them that cost at most a tenth
-  // more on equal lengths.  5 tokens for each of 8 sequences of up to 16,384: 2 / 4 / 7 / 9 / 14 shares 173 / 157 / 146 /
-  // 144 / 161 us.
+  // more on equal lengths.  5 tokens for each of 8 sequences of up to 16,384: 2 / 4 / 7 / 9 / 14 shares 176 / 159 / 150 /
+  // 149 / 166 us.
   if (g.B > 1) {
     const double limit = time(best) * 1.1;
     for (int ns = best + 1; ns <= most; ++ns)

@@ -18,11 +18,11 @@
 // products, four warps scale and store the result of the previous tile.
 //
 // What bounds it: at D = 128 the expansion and the stores (kv_read of 4 x 8192
-// positions, 8 KV heads: 66 us, 2.4 TB/s, a third of the copy rate).  At larger
+// positions, 8 KV heads: 64 us, 2.5 TB/s, a third of the copy rate).  At larger
 // D a row is expanded again for every NC columns, up to 8 times at D = 512, and
 // the latency of BF16 rows counts, which are read once more for their largest
-// value: 4 x 4099 positions at D = 512 take 220 us as INT2 rows into bf16, 500
-// us into float32 and 1.04 ms with 2560 BF16 rows among them.  Reading those
+// value: 4 x 4099 positions at D = 512 take 208 us as INT2 rows into bf16, 490
+// us into float32, and 486 us and 1.05 ms with 2560 BF16 rows among them.  Reading those
 // rows by whole warps, line by line, was slower (1.33 ms).  Every wait is
 // bounded, as in the attention kernels.
 #include <algorithm>

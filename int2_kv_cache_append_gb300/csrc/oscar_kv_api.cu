@@ -278,10 +278,10 @@ int validate_prefix(const oscar_kv_config* cfg, const oscar_kv_config* pcfg) {
 // Longest own cache that attn_decode_prefix gives to the row attention, which
 // runs beside the prefix's; longer ones go to attn_decode's kernels, which take
 // about 20 us more to begin with and less per position.  Row attention against
-// those, us a call: 8 sequences x 8 KV heads with 64 / 512 positions 36 / 48
-// against 54 / 56, 32 x 8 with 64 / 256 / 512 / 1024 62 / 75 / 85 / 95 against
-// 65 / 71 / 73 / 77, at D = 512 with 64 / 256 / 512 153 / 222 / 257 against
-// 208 / 230 / 239.
+// those on a prefix of 2048 positions, us a call: 8 sequences x 8 KV heads with
+// 64 / 512 / 1024 positions 37 / 47 / 49 against 52 / 55 / 55, 32 x 8 with 64 /
+// 256 / 512 / 1024 57 / 71 / 82 / 94 against 65 / 68 / 72 / 75, 8 x 8 at D = 512
+// with 64 / 256 / 512 / 1024 69 / 92 / 118 / 120 against 117 / 127 / 129 / 133.
 constexpr int kOwnRows = 1024, kOwnTiles = 512;  // positions; tiles of 128 in all
 int own_rows_limit(const Geom& g) {
   return int(std::min<int64_t>(kOwnRows, kOwnTiles / (int64_t(g.B) * g.Hkv) * 128));

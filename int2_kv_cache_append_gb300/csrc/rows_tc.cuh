@@ -443,9 +443,9 @@ constexpr int kRawStage = kTok * 36;  // staged codes (32 bytes) and scale / zer
 constexpr int kRank = kTok * 32;      // one tile's rank-one operand
 
 // First tile of share s of ns.  Tiles with BF16 rows take about kWideCost times an INT2 tile's time, and the shares are of
-// equal time: 32 tokens over 16,384 positions at D = 512 with windows of 512 + 2048 took 743 / 661 / 583 / 581 us with
-// costs of 1 / 2 / 3 / 4, a chunk at D = 128 least with 3.
-constexpr int kWideCost = 3;
+// equal time: 32 tokens over 16,384 positions at D = 512 with windows of 512 + 2048 take 608 / 528 / 448 / 423 us with
+// costs of 1 / 2 / 3 / 4, 5 drafted tokens at D = 128 191 / 157 / 154 / 146 us, a chunk of 2048 the same with all of them.
+constexpr int kWideCost = 4;
 __device__ __forceinline__ int share_start(const Geom& g, int T, int blocks, int s, int ns) {
   const int w = g.vb ? 1 : kWideCost;
   const int lo = min(blocks, (g.S + kTok - 1) / kTok), hi = min(blocks, max(lo, (T - g.W) / kTok));  // INT2 tiles: lo .. hi - 1
