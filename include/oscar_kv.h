@@ -136,7 +136,9 @@ typedef enum {
   OSCAR_ERR_WORKSPACE = -3,   /* workspace smaller than one split needs */
   OSCAR_ERR_LAUNCH = -4,      /* a CUDA launch or attribute call failed */
   OSCAR_ERR_UNSUPPORTED = -5  /* head_dim not in {128, 256, 512}, group != 128, G > 8, or a decode
-                                 whose B * Hkv * (S, W or, with OSCAR_FLAG_V_BF16, capacity) >= 2^31 */
+                                 whose B * Hkv * (S, W or, with OSCAR_FLAG_V_BF16, capacity) >= 2^31, or
+                                 an attn_extend or attn_decode_prefix over a capacity above 2^31 - 1025
+                                 or of 2^31 and more query rows */
 } oscar_status;
 
 /* bits OR-ed into *dev_status by the kernels */

@@ -251,8 +251,12 @@ int launch_rows(const oscar_kv_config* cfg, const oscar::RowsArgs& a, cudaStream
   return (cfg->flags & OSCAR_FLAG_OUT_FP32) ? oscar::launch_attn_rows(a, st) : oscar::launch_attn_rows_tc(a, st);
 }
 
-// The row kernels count rows and workspace slots in ranges of these limits.
-bool rows_supported(const Geom& g, int64_t n) { return n * g.G < (int64_t(1) << 30) && g.B * n * g.Hq < (int64_t(1) << 31); }
+// The row kernels count rows and workspace slots in ranges of these limits, and
+// positions in 32 bits up to a few tiles behind the last one.
+constexpr int kMostPositions = 0x7fffffff - 1024;
+bool rows_supported(const Geom& g, int64_t n) {
+  return n * g.G < (int64_t(1) << 30) && g.B * n * g.Hq < (int64_t(1) << 31) && g.cap <= kMostPositions;
+}
 
 // The largest split count up to `want` whose workspace fits, 0 if none does;
 // an explicit count has to fit in full.
@@ -272,7 +276,7 @@ int validate_prefix(const oscar_kv_config* cfg, const oscar_kv_config* pcfg) {
   if (pcfg->batch != 1 || pcfg->num_q_heads != cfg->num_q_heads || pcfg->num_kv_heads != cfg->num_kv_heads ||
       pcfg->head_dim != cfg->head_dim || pcfg->flags != cfg->flags)
     return OSCAR_ERR_INVALID;
-  return rows_supported(make_geom(pcfg), cfg->batch) ? OSCAR_OK : OSCAR_ERR_UNSUPPORTED;
+  return rows_supported(make_geom(pcfg), cfg->batch) && cfg->capacity <= kMostPositions ? OSCAR_OK : OSCAR_ERR_UNSUPPORTED;
 }
 
 // Longest own cache that attn_decode_prefix gives to the row attention, which
