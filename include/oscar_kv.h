@@ -362,7 +362,8 @@ int kv_read(const oscar_kv_config* cfg, const void* cache, int32_t layer, const 
  * so scores and lse have float32 accuracy
  * (relative 1e-6, the tensor cores' sums being cut off rather than rounded);
  * probabilities and value rows are rounded to fp16 (relative 2^-11 each; a
- * probability below 2^-22 of its row's largest to 2^-33 of that), for many rows
+ * probability below 2^-22 of its row's largest to 2^-33 of that, a value below
+ * 2^-6 of its row's largest to 2^-17 of that at worst), for many rows
  * the merged rows and R_V in the un-rotation, too.  OSCAR_DEV_TIMEOUT in
  * dev_status: a bounded wait inside a kernel ran out and out is not valid.
  * n_new = 0 does nothing (q, out, lse and workspace may then be NULL); n_new >

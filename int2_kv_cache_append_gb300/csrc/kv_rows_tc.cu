@@ -7,11 +7,11 @@
 // A CTA keeps its NC columns of the matrix in shared memory as fp16 values,
 // split into two parts where the result is float32 or a query, and walks the
 // row tiles.  X is expanded to fp16 operands in units of 64 channels: cached
-// INT2 rows as s (c - 1) with the middles as a rank-one term (see expand_k), all
-// rows scaled by a power of two per row, the others with a second set of
-// units for the rounding residues where the result is float32; merged rows are
+// INT2 rows as s (c - 1) with the middles as a rank-one term (see expand_k), every
+// row scaled by a power of two of its own, with a second set of units for the
+// rounding residues where the result is float32 and there are any; merged rows are
 // such operands already.  A bf16 result takes one product, R and X rounded to
-// fp16 (2^-12 each, against 2^-9 of the output); a query from bf16 two; a
+// fp16 (2^-11 each, against 2^-8 of the output); a query from bf16 two; a
 // float32 result two or three, 2^-22.
 //
 // Two groups of four warps expand alternate tiles, one warp issues the

@@ -471,7 +471,7 @@ struct Tiles {
 // rank-one term of 16 more k (rank_key), so the products' sums are the scores.
 // Lloyd-Max levels are the uniform ones plus 0.16 (0, 1, 1, 2): z + rho s is the
 // middle, and s (-rho, 0, 1, rho + 1) is rounded to fp16 with the residues in a
-// second set of units, which only Q's high part meets (2^-24 of a product is lost).
+// second set of units, which only Q's high part meets (up to 2^-22 of a product is lost).
 // BF16 keys are exact in fp16 within its range.  Every key row is scaled by a
 // power of two of its own, one half (which keeps 2 s and z + s within fp16) where
 // its largest value lies between 2^-2 and 2^14, else what brings that just below

@@ -51,9 +51,9 @@ def test_extend(D, n, T, flags):
     hidden = np.arange(T)[None, :] > (T - n + np.arange(n))[:, None]
     lm = bool(flags & K.FLAG_LLOYD_MAX)
     for h in range(8):
-        mid, steps, _ = B.pieces(c, cache, 0, 0, h // 4, T)
-        V = O.dequant_history(c, cache, 0, 1, 0, h // 4, T).astype(np.float64)
-        want, wlse, ob, lb = B.attend(q[0, :, h].astype(np.float64), mid, steps, V, hidden, D ** -0.5, lm)
+        mid, steps, _, factor = B.pieces(c, cache, 0, 0, h // 4, T)
+        V, floor = B.values(c, cache, 0, 0, h // 4, T)
+        want, wlse, ob, lb = B.attend(q[0, :, h].astype(np.float64), mid, steps, factor, V, floor, hidden, D ** -0.5, lm)
         check("lse", lse[0, :, h].double().cpu().numpy(), wlse, lb)
         check("out", out[0, :, h].double().cpu().numpy(), want, ob)
 
@@ -74,9 +74,9 @@ def test_prefix(D, batch, flags):
     for b in range(batch):
         for h in range(8):
             parts = [B.pieces(pc, pcache, 0, 0, h // 4, P), B.pieces(c, cache, 0, b, h // 4, lens[b])]
-            mid, steps = (np.concatenate([x[i] for x in parts]) for i in range(2))
-            V = np.concatenate([O.dequant_history(pc, pcache, 0, 1, 0, h // 4, P), O.dequant_history(c, cache, 0, 1, b, h // 4, lens[b])])
-            want, wlse, ob, lb = B.attend(q[b, :, h].astype(np.float64), mid, steps, V.astype(np.float64),
+            mid, steps, factor = (np.concatenate([x[i] for x in parts]) for i in (0, 1, 3))
+            V, floor = (np.concatenate(x) for x in zip(B.values(pc, pcache, 0, 0, h // 4, P), B.values(c, cache, 0, b, h // 4, lens[b])))
+            want, wlse, ob, lb = B.attend(q[b, :, h].astype(np.float64), mid, steps, factor, V, floor,
                                           np.zeros((1, P + lens[b]), bool), D ** -0.5, lm)
             check("lse", lse[b, h].double().cpu().numpy(), wlse[0], lb[0])
             check("out", out[b, h].double().cpu().numpy(), want[0], ob[0])

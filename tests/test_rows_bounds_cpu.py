@@ -24,12 +24,12 @@ def test_bounds(D, flags, parts):
     lm, scale = bool(flags), D ** -0.5
     worst = {d: 0.0 for d in ["", *parts]}
     for h in range(c.num_q_heads):
-        mid, steps, s = B.pieces(c, cache, 0, 0, h // c.G, T)
-        V = O.dequant_history(c, cache, 0, 1, 0, h // c.G, T)
+        mid, steps, s, factor = B.pieces(c, cache, 0, 0, h // c.G, T)
+        V, floor = B.values(c, cache, 0, 0, h // c.G, T)
         x = q[0, :, h].astype(np.float64)
         hidden = np.zeros((n, T), bool)
-        _, lse, _, lb = B.attend(x, mid, steps, V, hidden, scale, lm)
-        bound = B.score_bound(x, mid, steps, scale, lm)
+        _, lse, _, lb = B.attend(x, mid, steps, factor, V, floor, hidden, scale, lm)
+        bound = B.score_bound(x, mid, steps, factor, scale, lm)
         exact = scale * (x @ (steps + np.repeat(mid, 128, axis=1)).T)
         for d in worst:
             got = B.emulated_scores(x, mid, steps, s, scale, lm, d)
