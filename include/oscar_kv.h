@@ -420,6 +420,132 @@ int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const osca
                        uint64_t workspace_bytes, int32_t* dev_status, void* stream);
 
 /*
+ * Operators around the cache: what makes the rows that kv_append takes, the
+ * attention of a prompt before any of it is cached, and what shrinks a cache.
+ * (No counterpart on the pages.)  Of the configuration they use the heads,
+ * head_dim, batch and OSCAR_FLAG_IN_FP32 / _OUT_FP32, and what they say besides.
+ *
+ * Packed rows: the tokens of all sequences of a batch behind each other, n_rows in
+ * all; cu_seqlens (device int32 [B + 1], non-decreasing, within 0 .. n_rows) says
+ * where each begins: sequence b has the rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1,
+ * none if both are equal.  Rows before the first and behind the last sequence are
+ * not used, and of outputs left as they were.
+ */
+
+/*
+ * qk_norm_rope — root-mean-square norm of every query and key head, then the
+ * rotary position rotation, in one pass: with x one head's row,
+ *   y = x / sqrt(mean(x^2) + eps) * weight,
+ * and for i < rot_dim / 2 the pair (y[i], y[i + rot_dim / 2]), interleaved != 0:
+ * (y[2 i], y[2 i + 1]), turned by positions[t] * inv_freq[i]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin).
+ * Channels from rot_dim on are only normed.
+ *   q, k       device rows, bf16 (float32 with OSCAR_FLAG_IN_FP32): token t's heads
+ *              at t * q_stride (k_stride) elements, head_dim apart, as they lie in
+ *              the output of a fused projection.  16-byte aligned, strides a
+ *              multiple of 16 bytes.
+ *   q_weight, k_weight  device float32 [D], 16-byte aligned.
+ *   positions  device int32 [n_rows]; inv_freq device float32 [rot_dim / 2].  The
+ *              angle is taken modulo a turn in 64-bit fixed point, at any position.
+ *   rot_dim    a multiple of 16, at most D; 0: no rotation (positions and
+ *              inv_freq may then be NULL).
+ *   q_out, k_out  device [n_rows][Hq][D], [n_rows][Hkv][D] in the type of q and k,
+ *              16-byte aligned.  An output may be its own input when that is
+ *              dense; otherwise they must not overlap.
+ * Norm and rotation in float32, one rounding at the end.  n_rows = 0 does nothing.
+ */
+int qk_norm_rope(const oscar_kv_config* cfg, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                 int32_t n_rows, const float* q_weight, const float* k_weight, float eps, const int32_t* positions,
+                 const float* inv_freq, int32_t rot_dim, int32_t interleaved, void* q_out, void* k_out, void* stream);
+
+/*
+ * attn_prompt — causal attention of packed prompts over their own K and V, as they
+ * come from the projections (nothing cached, rotated or quantised): token t of a
+ * sequence attends to its tokens 0 .. t; query head i uses KV head i / (Hq / Hkv).
+ *   q, k, v    device [n_rows][Hq][D], [n_rows][Hkv][D] twice, bf16 (float32 with
+ *              OSCAR_FLAG_IN_FP32), 16-byte aligned.
+ *   sm_scale   softmax scale; <= 0 means 1/sqrt(D).
+ *   out        device [n_rows][Hq][D] bf16 (float32 with OSCAR_FLAG_OUT_FP32).
+ *   lse        device float32 [n_rows][Hq] or NULL: natural-log log-sum-exp.
+ * bf16 inputs and outputs are computed on the tensor cores: scores, softmax
+ * statistics and output sums in float32, probabilities rounded to bf16 (relative
+ * 2^-8) for their product with V.  Otherwise everything is float32.  What is not a
+ * number or infinite in K or V of a token reaches only the tokens that see it.
+ * Repeated calls give the same bits.  Bounds of cu_seqlens that are out of range or
+ * out of order are clamped and set OSCAR_DEV_OVER_CAPACITY.  n_rows = 0 does
+ * nothing; n_rows * Hq >= 2^31 is OSCAR_ERR_UNSUPPORTED.
+ */
+int attn_prompt(const oscar_kv_config* cfg, const void* q, const void* k, const void* v, int32_t n_rows,
+                const int32_t* cu_seqlens, float sm_scale, void* out, float* lse, int32_t* dev_status, void* stream);
+
+/*
+ * kv_append_packed — kv_append of packed rows: sequence b gets its
+ * n = cu_seqlens[b + 1] - cu_seqlens[b] new tokens at start_pos[b], with the codec, the
+ * windows (the ring has the last `recent` of its own n) and the results of a
+ * kv_append of these n rows to a cache of that sequence alone.
+ *   k_new, v_new  device [n_rows][Hkv][D] post-RoPE rows, bf16 (float32 with
+ *              OSCAR_FLAG_IN_FP32), 16-byte aligned.
+ * Other arguments and errors as kv_append.  Sequences without rows stay as they are;
+ * n_rows = 0 does nothing (k_new and v_new may then be NULL).
+ */
+int kv_append_packed(const oscar_kv_config* cfg, void* cache, int32_t layer, const void* k_new, const void* v_new,
+                     int32_t n_rows, const int32_t* cu_seqlens, const int32_t* start_pos, const float* R_K,
+                     const float* R_V, int32_t* dev_status, void* stream);
+
+/*
+ * attn_mass — the attention weight that every cached position receives from the
+ * last query tokens of its sequence, added up over tokens and the query heads of a
+ * KV head (for one decode step n_new = 1; for a prompt its last tokens):
+ *   mass_out[b][h][p] = mass_in[b][h][p] + sum over t < q_lens[b] and the query heads i of h,
+ *     p <= seq_lens[b] - q_lens[b] + t, of exp(sm_scale q[b][t][i] . k_p - lse[b][t][i]).
+ *   q, n_new, q_lens, seq_lens, seq_len_hint, sm_scale, R_K  as attn_extend.
+ *   lse        device float32 [B][n_new][Hq]: what attn_extend (attn_decode for
+ *              n_new = 1) returned; a token whose lse is -inf adds nothing.
+ *   mass_in    device float32 [B][Hkv][capacity] or NULL (= 0); mass_out the same
+ *              shape, may be mass_in.  Positions >= seq_lens[b] of mass_out are left
+ *              as they were.
+ *   workspace  device, 256-byte aligned, attn_mass_workspace_query bytes.
+ * Keys enter with float32 accuracy, sums are float32 in a fixed order (repeated calls give the
+ * same bits).  More than 65535 (sequence, KV head) pairs are OSCAR_ERR_UNSUPPORTED.
+ */
+int attn_mass_workspace_query(const oscar_kv_config* cfg, int32_t n_new, uint64_t* bytes);
+int attn_mass(const oscar_kv_config* cfg, const void* cache, int32_t layer, const void* q, int32_t n_new,
+              const int32_t* q_lens, const int32_t* seq_lens, int32_t seq_len_hint, const float* R_K, float sm_scale,
+              const float* lse, const float* mass_in, float* mass_out, void* workspace, uint64_t workspace_bytes,
+              int32_t* dev_status, void* stream);
+
+/*
+ * kv_evict — a layer of a cache, without the positions of least mass, into another
+ * cache.  With T = seq_lens[b], each KV head of a sequence keeps its sink
+ * [0, min(S, T)), its window [max(S, T - W), T) and of the n positions between them the
+ * min(n, keep) of largest mass, among equal ones those of lower position, in order of
+ * position.  They become positions 0 .. T' - 1 of the other cache, T' = T - n +
+ * min(n, keep), which then is as any cache of that length: rows are moved as they
+ * are, nothing is quantised again.  The heads of a sequence keep different positions.
+ *   mass       device float32 [B][Hkv][capacity] (attn_mass); what is not a number
+ *              counts as the least.
+ *   out_cfg    the other cache's configuration: num_layers, capacity and clips may
+ *              differ; capacity >= min(cfg->capacity, S + W + keep), else
+ *              OSCAR_ERR_CAPACITY.
+ *   out_cache  device; the layers read and written must not overlap.
+ *   out_mass   device float32 [B][Hkv][out_cfg->capacity] or NULL: the masses of the
+ *              positions that stay, 0 from T' on; must not overlap mass.
+ *   kept       device int32 [B][Hkv][keep] or NULL: the kept positions between sink
+ *              and window, -1 behind the last.
+ *   new_lens   device int32 [B]: T'; may be seq_lens.
+ *   workspace  device, 256-byte aligned, kv_evict_workspace_query bytes.
+ * Keys keep the position rotation that they were appended with: the next token's own
+ * (qk_norm_rope) goes on counting from T, its start_pos is T'.  A length above capacity
+ * is clamped and sets OSCAR_DEV_OVER_CAPACITY; one below 1 gives T' = 0.  More than 65535
+ * (sequence, KV head) pairs are OSCAR_ERR_UNSUPPORTED.
+ */
+int kv_evict_workspace_query(const oscar_kv_config* cfg, int32_t keep, uint64_t* bytes);
+int kv_evict(const oscar_kv_config* cfg, const void* cache, int32_t layer, const float* mass, const int32_t* seq_lens,
+             int32_t keep, const oscar_kv_config* out_cfg, void* out_cache, int32_t out_layer, float* out_mass,
+             int32_t* kept, int32_t* new_lens, void* workspace, uint64_t workspace_bytes, int32_t* dev_status,
+             void* stream);
+
+/*
  * oscar_kv_set_profile_events — measurement hook (no counterpart on the pages).
  * While both events are non-NULL (cudaEvent_t passed as void*), every
  * attn_decode call made from the calling host thread records `split_start` on

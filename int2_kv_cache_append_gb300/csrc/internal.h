@@ -21,12 +21,30 @@ struct AppendArgs {
   float* debug_rot;
   int32_t* status;
   int n_new;
-  int64_t rows;          // B * n_new * Hkv
+  int64_t rows;          // B * n_new * Hkv, or with cu all packed rows * Hkv
   float k_clip, v_clip;
   int in_fp32;
   int hadamard;          // rotate by the in-quant Hadamard (R_K, R_V unused)
   FastDiv div_hkv, div_n_new;  // set by the tensor-core launcher (rows < 2^31)
+  const int32_t* cu;     // [B + 1]: packed rows, sequence b's are cu[b] .. cu[b + 1] - 1; NULL: n_new of each
 };
+
+// Whose new token a packed row is: the sequence b with cu[b] <= row < cu[b + 1] (the search keeps both sides, so the token
+// index is never negative and below the count whatever cu holds), or none.
+struct NewToken {
+  int b, t, count;  // sequence (-1: none), its token, its new tokens
+};
+__device__ __forceinline__ NewToken packed_token(const int32_t* cu, int B, int64_t row) {
+  if (row < cu[0] || row >= cu[B]) return {-1, 0, 0};
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= row) lo = mid;
+    else hi = mid;
+  }
+  const int first = cu[lo];
+  return {lo, int(row - first), cu[hi] - first};
+}
 
 struct DecodeArgs {
   Geom g;
@@ -178,5 +196,69 @@ struct FinishArgs {
 };
 int launch_finish_rows(const FinishArgs& a, cudaStream_t stream);
 int launch_finish_rows_tc(const FinishArgs& a, cudaStream_t stream);
+
+// Norm and position rotation of query and key heads (norm_rope.cu).
+struct NormRopeArgs {
+  const void* q;          // token t's rows at t * q_stride, its heads D apart
+  const void* k;
+  int64_t q_stride, k_stride;  // elements
+  const float* q_weight;  // [D]
+  const float* k_weight;
+  const int32_t* positions;  // [n]
+  const float* inv_freq;  // [rot / 2]
+  void* q_out;            // [n][Hq][D]
+  void* k_out;            // [n][Hkv][D]
+  float eps;
+  int n, Hq, Hkv, D, rot, interleaved, fp32;
+  int tb;                 // tokens of a block's turn (set by the launcher)
+};
+int launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
+
+// Causal attention of packed prompts over their own K and V.
+struct PromptArgs {
+  const void* q;          // [n][Hq][D]
+  const void* k;          // [n][Hkv][D]
+  const void* v;
+  const int32_t* cu;      // [B + 1]
+  void* out;              // [n][Hq][D]
+  float* lse;             // [n][Hq] or NULL
+  int32_t* status;
+  int n, B, Hq, Hkv, G, D;
+  int in_fp32, out_fp32;
+  float qscale;           // sm_scale * log2(e)
+};
+int launch_attn_prompt(const PromptArgs& a, cudaStream_t stream);  // float32 (attn_prompt.cu)
+
+// Attention weight of every cached position (attn_mass.cu).
+struct MassArgs {
+  Geom g;
+  const uint8_t* layer_base;
+  const int32_t* seq_lens;  // [B]
+  const int32_t* q_lens;    // [B] or NULL (= n)
+  const float* qrot;        // [B][n][Hq][D] rotated queries in log2 units
+  const float* lse;         // [B][n][Hq]
+  const float* mass_in;     // [B][Hkv][cap] or NULL (= 0)
+  float* mass_out;
+  int32_t* status;
+  int n, top;               // top: no sequence is longer
+};
+int launch_attn_mass(const MassArgs& a, cudaStream_t stream);
+
+// Rows of largest mass and the windows into another cache (kv_evict.cu).
+struct EvictArgs {
+  Geom g, og;               // of the cache and of the one that is written
+  const uint8_t* base;
+  uint8_t* out_base;
+  const float* mass;        // [B][Hkv][cap]
+  const int32_t* seq_lens;  // [B]
+  int32_t* new_lens;        // [B]
+  float* out_mass;          // [B][Hkv][out cap] or NULL
+  int32_t* kept;            // [B][Hkv][keep] or NULL
+  int32_t* list;            // workspace: [B][Hkv][list_cap] kept positions
+  int32_t* lens;            // workspace: [B] lengths, clamped
+  int32_t* status;
+  int keep, list_cap;
+};
+int launch_kv_evict(const EvictArgs& a, cudaStream_t stream);
 
 }  // namespace oscar

@@ -40,6 +40,13 @@
 namespace oscar {
 namespace {
 
+// Token index bt of a batch of n_new tokens each, or of packed rows.
+__device__ __forceinline__ NewToken new_token(const AppendArgs& a, int64_t bt) {
+  if (a.cu) return packed_token(a.cu, a.g.B, bt);
+  return {int(bt / a.n_new), int(bt % a.n_new), a.n_new};
+}
+
+
 constexpr int kAppendThreads = 128;
 // appends of at most this many rows per role take the row-parallel kernel
 constexpr int64_t kSmallAppendRows = 1024;
@@ -130,10 +137,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
   const Geom& g = a.g;
   const int h = int(row % g.Hkv);
   const int64_t bt = row / g.Hkv;
-  const int t = int(bt % a.n_new);
-  const int b = int(bt / a.n_new);
-  const int p = a.start_pos[b] + t;
-  const int newlen = a.start_pos[b] + a.n_new;
+  const NewToken tok = new_token(a, bt);
+  if (tok.b < 0) return;
+  const int b = tok.b;
+  const int p = a.start_pos[b] + tok.t;
+  const int newlen = a.start_pos[b] + tok.count;
   const float* rr = rs + threadIdx.x * C::LD;
 
   if (a.debug_rot) {
@@ -415,10 +423,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_rows_kernel(const Ap
     }
     const int h = int(row % g.Hkv);
     const int64_t bt = row / g.Hkv;
-    const int t = int(bt % a.n_new);
-    const int b = int(bt / a.n_new);
-    const int p = a.start_pos[b] + t;
-    const int newlen = a.start_pos[b] + a.n_new;
+    const NewToken tok = new_token(a, bt);
+    if (tok.b < 0) continue;
+    const int b = tok.b;
+    const int p = a.start_pos[b] + tok.t;
+    const int newlen = a.start_pos[b] + tok.count;
     if (p < 0 || p >= g.cap) {
       if (lane == 0) status_or(a.status, OSCAR_DEV_OVER_CAPACITY);
       continue;
@@ -726,10 +735,11 @@ __global__ void __launch_bounds__(kAppendThreads)
     }
     const int h = int(row % g.Hkv);
     const int64_t bt = row / g.Hkv;
-    const int t = int(bt % a.n_new);
-    const int b = int(bt / a.n_new);
-    const int p = a.start_pos[b] + t;
-    const int newlen = a.start_pos[b] + a.n_new;
+    const NewToken tok = new_token(a, bt);
+    if (tok.b < 0) continue;
+    const int b = tok.b;
+    const int p = a.start_pos[b] + tok.t;
+    const int newlen = a.start_pos[b] + tok.count;
     if (p < 0 || p >= g.cap) {
       if (lane == 0) status_or(a.status, OSCAR_DEV_OVER_CAPACITY);
       continue;

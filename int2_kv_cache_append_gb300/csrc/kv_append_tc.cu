@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       tc_fence_after();
       const uint32_t taddr = tmem + (uint32_t(32 * quarter) << 16) + uint32_t(s) * kD;
       const int64_t row = tile * kTileRows + 32 * quarter + lane;
-      const bool valid = row < a.rows;
+      bool valid = row < a.rows;
 
       // pass 1: raw row min / max (NaN-propagating, so a NaN row shows as non-finite).
       // The loops over the four 32-column chunks stay rolled: sixteen warps run
@@ -332,16 +332,22 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const uint32_t r32 = uint32_t(row);
         const uint32_t bt = fastdiv(r32, a.div_hkv);
         const int h = int(r32 - bt * uint32_t(g.Hkv));
-        const uint32_t bq = fastdiv(bt, a.div_n_new);
-        const int t = int(bt - bq * uint32_t(a.n_new));
-        b = int(bq);
+        int t, count = a.n_new;
+        if (a.cu) {
+          const NewToken tok = packed_token(a.cu, g.B, bt);
+          valid = tok.b >= 0;
+          b = max(tok.b, 0), t = tok.t, count = tok.count;
+        } else {
+          b = int(fastdiv(bt, a.div_n_new));
+          t = int(bt - uint32_t(b) * uint32_t(a.n_new));
+        }
         const int sp = b < kSposCache ? spos[b] : a.start_pos[b];
         p = sp + t;
-        newlen = sp + a.n_new;
+        newlen = sp + count;
         bh = int64_t(b) * g.Hkv + h;
-        if (!finite) status_or(a.status, OSCAR_DEV_NONFINITE);
-        if (!rng_ok) status_or(a.status, OSCAR_DEV_FP16_RANGE);
-        if (p < 0 || p >= g.cap) status_or(a.status, OSCAR_DEV_OVER_CAPACITY);
+        if (valid && !finite) status_or(a.status, OSCAR_DEV_NONFINITE);
+        if (valid && !rng_ok) status_or(a.status, OSCAR_DEV_FP16_RANGE);
+        if (valid && (p < 0 || p >= g.cap)) status_or(a.status, OSCAR_DEV_OVER_CAPACITY);
       }
       const bool in_cache = valid && p >= 0 && p < g.cap;
       const bool to_sink = in_cache && p < g.S;
@@ -525,7 +531,7 @@ int launch_append_tc(const AppendArgs& a, cudaStream_t stream) {
   const int per_role = int(std::min<int64_t>(ntiles, std::max(1, sms[dev] / 2)));
   AppendArgs ka = a;
   ka.div_hkv = fastdiv_make(uint32_t(a.g.Hkv));
-  ka.div_n_new = fastdiv_make(uint32_t(a.n_new));
+  ka.div_n_new = fastdiv_make(uint32_t(std::max(a.n_new, 1)));
   kv_append_tc_kernel<<<dim3(per_role, 2, 1), kThreadsTc, kSmemTc, stream>>>(mk, mv, ka);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
 }

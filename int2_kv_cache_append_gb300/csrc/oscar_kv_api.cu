@@ -67,13 +67,13 @@ namespace {
 // Validates kv_append's arguments and fills *a; launches nothing.
 int prep_append(const oscar_kv_config* cfg, void* cache, int32_t layer, const void* k_new, const void* v_new,
                 const int32_t* start_pos, int32_t n_new, const float* R_K, const float* R_V, float* debug_rot_out,
-                int32_t* dev_status, oscar::AppendArgs* a) {
+                int32_t* dev_status, oscar::AppendArgs* a, bool no_rows = false) {
   const int v = validate(cfg);
   if (v != OSCAR_OK) return v;
   // with the in-quant Hadamard the rotation matrices are not read (NULL allowed)
   const bool had = (cfg->flags & OSCAR_FLAG_HADAMARD) != 0;
   if (had) R_K = R_V = nullptr;
-  if (!cache || !k_new || !v_new || !start_pos || (!had && (!R_K || !R_V))) return OSCAR_ERR_INVALID;
+  if (!cache || (!no_rows && (!k_new || !v_new)) || !start_pos || (!had && (!R_K || !R_V))) return OSCAR_ERR_INVALID;
   if (layer < 0 || layer >= cfg->num_layers || n_new < 0) return OSCAR_ERR_INVALID;
   if (!aligned(cache, 256) || !aligned(R_K, 16) || !aligned(R_V, 16) || !aligned(k_new, 16) ||
       !aligned(v_new, 16) || (debug_rot_out && !aligned(debug_rot_out, 16)))
@@ -94,6 +94,7 @@ int prep_append(const oscar_kv_config* cfg, void* cache, int32_t layer, const vo
   a->v_clip = cfg->v_clip;
   a->in_fp32 = (cfg->flags & OSCAR_FLAG_IN_FP32) ? 1 : 0;
   a->hadamard = had ? 1 : 0;
+  a->cu = nullptr;
   return OSCAR_OK;
 }
 
@@ -254,6 +255,7 @@ int launch_rows(const oscar_kv_config* cfg, const oscar::RowsArgs& a, cudaStream
 // The row kernels count rows and workspace slots in ranges of these limits, and
 // positions in 32 bits up to a few tiles behind the last one.
 constexpr int kMostPositions = 0x7fffffff - 1024;
+constexpr int kMostUnits = 65535;  // (sequence, KV head) pairs of attn_mass and kv_evict: a grid's second dimension
 bool rows_supported(const Geom& g, int64_t n) {
   return n * g.G < (int64_t(1) << 30) && g.B * n * g.Hq < (int64_t(1) << 31) && g.cap <= kMostPositions;
 }
@@ -265,6 +267,27 @@ int fit_splits(const Geom& g, int64_t rows, int want, bool explicit_count, uint6
   if (!explicit_count)
     while (ns > 1 && rows_workspace(g, rows, ns) > bytes) --ns;
   return rows_workspace(g, rows, ns) > bytes ? 0 : ns;
+}
+
+// Caches that kv_evict reads and writes: the same but for layers, capacity and clips.
+int validate_evict(const oscar_kv_config* cfg, const oscar_kv_config* ocfg, int32_t keep) {
+  int v = validate(cfg);
+  if (v != OSCAR_OK) return v;
+  v = validate(ocfg);
+  if (v != OSCAR_OK) return v;
+  if (ocfg->batch != cfg->batch || ocfg->num_q_heads != cfg->num_q_heads || ocfg->num_kv_heads != cfg->num_kv_heads ||
+      ocfg->head_dim != cfg->head_dim || ocfg->sink != cfg->sink || ocfg->recent != cfg->recent || ocfg->flags != cfg->flags ||
+      keep < 0)
+    return OSCAR_ERR_INVALID;
+  const int64_t most = std::min<int64_t>(cfg->capacity, int64_t(cfg->sink) + cfg->recent + keep);
+  if (ocfg->capacity < most) return OSCAR_ERR_CAPACITY;
+  const int64_t units = int64_t(cfg->batch) * cfg->num_kv_heads;
+  return units <= kMostUnits && cfg->capacity <= kMostPositions && ocfg->capacity <= kMostPositions ? OSCAR_OK : OSCAR_ERR_UNSUPPORTED;
+}
+int evict_list(const Geom& g, int32_t keep) { return std::min(keep, std::max(0, g.cap - g.S)); }
+bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
 }
 
 // The prefix cache has the shape of the sequences' own, with one sequence.
@@ -534,6 +557,187 @@ int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const osca
   if (rc == OSCAR_OK) rc = oscar::launch_decode(d, st);
   if (rc == OSCAR_OK) rc = oscar::launch_finish_rows(p.fin, st);
   return rc;
+}
+
+int qk_norm_rope(const oscar_kv_config* cfg, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                 int32_t n_rows, const float* q_weight, const float* k_weight, float eps, const int32_t* positions,
+                 const float* inv_freq, int32_t rot_dim, int32_t interleaved, void* q_out, void* k_out, void* stream) {
+  const int v = validate(cfg);
+  if (v != OSCAR_OK) return v;
+  const int D = cfg->head_dim;
+  if (n_rows < 0 || !(eps >= 0.f) || std::isinf(eps) || rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0 || !q_weight || !k_weight ||
+      (rot_dim > 0 && !inv_freq))
+    return OSCAR_ERR_INVALID;
+  if (n_rows != 0 && (!q || !k || !q_out || !k_out || (rot_dim > 0 && !positions))) return OSCAR_ERR_INVALID;
+  const bool fp32 = (cfg->flags & OSCAR_FLAG_IN_FP32) != 0;
+  const int64_t piece = fp32 ? 4 : 8;  // elements of 16 bytes
+  if (q_stride < int64_t(cfg->num_q_heads) * D || k_stride < int64_t(cfg->num_kv_heads) * D || q_stride % piece != 0 ||
+      k_stride % piece != 0)
+    return OSCAR_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(q_weight, 16) ||
+      !aligned(k_weight, 16))
+    return OSCAR_ERR_INVALID;
+  if (n_rows == 0) return OSCAR_OK;
+  oscar::NormRopeArgs a{};
+  a.q = q;
+  a.k = k;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.eps = eps;
+  a.n = n_rows;
+  a.Hq = cfg->num_q_heads;
+  a.Hkv = cfg->num_kv_heads;
+  a.D = D;
+  a.rot = rot_dim;
+  a.interleaved = interleaved ? 1 : 0;
+  a.fp32 = fp32 ? 1 : 0;
+  return oscar::launch_norm_rope(a, static_cast<cudaStream_t>(stream));
+}
+
+int attn_prompt(const oscar_kv_config* cfg, const void* q, const void* k, const void* v, int32_t n_rows,
+                const int32_t* cu_seqlens, float sm_scale, void* out, float* lse, int32_t* dev_status, void* stream) {
+  const int rc = validate(cfg);
+  if (rc != OSCAR_OK) return rc;
+  if (n_rows < 0 || !cu_seqlens || (n_rows != 0 && (!q || !k || !v || !out))) return OSCAR_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16)) return OSCAR_ERR_INVALID;
+  const Geom g = make_geom(cfg);
+  if (int64_t(n_rows) * g.Hq >= (int64_t(1) << 31)) return OSCAR_ERR_UNSUPPORTED;
+  if (n_rows == 0) return OSCAR_OK;
+  oscar::PromptArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.cu = cu_seqlens;
+  a.out = out;
+  a.lse = lse;
+  a.status = dev_status;
+  a.n = n_rows;
+  a.B = g.B;
+  a.Hq = g.Hq;
+  a.Hkv = g.Hkv;
+  a.G = g.G;
+  a.D = g.D;
+  a.in_fp32 = (cfg->flags & OSCAR_FLAG_IN_FP32) ? 1 : 0;
+  a.out_fp32 = (cfg->flags & OSCAR_FLAG_OUT_FP32) ? 1 : 0;
+  a.qscale = log2_scale(g, sm_scale);
+  return oscar::launch_attn_prompt(a, static_cast<cudaStream_t>(stream));
+}
+
+int kv_append_packed(const oscar_kv_config* cfg, void* cache, int32_t layer, const void* k_new, const void* v_new,
+                     int32_t n_rows, const int32_t* cu_seqlens, const int32_t* start_pos, const float* R_K,
+                     const float* R_V, int32_t* dev_status, void* stream) {
+  if (!cu_seqlens || n_rows < 0) return OSCAR_ERR_INVALID;
+  oscar::AppendArgs a;
+  const int v = prep_append(cfg, cache, layer, k_new, v_new, start_pos, 0, R_K, R_V, nullptr, dev_status, &a, n_rows == 0);
+  if (v != OSCAR_OK) return v;
+  a.cu = cu_seqlens;
+  a.rows = int64_t(n_rows) * cfg->num_kv_heads;
+  return oscar::launch_append(a, static_cast<cudaStream_t>(stream));
+}
+
+int attn_mass_workspace_query(const oscar_kv_config* cfg, int32_t n_new, uint64_t* bytes) {
+  const int v = validate(cfg);
+  if (v != OSCAR_OK) return v;
+  if (!bytes || n_new < 0) return OSCAR_ERR_INVALID;
+  if (n_new > cfg->capacity) return OSCAR_ERR_CAPACITY;
+  const Geom g = make_geom(cfg);
+  if (!rows_supported(g, n_new) || int64_t(g.B) * g.Hkv > kMostUnits) return OSCAR_ERR_UNSUPPORTED;
+  *bytes = oscar::align256(uint64_t(g.B) * n_new * g.Hq * g.D * 4);
+  return OSCAR_OK;
+}
+
+int attn_mass(const oscar_kv_config* cfg, const void* cache, int32_t layer, const void* q, int32_t n_new,
+              const int32_t* q_lens, const int32_t* seq_lens, int32_t seq_len_hint, const float* R_K, float sm_scale,
+              const float* lse, const float* mass_in, float* mass_out, void* workspace, uint64_t workspace_bytes,
+              int32_t* dev_status, void* stream) {
+  uint64_t need = 0;
+  const int v = attn_mass_workspace_query(cfg, n_new, &need);
+  if (v != OSCAR_OK) return v;
+  const bool had = (cfg->flags & OSCAR_FLAG_HADAMARD) != 0;
+  if (had) R_K = nullptr;
+  if (!cache || !seq_lens || !mass_out || (!had && !R_K) || (n_new != 0 && (!q || !lse || !workspace))) return OSCAR_ERR_INVALID;
+  if (layer < 0 || layer >= cfg->num_layers || seq_len_hint < 0) return OSCAR_ERR_INVALID;
+  if (!aligned(cache, 256) || !aligned(workspace, 256) || !aligned(R_K, 16) || !aligned(q, 16)) return OSCAR_ERR_INVALID;
+  if (seq_len_hint > cfg->capacity) return OSCAR_ERR_CAPACITY;
+  if (workspace_bytes < need) return OSCAR_ERR_WORKSPACE;
+  const Geom g = make_geom(cfg);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  oscar::QrotRowsArgs r{};
+  r.q = q;
+  r.qrot = static_cast<float*>(workspace);
+  r.R_K = R_K;
+  r.status = dev_status;
+  r.q_lens = q_lens;
+  r.rows = int64_t(g.B) * n_new * g.Hq;
+  r.n = n_new;
+  r.Hq = g.Hq;
+  r.D = g.D;
+  r.in_fp32 = (cfg->flags & OSCAR_FLAG_IN_FP32) ? 1 : 0;
+  r.hadamard = had ? 1 : 0;
+  r.qscale = log2_scale(g, sm_scale);
+  oscar::MassArgs a{};
+  a.g = g;
+  a.layer_base = static_cast<const uint8_t*>(cache) + uint64_t(layer) * g.layer_bytes;
+  a.seq_lens = seq_lens;
+  a.q_lens = q_lens;
+  a.qrot = r.qrot;
+  a.lse = lse;
+  a.mass_in = mass_in;
+  a.mass_out = mass_out;
+  a.status = dev_status;
+  a.n = n_new;
+  a.top = seq_len_hint > 0 ? seq_len_hint : g.cap;
+  const int rc = n_new ? oscar::launch_qrot_rows(r, st) : OSCAR_OK;
+  return rc == OSCAR_OK ? oscar::launch_attn_mass(a, st) : rc;
+}
+
+int kv_evict_workspace_query(const oscar_kv_config* cfg, int32_t keep, uint64_t* bytes) {
+  const int v = validate(cfg);
+  if (v != OSCAR_OK) return v;
+  if (!bytes || keep < 0) return OSCAR_ERR_INVALID;
+  const Geom g = make_geom(cfg);
+  if (int64_t(g.B) * g.Hkv > kMostUnits || g.cap > kMostPositions) return OSCAR_ERR_UNSUPPORTED;
+  *bytes = oscar::align256(uint64_t(g.B) * 4) + oscar::align256(uint64_t(g.B) * g.Hkv * evict_list(g, keep) * 4);
+  return OSCAR_OK;
+}
+
+int kv_evict(const oscar_kv_config* cfg, const void* cache, int32_t layer, const float* mass, const int32_t* seq_lens,
+             int32_t keep, const oscar_kv_config* out_cfg, void* out_cache, int32_t out_layer, float* out_mass,
+             int32_t* kept, int32_t* new_lens, void* workspace, uint64_t workspace_bytes, int32_t* dev_status, void* stream) {
+  const int v = validate_evict(cfg, out_cfg, keep);
+  if (v != OSCAR_OK) return v;
+  if (!cache || !out_cache || !mass || !seq_lens || !new_lens || !workspace) return OSCAR_ERR_INVALID;
+  if (layer < 0 || layer >= cfg->num_layers || out_layer < 0 || out_layer >= out_cfg->num_layers) return OSCAR_ERR_INVALID;
+  if (!aligned(cache, 256) || !aligned(out_cache, 256) || !aligned(workspace, 256)) return OSCAR_ERR_INVALID;
+  oscar::EvictArgs a{};
+  a.g = make_geom(cfg);
+  a.og = make_geom(out_cfg);
+  a.base = static_cast<const uint8_t*>(cache) + uint64_t(layer) * a.g.layer_bytes;
+  a.out_base = static_cast<uint8_t*>(out_cache) + uint64_t(out_layer) * a.og.layer_bytes;
+  const uint64_t units = uint64_t(a.g.B) * a.g.Hkv;
+  if (overlap(a.base, a.g.layer_bytes, a.out_base, a.og.layer_bytes) ||
+      (out_mass && overlap(mass, units * a.g.cap * 4, out_mass, units * a.og.cap * 4)))
+    return OSCAR_ERR_INVALID;
+  uint64_t need = 0;
+  if (kv_evict_workspace_query(cfg, keep, &need) != OSCAR_OK || workspace_bytes < need) return OSCAR_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.mass = mass;
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.out_mass = out_mass;
+  a.kept = keep > 0 ? kept : nullptr;
+  a.lens = take<int32_t>(&ws, uint64_t(a.g.B) * 4);
+  a.list = reinterpret_cast<int32_t*>(ws);
+  a.status = dev_status;
+  a.keep = keep;
+  a.list_cap = evict_list(a.g, keep);
+  return oscar::launch_kv_evict(a, static_cast<cudaStream_t>(stream));
 }
 
 int oscar_kv_set_profile_events(void* split_start, void* split_stop) {

@@ -1,0 +1,68 @@
+// Which tile of which sequence a block of attn_prompt takes.
+#pragma once
+
+#include "internal.h"
+
+namespace oscar {
+
+struct PromptItem {
+  int b, tile;     // sequence (-1: none) and its tile
+  int start, len;  // the sequence's first packed row and length
+};
+
+// A sequence of len tokens has ceil(len * num / den) tiles; most that n packed
+// tokens of B sequences can give.
+inline int64_t prompt_items(const PromptArgs& a, int num, int den) { return int64_t(a.n) * num / den + a.B; }
+
+__device__ __forceinline__ int2 prompt_span(const PromptArgs& a, int b) {
+  const int lo = min(max(a.cu[b], 0), a.n), hi = min(max(a.cu[b + 1], lo), a.n);
+  return make_int2(lo, hi - lo);
+}
+
+// One warp: flags bounds that are not within the rows or not in order.
+__device__ __forceinline__ void prompt_check(const PromptArgs& a) {
+  bool bad = false;
+  for (int b = threadIdx.x & 31; b < a.B; b += 32) bad |= a.cu[b] < 0 || a.cu[b + 1] < a.cu[b] || a.cu[b + 1] > a.n;
+  if (bad) status_or(a.status, OSCAR_DEV_OVER_CAPACITY);
+}
+
+// Item i of the tiles of all sequences, later tiles first: with a causal mask a
+// tile's work grows with its index, and blocks start in the order of i, so the
+// longest run first and the short ones fill the end.  Called by a whole warp.
+// Sequences with more than L tiles have one of index L: item i has the index L
+// with C(L + 1) <= i < C(L), C(L) = sum over the sequences of max(0, tiles - L).
+__device__ __forceinline__ PromptItem prompt_item(const PromptArgs& a, int i, int num, int den) {
+  const int lane = threadIdx.x & 31;
+  auto tiles = [&](int b) { return (int64_t(prompt_span(a, b).y) * num + den - 1) / den; };
+  auto above = [&](int64_t level) {
+    int64_t c = 0;
+    for (int b = lane; b < a.B; b += 32) c += max(int64_t(0), tiles(b) - level);
+    for (int x = 16; x; x >>= 1) c += __shfl_xor_sync(0xffffffffu, c, x);
+    return c;
+  };
+  PromptItem it{-1, 0, 0, 0};
+  if (above(0) <= i) return it;
+  int64_t lo = 0, hi = int64_t(a.n) * num / den + 1;  // C(lo) > i >= C(hi)
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    if (above(mid) > i) lo = mid;
+    else hi = mid;
+  }
+  int64_t rank = i - above(lo + 1);  // among the sequences with more than lo tiles
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const bool has = b0 + lane < a.B && tiles(b0 + lane) > lo;
+    const unsigned mask = __ballot_sync(0xffffffffu, has);
+    const int count = __popc(mask);
+    if (rank < count) {
+      it.b = b0 + __fns(mask, 0, int(rank) + 1);
+      it.tile = int(lo);
+      const int2 s = prompt_span(a, it.b);
+      it.start = s.x, it.len = s.y;
+      return it;
+    }
+    rank -= count;
+  }
+  return it;
+}
+
+}  // namespace oscar

@@ -34,6 +34,8 @@ STATUS_NAMES = {0: "OK", -1: "INVALID", -2: "CAPACITY", -3: "WORKSPACE", -4: "LA
 # every symbol include/oscar_kv.h declares
 EXPORTS = ("kv_layout_query", "kv_append", "attn_decode", "decode_step", "attn_decode_static", "kv_read",
            "attn_extend_workspace_query", "attn_extend", "attn_decode_prefix_workspace_query", "attn_decode_prefix",
+           "qk_norm_rope", "attn_prompt", "kv_append_packed", "attn_mass_workspace_query", "attn_mass",
+           "kv_evict_workspace_query", "kv_evict",
            "oscar_kv_set_profile_events", "oscar_kv_set_wait_test", "oscar_kv_decode_kernels",
            "oscar_calibrate_workspace_query",
            "oscar_calibrate_rk",
@@ -122,6 +124,16 @@ def lib():
                                          ctypes.c_int32, P, ctypes.c_int32, P, P, ctypes.c_float, ctypes.c_int32, P, P,
                                          P, ctypes.c_uint64, P, P]
         L.attn_decode_prefix.restype = ctypes.c_int
+        C, I32, I64, F32, U64 = ctypes.POINTER(_Config), ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_uint64
+        for name, args in (("qk_norm_rope", [C, P, I64, P, I64, I32, P, P, F32, P, P, I32, I32, P, P, P]),
+                           ("attn_prompt", [C, P, P, P, I32, P, F32, P, P, P, P]),
+                           ("kv_append_packed", [C, P, I32, P, P, I32, P, P, P, P, P, P]),
+                           ("attn_mass_workspace_query", [C, I32, ctypes.POINTER(U64)]),
+                           ("attn_mass", [C, P, I32, P, I32, P, P, I32, P, F32, P, P, P, P, U64, P, P]),
+                           ("kv_evict_workspace_query", [C, I32, ctypes.POINTER(U64)]),
+                           ("kv_evict", [C, P, I32, P, P, I32, C, P, I32, P, P, P, P, U64, P, P])):
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = ctypes.c_int
         L.oscar_kv_set_profile_events.argtypes = [P, P]
         L.oscar_kv_set_profile_events.restype = ctypes.c_int
         L.oscar_kv_set_wait_test.argtypes = [ctypes.c_uint64, ctypes.c_int32]
@@ -432,6 +444,172 @@ def attn_decode_prefix(cfg: KVConfig, cache, prefix_cfg: KVConfig, prefix_cache,
                                   _stream(stream))
     if check and rc != 0:
         raise OscarError("attn_decode_prefix", rc)
+    return rc
+
+
+def _out_dtypes(cfg: KVConfig):
+    torch = _dt()
+    return (torch.float32,) if cfg.flags & FLAG_OUT_FP32 else (torch.bfloat16,)
+
+
+def _token_rows(t, name: str, kinds, shape) -> int:
+    """Elements from one token's heads [heads][head_dim] to the next one's, which may lie further on (a fused projection)."""
+    _check(t, name, kinds, shape=shape)
+    if not t.is_cuda:
+        raise ValueError(f"oscar_kv: expected a CUDA tensor, got one on {t.device}")
+    n, heads, d = shape
+    dense = heads * d
+    if n == 0:
+        return dense
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"oscar_kv: the heads of a token of {name} must be contiguous")
+    return dense if n == 1 else int(t.stride(0))
+
+
+def qk_norm_rope(cfg: KVConfig, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, eps: float = 1e-6,
+                 interleaved: bool = False, stream=None, check: bool = True) -> int:
+    """Root-mean-square norm of every head of q [n][Hq][D] and k [n][Hkv][D] (strided over the tokens, as views of a fused
+    projection), then the rotation of the first 2 * len(inv_freq) channels by positions * inv_freq (None: no rotation),
+    into q_out and k_out."""
+    torch = _dt()
+    D = cfg.head_dim
+    if q is None or q.dim() != 3:
+        raise ValueError("oscar_kv: q must be [n][num_q_heads][head_dim]")
+    n = int(q.shape[0])
+    kinds = _in_dtypes(cfg)
+    shapes = (n, cfg.num_q_heads, D), (n, cfg.num_kv_heads, D)
+    strides = _token_rows(q, "q", kinds, shapes[0]), _token_rows(k, "k", kinds, shapes[1])
+    _check(q_out, "q_out", kinds, shape=shapes[0])
+    _check(k_out, "k_out", kinds, shape=shapes[1])
+    _check(q_weight, "q_weight", (torch.float32,), shape=(D,))
+    _check(k_weight, "k_weight", (torch.float32,), shape=(D,))
+    _check(inv_freq, "inv_freq", (torch.float32,), optional=True)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    _check(positions, "positions", (torch.int32,), shape=(n,), optional=rot == 0)
+    _same_device(q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out)
+    rc = lib().qk_norm_rope(ctypes.byref(cfg.c()), q.data_ptr(), strides[0], k.data_ptr(), strides[1], n, _ptr(q_weight),
+                            _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), rot, int(bool(interleaved)),
+                            _ptr(q_out), _ptr(k_out), _stream(stream))
+    if check and rc != 0:
+        raise OscarError("qk_norm_rope", rc)
+    return rc
+
+
+def attn_prompt(cfg: KVConfig, q, k, v, cu_seqlens, out, lse=None, sm_scale: float = 0.0, status=None, stream=None,
+                check: bool = True) -> int:
+    """Causal attention of packed prompts, q and out [n][Hq][D], over their own k and v [n][Hkv][D]: sequence b has the
+    rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1; other rows of out and lse ([n][Hq]) are left as they were."""
+    torch = _dt()
+    if q is None or q.dim() != 3:
+        raise ValueError("oscar_kv: q must be [n][num_q_heads][head_dim]")
+    n, Hq, H, D = int(q.shape[0]), cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim
+    _check(q, "q", _in_dtypes(cfg), shape=(n, Hq, D))
+    _check(k, "k", _in_dtypes(cfg), shape=(n, H, D))
+    _check(v, "v", _in_dtypes(cfg), shape=(n, H, D))
+    _check(cu_seqlens, "cu_seqlens", (torch.int32,), shape=(cfg.batch + 1,))
+    _check(out, "out", _out_dtypes(cfg), shape=(n, Hq, D))
+    _check(lse, "lse", (torch.float32,), shape=(n, Hq), optional=True)
+    _check(status, "status", (torch.int32,), min_bytes=4, optional=True)
+    _same_device(q, k, v, cu_seqlens, out, lse, status)
+    rc = lib().attn_prompt(ctypes.byref(cfg.c()), _ptr(q), _ptr(k), _ptr(v), n, _ptr(cu_seqlens), float(sm_scale), _ptr(out),
+                           _ptr(lse), _ptr(status), _stream(stream))
+    if check and rc != 0:
+        raise OscarError("attn_prompt", rc)
+    return rc
+
+
+def kv_append_packed(cfg: KVConfig, cache, layer: int, k_new, v_new, cu_seqlens, start_pos, R_K, R_V, status=None,
+                     stream=None, check: bool = True) -> int:
+    """kv_append of packed rows k_new, v_new [n][Hkv][D]: sequence b gets the rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1
+    at start_pos[b]."""
+    torch = _dt()
+    if k_new is None or k_new.dim() != 3:
+        raise ValueError("oscar_kv: k_new must be [n][num_kv_heads][head_dim]")
+    n = int(k_new.shape[0])
+    shape = (n, cfg.num_kv_heads, cfg.head_dim)
+    _check(k_new, "k_new", _in_dtypes(cfg), shape=shape)
+    _check(v_new, "v_new", _in_dtypes(cfg), shape=shape)
+    _check(cu_seqlens, "cu_seqlens", (torch.int32,), shape=(cfg.batch + 1,))
+    _check(start_pos, "start_pos", (torch.int32,), shape=(cfg.batch,))
+    _check(status, "status", (torch.int32,), min_bytes=4, optional=True)
+    c = _check_cache(cfg, cache)
+    _check_rot(cfg, R_K, "R_K")
+    _check_rot(cfg, R_V, "R_V")
+    _same_device(cache, k_new, v_new, cu_seqlens, start_pos, R_K, R_V, status)
+    rc = lib().kv_append_packed(c, _ptr(cache), layer, _ptr(k_new), _ptr(v_new), n, _ptr(cu_seqlens), _ptr(start_pos),
+                                _ptr(R_K), _ptr(R_V), _ptr(status), _stream(stream))
+    if check and rc != 0:
+        raise OscarError("kv_append_packed", rc)
+    return rc
+
+
+def attn_mass_workspace_bytes(cfg: KVConfig, n_new: int) -> int:
+    n = ctypes.c_uint64(0)
+    rc = lib().attn_mass_workspace_query(ctypes.byref(cfg.c()), int(n_new), ctypes.byref(n))
+    if rc != 0:
+        raise OscarError("attn_mass_workspace_query", rc)
+    return int(n.value)
+
+
+def attn_mass(cfg: KVConfig, cache, layer: int, q, seq_lens, R_K, lse, mass_out, workspace, mass_in=None, q_lens=None,
+              seq_len_hint: int = 0, sm_scale: float = 0.0, status=None, stream=None, check: bool = True) -> int:
+    """mass_out [B][Hkv][capacity] = mass_in (None: 0) plus the attention weight that every cached position receives from
+    the last q_lens[b] (None: n) tokens of its sequence, q [B][n][Hq][D] with the lse [B][n][Hq] of their attention."""
+    torch = _dt()
+    B, Hq, D = cfg.batch, cfg.num_q_heads, cfg.head_dim
+    if q is None or q.dim() != 4:
+        raise ValueError("oscar_kv: q must be [batch][n_new][num_q_heads][head_dim]")
+    n = int(q.shape[1])
+    whole = (B, cfg.num_kv_heads, cfg.capacity)
+    _check(q, "q", _in_dtypes(cfg), shape=(B, n, Hq, D))
+    _check(lse, "lse", (torch.float32,), shape=(B, n, Hq))
+    _check(mass_out, "mass_out", (torch.float32,), shape=whole)
+    _check(mass_in, "mass_in", (torch.float32,), shape=whole, optional=True)
+    _check(seq_lens, "seq_lens", (torch.int32,), shape=(B,))
+    _check(q_lens, "q_lens", (torch.int32,), shape=(B,), optional=True)
+    _check(status, "status", (torch.int32,), min_bytes=4, optional=True)
+    _check(workspace, "workspace", (torch.uint8,))
+    c = _check_cache(cfg, cache)
+    _check_rot(cfg, R_K, "R_K")
+    _same_device(cache, q, seq_lens, q_lens, R_K, lse, mass_in, mass_out, workspace, status)
+    rc = lib().attn_mass(c, _ptr(cache), layer, _ptr(q), n, _ptr(q_lens), _ptr(seq_lens), int(seq_len_hint), _ptr(R_K),
+                         float(sm_scale), _ptr(lse), _ptr(mass_in), _ptr(mass_out), _ptr(workspace),
+                         int(workspace.numel()), _ptr(status), _stream(stream))
+    if check and rc != 0:
+        raise OscarError("attn_mass", rc)
+    return rc
+
+
+def kv_evict_workspace_bytes(cfg: KVConfig, keep: int) -> int:
+    n = ctypes.c_uint64(0)
+    rc = lib().kv_evict_workspace_query(ctypes.byref(cfg.c()), int(keep), ctypes.byref(n))
+    if rc != 0:
+        raise OscarError("kv_evict_workspace_query", rc)
+    return int(n.value)
+
+
+def kv_evict(cfg: KVConfig, cache, layer: int, mass, seq_lens, keep: int, out_cfg: KVConfig, out_cache, out_layer: int,
+             new_lens, workspace, out_mass=None, kept=None, status=None, stream=None, check: bool = True) -> int:
+    """A layer of `cache` without all but the `keep` positions of largest mass [B][Hkv][capacity] between sink and window
+    of every KV head, into a layer of out_cache; new_lens [B] (may be seq_lens) receives the lengths, out_mass
+    [B][Hkv][out capacity] the masses of what stays, kept [B][Hkv][keep] its old positions (-1 behind the last)."""
+    torch = _dt()
+    B, H = cfg.batch, cfg.num_kv_heads
+    _check(mass, "mass", (torch.float32,), shape=(B, H, cfg.capacity))
+    _check(seq_lens, "seq_lens", (torch.int32,), shape=(B,))
+    _check(new_lens, "new_lens", (torch.int32,), shape=(B,))
+    _check(out_mass, "out_mass", (torch.float32,), shape=(B, H, out_cfg.capacity), optional=True)
+    _check(kept, "kept", (torch.int32,), shape=(B, H, int(keep)), optional=True)
+    _check(status, "status", (torch.int32,), min_bytes=4, optional=True)
+    _check(workspace, "workspace", (torch.uint8,))
+    c = _check_cache(cfg, cache)
+    oc = _check_cache(out_cfg, out_cache, "out_cache")
+    _same_device(cache, out_cache, mass, seq_lens, new_lens, out_mass, kept, workspace, status)
+    rc = lib().kv_evict(c, _ptr(cache), layer, _ptr(mass), _ptr(seq_lens), int(keep), oc, _ptr(out_cache), out_layer,
+                        _ptr(out_mass), _ptr(kept), _ptr(new_lens), _ptr(workspace), int(workspace.numel()), _ptr(status),
+                        _stream(stream))
+    if check and rc != 0:
+        raise OscarError("kv_evict", rc)
     return rc
 
 
