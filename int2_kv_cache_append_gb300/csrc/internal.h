@@ -92,6 +92,9 @@ int launch_append_tc(const AppendArgs& a, cudaStream_t stream);  // D = 128, bf1
 // 2-D tiled TMA map of a row-major bf16 matrix [rows][cols], 128-byte swizzle
 bool encode_rows_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t cols, uint32_t box_cols,
                       uint32_t box_rows);
+// 3-D tiled TMA map of bf16 heads [rows][heads][D], box of 64 channels of box_heads heads of box_rows rows, 128-byte swizzle
+bool encode_heads_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t heads, uint32_t D, uint32_t box_heads,
+                       uint32_t box_rows);
 // 2-D tiled TMA map of a row-major float32 matrix [rows][cols], no swizzle
 bool encode_f32_tiles(CUtensorMap* m, const float* ptr, uint64_t rows, uint64_t cols, uint32_t box_cols,
                       uint32_t box_rows);
@@ -226,8 +229,11 @@ struct PromptArgs {
   int n, B, Hq, Hkv, G, D;
   int in_fp32, out_fp32;
   float qscale;           // sm_scale * log2(e)
+  uint32_t wait_turns;    // as in RowsArgs
+  int wait_poison;
 };
 int launch_attn_prompt(const PromptArgs& a, cudaStream_t stream);  // float32 (attn_prompt.cu)
+int launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t stream);  // bf16, head_dim 128 (attn_prompt_tc.cu)
 
 // Attention weight of every cached position (attn_mass.cu).
 struct MassArgs {
