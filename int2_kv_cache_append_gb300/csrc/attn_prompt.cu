@@ -195,7 +195,7 @@ int launch_t(const PromptArgs& a, cudaStream_t stream) {
 
 int launch_attn_prompt(const PromptArgs& a, cudaStream_t stream) {
   if (a.in_fp32) return a.out_fp32 ? launch_t<float, float>(a, stream) : launch_t<float, __nv_bfloat16>(a, stream);
-  return a.out_fp32 ? launch_t<__nv_bfloat16, float>(a, stream) : launch_t<__nv_bfloat16, __nv_bfloat16>(a, stream);
+  return launch_t<__nv_bfloat16, float>(a, stream);
 }
 
 }  // namespace oscar

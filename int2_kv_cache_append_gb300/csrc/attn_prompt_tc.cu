@@ -25,8 +25,7 @@
 // replaced by zero there, and added to the rows that see it at the end.
 #include <algorithm>
 
-#include "prompt_items.cuh"
-#include "rows_tc.cuh"
+#include "prompt_tc.cuh"
 
 namespace oscar {
 namespace {
@@ -47,47 +46,6 @@ static_assert(oBar % 8 == 0 && kBytes <= 232448 - 64, "shared memory");
 constexpr uint32_t cS = 0, cO = 256;   // TMEM columns, 128 per tile
 constexpr int kSoftRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSoftRegs + kOtherRegs <= 3 * 168, "registers of a launch with 168 a thread");
-
-constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // both operands bf16
-
-__device__ __forceinline__ uint32_t bf162_of(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-
-// V rows of a tile that some rows of the block do not see: zero for what is infinite or not a number.  odd [3][D]: the
-// first token of the sequence with a NaN, +inf, -inf in a channel.
-__device__ __forceinline__ void check_values(uint8_t* tile, int* odd, int token0, int seen_by_all, int len, int x) {
-#pragma unroll 1
-  for (int r = x; r < kTok; r += 64) {
-    const int token = token0 + r;
-    if (token <= seen_by_all) continue;
-    uint32_t most = 0;
-#pragma unroll
-    for (int block = 0; block < 2; ++block)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {  // the 16-byte pieces of a row in an order of its own: no bank twice
-        const uint4 v = *reinterpret_cast<const uint4*>(tile + block * (kTile / 2) + r * 128 + ((i + r) & 7) * 16);
-        most = absmax2(absmax2(absmax2(absmax2(most, v.x), v.y), v.z), v.w);
-      }
-    if ((most & 0xFFFFu) < 0x7F80u && (most >> 16) < 0x7F80u) continue;
-#pragma unroll 1
-    for (int c = 0; c < D; ++c) {
-      uint16_t* at = reinterpret_cast<uint16_t*>(tile + (c / 64) * (kTile / 2) + r * 128 + (((c & 63) / 8) ^ (r & 7)) * 16 + (c & 7) * 2);
-      const uint32_t v = *at;
-      if ((v & 0x7FFFu) < 0x7F80u) continue;
-      *at = 0;
-      if (token < len) atomicMin(odd + ((v & 0x7FFFu) > 0x7F80u ? 0 : v < 0x8000u ? 1 : 2) * D + c, token);
-    }
-  }
-}
 
 __global__ void __launch_bounds__(kThreads, 1)
     attn_prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -378,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = check0; j < nt && ok; ++j) {
         const int s = 2 * j + 1;
         ok = wait_warp(values + 8 * (j - check0), 0, a.wait_turns);
-        if (ok) check_values(sm + oKV + (s % kStages) * kTile, odd, j * kTok, t0, it.len, threadIdx.x - kCheck * 32);
+        if (ok) check_values<kTok, D>(sm + oKV + (s % kStages) * kTile, odd, j * kTok, t0, it.len, threadIdx.x - kCheck * 32);
         __syncwarp();
         for (int c = lane; c < 3 * D; c += 32)
           if (odd[c] != 0x7fffffff) *any_odd = 1;

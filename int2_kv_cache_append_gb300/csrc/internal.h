@@ -234,6 +234,7 @@ struct PromptArgs {
 };
 int launch_attn_prompt(const PromptArgs& a, cudaStream_t stream);  // float32 (attn_prompt.cu)
 int launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t stream);  // bf16, head_dim 128 (attn_prompt_tc.cu)
+int launch_attn_prompt_wide(const PromptArgs& a, cudaStream_t stream);  // bf16, head_dim 256, 512 (attn_prompt_wide.cu)
 
 // Attention weight of every cached position (attn_mass.cu).
 struct MassArgs {

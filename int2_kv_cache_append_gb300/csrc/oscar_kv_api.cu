@@ -629,7 +629,8 @@ int attn_prompt(const oscar_kv_config* cfg, const void* q, const void* k, const 
   a.wait_turns = oscar::wait_turns();
   a.wait_poison = oscar::g_test_wait_poison;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return a.D == 128 && !a.in_fp32 && !a.out_fp32 ? oscar::launch_attn_prompt_tc(a, st) : oscar::launch_attn_prompt(a, st);
+  if (a.in_fp32 || a.out_fp32) return oscar::launch_attn_prompt(a, st);
+  return a.D == 128 ? oscar::launch_attn_prompt_tc(a, st) : oscar::launch_attn_prompt_wide(a, st);
 }
 
 int kv_append_packed(const oscar_kv_config* cfg, void* cache, int32_t layer, const void* k_new, const void* v_new,

@@ -1,0 +1,53 @@
+// Device code shared by attn_prompt's tensor-core kernels.
+#pragma once
+
+#include "prompt_items.cuh"
+#include "rows_tc.cuh"
+
+namespace oscar {
+
+constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // instruction descriptor: both operands bf16
+
+__device__ __forceinline__ uint32_t bf162_of(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// `rows` V rows of 128 channels (two blocks of 64, swizzled) that some query rows of the block do not see: zero for what is
+// infinite or not a number.  odd [3][channels]: the first token of the sequence with a NaN, +inf, -inf in a channel.  By 64
+// threads, x of them.
+template <int rows, int channels>
+__device__ __forceinline__ void check_values(uint8_t* tile, int* odd, int token0, int seen_by_all, int len, int x) {
+  constexpr int kBlock = rows * 128;
+#pragma unroll 1
+  for (int r = x; r < rows; r += 64) {
+    const int token = token0 + r;
+    if (token <= seen_by_all) continue;
+    uint32_t most = 0;
+#pragma unroll
+    for (int block = 0; block < 2; ++block)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // the 16-byte pieces of a row in an order of its own: no bank twice
+        const uint4 v = *reinterpret_cast<const uint4*>(tile + block * kBlock + r * 128 + ((i + r) & 7) * 16);
+        most = absmax2(absmax2(absmax2(absmax2(most, v.x), v.y), v.z), v.w);
+      }
+    if ((most & 0xFFFFu) < 0x7F80u && (most >> 16) < 0x7F80u) continue;
+#pragma unroll 1
+    for (int c = 0; c < 128; ++c) {
+      uint16_t* at = reinterpret_cast<uint16_t*>(tile + (c / 64) * kBlock + r * 128 + (((c & 63) / 8) ^ (r & 7)) * 16 + (c & 7) * 2);
+      const uint32_t v = *at;
+      if ((v & 0x7FFFu) < 0x7F80u) continue;
+      *at = 0;
+      if (token < len) atomicMin(odd + ((v & 0x7FFFu) > 0x7F80u ? 0 : v < 0x8000u ? 1 : 2) * channels + c, token);
+    }
+  }
+}
+
+}  // namespace oscar
