@@ -247,7 +247,8 @@ struct MassArgs {
   const float* mass_in;     // [B][Hkv][cap] or NULL (= 0)
   float* mass_out;
   int32_t* status;
-  int n, top;               // top: no sequence is longer
+  int n, top;               // top: length for which the grid is laid out
+  int chunk;                // positions of a block (set by the launcher)
 };
 int launch_attn_mass(const MassArgs& a, cudaStream_t stream);
 
