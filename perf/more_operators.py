@@ -513,6 +513,10 @@ def _own(st):
             st["out_cfg"] = _config(case, st["out_lay"]["capacity"])
             size = K.kv_evict_workspace_bytes(st["cfg"], case["keep"])
         st["ws"] = torch.empty(size, dtype=torch.uint8, device="cuda")
+        if op == "append":
+            st["whole"] = _whole(case, st["lay"], st["cache"])
+        elif op == "evict":
+            st["whole"] = _whole(case, st["out_lay"], st["out_cache"])
     cfg = st["cfg"]
     if op == "rope":
         K.qk_norm_rope(cfg, st["q"], st["k"], st["qw"], st["kw"], st["positions"], st["inv_freq"], st["q_out"], st["k_out"],
@@ -523,16 +527,14 @@ def _own(st):
         return {"out": st["out"], "lse": st["lse"]}
     if op == "append":
         K.kv_append_packed(cfg, st["cache"], 0, st["k"], st["v"], st["cu"], st["start"], None, None)
-        return _whole(case, st["lay"], st["cache"])
+        return st["whole"]
     if op == "mass":
         K.attn_mass(cfg, st["cache"], 0, st["q"], st["lens"], None if case["hadamard"] else st["rot"], st["lse"], st["out"],
                     st["ws"], mass_in=st["mass"], q_lens=st["q_lens"], seq_len_hint=case["length"])
         return {"mass": st["out"]}
     K.kv_evict(cfg, st["cache"], 0, st["mass"], st["lens"], case["keep"], st["out_cfg"], st["out_cache"], 0, st["new_lens"],
                st["ws"], out_mass=st["out_mass"], kept=st["kept"])
-    res = {"mass": st["out_mass"], "kept": st["kept"], "lens": st["new_lens"]}
-    res.update(_whole(case, st["out_lay"], st["out_cache"]))
-    return res
+    return {"mass": st["out_mass"], "kept": st["kept"], "lens": st["new_lens"], **st["whole"]}
 
 
 def run(state):
