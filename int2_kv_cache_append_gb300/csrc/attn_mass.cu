@@ -23,7 +23,7 @@
 // masses of which stay in shared memory.
 #include <algorithm>
 
-#include "rows.cuh"
+#include "rows_tc.cuh"
 
 namespace oscar {
 namespace {
@@ -32,12 +32,6 @@ constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kBatch = 32;          // positions of a warp's turn
 constexpr int kMostChunk = 4096;    // positions of a block
 
-// 2^x, results below the normal range are 0
-__device__ __forceinline__ float ex2z(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // The codes at bits 2 p and 16 + 2 p of a word as fp16 values code * 2^-16.
 template <uint32_t mask>
 __device__ __forceinline__ void codes_of(uint32_t w, uint32_t (&r)[8]) {

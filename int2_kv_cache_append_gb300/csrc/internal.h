@@ -45,6 +45,11 @@ __device__ __forceinline__ NewToken packed_token(const int32_t* cu, int B, int64
   const int first = cu[lo];
   return {lo, int(row - first), cu[hi] - first};
 }
+// Token index bt of a batch of n_new tokens each, or of packed rows.
+__device__ __forceinline__ NewToken new_token(const AppendArgs& a, int64_t bt) {
+  if (a.cu) return packed_token(a.cu, a.g.B, bt);
+  return {int(bt / a.n_new), int(bt % a.n_new), a.n_new};
+}
 
 struct DecodeArgs {
   Geom g;
@@ -89,6 +94,7 @@ inline uint64_t wait_limit_ns() { return g_test_wait_ns > 0 ? g_test_wait_ns : 2
 inline uint32_t wait_turns() { return uint32_t((wait_limit_ns() + 999) / 1000); }
 int launch_append(const AppendArgs& a, cudaStream_t stream);
 int launch_append_tc(const AppendArgs& a, cudaStream_t stream);  // D = 128, bf16 inputs
+int launch_append_had(const AppendArgs& a, cudaStream_t stream);  // in-quant Hadamard, many rows (kv_append_had.cu)
 // 2-D tiled TMA map of a row-major bf16 matrix [rows][cols], 128-byte swizzle
 bool encode_rows_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t cols, uint32_t box_cols,
                       uint32_t box_rows);
@@ -266,6 +272,7 @@ struct EvictArgs {
   int32_t* lens;            // workspace: [B] lengths, clamped
   int32_t* status;
   int keep, list_cap;
+  int body_blocks;          // gather blocks before the windows' (set by the launcher)
 };
 int launch_kv_evict(const EvictArgs& a, cudaStream_t stream);
 

@@ -40,12 +40,6 @@
 namespace oscar {
 namespace {
 
-// Token index bt of a batch of n_new tokens each, or of packed rows.
-__device__ __forceinline__ NewToken new_token(const AppendArgs& a, int64_t bt) {
-  if (a.cu) return packed_token(a.cu, a.g.B, bt);
-  return {int(bt / a.n_new), int(bt % a.n_new), a.n_new};
-}
-
 
 constexpr int kAppendThreads = 128;
 // appends of at most this many rows per role take the row-parallel kernel
@@ -921,10 +915,12 @@ int launch_append_small(const AppendArgs& a, cudaStream_t stream) {
   return a.rows > 512 ? launch_append_rows<D, 8, false>(a, stream) : launch_append_rows<D, 4, false>(a, stream);
 }
 
-// the in-quant Hadamard reads no matrix, so every append takes the
-// row-parallel kernel
+// the in-quant Hadamard reads no matrix, so a decode step takes the row-parallel
+// kernel, with its programmatic launch; more rows go eight to a warp
+// (kv_append_had.cu)
 template <int D>
 int launch_append_hadamard(const AppendArgs& a, cudaStream_t stream) {
+  if (a.rows > kSmallAppendRows) return launch_append_had(a, stream);
   return a.rows > 512 ? launch_append_rows<D, 8, true>(a, stream) : launch_append_rows<D, 4, true>(a, stream);
 }
 

@@ -255,6 +255,7 @@ int launch_rows(const oscar_kv_config* cfg, const oscar::RowsArgs& a, cudaStream
 // The row kernels count rows and workspace slots in ranges of these limits, and
 // positions in 32 bits up to a few tiles behind the last one.
 constexpr int kMostPositions = 0x7fffffff - 1024;
+constexpr int kMostEvict = 0x7fffffff - 16384;  // kv_evict counts on by up to a block's loads
 constexpr int kMostUnits = 65535;  // (sequence, KV head) pairs of attn_mass and kv_evict: a grid's second dimension
 bool rows_supported(const Geom& g, int64_t n) {
   return n * g.G < (int64_t(1) << 30) && g.B * n * g.Hq < (int64_t(1) << 31) && g.cap <= kMostPositions;
@@ -282,7 +283,7 @@ int validate_evict(const oscar_kv_config* cfg, const oscar_kv_config* ocfg, int3
   const int64_t most = std::min<int64_t>(cfg->capacity, int64_t(cfg->sink) + cfg->recent + keep);
   if (ocfg->capacity < most) return OSCAR_ERR_CAPACITY;
   const int64_t units = int64_t(cfg->batch) * cfg->num_kv_heads;
-  return units <= kMostUnits && cfg->capacity <= kMostPositions && ocfg->capacity <= kMostPositions ? OSCAR_OK : OSCAR_ERR_UNSUPPORTED;
+  return units <= kMostUnits && cfg->capacity <= kMostEvict && ocfg->capacity <= kMostEvict ? OSCAR_OK : OSCAR_ERR_UNSUPPORTED;
 }
 int evict_list(const Geom& g, int32_t keep) { return std::min(keep, std::max(0, g.cap - g.S)); }
 bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
@@ -706,7 +707,7 @@ int kv_evict_workspace_query(const oscar_kv_config* cfg, int32_t keep, uint64_t*
   if (v != OSCAR_OK) return v;
   if (!bytes || keep < 0) return OSCAR_ERR_INVALID;
   const Geom g = make_geom(cfg);
-  if (int64_t(g.B) * g.Hkv > kMostUnits || g.cap > kMostPositions) return OSCAR_ERR_UNSUPPORTED;
+  if (int64_t(g.B) * g.Hkv > kMostUnits || g.cap > kMostEvict) return OSCAR_ERR_UNSUPPORTED;
   *bytes = oscar::align256(uint64_t(g.B) * 4) + oscar::align256(uint64_t(g.B) * g.Hkv * evict_list(g, keep) * 4);
   return OSCAR_OK;
 }
