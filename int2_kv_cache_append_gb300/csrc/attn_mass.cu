@@ -83,22 +83,41 @@ __global__ void __launch_bounds__(kThreads, (resident<D, NB>())) attn_mass_kerne
     const int i0 = max(p0, g.S), i1 = min(p1, window);        // INT2 positions
     const bool wide = p0 < min(g.S, T) || p1 > window;
     for (int i = threadIdx.x; i < p1 - p0; i += kThreads) mass[i] = 0.f;
-    uint2 raw[Dg][4];
-    uint32_t szr[Dg][4];
-    auto load = [&](int p) {
+    struct Batch {
+      uint2 words[Dg][4];
+      uint32_t sz[Dg][4];
+    };
+    const uint8_t* my_codes = codes + 8 * col;
+    auto load = [&](Batch& x, int p) {
+      const int at = p + row8 - g.S;
+      if (p + kBatch <= i1) {  // positions 8 apart are constants apart
+        const uint8_t *c = my_codes + int64_t(at) * (D / 4), *z = sz + int64_t(at) * (Dg * 4);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t at = min(p + 8 * i + row8, i1 - 1) - g.S;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < Dg; ++j) {
-          raw[j][i] = __ldg(reinterpret_cast<const uint2*>(codes + at * (D / 4) + 32 * j + 8 * col));
-          szr[j][i] = __ldg(reinterpret_cast<const uint32_t*>(sz + at * (Dg * 4) + 4 * j));
+          for (int j = 0; j < Dg; ++j) {
+            x.words[j][i] = __ldg(reinterpret_cast<const uint2*>(c + i * 8 * (D / 4) + 32 * j));
+            x.sz[j][i] = __ldg(reinterpret_cast<const uint32_t*>(z + i * 8 * (Dg * 4) + 4 * j));
+          }
+      } else if (p < i1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t last = min(at + 8 * i, i1 - 1 - g.S);
+#pragma unroll
+          for (int j = 0; j < Dg; ++j) {
+            x.words[j][i] = __ldg(reinterpret_cast<const uint2*>(my_codes + last * (D / 4) + 32 * j));
+            x.sz[j][i] = __ldg(reinterpret_cast<const uint32_t*>(sz + last * (Dg * 4) + 4 * j));
+          }
         }
       }
     };
+    constexpr int kStep = kBatch * kWarps;
+    constexpr bool kAhead = D == 128 && NB < 4;  // two batches under way where the registers allow
     for (int r0 = 0; r0 < rows; r0 += R) {
       int p = i0 + kBatch * warp;
-      if (p < i1) load(p);
+      Batch x0, x1;
+      load(x0, p);
+      if (kAhead) load(x1, p + kStep);
       // ----------------- the rows' fragments, factors and references ------------------
       __syncthreads();
       for (int r = warp; r < R; r += kWarps) {
@@ -194,19 +213,12 @@ __global__ void __launch_bounds__(kThreads, (resident<D, NB>())) attn_mass_kerne
       };
 
       // ------------------------------- INT2 rows --------------------------------------
-      for (; p < i1; p += kBatch * kWarps) {
+      auto take = [&](const Batch& now, int p) {
         float s[NB][4];
 #pragma unroll
         for (int t = 0; t < NB; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
-        uint2 now[Dg][4];
-        uint32_t nsz[Dg][4];
-#pragma unroll
-        for (int j = 0; j < Dg; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) now[j][i] = raw[j][i], nsz[j][i] = szr[j][i];
-        if (p + kBatch * kWarps < i1) load(p + kBatch * kWarps);
 #pragma unroll
         for (int j = 0; j < Dg; ++j) {
           float acc[NB][2][4], high[NB][2][4];
@@ -223,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, (resident<D, NB>())) attn_mass_kerne
               uint32_t r[4][8];
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
-                const uint32_t w = i ? now[j][x].y : now[j][x].x;
+                const uint32_t w = i ? now.words[j][x].y : now.words[j][x].x;
                 if (level) codes_of<0x02000200u>(w, r[x]);
                 else codes_of<0x03000300u>(w, r[x]);
               }
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, (resident<D, NB>())) attn_mass_kerne
           }
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&nsz[j][x]));
+            const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&now.sz[j][x]));
 #pragma unroll
             for (int t = 0; t < NB; ++t) {
               float dot = acc[t][x >> 1][2 * (x & 1)] + acc[t][x >> 1][2 * (x & 1) + 1];
@@ -249,6 +261,22 @@ __global__ void __launch_bounds__(kThreads, (resident<D, NB>())) attn_mass_kerne
           }
         }
         weigh(s, p, i1);
+      };
+#pragma unroll 1
+      while (p < i1) {
+        if (kAhead) {
+          take(x0, p);
+          load(x0, p + 2 * kStep);
+          p += kStep;
+          if (p >= i1) break;
+          take(x1, p);
+          load(x1, p + 2 * kStep);
+        } else {
+          x1 = x0;
+          load(x0, p + kStep);
+          take(x1, p);
+        }
+        p += kStep;
       }
 
       // ------------------------------- BF16 rows --------------------------------------

@@ -219,7 +219,7 @@ struct NormRopeArgs {
   void* k_out;            // [n][Hkv][D]
   float eps;
   int n, Hq, Hkv, D, rot, interleaved, fp32;
-  int tb;                 // tokens of a block's turn (set by the launcher)
+  int wpt;                // warps of a token (set by the launcher)
 };
 int launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
 

@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;        // 11 bits of a key
-constexpr int kLoads = 8;          // masses of a thread under way
+constexpr int kLoads = 4;          // masses of a thread under way
 constexpr int kMostCluster = 8;
 constexpr int kGatherThreads = 256;
 constexpr int kBody = 128;         // new positions of a gather block
@@ -77,7 +77,7 @@ __device__ __forceinline__ int block_exclusive(int x, int* warp_sums) {
   return sum - x + (warp ? warp_sums[warp - 1] : 0);
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const EvictArgs a) {
   __shared__ int hist[kBins], sums[kSelWarps], above_of[kSelWarps], same_of[kSelWarps];
   __shared__ int pick, left, totals[2];
   const cg::cluster_group cluster = cg::this_cluster();

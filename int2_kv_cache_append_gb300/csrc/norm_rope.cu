@@ -9,8 +9,9 @@
 // Angles: position * inv_freq exceeds float32 after a few thousand positions (at
 // 10^6 its last bit is 0.06), so an angle is counted in turns modulo one, in
 // 64-bit fixed point: inv_freq / 2 pi mod 1 once per block in float64, then one
-// 64-bit integer product per (token, frequency), exact modulo 2^64.  The tokens'
-// sines and cosines lie in shared memory and serve all their heads.
+// 64-bit integer product per (token, frequency), exact modulo 2^64.  A warp has a
+// token (or shares it with others, if there are few): its lanes' sines, cosines
+// and weights stay in registers over all the token's heads.
 //
 // A row belongs to D / 16 lanes; each lane holds 8 channels of the first and 8 of
 // the second half of the rotated channels (and likewise of the rest, if there is
@@ -23,7 +24,7 @@
 namespace oscar {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 8, kThreads = kWarps * 32;
 
 template <typename T>
 struct Vec8;  // 8 channels as float32
@@ -62,13 +63,17 @@ struct Vec8<float> {
   }
 };
 
+// Rows of a warp, each with D / 16 lanes.
+template <int D>
+constexpr int kRowsOfWarp = 32 / (D / 16);
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs a) {
-  constexpr int LPR = D / 16, RPW = 32 / LPR;  // lanes of a row, rows of a warp
-  extern __shared__ float2 turn[];             // [tb][rot / 2] (cos, sin), then the frequencies
-  const int half = a.rot / 2, heads = a.Hq + a.Hkv;
-  uint64_t* freq = reinterpret_cast<uint64_t*>(turn + a.tb * half);
-  const int lane = threadIdx.x & 31, part = lane % LPR;
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormRopeArgs a) {
+  constexpr int LPR = D / 16, RPW = kRowsOfWarp<D>;
+  __shared__ uint64_t freq[D / 2];
+  __shared__ float2 turns[kWarps][D / 2];  // a warp's token: (cos, sin)
+  const int half = a.rot / 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = lane % LPR, sub = lane / LPR;
   // this lane's channels: first .. + 7 and second .. + 7
   const bool rotated = part < a.rot / 16;
   const int rest = part - a.rot / 16;
@@ -80,92 +85,110 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
     freq[i] = uint64_t(f * 18446744073709551616.0);
   }
   __syncthreads();
-  const int groups = (a.n + a.tb - 1) / a.tb;
-  for (int grp = blockIdx.x; grp < groups; grp += gridDim.x) {
-    const int t0 = grp * a.tb, tokens = min(a.tb, a.n - t0);
-    for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
-      const int64_t pos = __ldg(a.positions + t0 + i / half);
-      const uint64_t x = uint64_t(pos) * freq[i % half];
-      float s, c;
-      sincospif(float(int32_t(x >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns in [-1, 1)
-      turn[i] = make_float2(c, s);
+  const int groups_q = (a.Hq + RPW - 1) / RPW, groups = groups_q + (a.Hkv + RPW - 1) / RPW;
+  float2* turn = turns[warp];
+  // `wpt` warps share a token's heads
+  const int per_block = kWarps / a.wpt, share = warp % a.wpt;
+  for (int64_t t = int64_t(blockIdx.x) * per_block + warp / a.wpt; t < a.n; t += int64_t(gridDim.x) * per_block) {
+    if (half) {
+      const int64_t pos = __ldg(a.positions + t);
+      __syncwarp();
+      for (int i = lane; i < half; i += 32) {
+        const uint64_t x = uint64_t(pos) * freq[i];
+        float s, c;
+        sincospif(float(int32_t(x >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns in [-1, 1)
+        turn[i] = make_float2(c, s);
+      }
+      __syncwarp();
     }
-    __syncthreads();
-    const int rows = tokens * heads;
-    for (int r0 = (threadIdx.x >> 5) * RPW; r0 < rows; r0 += kThreads / 32 * RPW) {
-      const int r = r0 + lane / LPR;
-      const bool live = r < rows;
-      const int t = live ? r / heads : 0, hd = live ? r % heads : 0;
-      const bool key = hd >= a.Hq;
-      const int64_t tok = t0 + t;
-      const T* src = key ? static_cast<const T*>(a.k) + tok * a.k_stride + (hd - a.Hq) * D
-                         : static_cast<const T*>(a.q) + tok * a.q_stride + hd * D;
-      T* dst = key ? static_cast<T*>(a.k_out) + (tok * a.Hkv + (hd - a.Hq)) * D
-                   : static_cast<T*>(a.q_out) + (tok * a.Hq + hd) * D;
-      Vec8<T> x0, x1;
-      if (live) x0.load(src + first), x1.load(src + second);
+    float2 cs[8];  // of the lane's pairs: half: i with first + i; interleaved: first's four, then second's
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      cs[i] = !rotated ? make_float2(1.f, 0.f) : a.interleaved ? turn[((i < 4 ? first : second) >> 1) + (i & 3)] : turn[first + i];
+    int kind = -1;  // whose weights w holds: 0 queries, 1 keys
+    float w[16];
+    auto rows = [&](int gi, Vec8<T>& x, Vec8<T>& y) {  // loads; the row's head or -1
+      const bool key = gi >= groups_q;
+      const int hd = (key ? gi - groups_q : gi) * RPW + sub;
+      if (gi >= groups || hd >= (key ? a.Hkv : a.Hq)) return -1;
+      const T* src = (key ? static_cast<const T*>(a.k) + t * a.k_stride : static_cast<const T*>(a.q) + t * a.q_stride) + hd * D;
+      x.load(src + first), y.load(src + second);
+      return hd;
+    };
+    auto finish = [&](int gi, int hd, const Vec8<T>& x, const Vec8<T>& y) {
+      if (gi >= groups) return;
+      const int key = gi >= groups_q;
+      if (key != kind) {
+        kind = key;
+        const float4* src = reinterpret_cast<const float4*>(key ? a.k_weight : a.q_weight);
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          const float4 u = __ldg(src + (first + i) / 4), v = __ldg(src + (second + i) / 4);
+          w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
+          w[8 + i] = v.x, w[9 + i] = v.y, w[10 + i] = v.z, w[11 + i] = v.w;
+        }
+      }
       float u[8], v[8];
-      x0.to(u), x1.to(v);
+      x.to(u), y.to(v);
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum = fmaf(u[i], u[i], fmaf(v[i], v[i], sum));
 #pragma unroll
       for (int m = LPR / 2; m; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
       const float f = 1.0f / sqrtf(sum * (1.0f / D) + a.eps);
-      const float4* w = reinterpret_cast<const float4*>(key ? a.k_weight : a.q_weight);
 #pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        const float4 wu = __ldg(w + (first + i) / 4), wv = __ldg(w + (second + i) / 4);
-        u[i] *= f * wu.x, u[i + 1] *= f * wu.y, u[i + 2] *= f * wu.z, u[i + 3] *= f * wu.w;
-        v[i] *= f * wv.x, v[i + 1] *= f * wv.y, v[i + 2] *= f * wv.z, v[i + 3] *= f * wv.w;
-      }
-      if (rotated) {
-        const float2* cs = turn + t * half;
-        if (a.interleaved) {
+      for (int i = 0; i < 8; ++i) u[i] *= f * w[i], v[i] *= f * w[8 + i];
+      if (a.interleaved) {
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            const float2 p = cs[(first + i) / 2], q = cs[(second + i) / 2];
-            const float u0 = u[i], v0 = v[i];
-            u[i] = u0 * p.x - u[i + 1] * p.y, u[i + 1] = u[i + 1] * p.x + u0 * p.y;
-            v[i] = v0 * q.x - v[i + 1] * q.y, v[i + 1] = v[i + 1] * q.x + v0 * q.y;
-          }
-        } else {
+        for (int i = 0; i < 8; i += 2) {
+          const float2 p = cs[i / 2], q = cs[4 + i / 2];
+          const float u0 = u[i], v0 = v[i];
+          u[i] = u0 * p.x - u[i + 1] * p.y, u[i + 1] = u[i + 1] * p.x + u0 * p.y;
+          v[i] = v0 * q.x - v[i + 1] * q.y, v[i + 1] = v[i + 1] * q.x + v0 * q.y;
+        }
+      } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 p = cs[first + i];
-            const float u0 = u[i];
-            u[i] = u0 * p.x - v[i] * p.y, v[i] = v[i] * p.x + u0 * p.y;
-          }
+        for (int i = 0; i < 8; ++i) {
+          const float u0 = u[i];
+          u[i] = u0 * cs[i].x - v[i] * cs[i].y, v[i] = v[i] * cs[i].x + u0 * cs[i].y;
         }
       }
-      if (live) Vec8<T>::store(dst + first, u), Vec8<T>::store(dst + second, v);
+      if (hd < 0) return;
+      T* dst = key ? static_cast<T*>(a.k_out) + (t * a.Hkv + hd) * D : static_cast<T*>(a.q_out) + (t * a.Hq + hd) * D;
+      Vec8<T>::store(dst + first, u), Vec8<T>::store(dst + second, v);
+    };
+    // two groups' loads under way at a time
+    for (int gi = share; gi < groups; gi += 2 * a.wpt) {
+      Vec8<T> x0{}, y0{}, x1{}, y1{};
+      const int h0 = rows(gi, x0, y0), h1 = rows(gi + a.wpt, x1, y1);
+      finish(gi, h0, x0, y0);
+      finish(gi + a.wpt, h1, x1, y1);
     }
-    __syncthreads();
   }
 }
 
-template <typename T>
-int launch_t(const NormRopeArgs& a, int blocks, cudaStream_t stream) {
-  const size_t smem = size_t(a.tb) * (a.rot / 2) * sizeof(float2) + size_t(a.rot / 2) * sizeof(uint64_t);
-  switch (a.D) {
-    case 128: norm_rope_kernel<T, 128><<<blocks, kThreads, smem, stream>>>(a); break;
-    case 256: norm_rope_kernel<T, 256><<<blocks, kThreads, smem, stream>>>(a); break;
-    default: norm_rope_kernel<T, 512><<<blocks, kThreads, smem, stream>>>(a); break;
-  }
+template <typename T, int D>
+int launch_d(NormRopeArgs a, int sms, cudaStream_t stream) {
+  const int groups = (a.Hq + kRowsOfWarp<D> - 1) / kRowsOfWarp<D> + (a.Hkv + kRowsOfWarp<D> - 1) / kRowsOfWarp<D>;
+  // warps of a token: all eight for few tokens, whose latency counts, one where there are enough to fill the GPU
+  a.wpt = 1;
+  while (a.wpt < kWarps && int64_t(a.n) * a.wpt < 24 * sms && a.wpt < groups) a.wpt *= 2;
+  const int64_t blocks = (int64_t(a.n) * a.wpt + kWarps - 1) / kWarps;
+  norm_rope_kernel<T, D><<<unsigned(std::min<int64_t>(blocks, 8 * sms)), kThreads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
+}
+template <typename T>
+int launch_t(const NormRopeArgs& a, int sms, cudaStream_t stream) {
+  return a.D == 128 ? launch_d<T, 128>(a, sms, stream) : a.D == 256 ? launch_d<T, 256>(a, sms, stream) : launch_d<T, 512>(a, sms, stream);
 }
 
 }  // namespace
 
-int launch_norm_rope(const NormRopeArgs& args, cudaStream_t stream) {
+int launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
   int sms = 0, dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return OSCAR_ERR_LAUNCH;
-  NormRopeArgs a = args;
-  const int most = sms * 4;
-  a.tb = std::min(4, std::max(1, a.n / most));
-  const int blocks = std::min(most, (a.n + a.tb - 1) / a.tb);
-  return a.fp32 ? launch_t<float>(a, blocks, stream) : launch_t<__nv_bfloat16>(a, blocks, stream);
+  return a.fp32 ? launch_t<float>(a, sms, stream) : launch_t<__nv_bfloat16>(a, sms, stream);
 }
 
 }  // namespace oscar

@@ -172,17 +172,22 @@ def _check(t, name: str, dtypes, shape=None, min_bytes=None, optional: bool = Fa
         raise ValueError(f"oscar_kv: {name} holds {t.nbytes} bytes, needs {min_bytes}")
 
 
+_torch = None
+
+
 def _dt():
-    import torch
-    return torch
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
 
 
 _known = {}  # (C struct, cache bytes) of the configurations in use, by their values
 
 
 def _known_cfg(cfg: "KVConfig"):
-    key = (cfg.num_layers, cfg.batch, cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim, cfg.sink, cfg.recent,
-           cfg.capacity, cfg.k_clip, cfg.v_clip, cfg.flags, cfg.group_size)
+    key = tuple(cfg.__dict__.values())  # the fields, in their order
     hit = _known.get(key)
     if hit is None:
         if len(_known) >= 256:
@@ -447,23 +452,87 @@ def attn_decode_prefix(cfg: KVConfig, cache, prefix_cfg: KVConfig, prefix_cache,
     return rc
 
 
-def _out_dtypes(cfg: KVConfig):
-    torch = _dt()
-    return (torch.float32,) if cfg.flags & FLAG_OUT_FP32 else (torch.bfloat16,)
+class _Args:
+    """Checks the tensor arguments of one call and gives their addresses: type, shape, memory (dense, unless the caller says
+    otherwise) and device.  The library launches on the current device, so every tensor has to be there."""
+
+    def __init__(self, cfg: KVConfig):
+        torch = _dt()
+        self.device = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+        self.cfg = cfg
+        flags = cfg.flags
+        self.kind_in = torch.float32 if flags & FLAG_IN_FP32 else torch.bfloat16
+        self.kind_out = torch.float32 if flags & FLAG_OUT_FP32 else torch.bfloat16
+
+    def place(self, t):
+        d = t.get_device()
+        if d != self.device:
+            if d < 0:
+                raise ValueError(f"oscar_kv: expected a CUDA tensor, got one on {t.device}")
+            if self.device == -2:
+                self.device = _dt().cuda.current_device()
+                return self.place(t)
+            raise ValueError(f"oscar_kv: tensor on {t.device}, current device is cuda:{self.device}")
+        return t.data_ptr()
+
+    def __call__(self, t, name: str, kind, shape, optional: bool = False):
+        if t is None:
+            if optional:
+                return None
+            raise ValueError(f"oscar_kv: {name} is required")
+        if t.dtype is not kind or t.shape != shape:
+            _check(t, name, (kind,), shape=shape)
+        if not t.is_contiguous():
+            raise ValueError("oscar_kv: expected a contiguous tensor")
+        return self.place(t)
+
+    def memory(self, t, name: str, kind, nbytes: int, optional: bool = False):
+        """Any shape, nbytes at least."""
+        if t is None:
+            if optional:
+                return None
+            raise ValueError(f"oscar_kv: {name} is required")
+        if t.dtype is not kind or t.nbytes < nbytes:
+            _check(t, name, (kind,), min_bytes=nbytes)
+        if not t.is_contiguous():
+            raise ValueError("oscar_kv: expected a contiguous tensor")
+        return self.place(t)
+
+    def cache(self, cfg: KVConfig, t, name: str = "cache"):
+        """The configuration for the library, and the cache's address."""
+        c, total = _known_cfg(cfg)
+        return ctypes.byref(c), self.memory(t, name, _dt().uint8, total)
+
+    def rotation(self, t, name: str):
+        return self.memory(t, name, _dt().float32, self.cfg.head_dim * self.cfg.head_dim * 4,
+                           optional=bool(self.cfg.flags & FLAG_HADAMARD))
+
+    def status(self, t):
+        return None if t is None else self.memory(t, "status", _dt().int32, 4)
+
+    def token_rows(self, t, name: str, shape):
+        """Address of [tokens][heads][head_dim] and the elements from one token to the next, which may lie further on than the
+        token's heads reach (a fused projection)."""
+        _check(t, name, (self.kind_in,), shape=shape)
+        at = self.place(t)
+        n, heads, d = shape
+        if n == 0:
+            return at, heads * d
+        step, head, one = t.stride()
+        if one != 1 or (heads > 1 and head != d):
+            raise ValueError(f"oscar_kv: the heads of a token of {name} must be contiguous")
+        return at, heads * d if n == 1 else step
+
+    def stream(self, stream):
+        if stream is None:
+            return _dt().cuda.current_stream(self.device).cuda_stream
+        return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _token_rows(t, name: str, kinds, shape) -> int:
-    """Elements from one token's heads [heads][head_dim] to the next one's, which may lie further on (a fused projection)."""
-    _check(t, name, kinds, shape=shape)
-    if not t.is_cuda:
-        raise ValueError(f"oscar_kv: expected a CUDA tensor, got one on {t.device}")
-    n, heads, d = shape
-    dense = heads * d
-    if n == 0:
-        return dense
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
-        raise ValueError(f"oscar_kv: the heads of a token of {name} must be contiguous")
-    return dense if n == 1 else int(t.stride(0))
+def _result(fn: str, rc: int, check: bool) -> int:
+    if check and rc != 0:
+        raise OscarError(fn, rc)
+    return rc
 
 
 def qk_norm_rope(cfg: KVConfig, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, eps: float = 1e-6,
@@ -472,27 +541,19 @@ def qk_norm_rope(cfg: KVConfig, q, k, q_weight, k_weight, positions, inv_freq, q
     projection), then the rotation of the first 2 * len(inv_freq) channels by positions * inv_freq (None: no rotation),
     into q_out and k_out."""
     torch = _dt()
-    D = cfg.head_dim
     if q is None or q.dim() != 3:
         raise ValueError("oscar_kv: q must be [n][num_q_heads][head_dim]")
-    n = int(q.shape[0])
-    kinds = _in_dtypes(cfg)
-    shapes = (n, cfg.num_q_heads, D), (n, cfg.num_kv_heads, D)
-    strides = _token_rows(q, "q", kinds, shapes[0]), _token_rows(k, "k", kinds, shapes[1])
-    _check(q_out, "q_out", kinds, shape=shapes[0])
-    _check(k_out, "k_out", kinds, shape=shapes[1])
-    _check(q_weight, "q_weight", (torch.float32,), shape=(D,))
-    _check(k_weight, "k_weight", (torch.float32,), shape=(D,))
-    _check(inv_freq, "inv_freq", (torch.float32,), optional=True)
+    arg, n, D = _Args(cfg), q.shape[0], cfg.head_dim
+    shape_q, shape_k, f32 = (n, cfg.num_q_heads, D), (n, cfg.num_kv_heads, D), torch.float32
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    _check(positions, "positions", (torch.int32,), shape=(n,), optional=rot == 0)
-    _same_device(q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out)
-    rc = lib().qk_norm_rope(ctypes.byref(cfg.c()), q.data_ptr(), strides[0], k.data_ptr(), strides[1], n, _ptr(q_weight),
-                            _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), rot, int(bool(interleaved)),
-                            _ptr(q_out), _ptr(k_out), _stream(stream))
-    if check and rc != 0:
-        raise OscarError("qk_norm_rope", rc)
-    return rc
+    (pq, sq), (pk, sk) = arg.token_rows(q, "q", shape_q), arg.token_rows(k, "k", shape_k)
+    rc = lib().qk_norm_rope(ctypes.byref(_known_cfg(cfg)[0]), pq, sq, pk, sk, n, arg(q_weight, "q_weight", f32, (D,)),
+                            arg(k_weight, "k_weight", f32, (D,)), eps,
+                            arg(positions, "positions", torch.int32, (n,), optional=rot == 0),
+                            arg(inv_freq, "inv_freq", f32, (rot // 2,), optional=True), rot, 1 if interleaved else 0,
+                            arg(q_out, "q_out", arg.kind_in, shape_q), arg(k_out, "k_out", arg.kind_in, shape_k),
+                            arg.stream(stream))
+    return _result("qk_norm_rope", rc, check)
 
 
 def attn_prompt(cfg: KVConfig, q, k, v, cu_seqlens, out, lse=None, sm_scale: float = 0.0, status=None, stream=None,
@@ -502,20 +563,13 @@ def attn_prompt(cfg: KVConfig, q, k, v, cu_seqlens, out, lse=None, sm_scale: flo
     torch = _dt()
     if q is None or q.dim() != 3:
         raise ValueError("oscar_kv: q must be [n][num_q_heads][head_dim]")
-    n, Hq, H, D = int(q.shape[0]), cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim
-    _check(q, "q", _in_dtypes(cfg), shape=(n, Hq, D))
-    _check(k, "k", _in_dtypes(cfg), shape=(n, H, D))
-    _check(v, "v", _in_dtypes(cfg), shape=(n, H, D))
-    _check(cu_seqlens, "cu_seqlens", (torch.int32,), shape=(cfg.batch + 1,))
-    _check(out, "out", _out_dtypes(cfg), shape=(n, Hq, D))
-    _check(lse, "lse", (torch.float32,), shape=(n, Hq), optional=True)
-    _check(status, "status", (torch.int32,), min_bytes=4, optional=True)
-    _same_device(q, k, v, cu_seqlens, out, lse, status)
-    rc = lib().attn_prompt(ctypes.byref(cfg.c()), _ptr(q), _ptr(k), _ptr(v), n, _ptr(cu_seqlens), float(sm_scale), _ptr(out),
-                           _ptr(lse), _ptr(status), _stream(stream))
-    if check and rc != 0:
-        raise OscarError("attn_prompt", rc)
-    return rc
+    arg, n, Hq, D = _Args(cfg), q.shape[0], cfg.num_q_heads, cfg.head_dim
+    rows, kv = (n, Hq, D), (n, cfg.num_kv_heads, D)
+    rc = lib().attn_prompt(ctypes.byref(_known_cfg(cfg)[0]), arg(q, "q", arg.kind_in, rows), arg(k, "k", arg.kind_in, kv),
+                           arg(v, "v", arg.kind_in, kv), n, arg(cu_seqlens, "cu_seqlens", torch.int32, (cfg.batch + 1,)),
+                           sm_scale, arg(out, "out", arg.kind_out, rows),
+                           arg(lse, "lse", torch.float32, (n, Hq), optional=True), arg.status(status), arg.stream(stream))
+    return _result("attn_prompt", rc, check)
 
 
 def kv_append_packed(cfg: KVConfig, cache, layer: int, k_new, v_new, cu_seqlens, start_pos, R_K, R_V, status=None,
@@ -525,29 +579,19 @@ def kv_append_packed(cfg: KVConfig, cache, layer: int, k_new, v_new, cu_seqlens,
     torch = _dt()
     if k_new is None or k_new.dim() != 3:
         raise ValueError("oscar_kv: k_new must be [n][num_kv_heads][head_dim]")
-    n = int(k_new.shape[0])
-    shape = (n, cfg.num_kv_heads, cfg.head_dim)
-    _check(k_new, "k_new", _in_dtypes(cfg), shape=shape)
-    _check(v_new, "v_new", _in_dtypes(cfg), shape=shape)
-    _check(cu_seqlens, "cu_seqlens", (torch.int32,), shape=(cfg.batch + 1,))
-    _check(start_pos, "start_pos", (torch.int32,), shape=(cfg.batch,))
-    _check(status, "status", (torch.int32,), min_bytes=4, optional=True)
-    c = _check_cache(cfg, cache)
-    _check_rot(cfg, R_K, "R_K")
-    _check_rot(cfg, R_V, "R_V")
-    _same_device(cache, k_new, v_new, cu_seqlens, start_pos, R_K, R_V, status)
-    rc = lib().kv_append_packed(c, _ptr(cache), layer, _ptr(k_new), _ptr(v_new), n, _ptr(cu_seqlens), _ptr(start_pos),
-                                _ptr(R_K), _ptr(R_V), _ptr(status), _stream(stream))
-    if check and rc != 0:
-        raise OscarError("kv_append_packed", rc)
-    return rc
+    arg, n = _Args(cfg), k_new.shape[0]
+    rows, i32 = (n, cfg.num_kv_heads, cfg.head_dim), torch.int32
+    c, at = arg.cache(cfg, cache)
+    rc = lib().kv_append_packed(c, at, layer, arg(k_new, "k_new", arg.kind_in, rows), arg(v_new, "v_new", arg.kind_in, rows), n,
+                                arg(cu_seqlens, "cu_seqlens", i32, (cfg.batch + 1,)),
+                                arg(start_pos, "start_pos", i32, (cfg.batch,)), arg.rotation(R_K, "R_K"),
+                                arg.rotation(R_V, "R_V"), arg.status(status), arg.stream(stream))
+    return _result("kv_append_packed", rc, check)
 
 
 def attn_mass_workspace_bytes(cfg: KVConfig, n_new: int) -> int:
     n = ctypes.c_uint64(0)
-    rc = lib().attn_mass_workspace_query(ctypes.byref(cfg.c()), int(n_new), ctypes.byref(n))
-    if rc != 0:
-        raise OscarError("attn_mass_workspace_query", rc)
+    _result("attn_mass_workspace_query", lib().attn_mass_workspace_query(ctypes.byref(cfg.c()), int(n_new), ctypes.byref(n)), True)
     return int(n.value)
 
 
@@ -556,35 +600,23 @@ def attn_mass(cfg: KVConfig, cache, layer: int, q, seq_lens, R_K, lse, mass_out,
     """mass_out [B][Hkv][capacity] = mass_in (None: 0) plus the attention weight that every cached position receives from
     the last q_lens[b] (None: n) tokens of its sequence, q [B][n][Hq][D] with the lse [B][n][Hq] of their attention."""
     torch = _dt()
-    B, Hq, D = cfg.batch, cfg.num_q_heads, cfg.head_dim
     if q is None or q.dim() != 4:
         raise ValueError("oscar_kv: q must be [batch][n_new][num_q_heads][head_dim]")
-    n = int(q.shape[1])
-    whole = (B, cfg.num_kv_heads, cfg.capacity)
-    _check(q, "q", _in_dtypes(cfg), shape=(B, n, Hq, D))
-    _check(lse, "lse", (torch.float32,), shape=(B, n, Hq))
-    _check(mass_out, "mass_out", (torch.float32,), shape=whole)
-    _check(mass_in, "mass_in", (torch.float32,), shape=whole, optional=True)
-    _check(seq_lens, "seq_lens", (torch.int32,), shape=(B,))
-    _check(q_lens, "q_lens", (torch.int32,), shape=(B,), optional=True)
-    _check(status, "status", (torch.int32,), min_bytes=4, optional=True)
-    _check(workspace, "workspace", (torch.uint8,))
-    c = _check_cache(cfg, cache)
-    _check_rot(cfg, R_K, "R_K")
-    _same_device(cache, q, seq_lens, q_lens, R_K, lse, mass_in, mass_out, workspace, status)
-    rc = lib().attn_mass(c, _ptr(cache), layer, _ptr(q), n, _ptr(q_lens), _ptr(seq_lens), int(seq_len_hint), _ptr(R_K),
-                         float(sm_scale), _ptr(lse), _ptr(mass_in), _ptr(mass_out), _ptr(workspace),
-                         int(workspace.numel()), _ptr(status), _stream(stream))
-    if check and rc != 0:
-        raise OscarError("attn_mass", rc)
-    return rc
+    arg, n, B, Hq = _Args(cfg), q.shape[1], cfg.batch, cfg.num_q_heads
+    whole, f32, i32 = (B, cfg.num_kv_heads, cfg.capacity), torch.float32, torch.int32
+    c, at = arg.cache(cfg, cache)
+    ws = arg.memory(workspace, "workspace", torch.uint8, 0)
+    rc = lib().attn_mass(c, at, layer, arg(q, "q", arg.kind_in, (B, n, Hq, cfg.head_dim)), n,
+                         arg(q_lens, "q_lens", i32, (B,), optional=True), arg(seq_lens, "seq_lens", i32, (B,)), seq_len_hint,
+                         arg.rotation(R_K, "R_K"), sm_scale, arg(lse, "lse", f32, (B, n, Hq)),
+                         arg(mass_in, "mass_in", f32, whole, optional=True), arg(mass_out, "mass_out", f32, whole), ws,
+                         workspace.numel(), arg.status(status), arg.stream(stream))
+    return _result("attn_mass", rc, check)
 
 
 def kv_evict_workspace_bytes(cfg: KVConfig, keep: int) -> int:
     n = ctypes.c_uint64(0)
-    rc = lib().kv_evict_workspace_query(ctypes.byref(cfg.c()), int(keep), ctypes.byref(n))
-    if rc != 0:
-        raise OscarError("kv_evict_workspace_query", rc)
+    _result("kv_evict_workspace_query", lib().kv_evict_workspace_query(ctypes.byref(cfg.c()), int(keep), ctypes.byref(n)), True)
     return int(n.value)
 
 
@@ -594,23 +626,16 @@ def kv_evict(cfg: KVConfig, cache, layer: int, mass, seq_lens, keep: int, out_cf
     of every KV head, into a layer of out_cache; new_lens [B] (may be seq_lens) receives the lengths, out_mass
     [B][Hkv][out capacity] the masses of what stays, kept [B][Hkv][keep] its old positions (-1 behind the last)."""
     torch = _dt()
-    B, H = cfg.batch, cfg.num_kv_heads
-    _check(mass, "mass", (torch.float32,), shape=(B, H, cfg.capacity))
-    _check(seq_lens, "seq_lens", (torch.int32,), shape=(B,))
-    _check(new_lens, "new_lens", (torch.int32,), shape=(B,))
-    _check(out_mass, "out_mass", (torch.float32,), shape=(B, H, out_cfg.capacity), optional=True)
-    _check(kept, "kept", (torch.int32,), shape=(B, H, int(keep)), optional=True)
-    _check(status, "status", (torch.int32,), min_bytes=4, optional=True)
-    _check(workspace, "workspace", (torch.uint8,))
-    c = _check_cache(cfg, cache)
-    oc = _check_cache(out_cfg, out_cache, "out_cache")
-    _same_device(cache, out_cache, mass, seq_lens, new_lens, out_mass, kept, workspace, status)
-    rc = lib().kv_evict(c, _ptr(cache), layer, _ptr(mass), _ptr(seq_lens), int(keep), oc, _ptr(out_cache), out_layer,
-                        _ptr(out_mass), _ptr(kept), _ptr(new_lens), _ptr(workspace), int(workspace.numel()), _ptr(status),
-                        _stream(stream))
-    if check and rc != 0:
-        raise OscarError("kv_evict", rc)
-    return rc
+    arg, B, H = _Args(cfg), cfg.batch, cfg.num_kv_heads
+    f32, i32 = torch.float32, torch.int32
+    c, at = arg.cache(cfg, cache)
+    oc, out_at = arg.cache(out_cfg, out_cache, "out_cache")
+    ws = arg.memory(workspace, "workspace", torch.uint8, 0)
+    rc = lib().kv_evict(c, at, layer, arg(mass, "mass", f32, (B, H, cfg.capacity)), arg(seq_lens, "seq_lens", i32, (B,)), keep, oc,
+                        out_at, out_layer, arg(out_mass, "out_mass", f32, (B, H, out_cfg.capacity), optional=True),
+                        arg(kept, "kept", i32, (B, H, keep), optional=True), arg(new_lens, "new_lens", i32, (B,)), ws,
+                        workspace.numel(), arg.status(status), arg.stream(stream))
+    return _result("kv_evict", rc, check)
 
 
 def set_profile_events(start=None, stop=None) -> None:
