@@ -9,18 +9,19 @@
 // A decode step's rows are few, and the bytes of K bound it (36 per position at
 // head_dim 128, and 8 of the masses); so keys go from global memory to registers
 // to mma.sync m16n8k16, positions on M, and nothing but the sum over rows is
-// written.  A warp takes 32 positions at a time, with the next ones' loads in
-// flight: a lane's two code words of a row are exactly its A fragments of the
-// group (the header's K layout), unpacked by a shift and an AND each into fp16
-// subnormals, code * 2^-16, at the top of the mantissa, where the products lose
-// nothing (common.cuh).  The columns are four query rows' high and low fp16 parts,
-// 22 bits in all, scaled by a power of two per row; a lane then has its row's
-// whole score in two accumulators, and the rows' sum is two shuffles.
-// BF16 rows take the same path with three bf16 parts; a lane's 16-byte pieces
-// of a row are its fragments, channels in an order of their own.
+// written.  A warp works for itself, without shared memory: 32 positions at a
+// time, the next ones' loads under way.  A lane's two code words of a row are
+// exactly its A fragments of the group (the header's K layout), unpacked by a
+// shift and an AND each into fp16 subnormals, code * 2^-16, at the top of the
+// mantissa, where the products lose nothing (common.cuh).  The columns are four
+// query rows' high and low fp16 parts, 22 bits in all, scaled by a power of two
+// per row; a lane then has its row's whole score in two accumulators, and the sum
+// over the rows is two shuffles.  BF16 rows take the same path with three bf16
+// parts; a lane's 16-byte pieces of a row are its fragments, channels in an order
+// of their own.
 //
-// Blocks of query rows (up to 16) follow each other over a block's positions, the
-// masses of which stay in shared memory.
+// The rows' fragments are written once by a kernel of their own behind the query
+// rotation: built by every block they cost as much as the positions themselves.
 #include <algorithm>
 
 #include "rows_tc.cuh"
@@ -30,190 +31,246 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kBatch = 32;          // positions of a warp's turn
-constexpr int kMostChunk = 4096;    // positions of a block
+constexpr int kMostPiece = 256;     // positions of a warp
 
-// The codes at bits 2 p and 16 + 2 p of a word as fp16 values code * 2^-16.
-template <uint32_t mask>
+// The codes at bits 2 p and 16 + 2 p of a word as fp16 values: code * 2^-16 for odd p, whose shift to the top of the
+// mantissa leaves the even one below it, code * 2^-18.  (A shift for each would cost a quarter more of what the kernel has
+// most of, logic instructions.)  The query's fragments are four times larger there.  bits: 3, or 2 for the high bit alone.
+template <uint32_t bits>
 __device__ __forceinline__ void codes_of(uint32_t w, uint32_t (&r)[8]) {
 #pragma unroll
-  for (int p = 0; p < 8; ++p) r[p] = (p < 4 ? w << (8 - 2 * p) : w >> (2 * p - 8)) & mask;
+  for (int p = 0; p < 8; p += 2) {
+    const uint32_t x = p < 4 ? w << (6 - 2 * p) : w >> (2 * p - 6);
+    r[p] = x & (bits * 0x00400040u);
+    r[p + 1] = x & (bits * 0x01000100u);
+  }
 }
 
-template <int D, int NB>
-struct Mass {
-  static constexpr int Dg = D / kGroup, KS = D / 16, R = 4 * NB;  // groups, k steps, rows of a block
-  static constexpr int o16 = 0;                       // fp16 fragments [NB][KS][32] x 8 bytes
-  static constexpr int oBf = o16 + NB * KS * 32 * 8;  // bf16 fragments [NB][2][KS][32] x 8 bytes
-  static constexpr int oSum = oBf + 2 * NB * KS * 32 * 8;  // [R][Dg] sums of the row
-  static constexpr int oRow = oSum + R * Dg * 4;      // [R] factor, reference (high, low), last position
-  static constexpr int oMass = oRow + R * 16;
-  static constexpr int kBytes = oMass + kMostChunk * 4;
+// What the fragment kernel leaves, per (sequence, KV head), for tiles of four rows: fp16 fragments [tiles][D / 16][32] and
+// bf16 fragments [tiles][2][D / 16][32] of 8 bytes; per row (factor, reference high and low, last position) and the sums of
+// its groups [D / 128].
+struct Frags {
+  uint2 *f16, *fbf;
+  float4* row;
+  float* sum;
 };
+template <int D>
+__host__ __device__ inline Frags frags_of(const MassArgs& a, int64_t unit) {
+  const int64_t units = int64_t(a.g.B) * a.g.Hkv, piece = int64_t(a.tiles) * (D / 16) * 32;
+  uint8_t* at = a.frags;
+  Frags f;
+  f.f16 = reinterpret_cast<uint2*>(at) + unit * piece;
+  at += units * piece * 8;
+  f.fbf = reinterpret_cast<uint2*>(at) + unit * piece * 2;
+  at += units * piece * 16;
+  f.row = reinterpret_cast<float4*>(at) + unit * a.tiles * 4;
+  at += units * a.tiles * 64;
+  f.sum = reinterpret_cast<float*>(at) + unit * a.tiles * 4 * (D / kGroup);
+  return f;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) mass_frags_kernel(const MassArgs a) {
+  constexpr int Dg = D / kGroup, KS = D / 16;
+  const Geom& g = a.g;
+  const int lane = threadIdx.x & 31;
+  const int64_t at_row = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5), units = int64_t(g.B) * g.Hkv;
+  const int64_t unit = at_row / (4 * a.tiles);
+  pdl_wait();  // the rotated queries
+  if (unit >= units) return;
+  const int row = int(at_row - unit * 4 * a.tiles), b = int(unit / g.Hkv), h = int(unit % g.Hkv);
+  const int T = max(0, min(a.seq_lens[b], g.cap)), ql = max(0, a.q_lens ? min(a.q_lens[b], a.n) : a.n);
+  const bool on = row < ql * g.G;
+  const Frags f = frags_of<D>(a, unit);
+  const int64_t at = (int64_t(b) * a.n + row / g.G) * g.Hq + h * g.G + row % g.G;
+  const float* q = a.qrot + (on ? at : 0) * D;
+  uint32_t most = 0;
+  float v[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    v[i] = on ? q[lane + 32 * i] : 0.f;
+    if (isfinite(v[i])) most = max(most, __float_as_uint(fabsf(v[i])));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  // the largest finite component lands in [2^12, 2^13)
+  const int e = max(-100, (int(most) >> 23) - 126 - 13);
+  const float up = pow2i(min(126, -e));
+  const int tile = row >> 2, lead = (2 * (row & 3)) * 4;  // the first lane of the row's column
+  float sums[Dg];
+#pragma unroll
+  for (int j = 0; j < Dg; ++j) sums[j] = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const int ch = lane + 32 * i;
+    // fp16 parts: k step ch / 16, the fragment's register and lane by ch % 16
+    const int k = ch & 15, c = (k & 7) >> 1, in = 2 * (k >> 3) + (k & 1);
+    const float x = v[i] * up * (k < 8 ? 4.f : 1.f);
+    const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
+    sums[i / 4] += (__half2float(hi) + __half2float(lo)) * (k < 8 ? 0.25f : 1.f);
+    __half* to = reinterpret_cast<__half*>(f.f16 + (int64_t(tile) * KS + (ch >> 4)) * 32 + lead + c);
+    to[in] = hi;
+    to[16 + in] = lo;  // the next column: four lanes on
+    uint32_t w[3];
+    split3_bf16(v[i], w);
+    // piece ch / 8 = c + 4 m: registers x, y are step 2 m, z, w step 2 m + 1
+    const int piece = ch >> 3, cc = piece & 3, step = 2 * (piece >> 2) + ((ch & 7) >> 2), at2 = ch & 3;
+    uint16_t* s0 = reinterpret_cast<uint16_t*>(f.fbf + (int64_t(tile) * 2 * KS + step) * 32 + lead + cc);
+    uint16_t* s1 = s0 + KS * 32 * 4;
+    s0[at2] = uint16_t(w[0]);
+    s0[16 + at2] = uint16_t(w[1]);
+    s1[at2] = uint16_t(w[2]);
+    s1[16 + at2] = 0;
+  }
+#pragma unroll
+  for (int j = 0; j < Dg; ++j) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], o);
+    if (lane == 0) f.sum[row * Dg + j] = sums[j] * pow2i(max(-126, e));
+  }
+  if (lane == 0) {
+    const float x = on ? a.lse[at] : -INFINITY;
+    float hi = x * 1.4426950408889634f;
+    // the product's rounding and what the constant leaves out
+    float lo = fmaf(x, 1.4426950408889634f, -hi) + x * 1.9259629911266175e-8f;
+    if (!isfinite(hi)) hi = x == -INFINITY ? INFINITY : hi, lo = 0.f;  // a row without weight
+    f.row[row] = make_float4(pow2i(min(127, max(-126, e + 16))), hi, lo, __int_as_float(on ? T - ql + row / g.G : -1));
+  }
+}
 
 // Blocks on an SM at least, for the registers.
 template <int D, int NB>
-constexpr int resident() { return NB == 4 || D == 512 ? 2 : D == 256 ? 3 : NB == 1 ? 5 : 4; }
+constexpr int resident() { return D == 128 ? (NB == 1 ? 4 : 3) : 2; }
 
-template <int D, int NB, bool LM>
+// NB tiles of four rows at a time; ONE: there are no more.
+template <int D, int NB, bool LM, bool ONE>
 __global__ void __launch_bounds__(kThreads, (resident<D, NB>())) attn_mass_kernel(const MassArgs a) {
-  using C = Mass<D, NB>;
-  constexpr int Dg = C::Dg, KS = C::KS, R = C::R;
-  extern __shared__ __align__(16) uint8_t sm[];
-  uint2* f16 = reinterpret_cast<uint2*>(sm + C::o16);
-  uint2* fbf = reinterpret_cast<uint2*>(sm + C::oBf);
-  float* qsum = reinterpret_cast<float*>(sm + C::oSum);
-  float4* rowc = reinterpret_cast<float4*>(sm + C::oRow);
-  float* mass = reinterpret_cast<float*>(sm + C::oMass);
+  constexpr int Dg = D / kGroup, KS = D / 16;
+  constexpr bool kHold = ONE && NB * KS <= 16;  // the fragments stay in registers
+  constexpr bool kAhead = D == 128;             // as does a second batch; of longer rows one is enough under way
   const Geom& g = a.g;
-  const int unit = blockIdx.y, b = unit / g.Hkv, h = unit % g.Hkv;
+  const int unit = blockIdx.y, b = unit / g.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row8 = lane >> 2, col = lane & 3;
   const int given = a.seq_lens[b], T = max(0, min(given, g.cap));
   if (given > g.cap && blockIdx.x == 0 && threadIdx.x == 0) status_or(a.status, OSCAR_DEV_OVER_CAPACITY);
-  const int ql = max(0, a.q_lens ? min(a.q_lens[b], a.n) : a.n), rows = ql * g.G;
-  const int window = max(g.S, T - g.W);  // the ring's first position
+  const int ql = max(0, a.q_lens ? min(a.q_lens[b], a.n) : a.n), tiles = (ql * g.G + 3) / 4;
+  const int seen = T - ql;                // every row sees the positions up to this one
+  const int window = max(g.S, T - g.W);   // the ring's first position
   const uint8_t* base = a.layer_base;
-  const uint8_t* codes = base + g.sink_bytes + g.ring_bytes + int64_t(unit) * g.ncap * (D / 4);
+  const uint8_t* codes = base + g.sink_bytes + g.ring_bytes + int64_t(unit) * g.ncap * (D / 4) + 8 * col;
   const uint8_t* sz = base + g.sink_bytes + g.ring_bytes + g.codes_bytes + int64_t(unit) * g.ncap * (Dg * 4);
   const uint8_t* sink = base + int64_t(unit) * g.S * (2 * D);
   const uint8_t* ring = base + g.sink_bytes + int64_t(unit) * g.W * (2 * D);
-  pdl_wait();  // the rotated queries
+  const Frags f = frags_of<D>(a, unit);
+  const float* mass_in = a.mass_in ? a.mass_in + int64_t(unit) * g.cap : nullptr;
+  float* mass_out = a.mass_out + int64_t(unit) * g.cap;
 
-  for (int64_t c0 = int64_t(blockIdx.x) * a.chunk; c0 < T; c0 += int64_t(gridDim.x) * a.chunk) {
-    const int p0 = int(c0), p1 = min(T, p0 + a.chunk);
-    const int i0 = max(p0, g.S), i1 = min(p1, window);        // INT2 positions
-    const bool wide = p0 < min(g.S, T) || p1 > window;
-    for (int i = threadIdx.x; i < p1 - p0; i += kThreads) mass[i] = 0.f;
-    struct Batch {
-      uint2 words[Dg][4];
-      uint32_t sz[Dg][4];
-    };
-    const uint8_t* my_codes = codes + 8 * col;
-    auto load = [&](Batch& x, int p) {
-      const int at = p + row8 - g.S;
-      if (p + kBatch <= i1) {  // positions 8 apart are constants apart
-        const uint8_t *c = my_codes + int64_t(at) * (D / 4), *z = sz + int64_t(at) * (Dg * 4);
+  struct Batch {
+    uint2 words[Dg][4];
+    uint32_t sz[Dg][4];
+    float mass;  // of the position that this lane writes
+  };
+  // INT2 positions p + row8 + 8 i below end
+  auto load = [&](Batch& x, int p, int end) {
+    const int at = p + row8 - g.S;
+    if (p + kBatch <= end) {  // positions 8 apart are constants apart
+      const uint8_t *c = codes + int64_t(at) * (D / 4), *z = sz + int64_t(at) * (Dg * 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < Dg; ++j) {
-            x.words[j][i] = __ldg(reinterpret_cast<const uint2*>(c + i * 8 * (D / 4) + 32 * j));
-            x.sz[j][i] = __ldg(reinterpret_cast<const uint32_t*>(z + i * 8 * (Dg * 4) + 4 * j));
-          }
-      } else if (p < i1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t last = min(at + 8 * i, i1 - 1 - g.S);
-#pragma unroll
-          for (int j = 0; j < Dg; ++j) {
-            x.words[j][i] = __ldg(reinterpret_cast<const uint2*>(my_codes + last * (D / 4) + 32 * j));
-            x.sz[j][i] = __ldg(reinterpret_cast<const uint32_t*>(sz + last * (Dg * 4) + 4 * j));
-          }
-        }
-      }
-    };
-    constexpr int kStep = kBatch * kWarps;
-    constexpr bool kAhead = D == 128 && NB < 4;  // two batches under way where the registers allow
-    for (int r0 = 0; r0 < rows; r0 += R) {
-      int p = i0 + kBatch * warp;
-      Batch x0, x1;
-      load(x0, p);
-      if (kAhead) load(x1, p + kStep);
-      // ----------------- the rows' fragments, factors and references ------------------
-      __syncthreads();
-      for (int r = warp; r < R; r += kWarps) {
-        const int row = r0 + r;
-        const bool on = row < rows;
-        const int64_t at = int64_t(b * a.n + row / g.G) * g.Hq + h * g.G + row % g.G;
-        const float* q = a.qrot + (on ? at : 0) * D;
-        uint32_t most = 0;
-        float v[D / 32];
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          v[i] = on ? q[lane + 32 * i] : 0.f;
-          if (isfinite(v[i])) most = max(most, __float_as_uint(fabsf(v[i])));
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-        // the largest finite component lands in [2^14, 2^15)
-        const int e = max(-100, (int(most) >> 23) - 126 - 15);
-        const float up = pow2i(min(126, -e));
-        float sums[Dg];
-#pragma unroll
-        for (int j = 0; j < Dg; ++j) sums[j] = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const int ch = lane + 32 * i;
-          // fp16 parts: group j = ch / 128, k step (ch % 128) / 16 of it, the fragment's half and lane by ch % 16
-          const float x = v[i] * up;
-          const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
-          sums[i / 4] += __half2float(hi) + __half2float(lo);
-          const int k = ch & 15, c = (k & 7) >> 1, reg = k >> 3, part = k & 1;
-          __half* f = reinterpret_cast<__half*>(f16 + ((r >> 2) * KS + (ch >> 4)) * 32 + (2 * (r & 3)) * 4 + c);
-          f[2 * reg + part] = hi;
-          f[16 + 2 * reg + part] = lo;  // the next column: four lanes on
-          if (wide) {
-            uint32_t w[3];
-            split3_bf16(v[i], w);
-            // piece ch / 8 = col + 4 m: registers x, y are step 2 m, z, w step 2 m + 1
-            const int piece = ch >> 3, cc = piece & 3, m = piece >> 2, in = ch & 7;
-            const int step = 2 * m + (in >> 2), rg = (in >> 1) & 1;
-            uint16_t* s0 = reinterpret_cast<uint16_t*>(fbf + (((r >> 2) * 2) * KS + step) * 32 + (2 * (r & 3)) * 4 + cc);
-            uint16_t* s1 = reinterpret_cast<uint16_t*>(fbf + (((r >> 2) * 2 + 1) * KS + step) * 32 + (2 * (r & 3)) * 4 + cc);
-            s0[2 * rg + (in & 1)] = uint16_t(w[0]);
-            s0[16 + 2 * rg + (in & 1)] = uint16_t(w[1]);
-            s1[2 * rg + (in & 1)] = uint16_t(w[2]);
-            s1[16 + 2 * rg + (in & 1)] = 0;
-          }
-        }
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < Dg; ++j) {
-#pragma unroll
-          for (int o = 16; o; o >>= 1) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], o);
-          if (lane == 0) qsum[r * Dg + j] = sums[j] * pow2i(max(-126, e));
+          x.words[j][i] = __ldg(reinterpret_cast<const uint2*>(c + i * 8 * (D / 4) + 32 * j));
+          x.sz[j][i] = __ldg(reinterpret_cast<const uint32_t*>(z + i * 8 * (Dg * 4) + 4 * j));
         }
-        if (lane == 0) {
-          const float x = on ? a.lse[at] : -INFINITY;
-          float hi = x * 1.4426950408889634f;
-          // the product's rounding and what the constant leaves out
-          float lo = fmaf(x, 1.4426950408889634f, -hi) + x * 1.9259629911266175e-8f;
-          if (!isfinite(hi)) hi = x == -INFINITY ? INFINITY : hi, lo = 0.f;  // a row without weight
-          rowc[r] = make_float4(pow2i(min(127, max(-126, e + 16))), hi, lo, __int_as_float(on ? T - ql + row / g.G : -1));
+    } else if (p < end) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t last = min(at + 8 * i, end - 1 - g.S);
+#pragma unroll
+        for (int j = 0; j < Dg; ++j) {
+          x.words[j][i] = __ldg(reinterpret_cast<const uint2*>(codes + last * (D / 4) + 32 * j));
+          x.sz[j][i] = __ldg(reinterpret_cast<const uint32_t*>(sz + last * (Dg * 4) + 4 * j));
         }
       }
-      __syncthreads();
-      float fac[NB], ref[NB], ref2[NB], sums[NB][Dg];
-      int last[NB];
+    }
+    x.mass = mass_in && p + 8 * col + row8 < end ? mass_in[p + 8 * col + row8] : 0.f;
+  };
+  struct Rows {  // this lane's row of each tile
+    float fac[NB], ref[NB], ref2[NB], sum[NB][Dg];
+    int last[NB];
+  };
+  auto rows_of = [&](Rows& r, int t0) {
 #pragma unroll
-      for (int t = 0; t < NB; ++t) {
-        const float4 x = rowc[4 * t + col];
-        fac[t] = x.x, ref[t] = x.y, ref2[t] = x.z, last[t] = __float_as_int(x.w);
+    for (int t = 0; t < NB; ++t) {
+      const int row = 4 * min(t0 + t, tiles - 1) + col;
+      const float4 x = f.row[row];
+      r.fac[t] = x.x, r.ref[t] = t0 + t < tiles ? x.y : INFINITY, r.ref2[t] = x.z, r.last[t] = __float_as_int(x.w);
 #pragma unroll
-        for (int j = 0; j < Dg; ++j) sums[t][j] = qsum[(4 * t + col) * Dg + j];
+      for (int j = 0; j < Dg; ++j) r.sum[t][j] = f.sum[row * Dg + j];
+    }
+  };
+  // scores of four positions (0, 8, 16, 24 and row8 on) against this lane's rows: their weights
+  auto weigh = [&](const Rows& r, const float (&s)[NB][4], int p, float (&w)[4]) {
+    if (p + kBatch - 1 <= seen) {
+#pragma unroll
+      for (int t = 0; t < NB; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] += ex2z((s[t][i] - r.ref[t]) - r.ref2[t]);
+      return;
+    }
+#pragma unroll
+    for (int t = 0; t < NB; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x = ex2z((s[t][i] - r.ref[t]) - r.ref2[t]);
+        w[i] += p + 8 * i + row8 <= r.last[t] ? x : 0.f;
       }
-      const int seen = T - ql;  // every row sees the positions up to this one
-      // scores of four positions (0, 8, 16, 24 and row8 on) against this lane's rows: their weights, summed over the rows
-      auto weigh = [&](const float (&s)[NB][4], int p, int end) {
-        float w[4] = {0.f, 0.f, 0.f, 0.f};
+  };
+  // the rows' sum; column i of the quad writes position 8 i + row8
+  auto write = [&](float (&w)[4], int p, int end, float before) {
 #pragma unroll
-        for (int t = 0; t < NB; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = ex2z((s[t][i] - ref[t]) - ref2[t]);
-            w[i] += p + 8 * i + row8 <= max(seen, last[t]) ? x : 0.f;
-          }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[i] += __shfl_xor_sync(0xffffffffu, w[i], 1);
-          w[i] += __shfl_xor_sync(0xffffffffu, w[i], 2);
-        }
-        // column i of the quad writes position 8 i + row8
-        const float x = col == 0 ? w[0] : col == 1 ? w[1] : col == 2 ? w[2] : w[3];
-        const int at = p + 8 * col + row8;
-        if (at < end) mass[at - p0] += x;
-      };
+    for (int i = 0; i < 4; ++i) {
+      w[i] += __shfl_xor_sync(0xffffffffu, w[i], 1);
+      w[i] += __shfl_xor_sync(0xffffffffu, w[i], 2);
+    }
+    const float x = col == 0 ? w[0] : col == 1 ? w[1] : col == 2 ? w[2] : w[3];
+    const int at = p + 8 * col + row8;
+    if (at < end) mass_out[at] = x + before;
+  };
 
-      // ------------------------------- INT2 rows --------------------------------------
-      auto take = [&](const Batch& now, int p) {
+  const int64_t first = (int64_t(blockIdx.x) * kWarps + warp) * a.piece;
+  Batch x0;
+  if (kAhead && first < T) load(x0, max(int(first), g.S), min(min(T, int(first) + a.piece), window));
+  pdl_wait();  // the fragments; every block, also one without positions
+  Rows held;
+  uint2 frag[kHold ? NB : 1][kHold ? KS : 1];
+  if (ONE && first < T && tiles) {
+    rows_of(held, 0);
+    if (kHold) {
+#pragma unroll
+      for (int t = 0; t < NB; ++t)
+#pragma unroll
+        for (int k = 0; k < KS; ++k) frag[kHold ? t : 0][kHold ? k : 0] = f.f16[(int64_t(min(t, tiles - 1)) * KS + k) * 32 + lane];
+    }
+  }
+
+  for (int64_t c0 = first; c0 < T; c0 += int64_t(gridDim.x) * kWarps * a.piece) {
+    const int p0 = int(c0), p1 = min(T, p0 + a.piece);
+    const int i0 = max(p0, g.S), i1 = min(p1, window);  // INT2 positions
+    if (kAhead && c0 != first) load(x0, i0, i1);
+#pragma unroll 1
+    for (int p = i0; p < i1; p += kBatch) {
+      Batch now;
+      if (kAhead) {
+        now = x0;
+        if (p + kBatch < i1) load(x0, p + kBatch, i1);
+      } else {
+        load(now, p, i1);
+      }
+      float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int t0 = 0; t0 < (ONE ? min(tiles, 1) : tiles); t0 += NB) {
+        if (!ONE) rows_of(held, t0);
         float s[NB][4];
 #pragma unroll
         for (int t = 0; t < NB; ++t)
@@ -235,17 +292,20 @@ __global__ void __launch_bounds__(kThreads, (resident<D, NB>())) attn_mass_kerne
               uint32_t r[4][8];
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
-                const uint32_t w = i ? now.words[j][x].y : now.words[j][x].x;
-                if (level) codes_of<0x02000200u>(w, r[x]);
-                else codes_of<0x03000300u>(w, r[x]);
+                uint32_t word = i ? now.words[j][x].y : now.words[j][x].x;
+                // unpacked again for every block of rows: all of a batch's codes do not fit the registers
+                if (!ONE) asm volatile("" : "+r"(word));
+                if (level) codes_of<2>(word, r[x]);
+                else codes_of<3>(word, r[x]);
               }
 #pragma unroll
               for (int k = 0; k < 4; ++k)
 #pragma unroll
                 for (int t = 0; t < NB; ++t) {
-                  const uint2 f = f16[(t * KS + 8 * j + 4 * i + k) * 32 + lane];
-                  mma_f16(level ? high[t][0] : acc[t][0], r[0][2 * k], r[1][2 * k], r[0][2 * k + 1], r[1][2 * k + 1], f.x, f.y);
-                  mma_f16(level ? high[t][1] : acc[t][1], r[2][2 * k], r[3][2 * k], r[2][2 * k + 1], r[3][2 * k + 1], f.x, f.y);
+                  const int ks = 8 * j + 4 * i + k;
+                  const uint2 q = kHold ? frag[kHold ? t : 0][kHold ? ks : 0] : f.f16[(int64_t(min(t0 + t, tiles - 1)) * KS + ks) * 32 + lane];
+                  mma_f16(level ? high[t][0] : acc[t][0], r[0][2 * k], r[1][2 * k], r[0][2 * k + 1], r[1][2 * k + 1], q.x, q.y);
+                  mma_f16(level ? high[t][1] : acc[t][1], r[2][2 * k], r[3][2 * k], r[2][2 * k + 1], r[3][2 * k + 1], q.x, q.y);
                 }
             }
           }
@@ -256,123 +316,108 @@ __global__ void __launch_bounds__(kThreads, (resident<D, NB>())) attn_mass_kerne
             for (int t = 0; t < NB; ++t) {
               float dot = acc[t][x >> 1][2 * (x & 1)] + acc[t][x >> 1][2 * (x & 1) + 1];
               if (LM) dot = fmaf(kLmRho, dot, kLmHi * (high[t][x >> 1][2 * (x & 1)] + high[t][x >> 1][2 * (x & 1) + 1]));
-              s[t][x] = fmaf(z.x * fac[t], dot, fmaf(z.y, sums[t][j], s[t][x]));
+              s[t][x] = fmaf(z.x * held.fac[t], dot, fmaf(z.y, held.sum[t][j], s[t][x]));
             }
           }
         }
-        weigh(s, p, i1);
-      };
-#pragma unroll 1
-      while (p < i1) {
-        if (kAhead) {
-          take(x0, p);
-          load(x0, p + 2 * kStep);
-          p += kStep;
-          if (p >= i1) break;
-          take(x1, p);
-          load(x1, p + 2 * kStep);
-        } else {
-          x1 = x0;
-          load(x0, p + kStep);
-          take(x1, p);
-        }
-        p += kStep;
+        weigh(held, s, p, w);
       }
-
-      // ------------------------------- BF16 rows --------------------------------------
-      if (wide) {
-        auto region = [&](int from, int to, bool is_ring) {
-          for (int q = from + kBatch * warp; q < to; q += kBatch * kWarps) {
-            const uint4* src[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = min(q + 8 * i + row8, to - 1);
-              src[i] = reinterpret_cast<const uint4*>(is_ring ? ring + int64_t(at % g.W) * (2 * D) : sink + int64_t(at) * (2 * D)) + col;
-            }
-            float acc[NB][2][2][4];
-#pragma unroll
-            for (int t = 0; t < NB; ++t)
-#pragma unroll
-              for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[t][0][m][i] = 0.f, acc[t][1][m][i] = 0.f;
-#pragma unroll 2
-            for (int m = 0; m < D / 32; ++m) {
-              uint4 x[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) x[i] = __ldg(src[i] + 4 * m);
-#pragma unroll
-              for (int t = 0; t < NB; ++t)
-#pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                  const uint2 f = fbf[((2 * t + part) * KS + 2 * m) * 32 + lane], f1 = fbf[((2 * t + part) * KS + 2 * m + 1) * 32 + lane];
-                  mma_bf16(acc[t][part][0], x[0].x, x[1].x, x[0].y, x[1].y, f.x, f.y);
-                  mma_bf16(acc[t][part][0], x[0].z, x[1].z, x[0].w, x[1].w, f1.x, f1.y);
-                  mma_bf16(acc[t][part][1], x[2].x, x[3].x, x[2].y, x[3].y, f.x, f.y);
-                  mma_bf16(acc[t][part][1], x[2].z, x[3].z, x[2].w, x[3].w, f1.x, f1.y);
-                }
-            }
-            float s[NB][4];
-#pragma unroll
-            for (int t = 0; t < NB; ++t)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                s[t][i] = (acc[t][0][i >> 1][2 * (i & 1)] + acc[t][0][i >> 1][2 * (i & 1) + 1]) + acc[t][1][i >> 1][2 * (i & 1)];
-            weigh(s, q, to);
-          }
-        };
-        region(p0, min(p1, min(g.S, T)), false);
-        region(max(p0, window), p1, true);
-      }
+      write(w, p, i1, now.mass);
     }
-    __syncthreads();
-    const int64_t to = int64_t(unit) * g.cap + p0;
-    for (int i = threadIdx.x; i < p1 - p0; i += kThreads) a.mass_out[to + i] = mass[i] + (a.mass_in ? a.mass_in[to + i] : 0.f);
-    __syncthreads();
+
+    // --------------------------------- BF16 rows ----------------------------------------
+    auto region = [&](int from, int to, bool is_ring) {
+#pragma unroll 1
+      for (int p = from; p < to; p += kBatch) {
+        const uint4* src[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = min(p + 8 * i + row8, to - 1);
+          src[i] = reinterpret_cast<const uint4*>(is_ring ? ring + int64_t(at % g.W) * (2 * D) : sink + int64_t(at) * (2 * D)) + col;
+        }
+        const float before = mass_in && p + 8 * col + row8 < to ? mass_in[p + 8 * col + row8] : 0.f;
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int t0 = 0; t0 < tiles; t0 += NB) {
+          if (!ONE) rows_of(held, t0);
+          float acc[NB][2][2][4];
+#pragma unroll
+          for (int t = 0; t < NB; ++t)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[t][0][m][i] = 0.f, acc[t][1][m][i] = 0.f;
+#pragma unroll 2
+          for (int m = 0; m < D / 32; ++m) {
+            uint4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = __ldg(src[i] + 4 * m);
+#pragma unroll
+            for (int t = 0; t < NB; ++t)
+#pragma unroll
+              for (int part = 0; part < 2; ++part) {
+                const uint2* q = f.fbf + ((2 * int64_t(min(t0 + t, tiles - 1)) + part) * KS + 2 * m) * 32 + lane;
+                const uint2 u = q[0], v = q[32];
+                mma_bf16(acc[t][part][0], x[0].x, x[1].x, x[0].y, x[1].y, u.x, u.y);
+                mma_bf16(acc[t][part][0], x[0].z, x[1].z, x[0].w, x[1].w, v.x, v.y);
+                mma_bf16(acc[t][part][1], x[2].x, x[3].x, x[2].y, x[3].y, u.x, u.y);
+                mma_bf16(acc[t][part][1], x[2].z, x[3].z, x[2].w, x[3].w, v.x, v.y);
+              }
+          }
+          float s[NB][4];
+#pragma unroll
+          for (int t = 0; t < NB; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              s[t][i] = (acc[t][0][i >> 1][2 * (i & 1)] + acc[t][0][i >> 1][2 * (i & 1) + 1]) + acc[t][1][i >> 1][2 * (i & 1)];
+          weigh(held, s, p, w);
+        }
+        write(w, p, to, before);
+      }
+    };
+    region(p0, min(p1, min(g.S, T)), false);
+    region(max(p0, window), p1, true);
   }
 }
 
-template <int D, int NB, bool LM>
-int launch_l(const MassArgs& a, dim3 grid, cudaStream_t stream) {
-  constexpr int smem = Mass<D, NB>::kBytes;
-  static bool done[64] = {false};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return OSCAR_ERR_LAUNCH;
-  if (!done[dev]) {
-    if (cudaFuncSetAttribute(attn_mass_kernel<D, NB, LM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-      return OSCAR_ERR_LAUNCH;
-    done[dev] = true;
+template <int D, int NB, bool LM, bool ONE>
+int launch_one(const MassArgs& a, cudaStream_t stream) {
+  const int64_t rows = int64_t(a.g.B) * a.g.Hkv * a.tiles * 4;
+  if (rows > 0) {
+    const int rc = row_launch(true, mass_frags_kernel<D>, dim3(unsigned((rows + kWarps - 1) / kWarps)), kThreads, 0, stream, a);
+    if (rc != OSCAR_OK) return rc;
   }
-  return row_launch(a.n > 0, attn_mass_kernel<D, NB, LM>, grid, kThreads, smem, stream, a);
+  const int64_t block = int64_t(kWarps) * a.piece;
+  const dim3 grid(unsigned((a.top + block - 1) / block), unsigned(a.g.B * a.g.Hkv));
+  return row_launch(rows > 0, attn_mass_kernel<D, NB, LM, ONE>, grid, kThreads, 0, stream, a);
 }
-template <int D, int NB>
-int launch_n(const MassArgs& a, dim3 grid, cudaStream_t stream) {
-  return a.g.lm ? launch_l<D, NB, true>(a, grid, stream) : launch_l<D, NB, false>(a, grid, stream);
+template <int D, int NB, bool ONE>
+int launch_n(const MassArgs& a, cudaStream_t stream) {
+  return a.g.lm ? launch_one<D, NB, true, ONE>(a, stream) : launch_one<D, NB, false, ONE>(a, stream);
 }
 template <int D>
-int launch_d(const MassArgs& a, dim3 grid, cudaStream_t stream) {
-  const int64_t rows = int64_t(a.n) * a.g.G;
-  return rows <= 4 ? launch_n<D, 1>(a, grid, stream) : rows <= 8 ? launch_n<D, 2>(a, grid, stream) : launch_n<D, 4>(a, grid, stream);
+int launch_d(const MassArgs& a, cudaStream_t stream) {
+  return a.tiles <= 1 ? launch_n<D, 1, true>(a, stream) : a.tiles == 2 ? launch_n<D, 2, true>(a, stream)
+                                                                       : launch_n<D, 4, false>(a, stream);
 }
 
 }  // namespace
 
+uint64_t mass_frag_bytes(const Geom& g, int n) {
+  const uint64_t rows = uint64_t(g.B) * g.Hkv * ((int64_t(n) * g.G + 3) / 4) * 4;
+  return rows * (uint64_t(g.D) * 12 + 16 + g.Dg * 4);
+}
+
 int launch_attn_mass(const MassArgs& args, cudaStream_t stream) {
   MassArgs a = args;
-  const int64_t units = int64_t(a.g.B) * a.g.Hkv;
+  a.tiles = int((int64_t(a.n) * a.g.G + 3) / 4);
   int dev = 0, sms = 0;
-  if (units > 65535 || cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return OSCAR_ERR_LAUNCH;
-  // positions of a block: enough blocks for every SM to have eight, no more than its masses' shared memory holds
-  const int64_t even = (int64_t(a.top) * units + 8 * sms - 1) / (8 * sms);
-  a.chunk = int(std::min<int64_t>(kMostChunk, std::max<int64_t>(kBatch * kWarps, (even + 127) / 128 * 128)));
-  const dim3 grid(unsigned((a.top + a.chunk - 1) / a.chunk), unsigned(units));
-  switch (a.g.D) {
-    case 128: return launch_d<128>(a, grid, stream);
-    case 256: return launch_d<256>(a, grid, stream);
-    default: return launch_d<512>(a, grid, stream);
-  }
+  // positions of a warp: few enough for every SM to have 32 warps in turn
+  const int64_t even = int64_t(a.top) * a.g.B * a.g.Hkv / (32 * sms);
+  a.piece = int(std::min<int64_t>(kMostPiece, std::max<int64_t>(kBatch, even / kBatch * kBatch)));
+  return a.g.D == 128 ? launch_d<128>(a, stream) : a.g.D == 256 ? launch_d<256>(a, stream) : launch_d<512>(a, stream);
 }
 
 }  // namespace oscar

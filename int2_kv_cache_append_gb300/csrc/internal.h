@@ -253,9 +253,11 @@ struct MassArgs {
   const float* mass_in;     // [B][Hkv][cap] or NULL (= 0)
   float* mass_out;
   int32_t* status;
+  uint8_t* frags;           // workspace: the query rows as matrix fragments, mass_frag_bytes
   int n, top;               // top: length for which the grid is laid out
-  int chunk;                // positions of a block (set by the launcher)
+  int tiles, piece;         // of four query rows; positions of a warp (set by the launcher)
 };
+uint64_t mass_frag_bytes(const Geom& g, int n);
 int launch_attn_mass(const MassArgs& a, cudaStream_t stream);
 
 // Rows of largest mass and the windows into another cache (kv_evict.cu).

@@ -653,7 +653,7 @@ int attn_mass_workspace_query(const oscar_kv_config* cfg, int32_t n_new, uint64_
   if (n_new > cfg->capacity) return OSCAR_ERR_CAPACITY;
   const Geom g = make_geom(cfg);
   if (!rows_supported(g, n_new) || int64_t(g.B) * g.Hkv > kMostUnits) return OSCAR_ERR_UNSUPPORTED;
-  *bytes = oscar::align256(uint64_t(g.B) * n_new * g.Hq * g.D * 4);
+  *bytes = oscar::align256(uint64_t(g.B) * n_new * g.Hq * g.D * 4) + oscar::align256(oscar::mass_frag_bytes(g, n_new));
   return OSCAR_OK;
 }
 
@@ -675,7 +675,8 @@ int attn_mass(const oscar_kv_config* cfg, const void* cache, int32_t layer, cons
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   oscar::QrotRowsArgs r{};
   r.q = q;
-  r.qrot = static_cast<float*>(workspace);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  r.qrot = take<float>(&ws, uint64_t(g.B) * n_new * g.Hq * g.D * 4);
   r.R_K = R_K;
   r.status = dev_status;
   r.q_lens = q_lens;
@@ -696,6 +697,7 @@ int attn_mass(const oscar_kv_config* cfg, const void* cache, int32_t layer, cons
   a.mass_in = mass_in;
   a.mass_out = mass_out;
   a.status = dev_status;
+  a.frags = ws;
   a.n = n_new;
   a.top = seq_len_hint > 0 ? seq_len_hint : g.cap;
   const int rc = n_new ? oscar::launch_qrot_rows(r, st) : OSCAR_OK;
