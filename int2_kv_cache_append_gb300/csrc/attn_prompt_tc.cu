@@ -15,6 +15,10 @@
 // execute in the order of issue, so S_w of the next positions may follow P_w V
 // over the same columns, and a finished S_w says that O_w is complete.
 //
+// A block stays for many items: the loads, which also find the items, run ahead into
+// the next one's tiles, and its first products run under the last one's softmax and
+// output.
+//
 // Softmax: a thread has a row; its reference M follows the row's maximum only when
 // that has grown by 2^8, and then the warp rescales its rows of O.  P is rounded to
 // bf16, V's type; row sums are taken before the rounding, in float32.
@@ -40,12 +44,35 @@ constexpr int kChecked = 2;            // position tiles with tokens that some r
 constexpr float kNone = -1e30f;
 constexpr float kTop = 8.f;            // log2 of the largest P
 constexpr int oQ = 0, oKV = 2 * kTile, oOdd = oKV + kStages * kTile, oBar = oOdd + 3 * D * 4;
-constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 * kChecked + 1;
+constexpr int kItems = 3;              // items found ahead
+constexpr int kBars = 2 * kStages + 5 * 2 + 2 * kChecked + 1 + 2 * kItems + 1;
 constexpr int kBytes = oBar + kBars * 8 + 32 + 1024;  // + alignment slack
 static_assert(oBar % 8 == 0 && kBytes <= 232448 - 64, "shared memory");
 constexpr uint32_t cS = 0, cO = 256;   // TMEM columns, 128 per tile
 constexpr int kSoftRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSoftRegs + kOtherRegs <= 3 * 168, "registers of a launch with 168 a thread");
+
+// Barriers, by their order in shared memory.
+struct Bars {
+  uint32_t full, empty, q_full, q_empty, s_full, p_full, o_full, values, checked, odd_free, item_full, item_empty, drained;
+  __device__ __forceinline__ explicit Bars(uint32_t at) {
+    full = at, empty = full + 8 * kStages, q_full = empty + 8 * kStages, q_empty = q_full + 16, s_full = q_empty + 16,
+    p_full = s_full + 16, o_full = p_full + 16, values = o_full + 16, checked = values + 8 * kChecked,
+    odd_free = checked + 8 * kChecked, item_full = odd_free + 8, item_empty = item_full + 8 * kItems,
+    drained = item_empty + 8 * kItems;
+  }
+};
+
+// An item as all roles see it: its sequence and head, first token, tiles of positions of both query tiles.
+struct Work {
+  int start, len, h, t0, nA, nB, nt, check0;
+  __device__ __forceinline__ Work(const PromptItem& it, int head, int tt) : start(it.start), len(it.len), h(head), t0(it.tile * 2 * tt) {
+    auto tiles = [&](int first) { return first < len ? (min(first + tt, len) + kTok - 1) / kTok : 0; };
+    nA = tiles(t0), nB = tiles(t0 + tt), nt = max(nA, nB);
+    check0 = (t0 + 1) / kTok;  // the first tile with a token behind t0
+  }
+  __device__ __forceinline__ int checks() const { return max(0, min(kChecked, nt - check0)); }
+};
 
 __global__ void __launch_bounds__(kThreads, 1)
     attn_prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -54,40 +81,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
-  __shared__ PromptItem item;
+  __shared__ PromptItem items[kItems];
+  __shared__ int heads[kItems];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tt = N / a.G;  // tokens of a tile
-
-  const uint32_t bar = base + oBar;
-  const uint32_t full = bar, empty = full + 8 * kStages, q_full = empty + 8 * kStages, s_full = q_full + 16,
-                 p_full = s_full + 16, o_full = p_full + 16, values = o_full + 16, checked = values + 8 * kChecked,
-                 drained = checked + 8 * kChecked;
+  const Bars bar(base + oBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + oBar + kBars * 8);
   int* odd = reinterpret_cast<int*>(sm + oOdd);
   int* any_odd = reinterpret_cast<int*>(tmem_slot + 1);
-  if (warp == 0) {
-    if (blockIdx.x == 0) prompt_check(a);
-    const PromptItem it = prompt_item(a, blockIdx.x / a.Hkv, 1, 2 * tt);
-    if (lane == 0) item = it;
-  }
   if (threadIdx.x == kLoad * 32) {
-    for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(bar.full + 8 * i, 1), mbar_init(bar.empty + 8 * i, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + 8 * i, 1);
-      mbar_init(s_full + 8 * i, 1 + (i == 0 && a.wait_poison > 0));
-      mbar_init(p_full + 8 * i, 4);
-      mbar_init(o_full + 8 * i, 1);
+      mbar_init(bar.q_full + 8 * i, 1), mbar_init(bar.q_empty + 8 * i, 1);
+      mbar_init(bar.s_full + 8 * i, 1 + (i == 0 && a.wait_poison > 0));
+      mbar_init(bar.p_full + 8 * i, 4);
+      mbar_init(bar.o_full + 8 * i, 1);
     }
-    for (int i = 0; i < kChecked; ++i) mbar_init(values + 8 * i, 1), mbar_init(checked + 8 * i, 2);
-    mbar_init(drained, 1);
+    for (int i = 0; i < kChecked; ++i) mbar_init(bar.values + 8 * i, 1), mbar_init(bar.checked + 8 * i, 2);
+    mbar_init(bar.odd_free, kSoftWarps);
+    for (int i = 0; i < kItems; ++i) mbar_init(bar.item_full + 8 * i, 1), mbar_init(bar.item_empty + 8 * i, kSoftWarps + 3);
+    mbar_init(bar.drained, 1);
     mbar_fence_init();
   }
   if (threadIdx.x == kCheck * 32) *any_odd = 0;
   if (warp >= kCheck)
     for (int i = threadIdx.x - kCheck * 32; i < 3 * D; i += 64) odd[i] = 0x7fffffff;
-  __syncthreads();
-  const PromptItem it = item;
-  if (it.b < 0) return;
   if (warp == kMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -96,174 +114,256 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int h = blockIdx.x % a.Hkv, t0 = it.tile * 2 * tt;
-  auto tiles_of = [&](int w) {  // position tiles of query tile w
-    const int first = t0 + w * tt;
-    return first < it.len ? (min(first + tt, it.len) + kTok - 1) / kTok : 0;
-  };
-  const int nA = tiles_of(0), nB = tiles_of(1), nt = max(nA, nB);
-  const int check0 = (t0 + 1) / kTok;  // the first tile with a token behind t0
   auto fail = [&]() { status_or(a.status, OSCAR_DEV_TIMEOUT); };
+  auto wait = [&](uint32_t br, uint32_t parity) { return wait_warp(br, parity, a.wait_turns); };
+  // The next item, by every warp but the loads': false at the end (or where a wait ran out: ok).
+  auto next = [&](Ring<kItems>& at, bool& ok, PromptItem& it, int& h) {
+    ok = wait(bar.item_full + 8 * at.at, at.phase);
+    if (!ok) return false;
+    it = items[at.at], h = heads[at.at];
+    __syncwarp();
+    mbar_arrive_if(bar.item_empty + 8 * at.at, lane == 0);
+    at.next();
+    return it.b >= 0;
+  };
 
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    const int w = warp >> 2, row = threadIdx.x & 127, n = w ? nB : nA;
-    const int first = t0 + w * tt, tok = first + row / a.G;
-    const bool live = row < tt * a.G && tok < it.len;
-    const int lim = live ? tok : -1, least = first + (row & ~31) / a.G;  // the warp's first token
+    const int w = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
     const uint32_t S = tmem + lanes + cS + 128 * w, O = tmem + lanes + cO + 128 * w;
     const uint64_t scale2 = splat_x2(a.qscale);
-    float M = kNone;
-    uint64_t l2 = 0;
+    uint32_t s_phase = 0, o_phase = 0, c_phase = 0;
+    Ring<kItems> at_item;
     bool ok = true;
+    PromptItem it;
+    int h;
 #pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-      ok = wait_warp(s_full + 8 * w, j & 1, a.wait_turns);
+    while (next(at_item, ok, it, h)) {
+      const Work x(it, h, tt);
+      const int n = w ? x.nB : x.nA, first = x.t0 + w * tt, tok = first + row / a.G;
+      const bool live = row < tt * a.G && tok < x.len;
+      const int lim = live ? tok : -1, least = first + (row & ~31) / a.G;  // the warp's first token
+      float M = kNone;
+      uint64_t l2 = 0;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        ok = wait(bar.s_full + 8 * w, s_phase);
+        if (!ok) break;
+        s_phase ^= 1;
+        fence_after();
+        uint32_t r[64], u[64];
+        tmem_ld64(S, r);
+        tmem_ld64(S + 64, u);
+        if (j * kTok + kTok - 1 > least) {
+          const int see = lim - j * kTok;
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            r[c] = c <= see ? r[c] : 0xFF800000u;
+            u[c] = c + 64 <= see ? u[c] : 0xFF800000u;
+          }
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          top[0] = max3(top[0], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+          top[1] = max3(top[1], __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
+          top[2] = max3(top[2], __uint_as_float(u[c]), __uint_as_float(u[c + 1]));
+          top[3] = max3(top[3], __uint_as_float(u[c + 2]), __uint_as_float(u[c + 3]));
+        }
+        const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.qscale;
+        const bool grow = t > M + kTop;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? exp2f(M - t) : 1.f;
+          if (grow) M = t;
+          l2 = mul2(l2, splat_x2(f));
+          if (j > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(O + c, o);
+              tmem_wait16(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16(O + c, o);
+            }
+          }
+        }
+        const uint64_t m2 = splat_x2(-M);
+        uint64_t sum = 0, sum1 = 0;
+        auto half = [&](const uint32_t (&x)[64], uint32_t to) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float y, z;
+              unpack2(fma2(pack2(__uint_as_float(x[c + 2 * i]), __uint_as_float(x[c + 2 * i + 1])), scale2, m2), y, z);
+              y = ex2z(y);
+              z = ex2z(z);
+              p[i] = bf162_of(y, z);
+              if (i & 1) sum = add2(sum, pack2(y, z));
+              else sum1 = add2(sum1, pack2(y, z));
+            }
+            tmem_st16(to + c / 2, p);
+          }
+        };
+        half(r, S);
+        half(u, S + 32);
+        l2 = add2(l2, add2(sum, sum1));
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        fence_before();
+        __syncwarp();
+        mbar_arrive_if(bar.p_full + 8 * w, lane == 0);
+      }
+      if (ok && n > 0) {
+        ok = wait(bar.o_full + 8 * w, o_phase);
+        o_phase ^= 1;
+      }
+      for (int i = 0; i < kChecked; ++i) ok = ok && wait(bar.checked + 8 * i, c_phase);
+      c_phase ^= 1;
       if (!ok) break;
-      fence_after();
-      uint32_t r[64], u[64];
-      tmem_ld64(S, r);
-      tmem_ld64(S + 64, u);
-      if (j * kTok + kTok - 1 > least) {
-        const int see = lim - j * kTok;
-#pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          r[c] = c <= see ? r[c] : 0xFF800000u;
-          u[c] = c + 64 <= see ? u[c] : 0xFF800000u;
-        }
-      }
-      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 64; c += 4) {
-        top[0] = max3(top[0], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
-        top[1] = max3(top[1], __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
-        top[2] = max3(top[2], __uint_as_float(u[c]), __uint_as_float(u[c + 1]));
-        top[3] = max3(top[3], __uint_as_float(u[c + 2]), __uint_as_float(u[c + 3]));
-      }
-      const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.qscale;
-      const bool grow = t > M + kTop;
-      if (__any_sync(0xffffffffu, grow)) {
-        const float f = grow ? exp2f(M - t) : 1.f;
-        if (grow) M = t;
-        l2 = mul2(l2, splat_x2(f));
-        if (j > 0) {
+      if (n > 0) {
+        fence_after();
+        float l, l1;
+        unpack2(l2, l, l1);
+        l += l1;
+        const float inv = 1.0f / l;
+        const bool strange = *any_odd != 0;
+        const int64_t at = int64_t(x.start + tok) * a.Hq + x.h * a.G + row % a.G;
+        if (live && a.lse) a.lse[at] = (M + log2f(l)) * 0.6931471805599453f;
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * D);
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(O + c, o);
-            tmem_wait16(o);
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[2][16];
+          tmem_ld16(O + c, o[0]);
+          tmem_ld16(O + c + 16, o[1]);
+          tmem_wait16(o[0]);
+          tmem_wait16(o[1]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st16(O + c, o);
+          for (int e = 0; e < 2; ++e) {
+            float y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(o[e][i]) * inv;
+            if (strange) {
+              const int* at_c = odd + c + 16 * e;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                if (at_c[i] <= tok) y[i] = __int_as_float(0x7FC00000);
+                if (at_c[D + i] <= tok) y[i] += INFINITY;
+                if (at_c[2 * D + i] <= tok) y[i] -= INFINITY;
+              }
+            }
+            if (live) {
+              uint32_t q[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) q[i] = bf162_of(y[2 * i], y[2 * i + 1]);
+              dst[c / 8 + 2 * e] = make_uint4(q[0], q[1], q[2], q[3]);
+              dst[c / 8 + 2 * e + 1] = make_uint4(q[4], q[5], q[6], q[7]);
+            }
           }
         }
+        fence_before();  // O has been read when the next item's first P arrives
       }
-      const uint64_t m2 = splat_x2(-M);
-      uint64_t sum = 0, sum1 = 0;
-      auto half = [&](const uint32_t (&x)[64], uint32_t to) {
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float y, z;
-            unpack2(fma2(pack2(__uint_as_float(x[c + 2 * i]), __uint_as_float(x[c + 2 * i + 1])), scale2, m2), y, z);
-            y = ex2z(y);
-            z = ex2z(z);
-            p[i] = bf162_of(y, z);
-            if (i & 1) sum = add2(sum, pack2(y, z));
-            else sum1 = add2(sum1, pack2(y, z));
-          }
-          tmem_st16(to + c / 2, p);
-        }
-      };
-      half(r, S);
-      half(u, S + 32);
-      l2 = add2(l2, add2(sum, sum1));
-      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-      fence_before();
       __syncwarp();
-      mbar_arrive_if(p_full + 8 * w, lane == 0);
-    }
-    if (n > 0 && ok) ok = wait_warp(o_full + 8 * w, 0, a.wait_turns);
-    for (int i = 0; i < min(kChecked, nt - check0) && ok; ++i) ok = wait_warp(checked + 8 * i, 0, a.wait_turns);
-    if (ok && n > 0) {
-      fence_after();
-      float l, l1;
-      unpack2(l2, l, l1);
-      l += l1;
-      const float inv = 1.0f / l;
-      const bool strange = *any_odd != 0;
-      const int64_t at = int64_t(it.start + tok) * a.Hq + h * a.G + row % a.G;
-      if (live && a.lse) a.lse[at] = (M + log2f(l)) * 0.6931471805599453f;
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * D);
-#pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
-        uint32_t o[16];
-        tmem_ld16(O + c, o);
-        tmem_wait16(o);
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(o[i]) * inv;
-        if (strange) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (odd[c + i] <= tok) x[i] = __int_as_float(0x7FC00000);
-            if (odd[D + c + i] <= tok) x[i] += INFINITY;
-            if (odd[2 * D + c + i] <= tok) x[i] -= INFINITY;
-          }
-        }
-        if (live) {
-          uint32_t q[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) q[i] = bf162_of(x[2 * i], x[2 * i + 1]);
-          dst[c / 8] = make_uint4(q[0], q[1], q[2], q[3]);
-          dst[c / 8 + 1] = make_uint4(q[4], q[5], q[6], q[7]);
-        }
-      }
+      mbar_arrive_if(bar.odd_free, lane == 0);
     }
     if (!ok && lane == 0) fail();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoad) {
       // ------------------------------- loads -----------------------------------
-      if (lane == 0) {
-        // the V tiles that are looked through have a barrier of their own, which that pair waits for: it would be behind in
-        // the phases of `full`, which here completes at once
-        auto tile = [&](int s, const CUtensorMap* map, int token) {
-          const uint32_t to = base + oKV + (s % kStages) * kTile;
-          uint32_t br = full + 8 * (s % kStages);
-          if ((s & 1) && s / 2 >= check0) {
-            mbar_arrive(br);
-            br = values + 8 * (s / 2 - check0);
-          }
-          mbar_arrive_expect_tx(br, kTile);
-          tma_load_2d(to, map, h * D, it.start + token, br);
-          tma_load_2d(to + kTile / 2, map, h * D + 64, it.start + token, br);
-        };
-        auto queries = [&](int w) {
-          mbar_arrive_expect_tx(q_full + 8 * w, 2 * tt * a.G * 128);
-          for (int c = 0; c < 2; ++c)
-            tma_load_3d(base + oQ + w * kTile + c * (kTile / 2), &mq, 64 * c, h * a.G, it.start + t0 + w * tt, q_full + 8 * w);
-        };
-        queries(0);
-        bool ok = true;
-        int s = 0;
-        for (; s < 2 * nt && ok; ++s) {
-          if (s >= kStages) ok = mbar_wait(empty + 8 * (s % kStages), (s / kStages - 1) & 1, a.wait_turns * 1000ull);
-          if (!ok) break;
-          tile(s, s & 1 ? &mv : &mk, (s / 2) * kTok);
-          if (s == 0 && nB > 0) queries(1);
+      // It also finds the items, in the order of prompt_item, dealt to the blocks forth and back, so that those with the
+      // longest of one round have the shortest of the next.
+      const int64_t total = prompt_items(a, 1, 2 * tt) * a.Hkv;
+      if (blockIdx.x == 0) prompt_check(a);
+      const uint64_t limit = a.wait_turns * 1000ull;
+      Ring<kItems> at_item;
+      Ring<kStages> at;
+      uint32_t q_phase = 0, q_used = 0, v_phase = 0, v_used = 0, c_phase = 0;  // bits of the barriers of a kind
+      int64_t round = 0;
+      int published = 0, issued = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (;;) {
+        PromptItem it{-1, 0, 0, 0};
+        int h = 0;
+        while (round * gridDim.x < total) {
+          const int64_t i = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+          ++round;
+          if (i >= total) continue;
+          it = prompt_item(a, int(i / a.Hkv), 1, 2 * tt);
+          h = int(i % a.Hkv);
+          break;
         }
+        if (published >= kItems) ok = wait(bar.item_empty + 8 * at_item.at, at_item.phase ^ 1);
+        if (!ok) break;
+        if (lane == 0) {
+          items[at_item.at] = it, heads[at_item.at] = h;
+          mbar_arrive(bar.item_full + 8 * at_item.at);
+        }
+        at_item.next();
+        if (it.b < 0) break;
+        if (lane == 0) {
+          const Work x(it, h, tt);
+          auto room = [&]() {
+            if (ok && issued >= kStages) ok = mbar_wait(bar.empty + 8 * at.at, at.phase ^ 1, limit);
+            return ok;
+          };
+          auto tile = [&](const CUtensorMap* map, int token, uint32_t br) {
+            const uint32_t to = base + oKV + at.at * kTile;
+            mbar_arrive_expect_tx(br, kTile);
+            tma_load_2d(to, map, x.h * D, x.start + token, br);
+            tma_load_2d(to + kTile / 2, map, x.h * D + 64, x.start + token, br);
+            at.next(), ++issued;
+          };
+          auto queries = [&](int w) {  // once the products of the item before that has the tile have read it
+            if (ok && (q_used >> w & 1)) ok = mbar_wait(bar.q_empty + 8 * w, (q_phase >> w & 1) ^ 1, limit);
+            if (!ok) return;
+            mbar_arrive_expect_tx(bar.q_full + 8 * w, 2 * tt * a.G * 128);
+            for (int c = 0; c < 2; ++c)
+              tma_load_3d(base + oQ + w * kTile + c * (kTile / 2), &mq, 64 * c, x.h * a.G, x.start + x.t0 + w * tt, bar.q_full + 8 * w);
+            q_used |= 1u << w, q_phase ^= 1u << w;
+          };
+          bool told = published == 0;
+          auto before = [&]() {  // the item before has been looked through
+            for (int i = 0; i < kChecked && !told && ok; ++i) ok = mbar_wait(bar.checked + 8 * i, c_phase, limit);
+            if (!told) c_phase ^= 1;
+            told = true;
+          };
+          for (int j = 0; j < x.nt && ok; ++j) {
+            if (room()) tile(&mk, j * kTok, bar.full + 8 * at.at);
+            if (j == 0) {
+              queries(0);
+              if (x.nB > 0) queries(1);
+            }
+            // V tiles that are looked through have a barrier of their own, which that pair of warps waits for: it would be
+            // behind in the phases of `full`, which here completes at once
+            if (j >= x.check0) before();
+            if (!room()) break;
+            uint32_t br = bar.full + 8 * at.at;
+            if (j >= x.check0) {
+              mbar_arrive(br);
+              const int i = j - x.check0;
+              br = bar.values + 8 * i;
+              v_used |= 1u << i, v_phase ^= 1u << i;
+            }
+            tile(&mv, j * kTok, br);
+          }
+          if (ok) before();
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ++published;
+        if (!ok) break;
+      }
+      if (lane == 0) {
         if (!ok) fail();
         // what was issued lands before the block ends, also where a wait ran out
-        mbar_wait(q_full, 0);
-        if (nB > 0) mbar_wait(q_full + 8, 0);
-        for (int i = max(0, s - kStages); i < s; ++i) {
-          if ((i & 1) && i / 2 >= check0) mbar_wait(values + 8 * (i / 2 - check0), 0);
-          else mbar_wait(full + 8 * (i % kStages), (i / kStages) & 1);
+        for (int i = 0; i < 2; ++i) {
+          if (q_used >> i & 1) mbar_wait(bar.q_full + 8 * i, (q_phase >> i & 1) ^ 1);
+          if (v_used >> i & 1) mbar_wait(bar.values + 8 * i, (v_phase >> i & 1) ^ 1);
         }
+        for (int i = max(0, issued - kStages); i < issued; ++i) mbar_wait(bar.full + 8 * (i % kStages), (i / kStages) & 1);
       }
     } else if (warp == kMma) {
       // ------------------------------ products ---------------------------------
@@ -271,14 +371,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t id_qk = idesc_of(kTok, false, false) | kBf16, id_pv = idesc_of(D, false, true) | kBf16;
       const uint32_t dQ = desc_of(base + oQ, 16), dK = desc_of(base + oKV, 16), dV = desc_of(base + oKV, kTile / 2);
       Waits waits{a.wait_turns};
-      Ring<kStages> kr, vr;  // stages of the next K and V tile: 0, 2, 4, .. and 1, 3, 5, ..
+      Ring<kStages> kr, vr;  // stages of the next K and V tile, which alternate
       vr.next();
       auto product_qk = [&](int w) {
         const uint32_t k = dK + kr.at * (kTile >> 4), q = dQ + w * (kTile >> 4);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           mma_f16_ss(cS + 128 * w, q + (j >> 2) * (kTile >> 5) + 2 * (j & 3), k + (j >> 2) * (kTile >> 5) + 2 * (j & 3), id_qk, j > 0, leader);
-        mma_commit(s_full + 8 * w, leader);
+        mma_commit(bar.s_full + 8 * w, leader);
       };
       auto product_pv = [&](int w, uint32_t acc) {
         const uint32_t v = dV + vr.at * (kTile >> 4);
@@ -286,63 +386,108 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 8; ++j) mma_f16_ts(cO + 128 * w, cS + 128 * w + 8 * j, v + 128 * j, id_pv, j ? 1 : acc, leader);
       };
       waits.ok &= tmem == 0;  // all of TMEM: column addresses are constants
-      waits.on(q_full, 0);
-      waits.on(full + 8 * kr.at, kr.phase);
-      fence_after();
-      if (waits.ok) product_qk(0);
-      if (nB > 0) {
-        waits.on(q_full + 8, 0);
-        fence_after();
-        if (waits.ok) product_qk(1);
-      }
-      if (waits.ok) mma_commit(empty + 8 * kr.at, leader);
-      kr.next(), kr.next();
+      uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, c_phase = 0;
+      Ring<kItems> at_item;
+      bool ok = true;
+      PromptItem it;
+      int h;
 #pragma unroll 1
-      for (int j = 0; j < nt; ++j) {
-        waits.on(full + 8 * vr.at, vr.phase);
-        if (j >= check0) waits.on(checked + 8 * (j - check0), 0);
-        const bool more = j + 1 < nt;
+      while (__all_sync(0xffffffffu, waits.ok) && next(at_item, ok, it, h)) {
+        const Work x(it, h, tt);
+        const int n[2] = {x.nA, x.nB};
+        waits.on(bar.full + 8 * kr.at, kr.phase);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const int n = w ? nB : nA;
-          if (j < n) {
-            waits.on(p_full + 8 * w, j & 1);
-            fence_after();
-            if (!__all_sync(0xffffffffu, waits.ok)) break;
-            product_pv(w, j > 0);
-            if (j + 1 == n) mma_commit(o_full + 8 * w, leader);
-          }
-          if (w == 1) mma_commit(empty + 8 * vr.at, leader);
-          if (j + 1 < n) {
-            waits.on(full + 8 * kr.at, kr.phase);
+        for (int w = 0; w < 2; ++w)
+          if (n[w] > 0) {
+            waits.on(bar.q_full + 8 * w, q_phase[w]);
+            q_phase[w] ^= 1;
             fence_after();
             if (!__all_sync(0xffffffffu, waits.ok)) break;
             product_qk(w);
+            if (n[w] == 1) mma_commit(bar.q_empty + 8 * w, leader);
           }
-          if (w == 1 && more) mma_commit(empty + 8 * kr.at, leader);
-        }
         if (!__all_sync(0xffffffffu, waits.ok)) break;
+        mma_commit(bar.empty + 8 * kr.at, leader);
         kr.next(), kr.next();
-        vr.next(), vr.next();
+#pragma unroll 1
+        for (int j = 0; j < x.nt; ++j) {
+          waits.on(bar.full + 8 * vr.at, vr.phase);
+          if (j >= x.check0) waits.on(bar.checked + 8 * (j - x.check0), c_phase);
+          const bool more = j + 1 < x.nt;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (j < n[w]) {
+              waits.on(bar.p_full + 8 * w, p_phase[w]);
+              p_phase[w] ^= 1;
+              fence_after();
+              if (!__all_sync(0xffffffffu, waits.ok)) break;
+              product_pv(w, j > 0);
+              if (j + 1 == n[w]) mma_commit(bar.o_full + 8 * w, leader);
+            }
+            if (w == 1) mma_commit(bar.empty + 8 * vr.at, leader);
+            if (j + 1 < n[w]) {
+              waits.on(bar.full + 8 * kr.at, kr.phase);
+              fence_after();
+              if (!__all_sync(0xffffffffu, waits.ok)) break;
+              product_qk(w);
+              if (j + 2 == n[w]) mma_commit(bar.q_empty + 8 * w, leader);
+            }
+          }
+          if (!__all_sync(0xffffffffu, waits.ok)) break;
+          if (more) {
+            mma_commit(bar.empty + 8 * kr.at, leader);
+            kr.next(), kr.next();
+          }
+          vr.next(), vr.next();
+        }
+        for (int i = x.checks(); i < kChecked; ++i) waits.on(bar.checked + 8 * i, c_phase);
+        c_phase ^= 1;
       }
-      if (!__all_sync(0xffffffffu, waits.ok) && lane == 0) fail();
-      mma_commit(drained, leader);  // every product issued is complete before TMEM is freed
-      mbar_wait(drained, 0);
+      if (!__all_sync(0xffffffffu, waits.ok && ok) && lane == 0) fail();
+      mma_commit(bar.drained, leader);  // every product issued is complete before TMEM is freed
+      mbar_wait(bar.drained, 0);
       __syncwarp();
     } else {
       // --------------------------- a look through V -----------------------------
+      const int me = threadIdx.x - kCheck * 32;
+      Ring<kItems> at_item;
+      uint32_t v_phase = 0, free_phase = 1;
+      int first_stage = 0;  // the item's
       bool ok = true;
+      PromptItem it;
+      int h;
 #pragma unroll 1
-      for (int j = check0; j < nt && ok; ++j) {
-        const int s = 2 * j + 1;
-        ok = wait_warp(values + 8 * (j - check0), 0, a.wait_turns);
-        if (ok) check_values<kTok, D>(sm + oKV + (s % kStages) * kTile, odd, j * kTok, t0, it.len, threadIdx.x - kCheck * 32);
-        __syncwarp();
-        for (int c = lane; c < 3 * D; c += 32)
-          if (odd[c] != 0x7fffffff) *any_odd = 1;
-        fence_async();
-        __syncwarp();
-        mbar_arrive_if(checked + 8 * (j - check0), lane == 0);
+      while (next(at_item, ok, it, h)) {
+        const Work x(it, h, tt);
+        // the rows of the item before have been written (of the first: at once)
+        ok = wait(bar.odd_free, free_phase);
+        if (!ok) break;
+        free_phase ^= 1;
+        asm volatile("bar.sync 4, 64;" ::: "memory");
+        const bool reset = *any_odd != 0;
+        asm volatile("bar.sync 4, 64;" ::: "memory");
+        if (reset) {
+          for (int i = me; i < 3 * D; i += 64) odd[i] = 0x7fffffff;
+          if (me == 0) *any_odd = 0;
+          asm volatile("bar.sync 4, 64;" ::: "memory");
+        }
+        for (int i = 0; i < kChecked; ++i) {
+          if (i < x.checks()) {
+            ok = wait(bar.values + 8 * i, v_phase >> i & 1);
+            if (!ok) break;
+            v_phase ^= 1u << i;
+            const int j = x.check0 + i, stage = (first_stage + 2 * j + 1) % kStages;
+            check_values<kTok, D>(sm + oKV + stage * kTile, odd, j * kTok, x.t0, x.len, me);
+            __syncwarp();
+            for (int c = lane; c < 3 * D; c += 32)
+              if (odd[c] != 0x7fffffff) *any_odd = 1;
+            fence_async();
+          }
+          __syncwarp();
+          mbar_arrive_if(bar.checked + 8 * i, lane == 0);
+        }
+        if (!ok) break;
+        first_stage = (first_stage + 2 * x.nt) % kStages;
       }
       if (!ok && lane == 0) fail();
     }
@@ -358,13 +503,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 int launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t stream) {
-  static bool done[64] = {false};
+  static int sms[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return OSCAR_ERR_LAUNCH;
-  if (!done[dev]) {
-    if (cudaFuncSetAttribute(attn_prompt_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
+  if (!sms[dev]) {
+    int n = 0;
+    if (cudaFuncSetAttribute(attn_prompt_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return OSCAR_ERR_LAUNCH;
-    done[dev] = true;
+    sms[dev] = n;
   }
   const int tt = N / a.G;
   CUtensorMap mq, mk, mv;
@@ -374,7 +521,7 @@ int launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t stream) {
     return OSCAR_ERR_LAUNCH;
   const int64_t items = prompt_items(a, 1, 2 * tt) * a.Hkv;
   if (items >= (int64_t(1) << 31)) return OSCAR_ERR_UNSUPPORTED;
-  attn_prompt_tc_kernel<<<unsigned(items), kThreads, kBytes, stream>>>(mq, mk, mv, a);
+  attn_prompt_tc_kernel<<<unsigned(std::min<int64_t>(items, sms[dev])), kThreads, kBytes, stream>>>(mq, mk, mv, a);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
 }
 

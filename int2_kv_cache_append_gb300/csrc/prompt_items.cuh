@@ -12,7 +12,7 @@ struct PromptItem {
 
 // A sequence of len tokens has ceil(len * num / den) tiles; most that n packed
 // tokens of B sequences can give.
-inline int64_t prompt_items(const PromptArgs& a, int num, int den) { return int64_t(a.n) * num / den + a.B; }
+__host__ __device__ inline int64_t prompt_items(const PromptArgs& a, int num, int den) { return int64_t(a.n) * num / den + a.B; }
 
 __device__ __forceinline__ int2 prompt_span(const PromptArgs& a, int b) {
   const int lo = min(max(a.cu[b], 0), a.n), hi = min(max(a.cu[b + 1], lo), a.n);
