@@ -5,7 +5,9 @@
 // h G + r mod G of token r / G) and walks the positions 64 at a time: S = Q K^T
 // from shared memory, 4 x 4 scores per thread, the online softmax with its row
 // statistics in registers, O += P V with 4 rows x D / 16 channels per thread.
-// The FMA pipes bound it.
+// Rows lie in shared memory as in memory, so copies are asynchronous and V's are
+// under way while the scores are formed; P takes K's place, so that two blocks of
+// head_dim 128 share an SM and cover each other's waits.  The FMA pipes bound it.
 #include <algorithm>
 
 #include "prompt_items.cuh"
@@ -14,8 +16,9 @@ namespace oscar {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 64, kTok = 64, kCh = 32;  // rows, positions, channels of a staged slice
-constexpr int kLd = kRows + 4;
+constexpr int kRows = 64, kTok = 64, kCh = 128;  // rows, positions, channels of a staged slice of K
+constexpr int kLdP = kRows + 4;
+constexpr int kLdK = kCh + 4;                    // rows 4 floats apart modulo the banks: 16-byte reads of 16 rows meet no bank twice
 
 template <typename T>
 __device__ __forceinline__ float4 load4(const T* p);
@@ -35,13 +38,36 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
                                             pack_bf162(__float2bfloat16_rn(v.z), __float2bfloat16_rn(v.w)));
 }
 
+// `rows` rows of `channels` (D apart in steps of `step` elements) to shared memory, zeros for those from `live` on; float32 by
+// asynchronous copies.
+template <int channels, int ld, typename T>
+__device__ __forceinline__ void stage(float* to, const T* from, int64_t step, int rows, int live) {
+  for (int i = threadIdx.x; i < rows * (channels / 4); i += kThreads) {
+    const int r = i / (channels / 4), c = 4 * (i % (channels / 4));
+    float* at = to + r * ld + c;
+    if (r >= live) {
+      *reinterpret_cast<float4*>(at) = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else if constexpr (sizeof(T) == 4) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(at)), "l"(from + r * step + c) : "memory");
+    } else {
+      *reinterpret_cast<float4*>(at) = load4(from + r * step + c);
+    }
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int groups>
+__device__ __forceinline__ void staged() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(groups) : "memory");
+}
+
 template <typename T, typename U, int D>
-__global__ void __launch_bounds__(kThreads) attn_prompt_kernel(const PromptArgs a) {
+__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 1) attn_prompt_kernel(const PromptArgs a) {
+  constexpr int kLdQ = D + 4, kVTok = 8192 / D;  // positions of a staged slice of V
   extern __shared__ float sm[];
-  float* qs = sm;                // [D][kLd], scaled to log2 units
-  float* ks = qs + D * kLd;      // [kCh][kLd]
-  float* vs = ks + kCh * kLd;    // [kCh tokens][D]
-  float* ps = vs + kCh * D;      // [kTok][kLd]
+  float* qs = sm;                    // [kRows][kLdQ], scaled to log2 units
+  float* ks = qs + kRows * kLdQ;     // [kTok][kLdK]; then P [kTok][kLdP]
+  float* vs = ks + kTok * kLdK;      // [kVTok][D]
+  float* ps = ks;
   __shared__ PromptItem shared_item;
   if (threadIdx.x < 32) {
     if (blockIdx.x == 0) prompt_check(a);
@@ -53,16 +79,19 @@ __global__ void __launch_bounds__(kThreads) attn_prompt_kernel(const PromptArgs 
   if (it.b < 0) return;
   const int h = blockIdx.x % a.Hkv, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   const int row0 = it.tile * kRows, rows = it.len * a.G;
+  const int64_t step = int64_t(a.Hkv) * D;
   const T* q = static_cast<const T*>(a.q);
-  const T* k = static_cast<const T*>(a.k) + int64_t(h) * D;
-  const T* v = static_cast<const T*>(a.v) + int64_t(h) * D;
+  const T* k = static_cast<const T*>(a.k) + (int64_t(it.start) * a.Hkv + h) * D;
+  const T* v = static_cast<const T*>(a.v) + (int64_t(it.start) * a.Hkv + h) * D;
+  const int all = row0 / a.G;                                 // every row sees the positions up to this one
+  const int end = min(it.len, (row0 + kRows - 1) / a.G + 1);  // and none sees this one
+  stage<kCh, kLdK>(ks, k, step, kTok, end);
   auto head_row = [&](int r) { return int64_t(it.start + r / a.G) * a.Hq + h * a.G + r % a.G; };
   for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
     const int r = i / (D / 4), c = 4 * (i % (D / 4));
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row0 + r < rows) x = load4(q + head_row(row0 + r) * D + c);
-    qs[c * kLd + r] = x.x * a.qscale, qs[(c + 1) * kLd + r] = x.y * a.qscale;
-    qs[(c + 2) * kLd + r] = x.z * a.qscale, qs[(c + 3) * kLd + r] = x.w * a.qscale;
+    *reinterpret_cast<float4*>(qs + r * kLdQ + c) = make_float4(x.x * a.qscale, x.y * a.qscale, x.z * a.qscale, x.w * a.qscale);
   }
   int last[4];  // the rows' last visible position
   float m[4], l[4], o[4][D / 16];
@@ -73,37 +102,42 @@ __global__ void __launch_bounds__(kThreads) attn_prompt_kernel(const PromptArgs 
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) o[i][j] = 0.f;
   }
-  const int all = row0 / a.G;                                     // every row sees the positions up to this one
-  const int end = min(it.len, (row0 + kRows - 1) / a.G + 1);      // and none sees this one
   for (int p0 = 0; p0 < end; p0 += kTok) {
-    float s[4][4] = {};
+    stage<D, D>(vs, v + p0 * step, step, kVTok, end - p0);  // under way while the scores are formed
+    float s[4][4] = {};                                     // position tx + 16 j
     for (int c0 = 0; c0 < D; c0 += kCh) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < kTok * (kCh / 4); i += kThreads) {
-        const int t = i / (kCh / 4), c = 4 * (i % (kCh / 4));
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p0 + t < end) x = load4(k + int64_t(it.start + p0 + t) * a.Hkv * D + c0 + c);
-        ks[c * kLd + t] = x.x, ks[(c + 1) * kLd + t] = x.y, ks[(c + 2) * kLd + t] = x.z, ks[(c + 3) * kLd + t] = x.w;
+      if (c0 > 0) {
+        __syncthreads();
+        stage<kCh, kLdK>(ks, k + p0 * step + c0, step, kTok, end - p0);
+        staged<0>();
+      } else {
+        staged<1>();
       }
       __syncthreads();
-#pragma unroll 8
-      for (int c = 0; c < kCh; ++c) {
-        const float4 x = *reinterpret_cast<const float4*>(qs + (c0 + c) * kLd + 4 * ty);
-        const float4 y = *reinterpret_cast<const float4*>(ks + c * kLd + 4 * tx);
-        const float xr[4] = {x.x, x.y, x.z, x.w}, yr[4] = {y.x, y.y, y.z, y.w};
+      const float *qr = qs + 4 * ty * kLdQ + c0, *kr = ks + tx * kLdK;
+#pragma unroll 4
+      for (int c = 0; c < kCh; c += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = *reinterpret_cast<const float4*>(qr + i * kLdQ + c);
+          y[i] = *reinterpret_cast<const float4*>(kr + 16 * i * kLdK + c);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[i][j] = fmaf(xr[i], yr[j], s[i][j]);
+          for (int j = 0; j < 4; ++j)
+            s[i][j] = fmaf(x[i].w, y[j].w, fmaf(x[i].z, y[j].z, fmaf(x[i].y, y[j].y, fmaf(x[i].x, y[j].x, s[i][j]))));
       }
     }
     const bool masked = p0 + kTok - 1 > all;
+    __syncthreads();  // P goes where K was
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (p0 + 4 * tx + j > last[i]) s[i][j] = -INFINITY;
+        if (p0 + tx + 16 * j > last[i]) s[i][j] = -INFINITY;
         top = fmaxf(top, s[i][j]);
       }
 #pragma unroll
@@ -122,21 +156,20 @@ __global__ void __launch_bounds__(kThreads) attn_prompt_kernel(const PromptArgs 
       l[i] = l[i] * f + sum;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) o[i][j] *= f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) ps[(4 * tx + j) * kLd + 4 * ty + i] = s[i][j];
     }
-    for (int t0 = 0; t0 < kTok && p0 + t0 < end; t0 += kCh) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < kCh * (D / 4); i += kThreads) {
-        const int t = i / (D / 4), c = 4 * (i % (D / 4));
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p0 + t0 + t < end) x = load4(v + int64_t(it.start + p0 + t0 + t) * a.Hkv * D + c);
-        *reinterpret_cast<float4*>(vs + t * D + c) = x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<float4*>(ps + (tx + 16 * j) * kLdP + 4 * ty) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+    for (int t0 = 0; t0 < kTok && p0 + t0 < end; t0 += kVTok) {
+      if (t0 > 0) {
+        __syncthreads();
+        stage<D, D>(vs, v + (p0 + t0) * step, step, kVTok, end - p0 - t0);
       }
+      staged<0>();
       __syncthreads();
 #pragma unroll 2
-      for (int t = 0; t < kCh; ++t) {
-        const float4 x = *reinterpret_cast<const float4*>(ps + (t0 + t) * kLd + 4 * ty);
+      for (int t = 0; t < kVTok; ++t) {
+        const float4 x = *reinterpret_cast<const float4*>(ps + (t0 + t) * kLdP + 4 * ty);
         const float xr[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
@@ -152,6 +185,8 @@ __global__ void __launch_bounds__(kThreads) attn_prompt_kernel(const PromptArgs 
         }
       }
     }
+    __syncthreads();
+    if (p0 + kTok < end) stage<kCh, kLdK>(ks, k + (p0 + kTok) * step, step, kTok, end - p0 - kTok);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -168,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) attn_prompt_kernel(const PromptArgs 
 
 template <typename T, typename U, int D>
 int launch_d(const PromptArgs& a, cudaStream_t stream) {
-  constexpr int smem = (D * kLd + kCh * kLd + kCh * D + kTok * kLd) * 4;
+  constexpr int smem = (kRows * (D + 4) + kTok * kLdK + 8192) * 4;
   static bool done[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return OSCAR_ERR_LAUNCH;
