@@ -8,7 +8,8 @@
 //
 //   select  one cluster of blocks per (sequence, KV head): the smallest kept key by
 //           three histogram passes over the masses (as integers that order as the
-//           numbers do; 11, 11 and 10 bits), the blocks' bins added through
+//           numbers do; 11, 11 and 10 bits), which stay in shared memory after the
+//           first, the blocks' bins added through
 //           distributed shared memory; then every warp counts and lists the kept
 //           ones of a contiguous piece;
 //   gather  the rows of every new position: a position of the new cache is a sink
@@ -29,6 +30,7 @@ namespace {
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;        // 11 bits of a key
 constexpr int kLoads = 4;          // masses of a thread under way
+constexpr int kHeld = 24 * 1024;   // keys of a block that stay in shared memory, read once; two blocks to an SM
 constexpr int kMostCluster = 8;
 constexpr int kGatherThreads = 256;
 constexpr int kBody = 128;         // new positions of a gather block
@@ -80,6 +82,7 @@ __device__ __forceinline__ int block_exclusive(int x, int* warp_sums) {
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const EvictArgs a) {
   __shared__ int hist[kBins], sums[kSelWarps], above_of[kSelWarps], same_of[kSelWarps];
   __shared__ int pick, left, totals[2];
+  extern __shared__ uint32_t held[];
   const cg::cluster_group cluster = cg::this_cluster();
   const int size = int(cluster.num_blocks()), rank = int(cluster.block_rank());
   const int unit = blockIdx.x / size, b = unit / a.g.Hkv;
@@ -105,6 +108,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
   }
   const float* mass = a.mass + int64_t(unit) * a.g.cap + a.g.S;
   const int part = (s.body + size - 1) / size, lo = min(s.body, rank * part), hi = min(s.body, lo + part);
+  auto key_at = [&](int i) { return i - lo < kHeld ? held[i - lo] : mass_key(__ldg(mass + i)); };
   uint32_t prefix = 0, mask = 0;
   int need = s.held;  // kept ones among the keys with this prefix
 #pragma unroll 1
@@ -115,7 +119,17 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     for (int i = lo + threadIdx.x; i < hi; i += kLoads * kSelThreads) {
       uint32_t key[kLoads];
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) key[u] = i + u * kSelThreads < hi ? mass_key(__ldg(mass + i + u * kSelThreads)) : 0u;
+      for (int u = 0; u < kLoads; ++u) {
+        const int at = i + u * kSelThreads;
+        key[u] = at >= hi ? 0u : round ? key_at(at) : mass_key(__ldg(mass + at));
+      }
+      if (round == 0) {
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const int at = i + u * kSelThreads;
+          if (at < hi && at - lo < kHeld) held[at - lo] = key[u];
+        }
+      }
 #pragma unroll
       for (int u = 0; u < kLoads; ++u)
         if (i + u * kSelThreads < hi && (key[u] & mask) == prefix) atomicAdd(&hist[(key[u] >> shift) & ((1u << bits) - 1)], 1);
@@ -146,7 +160,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
   for (int i = w0 + lane; i < w1; i += kLoads * 32) {
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
-      const uint32_t key = i + 32 * u < w1 ? mass_key(__ldg(mass + i + 32 * u)) : 0u;
+      const uint32_t key = i + 32 * u < w1 ? key_at(i + 32 * u) : 0u;
       above += i + 32 * u < w1 && key > prefix;
       same += i + 32 * u < w1 && key == prefix;
     }
@@ -170,7 +184,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
       const int i = i0 + 32 * u + lane;
-      key[u] = i < w1 ? mass_key(__ldg(mass + i)) : 0u;
+      key[u] = i < w1 ? key_at(i) : 0u;
     }
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
@@ -301,6 +315,13 @@ int launch_kv_evict(const EvictArgs& args, cudaStream_t stream) {
   if (units > 65535 || cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return OSCAR_ERR_LAUNCH;
+  static bool done[64] = {false};
+  if (dev >= 64) return OSCAR_ERR_LAUNCH;
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * 4) != cudaSuccess)
+      return OSCAR_ERR_LAUNCH;
+    done[dev] = true;
+  }
   // blocks of a unit: as many as fill the GPU (two on an SM), none with less than 4096 positions
   int size = 1;
   while (size < kMostCluster && 2 * size * units <= 2 * sms && a.g.cap / (2 * size) >= 4096) size *= 2;
@@ -311,6 +332,7 @@ int launch_kv_evict(const EvictArgs& args, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(units * size));
   cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = kHeld * 4;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
