@@ -71,7 +71,8 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 1) attn_prompt_kernel
   __shared__ PromptItem shared_item;
   if (threadIdx.x < 32) {
     if (blockIdx.x == 0) prompt_check(a);
-    const PromptItem it = prompt_item(a, blockIdx.x / a.Hkv, a.G, kRows);
+    int level = -1;
+    const PromptItem it = prompt_item(a, blockIdx.x / a.Hkv, a.G, kRows, level);
     if (threadIdx.x == 0) shared_item = it;
   }
   __syncthreads();

@@ -19,9 +19,12 @@
 // the next one's tiles, and its first products run under the last one's softmax and
 // output.
 //
-// Softmax: a thread has a row; its reference M follows the row's maximum only when
-// that has grown by 2^8, and then the warp rescales its rows of O.  P is rounded to
-// bf16, V's type; row sums are taken before the rounding, in float32.
+// Softmax: a thread has a row; its reference M lies 2^12 above the row's maximum when
+// it is chosen and follows it only when that has grown by 2^20, which makes the
+// warp rescale its rows of O: P and O are floating point, so their precision does
+// not depend on where M lies, and 2^20 is hardly ever reached (activations with
+// outliers, eight ragged prompts: @@).  P is rounded to bf16, V's type; row sums are
+// taken before the rounding, in float32.
 //
 // Positions that some of the block's rows do not see: their scores are set to
 // -inf, which makes P zero, and a warp pair looks through those V rows first: where
@@ -43,6 +46,7 @@ constexpr int kStages = 5;
 constexpr int kChecked = 2;            // position tiles with tokens that some rows do not see
 constexpr float kNone = -1e30f;
 constexpr float kTop = 8.f;            // log2 of the largest P
+constexpr float kAbove = 12.f;         // a new M lies this far above its row's maximum
 constexpr int oQ = 0, oKV = 2 * kTile, oOdd = oKV + kStages * kTile, oBar = oOdd + 3 * D * 4;
 constexpr int kItems = 3;              // items found ahead
 constexpr int kBars = 2 * kStages + 5 * 2 + 2 * kChecked + 1 + 2 * kItems + 1;
@@ -174,8 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.qscale;
         const bool grow = t > M + kTop;
         if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? exp2f(M - t) : 1.f;
-          if (grow) M = t;
+          const float f = grow ? exp2f(M - (t + kAbove)) : 1.f;
+          if (grow) M = t + kAbove;
           l2 = mul2(l2, splat_x2(f));
           if (j > 0) {
 #pragma unroll 1
@@ -282,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<kStages> at;
       uint32_t q_phase = 0, q_used = 0, v_phase = 0, v_used = 0, c_phase = 0;  // bits of the barriers of a kind
       int64_t round = 0;
+      int level = -1;
       int published = 0, issued = 0;
       bool ok = true;
 #pragma unroll 1
@@ -292,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t i = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
           ++round;
           if (i >= total) continue;
-          it = prompt_item(a, int(i / a.Hkv), 1, 2 * tt);
+          it = prompt_item(a, int(i / a.Hkv), 1, 2 * tt, level);
           h = int(i % a.Hkv);
           break;
         }

@@ -27,7 +27,7 @@ constexpr int kMma = 8, kLoad = 9, kCheck = 10;
 constexpr int kChecked = 2;            // position tiles with tokens that some rows do not see
 constexpr int kValueUnits = 4;         // V units of a position tile
 constexpr float kNone = -1e30f;
-constexpr float kTop = 8.f;
+constexpr float kTop = 8.f, kAbove = 12.f;
 constexpr uint32_t cS = 0, cO = 256;   // TMEM columns: two score tiles, O
 
 template <int D>
@@ -67,7 +67,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* swap = reinterpret_cast<float*>(sm + C::oSwap);  // [2][2][N]
   if (warp == 0) {
     if (blockIdx.x == 0) prompt_check(a);
-    const PromptItem it = prompt_item(a, blockIdx.x / (a.Hkv * kParts), 1, tt);
+    int level = -1;
+    const PromptItem it = prompt_item(a, blockIdx.x / (a.Hkv * kParts), 1, tt, level);
     if (lane == 0) item = it;
   }
   if (threadIdx.x == kLoad * 32) {
@@ -138,8 +139,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float t = fmaxf(mine[row], mine[N + row]) * a.qscale;
       const bool grow = t > M + kTop;
       if (__any_sync(0xffffffffu, grow)) {
-        const float f = grow ? exp2f(M - t) : 1.f;
-        if (grow) M = t;
+        const float f = grow ? exp2f(M - (t + kAbove)) : 1.f;
+        if (grow) M = t + kAbove;
         l2 = mul2(l2, splat_x2(f));
         if (j > 0) {
           ok = wait(p_done, (j - 1) & 1);  // O is not in use
