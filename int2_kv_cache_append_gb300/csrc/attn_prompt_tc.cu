@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool strange = *any_odd != 0;
         const int64_t at = int64_t(x.start + tok) * a.Hq + x.h * a.G + row % a.G;
         if (live && a.lse) a.lse[at] = (M + log2f(l)) * 0.6931471805599453f;
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * D);
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at * D;
+        const bool aligned32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[2][16];
@@ -258,13 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (at_c[2 * D + i] <= tok) y[i] -= INFINITY;
               }
             }
-            if (live) {
-              uint32_t q[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) q[i] = bf162_of(y[2 * i], y[2 * i + 1]);
-              dst[c / 8 + 2 * e] = make_uint4(q[0], q[1], q[2], q[3]);
-              dst[c / 8 + 2 * e + 1] = make_uint4(q[4], q[5], q[6], q[7]);
-            }
+            if (live) store16(dst + c + 16 * e, y, aligned32);
           }
         }
         fence_before();  // O has been read when the next item's first P arrives

@@ -20,6 +20,22 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// Sixteen bf16 values of a row, 32 bytes: one store where the address allows it.  The threads of a warp have rows of their own,
+// so a store costs by the rows that it touches, not by its bytes.
+__device__ __forceinline__ void store16(__nv_bfloat16* to, const float (&x)[16], bool aligned32) {
+  uint32_t q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = bf162_of(x[2 * i], x[2 * i + 1]);
+  if (aligned32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3]),
+                 "r"(q[4]), "r"(q[5]), "r"(q[6]), "r"(q[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(to)[0] = make_uint4(q[0], q[1], q[2], q[3]);
+    reinterpret_cast<uint4*>(to)[1] = make_uint4(q[4], q[5], q[6], q[7]);
+  }
+}
+
 // `rows` V rows of 128 channels (two blocks of 64, swizzled) that some query rows of the block do not see: zero for what is
 // infinite or not a number.  odd [3][channels]: the first token of the sequence with a NaN, +inf, -inf in a channel.  By 64
 // threads, x of them.
