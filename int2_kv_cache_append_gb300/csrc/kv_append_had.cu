@@ -55,17 +55,17 @@ __device__ __forceinline__ uint2 gather_words(const uint32_t (&w)[8], int q) {
   return make_uint2(r[0], r[1]);
 }
 
-template <int D, bool FP32>
-__global__ void __launch_bounds__(kThreads, 2) kv_append_had_kernel(const AppendArgs a) {
+template <int D, bool FP32, bool LM>
+__global__ void __launch_bounds__(kThreads, 3) kv_append_had_kernel(const AppendArgs a) {
   constexpr int LPR = D / 32, RPW = 32 / LPR;  // lanes of a row, rows of a warp
   const Geom& g = a.g;
   const int lane = threadIdx.x & 31, q = lane & 3, j = (lane % LPR) / 4, role = blockIdx.y;
-  const int64_t row = (int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * RPW + lane / LPR;
+  const uint32_t row = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * RPW + lane / LPR;  // below 2^31 + a block's
   const bool valid = row < a.rows;
   const int c0 = kGroup * j + 8 * q;  // the lane's first channel
   uint64_t x[4][4];                   // channels c0 + 32 m + 2 k, + 1
   {
-    const int64_t at = (valid ? row : 0) * D + c0;
+    const int64_t at = int64_t(valid ? row : 0) * D + c0;
     if (FP32) {
       const float* src = static_cast<const float*>(role ? a.v_new : a.k_new) + at;
 #pragma unroll
@@ -90,12 +90,19 @@ __global__ void __launch_bounds__(kThreads, 2) kv_append_had_kernel(const Append
   int b = 0, h = 0, p = -1, newlen = 0;
   bool mine = valid;
   if (valid) {
-    h = int(row % g.Hkv);
-    const NewToken tok = new_token(a, row / g.Hkv);
-    mine = tok.b >= 0;
-    b = max(tok.b, 0);
-    p = a.start_pos[b] + tok.t;
-    newlen = a.start_pos[b] + tok.count;
+    const uint32_t bt = fastdiv(row, a.div_hkv);
+    h = int(row - bt * uint32_t(g.Hkv));
+    int t, count = a.n_new;
+    if (a.cu) {
+      const NewToken tok = packed_token(a.cu, g.B, bt);
+      mine = tok.b >= 0;
+      b = max(tok.b, 0), t = tok.t, count = tok.count;
+    } else {
+      b = int(fastdiv(bt, a.div_n_new));
+      t = int(bt - uint32_t(b) * uint32_t(a.n_new));
+    }
+    p = a.start_pos[b] + t;
+    newlen = a.start_pos[b] + count;
   }
 
   // x H: bits 5 and 6, 0, 1 and 2 within the lane, 3 and 4 across
@@ -129,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_append_had_kernel(const Append
     for (int k = 0; k < 4; ++k) x[m][k] = mul2(across(x[m][k], 2, sign4), unit);
 
   if (a.debug_rot && valid) {
-    uint64_t* dst = reinterpret_cast<uint64_t*>(a.debug_rot + (row * 2 + role) * D + c0);
+    uint64_t* dst = reinterpret_cast<uint64_t*>(a.debug_rot + (int64_t(row) * 2 + role) * D + c0);
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -160,15 +167,24 @@ __global__ void __launch_bounds__(kThreads, 2) kv_append_had_kernel(const Append
   }
 
   float amax = 0.f;
-  bool finite = true;
 #pragma unroll
   for (int m = 0; m < 4; ++m)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 v = both(x[m][k]);
-      amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
-      finite = finite && isfinite(v.x) && isfinite(v.y);
+      amax = fmax3_nan(amax, fabsf(v.x), fabsf(v.y));
     }
+  const bool finite = isfinite(amax);
+  if (!finite) {  // the largest of those that are numbers
+    amax = 0.f;
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = both(x[m][k]);
+        amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+      }
+  }
 #pragma unroll
   for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if (inside && !finite) status_or(a.status, OSCAR_DEV_NONFINITE);
@@ -192,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_append_had_kernel(const Append
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   }
-  const float s32 = __fdiv_rn(__fsub_rn(mx, mn), g.lm ? kLmSpan : 3.0f);
+  const float s32 = __fdiv_rn(__fsub_rn(mx, mn), LM ? kLmSpan : 3.0f);
   const __half sh = __float2half_rn(s32), zh = __float2half_rn(mn);
   const float sf = __half2float(sh), zf = __half2float(zh);
   const bool rng_ok = isfinite(sf) && isfinite(zf);
@@ -206,8 +222,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_append_had_kernel(const Append
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 y = both(mul2(sub2(x[m][k], zz), ii));
-      const uint32_t u = g.lm ? lm_code(y.x) : min(__float2uint_rn(y.x), 3u);  // the conversion saturates below 0
-      const uint32_t v = g.lm ? lm_code(y.y) : min(__float2uint_rn(y.y), 3u);
+      const uint32_t u = LM ? lm_code(y.x) : min(__float2uint_rn(y.x), 3u);  // the conversion saturates below 0
+      const uint32_t v = LM ? lm_code(y.y) : min(__float2uint_rn(y.y), 3u);
       if (role == 0) {  // word 2 k + (m >> 1), code 2 (q >> 1) + 4 (m & 1) + (q & 1) of its low (even channel) and high half
         w[2 * k + (m >> 1)] |= (u | v << 16) << (8 * (m & 1));
       } else {          // word 2 k (+ 1), code q + 4 m
@@ -226,12 +242,16 @@ __global__ void __launch_bounds__(kThreads, 2) kv_append_had_kernel(const Append
 }
 
 template <int D>
-int launch_d(const AppendArgs& a, cudaStream_t stream) {
+int launch_d(const AppendArgs& args, cudaStream_t stream) {
+  if (args.rows >= (int64_t(1) << 31)) return OSCAR_ERR_UNSUPPORTED;
+  AppendArgs a = args;
+  a.div_hkv = fastdiv_make(uint32_t(a.g.Hkv));
+  a.div_n_new = fastdiv_make(uint32_t(a.n_new > 0 ? a.n_new : 1));
   const int64_t per = int64_t(kThreads / 32) * (32 / (D / 32)), blocks = (a.rows + per - 1) / per;
-  if (blocks >= (int64_t(1) << 31)) return OSCAR_ERR_UNSUPPORTED;
   const dim3 grid(unsigned(blocks), 2);
-  if (a.in_fp32) kv_append_had_kernel<D, true><<<grid, kThreads, 0, stream>>>(a);
-  else kv_append_had_kernel<D, false><<<grid, kThreads, 0, stream>>>(a);
+  const auto kernel = a.in_fp32 ? (a.g.lm ? kv_append_had_kernel<D, true, true> : kv_append_had_kernel<D, true, false>)
+                                : (a.g.lm ? kv_append_had_kernel<D, false, true> : kv_append_had_kernel<D, false, false>);
+  kernel<<<grid, kThreads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
 }
 

@@ -175,6 +175,18 @@ def test_without_lse(D):
     assert torch.equal(out[:150], p.out[:150])
 
 
+@pytest.mark.parametrize("D", [128, 256, 512])
+def test_an_output_at_any_16_bytes(D):
+    p = Prompt(D, 4, 2, [150, 41])
+    p.run()
+    flat = torch.full((p.out.numel() + 16,), 7.0, dtype=p.out.dtype, device="cuda")
+    out = flat[8:8 + p.out.numel()].view(p.out.shape)
+    K.attn_prompt(p.cfg, p.q, p.k, p.v, p.cu, out)
+    torch.cuda.synchronize()
+    assert out.data_ptr() % 32 == 16 and torch.equal(out, p.out)
+    assert bool((flat[:8] == 7).all()) and bool((flat[-8:] == 7).all())
+
+
 @pytest.mark.parametrize("D,lens", [(128, [600, 33]), (128, [1]), (256, [400]), (512, [300, 300])])
 def test_a_wait_that_runs_out(D, lens):
     from tests.test_gpu_rows_timeout import times_out_and_recovers
