@@ -20,6 +20,11 @@
 // parts; a lane's 16-byte pieces of a row are its fragments, channels in an order
 // of their own.
 //
+// What bounds it: instructions, about 300 a batch of 32 positions, over half of them
+// the codes' unpacking and the products (32 ragged sequences of up to 32K, 8 KV heads
+// of 4 rows: 103 us, 2.5 TB/s of K and masses); with many rows the mma.sync pipe and
+// its latency (256 rows over 16,384 positions x 8 KV heads: 96 us).
+//
 // The rows' fragments are written once by a kernel of their own behind the query
 // rotation: built by every block they cost as much as the positions themselves.
 #include <algorithm>
@@ -397,6 +402,8 @@ int launch_n(const MassArgs& a, cudaStream_t stream) {
 }
 template <int D>
 int launch_d(const MassArgs& a, cudaStream_t stream) {
+  // One or two tiles of rows: their fragments stay in registers.  Against the form for more, 4 rows of each of 64 units over
+  // 32,768 positions 51 us instead of 116, 8 rows of 64 units over 16,384 38 us instead of 57.
   return a.tiles <= 1 ? launch_n<D, 1, true>(a, stream) : a.tiles == 2 ? launch_n<D, 2, true>(a, stream)
                                                                        : launch_n<D, 4, false>(a, stream);
 }
@@ -414,9 +421,11 @@ int launch_attn_mass(const MassArgs& args, cudaStream_t stream) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return OSCAR_ERR_LAUNCH;
-  // positions of a warp: few enough for every SM to have 32 warps in turn
+  // Positions of a warp: few enough for every SM to have 32 warps in turn.  us a call with 32 / 64 / 128 / 256: 64 units of
+  // 32,768 positions 63 / 51 / 47 / 51, 256 of 8192 69 / 55 / 52 / 55, 8 of 32,768 15 / 14 / 15 / 20, 8 of 16,384 with 256 query
+  // rows each 96 / 127 / 169 / 289; 256 ragged ones of up to 32,768 107 with 128, 103 with 256.
   const int64_t even = int64_t(a.top) * a.g.B * a.g.Hkv / (32 * sms);
-  a.piece = int(std::min<int64_t>(kMostPiece, std::max<int64_t>(kBatch, even / kBatch * kBatch)));
+  a.piece = even >= 4 * kMostPiece ? kMostPiece : int(std::min<int64_t>(kMostPiece / 2, std::max<int64_t>(kBatch, even / kBatch * kBatch)));
   return a.g.D == 128 ? launch_d<128>(a, stream) : a.g.D == 256 ? launch_d<256>(a, stream) : launch_d<512>(a, stream);
 }
 

@@ -7,7 +7,9 @@
 // statistics in registers, O += P V with 4 rows x D / 16 channels per thread.
 // Rows lie in shared memory as in memory, so copies are asynchronous and V's are
 // under way while the scores are formed; P takes K's place, so that two blocks of
-// head_dim 128 share an SM and cover each other's waits.  The FMA pipes bound it.
+// head_dim 128 share an SM and cover each other's waits.  The FMA pipes bound it:
+// three prompts of up to 333 tokens, 24 heads, 88 us, of which the longest block's
+// six tiles are the most (all products at the FMA rate: 24 us).
 #include <algorithm>
 
 #include "prompt_items.cuh"

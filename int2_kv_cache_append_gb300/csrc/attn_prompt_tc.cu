@@ -22,14 +22,21 @@
 // Softmax: a thread has a row; its reference M lies 2^12 above the row's maximum when
 // it is chosen and follows it only when that has grown by 2^20, which makes the
 // warp rescale its rows of O: P and O are floating point, so their precision does
-// not depend on where M lies, and 2^20 is hardly ever reached (activations with
-// outliers, eight ragged prompts: @@).  P is rounded to bf16, V's type; row sums are
-// taken before the rounding, in float32.
+// not depend on where M lies, and 2^20 is hardly ever reached (M at the maximum,
+// followed from 2^8 on: 522 us instead of 450 for eight ragged prompts of
+// activations with outliers).  P is rounded to bf16, V's type; row sums are taken
+// before the rounding, in float32.
 //
 // Positions that some of the block's rows do not see: their scores are set to
 // -inf, which makes P zero, and a warp pair looks through those V rows first: where
 // a value is infinite or not a number, zero times it would reach every row.  It is
 // replaced by zero there, and added to the rows that see it at the end.
+//
+// What bounds it: over long sequences the tensor cores (16,384 tokens, 32 heads:
+// 1.38 ms, 1.59 PFLOP/s of the products that a causal mask leaves, 85 % of cuBLAS's
+// rate); over short ones the hand-over from item to item, where the output is read,
+// scaled and stored while the next scores wait (eight ragged prompts of up to 4096
+// tokens 440 us, 69 %; 64 of 512 204 us, 36 %).
 #include <algorithm>
 
 #include "prompt_tc.cuh"

@@ -916,11 +916,12 @@ int launch_append_small(const AppendArgs& a, cudaStream_t stream) {
 }
 
 // the in-quant Hadamard reads no matrix, so a decode step takes the row-parallel
-// kernel, with its programmatic launch; more rows go eight to a warp
-// (kv_append_had.cu)
+// kernel, with its programmatic launch; more rows go four lanes to 128 channels
+// (kv_append_had.cu; row-parallel against that, us: 512 rows of 128 3.7 / 4.0,
+// 1024 4.5 / 4.3, 8192 10.1 / 5.1; 128 rows of 512 3.3 / 4.1, 1024 8.4 / 4.5)
 template <int D>
 int launch_append_hadamard(const AppendArgs& a, cudaStream_t stream) {
-  if (a.rows > kSmallAppendRows) return launch_append_had(a, stream);
+  if (a.rows * D > kSmallAppendRows * 128) return launch_append_had(a, stream);
   return a.rows > 512 ? launch_append_rows<D, 8, true>(a, stream) : launch_append_rows<D, 4, true>(a, stream);
 }
 

@@ -8,6 +8,9 @@
 // of the row-parallel kernel in its order (bits 5, 6, then 0 .. 4; every step one
 // float32 rounding), so the bytes are the same.
 //
+// What bounds it: instructions, 850 for eight rows (four ragged prompts of 8192 tokens, 8
+// KV heads: 55 us, 2.1 TB/s; the row-parallel kernel 185 us).
+//
 // The lane's codes of a word lie in two bit pairs per half (K) or four (V); two
 // exchanges add the four lanes' parts up and leave each with two whole words.
 #include "rows_tc.cuh"

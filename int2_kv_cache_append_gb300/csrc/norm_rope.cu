@@ -17,6 +17,9 @@
 // the second half of the rotated channels (and likewise of the rest, if there is
 // one), so every pair lies within a lane, and its loads and stores are 16 bytes.
 // They are plain loads: a row may be written where it was read.
+//
+// What bounds it: DRAM (16,384 tokens of 72 heads in bf16, 604 MB: 115 us, 5.25 TB/s,
+// 79 % of a copy's rate); one decode step takes 4 us.
 #include <algorithm>
 
 #include "internal.h"
@@ -170,9 +173,11 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormRopeAr
 template <typename T, int D>
 int launch_d(NormRopeArgs a, int sms, cudaStream_t stream) {
   const int groups = (a.Hq + kRowsOfWarp<D> - 1) / kRowsOfWarp<D> + (a.Hkv + kRowsOfWarp<D> - 1) / kRowsOfWarp<D>;
-  // warps of a token: all eight for few tokens, whose latency counts, one where there are enough to fill the GPU
+  // Warps of a token: all eight for few tokens, whose latency counts, one where there are enough to fill the GPU.  us a call with
+  // 1 / 2 / 4 / 8 and 40 heads: 8 tokens 9.1 / 6.1 / 5.0 / 4.0, 256 9.1 / 6.4 / 5.0 / 5.0, 1024 9.4 / 7.8 / 10.3 / 11.9, 2048
+  // 11.7 / 13.1 / 14.8 / 17.2, 16,384 67 / 76 / 92 / 113.
   a.wpt = 1;
-  while (a.wpt < kWarps && int64_t(a.n) * a.wpt < 24 * sms && a.wpt < groups) a.wpt *= 2;
+  while (a.wpt < kWarps && int64_t(a.n) * a.wpt < 12 * sms && a.wpt < groups) a.wpt *= 2;
   const int64_t blocks = (int64_t(a.n) * a.wpt + kWarps - 1) / kWarps;
   norm_rope_kernel<T, D><<<unsigned(std::min<int64_t>(blocks, 8 * sms)), kThreads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
