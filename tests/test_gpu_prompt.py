@@ -137,6 +137,22 @@ def test_a_sequence_does_not_depend_on_its_batch(D):
         assert torch.equal(out, p.out[at]) and torch.equal(lse, p.lse[at])
 
 
+@pytest.mark.parametrize("D,lens", [(128, [4000, 3, 900, 1500] * 2), (256, [2000, 300, 1200]), (512, [1500, 700, 90])])
+def test_repeated_calls_give_the_same_bits(D, lens):
+    """Many items a block, run after run, with other work on the GPU beside every other one."""
+    p = Prompt(D, 16, 4, lens)
+    p.run()
+    want, lse = p.out.clone(), p.lse.clone()
+    other, x = torch.cuda.Stream(), torch.randn(4096, 4096, device="cuda")
+    for i in range(40):
+        p.out.fill_(7.0)
+        if i % 2:
+            with torch.cuda.stream(other):
+                x @ x
+        p.run()
+        assert torch.equal(p.out, want) and torch.equal(p.lse, lse), i
+
+
 @pytest.mark.parametrize("D,kind", [(128, "bf16"), (256, "bf16"), (512, "bf16"), (128, "fp32")])
 def test_many_sequences(D, kind):
     """More than a warp's lanes, empty ones among them, in any order of length."""

@@ -69,6 +69,17 @@ def test_positions_in_any_order_and_repeated():
     compare(q, k, w, pos, freqs(128), False, True, *out, 1e-6)
 
 
+def test_positions_below_zero_and_frequencies_above_a_turn():
+    n = 40
+    _, q, k, w = make(128, 4, 2, n, True, 2)
+    pos = np.arange(n) * 13 - 300
+    freq = torch.linspace(-7.0, 30.0, 64, device="cuda")
+    out = [torch.empty(n, h, 128, device="cuda") for h in (4, 2)]
+    K.qk_norm_rope(cfg(128, 4, 2, True), q, k, *w, dev_i32(pos), freq, *out)
+    torch.cuda.synchronize()
+    compare(q, k, w, pos, freq, False, True, *out, 1e-6)
+
+
 @pytest.mark.parametrize("n", [3, 3000])
 @pytest.mark.parametrize("fp32", [False, True], ids=["bf16", "fp32"])
 def test_outputs_over_their_dense_inputs(fp32, n):
