@@ -1,18 +1,20 @@
 // kv_append of many rows with the in-quant Hadamard.
 //
 // The rotation reads no matrix, so the rows' bytes are the bound if the codec's
-// instructions are few: a row of 128 channels has four lanes, 32 channels each
-// (channel = 128 j + 32 m + 8 q + i for lane q of group j), so five of the seven
-// butterfly stages and most of the extrema are within a lane, in packed float32
-// pairs, and eight rows of head_dim 128 share a warp.  Stages and codec are those
-// of the row-parallel kernel in its order (bits 5, 6, then 0 .. 4; every step one
-// float32 rounding), so the bytes are the same.
+// instructions are few: a row of 128 channels has four lanes with 32 consecutive
+// channels each (channel = 128 j + 32 q + i for lane q of group j), so five of the
+// seven butterfly stages and most of the extrema are within a lane, in packed
+// float32 pairs, and eight rows of head_dim 128 share a warp.  Stages and codec are
+// those of the row-parallel kernel in its order (bits 5, 6, then 0 .. 4; every step
+// one float32 rounding), so the bytes are the same.
 //
-// What bounds it: instructions, 850 for eight rows (four ragged prompts of 8192 tokens, 8
-// KV heads: 55 us, 2.1 TB/s; the row-parallel kernel 185 us).
+// Codes of channels 8 apart are next to each other in a word, of K and of V: a lane
+// packs byte g of its channels g, g + 8, g + 16, g + 24 with saturating conversions,
+// and one (K) or two (V) exchanges put the four lanes' bytes together.
 //
-// The lane's codes of a word lie in two bit pairs per half (K) or four (V); two
-// exchanges add the four lanes' parts up and leave each with two whole words.
+// What bounds it: instructions and their latency, 690 for eight rows (four ragged prompts of
+// 8192 tokens, 8 KV heads: 48 us, 2.4 TB/s; three blocks an SM instead of four 53 us; the
+// row-parallel kernel 185 us).
 #include "rows_tc.cuh"
 
 namespace oscar {
@@ -39,53 +41,41 @@ __device__ __forceinline__ uint64_t across(uint64_t x, int mask, uint64_t sign) 
   const float2 v = both(x);
   return fma2(x, sign, pack2(__shfl_xor_sync(0xffffffffu, v.x, mask), __shfl_xor_sync(0xffffffffu, v.y, mask)));
 }
-// word 2 L + .. of the eight partial words of four lanes, to lane L
-__device__ __forceinline__ uint2 gather_words(const uint32_t (&w)[8], int q) {
-  uint32_t u[4];
-  const bool up = q & 2;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t give = up ? w[i] : w[4 + i];
-    u[i] = (up ? w[4 + i] : w[i]) | __shfl_xor_sync(0xffffffffu, give, 2);
-  }
-  const bool odd = q & 1;
-  uint32_t r[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t give = odd ? u[i] : u[2 + i];
-    r[i] = (odd ? u[2 + i] : u[i]) | __shfl_xor_sync(0xffffffffu, give, 1);
-  }
-  return make_uint2(r[0], r[1]);
+// bits << 4 and two codes, each the nearest of 0 .. 3
+__device__ __forceinline__ uint32_t pack_codes(int second, int first, uint32_t bits) {
+  uint32_t d;
+  asm("cvt.pack.sat.u2.s32.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(second), "r"(first), "r"(bits));
+  return d;
 }
 
 template <int D, bool FP32, bool LM>
-__global__ void __launch_bounds__(kThreads, 3) kv_append_had_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) kv_append_had_kernel(const AppendArgs a) {
   constexpr int LPR = D / 32, RPW = 32 / LPR;  // lanes of a row, rows of a warp
   const Geom& g = a.g;
   const int lane = threadIdx.x & 31, q = lane & 3, j = (lane % LPR) / 4, role = blockIdx.y;
   const uint32_t row = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * RPW + lane / LPR;  // below 2^31 + a block's
   const bool valid = row < a.rows;
-  const int c0 = kGroup * j + 8 * q;  // the lane's first channel
-  uint64_t x[4][4];                   // channels c0 + 32 m + 2 k, + 1
+  const int c0 = kGroup * j + 32 * q;  // the lane's first channel
+  uint64_t x[16];                      // channels c0 + 2 k, + 1
   {
     const int64_t at = int64_t(valid ? row : 0) * D + c0;
     if (FP32) {
-      const float* src = static_cast<const float*>(role ? a.v_new : a.k_new) + at;
+      const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(role ? a.v_new : a.k_new) + at);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const float4 u = __ldg(reinterpret_cast<const float4*>(src + 32 * m)), v = __ldg(reinterpret_cast<const float4*>(src + 32 * m) + 1);
-        x[m][0] = pack2(u.x, u.y), x[m][1] = pack2(u.z, u.w), x[m][2] = pack2(v.x, v.y), x[m][3] = pack2(v.z, v.w);
+      for (int m = 0; m < 8; ++m) {
+        const float4 u = __ldg(src + m);
+        x[2 * m] = pack2(u.x, u.y), x[2 * m + 1] = pack2(u.z, u.w);
       }
     } else {
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(role ? a.v_new : a.k_new) + at;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(role ? a.v_new : a.k_new) + at);
       uint4 u[4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) u[m] = __ldg(reinterpret_cast<const uint4*>(src + 32 * m));
+      for (int m = 0; m < 4; ++m) u[m] = __ldg(src + m);
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const uint32_t w[4] = {u[m].x, u[m].y, u[m].z, u[m].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[m][k] = pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+        for (int k = 0; k < 4; ++k) x[4 * m + k] = pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
       }
     }
   }
@@ -108,42 +98,27 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_had_kernel(const Append
     newlen = a.start_pos[b] + count;
   }
 
-  // x H: bits 5 and 6, 0, 1 and 2 within the lane, 3 and 4 across
+  // x H: bits 5 and 6 across lanes, 0 within a pair, 1 .. 4 within the lane
+  const uint64_t sign5 = splat_x2(q & 1 ? -1.f : 1.f), sign6 = splat_x2(q & 2 ? -1.f : 1.f), unit = splat_x2(kInvSqrt128);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    butterfly(x[0][k], x[1][k]);
-    butterfly(x[2][k], x[3][k]);
-    butterfly(x[0][k], x[2][k]);
-    butterfly(x[1][k], x[3][k]);
-  }
-  const uint64_t sign3 = splat_x2(q & 1 ? -1.f : 1.f), sign4 = splat_x2(q & 2 ? -1.f : 1.f), unit = splat_x2(kInvSqrt128);
+  for (int k = 0; k < 16; ++k) x[k] = across(x[k], 1, sign5);
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 v = both(x[m][k]);
-      x[m][k] = pack2(v.x + v.y, v.x - v.y);
-    }
-    butterfly(x[m][0], x[m][1]);
-    butterfly(x[m][2], x[m][3]);
-    butterfly(x[m][0], x[m][2]);
-    butterfly(x[m][1], x[m][3]);
+  for (int k = 0; k < 16; ++k) {
+    const float2 v = both(across(x[k], 2, sign6));
+    x[k] = pack2(v.x + v.y, v.x - v.y);
   }
 #pragma unroll
-  for (int m = 0; m < 4; ++m)
+  for (int bit = 1; bit < 16; bit <<= 1)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[m][k] = across(x[m][k], 1, sign3);
+    for (int k = 0; k < 16; ++k)
+      if (!(k & bit)) butterfly(x[k], x[k | bit]);
 #pragma unroll
-  for (int m = 0; m < 4; ++m)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[m][k] = mul2(across(x[m][k], 2, sign4), unit);
+  for (int k = 0; k < 16; ++k) x[k] = mul2(x[k], unit);
 
   if (a.debug_rot && valid) {
     uint64_t* dst = reinterpret_cast<uint64_t*>(a.debug_rot + (int64_t(row) * 2 + role) * D + c0);
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) dst[16 * m + k] = x[m][k];
+    for (int k = 0; k < 16; ++k) dst[k] = x[k];
   }
   const bool inside = mine && p >= 0 && p < g.cap;
   if (mine && !inside && lane % LPR == 0) status_or(a.status, OSCAR_DEV_OVER_CAPACITY);
@@ -160,33 +135,32 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_had_kernel(const Append
       uint32_t u[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 v = both(x[m][k]);
+        const float2 v = both(x[4 * m + k]);
         u[k] = pack_bf162(__float2bfloat16_rn(v.x), __float2bfloat16_rn(v.y));
       }
       const uint4 w = make_uint4(u[0], u[1], u[2], u[3]);
-      if (to_sink || whole) d0[4 * m] = w;
-      if (to_ring) d1[4 * m] = w;
+      if (to_sink || whole) d0[m] = w;
+      if (to_ring) d1[m] = w;
     }
   }
 
-  float amax = 0.f;
+  float rmn = INFINITY, rmx = -INFINITY;
 #pragma unroll
-  for (int m = 0; m < 4; ++m)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 v = both(x[m][k]);
-      amax = fmax3_nan(amax, fabsf(v.x), fabsf(v.y));
-    }
-  const bool finite = isfinite(amax);
-  if (!finite) {  // the largest of those that are numbers
+  for (int k = 0; k < 16; ++k) {
+    const float2 v = both(x[k]);
+    rmn = fmin3_nan(rmn, v.x, v.y);
+    rmx = fmax3_nan(rmx, v.x, v.y);
+  }
+  const bool finite = isfinite(rmn) && isfinite(rmx);
+  float amax = fmaxf(fabsf(rmn), fabsf(rmx));
+  const bool strange = __any_sync(0xffffffffu, !finite);
+  if (strange) {  // the largest of those that are numbers
     amax = 0.f;
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 v = both(x[m][k]);
-        amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
-      }
+    for (int k = 0; k < 16; ++k) {
+      const float2 v = both(x[k]);
+      amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+    }
   }
 #pragma unroll
   for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -194,23 +168,25 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_had_kernel(const Append
   if (whole) return;  // all of the block
 
   const float tclip = __fmul_rn(role ? a.v_clip : a.k_clip, amax);
-  float mn = INFINITY, mx = -INFINITY;
+  auto clip = [&]() {
+    rmn = INFINITY, rmx = -INFINITY;
 #pragma unroll
-  for (int m = 0; m < 4; ++m)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float2 v = both(x[m][k]);
+    for (int k = 0; k < 16; ++k) {
+      float2 v = both(x[k]);
       v.x = fminf(fmaxf(v.x, -tclip), tclip);
       v.y = fminf(fmaxf(v.y, -tclip), tclip);
-      mn = fminf(mn, fminf(v.x, v.y));
-      mx = fmaxf(mx, fmaxf(v.x, v.y));
-      x[m][k] = pack2(v.x, v.y);
+      rmn = fminf(rmn, fminf(v.x, v.y));
+      rmx = fmaxf(rmx, fmaxf(v.x, v.y));
+      x[k] = pack2(v.x, v.y);
     }
+  };
+  if (strange) clip();
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    rmn = fminf(rmn, __shfl_xor_sync(0xffffffffu, rmn, o));
+    rmx = fmaxf(rmx, __shfl_xor_sync(0xffffffffu, rmx, o));
   }
+  const float mn = fminf(fmaxf(rmn, -tclip), tclip), mx = fminf(fmaxf(rmx, -tclip), tclip);  // of the clipped values
   const float s32 = __fdiv_rn(__fsub_rn(mx, mn), LM ? kLmSpan : 3.0f);
   const __half sh = __float2half_rn(s32), zh = __float2half_rn(mn);
   const float sf = __half2float(sh), zf = __half2float(zh);
@@ -218,29 +194,50 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_had_kernel(const Append
   const bool body = inside && p >= g.S;
   if (body && !rng_ok && q == 0) status_or(a.status, OSCAR_DEV_FP16_RANGE);
   const bool ok = rng_ok && sf != 0.f;
-  const uint64_t zz = splat_x2(zf), ii = splat_x2(ok ? __frcp_rn(sf) : 0.f);
-  uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  const float inv = ok ? __frcp_rn(sf) : 0.f;
+  auto code = [&](float y) { return LM ? lm_code(y) : __float2int_rn(y); };
+  // Values that the clip would change have the codes 0 and 3 without it where the clipped ones have (each step is
+  // monotone); a scale that is small beside the zero's rounding may make others of them.
+  const int top = code(__fmul_rn(__fsub_rn(mx, zf), inv)), bottom = code(__fmul_rn(__fsub_rn(mn, zf), inv));
+  if (__any_sync(0xffffffffu, ok && ((rmx > tclip && top < 3) || (rmn < -tclip && bottom > 0)))) clip();
+  const uint64_t zz = splat_x2(zf), ii = splat_x2(inv);
+  uint32_t w[2] = {0, 0};  // byte g: the codes of channels g + 8 k
 #pragma unroll
-  for (int m = 0; m < 4; ++m)
+  for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 y = both(mul2(sub2(x[m][k], zz), ii));
-      const uint32_t u = LM ? lm_code(y.x) : min(__float2uint_rn(y.x), 3u);  // the conversion saturates below 0
-      const uint32_t v = LM ? lm_code(y.y) : min(__float2uint_rn(y.y), 3u);
-      if (role == 0) {  // word 2 k + (m >> 1), code 2 (q >> 1) + 4 (m & 1) + (q & 1) of its low (even channel) and high half
-        w[2 * k + (m >> 1)] |= (u | v << 16) << (8 * (m & 1));
-      } else {          // word 2 k (+ 1), code q + 4 m
-        w[2 * k] |= u << (8 * m);
-        w[2 * k + 1] |= v << (8 * m);
+    for (int e = 2; e >= 0; e -= 2) {  // channels g and g + 1, g = 4 r + e
+      int lo[4], hi[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 y = both(mul2(sub2(x[4 * k + 2 * r + e / 2], zz), ii));
+        lo[k] = code(y.x), hi[k] = code(y.y);
       }
+      w[r] = pack_codes(hi[1], hi[0], pack_codes(hi[3], hi[2], w[r]));
+      w[r] = pack_codes(lo[1], lo[0], pack_codes(lo[3], lo[2], w[r]));
     }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = ok ? w[i] << (2 * q) : 0u;
-  const uint2 words = gather_words(w, q);
+  if (!ok) w[0] = w[1] = 0;
+  uint32_t words[2];
+  if (role == 0) {
+    // word 2 c + (q >> 1): bytes of c's channel pair, of the lanes q and q ^ 1 in turn; the even lane has c = 0, 1
+    const bool odd = q & 1;
+    const uint32_t keep = odd ? w[1] : w[0], got = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1);
+    const uint32_t u = odd ? got : keep, v = odd ? keep : got;
+    words[0] = prmt(u, v, 0x5140), words[1] = prmt(u, v, 0x7362);
+  } else {
+    // word g: byte g of the lanes in turn; lane q has words 2 q and 2 q + 1
+    const bool up = q & 2, odd = q & 1;
+    const uint32_t keep = up ? w[1] : w[0], got = __shfl_xor_sync(0xffffffffu, up ? w[0] : w[1], 2);  // of q, of q ^ 2
+    const uint32_t mine2 = prmt(keep, got, odd ? 0x7632 : 0x5410);
+    const uint32_t theirs = __shfl_xor_sync(0xffffffffu, prmt(keep, got, odd ? 0x5410 : 0x7632), 1);  // of q ^ 1, of q ^ 3
+    const uint32_t order = q == 0 ? 0x6240u : q == 1 ? 0x2604u : q == 2 ? 0x4062u : 0x0426u;
+    words[0] = prmt(mine2, theirs, order), words[1] = prmt(mine2, theirs, order + 0x1111u);
+  }
   if (!body) return;
   const int64_t irow = bh * g.ncap + (p - g.S);
   uint8_t* codes = role_base + g.sink_bytes + g.ring_bytes;
-  reinterpret_cast<uint2*>(codes + irow * (D / 4) + 32 * j)[q] = words;
+  uint32_t* to = reinterpret_cast<uint32_t*>(codes + irow * (D / 4) + 32 * j);
+  if (role == 0) to[4 * (q & 1) + (q >> 1)] = words[0], to[4 * (q & 1) + (q >> 1) + 2] = words[1];
+  else reinterpret_cast<uint2*>(to)[q] = make_uint2(words[0], words[1]);
   if (q == 0) reinterpret_cast<uint32_t*>(codes + g.codes_bytes)[irow * (D / kGroup) + j] = pack_half2(sh, zh);
 }
 
