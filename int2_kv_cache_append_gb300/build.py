@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "liboscar_kv.so")
 SOURCES = ["oscar_kv_api.cu", "kv_append.cu", "kv_append_tc.cu", "attn_decode.cu", "attn_decode_static.cu",
            "calibrate.cu", "kv_rows.cu", "attn_rows.cu", "attn_rows_tc.cu",
            "attn_rows_lanes.cu", "kv_rows_tc.cu", "norm_rope.cu", "attn_prompt.cu", "attn_prompt_tc.cu", "attn_prompt_wide.cu",
-           "attn_mass.cu", "kv_evict.cu", "kv_append_had.cu"]
+           "attn_mass.cu", "attn_mass_tc.cu", "kv_evict.cu", "kv_append_had.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

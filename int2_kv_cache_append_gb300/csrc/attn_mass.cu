@@ -22,8 +22,8 @@
 //
 // What bounds it: instructions, about 300 a batch of 32 positions, over half of them
 // the codes' unpacking and the products (32 ragged sequences of up to 32K, 8 KV heads
-// of 4 rows: 103 us, 2.5 TB/s of K and masses); with many rows the mma.sync pipe and
-// its latency (256 rows over 16,384 positions x 8 KV heads: 96 us).
+// of 4 rows: 103 us, 2.5 TB/s of K and masses); with many rows of head_dim 256 or 512 the
+// mma.sync pipe and its latency.  Many rows of head_dim 128: attn_mass_tc.cu.
 //
 // The rows' fragments are written once by a kernel of their own behind the query
 // rotation: built by every block they cost as much as the positions themselves.
@@ -408,22 +408,29 @@ int launch_d(const MassArgs& a, cudaStream_t stream) {
                                                                        : launch_n<D, 4, false>(a, stream);
 }
 
+// Query rows of a (sequence, KV head) that take the form with positions in the TMEM lanes (attn_mass_tc.cu).  us here / there
+// with 16, 24, 32, 64 rows: 8 units of 16,384 positions 18 / 20, 23 / 20, 24 / 20, 34 / 21; with 16, 32, 64: 64 units of 2000
+// 20 / 23, 29 / 24, 44 / 29, 128 units of 300 18 / 22, 25 / 25, 36 / 28.  Longer heads' keys do not fit beside the scores.
+bool many_rows(const Geom& g, int n) { return g.D == 128 && int64_t(n) * g.G > 24; }
+
 }  // namespace
 
 uint64_t mass_frag_bytes(const Geom& g, int n) {
+  if (many_rows(g, n)) return mass_image_bytes(g, n);
   const uint64_t rows = uint64_t(g.B) * g.Hkv * ((int64_t(n) * g.G + 3) / 4) * 4;
   return rows * (uint64_t(g.D) * 12 + 16 + g.Dg * 4);
 }
 
 int launch_attn_mass(const MassArgs& args, cudaStream_t stream) {
+  if (many_rows(args.g, args.n)) return launch_attn_mass_tc(args, stream);
   MassArgs a = args;
   a.tiles = int((int64_t(a.n) * a.g.G + 3) / 4);
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return OSCAR_ERR_LAUNCH;
   // Positions of a warp: few enough for every SM to have 32 warps in turn.  us a call with 32 / 64 / 128 / 256: 64 units of
-  // 32,768 positions 63 / 51 / 47 / 51, 256 of 8192 69 / 55 / 52 / 55, 8 of 32,768 15 / 14 / 15 / 20, 8 of 16,384 with 256 query
-  // rows each 96 / 127 / 169 / 289; 256 ragged ones of up to 32,768 107 with 128, 103 with 256.
+  // 32,768 positions 63 / 51 / 47 / 51, 256 of 8192 69 / 55 / 52 / 55, 8 of 32,768 15 / 14 / 15 / 20; 256 ragged ones of up to
+  // 32,768 107 with 128, 103 with 256.
   const int64_t even = int64_t(a.top) * a.g.B * a.g.Hkv / (32 * sms);
   a.piece = even >= 4 * kMostPiece ? kMostPiece : int(std::min<int64_t>(kMostPiece / 2, std::max<int64_t>(kBatch, even / kBatch * kBatch)));
   return a.g.D == 128 ? launch_d<128>(a, stream) : a.g.D == 256 ? launch_d<256>(a, stream) : launch_d<512>(a, stream);

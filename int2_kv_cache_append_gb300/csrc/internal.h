@@ -255,10 +255,14 @@ struct MassArgs {
   int32_t* status;
   uint8_t* frags;           // workspace: the query rows as matrix fragments, mass_frag_bytes
   int n, top;               // top: length for which the grid is laid out
-  int tiles, piece;         // of four query rows; positions of a warp (set by the launcher)
+  int tiles, piece;         // blocks of query rows; positions of a warp (set by the launcher)
+  uint32_t wait_turns;      // as in RowsArgs
+  int wait_poison;
 };
 uint64_t mass_frag_bytes(const Geom& g, int n);
 int launch_attn_mass(const MassArgs& a, cudaStream_t stream);
+uint64_t mass_image_bytes(const Geom& g, int n);  // attn_mass_tc.cu
+int launch_attn_mass_tc(const MassArgs& a, cudaStream_t stream);
 
 // Rows of largest mass and the windows into another cache (kv_evict.cu).
 struct EvictArgs {

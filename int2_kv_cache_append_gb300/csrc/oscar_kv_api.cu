@@ -698,6 +698,8 @@ int attn_mass(const oscar_kv_config* cfg, const void* cache, int32_t layer, cons
   a.mass_out = mass_out;
   a.status = dev_status;
   a.frags = ws;
+  a.wait_turns = oscar::wait_turns();
+  a.wait_poison = oscar::g_test_wait_poison;
   a.n = n_new;
   a.top = seq_len_hint > 0 ? seq_len_hint : g.cap;
   const int rc = n_new ? oscar::launch_qrot_rows(r, st) : OSCAR_OK;

@@ -197,3 +197,54 @@ def test_a_large_query_leaves_other_heads_alone(n, size):
     m.q[0, 0, 1] *= size
     got = m.run(out=torch.full_like(m.out, 5.0))
     assert torch.equal(got[0, 1], want[0, 1]) and torch.equal(got[1], want[1])
+
+
+MANY = [  # more than 32 query rows a KV head at head_dim 128: positions in the tensor memory's lanes
+    (128, 8, 1, 0, 0, [255, 256, 257, 1, 0], 16, None, 0),                     # 128 rows, tiles full and not
+    (128, 8, 2, 4, 8, [700, 30, 4, 11], 33, [33, 9, 33, 1], 0),                # 132 rows; before the sequence; a window only
+    (128, 6, 2, 100, 300, [900, 399, 250], 43, [43, 0, 20], K.FLAG_LLOYD_MAX),  # 129 rows; windows over two tiles; no row
+    (128, 5, 1, 3, 600, [590, 1200], 90, None, K.FLAG_HADAMARD | K.FLAG_IN_FP32),  # rows hidden inside the codes and the ring
+    (128, 16, 2, 64, 0, [520, 64, 65], 60, None, K.FLAG_V_BF16),               # 480 rows; no ring
+    (128, 8, 2, 0, 4, [300, 600], 290, None, 0),                               # hidden rows among codes
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=[f"{i}" for i in range(len(MANY))])
+def test_many_rows_against_64_bits(case):
+    m = Mass(*case)
+    m.run()
+    m.check()
+    assert int(m.st.item()) == 0
+    again = torch.full_like(m.out, 5.0)
+    for hint in (1, 200):
+        assert torch.equal(m.run(out=again.fill_(5.0), hint=hint), m.out)
+    in_place = m.before.clone()
+    for b, T in enumerate(m.lens):
+        in_place[b, :, max(T, 0):] = 5.0
+    assert torch.equal(m.run(out=in_place, before=in_place), m.out)
+
+
+@pytest.mark.parametrize("case", [MANY[1], MANY[2], MANY[3]])
+def test_a_wait_that_runs_out(case):
+    from tests.test_gpu_rows_timeout import times_out_and_recovers
+    m = Mass(*case)
+
+    def call():
+        m.out.fill_(5.0)
+        K.attn_mass(m.kc, m.cdev, 0, m.q, dev_i32(m.lens), m.R, m.lse, m.out, m.ws[:K.attn_mass_workspace_bytes(m.kc, m.n)],
+                    q_lens=dev_i32(m.q_lens), status=m.st)
+    times_out_and_recovers(call, [m.out], m.st)
+
+
+def test_many_rows_whose_query_or_weight_is_strange():
+    """What is not finite stays with its KV head; a row without weight adds nothing."""
+    m = Mass(128, 8, 2, 4, 8, [300, 64], 20)
+    want = m.run().clone()
+    m.q[0, 3, 1] = math.inf
+    m.q[1, 2, 5] *= 1e18
+    got = m.run(out=torch.full_like(m.out, 5.0))
+    assert torch.equal(got[0, 1], want[0, 1]) and torch.equal(got[1, 0], want[1, 0])
+    m = Mass(128, 8, 2, 4, 8, [300, 64], 20)
+    m.lse[0, :] = -math.inf
+    got = m.run(out=torch.full_like(m.out, 5.0))
+    assert torch.equal(got[0, :, :300], m.before[0, :, :300]) and torch.equal(got[1], want[1])
