@@ -222,5 +222,8 @@ def test_evict_workspace_formula(keep, rows):
 @pytest.mark.parametrize("n", [0, 1, 3, 64])
 def test_mass_workspace_formula(n):
     align = lambda x: (x + 255) // 256 * 256
-    rows = 2 * 2 * ((n * 4 + 3) // 4) * 4
-    assert K.attn_mass_workspace_bytes(CFG, n) == align(2 * n * 8 * 128 * 4) + align(rows * (128 * 12 + 16 + 4))
+    if n * 4 > 24:  # blocks of 96 query rows: two fp16 and three bf16 parts, five constants
+        parts = 2 * 2 * ((n * 4 + 95) // 96) * 96 * (128 * 10 + 5 * 4)
+    else:
+        parts = 2 * 2 * ((n * 4 + 3) // 4) * 4 * (128 * 12 + 16 + 4)
+    assert K.attn_mass_workspace_bytes(CFG, n) == align(2 * n * 8 * 128 * 4) + align(parts)
