@@ -476,13 +476,17 @@ int launch_attn_mass_tc(const MassArgs& args, cudaStream_t stream) {
   const int64_t units = int64_t(a.g.B) * a.g.Hkv, rows = units * a.tiles * kRows, sms = known[dev];
   const int rc = row_launch(true, mass_images_kernel, dim3(unsigned((rows + 3) / 4)), 128, 0, stream, a);
   if (rc != OSCAR_OK) return rc;
-  // Blocks of a unit: the rounds of the SMs times a block's tiles, a tile's time for its start and end
+  // Blocks of a unit: the rounds of the SMs times a block's tiles, a tile's time for its start and end; of many units as many
+  // that a block has 16 tiles at most, for ragged lengths.  us with 1 / 2 / 4 / 8 / 16 / 32: 256 units of up to 32,768
+  // positions, 32 rows each, 404 / 337 / 299 / 286 / 298 / 330, 256 rows 915 / 770 / 681 / 641 / 654 / 690; 200 of up to 9000
+  // 124 / 105 / 97 / 99 / 114 / 138.
   const int64_t tiles = (a.top + kTile - 1) / kTile + 1;
   int64_t best = 1, cost = INT64_MAX;
   for (int64_t x = 1; x <= std::min<int64_t>(tiles, std::max<int64_t>(1, 4 * sms / units)); ++x) {
     const int64_t c = (units * x + sms - 1) / sms * ((tiles + x - 1) / x + 1);
     if (c < cost) cost = c, best = x;
   }
+  best = std::max(best, (tiles + 15) / 16);
   return row_launch(true, attn_mass_tc_kernel, dim3(unsigned(best), unsigned(units)), kThreads, kBytes, stream, a);
 }
 

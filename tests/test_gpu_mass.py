@@ -248,3 +248,29 @@ def test_many_rows_whose_query_or_weight_is_strange():
     m.lse[0, :] = -math.inf
     got = m.run(out=torch.full_like(m.out, 5.0))
     assert torch.equal(got[0, :, :300], m.before[0, :, :300]) and torch.equal(got[1], want[1])
+
+
+def test_many_rows_captured_and_on_two_streams():
+    """Replays give the bits of a plain call, also while another call with a workspace of its own runs on a second stream."""
+    a, b = Mass(*MANY[1]), Mass(*MANY[3])
+    want = [m.run().clone() for m in (a, b)]
+    sizes = [K.attn_mass_workspace_bytes(m.kc, m.n) for m in (a, b)]
+    given = [(dev_i32(m.lens), dev_i32(m.q_lens)) for m in (a, b)]
+
+    def call(i, m, stream=None):
+        K.attn_mass(m.kc, m.cdev, 0, m.q, given[i][0], m.R, m.lse, m.out, m.ws[:sizes[i]], mass_in=m.before, q_lens=given[i][1],
+                    status=m.st, stream=stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(0, a)
+    other = torch.cuda.Stream()
+    for m in (a, b):
+        m.out.fill_(5.0)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        graph.replay()
+        with torch.cuda.stream(other):
+            call(1, b)
+    torch.cuda.synchronize()
+    assert torch.equal(a.out, want[0]) and torch.equal(b.out, want[1])
+    assert int(a.st.item()) == int(b.st.item()) == 0
