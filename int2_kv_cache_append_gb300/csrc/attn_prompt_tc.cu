@@ -21,11 +21,12 @@
 //
 // Softmax: a thread has a row; its reference M lies 2^12 above the row's maximum when
 // it is chosen and follows it only when that has grown by 2^20, which makes the
-// warp rescale its rows of O: P and O are floating point, so their precision does
-// not depend on where M lies, and 2^20 is hardly ever reached (M at the maximum,
-// followed from 2^8 on: 522 us instead of 450 for eight ragged prompts of
-// activations with outliers).  P is rounded to bf16, V's type; row sums are taken
-// before the rounding, in float32.
+// warp rescale its rows of O: P and O are floating point, so they lose nothing by
+// it, and 2^20 is hardly ever reached (M at the maximum, followed from 2^8 on: 522 us
+// instead of 450 for eight ragged prompts of activations with outliers).  P is
+// rounded to bf16, V's type.  With M at the maximum the largest weight would be 1,
+// without a rounding; anywhere else it has one like the others, so O is divided by the
+// sum of the rounded weights (RowSums), in float32; lse has the sum before the rounding.
 //
 // Positions that some of the block's rows do not see: their scores are set to
 // -inf, which makes P zero, and a warp pair looks through those V rows first: where
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = row < tt * a.G && tok < x.len;
       const int lim = live ? tok : -1, least = first + (row & ~31) / a.G;  // the warp's first token
       float M = kNone;
-      uint64_t l2 = 0;
+      RowSums sums;
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
         ok = wait(bar.s_full + 8 * w, s_phase);
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (__any_sync(0xffffffffu, grow)) {
           const float f = grow ? exp2f(M - (t + kAbove)) : 1.f;
           if (grow) M = t + kAbove;
-          l2 = mul2(l2, splat_x2(f));
+          sums.scale(f);
           if (j > 0) {
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const uint64_t m2 = splat_x2(-M);
-        uint64_t sum = 0, sum1 = 0;
+        TileSums part;
         auto half = [&](const uint32_t (&x)[64], uint32_t to) {
 #pragma unroll
           for (int c = 0; c < 64; c += 32) {
@@ -213,15 +214,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               y = ex2z(y);
               z = ex2z(z);
               p[i] = bf162_of(y, z);
-              if (i & 1) sum = add2(sum, pack2(y, z));
-              else sum1 = add2(sum1, pack2(y, z));
+              part.add(i & 1, y, z, p[i]);
             }
             tmem_st16(to + c / 2, p);
           }
         };
         half(r, S);
         half(u, S + 32);
-        l2 = add2(l2, add2(sum, sum1));
+        part.into(sums);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         fence_before();
         __syncwarp();
@@ -236,13 +236,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (n > 0) {
         fence_after();
-        float l, l1;
-        unpack2(l2, l, l1);
-        l += l1;
-        const float inv = 1.0f / l;
+        const float2 l = sums.total();
+        const float inv = 1.0f / l.y;
         const bool strange = *any_odd != 0;
         const int64_t at = int64_t(x.start + tok) * a.Hq + x.h * a.G + row % a.G;
-        if (live && a.lse) a.lse[at] = (M + log2f(l)) * 0.6931471805599453f;
+        if (live && a.lse) a.lse[at] = (M + log2f(l.x)) * 0.6931471805599453f;
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at * D;
         const bool aligned32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll 1

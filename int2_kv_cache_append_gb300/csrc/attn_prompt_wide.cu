@@ -41,8 +41,8 @@ struct Wide {
   static constexpr int kUnits = D == 256 ? 9 : 5;
   static constexpr int oRing = D * N * 2;
   static constexpr int oOdd = oRing + kUnits * kUnit;
-  static constexpr int oSwap = oOdd + 3 * kOut * 4;  // maxima [2][2][N], sums [2][N]
-  static constexpr int oBar = oSwap + 6 * N * 4;
+  static constexpr int oSwap = oOdd + 3 * kOut * 4;  // maxima [2][2][N], both sums [2][N]
+  static constexpr int oBar = oSwap + 8 * N * 4;
   static constexpr int kBars = 2 * kUnits + 2 + 2 + 1 + 1 + 2 * kChecked * kValueUnits + 1 + 1 + 2 * kItems + 1;
   static constexpr int kBytes = oBar + kBars * 8 + 32 + 1024;
   static_assert(oBar % 8 == 0 && kBytes <= 232448 - 64, "shared memory");
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
     const uint32_t O = tmem + lanes + cO + 128 * half;
     const uint64_t scale2 = splat_x2(a.qscale);
-    float* sums = swap + 4 * N;
+    float2* shared_sums = reinterpret_cast<float2*>(swap + 4 * N);
     uint32_t tile = 0, p_phase = 0, l_phase = 0;  // tile: of all items, s_full and the maxima alternate by it
     bool ok = true;
 #pragma unroll 1
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = row < tt * a.G && tok < x.len;
       const int lim = live ? tok : -1, least = x.t0 + (row & ~31) / a.G;
       float M = kNone;
-      uint64_t l2 = 0;
+      RowSums sums;
 #pragma unroll 1
       for (int j = 0; j < x.nt; ++j, ++tile) {
         const uint32_t S = tmem + lanes + cS + 128 * (tile & 1) + 64 * half;
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (__any_sync(0xffffffffu, grow)) {
           const float f = grow ? exp2f(M - (t + kAbove)) : 1.f;
           if (grow) M = t + kAbove;
-          l2 = mul2(l2, splat_x2(f));
+          sums.scale(f);
           if (j > 0) {
             ok = wait(bar.p_done, p_phase);  // O is not in use
             p_phase ^= 1;
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const uint64_t m2 = splat_x2(-M);
-        uint64_t sum = 0, sum1 = 0;
+        TileSums part;
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
           uint32_t p[16];
@@ -205,12 +205,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             y = ex2z(y);
             z = ex2z(z);
             p[i] = bf162_of(y, z);
-            if (i & 1) sum = add2(sum, pack2(y, z));
-            else sum1 = add2(sum1, pack2(y, z));
+            part.add(i & 1, y, z, p[i]);
           }
           tmem_st16(S + c / 2, p);  // the thread's 64 positions in 32 columns
         }
-        l2 = add2(l2, add2(sum, sum1));
+        part.into(sums);
         // every warp sees every phase of p_done: the next one cannot complete before this warp's arrival below
         if (!done) {
           ok = ok && wait(bar.p_done, p_phase);
@@ -225,17 +224,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       p_phase ^= 1;
       ok = ok && wait(bar.looked, l_phase);
       l_phase ^= 1;
-      float l, l1;
-      unpack2(l2, l, l1);
-      l += l1;
-      sums[half * N + row] = l;
+      shared_sums[half * N + row] = sums.total();
       if (any256(3, !ok)) {
         ok = false;
         break;
       }
       fence_after();
-      l = sums[row] + sums[N + row];
-      const float inv = 1.0f / l;
+      const float l = shared_sums[row].x + shared_sums[N + row].x;
+      const float inv = 1.0f / (shared_sums[row].y + shared_sums[N + row].y);
       const bool strange = *any_odd != 0;
       const int64_t at = int64_t(x.start + tok) * a.Hq + x.h * a.G + row % a.G;
       if (live && a.lse && half == 0 && x.part == 0) a.lse[at] = (M + log2f(l)) * 0.6931471805599453f;

@@ -13,6 +13,35 @@ __device__ __forceinline__ uint32_t bf162_of(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+// A row's P as the products see it: l, its sum, and r, the sum of the rounded values, which is what the output is divided by.
+// A rounding that all of a row's weight has in common then leaves the output as it is: with l there, too, one dominant weight's
+// own 2^-9 went straight into the row (activations with outliers: 2.08e-3 of the output's norm instead of 1.59e-3, of which its
+// rounding to bf16 is 1.5e-3).  lse has l.  Cost: two adds per pair of weights, 1265 -> 1286 us for 16,384 tokens; with the
+// values unpacked by logic instructions and added in pairs 1313.
+struct RowSums {
+  uint64_t l = 0, r = 0;
+  __device__ __forceinline__ void scale(float f) { l = mul2(l, splat_x2(f)), r = mul2(r, splat_x2(f)); }
+  __device__ __forceinline__ float2 total() const {
+    float a, b, c, d;
+    unpack2(l, a, b), unpack2(r, c, d);
+    return make_float2(a + b, c + d);
+  }
+};
+// What a tile adds to them, in two chains.
+struct TileSums {
+  uint64_t l[2] = {0, 0};
+  float lo[2] = {0.f, 0.f}, hi[2] = {0.f, 0.f};
+  __device__ __forceinline__ void add(int chain, float y, float z, uint32_t rounded) {
+    l[chain] = add2(l[chain], pack2(y, z));
+    asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %2;\n add.rn.f32.bf16 %0, x, %0;\n add.rn.f32.bf16 %1, y, %1;\n}\n"
+        : "+f"(lo[chain]), "+f"(hi[chain])
+        : "r"(rounded));
+  }
+  __device__ __forceinline__ void into(RowSums& s) const {
+    s.l = add2(s.l, add2(l[0], l[1]));
+    s.r = add2(s.r, add2(pack2(lo[0], hi[0]), pack2(lo[1], hi[1])));
+  }
+};
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
