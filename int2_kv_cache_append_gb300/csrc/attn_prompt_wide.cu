@@ -285,7 +285,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         head = int(i % each);
         break;
       }
-      if (published >= kItems) ok = wait(bar.item_empty + 8 * at_item.at, at_item.phase ^ 1);
+      const WideWork x(it, head, kParts, tt);
+      // `looked` of the item before, waited for once it is needed: before values are loaded that are looked through.  An item
+      // without such values (its only token ends a position tile) has its own `looked` as soon as the rows of the item before
+      // are written; a wait for that one's phase would then be a phase late and never end.  So it comes first.
+      bool told = published == 0;
+      if (!told && it.b >= 0 && x.checks() == 0) ok = wait(bar.looked, (published - 1) & 1), told = true;
+      if (ok && published >= kItems) ok = wait(bar.item_empty + 8 * at_item.at, at_item.phase ^ 1);
       if (!ok) break;
       if (lane == 0) {
         items[at_item.at] = it, heads[at_item.at] = head;
@@ -294,7 +300,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       at_item.next();
       if (it.b < 0) break;
       if (lane == 0) {
-        const WideWork x(it, head, kParts, tt);
         auto room = [&]() {
           if (ok && issued >= kUnits) ok = mbar_wait(bar.empty + 8 * at.at, at.phase ^ 1, limit);
           return ok;
@@ -306,7 +311,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             at.next(), ++issued;
           }
         };
-        bool told = published == 0;
         auto before = [&]() {  // the item before has been looked through
           if (!told && ok) ok = mbar_wait(bar.looked, (published - 1) & 1, limit);
           told = true;
@@ -343,7 +347,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j + 1 < x.nt) keys(j + 1);
           rows(j);
         }
-        if (ok) before();
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       ++published;
