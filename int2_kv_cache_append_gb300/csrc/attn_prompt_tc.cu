@@ -419,6 +419,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           waits.on(bar.full + 8 * vr.at, vr.phase);
           if (j >= x.check0) waits.on(bar.checked + 8 * (j - x.check0), c_phase);
           const bool more = j + 1 < x.nt;
+          // The phases of tiles that the item does not have: before its last product, without which no row is written and so
+          // nothing of the next item looked through.
+          if (!more) {
+            for (int i = x.checks(); i < kChecked; ++i) waits.on(bar.checked + 8 * i, c_phase);
+            c_phase ^= 1;
+          }
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (j < n[w]) {
@@ -445,8 +451,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           vr.next(), vr.next();
         }
-        for (int i = x.checks(); i < kChecked; ++i) waits.on(bar.checked + 8 * i, c_phase);
-        c_phase ^= 1;
       }
       if (!__all_sync(0xffffffffu, waits.ok && ok) && lane == 0) fail();
       mma_commit(bar.drained, leader);  // every product issued is complete before TMEM is freed

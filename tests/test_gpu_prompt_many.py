@@ -57,3 +57,36 @@ def test_items_with_nothing_to_look_through(D, G, heads, lens):
     p = Prompt(D, G * heads, heads, lens)
     p.run()
     each_as_alone(p, None if len(lens) < 5 else (0, 7, len(lens) - 1))
+
+
+LENS = [2500, 1700, 900, 1, 130, 257, 0, 640] * 2
+
+
+@pytest.mark.parametrize("D", [128, 256, 512])
+@pytest.mark.parametrize("G", [3, 5, 6, 7])
+def test_many_items_a_block(D, G):
+    assert items_of(D, G, 4, LENS) > 2 * sms()
+    p = Prompt(D, 4 * G, 4, LENS)
+    p.run()
+    each_as_alone(p)
+
+
+@pytest.mark.parametrize("D", [128, 256, 512])
+@pytest.mark.parametrize("G", [1, 4, 5])
+def test_what_is_not_finite_stays_with_its_item(D, G):
+    """Values that are infinite or not numbers all over the longest sequences, whose items come first: those of the others,
+    behind them in the same blocks, are as they are alone."""
+    heads = 8 if D == 128 else 4
+    assert items_of(D, G, heads, LENS) > sms()
+    p = Prompt(D, heads * G, heads, LENS)
+    g = torch.Generator().manual_seed(G)
+    for i in (0, 1, 8, 9):
+        n = p.lens[i]
+        t, h, c = (torch.randint(0, x, (60,), generator=g).cuda() for x in (n, heads, D))
+        x = torch.tensor([math.nan, math.inf, -math.inf]).repeat(20).bfloat16().cuda()
+        p.v[int(p.first[i]) + t, h, c] = x
+    p.run()
+    each_as_alone(p)
+    for i, T in enumerate(p.lens):
+        if T < 1700:
+            assert bool(torch.isfinite(p.out[int(p.first[i]):int(p.first[i + 1])].float()).all())
