@@ -11,6 +11,7 @@
 // three prompts of up to 333 tokens, 24 heads, 88 us, of which the longest block's
 // six tiles are the most (all products at the FMA rate: 24 us).
 #include <algorithm>
+#include <cfloat>
 
 #include "prompt_items.cuh"
 
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 1) attn_prompt_kernel
       }
 #pragma unroll
       for (int x = 8; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float next = fmaxf(fmaxf(m[i], top), -3e38f);  // finite also where nothing is visible
+      const float next = fmaxf(fmaxf(m[i], top), -FLT_MAX);  // finite also where nothing is visible
       const float f = exp2f(m[i] - next);
       m[i] = next;
       float sum = 0.f;

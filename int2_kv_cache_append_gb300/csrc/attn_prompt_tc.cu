@@ -52,9 +52,6 @@ constexpr int kMma = 8, kLoad = 9, kCheck = 10;
 constexpr int kTile = kTok * D * 2;    // bytes of a Q, K or V tile: two blocks of 64 channels
 constexpr int kStages = 5;
 constexpr int kChecked = 2;            // position tiles with tokens that some rows do not see
-constexpr float kNone = -1e30f;
-constexpr float kTop = 8.f;            // log2 of the largest P
-constexpr float kAbove = 12.f;         // a new M lies this far above its row's maximum
 constexpr int oQ = 0, oKV = 2 * kTile, oOdd = oKV + kStages * kTile, oBar = oOdd + 3 * D * 4;
 constexpr int kItems = 3;              // items found ahead
 constexpr int kBars = 2 * kStages + 5 * 2 + 2 * kChecked + 1 + 2 * kItems + 1;
@@ -144,7 +141,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
     const uint32_t S = tmem + lanes + cS + 128 * w, O = tmem + lanes + cO + 128 * w;
-    const uint64_t scale2 = splat_x2(a.qscale);
     uint32_t s_phase = 0, o_phase = 0, c_phase = 0;
     Ring<kItems> at_item;
     bool ok = true;
@@ -156,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = w ? x.nB : x.nA, first = x.t0 + w * tt, tok = first + row / a.G;
       const bool live = row < tt * a.G && tok < x.len;
       const int lim = live ? tok : -1, least = first + (row & ~31) / a.G;  // the warp's first token
-      float M = kNone;
+      Reference ref;
       RowSums sums;
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
@@ -183,11 +179,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           top[2] = max3(top[2], __uint_as_float(u[c]), __uint_as_float(u[c + 1]));
           top[3] = max3(top[3], __uint_as_float(u[c + 2]), __uint_as_float(u[c + 3]));
         }
-        const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.qscale;
-        const bool grow = t > M + kTop;
+        const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        const bool grow = most * ref.scale > ref.M + kTop;
         if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? exp2f(M - (t + kAbove)) : 1.f;
-          if (grow) M = t + kAbove;
+          const float f = grow ? ref.follow(most, a.qscale) : 1.f;
           sums.scale(f);
           if (j > 0) {
 #pragma unroll 1
@@ -201,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const uint64_t m2 = splat_x2(-M);
+        const uint64_t scale2 = splat_x2(ref.scale), m2 = splat_x2(-ref.M);
         TileSums part;
         auto half = [&](const uint32_t (&x)[64], uint32_t to) {
 #pragma unroll
@@ -240,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = 1.0f / l.y;
         const bool strange = *any_odd != 0;
         const int64_t at = int64_t(x.start + tok) * a.Hq + x.h * a.G + row % a.G;
-        if (live && a.lse) a.lse[at] = (M + log2f(l.x)) * 0.6931471805599453f;
+        if (live && a.lse) a.lse[at] = ref.lse(l.x, a.qscale);
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at * D;
         const bool aligned32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll 1

@@ -31,8 +31,6 @@ constexpr int kMma = 8, kLoad = 9, kCheck = 10;
 constexpr int kChecked = 2;            // position tiles with tokens that some rows do not see
 constexpr int kValueUnits = 4;         // V units of a position tile
 constexpr int kItems = 3;              // items found ahead
-constexpr float kNone = -1e30f;
-constexpr float kTop = 8.f, kAbove = 12.f;
 constexpr uint32_t cS = 0, cO = 256;   // TMEM columns: two score tiles, O
 
 template <int D>
@@ -134,7 +132,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
     const uint32_t O = tmem + lanes + cO + 128 * half;
-    const uint64_t scale2 = splat_x2(a.qscale);
     float2* shared_sums = reinterpret_cast<float2*>(swap + 4 * N);
     uint32_t tile = 0, p_phase = 0, l_phase = 0;  // tile: of all items, s_full and the maxima alternate by it
     bool ok = true;
@@ -144,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = x.t0 + row / a.G;
       const bool live = row < tt * a.G && tok < x.len;
       const int lim = live ? tok : -1, least = x.t0 + (row & ~31) / a.G;
-      float M = kNone;
+      Reference ref;
       RowSums sums;
 #pragma unroll 1
       for (int j = 0; j < x.nt; ++j, ++tile) {
@@ -170,12 +167,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        const float t = fmaxf(mine[row], mine[N + row]) * a.qscale;
-        const bool grow = t > M + kTop;
+        const float most = fmaxf(mine[row], mine[N + row]);
+        const bool grow = most * ref.scale > ref.M + kTop;
         bool done = j == 0;  // the products of the tile before
         if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? exp2f(M - (t + kAbove)) : 1.f;
-          if (grow) M = t + kAbove;
+          const float f = grow ? ref.follow(most, a.qscale) : 1.f;
           sums.scale(f);
           if (j > 0) {
             ok = wait(bar.p_done, p_phase);  // O is not in use
@@ -193,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const uint64_t m2 = splat_x2(-M);
+        const uint64_t scale2 = splat_x2(ref.scale), m2 = splat_x2(-ref.M);
         TileSums part;
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
@@ -234,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = 1.0f / (shared_sums[row].y + shared_sums[N + row].y);
       const bool strange = *any_odd != 0;
       const int64_t at = int64_t(x.start + tok) * a.Hq + x.h * a.G + row % a.G;
-      if (live && a.lse && half == 0 && x.part == 0) a.lse[at] = (M + log2f(l)) * 0.6931471805599453f;
+      if (live && a.lse && half == 0 && x.part == 0) a.lse[at] = ref.lse(l, a.qscale);
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at * D + x.part * kOut + 128 * half;
       const bool aligned32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll 1

@@ -1,6 +1,8 @@
 // Device code shared by attn_prompt's tensor-core kernels.
 #pragma once
 
+#include <cfloat>
+
 #include "prompt_items.cuh"
 #include "rows_tc.cuh"
 
@@ -13,6 +15,30 @@ __device__ __forceinline__ uint32_t bf162_of(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+constexpr float kTop = 8.f;     // log2 of the largest P
+constexpr float kAbove = 12.f;  // a new reference lies this far above its row's maximum
+
+// What a row's weights refer to: P = 2^(s scale - M) of a score s.  M's rounding is common to the row and does not count while P
+// stays within float32's range: up to |M| = 2^30 it is 2^5 at most.  Beyond, scores that are not the maximum have no weight,
+// since their neighbours in float32 are 2^6 apart; scale then is the power of two that makes M, the maximum times it,
+// 2^31 .. 2^32 without a rounding, and other scores at least 2^7 less.  Before the first score above -inf every
+// exponent is -inf.
+struct Reference {
+  float scale = 0x1p-8f, M = -FLT_MAX;
+  __device__ __forceinline__ float follow(float top, float qscale) {  // to the maximum `top`: the factor for what the row has
+    const float next = fmaf(top, qscale, kAbove), f = scale == qscale ? exp2f(M - next) : 0.f;
+    scale = qscale, M = next;
+    if (!(fabsf(next) <= 0x1p30f)) {
+      scale = pow2i(max(-126, min(127, 31 + 127 - (__float_as_int(fabsf(top)) >> 23))));
+      M = top * scale;
+    }
+    return f;
+  }
+  __device__ __forceinline__ float lse(float l, float qscale) const {
+    return ((scale == qscale ? M : M * (qscale / scale)) + log2f(l)) * 0.6931471805599453f;
+  }
+};
+
 // A row's P as the products see it: l, its sum, and r, the sum of the rounded values, which is what the output is divided by.
 // A rounding that all of a row's weight has in common then leaves the output as it is: with l there, too, one dominant weight's
 // own 2^-9 went straight into the row (activations with outliers: 2.08e-3 of the output's norm instead of 1.59e-3, of which its

@@ -64,3 +64,53 @@ def test_equal_weights_give_the_mean(D):
     out, _ = attend(D, q, k, v)
     assert torch.equal(out[200:390], v[at[:2]].float().mean(0).bfloat16().expand(190, 4, D))
     assert torch.equal(out[391:], v[at].float().mean(0).bfloat16().expand(T - 391, 4, D))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [128, 256, 512])
+@pytest.mark.parametrize("size", [1e5, 1e7, 1e9, 1e12, 1e20, 1e31, 1e37])
+@pytest.mark.parametrize("sign", ["any", "negative"])
+def test_scores_of_any_size(D, kind, size, sign):
+    """Scores q k_p of one channel, exact in float32 and further apart (2^-8 of them) than weights reach: a token's output is
+    the value of the largest score that it sees, or the mean of those that share it, also where all of them are far below
+    zero.  lse is that score, to its own last bits."""
+    T, flags = 333, K.FLAG_IN_FP32 | K.FLAG_OUT_FP32 if kind == "fp32" else 0
+    dtype = torch.float32 if flags else torch.bfloat16
+    g = torch.Generator().manual_seed(D)
+    q, k = torch.zeros(T, 2, D), torch.zeros(T, 1, D)
+    k[:, 0, 0] = -(1 + torch.randint(0, 128, (T,), generator=g) / 128.0)
+    if sign == "any":
+        k[::2] *= -1
+    root = 2.0 ** int(math.log2(size) / 2)
+    k *= root
+    q[:, 0, 0], q[:, 1, 0] = root, root * 1.5
+    v = torch.randint(1, 32, (T, 1, D), generator=g) / 1.0
+    q, k, v = (x.to(dtype).cuda() for x in (q, k, v))
+    out, lse = torch.empty_like(q), torch.empty(T, 2, device="cuda")
+    K.attn_prompt(K.KVConfig(1, 1, 2, 1, D, 0, 0, 1, flags=flags), q, k, v, dev_i32([0, T]), out, lse=lse)
+    torch.cuda.synchronize()
+    score = q[:, :, 0].double()[:, :, None] * k[:, 0, 0].double()  # [T][2][T]
+    score = torch.where(torch.ones(T, T, dtype=torch.bool, device="cuda").tril()[:, None], score, -math.inf)
+    top = score.amax(-1, keepdim=True)
+    w = (score == top).double()
+    want = (w / w.sum(-1, keepdim=True)) @ v[:, 0].double()
+    bound = want.abs() * (2.0 ** -8 if dtype == torch.bfloat16 else 0) + 32 * 8 * 2.0 ** -24
+    assert bool(((out.double() - want).abs() <= bound).all())
+    want = top[..., 0] / math.sqrt(D) + torch.log(w.sum(-1))
+    assert bool(((lse.double() - want).abs() <= want.abs() * 2.0 ** -21 + 1e-5).all())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [128, 256, 512])
+def test_a_score_at_the_end_of_the_range(D, kind):
+    """-3.24e38 in log2 units, for one token and for two."""
+    flags = K.FLAG_IN_FP32 | K.FLAG_OUT_FP32 if kind == "fp32" else 0
+    dtype = torch.float32 if flags else torch.bfloat16
+    q, k, v = (torch.zeros(2, 1, D) for _ in range(3))
+    q[:, 0, 0], k[:, 0, 0] = 1.8e19, -1.8e19
+    v[0], v[1] = 3, 5
+    q, k, v = (x.to(dtype).cuda() for x in (q, k, v))
+    out = torch.empty_like(q)
+    K.attn_prompt(K.KVConfig(1, 1, 1, 1, D, 0, 0, 1, flags=flags), q, k, v, dev_i32([0, 2]), out, sm_scale=math.log(2.0))
+    torch.cuda.synchronize()
+    assert bool((out[0] == 3).all()) and bool((out[1] == 4).all())
