@@ -486,7 +486,9 @@ int attn_prompt(const oscar_kv_config* cfg, const void* q, const void* k, const 
  *   k_new, v_new  device [n_rows][Hkv][D] post-RoPE rows, bf16 (float32 with
  *              OSCAR_FLAG_IN_FP32), 16-byte aligned.
  * Other arguments and errors as kv_append.  Sequences without rows stay as they are;
- * n_rows = 0 does nothing (k_new and v_new may then be NULL).
+ * n_rows = 0 does nothing (k_new and v_new may then be NULL).  Bounds of cu_seqlens that
+ * are out of range are clamped to the rows; they and bounds out of order (a row then goes
+ * to one of the sequences around it, or none) set OSCAR_DEV_OVER_CAPACITY.
  */
 int kv_append_packed(const oscar_kv_config* cfg, void* cache, int32_t layer, const void* k_new, const void* v_new,
                      int32_t n_rows, const int32_t* cu_seqlens, const int32_t* start_pos, const float* R_K,

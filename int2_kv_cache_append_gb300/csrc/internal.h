@@ -27,14 +27,27 @@ struct AppendArgs {
   int hadamard;          // rotate by the in-quant Hadamard (R_K, R_V unused)
   FastDiv div_hkv, div_n_new;  // set by the tensor-core launcher (rows < 2^31)
   const int32_t* cu;     // [B + 1]: packed rows, sequence b's are cu[b] .. cu[b + 1] - 1; NULL: n_new of each
+  int n_rows;            // with cu: all packed rows
 };
 
+// One warp: flags bounds of packed rows that are not within the n rows or not in order.
+__device__ __forceinline__ void packed_check(const int32_t* cu, int B, int n, int32_t* status) {
+  bool bad = false;
+  for (int b = threadIdx.x & 31; b < B; b += 32) bad |= cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > n;
+  if (bad) status_or(status, OSCAR_DEV_OVER_CAPACITY);
+}
+// By every append kernel, behind its wait for earlier ones: block 0's first warp.
+__device__ __forceinline__ void append_check(const AppendArgs& a) {
+  if (a.cu && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) packed_check(a.cu, a.g.B, a.n_rows, a.status);
+}
+
 // Whose new token a packed row is: the sequence b with cu[b] <= row < cu[b + 1] (the search keeps both sides, so the token
-// index is never negative and below the count whatever cu holds), or none.
+// index is never negative and below the count whatever cu holds), or none.  Bounds beyond the rows are clamped to them, so that
+// the count is one of rows that there are.
 struct NewToken {
   int b, t, count;  // sequence (-1: none), its token, its new tokens
 };
-__device__ __forceinline__ NewToken packed_token(const int32_t* cu, int B, int64_t row) {
+__device__ __forceinline__ NewToken packed_token(const int32_t* cu, int B, int n, int64_t row) {
   if (row < cu[0] || row >= cu[B]) return {-1, 0, 0};
   int lo = 0, hi = B;
   while (hi - lo > 1) {
@@ -42,12 +55,12 @@ __device__ __forceinline__ NewToken packed_token(const int32_t* cu, int B, int64
     if (cu[mid] <= row) lo = mid;
     else hi = mid;
   }
-  const int first = cu[lo];
-  return {lo, int(row - first), cu[hi] - first};
+  const int first = max(cu[lo], 0);
+  return {lo, int(row - first), min(cu[hi], n) - first};
 }
 // Token index bt of a batch of n_new tokens each, or of packed rows.
 __device__ __forceinline__ NewToken new_token(const AppendArgs& a, int64_t bt) {
-  if (a.cu) return packed_token(a.cu, a.g.B, bt);
+  if (a.cu) return packed_token(a.cu, a.g.B, a.n_rows, bt);
   return {int(bt / a.n_new), int(bt % a.n_new), a.n_new};
 }
 

@@ -40,7 +40,6 @@
 namespace oscar {
 namespace {
 
-
 constexpr int kAppendThreads = 128;
 // appends of at most this many rows per role take the row-parallel kernel
 constexpr int64_t kSmallAppendRows = 1024;
@@ -73,6 +72,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
   float* rs = smem + C::RPC * C::LD;  // [RPC][LD] rotated rows
 
   pdl_trigger();  // a dependent kernel may be scheduled now; it waits for our completion itself
+  append_check(a);
   const int role = blockIdx.y;
   const float* __restrict__ R = role ? a.R_V : a.R_K;
   const float ratio = role ? a.v_clip : a.k_clip;
@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_rows_kernel(const Ap
   // the kernel that produced this call's inputs.
   pdl_wait();
   pdl_trigger();
+  append_check(a);
   const int role = blockIdx.y;
   const int64_t row0 = int64_t(blockIdx.x) * RPC;
   const int tid = threadIdx.x;
@@ -580,6 +581,7 @@ __global__ void __launch_bounds__(kAppendThreads)
 
   pdl_wait();  // as in kv_append_rows_kernel
   pdl_trigger();
+  append_check(a);
   const int role = blockIdx.y;
   const int q = int(cluster_rank());                  // quant group of this CTA
   const int64_t row0 = int64_t(blockIdx.x / C::SL) * RPC;

@@ -52,6 +52,7 @@ template <int D, bool FP32, bool LM>
 __global__ void __launch_bounds__(kThreads, 4) kv_append_had_kernel(const AppendArgs a) {
   constexpr int LPR = D / 32, RPW = 32 / LPR;  // lanes of a row, rows of a warp
   const Geom& g = a.g;
+  append_check(a);
   const int lane = threadIdx.x & 31, q = lane & 3, j = (lane % LPR) / 4, role = blockIdx.y;
   const uint32_t row = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * RPW + lane / LPR;  // below 2^31 + a block's
   const bool valid = row < a.rows;
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_had_kernel(const Append
     h = int(row - bt * uint32_t(g.Hkv));
     int t, count = a.n_new;
     if (a.cu) {
-      const NewToken tok = packed_token(a.cu, g.B, bt);
+      const NewToken tok = packed_token(a.cu, g.B, a.n_rows, bt);
       mine = tok.b >= 0;
       b = max(tok.b, 0), t = tok.t, count = tok.count;
     } else {

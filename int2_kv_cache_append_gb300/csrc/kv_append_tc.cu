@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   auto acc_empty = [&](int s) { return bar0 + 96u + 8u * s; };  // s < 4
 
   pdl_trigger();  // a dependent kernel may be scheduled now; it waits for our completion itself
+  append_check(a);
   const int role = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float* __restrict__ R = role ? a.R_V : a.R_K;
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const int h = int(r32 - bt * uint32_t(g.Hkv));
         int t, count = a.n_new;
         if (a.cu) {
-          const NewToken tok = packed_token(a.cu, g.B, bt);
+          const NewToken tok = packed_token(a.cu, g.B, a.n_rows, bt);
           valid = tok.b >= 0;
           b = max(tok.b, 0), t = tok.t, count = tok.count;
         } else {

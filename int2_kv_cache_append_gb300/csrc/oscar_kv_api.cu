@@ -95,6 +95,7 @@ int prep_append(const oscar_kv_config* cfg, void* cache, int32_t layer, const vo
   a->in_fp32 = (cfg->flags & OSCAR_FLAG_IN_FP32) ? 1 : 0;
   a->hadamard = had ? 1 : 0;
   a->cu = nullptr;
+  a->n_rows = 0;
   return OSCAR_OK;
 }
 
@@ -642,6 +643,7 @@ int kv_append_packed(const oscar_kv_config* cfg, void* cache, int32_t layer, con
   const int v = prep_append(cfg, cache, layer, k_new, v_new, start_pos, 0, R_K, R_V, nullptr, dev_status, &a, n_rows == 0);
   if (v != OSCAR_OK) return v;
   a.cu = cu_seqlens;
+  a.n_rows = n_rows;
   a.rows = int64_t(n_rows) * cfg->num_kv_heads;
   return oscar::launch_append(a, static_cast<cudaStream_t>(stream));
 }

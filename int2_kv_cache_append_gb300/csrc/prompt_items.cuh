@@ -19,12 +19,8 @@ __device__ __forceinline__ int2 prompt_span(const PromptArgs& a, int b) {
   return make_int2(lo, hi - lo);
 }
 
-// One warp: flags bounds that are not within the rows or not in order.
-__device__ __forceinline__ void prompt_check(const PromptArgs& a) {
-  bool bad = false;
-  for (int b = threadIdx.x & 31; b < a.B; b += 32) bad |= a.cu[b] < 0 || a.cu[b + 1] < a.cu[b] || a.cu[b + 1] > a.n;
-  if (bad) status_or(a.status, OSCAR_DEV_OVER_CAPACITY);
-}
+// One warp.
+__device__ __forceinline__ void prompt_check(const PromptArgs& a) { packed_check(a.cu, a.B, a.n, a.status); }
 
 // Item i of the tiles of all sequences, later tiles first: with a causal mask a
 // tile's work grows with its index, and blocks start in the order of i, so the
