@@ -187,7 +187,8 @@ _known = {}  # (C struct, cache bytes) of the configurations in use, by their va
 
 
 def _known_cfg(cfg: "KVConfig"):
-    key = tuple(cfg.__dict__.values())  # the fields, in their order
+    key = (cfg.num_layers, cfg.batch, cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim, cfg.sink, cfg.recent,
+           cfg.capacity, cfg.k_clip, cfg.v_clip, cfg.flags, cfg.group_size)
     hit = _known.get(key)
     if hit is None:
         if len(_known) >= 256:
