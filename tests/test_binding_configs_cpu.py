@@ -30,8 +30,7 @@ def test_attributes_that_cannot_be_hashed():
 def test_the_order_in_which_fields_were_set():
     """Two configurations whose fields' values, in the order of their last assignment, are the same."""
     a, b = (K.KVConfig(1, 2, 8, 2, 128, 4, 8, 64) for _ in range(2))
-    names = [f.name for f in dataclasses.fields(b)]
-    names[names.index("sink")], names[names.index("recent")] = "recent", "sink"
+    names = [{"sink": "recent", "recent": "sink"}.get(f.name, f.name) for f in dataclasses.fields(b)]
     values = list(vars(b).values())
     vars(b).clear()
     for name, value in zip(names, values):
