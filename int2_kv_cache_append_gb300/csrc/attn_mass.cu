@@ -89,11 +89,13 @@ __global__ void __launch_bounds__(kThreads) mass_frags_kernel(const MassArgs a) 
   const Frags f = frags_of<D>(a, unit);
   const int64_t at = (int64_t(b) * a.n + row / g.G) * g.Hq + h * g.G + row % g.G;
   const float* q = a.qrot + (on ? at : 0) * D;
+  const float lse = on ? a.lse[at] : -INFINITY;
+  const bool weighs = lse != -INFINITY;  // else the query may be anything
   uint32_t most = 0;
   float v[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
-    v[i] = on ? q[lane + 32 * i] : 0.f;
+    v[i] = weighs ? q[lane + 32 * i] : 0.f;
     if (isfinite(v[i])) most = max(most, __float_as_uint(fabsf(v[i])));
   }
 #pragma unroll
@@ -134,11 +136,10 @@ __global__ void __launch_bounds__(kThreads) mass_frags_kernel(const MassArgs a) 
     if (lane == 0) f.sum[row * Dg + j] = sums[j] * pow2i(max(-126, e));
   }
   if (lane == 0) {
-    const float x = on ? a.lse[at] : -INFINITY;
-    float hi = x * 1.4426950408889634f;
+    float hi = lse * 1.4426950408889634f;
     // the product's rounding and what the constant leaves out
-    float lo = fmaf(x, 1.4426950408889634f, -hi) + x * 1.9259629911266175e-8f;
-    if (!isfinite(hi)) hi = x == -INFINITY ? INFINITY : hi, lo = 0.f;  // a row without weight
+    float lo = fmaf(lse, 1.4426950408889634f, -hi) + lse * 1.9259629911266175e-8f;
+    if (!isfinite(hi)) hi = weighs ? hi : INFINITY, lo = 0.f;
     f.row[row] = make_float4(pow2i(min(127, max(-126, e + 16))), hi, lo, __int_as_float(on ? T - ql + row / g.G : -1));
   }
 }

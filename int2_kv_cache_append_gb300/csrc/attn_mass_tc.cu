@@ -83,12 +83,14 @@ __global__ void __launch_bounds__(128) mass_images_kernel(const MassArgs a) {
   const Images f = images_of(a, unit);
   const int64_t at = (int64_t(b) * a.n + row / g.G) * g.Hq + h * g.G + row % g.G;
   const float* q = a.qrot + (on ? at : 0) * D;
+  const float lse = on ? a.lse[at] : -INFINITY;
+  const bool weighs = lse != -INFINITY;  // else the query may be anything
   // columns k = 4 lane .. + 3 of the codes' order: word k / 16 holds channels 64 (w & 1) + 16 (p / 2) + 8 (p & 1) + 2 (w / 2)
   // and the next one as pair p
   const int w = lane >> 2, c0 = 64 * (w & 1) + 16 * (lane & 3) + 2 * (w >> 1);
   float2 u = make_float2(0.f, 0.f), v = u;
   float4 n4 = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (on) {
+  if (weighs) {
     u = *reinterpret_cast<const float2*>(q + c0);
     v = *reinterpret_cast<const float2*>(q + c0 + 8);
     n4 = *reinterpret_cast<const float4*>(q + 4 * lane);  // the BF16 rows' order
@@ -122,11 +124,10 @@ __global__ void __launch_bounds__(128) mass_images_kernel(const MassArgs a) {
   for (int part = 0; part < 3; ++part)
     *reinterpret_cast<uint2*>(to + part * 2 * kPiece) = make_uint2(s[0][part] | s[1][part] << 16, s[2][part] | s[3][part] << 16);
   if (lane == 0) {
-    const float l = on ? a.lse[at] : -INFINITY;
-    float high = l * 1.4426950408889634f;
+    float high = lse * 1.4426950408889634f;
     // the product's rounding and what the constant leaves out
-    float low = fmaf(l, 1.4426950408889634f, -high) + l * 1.9259629911266175e-8f;
-    if (!isfinite(high)) high = l == -INFINITY ? INFINITY : high, low = 0.f;  // a row without weight
+    float low = fmaf(lse, 1.4426950408889634f, -high) + lse * 1.9259629911266175e-8f;
+    if (!isfinite(high)) high = weighs ? high : INFINITY, low = 0.f;
     f.row[row] = make_float4(pow2i(min(127, max(-126, e))), high, low, 0.f);
     f.sum[row] = sum * pow2i(min(127, max(-126, e)));
   }
