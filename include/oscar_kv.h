@@ -465,7 +465,8 @@ int qk_norm_rope(const oscar_kv_config* cfg, const void* q, int64_t q_stride, co
  *   q, k, v    device [n_rows][Hq][D], [n_rows][Hkv][D] twice, bf16 (float32 with
  *              OSCAR_FLAG_IN_FP32), 16-byte aligned.
  *   sm_scale   softmax scale; <= 0 means 1/sqrt(D).
- *   out        device [n_rows][Hq][D] bf16 (float32 with OSCAR_FLAG_OUT_FP32).
+ *   out        device [n_rows][Hq][D] bf16 (float32 with OSCAR_FLAG_OUT_FP32); must not
+ *              overlap q, k or v: a row is written while others are still to be read.
  *   lse        device float32 [n_rows][Hq] or NULL: natural-log log-sum-exp.
  * bf16 inputs and outputs are computed on the tensor cores: scores, softmax
  * statistics and output sums in float32, probabilities rounded to bf16 (relative

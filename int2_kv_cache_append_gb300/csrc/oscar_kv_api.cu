@@ -2,6 +2,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <utility>
 
 #include "internal.h"
 
@@ -611,6 +612,10 @@ int attn_prompt(const oscar_kv_config* cfg, const void* q, const void* k, const 
   const Geom g = make_geom(cfg);
   if (int64_t(n_rows) * g.Hq >= (int64_t(1) << 31)) return OSCAR_ERR_UNSUPPORTED;
   if (n_rows == 0) return OSCAR_OK;
+  const uint64_t q_values = uint64_t(n_rows) * g.Hq * g.D, kv_values = uint64_t(n_rows) * g.Hkv * g.D;
+  const uint64_t size_in = (cfg->flags & OSCAR_FLAG_IN_FP32) ? 4 : 2, size_out = (cfg->flags & OSCAR_FLAG_OUT_FP32) ? 4 : 2;
+  for (const auto& [in, values] : {std::pair(q, q_values), std::pair(k, kv_values), std::pair(v, kv_values)})
+    if (overlap(in, values * size_in, out, q_values * size_out)) return OSCAR_ERR_INVALID;
   oscar::PromptArgs a{};
   a.q = q;
   a.k = k;
