@@ -451,7 +451,7 @@ int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const osca
  *              inv_freq may then be NULL).
  *   q_out, k_out  device [n_rows][Hq][D], [n_rows][Hkv][D] in the type of q and k,
  *              16-byte aligned.  An output may be its own input when that is
- *              dense; otherwise they must not overlap.
+ *              dense; otherwise no output overlaps an input or the other output.
  * Norm and rotation in float32, one rounding at the end.  n_rows = 0 does nothing.
  */
 int qk_norm_rope(const oscar_kv_config* cfg, const void* q, int64_t q_stride, const void* k, int64_t k_stride,

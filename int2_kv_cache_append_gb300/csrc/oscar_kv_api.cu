@@ -581,6 +581,14 @@ int qk_norm_rope(const oscar_kv_config* cfg, const void* q, int64_t q_stride, co
       !aligned(k_weight, 16))
     return OSCAR_ERR_INVALID;
   if (n_rows == 0) return OSCAR_OK;
+  // a row may be written where it was read, not where another one still is
+  const uint64_t size = fp32 ? 4 : 2, q_row = uint64_t(cfg->num_q_heads) * D, k_row = uint64_t(cfg->num_kv_heads) * D;
+  const uint64_t q_span = (uint64_t(n_rows - 1) * q_stride + q_row) * size, k_span = (uint64_t(n_rows - 1) * k_stride + k_row) * size;
+  const uint64_t q_bytes = n_rows * q_row * size, k_bytes = n_rows * k_row * size;
+  const bool q_place = q_out == q && q_span == q_bytes, k_place = k_out == k && k_span == k_bytes;
+  if ((!q_place && overlap(q_out, q_bytes, q, q_span)) || (!k_place && overlap(k_out, k_bytes, k, k_span)) ||
+      overlap(q_out, q_bytes, k, k_span) || overlap(k_out, k_bytes, q, q_span) || overlap(q_out, q_bytes, k_out, k_bytes))
+    return OSCAR_ERR_INVALID;
   oscar::NormRopeArgs a{};
   a.q = q;
   a.k = k;

@@ -26,3 +26,18 @@ def test_attn_prompt(flags):
         args = [far + i * (1 << 20) for i in range(3)]
         args[i] = P
         assert K.lib().attn_prompt(_c(cfg), *args, 5, P, 0.0, P, None, None, None) == INVALID
+
+
+def rope(n=5, q=P, qs=8 * 128, k=P + (1 << 24), ks=2 * 128, qo=P + (2 << 24), ko=P + (3 << 24), fp32=False):
+    cfg = K.KVConfig(1, 2, 8, 2, 128, 4, 8, 64, flags=K.FLAG_IN_FP32 if fp32 else 0)
+    return K.lib().qk_norm_rope(_c(cfg), q, qs, k, ks, n, P, P, 1e-6, P, P, 128, 0, qo, ko, None)
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+def test_qk_norm_rope(fp32):
+    size = 4 if fp32 else 2
+    q, k = 5 * 8 * 128 * size, 5 * 2 * 128 * size
+    for over in (dict(qo=P + 16), dict(qo=P - 16), dict(ko=P + q - 16), dict(qo=P + (1 << 24) + k - 16), dict(ko=P + (2 << 24) + q - 16),
+                 dict(ko=P + (1 << 24) + 16), dict(qs=8 * 128 + 8, qo=P), dict(ks=3 * 128, ko=P + (1 << 24)),
+                 dict(q=P, qs=12 * 128, k=P + 8 * 128 * size, ks=12 * 128, qo=P + 10 * 128 * size)):
+        assert rope(fp32=fp32, **over) == INVALID
