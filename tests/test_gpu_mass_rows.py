@@ -28,3 +28,12 @@ def test_a_token_without_weight_may_hold_anything(D, n, flags, strange):
     m.q[0, 0] = m.q[1, n - 1, 3] = strange
     got = m.run(out=torch.full_like(m.out, 5.0))
     assert bool(torch.isfinite(got).all()) and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("Hq,Hkv,n,flags", [
+    (8, 1, 1, K.FLAG_LLOYD_MAX), (10, 2, 1, K.FLAG_LLOYD_MAX), (4, 1, 5, K.FLAG_LLOYD_MAX),  # two tiles of four rows; more
+    (8, 1, 3, 0), (8, 1, 3, K.FLAG_LLOYD_MAX), (5, 1, 5, 0), (5, 1, 5, K.FLAG_LLOYD_MAX)])   # 24 and 25 rows: both forms
+def test_forms_and_their_borders_at_head_dim_128(Hq, Hkv, n, flags):
+    m = Mass(128, Hq, Hkv, 4, 40, [400, 64, 33], n, flags=flags)
+    m.run()
+    m.check()
