@@ -410,9 +410,11 @@ int launch_d(const MassArgs& a, cudaStream_t stream) {
 }
 
 // Query rows of a (sequence, KV head) that take the form with positions in the TMEM lanes (attn_mass_tc.cu).  us here / there
-// with 16, 24, 32, 64 rows: 8 units of 16,384 positions 18 / 20, 23 / 20, 24 / 20, 34 / 21; with 16, 32, 64: 64 units of 2000
-// 20 / 23, 29 / 24, 44 / 29, 128 units of 300 18 / 22, 25 / 25, 36 / 28.  Longer heads' keys do not fit beside the scores.
-bool many_rows(const Geom& g, int n) { return g.D == 128 && int64_t(n) * g.G > 24; }
+// with 4, 8, 16, 24, 64 rows: 256 ragged units of up to 32,768 positions 101 / 327, 160 / 328, 273 / 334, 390 / 335, 658 / 381;
+// 256 of 32,768 139 / 510, 229 / 511, 408 / 516, 588 / 517, 1001 / 593; 32 ragged ones 24 / 55, 30 / 55, 45 / 56, 65 / 56, 111 / 65;
+// 8 of 16,384 12 / 18, 15 / 18, 17 / 18, 22 / 18, 32 / 19; 128 ragged ones of up to 2000 15 / 31, 19 / 31, 25 / 33, 35 / 35,
+// 54 / 40.  (17 rows cost here what 32 do: four tiles of four at a time.)  Longer heads' keys do not fit beside the scores.
+bool many_rows(const Geom& g, int n) { return g.D == 128 && int64_t(n) * g.G > 16; }
 
 }  // namespace
 

@@ -49,7 +49,7 @@ struct Bars {
 constexpr int kBytes = oBar + 10 * 8 + 16 + 1024;  // + TMEM address, alignment slack
 static_assert(oBar % 8 == 0 && kBytes <= 232448, "shared memory");
 
-// What mass_images_kernel leaves per (sequence, KV head), by blocks of 128 rows
+// What mass_images_kernel leaves per (sequence, KV head), by blocks of kRows rows
 struct Images {
   uint8_t *f16, *bf;
   float4* row;  // factor, reference high and low

@@ -31,8 +31,9 @@ def test_a_token_without_weight_may_hold_anything(D, n, flags, strange):
 
 
 @pytest.mark.parametrize("Hq,Hkv,n,flags", [
-    (8, 1, 1, K.FLAG_LLOYD_MAX), (10, 2, 1, K.FLAG_LLOYD_MAX), (4, 1, 5, K.FLAG_LLOYD_MAX),  # two tiles of four rows; more
-    (8, 1, 3, 0), (8, 1, 3, K.FLAG_LLOYD_MAX), (5, 1, 5, 0), (5, 1, 5, K.FLAG_LLOYD_MAX)])   # 24 and 25 rows: both forms
+    (8, 1, 1, K.FLAG_LLOYD_MAX), (10, 2, 1, K.FLAG_LLOYD_MAX), (3, 1, 3, K.FLAG_LLOYD_MAX),  # two tiles of four rows; more
+    (8, 1, 2, 0), (4, 1, 4, K.FLAG_LLOYD_MAX), (1, 1, 17, 0), (2, 2, 17, K.FLAG_LLOYD_MAX),  # 16 and 17 rows: both forms
+    (8, 1, 3, 0), (8, 1, 3, K.FLAG_LLOYD_MAX), (5, 1, 5, 0), (5, 1, 5, K.FLAG_LLOYD_MAX)])   # 24 and 25
 def test_forms_and_their_borders_at_head_dim_128(Hq, Hkv, n, flags):
     m = Mass(128, Hq, Hkv, 4, 40, [400, 64, 33], n, flags=flags)
     m.run()
