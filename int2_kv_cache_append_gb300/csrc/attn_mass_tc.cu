@@ -34,7 +34,6 @@ constexpr int kTile = 256;                    // positions: two accumulators
 constexpr int kRows = 96;                     // query rows of a block of them
 constexpr int kPiece = kRows * 128;           // bytes of half of their channels
 constexpr int kSoftWarps = 8, kMma = kSoftWarps, kCopy = kMma + 1, kThreads = (kCopy + 1) * 32;
-constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // instruction descriptor: both operands bf16
 constexpr int kImage16 = 4 * kPiece, kImageBf = 6 * kPiece;  // parts x channel halves
 constexpr uint32_t cKeys = 0, cScores = 128, kScores = 2 * kRows;  // TMEM columns: 64 per accumulator; two buffers
 constexpr int oB = 0;                         // [2 buffers]

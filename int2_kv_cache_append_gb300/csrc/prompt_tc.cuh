@@ -8,8 +8,6 @@
 
 namespace oscar {
 
-constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // instruction descriptor: both operands bf16
-
 __device__ __forceinline__ uint32_t bf162_of(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));

@@ -24,6 +24,7 @@ __device__ __forceinline__ constexpr uint32_t idesc_of(int n, bool a_mn_major, b
   return (1u << 4) | (a_mn_major ? 1u << 15 : 0u) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) |
          (uint32_t(128 >> 4) << 24);
 }
+constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // instruction descriptor: both operands bf16
 // Issued by the lane with `leader` set; the whole warp comes along, so that
 // descriptors are computed in uniform registers (in one lane's branch every
 // product costs an extra eight instructions, more than its own 64 cycles).
