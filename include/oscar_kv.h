@@ -452,7 +452,8 @@ int attn_decode_prefix(const oscar_kv_config* cfg, const void* cache, const osca
  *   q_out, k_out  device [n_rows][Hq][D], [n_rows][Hkv][D] in the type of q and k,
  *              16-byte aligned.  An output may be its own input when that is
  *              dense; otherwise no output overlaps an input or the other output.
- * Norm and rotation in float32, one rounding at the end.  n_rows = 0 does nothing.
+ * Norm and rotation in float32, one rounding at the end: squares that add up to more
+ * than float32 holds give a row of zeros.  n_rows = 0 does nothing.
  */
 int qk_norm_rope(const oscar_kv_config* cfg, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                  int32_t n_rows, const float* q_weight, const float* k_weight, float eps, const int32_t* positions,
@@ -470,7 +471,8 @@ int qk_norm_rope(const oscar_kv_config* cfg, const void* q, int64_t q_stride, co
  *   lse        device float32 [n_rows][Hq] or NULL: natural-log log-sum-exp.
  * bf16 inputs and outputs are computed on the tensor cores: scores, softmax
  * statistics and output sums in float32, probabilities rounded to bf16 (relative
- * 2^-8) for their product with V.  Otherwise everything is float32.  What is not a
+ * 2^-8) for their product with V, which is divided by the rounded ones' sum.
+ * Otherwise everything is float32.  What is not a
  * number or infinite in K or V of a token reaches only the tokens that see it.
  * Repeated calls give the same bits.  Bounds of cu_seqlens that are out of range or
  * out of order are clamped and set OSCAR_DEV_OVER_CAPACITY.  n_rows = 0 does
@@ -508,8 +510,8 @@ int kv_append_packed(const oscar_kv_config* cfg, void* cache, int32_t layer, con
  *              shape, may be mass_in.  Positions >= seq_lens[b] of mass_out are left
  *              as they were.
  *   workspace  device, 256-byte aligned, attn_mass_workspace_query bytes.
- * Keys enter with float32 accuracy, sums are float32 in a fixed order (repeated calls give the
- * same bits).  More than 65535 (sequence, KV head) pairs are OSCAR_ERR_UNSUPPORTED.
+ * Keys enter as they are cached, the rotated queries with 22 bits of a row's largest component
+ * (24 against BF16 rows), sums are float32 in a fixed order (repeated calls give the same bits).  More than 65535 (sequence, KV head) pairs are OSCAR_ERR_UNSUPPORTED.
  */
 int attn_mass_workspace_query(const oscar_kv_config* cfg, int32_t n_new, uint64_t* bytes);
 int attn_mass(const oscar_kv_config* cfg, const void* cache, int32_t layer, const void* q, int32_t n_new,

@@ -34,10 +34,10 @@
 // replaced by zero there, and added to the rows that see it at the end.
 //
 // What bounds it: over long sequences the tensor cores (16,384 tokens, 32 heads:
-// 1.38 ms, 1.59 PFLOP/s of the products that a causal mask leaves, 85 % of cuBLAS's
+// 1.43 ms, 1.54 PFLOP/s of the products that a causal mask leaves, 82 % of cuBLAS's
 // rate); over short ones the hand-over from item to item, where the output is read,
 // scaled and stored while the next scores wait (eight ragged prompts of up to 4096
-// tokens 440 us, 69 %; 64 of 512 204 us, 36 %).
+// tokens 463 us, 64 %; 64 of 512 217 us, 34 %).
 #include <algorithm>
 
 #include "prompt_tc.cuh"

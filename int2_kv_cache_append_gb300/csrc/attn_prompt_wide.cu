@@ -12,10 +12,10 @@
 //
 // Softmax: eight warps; the two threads of a row have 64 positions each and
 // exchange their maxima once per tile.  What bounds it at head_dim 256 is what
-// bounds head_dim 128 (8192 tokens, 16 heads: 335 us, 1.64 PFLOP/s); at 512 a third
+// bounds head_dim 128 (8192 tokens, 16 heads: 356 us, 1.54 PFLOP/s); at 512 a third
 // of the products are the second half's scores, and 80 KB of units under way do not
 // cover the way from L2 (8192 tokens 1.06 ms, 1.04 PFLOP/s without those; four
-// ragged prompts of 2048 320 us, 0.69).  Arithmetic, masks, the look through V and
+// ragged prompts of 2048 329 us, 0.48).  Arithmetic, masks, the look through V and
 // the order of the items are those of head_dim 128 (attn_prompt_tc.cu).
 #include <algorithm>
 

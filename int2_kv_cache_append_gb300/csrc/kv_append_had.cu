@@ -13,7 +13,7 @@
 // and one (K) or two (V) exchanges put the four lanes' bytes together.
 //
 // What bounds it: instructions and their latency, 690 for eight rows (four ragged prompts of
-// 8192 tokens, 8 KV heads: 48 us, 2.4 TB/s; three blocks an SM instead of four 53 us; the
+// 8192 tokens, 8 KV heads: 46.5 us, 2.5 TB/s; three blocks an SM instead of four 53 us; the
 // row-parallel kernel 185 us).
 #include "rows_tc.cuh"
 
