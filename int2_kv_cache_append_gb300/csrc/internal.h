@@ -35,6 +35,7 @@ __device__ __forceinline__ void packed_check(const int32_t* cu, int B, int n, in
   bool bad = false;
   for (int b = threadIdx.x & 31; b < B; b += 32) bad |= cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > n;
   if (bad) status_or(status, OSCAR_DEV_OVER_CAPACITY);
+  __syncwarp();  // what follows may want the whole warp (tcgen05.alloc)
 }
 // By every append kernel, behind its wait for earlier ones: block 0's first warp.
 __device__ __forceinline__ void append_check(const AppendArgs& a) {
