@@ -37,9 +37,12 @@ __device__ __forceinline__ void packed_check(const int32_t* cu, int B, int n, in
   if (bad) status_or(status, OSCAR_DEV_OVER_CAPACITY);
   __syncwarp();  // what follows may want the whole warp (tcgen05.alloc)
 }
-// By every append kernel, behind its wait for earlier ones: block 0's first warp.
+// By every append kernel of packed rows, behind its wait for earlier ones: block 0's first warp.  Packed rows have kernels of
+// their own (PACKED): asking for them in a decode step's append cost 1.3 of the 212 us of a layer (32 sequences of 32,768 tokens,
+// 8 KV heads).
+template <bool PACKED>
 __device__ __forceinline__ void append_check(const AppendArgs& a) {
-  if (a.cu && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) packed_check(a.cu, a.g.B, a.n_rows, a.status);
+  if (PACKED && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) packed_check(a.cu, a.g.B, a.n_rows, a.status);
 }
 
 // Whose new token a packed row is: the sequence b with cu[b] <= row < cu[b + 1] (the search keeps both sides, so the token
@@ -60,8 +63,9 @@ __device__ __forceinline__ NewToken packed_token(const int32_t* cu, int B, int n
   return {lo, int(row - first), min(cu[hi], n) - first};
 }
 // Token index bt of a batch of n_new tokens each, or of packed rows.
+template <bool PACKED>
 __device__ __forceinline__ NewToken new_token(const AppendArgs& a, int64_t bt) {
-  if (a.cu) return packed_token(a.cu, a.g.B, a.n_rows, bt);
+  if (PACKED) return packed_token(a.cu, a.g.B, a.n_rows, bt);
   return {int(bt / a.n_new), int(bt % a.n_new), a.n_new};
 }
 

@@ -64,7 +64,7 @@ __device__ __forceinline__ int slot_channel(int role, int w, int s) {
   return 8 * s + w;
 }
 
-template <int D>
+template <int D, bool PACKED>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
   using C = AppendCfg<D>;
   extern __shared__ float smem[];
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
   float* rs = smem + C::RPC * C::LD;  // [RPC][LD] rotated rows
 
   pdl_trigger();  // a dependent kernel may be scheduled now; it waits for our completion itself
-  append_check(a);
+  append_check<PACKED>(a);
   const int role = blockIdx.y;
   const float* __restrict__ R = role ? a.R_V : a.R_K;
   const float ratio = role ? a.v_clip : a.k_clip;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
   const Geom& g = a.g;
   const int h = int(row % g.Hkv);
   const int64_t bt = row / g.Hkv;
-  const NewToken tok = new_token(a, bt);
+  const NewToken tok = new_token<PACKED>(a, bt);
   if (tok.b < 0) return;
   const int b = tok.b;
   const int p = a.start_pos[b] + tok.t;
@@ -363,7 +363,7 @@ __device__ __forceinline__ bool rotate_by_matrix(const AppendArgs& a, unsigned c
   return true;
 }
 
-template <int D, int RPC, bool HAD>
+template <int D, int RPC, bool HAD, bool PACKED>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_rows_kernel(const AppendArgs a) {
   using C = RowsCfg<D, RPC>;
   extern __shared__ __align__(128) unsigned char sm[];
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_rows_kernel(const Ap
   // the kernel that produced this call's inputs.
   pdl_wait();
   pdl_trigger();
-  append_check(a);
+  append_check<PACKED>(a);
   const int role = blockIdx.y;
   const int64_t row0 = int64_t(blockIdx.x) * RPC;
   const int tid = threadIdx.x;
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_rows_kernel(const Ap
     }
     const int h = int(row % g.Hkv);
     const int64_t bt = row / g.Hkv;
-    const NewToken tok = new_token(a, bt);
+    const NewToken tok = new_token<PACKED>(a, bt);
     if (tok.b < 0) continue;
     const int b = tok.b;
     const int p = a.start_pos[b] + tok.t;
@@ -567,7 +567,7 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t saddr, uint32_t rank
   return v;
 }
 
-template <int D, int RPC>
+template <int D, int RPC, bool PACKED>
 __global__ void __launch_bounds__(kAppendThreads)
     kv_append_slices_kernel(const __grid_constant__ CUtensorMap tmRK, const __grid_constant__ CUtensorMap tmRV,
                             const AppendArgs a) {
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kAppendThreads)
 
   pdl_wait();  // as in kv_append_rows_kernel
   pdl_trigger();
-  append_check(a);
+  append_check<PACKED>(a);
   const int role = blockIdx.y;
   const int q = int(cluster_rank());                  // quant group of this CTA
   const int64_t row0 = int64_t(blockIdx.x / C::SL) * RPC;
@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     }
     const int h = int(row % g.Hkv);
     const int64_t bt = row / g.Hkv;
-    const NewToken tok = new_token(a, bt);
+    const NewToken tok = new_token<PACKED>(a, bt);
     if (tok.b < 0) continue;
     const int b = tok.b;
     const int p = a.start_pos[b] + tok.t;
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(kAppendThreads)
   }
 }
 
-template <int D, int RPC, bool HAD>
+template <int D, int RPC, bool HAD, bool PACKED>
 int launch_append_rows(const AppendArgs& a, cudaStream_t stream) {
   using C = RowsCfg<D, RPC>;
   constexpr uint32_t smem = HAD ? C::SMEM_HAD : C::SMEM;
@@ -819,7 +819,7 @@ int launch_append_rows(const AppendArgs& a, cudaStream_t stream) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && !attr_set[dev]) {
-    if (cudaFuncSetAttribute(kv_append_rows_kernel<D, RPC, HAD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(kv_append_rows_kernel<D, RPC, HAD, PACKED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem) != cudaSuccess)
       return OSCAR_ERR_LAUNCH;
     attr_set[dev] = 1;
@@ -834,7 +834,7 @@ int launch_append_rows(const AppendArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_append_rows_kernel<D, RPC, HAD>, a) == cudaSuccess ? OSCAR_OK
+  return cudaLaunchKernelEx(&cfg, kv_append_rows_kernel<D, RPC, HAD, PACKED>, a) == cudaSuccess ? OSCAR_OK
                                                                                        : OSCAR_ERR_LAUNCH;
 }
 
@@ -867,14 +867,14 @@ bool encode_f32_tiles(CUtensorMap* m, const float* ptr, uint64_t rows, uint64_t 
 
 namespace {
 
-template <int D, int RPC>
+template <int D, int RPC, bool PACKED>
 int launch_append_slices(const AppendArgs& a, cudaStream_t stream) {
   using C = SliceCfg<D, RPC>;
   static int attr_set[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && !attr_set[dev]) {
-    if (cudaFuncSetAttribute(kv_append_slices_kernel<D, RPC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(kv_append_slices_kernel<D, RPC, PACKED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::SMEM) != cudaSuccess)
       return OSCAR_ERR_LAUNCH;
     attr_set[dev] = 1;
@@ -898,7 +898,7 @@ int launch_append_slices(const AppendArgs& a, cudaStream_t stream) {
   CUtensorMap mk, mv;
   if (!encode_f32_tiles(&mk, a.R_K, D, D, kGroup, C::CH_ROWS) || !encode_f32_tiles(&mv, a.R_V, D, D, kGroup, C::CH_ROWS))
     return OSCAR_ERR_LAUNCH;
-  return cudaLaunchKernelEx(&cfg, kv_append_slices_kernel<D, RPC>, mk, mv, a) == cudaSuccess ? OSCAR_OK
+  return cudaLaunchKernelEx(&cfg, kv_append_slices_kernel<D, RPC, PACKED>, mk, mv, a) == cudaSuccess ? OSCAR_OK
                                                                                             : OSCAR_ERR_LAUNCH;
 }
 
@@ -908,51 +908,49 @@ int launch_append_slices(const AppendArgs& a, cudaStream_t stream) {
 // 17.1 us); otherwise one CTA per RPC rows (larger K-only-INT2 or Lloyd-Max
 // appends, where the sliced grid's per-CTA set-up costs more than the shared
 // stream of R saves: 65,536 rows per role 3.3 vs 4.7 ms).
-template <int D>
+template <int D, bool PACKED>
 int launch_append_small(const AppendArgs& a, cudaStream_t stream) {
   if constexpr (D >= 256) {
     if (a.rows <= kSmallAppendRows)
-      return a.rows > 512 ? launch_append_slices<D, 8>(a, stream) : launch_append_slices<D, 4>(a, stream);
+      return a.rows > 512 ? launch_append_slices<D, 8, PACKED>(a, stream) : launch_append_slices<D, 4, PACKED>(a, stream);
   }
-  return a.rows > 512 ? launch_append_rows<D, 8, false>(a, stream) : launch_append_rows<D, 4, false>(a, stream);
+  return a.rows > 512 ? launch_append_rows<D, 8, false, PACKED>(a, stream) : launch_append_rows<D, 4, false, PACKED>(a, stream);
 }
 
 // the in-quant Hadamard reads no matrix, so a decode step takes the row-parallel
 // kernel, with its programmatic launch; more rows go four lanes to 128 channels
 // (kv_append_had.cu; row-parallel against that, us: 512 rows of 128 3.7 / 4.0,
 // 1024 4.5 / 4.3, 8192 10.1 / 5.1; 128 rows of 512 3.3 / 4.1, 1024 8.4 / 4.5)
-template <int D>
+template <int D, bool PACKED>
 int launch_append_hadamard(const AppendArgs& a, cudaStream_t stream) {
   if (a.rows * D > kSmallAppendRows * 128) return launch_append_had(a, stream);
-  return a.rows > 512 ? launch_append_rows<D, 8, true>(a, stream) : launch_append_rows<D, 4, true>(a, stream);
+  return a.rows > 512 ? launch_append_rows<D, 8, true, PACKED>(a, stream) : launch_append_rows<D, 4, true, PACKED>(a, stream);
 }
 
-template <int D>
+template <int D, bool PACKED>
 int launch_append_d(const AppendArgs& a, cudaStream_t stream) {
   using C = AppendCfg<D>;
   static int attr_set[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && !attr_set[dev]) {
-    if (cudaFuncSetAttribute(kv_append_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+    if (cudaFuncSetAttribute(kv_append_kernel<D, PACKED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
         cudaSuccess)
       return OSCAR_ERR_LAUNCH;
     attr_set[dev] = 1;
   }
   const dim3 grid(unsigned((a.rows + C::RPC - 1) / C::RPC), 2, 1);
-  kv_append_kernel<D><<<grid, kAppendThreads, C::SMEM, stream>>>(a);
+  kv_append_kernel<D, PACKED><<<grid, kAppendThreads, C::SMEM, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
 }
 
-}  // namespace
-
-int launch_append(const AppendArgs& a, cudaStream_t stream) {
-  if (a.rows == 0) return OSCAR_OK;
+template <bool PACKED>
+int launch_append_p(const AppendArgs& a, cudaStream_t stream) {
   if (a.hadamard) {
     switch (a.g.D) {
-      case 128: return launch_append_hadamard<128>(a, stream);
-      case 256: return launch_append_hadamard<256>(a, stream);
-      case 512: return launch_append_hadamard<512>(a, stream);
+      case 128: return launch_append_hadamard<128, PACKED>(a, stream);
+      case 256: return launch_append_hadamard<256, PACKED>(a, stream);
+      case 512: return launch_append_hadamard<512, PACKED>(a, stream);
       default: return OSCAR_ERR_UNSUPPORTED;
     }
   }
@@ -960,19 +958,26 @@ int launch_append(const AppendArgs& a, cudaStream_t stream) {
   // row-parallel kernel at every size
   if (a.rows <= kSmallAppendRows || a.g.vb || a.g.lm) {
     switch (a.g.D) {
-      case 128: return launch_append_small<128>(a, stream);
-      case 256: return launch_append_small<256>(a, stream);
-      case 512: return launch_append_small<512>(a, stream);
+      case 128: return launch_append_small<128, PACKED>(a, stream);
+      case 256: return launch_append_small<256, PACKED>(a, stream);
+      case 512: return launch_append_small<512, PACKED>(a, stream);
       default: return OSCAR_ERR_UNSUPPORTED;
     }
   }
   if (a.g.D == 128 && !a.in_fp32 && a.rows < (int64_t(1) << 31)) return launch_append_tc(a, stream);
   switch (a.g.D) {
-    case 128: return launch_append_d<128>(a, stream);
-    case 256: return launch_append_d<256>(a, stream);
-    case 512: return launch_append_d<512>(a, stream);
+    case 128: return launch_append_d<128, PACKED>(a, stream);
+    case 256: return launch_append_d<256, PACKED>(a, stream);
+    case 512: return launch_append_d<512, PACKED>(a, stream);
     default: return OSCAR_ERR_UNSUPPORTED;
   }
+}
+
+}  // namespace
+
+int launch_append(const AppendArgs& a, cudaStream_t stream) {
+  if (a.rows == 0) return OSCAR_OK;
+  return a.cu ? launch_append_p<true>(a, stream) : launch_append_p<false>(a, stream);
 }
 
 }  // namespace oscar

@@ -48,7 +48,7 @@ __device__ __forceinline__ uint32_t pack_codes(int second, int first, uint32_t b
   return d;
 }
 
-template <int D, bool FP32, bool LM>
+template <int D, bool FP32, bool LM, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 4) kv_append_had_kernel(const AppendArgs a) {
   constexpr int LPR = D / 32, RPW = 32 / LPR;  // lanes of a row, rows of a warp
   // Launched like the row-parallel kernel, for decode steps of large batches: a layer of 160 sequences and 8 heads takes 82.1 us,
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_had_kernel(const Append
   pdl_wait();
   pdl_trigger();
   const Geom& g = a.g;
-  append_check(a);
+  append_check<PACKED>(a);
   const int lane = threadIdx.x & 31, q = lane & 3, j = (lane % LPR) / 4, role = blockIdx.y;
   const uint32_t row = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * RPW + lane / LPR;  // below 2^31 + a block's
   const bool valid = row < a.rows;
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_had_kernel(const Append
     const uint32_t bt = fastdiv(row, a.div_hkv);
     h = int(row - bt * uint32_t(g.Hkv));
     int t, count = a.n_new;
-    if (a.cu) {
+    if (PACKED) {
       const NewToken tok = packed_token(a.cu, g.B, a.n_rows, bt);
       mine = tok.b >= 0;
       b = max(tok.b, 0), t = tok.t, count = tok.count;
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_had_kernel(const Append
   if (q == 0) reinterpret_cast<uint32_t*>(codes + g.codes_bytes)[irow * (D / kGroup) + j] = pack_half2(sh, zh);
 }
 
-template <int D>
+template <int D, bool PACKED>
 int launch_d(const AppendArgs& args, cudaStream_t stream) {
   if (args.rows >= (int64_t(1) << 31)) return OSCAR_ERR_UNSUPPORTED;
   AppendArgs a = args;
@@ -254,15 +254,18 @@ int launch_d(const AppendArgs& args, cudaStream_t stream) {
   a.div_n_new = fastdiv_make(uint32_t(a.n_new > 0 ? a.n_new : 1));
   const int64_t per = int64_t(kThreads / 32) * (32 / (D / 32)), blocks = (a.rows + per - 1) / per;
   const dim3 grid(unsigned(blocks), 2);
-  const auto kernel = a.in_fp32 ? (a.g.lm ? kv_append_had_kernel<D, true, true> : kv_append_had_kernel<D, true, false>)
-                                : (a.g.lm ? kv_append_had_kernel<D, false, true> : kv_append_had_kernel<D, false, false>);
+  const auto kernel = a.in_fp32 ? (a.g.lm ? kv_append_had_kernel<D, true, true, PACKED> : kv_append_had_kernel<D, true, false, PACKED>)
+                                : (a.g.lm ? kv_append_had_kernel<D, false, true, PACKED> : kv_append_had_kernel<D, false, false, PACKED>);
   return row_launch(true, kernel, grid, kThreads, 0, stream, a);
+}
+
+template <bool PACKED>
+int launch_p(const AppendArgs& a, cudaStream_t stream) {
+  return a.g.D == 128 ? launch_d<128, PACKED>(a, stream) : a.g.D == 256 ? launch_d<256, PACKED>(a, stream) : launch_d<512, PACKED>(a, stream);
 }
 
 }  // namespace
 
-int launch_append_had(const AppendArgs& a, cudaStream_t stream) {
-  return a.g.D == 128 ? launch_d<128>(a, stream) : a.g.D == 256 ? launch_d<256>(a, stream) : launch_d<512>(a, stream);
-}
+int launch_append_had(const AppendArgs& a, cudaStream_t stream) { return a.cu ? launch_p<true>(a, stream) : launch_p<false>(a, stream); }
 
 }  // namespace oscar

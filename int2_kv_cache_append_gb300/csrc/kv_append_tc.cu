@@ -126,6 +126,7 @@ __device__ __forceinline__ uint32_t sw128_offset(int row, int k) {
   return uint32_t(kb) * kKBlockBytes + uint32_t(row) * 128 + uint32_t(chunk) * 16 + uint32_t(kin & 7) * 2;
 }
 
+template <bool PACKED>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     kv_append_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const AppendArgs a) {
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   auto acc_empty = [&](int s) { return bar0 + 96u + 8u * s; };  // s < 4
 
   pdl_trigger();  // a dependent kernel may be scheduled now; it waits for our completion itself
-  append_check(a);
+  append_check<PACKED>(a);
   const int role = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float* __restrict__ R = role ? a.R_V : a.R_K;
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const uint32_t bt = fastdiv(r32, a.div_hkv);
         const int h = int(r32 - bt * uint32_t(g.Hkv));
         int t, count = a.n_new;
-        if (a.cu) {
+        if (PACKED) {
           const NewToken tok = packed_token(a.cu, g.B, a.n_rows, bt);
           valid = tok.b >= 0;
           b = max(tok.b, 0), t = tok.t, count = tok.count;
@@ -526,13 +527,14 @@ bool make_rows_map(CUtensorMap* m, const void* ptr, int64_t rows) {
 
 }  // namespace
 
-int launch_append_tc(const AppendArgs& a, cudaStream_t stream) {
+template <bool PACKED>
+static int launch_tc(const AppendArgs& a, cudaStream_t stream) {
   static int attr_set[64] = {0};
   static int sms[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return OSCAR_ERR_LAUNCH;
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(kv_append_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTc) !=
+    if (cudaFuncSetAttribute(kv_append_tc_kernel<PACKED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTc) !=
             cudaSuccess ||
         cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return OSCAR_ERR_LAUNCH;
@@ -546,8 +548,10 @@ int launch_append_tc(const AppendArgs& a, cudaStream_t stream) {
   AppendArgs ka = a;
   ka.div_hkv = fastdiv_make(uint32_t(a.g.Hkv));
   ka.div_n_new = fastdiv_make(uint32_t(std::max(a.n_new, 1)));
-  kv_append_tc_kernel<<<dim3(per_role, 2, 1), kThreadsTc, kSmemTc, stream>>>(mk, mv, ka);
+  kv_append_tc_kernel<PACKED><<<dim3(per_role, 2, 1), kThreadsTc, kSmemTc, stream>>>(mk, mv, ka);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_LAUNCH;
 }
+
+int launch_append_tc(const AppendArgs& a, cudaStream_t stream) { return a.cu ? launch_tc<true>(a, stream) : launch_tc<false>(a, stream); }
 
 }  // namespace oscar
